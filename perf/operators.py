@@ -20,7 +20,7 @@ import torch
 
 own = False
 
-PAGE = 64           # tokens of a cache page
+PAGE = 64           # tokens of a cache page: keys [64, d], values [4, d, 16] (16 tokens side by side)
 FP8_MAX = 448.0     # largest e4m3 value
 SCALE_MIN = 2.0 ** -96
 
@@ -256,7 +256,7 @@ def prepare(case, seed):
         e = torch.randint(-8, -5, (pages, case["Hkv"]), generator=g, device=dev)
         return _pow2(e)
 
-    s["k_cache"], s["v_cache"] = cache((pages, case["Hkv"], PAGE, d)), cache((pages, case["Hkv"], d, PAGE))
+    s["k_cache"], s["v_cache"] = cache((pages, case["Hkv"], PAGE, d)), cache((pages, case["Hkv"], PAGE // 16, d, 16))
     s["k_scale"], s["v_scale"] = scales(), scales()
     return s
 
@@ -375,13 +375,13 @@ def _plain_append_one(cache, scale, x, place, page_of, slot, first, transposed):
     old = torch.where((first > 0)[:, None], scale[place], torch.zeros_like(top))
     s = torch.maximum(old, _pow2_scale(top))
     kept = cache[place].view(torch.float8_e4m3fn).float()
-    kept = kept.transpose(2, 3) if transposed else kept                       # [U, H, 64, d]
+    kept = kept.transpose(3, 4).flatten(2, 3) if transposed else kept         # [U, H, 64, d]
     again = (kept * (old / s)[:, :, None, None]).to(torch.float8_e4m3fn).view(torch.uint8)
     was = kept.to(torch.float8_e4m3fn).view(torch.uint8)
     before = torch.arange(PAGE, device=x.device)[None, :] < first[:, None]
     page = torch.where(before[:, None, :, None], again, was)
     page[page_of, :, slot] = (x / s[page_of][:, :, None]).to(torch.float8_e4m3fn).view(torch.uint8)
-    cache[place] = page.transpose(2, 3).contiguous() if transposed else page
+    cache[place] = page.unflatten(2, (PAGE // 16, 16)).transpose(3, 4).contiguous() if transposed else page
     scale[place] = s
 
 
@@ -415,9 +415,9 @@ def _plain_decode(s):
     N, Hkv, d = case["nseq"], case["Hkv"], case["d"]
     G, t = case["Hq"] // Hkv, s["table"].long()
     k = s["k_cache"].view(torch.float8_e4m3fn)[t].float() * s["k_scale"][t][..., None, None]   # [N, P, H, 64, d]
-    v = s["v_cache"].view(torch.float8_e4m3fn)[t].float() * s["v_scale"][t][..., None, None]   # [N, P, H, d, 64]
+    v = s["v_cache"].view(torch.float8_e4m3fn)[t].float() * s["v_scale"][t][..., None, None, None]
     k = k.permute(0, 2, 4, 1, 3).flatten(3).contiguous()                                       # [N, H, d, P 64]
-    v = v.permute(0, 2, 1, 4, 3).flatten(2, 3).contiguous()                                    # [N, H, P 64, d]
+    v = v.permute(0, 2, 1, 3, 5, 4).flatten(2, 4).contiguous()                                 # [N, H, P 64, d]
     x = torch.matmul(s["q"].float().view(N, Hkv, G, d), k).mul_(1 / math.sqrt(d))
     j = torch.arange(x.shape[-1], device="cuda")[None, :]
     n = s["len"].long()[:, None]
@@ -563,12 +563,14 @@ def _exact_append(s):
                 part = x[:, done:done + n]
                 scale = torch.ceil(torch.log2(part.abs().amax((1, 2)) / 448.0)).clamp_min(-96.0)
                 scale = _pow2(scale.long()).double()
-                values = out[name][page] if name == "k" else out[name][page].transpose(1, 2)   # [H, 64, d]
+                values = out[name][page]                                       # [H, 64, d]
+                values = values.transpose(2, 3).flatten(1, 2) if name == "v" else values
                 if off:
                     old = out[name + "_scale"][page]
                     scale = torch.maximum(scale, old)
                     values[:, :off] = _exact_e4m3(values[:, :off] * (old / scale)[:, None, None])
                 values[:, off:off + n] = _exact_e4m3(part / scale[:, None, None])
+                out[name][page] = values if name == "k" else values.unflatten(1, (PAGE // 16, 16)).transpose(2, 3)
                 out[name + "_scale"][page] = scale
                 done += n
         begin += new[i]
@@ -583,7 +585,8 @@ def _exact_decode(s):
         t = s["table"][i, :(n + PAGE - 1) // PAGE].long()
         begin = max(0, n - c["window"]) if c["window"] else 0
         k = (kc[t].double() * s["k_scale"][t].double()[..., None, None]).transpose(0, 1).flatten(1, 2)[:, begin:n]
-        v = (vc[t].double() * s["v_scale"][t].double()[..., None, None]).permute(1, 0, 3, 2).flatten(1, 2)[:, begin:n]
+        v = (vc[t].double() * s["v_scale"][t].double()[..., None, None, None])
+        v = v.permute(1, 0, 2, 4, 3).flatten(1, 3)[:, begin:n]
         q = s["q"][i].double().view(c["Hkv"], G, c["d"])
         p = torch.softmax(torch.bmm(q, k.transpose(1, 2).contiguous()) * c["d"] ** -0.5, -1)
         rows.append(torch.bmm(p, v.contiguous()).reshape(c["Hq"], c["d"]))
