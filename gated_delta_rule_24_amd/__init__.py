@@ -14,15 +14,24 @@ The entry points keep the C names:
 * :func:`gdr_chunk_fwd_varlen`, :func:`gdr_chunk_bwd_varlen` — the forward
   and backward over packed variable-length sequences
 
+* :func:`gdr_rope`, :func:`gdr_attn_fwd`, :func:`gdr_attn_bwd` (and their
+  packed forms) — the attention layers a hybrid stack puts between recurrent
+  ones: rotary positions, causal attention over a window or the whole past
+* :func:`gdr_kv_append`, :func:`gdr_attn_decode` — that layer's 8-bit paged
+  cache and its attention for one token
+
 and :func:`chunk_fwd`, :func:`decode_step`, :func:`chunk_bwd`,
-:func:`chunk_fwd_varlen`, :func:`chunk_bwd_varlen` are the same calls with
-outputs allocated for the caller.
+:func:`chunk_fwd_varlen`, :func:`chunk_bwd_varlen`, :func:`rope`,
+:func:`attn_fwd`, :func:`attn_bwd`, :func:`attn_fwd_varlen`,
+:func:`attn_bwd_varlen`, :func:`kv_append`, :func:`attn_decode` are the same
+calls with outputs allocated for the caller.
 """
 from __future__ import annotations
 
 import ctypes
+import math
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -38,6 +47,12 @@ GDR_W_SCALAR = 0x10
 GDR_FWD_GENERIC = 0x20
 GDR_GATE_LOGITS = 0x40
 GDR_FWD_SPLIT = 0x80
+GDR_TOKEN_MAJOR = 0x1000
+GDR_ROPE_INTERLEAVED = 0x2000
+GDR_ROPE_INVERSE = 0x4000
+
+# tokens of a cache page
+GDR_KV_PAGE = 64
 
 _STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "workspace", 4: "launch", 5: "device"}
 
@@ -93,6 +108,25 @@ def _load():
         lib.gdr_mixer_prologue_bwd.restype = I
         lib.gdr_mixer_epilogue_bwd.argtypes = [P] * 7 + [I] * 4 + [U, P, S, P]
         lib.gdr_mixer_epilogue_bwd.restype = I
+        F = ctypes.c_float
+        lib.gdr_rope.argtypes = [P] * 6 + [I] * 7 + [F, U, P]
+        lib.gdr_rope.restype = I
+        lib.gdr_attn_fwd.argtypes = [P] * 5 + [I] * 7 + [F, U, P]
+        lib.gdr_attn_fwd.restype = I
+        lib.gdr_attn_fwd_varlen.argtypes = [P] * 6 + [I] * 6 + [F, U, P]
+        lib.gdr_attn_fwd_varlen.restype = I
+        lib.gdr_attn_bwd_workspace_bytes.argtypes = [I] * 6
+        lib.gdr_attn_bwd_workspace_bytes.restype = S
+        lib.gdr_attn_bwd.argtypes = [P] * 9 + [I] * 7 + [F, U, P, S, P]
+        lib.gdr_attn_bwd.restype = I
+        lib.gdr_attn_bwd_varlen.argtypes = [P] * 10 + [I] * 6 + [F, U, P, S, P]
+        lib.gdr_attn_bwd_varlen.restype = I
+        lib.gdr_kv_append.argtypes = [P] * 9 + [I] * 6 + [U, P]
+        lib.gdr_kv_append.restype = I
+        lib.gdr_attn_decode_workspace_bytes.argtypes = [I] * 6
+        lib.gdr_attn_decode_workspace_bytes.restype = S
+        lib.gdr_attn_decode.argtypes = [P] * 8 + [I] * 7 + [F, U, P, S, P]
+        lib.gdr_attn_decode.restype = I
         _lib = lib
     return _lib
 
@@ -107,7 +141,9 @@ EXPORTED_SYMBOLS = ("gdr_abi_version", "gdr_status_string", "gdr_chunk_fwd_works
                     "gdr_decode_step", "gdr_chunk_bwd_workspace_bytes", "gdr_chunk_bwd",
                     "gdr_chunk_bwd_varlen_workspace_bytes", "gdr_chunk_bwd_varlen",
                     "gdr_mixer_prologue", "gdr_mixer_epilogue", "gdr_mixer_bwd_workspace_bytes",
-                    "gdr_mixer_prologue_bwd", "gdr_mixer_epilogue_bwd")
+                    "gdr_mixer_prologue_bwd", "gdr_mixer_epilogue_bwd", "gdr_rope", "gdr_attn_fwd",
+                    "gdr_attn_fwd_varlen", "gdr_attn_bwd_workspace_bytes", "gdr_attn_bwd", "gdr_attn_bwd_varlen",
+                    "gdr_kv_append", "gdr_attn_decode_workspace_bytes", "gdr_attn_decode")
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -265,6 +301,64 @@ def gdr_mixer_epilogue_bwd(o, g, norm_weight, dy, d_o, dg, dnorm_weight, B, H, T
                                         _ptr(dg), _ptr(dnorm_weight), B, H, T, d_v, flags,
                                         _ptr(workspace), workspace_bytes, _stream(stream))
     _check("gdr_mixer_epilogue_bwd", st)
+
+
+def gdr_rope(q, k, q_out, k_out, inv_freq, positions, position0, B, Hq, Hk, T, d, rot_dim, scale, flags,
+             stream=None):
+    st = _load().gdr_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(inv_freq), _ptr(positions), position0,
+                          B, Hq, Hk, T, d, rot_dim, scale, flags, _stream(stream))
+    _check("gdr_rope", st)
+
+
+def gdr_attn_fwd(q, k, v, o, lse, B, Hq, Hkv, Tq, Tk, d, window, scale, flags, stream=None):
+    st = _load().gdr_attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, Hq, Hkv, Tq, Tk, d, window, scale,
+                              flags, _stream(stream))
+    _check("gdr_attn_fwd", st)
+
+
+def gdr_attn_fwd_varlen(q, k, v, o, lse, cu_seqlens, nseq, Hq, Hkv, T, d, window, scale, flags, stream=None):
+    st = _load().gdr_attn_fwd_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(cu_seqlens), nseq, Hq,
+                                     Hkv, T, d, window, scale, flags, _stream(stream))
+    _check("gdr_attn_fwd_varlen", st)
+
+
+def gdr_attn_bwd_workspace_bytes(B, Hq, Hkv, Tq, Tk, d) -> int:
+    return int(_load().gdr_attn_bwd_workspace_bytes(B, Hq, Hkv, Tq, Tk, d))
+
+
+def gdr_attn_bwd(q, k, v, o, lse, dO, dq, dk, dv, B, Hq, Hkv, Tq, Tk, d, window, scale, flags, workspace,
+                 workspace_bytes, stream=None):
+    st = _load().gdr_attn_bwd(*[_ptr(x) for x in (q, k, v, o, lse, dO, dq, dk, dv)], B, Hq, Hkv, Tq, Tk, d, window,
+                              scale, flags, _ptr(workspace), workspace_bytes, _stream(stream))
+    _check("gdr_attn_bwd", st)
+
+
+def gdr_attn_bwd_varlen(q, k, v, o, lse, dO, dq, dk, dv, cu_seqlens, nseq, Hq, Hkv, T, d, window, scale, flags,
+                        workspace, workspace_bytes, stream=None):
+    st = _load().gdr_attn_bwd_varlen(*[_ptr(x) for x in (q, k, v, o, lse, dO, dq, dk, dv, cu_seqlens)], nseq, Hq,
+                                     Hkv, T, d, window, scale, flags, _ptr(workspace), workspace_bytes,
+                                     _stream(stream))
+    _check("gdr_attn_bwd_varlen", st)
+
+
+def gdr_kv_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cache_len, cu_seqlens, nseq, Hkv, T, d,
+                  n_pages, max_pages, flags=0, stream=None):
+    st = _load().gdr_kv_append(*[_ptr(x) for x in (k, v, k_cache, v_cache, k_scale, v_scale, block_table, cache_len,
+                                                   cu_seqlens)], nseq, Hkv, T, d, n_pages, max_pages, flags,
+                               _stream(stream))
+    _check("gdr_kv_append", st)
+
+
+def gdr_attn_decode_workspace_bytes(N, Hq, Hkv, d, max_pages, window) -> int:
+    return int(_load().gdr_attn_decode_workspace_bytes(N, Hq, Hkv, d, max_pages, window))
+
+
+def gdr_attn_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_len, o, N, Hq, Hkv, d, n_pages,
+                    max_pages, window, scale, flags, workspace=None, workspace_bytes=0, stream=None):
+    st = _load().gdr_attn_decode(*[_ptr(x) for x in (q, k_cache, v_cache, k_scale, v_scale, block_table, cache_len,
+                                                     o)], N, Hq, Hkv, d, n_pages, max_pages, window, scale, flags,
+                                 _ptr(workspace), workspace_bytes, _stream(stream))
+    _check("gdr_attn_decode", st)
 
 
 # ---------------------------------------------------------------------------
@@ -471,3 +565,271 @@ def mixer_epilogue_bwd(o, g, norm_weight, dy, stream=None):
     gdr_mixer_epilogue_bwd(o, g, norm_weight, dy, out["d_o"], out["dg"], out["dnorm_weight"], B, H, T,
                            dv_, 0, ws, nb, stream)
     return out
+
+
+# ---------------------------------------------------------------------------
+# the attention layer of a hybrid stack
+# ---------------------------------------------------------------------------
+
+
+def _expect(name, t, shape, dtype, device):
+    """The tensor a call takes: its shape, type and device."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _kept_for(stream, *tensors):
+    """Tensors allocated here and used on another stream: the allocator must not
+    give their memory away before that stream is done with it."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def rope_frequencies(rot_dim, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
+                     trained: int = 0, low: float = 1.0, high: float = 32.0, device="cuda"):
+    """(inv_freq fp32 [rot_dim / 2], scale) for :func:`rope`: base^(-2i / rot_dim),
+    scaled to contexts `factor` times the trained ones by
+
+    * "linear": every frequency divided by factor;
+    * "base": the base raised to base * factor^(rot_dim / (rot_dim - 2)), which
+      leaves the first frequency and divides the last by factor;
+    * "parts": by how often a frequency turns over `trained` tokens: at least
+      `high` times unchanged, at most `low` times divided by factor, between them
+      a linear blend; with scale 0.1 ln(factor) + 1 on the turned channels."""
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rot_dim must be even")
+    i = torch.arange(rot_dim // 2, dtype=torch.float64)
+    scale = 1.0
+    if scaling == "base":
+        if rot_dim < 4:
+            raise ValueError("scaling 'base' needs rot_dim of at least 4")
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    f = torch.pow(torch.tensor(base, dtype=torch.float64), -2.0 * i / rot_dim)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "parts":
+        if trained < 1 or not low < high:
+            raise ValueError("scaling 'parts' needs the trained length and low < high")
+        keep = ((trained * f / (2 * math.pi) - low) / (high - low)).clamp(0.0, 1.0)
+        f = f * keep + f / factor * (1 - keep)
+        scale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "base"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return f.float().to(device), scale
+
+
+def rope(q, k, inv_freq, positions=None, position0: int = 0, interleaved: bool = False, inverse: bool = False,
+         scale: float = 1.0, token_major: bool = False, q_out=None, k_out=None, stream=None):
+    """Rotary positions.  q: [B,Hq,T,d], k: [B,Hk,T,d] or None, bf16 or fp32
+    (token_major: [B,T,H,d]); packed streams [H,T,d] ([T,H,d]) count as B = 1;
+    inv_freq: fp32 [rot_dim/2]; positions: int32 [B,T] (packed: [T]) or None for
+    position0 + t.  inverse turns back: the gradients of q and k from those of the
+    results.  Returns (q_out, k_out); they may be given, also as q and k themselves."""
+    packed = q.dim() == 3
+    if q.dim() not in (3, 4) or (k is not None and k.dim() != q.dim()):
+        raise ValueError("q and k must both be [B,H,T,d] or both packed [H,T,d]")
+    ht = (1, 0) if token_major else (0, 1)
+    B, d = (1 if packed else q.shape[0]), q.shape[-1]
+    inner = q.shape[-3:-1]
+    Hq, T = inner[ht[0]], inner[ht[1]]
+    flags = _act_flag(q)
+    Hk = 0
+    if k is not None:
+        Hk = k.shape[-3:-1][ht[0]]
+        want = ((T, Hk, d) if token_major else (Hk, T, d))
+        _expect("k", k, want if packed else (B,) + want, q.dtype, q.device)
+    _expect("inv_freq", inv_freq, (inv_freq.numel(),), torch.float32, q.device)
+    if positions is not None:
+        _expect("positions", positions, (T,) if packed else (B, T), torch.int32, q.device)
+    flags |= (GDR_TOKEN_MAJOR if token_major else 0) | (GDR_ROPE_INTERLEAVED if interleaved else 0) \
+        | (GDR_ROPE_INVERSE if inverse else 0)
+    made_q = made_k = None
+    if q_out is None:
+        q_out = made_q = torch.empty_like(q)
+    if k is not None and k_out is None:
+        k_out = made_k = torch.empty_like(k)
+    _expect("q_out", q_out, q.shape, q.dtype, q.device)
+    if k is not None:
+        _expect("k_out", k_out, k.shape, k.dtype, k.device)
+    with torch.cuda.device(q.device):
+        gdr_rope(q, k, q_out, k_out if k is not None else None, inv_freq, positions, position0, B, Hq, Hk, T, d,
+                 2 * inv_freq.numel(), scale, flags, stream)
+    _kept_for(stream, made_q, made_k)
+    return q_out, k_out if k is not None else None
+
+
+def _attn_shapes(q, k, v, packed, token_major):
+    """(B, Hq, Hkv, Tq, Tk, d) of attention's inputs, checked."""
+    n = 3 if packed else 4
+    if q.dim() != n or k.dim() != n:
+        raise ValueError("q, k and v must be " + ("[H,T,d]" if packed else "[B,H,T,d]"))
+    ht = (1, 0) if token_major else (0, 1)
+    (Hq, Tq), (Hkv, Tk) = ([x.shape[-3:-1][i] for i in ht] for x in (q, k))
+    B, d = (1 if packed else q.shape[0]), q.shape[-1]
+    if q.dtype != torch.bfloat16:
+        raise ValueError(f"q must be torch.bfloat16, got {q.dtype}")
+    want = (Tk, Hkv, d) if token_major else (Hkv, Tk, d)
+    want = want if packed else (B,) + want
+    _expect("k", k, want, torch.bfloat16, q.device)
+    _expect("v", v, want, torch.bfloat16, q.device)
+    return B, Hq, Hkv, Tq, Tk, d
+
+
+def attn_fwd(q, k, v, window: int = 0, scale: Optional[float] = None, token_major: bool = False,
+             return_lse: bool = True, stream=None):
+    """Causal attention.  q: [B,Hq,Tq,d], k, v: [B,Hkv,Tk,d] bf16 (token_major:
+    [B,T,H,d]); query i sees the keys up to i + Tk - Tq, the last `window` of them
+    (0: all); scale: 1/sqrt(d) if None.  Returns (o as q, lse fp32 [B,Hq,Tq] or None)."""
+    B, Hq, Hkv, Tq, Tk, d = _attn_shapes(q, k, v, False, token_major)
+    o = torch.empty_like(q)
+    lse = torch.empty((B, Hq, Tq), dtype=torch.float32, device=q.device) if return_lse else None
+    with torch.cuda.device(q.device):
+        gdr_attn_fwd(q, k, v, o, lse, B, Hq, Hkv, Tq, Tk, d, window, d ** -0.5 if scale is None else scale,
+                     GDR_TOKEN_MAJOR if token_major else 0, stream)
+    _kept_for(stream, o, lse)
+    return o, lse
+
+
+def attn_fwd_varlen(q, k, v, cu_seqlens, window: int = 0, scale: Optional[float] = None,
+                    token_major: bool = False, return_lse: bool = True, stream=None):
+    """Packed sequences: q: [Hq,T,d], k, v: [Hkv,T,d] bf16 (token_major: [T,H,d]);
+    cu_seqlens: int32 [nseq+1] on the GPU.  Returns (o as q, lse fp32 [Hq,T] or None);
+    rows from cu_seqlens[nseq] on are not written."""
+    B, Hq, Hkv, T, Tk, d = _attn_shapes(q, k, v, True, token_major)
+    if T != Tk:
+        raise ValueError("packed q, k and v must have the same tokens")
+    _expect("cu_seqlens", cu_seqlens, (cu_seqlens.numel(),), torch.int32, q.device)
+    o = torch.empty_like(q)
+    lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device) if return_lse else None
+    with torch.cuda.device(q.device):
+        gdr_attn_fwd_varlen(q, k, v, o, lse, cu_seqlens, cu_seqlens.numel() - 1, Hq, Hkv, T, d, window,
+                            d ** -0.5 if scale is None else scale, GDR_TOKEN_MAJOR if token_major else 0, stream)
+    _kept_for(stream, o, lse)
+    return o, lse
+
+
+def _attn_bwd(q, k, v, o, lse, dO, cu_seqlens, window, scale, token_major, stream):
+    packed = cu_seqlens is not None
+    B, Hq, Hkv, Tq, Tk, d = _attn_shapes(q, k, v, packed, token_major)
+    if packed and Tq != Tk:
+        raise ValueError("packed q, k and v must have the same tokens")
+    _expect("o", o, q.shape, torch.bfloat16, q.device)
+    _expect("dO", dO, q.shape, torch.bfloat16, q.device)
+    _expect("lse", lse, (Hq, Tq) if packed else (B, Hq, Tq), torch.float32, q.device)
+    scale = d ** -0.5 if scale is None else scale
+    flags = GDR_TOKEN_MAJOR if token_major else 0
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    nbytes = gdr_attn_bwd_workspace_bytes(B, Hq, Hkv, Tq, Tk, d)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes > 0 else None
+    with torch.cuda.device(q.device):
+        if packed:
+            _expect("cu_seqlens", cu_seqlens, (cu_seqlens.numel(),), torch.int32, q.device)
+            gdr_attn_bwd_varlen(q, k, v, o, lse, dO, dq, dk, dv, cu_seqlens, cu_seqlens.numel() - 1, Hq, Hkv, Tq, d,
+                                window, scale, flags, ws, nbytes, stream)
+        else:
+            gdr_attn_bwd(q, k, v, o, lse, dO, dq, dk, dv, B, Hq, Hkv, Tq, Tk, d, window, scale, flags, ws, nbytes,
+                         stream)
+    _kept_for(stream, dq, dk, dv, ws)
+    return dict(dq=dq, dk=dk, dv=dv)
+
+
+def attn_bwd(q, k, v, o, lse, dO, window: int = 0, scale: Optional[float] = None, token_major: bool = False,
+             stream=None):
+    """Gradients of <dO, o>: dict dq, dk, dv (bf16, as q, k, v), from what
+    :func:`attn_fwd` took and returned with the same window, scale and layout."""
+    return _attn_bwd(q, k, v, o, lse, dO, None, window, scale, token_major, stream)
+
+
+def attn_bwd_varlen(q, k, v, o, lse, dO, cu_seqlens, window: int = 0, scale: Optional[float] = None,
+                    token_major: bool = False, stream=None):
+    """The same for :func:`attn_fwd_varlen`."""
+    return _attn_bwd(q, k, v, o, lse, dO, cu_seqlens, window, scale, token_major, stream)
+
+
+class KVCache(NamedTuple):
+    """A paged 8-bit cache: e4m3 bytes and one power-of-two scale per (page, head).
+    k: uint8 [n_pages,Hkv,64,d], v: uint8 [n_pages,Hkv,4,d,16] (value of token
+    16 g + i and channel c at [g,c,i]), k_scale, v_scale: fp32 [n_pages,Hkv]."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+
+def kv_cache(n_pages, Hkv, d, device="cuda") -> KVCache:
+    """An empty cache (its contents count only where kv_append has written)."""
+    P = GDR_KV_PAGE
+    return KVCache(torch.empty((n_pages, Hkv, P, d), dtype=torch.uint8, device=device),
+                   torch.empty((n_pages, Hkv, P // 16, d, 16), dtype=torch.uint8, device=device),
+                   torch.empty((n_pages, Hkv), dtype=torch.float32, device=device),
+                   torch.empty((n_pages, Hkv), dtype=torch.float32, device=device))
+
+
+def _cache_shapes(cache, block_table, cache_len, device):
+    n_pages, Hkv, P, d = cache.k.shape
+    if P != GDR_KV_PAGE:
+        raise ValueError(f"a page holds {GDR_KV_PAGE} tokens, got {P}")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [nseq, max_pages]")
+    _expect("cache.k", cache.k, (n_pages, Hkv, P, d), torch.uint8, device)
+    _expect("cache.v", cache.v, (n_pages, Hkv, P // 16, d, 16), torch.uint8, device)
+    _expect("cache.k_scale", cache.k_scale, (n_pages, Hkv), torch.float32, device)
+    _expect("cache.v_scale", cache.v_scale, (n_pages, Hkv), torch.float32, device)
+    _expect("block_table", block_table, block_table.shape, torch.int32, device)
+    _expect("cache_len", cache_len, (block_table.shape[0],), torch.int32, device)
+    return n_pages, Hkv, d
+
+
+def kv_append(k, v, cache: KVCache, block_table, cache_len, cu_seqlens=None, token_major: bool = False, stream=None):
+    """Write new tokens behind the cache_len int32 [nseq] tokens of each sequence.
+    k, v: bf16 [nseq,Hkv,d], one token each; or with cu_seqlens int32 [nseq+1]
+    packed [Hkv,T,d] (token_major: [T,Hkv,d]).  block_table: int32 [nseq,max_pages].
+    cache_len stays as it is: raise it by the new lengths afterwards."""
+    n_pages, Hkv, d = _cache_shapes(cache, block_table, cache_len, k.device)
+    nseq = block_table.shape[0]
+    if cu_seqlens is None:
+        T, want = nseq, (nseq, Hkv, d)
+    else:
+        if k.dim() != 3:
+            raise ValueError("packed k and v must be [Hkv,T,d] or token-major [T,Hkv,d]")
+        T = k.shape[0 if token_major else 1]
+        want = (T, Hkv, d) if token_major else (Hkv, T, d)
+        _expect("cu_seqlens", cu_seqlens, (nseq + 1,), torch.int32, k.device)
+    _expect("k", k, want, torch.bfloat16, k.device)
+    _expect("v", v, want, torch.bfloat16, k.device)
+    with torch.cuda.device(k.device):
+        gdr_kv_append(k, v, cache.k, cache.v, cache.k_scale, cache.v_scale, block_table, cache_len, cu_seqlens, nseq,
+                      Hkv, T, d, n_pages, block_table.shape[1], GDR_TOKEN_MAJOR if token_major else 0, stream)
+
+
+def attn_decode(q, cache: KVCache, block_table, cache_len, window: int = 0, scale: Optional[float] = None,
+                out_dtype=torch.float32, o=None, stream=None):
+    """Attention of one token per sequence over the cache: q bf16 [N,Hq,d], the
+    last of each sequence's cache_len tokens; sees all of them or the last
+    `window`.  Returns o [N,Hq,d] of out_dtype (fp32 or bf16)."""
+    n_pages, Hkv, d = _cache_shapes(cache, block_table, cache_len, q.device)
+    N, max_pages = block_table.shape
+    if q.dim() != 3:
+        raise ValueError("q must be [N,Hq,d]")
+    Hq = q.shape[1]
+    _expect("q", q, (N, Hq, d), torch.bfloat16, q.device)
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"out_dtype must be float32 or bfloat16, got {out_dtype}")
+    made = None
+    if o is None:
+        o = made = torch.empty((N, Hq, d), dtype=out_dtype, device=q.device)
+    _expect("o", o, (N, Hq, d), out_dtype, q.device)
+    nbytes = gdr_attn_decode_workspace_bytes(N, Hq, Hkv, d, max_pages, window)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes > 0 else None
+    with torch.cuda.device(q.device):
+        gdr_attn_decode(q, cache.k, cache.v, cache.k_scale, cache.v_scale, block_table, cache_len, o, N, Hq, Hkv, d,
+                        n_pages, max_pages, window, d ** -0.5 if scale is None else scale,
+                        GDR_OUT_BF16 if out_dtype == torch.bfloat16 else 0, ws, nbytes, stream)
+    _kept_for(stream, made, ws)
+    return o

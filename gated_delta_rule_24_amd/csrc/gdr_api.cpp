@@ -6,6 +6,7 @@
 #include <string.h>
 
 #include "gdr_launch.h"
+#include "gdr_attn.h"
 
 namespace {
 
@@ -52,6 +53,78 @@ gdr_status from_hip(hipError_t e) {
     if (e == hipSuccess) return GDR_OK;
     if (e == hipErrorInvalidValue) return GDR_ERR_UNSUPPORTED;
     return GDR_ERR_LAUNCH;
+}
+
+// The attention layer's sizes: (batch, head) units and 16-row tiles are numbered
+// in 32 bits, element offsets in 64.
+bool attn_sizes_ok(int B, long long H, int T) {
+    return H <= (1LL << 28) && (long long)B * H <= (1LL << 28) && (long long)B * H * (((long long)T + 15) / 16) <= (1LL << 31) - 1;
+}
+
+gdr_status attn_args(int B, int Hq, int Hkv, int Tq, int Tk, int d, int window, float scale, uint32_t flags) {
+    if (flags & ~(GDR_ACT_F32 | GDR_TOKEN_MAJOR)) return GDR_ERR_INVALID_ARG;
+    if (B < 1 || Hq < 1 || Hkv < 1 || Tq < 0 || Tk < 0 || window < 0) return GDR_ERR_INVALID_ARG;
+    if (Hq % Hkv != 0 || !(scale > 0.f) || !(scale - scale == 0.f)) return GDR_ERR_INVALID_ARG;
+    // places of queries and keys are signed 32-bit, with room for a tile behind the last
+    if (Tq > (1 << 30) || Tk > (1 << 30)) return GDR_ERR_INVALID_ARG;
+    if (!attn_sizes_ok(B, Hq, Tq) || !attn_sizes_ok(B, Hq, Tk)) return GDR_ERR_INVALID_ARG;
+    if ((d != 64 && d != 128) || (flags & GDR_ACT_F32)) return GDR_ERR_UNSUPPORTED;
+    return GDR_OK;
+}
+
+gdr::AttnStrides attn_strides(int H, int T, int d, bool token_major) {
+    if (token_major) return {(long long)T * H * d, d, (long long)H * d};
+    return {(long long)H * T * d, (long long)T * d, d};
+}
+
+gdr::AttnParams attn_params(const void* q, const void* k, const void* v, int B, int Hq, int Hkv, int Tq, int Tk,
+                            int d, int window, float scale, uint32_t flags) {
+    gdr::AttnParams p = {};
+    p.q = q; p.k = k; p.v = v;
+    p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.Tq = Tq; p.Tk = Tk; p.d = d;
+    // a window that reaches behind the first key is none
+    p.window = window < Tk ? window : 0;
+    p.scale = scale; p.splits = 1;
+    p.sq = attn_strides(Hq, Tq, d, (flags & GDR_TOKEN_MAJOR) != 0);
+    p.sk = attn_strides(Hkv, Tk, d, (flags & GDR_TOKEN_MAJOR) != 0);
+    return p;
+}
+
+size_t attn_delta_bytes(int B, int Hq, int Tq) {
+    return (2 * (size_t)B * Hq * Tq * sizeof(float) + 255) / 256 * 256;   // D, then the log-sum-exps
+}
+
+gdr_status attn_bwd_run(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
+                        void* dq, void* dk, void* dv, const int* cu_seqlens, int nseq, int B, int Hq, int Hkv, int Tq,
+                        int Tk, int d, int window, float scale, uint32_t flags, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+    const void* ptrs[] = {q, k, v, o, lse, dO, dq, dk, dv, workspace};
+    for (const void* ptr : ptrs)
+        if (ptr && !aligned16(ptr)) return GDR_ERR_INVALID_ARG;
+    const size_t need = gdr_attn_bwd_workspace_bytes(B, Hq, Hkv, Tq, Tk, d);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return GDR_ERR_WORKSPACE;
+    gdr_status ds = check_device();
+    if (ds != GDR_OK) return ds;
+    gdr::AttnParams p = attn_params(q, k, v, B, Hq, Hkv, Tq, Tk, d, window, scale, flags);
+    p.o = const_cast<void*>(o); p.lse = const_cast<float*>(lse);
+    p.dO = dO; p.dq = dq; p.dk = dk; p.dv = dv;
+    p.cu_seqlens = cu_seqlens; p.nseq = nseq;
+    p.delta = static_cast<float*>(workspace);
+    p.splits = gdr::attn_bwd_splits(B, Hq, Hkv, Tk);
+    if (p.splits > 1)
+        p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + attn_delta_bytes(B, Hq, Tq));
+    return from_hip(gdr::launch_attn_bwd(p, (hipStream_t)stream));
+}
+
+gdr_status decode_args(int N, int Hq, int Hkv, int d, int n_pages, int max_pages, int window, float scale,
+                       uint32_t flags) {
+    if (flags & ~GDR_OUT_BF16) return GDR_ERR_INVALID_ARG;
+    if (N < 1 || Hq < 1 || Hkv < 1 || n_pages < 1 || max_pages < 1 || window < 0) return GDR_ERR_INVALID_ARG;
+    if (Hq % Hkv != 0 || !(scale > 0.f) || !(scale - scale == 0.f)) return GDR_ERR_INVALID_ARG;
+    // (sequence, head) pairs and a sequence's tokens are numbered in 32 bits
+    if ((long long)N * Hq > (1LL << 28) || max_pages > (1 << 24)) return GDR_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return GDR_ERR_UNSUPPORTED;
+    return GDR_OK;
 }
 
 }  // namespace
@@ -390,6 +463,155 @@ gdr_status gdr_mixer_epilogue_bwd(const float* o, const void* g, const float* no
     p.part = reinterpret_cast<float*>(workspace);
     p.rows = (long long)B * H * T;
     return from_hip(gdr::launch_mixer_epilogue_bwd(p, d_v, (hipStream_t)stream));
+}
+
+gdr_status gdr_rope(const void* q, const void* k, void* q_out, void* k_out, const float* inv_freq,
+                    const int* positions, int position0, int B, int Hq, int Hk, int T, int d, int rot_dim,
+                    float scale, uint32_t flags, void* stream) {
+    if (flags & ~(GDR_ACT_F32 | GDR_TOKEN_MAJOR | GDR_ROPE_INTERLEAVED | GDR_ROPE_INVERSE)) return GDR_ERR_INVALID_ARG;
+    if (B < 1 || T < 0 || Hq < 0 || Hk < 0 || (long long)Hq + Hk < 1) return GDR_ERR_INVALID_ARG;
+    if (!head_size_ok(d)) return GDR_ERR_UNSUPPORTED;
+    if (rot_dim < 1 || rot_dim > d) return GDR_ERR_INVALID_ARG;
+    if (rot_dim % 16 != 0) return GDR_ERR_UNSUPPORTED;
+    if (!(scale - scale == 0.f)) return GDR_ERR_INVALID_ARG;   // infinite or NaN
+    if (!attn_sizes_ok(B, (long long)Hq + Hk, T) || (long long)B * T > (1LL << 31) - 1) return GDR_ERR_INVALID_ARG;
+    if (T > 0 && (!inv_freq || (Hq > 0 && (!q || !q_out)) || (Hk > 0 && (!k || !k_out)))) return GDR_ERR_INVALID_ARG;
+    const void* ptrs[] = {q, k, q_out, k_out, inv_freq, positions};
+    for (const void* ptr : ptrs)
+        if (ptr && !aligned16(ptr)) return GDR_ERR_INVALID_ARG;
+    gdr_status ds = check_device();
+    if (ds != GDR_OK) return ds;
+    gdr::RopeParams p;
+    p.q = q; p.k = k; p.q_out = q_out; p.k_out = k_out;
+    p.inv_freq = inv_freq; p.positions = positions; p.position0 = position0;
+    p.rows = (long long)B * T; p.T = T; p.Hq = Hq; p.Hk = Hk; p.d = d; p.rot = rot_dim;
+    p.heads = 0; p.scale = scale; p.flags = flags;
+    return from_hip(gdr::launch_rope(p, (hipStream_t)stream));
+}
+
+gdr_status gdr_attn_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv,
+                        int Tq, int Tk, int d, int window, float scale, uint32_t flags, void* stream) {
+    const gdr_status st = attn_args(B, Hq, Hkv, Tq, Tk, d, window, scale, flags);
+    if (st != GDR_OK) return st;
+    if (Tq > 0 && (!q || !o || (Tk > 0 && (!k || !v)))) return GDR_ERR_INVALID_ARG;
+    const void* ptrs[] = {q, k, v, o, lse};
+    for (const void* ptr : ptrs)
+        if (ptr && !aligned16(ptr)) return GDR_ERR_INVALID_ARG;
+    gdr_status ds = check_device();
+    if (ds != GDR_OK) return ds;
+    gdr::AttnParams p = attn_params(q, k, v, B, Hq, Hkv, Tq, Tk, d, window, scale, flags);
+    p.o = o; p.lse = lse;
+    return from_hip(gdr::launch_attn_fwd(p, (hipStream_t)stream));
+}
+
+gdr_status gdr_attn_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* lse,
+                               const int* cu_seqlens, int nseq, int Hq, int Hkv, int T, int d, int window,
+                               float scale, uint32_t flags, void* stream) {
+    const gdr_status st = attn_args(1, Hq, Hkv, T, T, d, window, scale, flags);
+    if (st != GDR_OK) return st;
+    if (nseq < 1 || !cu_seqlens) return GDR_ERR_INVALID_ARG;
+    if (T > 0 && (!q || !o || !k || !v)) return GDR_ERR_INVALID_ARG;
+    const void* ptrs[] = {q, k, v, o, lse, cu_seqlens};
+    for (const void* ptr : ptrs)
+        if (ptr && !aligned16(ptr)) return GDR_ERR_INVALID_ARG;
+    gdr_status ds = check_device();
+    if (ds != GDR_OK) return ds;
+    gdr::AttnParams p = attn_params(q, k, v, 1, Hq, Hkv, T, T, d, window, scale, flags);
+    p.o = o; p.lse = lse; p.cu_seqlens = cu_seqlens; p.nseq = nseq;
+    return from_hip(gdr::launch_attn_fwd(p, (hipStream_t)stream));
+}
+
+size_t gdr_attn_bwd_workspace_bytes(int B, int Hq, int Hkv, int Tq, int Tk, int d) {
+    if (attn_args(B, Hq, Hkv, Tq, Tk, d, 0, 1.f, 0) != GDR_OK) return 0;
+    const int splits = gdr::attn_bwd_splits(B, Hq, Hkv, Tk);
+    const size_t part = splits > 1 ? 2 * (size_t)splits * B * Hkv * Tk * d * sizeof(float) : 0;
+    return attn_delta_bytes(B, Hq, Tq) + part;
+}
+
+gdr_status gdr_attn_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
+                        void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int Tq, int Tk, int d, int window,
+                        float scale, uint32_t flags, void* workspace, size_t workspace_bytes, void* stream) {
+    const gdr_status st = attn_args(B, Hq, Hkv, Tq, Tk, d, window, scale, flags);
+    if (st != GDR_OK) return st;
+    if (Tq > 0 && (!q || !o || !lse || !dO || !dq)) return GDR_ERR_INVALID_ARG;
+    if (Tk > 0 && (!k || !v || !dk || !dv)) return GDR_ERR_INVALID_ARG;
+    return attn_bwd_run(q, k, v, o, lse, dO, dq, dk, dv, nullptr, 0, B, Hq, Hkv, Tq, Tk, d, window, scale, flags,
+                        workspace, workspace_bytes, stream);
+}
+
+gdr_status gdr_attn_bwd_varlen(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                               const void* dO, void* dq, void* dk, void* dv, const int* cu_seqlens, int nseq, int Hq,
+                               int Hkv, int T, int d, int window, float scale, uint32_t flags, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+    const gdr_status st = attn_args(1, Hq, Hkv, T, T, d, window, scale, flags);
+    if (st != GDR_OK) return st;
+    if (nseq < 1 || !cu_seqlens || !aligned16(cu_seqlens)) return GDR_ERR_INVALID_ARG;
+    if (T > 0 && (!q || !k || !v || !o || !lse || !dO || !dq || !dk || !dv)) return GDR_ERR_INVALID_ARG;
+    return attn_bwd_run(q, k, v, o, lse, dO, dq, dk, dv, cu_seqlens, nseq, 1, Hq, Hkv, T, T, d, window, scale, flags,
+                        workspace, workspace_bytes, stream);
+}
+
+gdr_status gdr_kv_append(const void* k, const void* v, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                         const int* block_table, const int* cache_len, const int* cu_seqlens, int nseq, int Hkv,
+                         int T, int d, int n_pages, int max_pages, uint32_t flags, void* stream) {
+    if (flags & ~GDR_TOKEN_MAJOR) return GDR_ERR_INVALID_ARG;
+    if (nseq < 1 || Hkv < 1 || T < 0 || n_pages < 1 || max_pages < 1) return GDR_ERR_INVALID_ARG;
+    if (!cu_seqlens && T != nseq) return GDR_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return GDR_ERR_UNSUPPORTED;
+    // pages of one call are numbered in 32 bits, heads on the grid's second axis
+    if (Hkv > 65535 || (long long)nseq * ((long long)T / 64 + 2) > (1LL << 31) - 1) return GDR_ERR_INVALID_ARG;
+    if ((long long)nseq * max_pages > (1LL << 40)) return GDR_ERR_INVALID_ARG;
+    if (T > 0 && (!k || !v)) return GDR_ERR_INVALID_ARG;
+    if (!k_cache || !v_cache || !k_scale || !v_scale || !block_table || !cache_len) return GDR_ERR_INVALID_ARG;
+    const void* ptrs[] = {k, v, k_cache, v_cache, k_scale, v_scale, block_table, cache_len, cu_seqlens};
+    for (const void* ptr : ptrs)
+        if (ptr && !aligned16(ptr)) return GDR_ERR_INVALID_ARG;
+    if (T == 0) return GDR_OK;
+    gdr_status ds = check_device();
+    if (ds != GDR_OK) return ds;
+    gdr::KvAppendParams p;
+    p.k = k; p.v = v;
+    p.k_cache = static_cast<uint8_t*>(k_cache); p.v_cache = static_cast<uint8_t*>(v_cache);
+    p.k_scale = k_scale; p.v_scale = v_scale;
+    p.block_table = block_table; p.cache_len = cache_len; p.cu_seqlens = cu_seqlens;
+    p.nseq = nseq; p.Hkv = Hkv; p.T = T; p.d = d; p.n_pages = n_pages; p.max_pages = max_pages;
+    const bool token_major = !cu_seqlens || (flags & GDR_TOKEN_MAJOR);
+    p.st = token_major ? (long long)Hkv * d : d;
+    p.sh = token_major ? d : (long long)T * d;
+    return from_hip(gdr::launch_kv_append(p, (hipStream_t)stream));
+}
+
+size_t gdr_attn_decode_workspace_bytes(int N, int Hq, int Hkv, int d, int max_pages, int window) {
+    if (decode_args(N, Hq, Hkv, d, 1, max_pages, window, 1.f, 0) != GDR_OK) return 0;
+    int per = 0;
+    const int splits = gdr::attn_decode_splits(N, Hq, Hkv, max_pages, window, &per);
+    return splits > 1 ? (size_t)splits * N * Hq * (d + 2) * sizeof(float) : 0;
+}
+
+gdr_status gdr_attn_decode(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                           const float* v_scale, const int* block_table, const int* cache_len, void* o, int N,
+                           int Hq, int Hkv, int d, int n_pages, int max_pages, int window, float scale,
+                           uint32_t flags, void* workspace, size_t workspace_bytes, void* stream) {
+    const gdr_status st = decode_args(N, Hq, Hkv, d, n_pages, max_pages, window, scale, flags);
+    if (st != GDR_OK) return st;
+    const void* ptrs[] = {q, k_cache, v_cache, k_scale, v_scale, block_table, cache_len, o};
+    for (const void* ptr : ptrs)
+        if (!ptr || !aligned16(ptr)) return GDR_ERR_INVALID_ARG;
+    if (workspace && !aligned16(workspace)) return GDR_ERR_INVALID_ARG;
+    const size_t need = gdr_attn_decode_workspace_bytes(N, Hq, Hkv, d, max_pages, window);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return GDR_ERR_WORKSPACE;
+    gdr_status ds = check_device();
+    if (ds != GDR_OK) return ds;
+    gdr::AttnDecodeParams p;
+    p.q = q;
+    p.k_cache = static_cast<const uint8_t*>(k_cache); p.v_cache = static_cast<const uint8_t*>(v_cache);
+    p.k_scale = k_scale; p.v_scale = v_scale; p.block_table = block_table; p.cache_len = cache_len; p.o = o;
+    p.N = N; p.Hq = Hq; p.Hkv = Hkv; p.d = d; p.n_pages = n_pages; p.max_pages = max_pages; p.window = window;
+    p.splits = gdr::attn_decode_splits(N, Hq, Hkv, max_pages, window, &p.split_pages);
+    p.part_o = need > 0 ? static_cast<float*>(workspace) : nullptr;
+    p.part_ml = need > 0 ? p.part_o + (size_t)p.splits * N * Hq * d : nullptr;
+    p.scale = scale; p.flags = flags;
+    return from_hip(gdr::launch_attn_decode(p, (hipStream_t)stream));
 }
 
 }  // extern "C"

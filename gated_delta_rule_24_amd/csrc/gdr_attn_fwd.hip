@@ -1,0 +1,236 @@
+// Causal attention, forward, over the whole past or a window, packed sequences
+// and shared key heads included:
+//   s_ij = scale q_i . k_j   (j <= p_i, j > p_i - window, same sequence; p_i = i + Tk - Tq)
+//   o_i = sum_j exp(s_ij - m_i) v_j / l_i,  lse_i = m_i + log l_i
+// in one pass over the keys with a running maximum m and sum l (fp32).
+//
+// A workgroup takes 128 queries of one head, 32 per wave, and walks the keys they
+// see in tiles of 64, staged through LDS by direct loads one tile ahead.
+//   S^T[key][query] = K Q^T      (32x32x16 MFMA, queries in registers throughout)
+//   O^T[channel][query] += V^T P^T
+// Both leave a lane with one query (column lane & 31), so the maximum, the sum
+// and the rescaling are per lane, and S^T's registers are P^T's operand as they
+// stand: an MFMA contracts over any order of the keys that both operands share,
+// so the value operand is read with the same order (transposing LDS reads).
+#include "gdr_attn_tile.h"
+
+namespace gdr {
+
+using namespace attn;
+
+namespace {
+
+constexpr int kBM = 128, kBN = 64, kWaves = 4;
+
+template <int D>
+struct __attribute__((aligned(16))) FwdSmem {
+    uint16_t k[2][kBN * D];
+    uint16_t v[2][kBN * D];
+    int bound[kBM];
+    int shared[2];
+    int bad[kWaves];
+};
+
+// The wave's 32 rows from the definition (see dot_row); lane r % 32 holds row r's
+// key range.
+template <int D>
+__device__ __forceinline__ void rows_one_by_one(const AttnParams& p, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                                                uint16_t* o, float* lse, int first, int used, int lo32, int hi32, int lane) {
+    const float to2 = p.scale * kLog2e;
+    for (int r = 0; r < 32 && first + r < used; ++r) {
+        const int lo = __builtin_amdgcn_readlane(lo32, r), hi = __builtin_amdgcn_readlane(hi32, r);
+        const uint16_t* qr = q + (long long)(first + r) * p.sq.t;
+        float m = -INFINITY, l = 0.f, acc[D / 64] = {};
+        for (int j = lo + lane; j < hi; j += 64) m = fmaxf(m, dot_row<D>(qr, k + (long long)j * p.sk.t) * to2);
+        for (int x = 32; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor(m, x, 64));
+        const float shift = m == -INFINITY ? 0.f : m;
+        for (int j0 = lo; j0 < hi; j0 += 64) {
+            float w = 0.f;
+            if (j0 + lane < hi) w = __builtin_amdgcn_exp2f(dot_row<D>(qr, k + (long long)(j0 + lane) * p.sk.t) * to2 - shift);
+            l += w;
+            add_rows<D>(acc, w, v + (long long)j0 * p.sk.t, p.sk.t, min(64, hi - j0), lane);
+        }
+        for (int x = 32; x > 0; x >>= 1) l += __shfl_xor(l, x, 64);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) o[(long long)(first + r) * p.sq.t + lane + 64 * c] = f32_to_bf16(acc[c] * inv);
+        if (lse && lane == 0) lse[first + r] = hi <= lo ? -INFINITY : shift / kLog2e + logf(l);
+    }
+}
+
+}  // namespace
+
+template <int D>
+__global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_kernel(AttnParams p, int tiles) {
+    constexpr int KS = D / 16, DB = D / 32;
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    FwdSmem<D>& sm = *reinterpret_cast<FwdSmem<D>*>(smem);
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int col = lane & 31, h = lane >> 5;
+
+    int unit, tile;
+    work_item(blockIdx.x, p.B * p.Hq, tiles, unit, tile);
+    tile = tiles - 1 - tile;                          // the rows that see most keys first
+    const int b = unit / p.Hq, hq = unit % p.Hq, hk = hq / (p.Hq / p.Hkv);
+    const int r0 = tile * kBM;
+
+    int used = p.Tq;
+    if (p.cu_seqlens) {
+        row_bounds<kBM, false>(p.cu_seqlens, p.nseq, p.Tq, r0, sm.bound, sm.shared, tid, 64 * kWaves, used);
+        if (r0 >= used) return;
+    }
+    const int row = r0 + 32 * wave + col;
+    const int at = row + p.Tk - p.Tq;                 // the query's place among the keys
+    const bool live = row < used;
+    int lo = p.cu_seqlens ? sm.bound[32 * wave + col] : 0, hi = live ? at + 1 : 0;
+    if (p.window > 0 && at - p.window + 1 > lo) lo = at - p.window + 1;
+    if (hi <= lo) { lo = 0; hi = 0; }                 // sees nothing
+    // the workgroup's keys: rows are in order, so their first and last rows bound them
+    const int last_row = min(r0 + kBM, used) - 1;
+    const int end = last_row + p.Tk - p.Tq + 1;
+    int begin = p.cu_seqlens ? sm.bound[0] : 0;
+    if (p.window > 0) begin = max(begin, r0 + p.Tk - p.Tq - p.window + 1);
+    begin = max(begin, 0);
+    // keys from lo_most on and below hi_least are seen by every row
+    int lo_most = p.cu_seqlens ? sm.bound[max(last_row - r0, 0)] : 0;
+    if (p.window > 0) lo_most = max(lo_most, last_row + p.Tk - p.Tq - p.window + 1);
+    const int hi_least = r0 + p.Tk - p.Tq + 1;
+
+    const uint16_t* qp = (const uint16_t*)p.q + b * p.sq.b + hq * p.sq.h;
+    const uint16_t* kp = (const uint16_t*)p.k + b * p.sk.b + hk * p.sk.h;
+    const uint16_t* vp = (const uint16_t*)p.v + b * p.sk.b + hk * p.sk.h;
+
+    bf8v qf[KS];
+    {
+        const uint16_t* qr = qp + (long long)min(row, p.Tq - 1) * p.sq.t + 8 * h;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) qf[s] = __builtin_bit_cast(bf8v, *reinterpret_cast<const uint4*>(qr + 16 * s));
+    }
+    float16v o[DB];
+#pragma unroll
+    for (int i = 0; i < DB; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[i][j] = 0.f;
+    float m = -INFINITY, l = 0.f;
+    const float to2 = p.scale * kLog2e;
+
+    const int j_first = begin / kBN * kBN;
+    const int n = end > begin ? (end - j_first + kBN - 1) / kBN : 0;
+    if (n > 0) {
+        stage<D, kBN, kWaves>(kp, p.sk.t, j_first, p.Tk - 1, sm.k[0], wave, lane);
+        stage<D, kBN, kWaves>(vp, p.sk.t, j_first, p.Tk - 1, sm.v[0], wave, lane);
+    }
+    bool bad = false;
+    for (int it = 0; it < n; ++it) {
+        const int j0 = j_first + it * kBN, buf = it & 1;
+        __builtin_amdgcn_s_waitcnt(0x0f70);           // vmcnt(0): this tile's loads
+        lds_barrier();
+        if (it + 1 < n) {
+            stage<D, kBN, kWaves>(kp, p.sk.t, j0 + kBN, p.Tk - 1, sm.k[buf ^ 1], wave, lane);
+            stage<D, kBN, kWaves>(vp, p.sk.t, j0 + kBN, p.Tk - 1, sm.v[buf ^ 1], wave, lane);
+        }
+        // tiles that some row of the workgroup sees in part: infinities and NaN among
+        // values that are masked for a row must not reach it through 0 * inf
+        const bool inner = j0 >= lo_most && j0 + kBN <= hi_least;
+        if (!inner) {
+            const bool mine = any_not_finite<D>(sm.v[buf] + 16 * wave * D, lane);
+            if (lane == 0) sm.bad[wave] = mine;
+            lds_barrier();
+            bad = (sm.bad[0] | sm.bad[1] | sm.bad[2] | sm.bad[3]) != 0;
+            if (bad) break;
+        }
+        if (__any(hi > j0 && lo < j0 + kBN)) {
+            const uint16_t* kt = sm.k[buf];
+            const uint16_t* vt = sm.v[buf];
+            float16v st[2];
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) st[kb][j] = 0.f;
+#pragma unroll
+                for (int s = 0; s < KS; ++s)
+                    st[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(row_frag<D>(kt, 32 * kb + col, 2 * s + h), qf[s], st[kb], 0, 0, 0);
+            }
+            if (__any(lo > j0 || hi < j0 + kBN)) {
+                const int base = j0 + 4 * h - lo;
+                const unsigned seen = (unsigned)(hi - lo);
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if ((unsigned)(base + 32 * kb + 8 * (i / 4) + i % 4) >= seen) st[kb][i] = -INFINITY;
+            }
+            float top = m;
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) top = fmaxf(top, st[kb][i]);
+            top = max_across32(top);
+            const float shift = top == -INFINITY ? 0.f : top * to2;
+            const float fade = m == top ? 1.f : __builtin_amdgcn_exp2f((m - top) * to2);
+            m = top;
+            float sum = 0.f;
+            bf8v pf[4];
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float x = __builtin_amdgcn_exp2f(st[kb][i] * to2 - shift);
+                    sum += x;
+                    pf[2 * kb + i / 8][i % 8] = (__bf16)x;
+                }
+            l = l * fade + sum;
+            if (__any(fade != 1.f)) {
+#pragma unroll
+                for (int i = 0; i < DB; ++i) o[i] *= fade;
+            }
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int i = 0; i < DB; ++i)
+                    o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(col_frag<D>(vt, 16 * s, i, lane), pf[s], o[i], 0, 0, 0);
+        }
+    }
+    if (bad) {
+        __builtin_amdgcn_s_waitcnt(0x0f70);           // no load into LDS outlives the wave
+        rows_one_by_one<D>(p, qp, kp, vp, (uint16_t*)p.o + b * p.sq.b + hq * p.sq.h,
+                           p.lse ? p.lse + ((long long)b * p.Hq + hq) * p.Tq : nullptr, r0 + 32 * wave, used, lo, hi, lane);
+        return;
+    }
+
+    l = sum_across32(l);
+    if (live) {
+        // a row that saw nothing has l = 0: its output is 0, its log-sum-exp -inf
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        uint16_t* orow = (uint16_t*)p.o + b * p.sq.b + hq * p.sq.h + (long long)row * p.sq.t;
+#pragma unroll
+        for (int i = 0; i < DB; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint2 u = make_uint2(pack_bf16(o[i][4 * j] * inv, o[i][4 * j + 1] * inv),
+                                           pack_bf16(o[i][4 * j + 2] * inv, o[i][4 * j + 3] * inv));
+                *reinterpret_cast<uint2*>(orow + 32 * i + 8 * j + 4 * h) = u;
+            }
+        if (p.lse && h == 0)
+            p.lse[((long long)b * p.Hq + hq) * p.Tq + row] = hi <= lo ? -INFINITY : m * p.scale + logf(l);
+    }
+}
+
+template <int D>
+static hipError_t launch_fwd_d(const AttnParams& p, hipStream_t st) {
+    static std::atomic<unsigned long long> done{0};
+    const void* fn = reinterpret_cast<const void*>(&attn_fwd_kernel<D>);
+    const hipError_t e = ensure_dyn_lds(fn, (int)sizeof(FwdSmem<D>), done);
+    if (e != hipSuccess) return e;
+    const int tiles = (p.Tq + kBM - 1) / kBM;
+    if (tiles == 0) return hipSuccess;
+    hipLaunchKernelGGL((attn_fwd_kernel<D>), dim3((unsigned)((long long)p.B * p.Hq * tiles)), dim3(64 * kWaves),
+                       sizeof(FwdSmem<D>), st, p, tiles);
+    return hipGetLastError();
+}
+
+hipError_t launch_attn_fwd(const AttnParams& p, hipStream_t st) {
+    return p.d == 64 ? launch_fwd_d<64>(p, st) : launch_fwd_d<128>(p, st);
+}
+
+}  // namespace gdr

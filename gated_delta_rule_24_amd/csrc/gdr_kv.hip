@@ -1,0 +1,493 @@
+// The paged 8-bit key/value cache: append of new tokens, and attention of one
+// query token per sequence over it.
+//
+// A page holds 64 tokens of every key head: keys [64][d], values [4][d][16]
+// (16 tokens side by side, so that a lane's 16-byte load is one channel of 16
+// tokens: the value operand of the matrix instruction, no transposing).  Values
+// are e4m3; a (page, head) has one scale for its keys and one for its values,
+// a power of two, so that a scale that grows later re-rounds only what falls
+// below the type's normal range.
+#include "gdr_device.h"
+#include "gdr_attn.h"
+
+namespace gdr {
+
+namespace {
+
+constexpr int kPage = 64;
+
+// 2^e, -126 <= e <= 127
+__device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// Exponent of the smallest power of two s >= 2^-96 with top <= 448 s, from
+// top = m 2^x, 1 <= m < 2, and 448 = 1.75 * 2^8 (0 and subnormals give the floor).
+__device__ __forceinline__ int scale_exponent(float top) {
+    const uint32_t u = __float_as_uint(top);
+    const int x = (int)(u >> 23) - 127;
+    const int e = x - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return e < -96 ? -96 : e;
+}
+
+__device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d) {
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+}
+
+// four e4m3 values times a power of two r <= 1, rounded again
+__device__ __forceinline__ uint32_t rescale_e4m3x4(uint32_t w, float r) {
+    return to_e4m3x4(__builtin_amdgcn_cvt_f32_fp8(w, 0) * r, __builtin_amdgcn_cvt_f32_fp8(w, 1) * r,
+                     __builtin_amdgcn_cvt_f32_fp8(w, 2) * r, __builtin_amdgcn_cvt_f32_fp8(w, 3) * r);
+}
+
+__device__ __forceinline__ int clampi(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// append
+// ---------------------------------------------------------------------------
+//
+// One workgroup owns one (touched page, head): it reads the new tokens that fall
+// into the page (1 to 64), takes their largest magnitude, raises the scale if
+// need be (then it re-rounds the page's older tokens), and writes the new ones.
+// Bound by HBM for prompts (2 bytes read, 1 written per value) and by latency
+// for one token.  The page's other slots are left as they were.
+template <int D>
+__global__ __launch_bounds__(256) void kv_append_kernel(KvAppendParams p) {
+    constexpr int VPT = D / 8;                        // 16-byte vectors of a token
+    constexpr int NV = kPage * VPT / 256;             // vectors a thread may hold
+    __shared__ __attribute__((aligned(16))) uint8_t tile[kPage * D];
+    __shared__ float s_top[8];
+    __shared__ int s_work[4];
+    const int tid = threadIdx.x, h = blockIdx.y;
+
+    // which page: sequence, page of it, first new slot, new tokens, their first row
+    int seq = blockIdx.x, page_i, off, n, row;
+    if (p.cu_seqlens == nullptr) {
+        const int len = max(p.cache_len[seq], 0);
+        page_i = len / kPage;
+        off = len % kPage;
+        n = 1;
+        row = seq;
+    } else {
+        // item blockIdx.x of the sequences' touched pages in order: a running
+        // sum over 256 sequences at a time
+        if (tid == 0) s_work[0] = -1;
+        int before = 0;
+        bool found = false;
+        for (int s0 = 0; s0 < p.nseq && !found; s0 += 256) {
+            const int s = s0 + tid;
+            int cnt = 0, a = 0, m = 0, len = 0;
+            if (s < p.nseq) {
+                a = clampi(p.cu_seqlens[s], 0, p.T);
+                m = clampi(p.cu_seqlens[s + 1], a, p.T) - a;
+                len = max(p.cache_len[s], 0);
+                cnt = m > 0 ? (len % kPage + m + kPage - 1) / kPage : 0;
+            }
+            int run = cnt;
+            for (int o = 1; o < 64; o <<= 1) {
+                const int y = __shfl_up(run, o, 64);
+                if ((tid & 63) >= o) run += y;
+            }
+            __syncthreads();
+            if ((tid & 63) == 63) s_top[tid >> 6] = __int_as_float(run);
+            __syncthreads();
+            int base = before, total = 0;
+            for (int w = 0; w < 4; ++w) {
+                const int c = __float_as_int(s_top[w]);
+                if (w < (tid >> 6)) base += c;
+                total += c;
+            }
+            const int end = base + run, begin = end - cnt, item = blockIdx.x;
+            if (item >= begin && item < end) {
+                const int i = item - begin, o = len % kPage;
+                const int from = i == 0 ? 0 : i * kPage - o;      // first of the sequence's new tokens here
+                s_work[1] = len / kPage + i;
+                s_work[2] = i == 0 ? o : 0;
+                s_work[3] = a + from;
+                s_work[0] = s;
+                s_top[4] = __int_as_float(min(m - from, kPage - (i == 0 ? o : 0)));
+            }
+            __syncthreads();
+            found = s_work[0] >= 0;
+            before += total;
+        }
+        if (!found) return;
+        seq = s_work[0]; page_i = s_work[1]; off = s_work[2]; row = s_work[3];
+        n = __float_as_int(s_top[4]);
+        __syncthreads();
+    }
+    if (page_i >= p.max_pages) return;                // past the table: dropped
+    const int page = p.block_table[(size_t)seq * p.max_pages + page_i];
+    if ((unsigned)page >= (unsigned)p.n_pages) return;
+
+    const size_t ph = (size_t)page * p.Hkv + h;
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+        const uint16_t* src = (const uint16_t*)(side ? p.v : p.k) + (long long)row * p.st + (long long)h * p.sh;
+        uint8_t* dst = (side ? p.v_cache : p.k_cache) + ph * (kPage * D);
+        float* scale_at = (side ? p.v_scale : p.k_scale) + ph;
+        const float old = off > 0 ? *scale_at : 0.f;
+        uint4 x[NV];
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int vec = tid + 256 * i, t = vec / VPT, c = vec % VPT;
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (t < n) x[i] = *reinterpret_cast<const uint4*>(src + (long long)t * p.st + 8 * c);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {             // infinities and NaN have no part in the scale
+                const float a = fabsf(__uint_as_float(w[j] << 16)), b = fabsf(__uint_as_float(w[j] & 0xffff0000u));
+                if (a < INFINITY) top = fmaxf(top, a);
+                if (b < INFINITY) top = fmaxf(top, b);
+            }
+        }
+        for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+        __syncthreads();
+        if ((tid & 63) == 0) s_top[tid >> 6] = top;
+        __syncthreads();
+        top = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
+        const int e = scale_exponent(top);
+        const float s = fmaxf(old, exp2_int(e)), inv = 1.f / s;      // exact: powers of two
+        const bool grew = off > 0 && s != old;
+        const float r = old * inv;
+        if (tid == 0) *scale_at = s;
+        // the new tokens' bytes: keys straight to their rows, values through LDS
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int vec = tid + 256 * i, t = vec / VPT, c = vec % VPT;
+            if (t < n) {
+                const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                float f[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    f[2 * j] = __uint_as_float(w[j] << 16) * inv;
+                    f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u) * inv;
+                }
+                const uint2 y = make_uint2(to_e4m3x4(f[0], f[1], f[2], f[3]), to_e4m3x4(f[4], f[5], f[6], f[7]));
+                if (side == 0) *reinterpret_cast<uint2*>(dst + (size_t)(off + t) * D + 8 * c) = y;
+                else *reinterpret_cast<uint2*>(tile + (off + t) * D + 8 * c) = y;
+            }
+        }
+        if (side == 0) {
+            if (grew)
+                for (int vec = tid; vec < off * (D / 16); vec += 256) {
+                    uint4* at = reinterpret_cast<uint4*>(dst + (size_t)vec * 16);
+                    const uint4 y = *at;
+                    *at = make_uint4(rescale_e4m3x4(y.x, r), rescale_e4m3x4(y.y, r), rescale_e4m3x4(y.z, r),
+                                     rescale_e4m3x4(y.w, r));
+                }
+        } else {
+            __syncthreads();
+            const int lo = grew ? 0 : off, hi = off + n;
+            // 16 slots of one channel: written whole where all are new, else the
+            // new bytes one by one, or (scale grown) read, re-rounded and merged
+            for (int vec = tid; vec < 4 * D; vec += 256) {
+                const int g = vec / D, c = vec % D, first = 16 * g;
+                if (first >= hi || first + 16 <= lo) continue;
+                uint8_t* at = dst + (size_t)vec * 16;
+                if (!grew && (first < off || first + 16 > hi)) {
+                    for (int j = max(first, off); j < min(first + 16, hi); ++j) at[j - first] = tile[j * D + c];
+                    continue;
+                }
+                uint32_t w[4] = {0, 0, 0, 0};
+                if (first < off || first + 16 > hi) {
+                    const uint4 y = *reinterpret_cast<const uint4*>(at);
+                    w[0] = y.x; w[1] = y.y; w[2] = y.z; w[3] = y.w;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t again = rescale_e4m3x4(w[j], r);
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const int slot = first + 4 * j + b;
+                        const uint32_t m = 0xffu << (8 * b);
+                        if (slot < off) w[j] = (w[j] & ~m) | (again & m);
+                        else if (slot < hi) w[j] = (w[j] & ~m) | ((uint32_t)tile[slot * D + c] << (8 * b));
+                    }
+                }
+                *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+    }
+}
+
+hipError_t launch_kv_append(const KvAppendParams& p, hipStream_t st) {
+    // a sequence's m new tokens touch at most m / 64 + 2 pages
+    const long long items = p.cu_seqlens ? (long long)p.T / kPage + 2LL * p.nseq : p.nseq;
+    dim3 grid((unsigned)items, (unsigned)p.Hkv), block(256);
+    if (p.d == 64) hipLaunchKernelGGL((kv_append_kernel<64>), grid, block, 0, st, p);
+    else hipLaunchKernelGGL((kv_append_kernel<128>), grid, block, 0, st, p);
+    return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// decode
+// ---------------------------------------------------------------------------
+//
+// o = sum_j p_j v_j / sum_j p_j, p_j = exp2(s_j - m), s_j = scale log2(e) q.k_j,
+// over the last `window` of the cached tokens (all: window 0).  Two bytes are
+// read per token and channel, and that is the bound: everything else fits beside
+// the reads.  A workgroup takes one run of pages of one (sequence, key head); its
+// four waves take pages in turn, each with its own running maximum and sum, and
+// join at the end.  Up to 16 query heads share the key head's reads as the 16
+// columns of one matrix instruction.
+//   scores  S^T[key][query] = K Q^T: a lane loads 16 bytes of a key's row (two
+//           instructions' worth); the key a tile's row m stands for is
+//           16 (m / 4) + 4 tile + m % 4, which leaves lane group g with the
+//           scores of keys 16 g .. 16 g + 15: the keys of its value loads.
+//   output  O^T[channel][query] += V^T P^T with P as the sum of two bf16 values:
+//           16 bits of it count, and an fp32 result keeps them (one bf16 leaves
+//           2^-9 per weight).
+// e4m3 is exact in bf16; the scales multiply the scores and the weights in fp32.
+namespace {
+
+constexpr int kDecWaves = 4;
+
+template <int D>
+struct DecodeSmem {
+    float o[kDecWaves][16][D + 4];
+    float ml[kDecWaves][16][2];
+};
+
+__device__ __forceinline__ bf8v e4m3x8_to_bf16(uint32_t a, uint32_t b) {
+    const bf2v x0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, false);
+    const bf2v x1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, true);
+    const bf2v x2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, false);
+    const bf2v x3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, true);
+    bf8v r;
+    r[0] = x0[0]; r[1] = x0[1]; r[2] = x1[0]; r[3] = x1[1];
+    r[4] = x2[0]; r[5] = x2[1]; r[6] = x3[0]; r[7] = x3[1];
+    return r;
+}
+
+__device__ __forceinline__ void store_out(const AttnDecodeParams& p, size_t idx, float x) {
+    if (p.flags & GDR_OUT_BF16) reinterpret_cast<uint16_t*>(p.o)[idx] = f32_to_bf16(x);
+    else reinterpret_cast<float*>(p.o)[idx] = x;
+}
+
+// first and one past the last cached token a query of this sequence sees
+__device__ __forceinline__ void decode_range(const AttnDecodeParams& p, int n, int& lo, int& hi) {
+    const long long room = (long long)p.max_pages * kPage;
+    const int len = p.cache_len[n];
+    hi = len < 0 ? 0 : (int)(len > room ? room : len);
+    lo = (p.window > 0 && len > p.window) ? min(len - p.window, hi) : 0;
+}
+
+}  // namespace
+
+template <int D>
+__global__ __launch_bounds__(64 * kDecWaves) void attn_decode_kernel(AttnDecodeParams p, int groups) {
+    constexpr int KS = D / 64;                        // 64-channel steps of a key row
+    constexpr int VT = D / 16;                        // 16-channel tiles of the output
+    __shared__ DecodeSmem<D> sm;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int col = lane & 15, g = lane >> 4;
+    int w = blockIdx.x;
+    const int qg = w % groups; w /= groups;
+    const int kh = w % p.Hkv; w /= p.Hkv;
+    const int n = w, split = blockIdx.y;
+    const int G = p.Hq / p.Hkv, q0 = kh * G + 16 * qg, nq = min(16, G - 16 * qg);
+
+    int lo, hi;
+    decode_range(p, n, lo, hi);
+    const int pg0 = lo / kPage + split * p.split_pages;
+    const int pg1 = min(pg0 + p.split_pages, (hi + kPage - 1) / kPage);
+    const bool none = pg0 >= pg1;
+    if (none && split > 0) return;                    // the join leaves this split out
+
+    // queries: column col, channels 64 s + 16 g + 8 half ..
+    bf8v qf[KS][2];
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (col < nq)
+                u = *reinterpret_cast<const uint4*>((const uint16_t*)p.q + ((size_t)n * p.Hq + q0 + col) * D + 64 * s +
+                                                    16 * g + 8 * hf);
+            qf[s][hf] = __builtin_bit_cast(bf8v, u);
+        }
+
+    float4v o[VT];
+#pragma unroll
+    for (int i = 0; i < VT; ++i) o[i] = float4v{0.f, 0.f, 0.f, 0.f};
+    float m = -INFINITY, l = 0.f;
+    const float to2 = p.scale * 1.4426950408889634f;
+    const int krow = 16 * (col >> 2) + (col & 3);     // key of tile 0's row `col`
+
+    for (int pg = pg0 + wave; pg < pg1; pg += kDecWaves) {
+        int page = p.block_table[(size_t)n * p.max_pages + pg];
+        const int first = pg * kPage;
+        const bool absent = (unsigned)page >= (unsigned)p.n_pages;
+        if (absent) page = 0;
+        const size_t ph = (size_t)page * p.Hkv + kh;
+        const uint8_t* kp = p.k_cache + ph * (kPage * D);
+        const uint8_t* vp = p.v_cache + ph * (kPage * D);
+        uint4 kk[4][KS], vv[VT];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+                kk[t][s] = *reinterpret_cast<const uint4*>(kp + (krow + 4 * t) * D + 64 * s + 16 * g);
+#pragma unroll
+        for (int i = 0; i < VT; ++i)
+            vv[i] = *reinterpret_cast<const uint4*>(vp + (size_t)(g * D + 16 * i + col) * 16);
+        const float ks = p.k_scale[ph] * to2, vs = p.v_scale[ph];
+
+        float4v sc[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            sc[t] = float4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e4m3x8_to_bf16(kk[t][s].x, kk[t][s].y), qf[s][0], sc[t], 0, 0, 0);
+                sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e4m3x8_to_bf16(kk[t][s].z, kk[t][s].w), qf[s][1], sc[t], 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sc[t][i] *= ks;
+        }
+        if (absent || first < lo || first + kPage > hi) {
+            // the first and last pages: masked keys count nothing, whatever their bytes
+            uint32_t keep[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                keep[t] = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int j = first + 16 * g + 4 * t + i;
+                    const bool in = !absent && j >= lo && j < hi;
+                    if (!in) sc[t][i] = -INFINITY;
+                    else keep[t] |= 0xffu << (8 * i);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < VT; ++i) {
+                vv[i].x &= keep[0]; vv[i].y &= keep[1]; vv[i].z &= keep[2]; vv[i].w &= keep[3];
+            }
+        }
+        float top = m;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[t][i]);
+        top = fmaxf(top, __shfl_xor(top, 16, 64));
+        top = max_across32(top);
+        const float at = top == -INFINITY ? 0.f : top;
+        const float fade = __builtin_amdgcn_exp2f(m - at);           // 0 from -inf
+        m = top;
+        l *= fade;
+#pragma unroll
+        for (int i = 0; i < VT; ++i) o[i] *= fade;
+        bf8v hi8[2], lo8[2];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float x = __builtin_amdgcn_exp2f(sc[t][i] - at);
+                l += x;
+                x *= vs;
+                const __bf16 a = (__bf16)x;
+                hi8[t >> 1][(t & 1) * 4 + i] = a;
+                lo8[t >> 1][(t & 1) * 4 + i] = (__bf16)(x - (float)a);
+            }
+#pragma unroll
+        for (int i = 0; i < VT; ++i) {
+            const bf8v v0 = e4m3x8_to_bf16(vv[i].x, vv[i].y), v1 = e4m3x8_to_bf16(vv[i].z, vv[i].w);
+            o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, hi8[0], o[i], 0, 0, 0);
+            o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, hi8[1], o[i], 0, 0, 0);
+            o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, lo8[0], o[i], 0, 0, 0);
+            o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, lo8[1], o[i], 0, 0, 0);
+        }
+    }
+
+    // join the waves: sums over the lane groups, then over the waves
+    l += __shfl_xor(l, 16, 64);
+    l = sum_across32(l);
+    if (g == 0) { sm.ml[wave][col][0] = m; sm.ml[wave][col][1] = l; }
+#pragma unroll
+    for (int i = 0; i < VT; ++i)
+        *reinterpret_cast<float4v*>(&sm.o[wave][col][16 * i + 4 * g]) = o[i];
+    __syncthreads();
+    for (int idx = threadIdx.x; idx < nq * D; idx += 64 * kDecWaves) {
+        const int c = idx / D, ch = idx % D;
+        float top = -INFINITY;
+#pragma unroll
+        for (int y = 0; y < kDecWaves; ++y) top = fmaxf(top, sm.ml[y][c][0]);
+        const float at = top == -INFINITY ? 0.f : top;
+        float sum = 0.f, x = 0.f;
+#pragma unroll
+        for (int y = 0; y < kDecWaves; ++y) {
+            const float f = __builtin_amdgcn_exp2f(sm.ml[y][c][0] - at);
+            sum += sm.ml[y][c][1] * f;
+            x += sm.o[y][c][ch] * f;
+        }
+        const size_t head = (size_t)n * p.Hq + q0 + c;
+        if (p.splits == 1) {
+            store_out(p, head * D + ch, top == -INFINITY && !(x != x) ? 0.f : x / sum);
+        } else {
+            const size_t at_row = (size_t)split * p.N * p.Hq + head;
+            p.part_o[at_row * D + ch] = x;
+            if (ch == 0) { p.part_ml[at_row * 2] = top; p.part_ml[at_row * 2 + 1] = sum; }
+        }
+    }
+}
+
+// Joins the splits that have pages: one thread per channel, one workgroup of
+// 256 threads per 256 / D heads.
+template <int D>
+__global__ __launch_bounds__(256) void attn_decode_join(AttnDecodeParams p) {
+    const size_t head = (size_t)blockIdx.x * (256 / D) + threadIdx.x / D;
+    const int ch = threadIdx.x % D;
+    const size_t rows = (size_t)p.N * p.Hq;
+    if (head >= rows) return;
+    int lo, hi;
+    decode_range(p, (int)(head / p.Hq), lo, hi);
+    const int pages = (hi + kPage - 1) / kPage - lo / kPage;
+    const int splits = max(1, (pages + p.split_pages - 1) / p.split_pages);
+    float top = -INFINITY;
+    for (int s = 0; s < splits; ++s) top = fmaxf(top, p.part_ml[(s * rows + head) * 2]);
+    const float at = top == -INFINITY ? 0.f : top;
+    float sum = 0.f, x = 0.f;
+    for (int s = 0; s < splits; ++s) {
+        const float f = __builtin_amdgcn_exp2f(p.part_ml[(s * rows + head) * 2] - at);
+        sum += p.part_ml[(s * rows + head) * 2 + 1] * f;
+        x += p.part_o[(s * rows + head) * D + ch] * f;
+    }
+    store_out(p, head * D + ch, top == -INFINITY && !(x != x) ? 0.f : x / sum);
+}
+
+int attn_decode_splits(int N, int Hq, int Hkv, int max_pages, int window, int* split_pages) {
+    const int G = Hq / Hkv, groups = (G + 15) / 16;
+    const long long base = (long long)N * Hkv * groups;
+    int pages = max_pages;
+    if (window > 0 && window / kPage + 2 < pages) pages = window / kPage + 2;
+    // at least two pages for each wave, and no more splits than fill the chip
+    // four times over
+    const long long want = (4LL * 768 + base - 1) / base;
+    long long per = (pages + want - 1) / want;
+    if (per < 2 * kDecWaves) per = 2 * kDecWaves;
+    *split_pages = (int)per;
+    const long long s = (pages + per - 1) / per;
+    return s < 1 ? 1 : (int)s;
+}
+
+hipError_t launch_attn_decode(const AttnDecodeParams& p, hipStream_t st) {
+    const int groups = (p.Hq / p.Hkv + 15) / 16;
+    dim3 grid((unsigned)((long long)p.N * p.Hkv * groups), (unsigned)p.splits), block(64 * kDecWaves);
+    if (p.d == 64) hipLaunchKernelGGL((attn_decode_kernel<64>), grid, block, 0, st, p, groups);
+    else hipLaunchKernelGGL((attn_decode_kernel<128>), grid, block, 0, st, p, groups);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.splits == 1) return e;
+    const int per = 256 / p.d;
+    dim3 jgrid((unsigned)(((long long)p.N * p.Hq + per - 1) / per));
+    if (p.d == 64) hipLaunchKernelGGL((attn_decode_join<64>), jgrid, block, 0, st, p);
+    else hipLaunchKernelGGL((attn_decode_join<128>), jgrid, block, 0, st, p);
+    return hipGetLastError();
+}
+
+}  // namespace gdr

@@ -103,6 +103,13 @@ typedef enum gdr_status {
                                     backward (workspace, bf16, chunk 64) and decode only;
                                     GDR_ERR_UNSUPPORTED elsewhere.                      */
 
+/* flags of the attention layer's calls (gdr_rope, gdr_attn_*, gdr_kv_append) */
+#define GDR_TOKEN_MAJOR      0x1000u /* tensors are [B, T, H, d] ([T, H, d] packed) instead
+                                        of [B, H, T, d] ([H, T, d])                  */
+#define GDR_ROPE_INTERLEAVED 0x2000u /* pairs of channels (2i, 2i + 1) instead of
+                                        (i, i + rot_dim / 2)                         */
+#define GDR_ROPE_INVERSE     0x4000u /* turn back: the transpose, which is the gradient  */
+
 #define GDR_ABI_VERSION 2
 
 int gdr_abi_version(void);
@@ -395,6 +402,157 @@ gdr_status gdr_mixer_epilogue_bwd(const float* o, const void* g, const float* no
                                   const float* dy, float* d_o, float* dg, float* dnorm_weight,
                                   int B, int H, int T, int d_v, uint32_t flags,
                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The attention layer of a hybrid stack.  Stacks of the gated delta rule put
+ * softmax attention layers between the recurrent ones, over a window of about
+ * 2,048 tokens ("Q&A page" Q5, "Gated DeltaNet-2 Review" hybrid cell) or over
+ * the whole past ("Gated DeltaNet explainer", three recurrent layers to one).
+ * The calls below are such a layer between the caller's projections: rotary
+ * positions, causal attention and its gradients for training and prompts, and
+ * for generation an 8-bit paged cache with its one-token attention.
+ *
+ * All of them: queries have Hq heads, keys and values Hkv heads, Hq a multiple
+ * of Hkv; query head h reads key head h / (Hq / Hkv).  Indexes and lengths in
+ * device memory (positions, cu_seqlens, block_table, cache_len) are not checked
+ * on the host; no content of them makes a kernel read or write outside the
+ * tensors.  Results do not depend on the order in which workgroups run.
+ */
+
+/*
+ * Rotary positions of queries and keys.  For channel pairs (a, b) of the first
+ * rot_dim channels, i < rot_dim / 2, at position t of the row:
+ *   theta = t * inv_freq[i],  y_a = scale (x_a cos theta - x_b sin theta),
+ *                             y_b = scale (x_b cos theta + x_a sin theta);
+ * GDR_ROPE_INVERSE turns by -theta (with the same scale: the gradient).  The
+ * other channels are copied.  Long contexts scale inv_freq and, where wanted,
+ * `scale`; the angle is formed in 64 bits, so far positions keep their accuracy.
+ *
+ *   q, q_out   : act  [B, Hq, T, d]       k, k_out : act [B, Hk, T, d]
+ *                (k and k_out are NULL when Hk = 0; q and q_out when Hq = 0;
+ *                an output may be its input, no other aliasing)
+ *   inv_freq   : fp32 [rot_dim / 2]
+ *   positions  : int32 [B, T] in device memory, or NULL: token t stands at
+ *                position0 + t
+ * Packed sequences: B = 1 and their positions.  One token of N sequences: B = N,
+ * T = 1.  Flags: GDR_ACT_F32, GDR_TOKEN_MAJOR, GDR_ROPE_INTERLEAVED,
+ * GDR_ROPE_INVERSE.  Supported: d in {16, 32, 64, 128}, rot_dim a multiple of 16
+ * up to d.
+ */
+gdr_status gdr_rope(const void* q, const void* k, void* q_out, void* k_out,
+                    const float* inv_freq, const int* positions, int position0,
+                    int B, int Hq, int Hk, int T, int d, int rot_dim, float scale,
+                    uint32_t flags, void* stream);
+
+/*
+ * Causal attention, forward.  Query i of Tq stands at place i + Tk - Tq among the
+ * Tk keys and sees the keys up to it, the last `window` of them when window > 0:
+ *   s_ij = scale q_i . k_j,  lse_i = log sum_j exp(s_ij),  o_i = sum_j exp(s_ij - lse_i) v_j.
+ * A query that sees no key (Tk < Tq) gets o = 0 and lse = -inf.  A key or value
+ * that a query does not see has no effect on it, NaN and infinities included.
+ *
+ *   q, o : bf16 [B, Hq, Tq, d]      k, v : bf16 [B, Hkv, Tk, d]
+ *   lse  : fp32 [B, Hq, Tq] in both layouts, written; NULL means not written
+ *   window : 0 (none) or the number of keys; scale > 0, finite
+ * Products run on bf16 MFMA with fp32 accumulation; the weights exp(s - m) are
+ * rounded to bf16 for the product with v (m the running maximum), their sum is
+ * kept in fp32.  Flags: GDR_TOKEN_MAJOR.  Supported: d in {64, 128};
+ * GDR_ERR_UNSUPPORTED otherwise (also for GDR_ACT_F32).  No workspace.
+ */
+gdr_status gdr_attn_fwd(const void* q, const void* k, const void* v, void* o, float* lse,
+                        int B, int Hq, int Hkv, int Tq, int Tk, int d, int window,
+                        float scale, uint32_t flags, void* stream);
+
+/*
+ * The same over packed sequences, as gdr_chunk_fwd_varlen packs them: q, o
+ * [Hq, T, d], k, v [Hkv, T, d], lse [Hq, T]; a query sees keys of its own
+ * sequence only.  cu_seqlens: int32 [nseq + 1] in device memory, non-decreasing
+ * from 0; rows from cu_seqlens[nseq] on (if it is below T) are not written.
+ */
+gdr_status gdr_attn_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* lse,
+                               const int* cu_seqlens, int nseq, int Hq, int Hkv, int T, int d,
+                               int window, float scale, uint32_t flags, void* stream);
+
+/*
+ * Gradients of gdr_attn_fwd for the loss <dO, o>: the probabilities are
+ * recomputed from lse, P = exp(s - lse), and
+ *   D_i = dO_i . o_i,  dS_ij = P_ij (dO_i . v_j - D_i),
+ *   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i P_ij dO_i,
+ * dk and dv summed over the query heads that share the key head, in a fixed order.
+ *
+ *   q, k, v, o, lse : as gdr_attn_fwd took and wrote them     dO : bf16, as o
+ *   dq : bf16, as q     dk, dv : bf16, as k   (written, never accumulated into;
+ *        keys that no query sees get 0)
+ *   workspace : device scratch of at least gdr_attn_bwd_workspace_bytes() bytes,
+ *        contents on entry ignored; calls that may overlap need one each
+ * Sums are fp32; P and dS are rounded to bf16 as operands.  Supported as
+ * gdr_attn_fwd.  The varlen call leaves rows from cu_seqlens[nseq] on unwritten.
+ */
+size_t gdr_attn_bwd_workspace_bytes(int B, int Hq, int Hkv, int Tq, int Tk, int d);
+
+gdr_status gdr_attn_bwd(const void* q, const void* k, const void* v, const void* o,
+                        const float* lse, const void* dO, void* dq, void* dk, void* dv,
+                        int B, int Hq, int Hkv, int Tq, int Tk, int d, int window,
+                        float scale, uint32_t flags, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+gdr_status gdr_attn_bwd_varlen(const void* q, const void* k, const void* v, const void* o,
+                               const float* lse, const void* dO, void* dq, void* dk, void* dv,
+                               const int* cu_seqlens, int nseq, int Hq, int Hkv, int T, int d,
+                               int window, float scale, uint32_t flags, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/*
+ * The paged 8-bit key/value cache.  A page holds GDR_KV_PAGE tokens of every
+ * key head as e4m3 values:
+ *   k_cache : uint8 [n_pages, Hkv, 64, d]      v_cache : uint8 [n_pages, Hkv, 4, d, 16]
+ *             (value of token 16 g + i and channel c at [g][c][i])
+ *   k_scale, v_scale : fp32 [n_pages, Hkv]; a value stands for e4m3 * scale
+ *   block_table : int32 [nseq, max_pages]: sequence n's token t is in page
+ *             block_table[n][t / 64], slot t % 64
+ *   cache_len : int32 [nseq]: tokens of each sequence in the cache
+ *
+ * gdr_kv_append writes new tokens behind the cache_len tokens of each sequence
+ * (cache_len itself is the caller's to raise).  Per touched page and head the
+ * scale becomes max(old, s), s the smallest power of two >= 2^-96 with every new
+ * finite |x| <= 448 s; old counts as 0 when the page's first slot is written.
+ * Values are round_e4m3(x / scale), to nearest even; infinities and NaN become
+ * NaN.  Where the scale grows, the page's older tokens are rounded again to it
+ * (exact but for values that fall below the normal range).  Slots behind the new
+ * tokens are left as they were.
+ *   k, v : bf16 [Hkv, T, d] ([T, Hkv, d] with GDR_TOKEN_MAJOR), sequence n's new
+ *          tokens cu_seqlens[n] .. cu_seqlens[n + 1] - 1; or cu_seqlens NULL:
+ *          [nseq, Hkv, d], one token of each sequence (T = nseq)
+ * Tokens past max_pages pages, or whose page is not in [0, n_pages), are dropped.
+ * The caller keeps two sequences of one call from writing to the same page.
+ * Supported: d in {64, 128}.
+ */
+#define GDR_KV_PAGE 64
+
+gdr_status gdr_kv_append(const void* k, const void* v, void* k_cache, void* v_cache,
+                         float* k_scale, float* v_scale, const int* block_table,
+                         const int* cache_len, const int* cu_seqlens, int nseq, int Hkv, int T,
+                         int d, int n_pages, int max_pages, uint32_t flags, void* stream);
+
+/*
+ * Attention of one query token per sequence over the cache: the query stands at
+ * the last of the cache_len tokens (append first) and sees all of them, or the
+ * last `window`.  A sequence of length 0 gets o = 0; tokens in pages outside
+ * [0, n_pages) count as masked; bytes of masked slots have no effect.
+ *   q : bf16 [N, Hq, d]       o : fp32 (or bf16 with GDR_OUT_BF16) [N, Hq, d]
+ *   workspace : device scratch of gdr_attn_decode_workspace_bytes() bytes (0:
+ *        none needed, may be NULL), contents on entry ignored; calls that may
+ *        overlap need one each
+ * Scores, weights and sums are fp32 (the weights enter the product as two bf16
+ * parts).  Flags: GDR_OUT_BF16.  Supported: d in {64, 128}.
+ */
+size_t gdr_attn_decode_workspace_bytes(int N, int Hq, int Hkv, int d, int max_pages, int window);
+
+gdr_status gdr_attn_decode(const void* q, const void* k_cache, const void* v_cache,
+                           const float* k_scale, const float* v_scale, const int* block_table,
+                           const int* cache_len, void* o, int N, int Hq, int Hkv, int d,
+                           int n_pages, int max_pages, int window, float scale, uint32_t flags,
+                           void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,373 @@
+"""gdr_attn_fwd / gdr_attn_bwd (and their packed forms) on the GPU against the
+definition in 64 bits, element by element within derived bounds."""
+import math
+
+import pytest
+import torch
+
+import gated_delta_rule_24_amd as gdr
+from tests import attn_reference as ref
+
+pytestmark = pytest.mark.gpu
+F64 = torch.float64
+
+
+def _inputs(B, Hq, Hkv, Tq, Tk, d, seed, by=1.0):
+    g = torch.Generator().manual_seed(seed)
+    mk = lambda H, T: (torch.randn((B, H, T, d), generator=g) * by).to(torch.bfloat16)  # noqa: E731
+    return dict(q=mk(Hq, Tq), k=mk(Hkv, Tk), v=mk(Hkv, Tk), dO=mk(Hq, Tq))
+
+
+def _give(x, packed, token_major):
+    x = x.transpose(1, 2).contiguous() if token_major else x
+    return (x[0] if packed else x).cuda()
+
+
+def _back(x, packed, token_major):
+    x = x[None] if packed else x
+    return (x.transpose(1, 2) if token_major else x).cpu().to(F64)
+
+
+def _within(name, got, want, tol):
+    both = torch.isfinite(want)
+    assert torch.equal(torch.isnan(got), torch.isnan(want)), name
+    inf = ~both & ~torch.isnan(want)
+    assert torch.equal(got[inf], want[inf]), name
+    off = (got - want).abs()[both] - tol[both]
+    assert off.numel() == 0 or float(off.max()) <= 0, f"{name}: {float(off.max()):.3g} over its bound"
+
+
+def _forward(x, window=0, cu=None, token_major=False, scale=None, **kw):
+    packed = cu is not None
+    q, k, v = (_give(x[n], packed, token_major) for n in "qkv")
+    if packed:
+        c = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        return gdr.attn_fwd_varlen(q, k, v, c, window=window, scale=scale, token_major=token_major, **kw)
+    return gdr.attn_fwd(q, k, v, window=window, scale=scale, token_major=token_major, **kw)
+
+
+def _backward(x, o, lse, window=0, cu=None, token_major=False, scale=None):
+    packed = cu is not None
+    q, k, v, dO = (_give(x[n], packed, token_major) for n in ("q", "k", "v", "dO"))
+    if packed:
+        c = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        return gdr.attn_bwd_varlen(q, k, v, o, lse, dO, c, window=window, scale=scale, token_major=token_major)
+    return gdr.attn_bwd(q, k, v, o, lse, dO, window=window, scale=scale, token_major=token_major)
+
+
+def _check(x, window=0, cu=None, token_major=False, scale=None, backward=True):
+    packed = cu is not None
+    y = {n: t.to(F64) for n, t in x.items()}
+    f = ref.attention(y["q"], y["k"], y["v"], window, scale, cu)
+    o, lse = _forward(x, window, cu, token_major, scale)
+    used = cu[-1] if packed else x["q"].shape[2]
+    cut = lambda t: t[:, :, :used]  # noqa: E731
+    _within("o", cut(_back(o, packed, token_major)), cut(f["o"]), cut(f["o_tol"]))
+    _within("lse", cut(lse[None].cpu().to(F64) if packed else lse.cpu().to(F64)), cut(f["lse"]), cut(f["lse_tol"]))
+    if backward:
+        r = ref.attention_bwd(y["q"], y["k"], y["v"], y["dO"], window, scale, cu)
+        got = _backward(x, o, lse, window, cu, token_major, scale)
+        ku = cu[-1] if packed else x["k"].shape[2]
+        for n in ("dq", "dk", "dv"):
+            u = used if n == "dq" else ku
+            _within(n, _back(got[n], packed, token_major)[:, :, :u], r[n][:, :, :u], r[n + "_tol"][:, :, :u])
+    return o, lse
+
+
+LENGTHS = [(1, 1), (2, 2), (31, 31), (32, 32), (33, 33), (63, 63), (64, 64), (65, 65), (127, 127), (128, 128),
+           (129, 129), (200, 200), (257, 257), (300, 300)]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Tq,Tk", LENGTHS)
+def test_lengths(Tq, Tk, d):
+    _check(_inputs(1, 2, 1, Tq, Tk, d, Tq), token_major=Tq % 2 == 0)
+
+
+@pytest.mark.parametrize("Tq,Tk", [(1, 300), (1, 64), (33, 300), (130, 259), (64, 65), (300, 33), (129, 1), (2, 1), (257, 128)])
+@pytest.mark.parametrize("window", [0, 40])
+def test_queries_at_the_end_of_the_keys(Tq, Tk, window):
+    """More keys than queries, and fewer: then the first rows see nothing."""
+    x = _inputs(2, 2, 2, Tq, Tk, 64, Tq + Tk)
+    o, lse = _check(x, window)
+    if Tk < Tq:
+        assert not bool(o[:, :, :Tq - Tk].any()) and bool((lse[:, :, :Tq - Tk] == -math.inf).all())
+
+
+@pytest.mark.parametrize("window", [1, 2, 31, 63, 64, 65, 100, 128, 299, 300, 10000])
+@pytest.mark.parametrize("d", [64, 128])
+def test_windows(window, d):
+    _check(_inputs(1, 2, 2, 300, 300, d, window), window)
+
+
+@pytest.mark.parametrize("B,Hq,Hkv", [(1, 1, 1), (2, 4, 1), (1, 6, 2), (3, 8, 8), (1, 12, 4), (1, 7, 1)])
+def test_heads(B, Hq, Hkv):
+    _check(_inputs(B, Hq, Hkv, 140, 140, 128, Hq), window=70, token_major=Hq % 2 == 0)
+
+
+@pytest.mark.parametrize("cu", [[0, 1], [0, 200], [0, 3, 3, 64, 65, 130, 200], [0, 0, 128, 200, 200], [0, 50, 150],
+                                [0, 0], list(range(0, 201, 1)), list(range(0, 201, 2)) + [200] * 700])
+@pytest.mark.parametrize("window,d", [(0, 64), (30, 128)])
+def test_packed(cu, window, d):
+    _check(_inputs(1, 4, 2, 200, 200, d, len(cu)), window, cu, token_major=len(cu) % 2 == 0)
+
+
+def test_rows_behind_the_last_sequence_are_left_alone():
+    x = _inputs(1, 2, 1, 200, 200, 64, 3)
+    q, k, v, dO = (_give(x[n], True, False) for n in ("q", "k", "v", "dO"))
+    cu = torch.tensor([0, 60, 131], dtype=torch.int32, device="cuda")
+    o, lse = torch.full_like(q, 7.0), torch.full((2, 200), 7.0, device="cuda")
+    gdr.gdr_attn_fwd_varlen(q, k, v, o, lse, cu, 2, 2, 1, 200, 64, 0, 0.125, 0)
+    assert bool((o[:, 131:] == 7).all()) and bool((lse[:, 131:] == 7).all()) and not bool((o[:, :131] == 7).all(-1).any())
+    dq, dk, dv = (torch.full_like(t, 7.0) for t in (q, k, v))
+    n = gdr.gdr_attn_bwd_workspace_bytes(1, 2, 1, 200, 200, 64)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    gdr.gdr_attn_bwd_varlen(q, k, v, o, lse, dO, dq, dk, dv, cu, 2, 2, 1, 200, 64, 0, 0.125, 0, ws, n)
+    for t in (dq, dk, dv):
+        assert bool((t[:, 131:] == 7).all()) and not bool((t[:, :131] == 7).all(-1).any())
+
+
+def test_bad_cu_seqlens_stay_inside():
+    """Values outside [0, T] are held inside; what comes out is unspecified, but
+    nothing outside the tensors is touched (guard rows stay)."""
+    x = _inputs(1, 2, 2, 150, 150, 64, 4)
+    for cu in ([-5, 70, 1000], [100, 20, 150], [0, 2 ** 31 - 1, -2 ** 31, 150]):
+        c = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        q, k, v, dO = (_give(x[n], True, False) for n in ("q", "k", "v", "dO"))
+        big = [torch.full((2 * 150 + 64, 64), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+        o, dq, dk, dv = (t[32:-32].view(2, 150, 64) for t in big)
+        lse = torch.zeros((2, 150), device="cuda")
+        gdr.gdr_attn_fwd_varlen(q, k, v, o, lse, c, len(cu) - 1, 2, 2, 150, 64, 0, 0.125, 0)
+        n = gdr.gdr_attn_bwd_workspace_bytes(1, 2, 2, 150, 150, 64)
+        ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+        gdr.gdr_attn_bwd_varlen(q, k, v, o, lse, dO, dq, dk, dv, c, len(cu) - 1, 2, 2, 150, 64, 0, 0.125, 0, ws, n)
+        torch.cuda.synchronize()
+        for t in big:
+            assert bool((t[:32] == 7).all()) and bool((t[-32:] == 7).all())
+
+
+@pytest.mark.parametrize("scale", [0.5, 1e-4, 3.0])
+def test_scales_and_large_scores(scale):
+    """Scores up to hundreds: one key takes the whole weight."""
+    _check(_inputs(1, 2, 2, 130, 130, 64, 5, by=2.0), scale=scale)
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("where", ["k", "v", "q", "dO"])
+@pytest.mark.parametrize("window,cu", [(0, None), (20, None), (0, [0, 90, 200])])
+def test_values_that_are_not_finite_reach_only_who_sees_them(value, where, window, cu):
+    d = 64
+    x = _inputs(1, 2, 1, 200, 200, d, 6)
+    x[where][0, 0, 90, 5] = value
+    packed = cu is not None
+    clean = _inputs(1, 2, 1, 200, 200, d, 6)
+    o, lse = _forward(x, window, cu)
+    o0, lse0 = _forward(clean, window, cu)
+    got, want = _back(o, packed, False), _back(o0, packed, False)
+    mask = ref.seen(200, 200, window, cu)
+    if where in ("k", "v"):
+        touched = mask[:, 90].nonzero()[:, 0]
+        hit = torch.zeros(200, dtype=torch.bool)
+        hit[touched] = True
+        f = ref.attention(*(clean[n].to(F64) for n in "qkv"), window, None, cu)
+        keep = (got - f["o"]).abs() <= f["o_tol"]
+        assert bool(keep[:, :, ~hit].all())
+        if where == "v":                     # its own channel only
+            bad = ~torch.isfinite(got)
+            assert bool(bad[:, :, hit, 5].all()) and not bool(bad[..., :5].any()) and not bool(bad[..., 6:].any())
+            if math.isinf(value):            # a positive weight times an infinity
+                assert bool((got[:, :, hit, 5] == value).all())
+        elif math.isnan(value):
+            assert bool(torch.isnan(got[:, :, hit]).all())
+    elif where == "q":
+        rows = torch.arange(200) != 90
+        assert torch.equal(got[:, :, rows], want[:, :, rows]) and torch.equal(got[:, 1], want[:, 1])
+    # backward from the clean forward's results: a gradient is touched only through a pair that is seen
+    b = _backward(x, o0, lse0, window, cu)
+    r = ref.attention_bwd(*(clean[n].to(F64) for n in ("q", "k", "v", "dO")), window, None, cu)
+    other_rows, other_keys = torch.ones(200, dtype=torch.bool), torch.ones(200, dtype=torch.bool)
+    if where in ("k", "v"):
+        other_rows[mask[:, 90]] = False
+        # a row's dS is touched at the key itself only, so other keys keep theirs
+        other_keys[90] = False
+    else:
+        other_rows[90] = False
+        other_keys[mask[90]] = False
+    heads = slice(None) if where in ("k", "v") else slice(0, 1)
+    for n, rows in (("dq", other_rows), ("dk", other_keys), ("dv", other_keys)):
+        g = _back(b[n], packed, False)[:, :, rows]
+        _within(n, g, r[n][:, :, rows], r[n + "_tol"][:, :, rows])
+    assert torch.equal(_back(b["dq"], packed, False)[:, 1:][:, :, other_rows],
+                       _back(_backward(clean, o0, lse0, window, cu)["dq"], packed, False)[:, 1:][:, :, other_rows]) or heads == slice(None)
+
+
+@pytest.mark.parametrize("where", ["v", "k", "q", "dO"])
+def test_nan_rows_come_out_as_the_formula_says(where):
+    """Against sums over the seen pairs only, NaN and infinities included."""
+    x = _inputs(1, 1, 1, 100, 100, 64, 16)
+    x[where][0, 0, 40, 3] = math.nan
+    x[where][0, 0, 70, 8] = math.nan
+    clean = _inputs(1, 1, 1, 100, 100, 64, 16)
+    y = {n: t.to(F64) for n, t in x.items()}
+    if where in ("v", "k", "q"):
+        o, _ = _forward(x, 25)
+        f = ref.attention(y["q"], y["k"], y["v"], 25)
+        got = _back(o, False, False)
+        assert torch.equal(torch.isnan(got), torch.isnan(f["o"]))
+    o0, lse0 = _forward(clean, 25)
+    b = _backward(x, o0, lse0, 25)
+    c = {n: t.to(F64) for n, t in clean.items()}
+    f = ref.attention(c["q"], c["k"], c["v"], 25)
+    # P from the scores of x with the clean log-sum-exp, as the call is given it
+    m = f["mask"]
+    z = torch.zeros((), dtype=F64)
+    P = torch.where(m, torch.exp(ref._dot(y["q"], y["k"]) * f["scale"] - f["lse"][..., None]), z)
+    dS = torch.where(m, P * (ref._dot(y["dO"], y["v"]) - (y["dO"] * f["o"]).sum(-1, keepdim=True)), z)
+    mt, Pt, dSt = m.t(), P.transpose(-1, -2), dS.transpose(-1, -2)
+
+    def nan_of(mask, w, t):
+        out = torch.zeros(w.shape[:-1] + (t.shape[-1],), dtype=F64)
+        for i in range(w.shape[-2]):
+            j = mask[i].nonzero()[:, 0]
+            out[..., i, :] = (w[..., i, j, None] * t[..., j, :]).sum(-2)
+        return torch.isnan(out)
+
+    assert torch.equal(torch.isnan(_back(b["dv"], False, False)), nan_of(mt, Pt, y["dO"]))
+    assert torch.equal(torch.isnan(_back(b["dk"], False, False)), nan_of(mt, dSt, y["q"]))
+    assert torch.equal(torch.isnan(_back(b["dq"], False, False)), nan_of(m, dS, y["k"]))
+
+
+def test_gradients_against_differences():
+    """<d, u> against central differences of the 64-bit loss along u."""
+    x = _inputs(1, 4, 2, 70, 70, 64, 7)
+    y = {n: t.to(F64) for n, t in x.items()}
+    o, lse = _forward(x, 33)
+    got = _backward(x, o, lse, 33)
+    r = ref.attention_bwd(y["q"], y["k"], y["v"], y["dO"], 33)
+    loss = lambda **a: float((ref.attention(a["q"], a["k"], a["v"], 33)["o"] * y["dO"]).sum())  # noqa: E731
+    g = torch.Generator().manual_seed(8)
+    for n in "qkv":
+        u = torch.randn(y[n].shape, generator=g, dtype=F64)
+        base = {m: y[m] for m in "qkv"}
+        eps = 1e-4
+        diff = (loss(**{**base, n: y[n] + eps * u}) - loss(**{**base, n: y[n] - eps * u})) / (2 * eps)
+        have = float((got["d" + n].cpu().to(F64) * u).sum())
+        # the bounds of the elements along u, and the differences' own eps^2 and 1e-16 / eps
+        assert abs(diff - have) <= float((r["d" + n + "_tol"] * u.abs()).sum()) + 1e-3
+
+
+@pytest.mark.parametrize("Tq,Tk,Hq,Hkv", [(300, 300, 4, 1), (1, 700, 2, 2), (500, 500, 8, 2)])
+def test_the_same_call_gives_the_same_bits(Tq, Tk, Hq, Hkv):
+    x = _inputs(2, Hq, Hkv, Tq, Tk, 128, 9)
+    o, lse = _forward(x, 200)
+    g = _backward(x, o, lse, 200)
+    for _ in range(3):
+        o2, lse2 = _forward(x, 200)
+        g2 = _backward(x, o2, lse2, 200)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2) and all(torch.equal(g[n], g2[n]) for n in g)
+
+
+def test_both_layouts_give_the_same_bits():
+    x = _inputs(2, 4, 2, 150, 150, 64, 10)
+    o, lse = _forward(x)
+    ot, lset = _forward(x, token_major=True)
+    assert torch.equal(ot.transpose(1, 2), o) and torch.equal(lse, lset)
+    g, gt = _backward(x, o, lse), _backward(x, ot, lset, token_major=True)
+    assert all(torch.equal(gt[n].transpose(1, 2), g[n]) for n in g)
+
+
+def test_empty_calls():
+    e = lambda T: torch.zeros((2, 2, T, 64), dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    o, lse = gdr.attn_fwd(e(0), e(5), e(5))
+    assert o.shape == (2, 2, 0, 64) and lse.shape == (2, 2, 0)
+    o, lse = gdr.attn_fwd(e(5) + 1, e(0), e(0))
+    assert not bool(o.any()) and bool((lse == -math.inf).all())
+    g = gdr.attn_bwd(e(5), e(0), e(0), o, lse, e(5) + 1)
+    assert not bool(g["dq"].any()) and g["dk"].shape == (2, 2, 0, 64)
+    g = gdr.attn_bwd(e(0), e(5), e(5), e(0), torch.zeros((2, 2, 0), device="cuda"), e(0))
+    assert not bool(g["dk"].any()) and not bool(g["dv"].any())
+
+
+def test_refusals():
+    x = torch.zeros((1, 2, 8, 64), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):
+        gdr.attn_fwd(x.float(), x, x)
+    with pytest.raises(ValueError):
+        gdr.attn_fwd(x, x, x[:, :, :4])
+    with pytest.raises(ValueError):
+        gdr.attn_fwd(x.transpose(1, 2), x, x)
+    with pytest.raises(ValueError):
+        gdr.attn_fwd_varlen(x[0], x[0], x[0], torch.tensor([0, 8], device="cuda"))     # int64
+    with pytest.raises(ValueError):
+        gdr.attn_fwd(x, x.cpu(), x)
+    with pytest.raises(gdr.GdrError):
+        gdr.attn_fwd(x, x, x, scale=-1.0)
+    with pytest.raises(gdr.GdrError):
+        gdr.attn_fwd(x, x, x, window=-3)
+    y = torch.zeros((1, 2, 8, 32), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(gdr.GdrError):
+        gdr.attn_fwd(y, y, y)
+    z = torch.zeros((1, 3, 8, 64), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(gdr.GdrError):
+        gdr.attn_fwd(z, x, x)
+    o, lse = gdr.attn_fwd(x, x, x)
+    with pytest.raises(ValueError):
+        gdr.attn_bwd(x, x, x, o, lse.double(), x)
+    with pytest.raises(ValueError):
+        gdr.attn_bwd(x, x, x, o.float(), lse, x)
+
+
+def test_streams_and_graphs():
+    """Two streams at once, and captured calls replayed between eager ones."""
+    x, y = _inputs(1, 4, 2, 260, 260, 64, 11), _inputs(1, 4, 2, 260, 260, 64, 12)
+    wx, wy = [], []
+    for inp, keep in ((x, wx), (y, wy)):
+        o, lse = _forward(inp, 100)
+        keep += [o, lse, *_backward(inp, o, lse, 100).values()]
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(3):
+        got = []
+        for s, inp in ((s1, x), (s2, y)):
+            with torch.cuda.stream(s):
+                o, lse = _forward(inp, 100)
+                got.append([o, lse, *_backward(inp, o, lse, 100).values()])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got[0], wx)) and all(torch.equal(a, b) for a, b in zip(got[1], wy))
+    q, k, v, dO = (x[n].cuda() for n in ("q", "k", "v", "dO"))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = gdr.attn_fwd(q, k, v, window=100)
+        g = gdr.attn_bwd(q, k, v, o, lse, dO, window=100)
+    for inp, want in ((x, wx), (y, wy), (x, wx)):
+        for t, n in ((q, "q"), (k, "k"), (v, "v"), (dO, "dO")):
+            t.copy_(inp[n])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip([o, lse, *g.values()], want))
+        o2, lse2 = _forward(y, 100)
+        assert torch.equal(o2, wy[0])
+
+
+def test_stream_argument():
+    x = _inputs(1, 2, 2, 130, 130, 64, 13)
+    q, k, v = (x[n].cuda() for n in "qkv")
+    want, _ = gdr.attn_fwd(q, k, v)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got, lse = gdr.attn_fwd(q, k, v, stream=s)
+    s.synchronize()
+    assert torch.equal(got, want)
+
+
+def test_long_rows():
+    """A long sequence, sampled rows against the definition."""
+    T, d = 5000, 128
+    x = _inputs(1, 2, 1, T, T, d, 14)
+    o, lse = _forward(x)
+    rows = [0, 1, 63, 64, 127, 128, 2047, 2048, 4095, 4999]
+    y = {n: t.to(F64) for n, t in x.items()}
+    for r in rows:
+        f = ref.attention(y["q"][:, :, r:r + 1], y["k"][:, :, :r + 1], y["v"][:, :, :r + 1])
+        _within("o", o[:, :, r:r + 1].cpu().to(F64), f["o"], f["o_tol"])
+        _within("lse", lse[:, :, r:r + 1].cpu().to(F64), f["lse"], f["lse_tol"])
