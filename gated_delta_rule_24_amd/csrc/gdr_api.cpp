@@ -65,6 +65,8 @@ gdr_status attn_args(int B, int Hq, int Hkv, int Tq, int Tk, int d, int window, 
     if (flags & ~(GDR_ACT_F32 | GDR_TOKEN_MAJOR)) return GDR_ERR_INVALID_ARG;
     if (B < 1 || Hq < 1 || Hkv < 1 || Tq < 0 || Tk < 0 || window < 0) return GDR_ERR_INVALID_ARG;
     if (Hq % Hkv != 0 || !(scale > 0.f) || !(scale - scale == 0.f)) return GDR_ERR_INVALID_ARG;
+    // byte offsets inside a tile of 64 rows are signed 32-bit
+    if (Hq > (1 << 16)) return GDR_ERR_INVALID_ARG;
     // places of queries and keys are signed 32-bit, with room for a tile behind the last
     if (Tq > (1 << 30) || Tk > (1 << 30)) return GDR_ERR_INVALID_ARG;
     if (!attn_sizes_ok(B, Hq, Tq) || !attn_sizes_ok(B, Hq, Tk)) return GDR_ERR_INVALID_ARG;

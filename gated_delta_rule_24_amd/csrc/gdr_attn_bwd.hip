@@ -7,6 +7,8 @@
 // the keys of its queries (three products), the key-side one the queries of its
 // keys and of every head that shares them (four products).  That recomputes the
 // scores and dO v once more than a single kernel would: seven products for five.
+#include <limits.h>
+
 #include "gdr_attn_tile.h"
 
 namespace gdr {
@@ -37,11 +39,11 @@ namespace {
 constexpr int kQM = 128, kQN = 64, kQWaves = 4;
 
 template <int D>
-struct __attribute__((aligned(16))) DqSmem {
+struct __attribute__((aligned(256))) DqSmem {
     uint16_t k[2][kQN * D];
     uint16_t v[2][kQN * D];
     int bound[kQM];
-    int shared[2];
+    int shared[3];
     int bad[kQWaves];
 };
 
@@ -68,7 +70,8 @@ __device__ __forceinline__ void queries_one_by_one(const AttnParams& p, long lon
             add_rows<D>(acc, w, k + (long long)j0 * p.sk.t, p.sk.t, min(64, hi - j0), lane);
         }
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) ((uint16_t*)p.dq)[row + lane + 64 * c] = f32_to_bf16(acc[c] * p.scale);
+        for (int c = 0; c < D / 64; ++c)
+            ((uint16_t*)p.dq)[row + lane + 64 * c] = f32_to_bf16(acc[c] * (hi - lo == 1 ? 0.f : p.scale));
     }
 }
 
@@ -77,7 +80,7 @@ __device__ __forceinline__ void queries_one_by_one(const AttnParams& p, long lon
 template <int D>
 __global__ __launch_bounds__(64 * kQWaves, 2) void attn_dq_kernel(AttnParams p, int tiles) {
     constexpr int KS = D / 16, DB = D / 32;
-    extern __shared__ __attribute__((aligned(16))) char smem[];
+    extern __shared__ __attribute__((aligned(256))) char smem[];
     DqSmem<D>& sm = *reinterpret_cast<DqSmem<D>*>(smem);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 31, h = lane >> 5;
@@ -113,11 +116,13 @@ __global__ __launch_bounds__(64 * kQWaves, 2) void attn_dq_kernel(AttnParams p, 
     const long long qrow = b * p.sq.b + hq * p.sq.h + (long long)min(row, p.Tq - 1) * p.sq.t;
     const long long stat = ((long long)b * p.Hq + hq) * p.Tq + min(row, p.Tq - 1);
 
+    const ReadAt<D> at_lane(lane);
+    const Stager<D, kQN, kQWaves> st_kv(p.sk.t, lane);
     const int j_first = begin / kQN * kQN;
     const int n = end > begin ? (end - j_first + kQN - 1) / kQN : 0;
     if (n > 0) {
-        stage<D, kQN, kQWaves>(kp, p.sk.t, j_first, p.Tk - 1, sm.k[0], wave, lane);
-        stage<D, kQN, kQWaves>(vp, p.sk.t, j_first, p.Tk - 1, sm.v[0], wave, lane);
+        st_kv.load(kp, j_first, p.Tk - 1, sm.k[0], wave, lane);
+        st_kv.load(vp, j_first, p.Tk - 1, sm.v[0], wave, lane);
     }
     bf8v qf[KS], gf[KS];
     float delta = 0.f;
@@ -146,11 +151,11 @@ __global__ __launch_bounds__(64 * kQWaves, 2) void attn_dq_kernel(AttnParams p, 
     bool bad = false;
     for (int it = 0; it < n; ++it) {
         const int j0 = j_first + it * kQN, buf = it & 1;
-        __builtin_amdgcn_s_waitcnt(0x0f70);           // vmcnt(0): this tile's loads
+        wait_loads();
         lds_barrier();
         if (it + 1 < n) {
-            stage<D, kQN, kQWaves>(kp, p.sk.t, j0 + kQN, p.Tk - 1, sm.k[buf ^ 1], wave, lane);
-            stage<D, kQN, kQWaves>(vp, p.sk.t, j0 + kQN, p.Tk - 1, sm.v[buf ^ 1], wave, lane);
+            st_kv.load(kp, j0 + kQN, p.Tk - 1, sm.k[buf ^ 1], wave, lane);
+            st_kv.load(vp, j0 + kQN, p.Tk - 1, sm.v[buf ^ 1], wave, lane);
         }
         const bool inner = j0 >= lo_most && j0 + kQN <= hi_least;
         if (!inner) {
@@ -162,8 +167,8 @@ __global__ __launch_bounds__(64 * kQWaves, 2) void attn_dq_kernel(AttnParams p, 
         }
         if (!__any(hi > j0 && lo < j0 + kQN)) continue;
         const bool whole = !__any(lo > j0 || hi < j0 + kQN);
-        const uint16_t* kt = sm.k[buf];
-        const uint16_t* vt = sm.v[buf];
+        const ReadAt<D> kt = at_lane.fresh(lds_address(sm.k[buf]));
+        constexpr int kV = offsetof(DqSmem<D>, v) - offsetof(DqSmem<D>, k);
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
             float16v st, dp;
@@ -171,9 +176,10 @@ __global__ __launch_bounds__(64 * kQWaves, 2) void attn_dq_kernel(AttnParams p, 
             zero16(dp);
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                st = __builtin_amdgcn_mfma_f32_32x32x16_bf16(row_frag<D>(kt, 32 * kb + col, 2 * s + h), qf[s], st, 0, 0, 0);
-                dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(row_frag<D>(vt, 32 * kb + col, 2 * s + h), gf[s], dp, 0, 0, 0);
+                st = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kt.row_frag(32 * kb, s), qf[s], st, 0, 0, 0);
+                dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kt.row_frag(32 * kb, s, kV), gf[s], dp, 0, 0, 0);
             }
+            sched_reads_ahead<4, 2 * KS, 1>();
             bf8v ds[2];
             const int base = j0 + 32 * kb + 4 * h - lo;
             const unsigned seen = (unsigned)(hi - lo);
@@ -187,21 +193,24 @@ __global__ __launch_bounds__(64 * kQWaves, 2) void attn_dq_kernel(AttnParams p, 
             for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int i = 0; i < DB; ++i)
-                    dq[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(col_frag<D>(kt, 32 * kb + 16 * s, i, lane), ds[s], dq[i], 0, 0, 0);
+                    dq[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kt.col_frag(32 * kb + 16 * s, i), ds[s], dq[i], 0, 0, 0);
+            sched_reads_ahead<4, 2 * DB, 2>();
         }
     }
     if (bad) {
-        __builtin_amdgcn_s_waitcnt(0x0f70);           // no load into LDS outlives the wave
+        wait_loads();                                 // no load into LDS outlives the wave
         const long long head = b * p.sq.b + hq * p.sq.h;
         queries_one_by_one<D>(p, head, kp, vp, r0 + 32 * wave, used, lo, hi, lse2, delta, lane);
         return;
     }
     if (live) {
+        // the softmax over one key is constant: its gradient is 0, not a rounding error
+        const float by = hi - lo == 1 ? 0.f : p.scale;
         uint16_t* out = (uint16_t*)p.dq + qrow;
 #pragma unroll
         for (int i = 0; i < DB; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) store4(out + 32 * i + 8 * j + 4 * h, dq[i], j, p.scale);
+            for (int j = 0; j < 4; ++j) store4(out + 32 * i + 8 * j + 4 * h, dq[i], j, by);
     }
 }
 
@@ -211,28 +220,38 @@ __global__ __launch_bounds__(64 * kQWaves, 2) void attn_dq_kernel(AttnParams p, 
 
 namespace {
 
-constexpr int kKN = 128, kKM = 64, kKWaves = 2, kKB = 2;   // keys, queries a step, waves, 32-key blocks of a wave
+constexpr int kKN = 128, kKM = 64, kKWaves = 4, kKB = 1;   // keys, queries a step, waves, 32-key blocks of a wave
+
+template <int D> constexpr int kKeyLds = D == 128 && kKB == 1 ? 3 : 0;
 
 template <int D>
-struct __attribute__((aligned(16))) DkvSmem {
+struct __attribute__((aligned(256))) DkvSmem {
     uint16_t q[2][kKM * D];
     uint16_t g[2][kKM * D];
     float delta[2][kKM];
     float lse2[2][kKM];
+    // key operands that do not fit the 256 registers beside the sums (d = 128): the
+    // last kKeyLds of a key's D / 16
+    uint4 key[kKWaves * kKB][kKeyLds<D> > 0 ? kKeyLds<D> : 1][64];
+    int4 range[kKN];            // of each key: first query, one past the last, one that sees only it
     int bound[kKN];
-    int shared[2];
+    int shared[3];
     int bad[kKWaves];
 };
+
+static_assert(sizeof(DkvSmem<128>) <= 80 * 1024 && sizeof(DkvSmem<64>) <= 80 * 1024, "two workgroups on a compute unit");
 
 // 32 keys from the definition (see dot_row); lane r % 32 holds key r's range of
 // queries.
 template <int D>
 __device__ __forceinline__ void keys_one_by_one(const AttnParams& p, const uint16_t* k, const uint16_t* v, int b, int bh, int hk,
-                                                int h0, int heads, int split, int first, int used, int lo32, int hi32, int lane) {
+                                                int h0, int heads, int split, int first, int used, int lo32, int hi32,
+                                                int only32, int lane) {
     const float to2 = p.scale * kLog2e;
     const long long all = (long long)p.B * p.Hq * p.Tq, one = (long long)p.B * p.Hkv * p.Tk * D;
     for (int r = 0; r < 32 && first + r < used; ++r) {
         const int lo = __builtin_amdgcn_readlane(lo32, r), hi = __builtin_amdgcn_readlane(hi32, r);
+        const int only = __builtin_amdgcn_readlane(only32, r);
         const long long j = (long long)(first + r) * p.sk.t;
         float dk[D / 64] = {}, dv[D / 64] = {};
         for (int hq = h0; hq < h0 + heads; ++hq) {
@@ -244,7 +263,7 @@ __device__ __forceinline__ void keys_one_by_one(const AttnParams& p, const uint1
                 if (i0 + lane < hi) {
                     const long long i = (long long)(i0 + lane) * p.sq.t;
                     x = __builtin_amdgcn_exp2f(dot_row<D>(q + i, k + j) * to2 - p.delta[all + stat + i0 + lane]);
-                    y = x * (dot_row<D>(g + i, v + j) - p.delta[stat + i0 + lane]);
+                    y = x * (dot_row<D>(g + i, v + j) - p.delta[stat + i0 + lane]) * (i0 + lane == only ? 0.f : 1.f);
                 }
                 add_rows<D>(dv, x, g + (long long)i0 * p.sq.t, p.sq.t, min(64, hi - i0), lane);
                 add_rows<D>(dk, y, q + (long long)i0 * p.sq.t, p.sq.t, min(64, hi - i0), lane);
@@ -268,9 +287,9 @@ __device__ __forceinline__ void keys_one_by_one(const AttnParams& p, const uint1
 }  // namespace
 
 template <int D>
-__global__ __launch_bounds__(64 * kKWaves, 1) void attn_dkv_kernel(AttnParams p, int tiles) {
+__global__ __launch_bounds__(64 * kKWaves, 2) void attn_dkv_kernel(AttnParams p, int tiles) {
     constexpr int KS = D / 16, DB = D / 32;
-    extern __shared__ __attribute__((aligned(16))) char smem[];
+    extern __shared__ __attribute__((aligned(256))) char smem[];
     DkvSmem<D>& sm = *reinterpret_cast<DkvSmem<D>*>(smem);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 31, h = lane >> 5;
@@ -287,17 +306,34 @@ __global__ __launch_bounds__(64 * kKWaves, 1) void attn_dkv_kernel(AttnParams p,
         if (c0 >= used) return;
         rows = used;
     }
-    // the queries that see key j: places j .. j + window - 1, inside its sequence
-    int key[kKB], lo[kKB], hi[kKB];
+    // the queries that see key j: places j .. j + window - 1, inside its sequence;
+    // kept in LDS, for the steps that need them lane by lane
+    int see_from = INT_MAX, see_to = 0, all_from = 0, all_to = INT_MAX;   // of the wave's keys: some row / every key
 #pragma unroll
     for (int kb = 0; kb < kKB; ++kb) {
         const int in = 32 * (kKB * wave + kb) + col, j = c0 + in;
-        key[kb] = j;
-        lo[kb] = max(j - off, 0);
-        hi[kb] = p.cu_seqlens ? min(sm.bound[in], rows) : rows;
-        if (p.window > 0) hi[kb] = min(hi[kb], j - off + p.window);
-        if (j >= used || hi[kb] <= lo[kb]) { lo[kb] = 0; hi[kb] = 0; }
+        int lo = max(j - off, 0), hi = p.cu_seqlens ? min(sm.bound[in], rows) : rows;
+        if (p.window > 0) hi = min(hi, j - off + p.window);
+        if (j >= used || hi <= lo) { lo = 0; hi = 0; }
+        // a query that sees this key alone, or -1: the window is one key, or the key is
+        // its sequence's first
+        const bool first = j == 0 || (p.cu_seqlens && (in == 0 ? sm.shared[2] != 0 : sm.bound[in - 1] == j));
+        if (h == 0) sm.range[in] = make_int4(lo, hi, (p.window == 1 || first) ? j - off : -1, 0);
+        if (hi > lo) see_from = min(see_from, lo);
+        see_to = max(see_to, hi);
+        all_from = max(all_from, hi > lo ? lo : INT_MAX);
+        all_to = min(all_to, hi);
     }
+    for (int x = 32; x > 0; x >>= 1) {
+        see_from = min(see_from, __shfl_xor(see_from, x, 64));
+        see_to = max(see_to, __shfl_xor(see_to, x, 64));
+        all_from = max(all_from, __shfl_xor(all_from, x, 64));
+        all_to = min(all_to, __shfl_xor(all_to, x, 64));
+    }
+    see_from = __builtin_amdgcn_readfirstlane(see_from);
+    see_to = __builtin_amdgcn_readfirstlane(see_to);
+    all_from = __builtin_amdgcn_readfirstlane(all_from);
+    all_to = __builtin_amdgcn_readfirstlane(all_to);
     const int last_key = min(c0 + kKN, used) - 1;
     const int begin = max(c0 - off, 0);
     int end = rows, hi_least = rows;
@@ -310,13 +346,16 @@ __global__ __launch_bounds__(64 * kKWaves, 1) void attn_dkv_kernel(AttnParams p,
 
     const uint16_t* kp = (const uint16_t*)p.k + b * p.sk.b + hk * p.sk.h;
     const uint16_t* vp = (const uint16_t*)p.v + b * p.sk.b + hk * p.sk.h;
-    bf8v kf[kKB][KS], vf[kKB][KS];
+    constexpr int KR = KS - kKeyLds<D>;
+    bf8v kf[kKB][KR], vf[kKB][KS];
 #pragma unroll
     for (int kb = 0; kb < kKB; ++kb) {
-        const long long kr = (long long)min(key[kb], p.Tk - 1) * p.sk.t + 8 * h;
+        const long long kr = (long long)min(c0 + 32 * (kKB * wave + kb) + col, p.Tk - 1) * p.sk.t + 8 * h;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            kf[kb][s] = __builtin_bit_cast(bf8v, *reinterpret_cast<const uint4*>(kp + kr + 16 * s));
+            const uint4 u = *reinterpret_cast<const uint4*>(kp + kr + 16 * s);
+            if (s < KR) kf[kb][s < KR ? s : 0] = __builtin_bit_cast(bf8v, u);
+            else sm.key[kKB * wave + kb][s < KR ? 0 : s - KR][lane] = u;
             vf[kb][s] = __builtin_bit_cast(bf8v, *reinterpret_cast<const uint4*>(vp + kr + 16 * s));
         }
     }
@@ -327,6 +366,8 @@ __global__ __launch_bounds__(64 * kKWaves, 1) void attn_dkv_kernel(AttnParams p,
         for (int i = 0; i < DB; ++i) { zero16(dk[kb][i]); zero16(dv[kb][i]); }
     const float to2 = p.scale * kLog2e;
 
+    const ReadAt<D> at_lane(lane);
+    const Stager<D, kKM, kKWaves> st_q(p.sq.t, lane);
     const int i_first = begin / kKM * kKM;
     const int per = end > begin ? (end - i_first + kKM - 1) / kKM : 0, n = per * heads;
     const long long all = (long long)p.B * p.Hq * p.Tq;
@@ -335,18 +376,19 @@ __global__ __launch_bounds__(64 * kKWaves, 1) void attn_dkv_kernel(AttnParams p,
         const int hq = h0 + it / per, i0 = i_first + it % per * kKM;
         const uint16_t* qp = (const uint16_t*)p.q + b * p.sq.b + hq * p.sq.h;
         const uint16_t* gp = (const uint16_t*)p.dO + b * p.sq.b + hq * p.sq.h;
-        stage<D, kKM, kKWaves>(qp, p.sq.t, i0, p.Tq - 1, sm.q[buf], wave, lane);
-        stage<D, kKM, kKWaves>(gp, p.sq.t, i0, p.Tq - 1, sm.g[buf], wave, lane);
-        const float* st = p.delta + (wave ? all : 0) + ((long long)b * p.Hq + hq) * p.Tq + min(i0 + lane, p.Tq - 1);
-        __builtin_amdgcn_global_load_lds(reinterpret_cast<const void __attribute__((address_space(1)))*>(
-                                             reinterpret_cast<uintptr_t>(st)),
-                                         (void __attribute__((address_space(3)))*)(wave ? sm.lse2[buf] : sm.delta[buf]), 4, 0, 0);
+        st_q.load(qp, i0, p.Tq - 1, sm.q[buf], wave, lane);
+        st_q.load(gp, i0, p.Tq - 1, sm.g[buf], wave, lane);
+        if (wave < 2) {
+            const float* st = p.delta + (wave ? all : 0) + ((long long)b * p.Hq + hq) * p.Tq + i0;
+            direct_load4(4 * min(lane, p.Tq - 1 - i0), (uint64_t)st,
+                         (uint32_t)(uintptr_t)(__attribute__((address_space(3))) float*)(wave ? sm.lse2[buf] : sm.delta[buf]));
+        }
     };
     if (n > 0) fetch(0, 0);
     bool bad = false;
     for (int it = 0; it < n; ++it) {
         const int i0 = i_first + it % per * kKM, buf = it & 1;
-        __builtin_amdgcn_s_waitcnt(0x0f70);           // vmcnt(0): this step's loads
+        wait_loads();
         lds_barrier();
         if (it + 1 < n) fetch(it + 1, buf ^ 1);
         const uint16_t* qt = sm.q[buf];
@@ -355,82 +397,140 @@ __global__ __launch_bounds__(64 * kKWaves, 1) void attn_dkv_kernel(AttnParams p,
         if (!inner) {
             bool mine = false;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                mine = mine || any_not_finite<D>(qt + (32 * wave + 16 * i) * D, lane) || any_not_finite<D>(gt + (32 * wave + 16 * i) * D, lane);
+            for (int i = 0; i < kKM / 16 / kKWaves; ++i) {
+                const int r = (kKM / kKWaves) * wave + 16 * i;
+                mine = mine || any_not_finite<D>(qt + r * D, lane) || any_not_finite<D>(gt + r * D, lane);
+            }
             if (lane == 0) sm.bad[wave] = mine;
             lds_barrier();
-            bad = (sm.bad[0] | sm.bad[1]) != 0;
+            bad = false;
+#pragma unroll
+            for (int w = 0; w < kKWaves; ++w) bad = bad || sm.bad[w] != 0;
             if (bad) break;
         }
+        const ReadAt<D> at = at_lane.fresh(lds_address(qt));
+        constexpr int kG = offsetof(DkvSmem<D>, g) - offsetof(DkvSmem<D>, q);
 #pragma unroll
         for (int ib = 0; ib < kKM / 32; ++ib) {
             const int ir = i0 + 32 * ib;
-            bool some = false, whole = true;
-#pragma unroll
-            for (int kb = 0; kb < kKB; ++kb) {
-                some |= hi[kb] > ir && lo[kb] < ir + 32;
-                whole &= lo[kb] <= ir && hi[kb] >= ir + 32;
-            }
-            if (!__any(some)) continue;
-            whole = __all(whole);
+            if (ir >= see_to || ir + 32 <= see_from) continue;
+            const bool whole = ir >= all_from && ir + 32 <= all_to;
+            // the weights, and dv from them
             float16v st[kKB], dp[kKB];
 #pragma unroll
-            for (int kb = 0; kb < kKB; ++kb) { zero16(st[kb]); zero16(dp[kb]); }
+            for (int kb = 0; kb < kKB; ++kb) zero16(st[kb]);
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                const bf8v a = row_frag<D>(qt, 32 * ib + col, 2 * s + h), g = row_frag<D>(gt, 32 * ib + col, 2 * s + h);
+                const bf8v a = at.row_frag(32 * ib, s);
 #pragma unroll
                 for (int kb = 0; kb < kKB; ++kb) {
-                    st[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, kf[kb][s], st[kb], 0, 0, 0);
-                    dp[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(g, vf[kb][s], dp[kb], 0, 0, 0);
+                    const bf8v k = s < KR ? kf[kb][s < KR ? s : 0]
+                                          : __builtin_bit_cast(bf8v, sm.key[kKB * wave + kb][s < KR ? 0 : s - KR][lane]);
+                    st[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, k, st[kb], 0, 0, 0);
                 }
             }
-            bf8v pf[kKB][2], ds[kKB][2];
+            sched_reads_ahead<3, KS, 1, kKB>();
+            __builtin_amdgcn_sched_barrier(0);        // the registers are full: no reads for the next part yet
+            bf8v pf[kKB][2];
 #pragma unroll
             for (int q4 = 0; q4 < 4; ++q4) {
                 const float4v l4 = *reinterpret_cast<const float4v*>(&sm.lse2[buf][32 * ib + 8 * q4 + 4 * h]);
-                const float4v d4 = *reinterpret_cast<const float4v*>(&sm.delta[buf][32 * ib + 8 * q4 + 4 * h]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int kb = 0; kb < kKB; ++kb)
 #pragma unroll
-                    for (int kb = 0; kb < kKB; ++kb) {
-                        float x = __builtin_amdgcn_exp2f(st[kb][4 * q4 + i] * to2 - l4[i]);
-                        float y = x * (dp[kb][4 * q4 + i] - d4[i]);
-                        if (!whole) {
-                            const int r = ir + 8 * q4 + 4 * h + i;
-                            const bool in = (unsigned)(r - lo[kb]) < (unsigned)(hi[kb] - lo[kb]);
-                            x = in ? x : 0.f;
-                            y = in ? y : 0.f;
-                        }
-                        pf[kb][q4 / 2][(q4 % 2) * 4 + i] = (__bf16)x;
-                        ds[kb][q4 / 2][(q4 % 2) * 4 + i] = (__bf16)y;
-                    }
+                    for (int i = 0; i < 4; ++i) st[kb][4 * q4 + i] = __builtin_amdgcn_exp2f(st[kb][4 * q4 + i] * to2 - l4[i]);
             }
+            if (!whole) {
+#pragma unroll
+                for (int kb = 0; kb < kKB; ++kb) {
+                    const int4 see = sm.range[32 * (kKB * wave + kb) + col];
+                    const int from = ir + 4 * h - see.x;
+                    const unsigned seen = (unsigned)(see.y - see.x);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if ((unsigned)(from + 8 * (i / 4) + i % 4) >= seen) st[kb][i] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int kb = 0; kb < kKB; ++kb)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) pf[kb][i / 8][i % 8] = (__bf16)st[kb][i];
 #pragma unroll
             for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int i = 0; i < DB; ++i) {
-                    const bf8v g = col_frag<D>(gt, 32 * ib + 16 * s, i, lane), a = col_frag<D>(qt, 32 * ib + 16 * s, i, lane);
+                    const bf8v g = at.col_frag(32 * ib + 16 * s, i, kG);
 #pragma unroll
-                    for (int kb = 0; kb < kKB; ++kb) {
-                        dv[kb][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(g, pf[kb][s], dv[kb][i], 0, 0, 0);
-                        dk[kb][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, ds[kb][s], dk[kb][i], 0, 0, 0);
+                    for (int kb = 0; kb < kKB; ++kb) dv[kb][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(g, pf[kb][s], dv[kb][i], 0, 0, 0);
+                }
+            sched_reads_ahead<3, 2 * DB, 2, kKB>();
+            __builtin_amdgcn_sched_barrier(0);
+            // their gradients, and dk from them
+#pragma unroll
+            for (int kb = 0; kb < kKB; ++kb) zero16(dp[kb]);
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                const bf8v g = at.row_frag(32 * ib, s, kG);
+#pragma unroll
+                for (int kb = 0; kb < kKB; ++kb) dp[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(g, vf[kb][s], dp[kb], 0, 0, 0);
+            }
+            sched_reads_ahead<3, KS, 1, kKB>();
+            __builtin_amdgcn_sched_barrier(0);
+            bf8v ds[kKB][2];
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4) {
+                const float4v d4 = *reinterpret_cast<const float4v*>(&sm.delta[buf][32 * ib + 8 * q4 + 4 * h]);
+#pragma unroll
+                for (int kb = 0; kb < kKB; ++kb)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) dp[kb][4 * q4 + i] = st[kb][4 * q4 + i] * (dp[kb][4 * q4 + i] - d4[i]);
+            }
+            if (!whole) {
+                // nothing from masked pairs (0 * NaN), nor from a query that sees this key only
+#pragma unroll
+                for (int kb = 0; kb < kKB; ++kb) {
+                    const int4 see = sm.range[32 * (kKB * wave + kb) + col];
+                    const int from = ir + 4 * h - see.x, alone = see.z - ir - 4 * h;
+                    const unsigned seen = (unsigned)(see.y - see.x);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int r = 8 * (i / 4) + i % 4;
+                        dp[kb][i] *= r == alone ? 0.f : 1.f;
+                        if ((unsigned)(from + r) >= seen) dp[kb][i] = 0.f;
                     }
                 }
+            }
+#pragma unroll
+            for (int kb = 0; kb < kKB; ++kb)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) ds[kb][i / 8][i % 8] = (__bf16)dp[kb][i];
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int i = 0; i < DB; ++i) {
+                    const bf8v a = at.col_frag(32 * ib + 16 * s, i);
+#pragma unroll
+                    for (int kb = 0; kb < kKB; ++kb) dk[kb][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, ds[kb][s], dk[kb][i], 0, 0, 0);
+                }
+            sched_reads_ahead<3, 2 * DB, 2, kKB>();
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
     if (bad) {
-        __builtin_amdgcn_s_waitcnt(0x0f70);           // no load into LDS outlives the wave
+        wait_loads();                                 // no load into LDS outlives the wave
 #pragma unroll
-        for (int kb = 0; kb < kKB; ++kb)
-            keys_one_by_one<D>(p, kp, vp, b, bh, hk, h0, heads, split, c0 + 32 * (kKB * wave + kb), used, lo[kb], hi[kb], lane);
+        for (int kb = 0; kb < kKB; ++kb) {
+            const int4 see = sm.range[32 * (kKB * wave + kb) + col];
+            keys_one_by_one<D>(p, kp, vp, b, bh, hk, h0, heads, split, c0 + 32 * (kKB * wave + kb), used, see.x, see.y, see.z, lane);
+        }
         return;
     }
 #pragma unroll
     for (int kb = 0; kb < kKB; ++kb) {
-        if (key[kb] >= used) continue;
+        const int key = c0 + 32 * (kKB * wave + kb) + col;
+        if (key >= used) continue;
         if (p.splits == 1) {
-            const long long at = b * p.sk.b + hk * p.sk.h + (long long)key[kb] * p.sk.t;
+            const long long at = b * p.sk.b + hk * p.sk.h + (long long)key * p.sk.t;
 #pragma unroll
             for (int i = 0; i < DB; ++i)
 #pragma unroll
@@ -440,7 +540,7 @@ __global__ __launch_bounds__(64 * kKWaves, 1) void attn_dkv_kernel(AttnParams p,
                 }
         } else {
             const long long one = (long long)p.B * p.Hkv * p.Tk * D;
-            float* at = p.part + split * one + ((long long)bh * p.Tk + key[kb]) * D;
+            float* at = p.part + split * one + ((long long)bh * p.Tk + key) * D;
 #pragma unroll
             for (int i = 0; i < DB; ++i)
 #pragma unroll

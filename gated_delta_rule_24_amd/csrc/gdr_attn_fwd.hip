@@ -23,11 +23,11 @@ namespace {
 constexpr int kBM = 128, kBN = 64, kWaves = 4;
 
 template <int D>
-struct __attribute__((aligned(16))) FwdSmem {
+struct __attribute__((aligned(256))) FwdSmem {
     uint16_t k[2][kBN * D];
     uint16_t v[2][kBN * D];
     int bound[kBM];
-    int shared[2];
+    int shared[3];
     int bad[kWaves];
 };
 
@@ -63,7 +63,7 @@ __device__ __forceinline__ void rows_one_by_one(const AttnParams& p, const uint1
 template <int D>
 __global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_kernel(AttnParams p, int tiles) {
     constexpr int KS = D / 16, DB = D / 32;
-    extern __shared__ __attribute__((aligned(16))) char smem[];
+    extern __shared__ __attribute__((aligned(256))) char smem[];
     FwdSmem<D>& sm = *reinterpret_cast<FwdSmem<D>*>(smem);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 31, h = lane >> 5;
@@ -114,85 +114,88 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_kernel(AttnParams p, 
     float m = -INFINITY, l = 0.f;
     const float to2 = p.scale * kLog2e;
 
+    const ReadAt<D> at_lane(lane);
+    const Stager<D, kBN, kWaves> st_kv(p.sk.t, lane);
     const int j_first = begin / kBN * kBN;
     const int n = end > begin ? (end - j_first + kBN - 1) / kBN : 0;
     if (n > 0) {
-        stage<D, kBN, kWaves>(kp, p.sk.t, j_first, p.Tk - 1, sm.k[0], wave, lane);
-        stage<D, kBN, kWaves>(vp, p.sk.t, j_first, p.Tk - 1, sm.v[0], wave, lane);
+        st_kv.load(kp, j_first, p.Tk - 1, sm.k[0], wave, lane);
+        st_kv.load(vp, j_first, p.Tk - 1, sm.v[0], wave, lane);
     }
     bool bad = false;
     for (int it = 0; it < n; ++it) {
         const int j0 = j_first + it * kBN, buf = it & 1;
-        __builtin_amdgcn_s_waitcnt(0x0f70);           // vmcnt(0): this tile's loads
+        wait_loads();
         lds_barrier();
         if (it + 1 < n) {
-            stage<D, kBN, kWaves>(kp, p.sk.t, j0 + kBN, p.Tk - 1, sm.k[buf ^ 1], wave, lane);
-            stage<D, kBN, kWaves>(vp, p.sk.t, j0 + kBN, p.Tk - 1, sm.v[buf ^ 1], wave, lane);
+            st_kv.load(kp, j0 + kBN, p.Tk - 1, sm.k[buf ^ 1], wave, lane);
+            st_kv.load(vp, j0 + kBN, p.Tk - 1, sm.v[buf ^ 1], wave, lane);
         }
         // tiles that some row of the workgroup sees in part: infinities and NaN among
         // values that are masked for a row must not reach it through 0 * inf
-        const bool inner = j0 >= lo_most && j0 + kBN <= hi_least;
-        if (!inner) {
+        const bool edge = j0 < lo_most || j0 + kBN > hi_least;
+        if (edge) {
             const bool mine = any_not_finite<D>(sm.v[buf] + 16 * wave * D, lane);
             if (lane == 0) sm.bad[wave] = mine;
             lds_barrier();
             bad = (sm.bad[0] | sm.bad[1] | sm.bad[2] | sm.bad[3]) != 0;
             if (bad) break;
+            if (!__any(hi > j0 && lo < j0 + kBN)) continue;
         }
-        if (__any(hi > j0 && lo < j0 + kBN)) {
-            const uint16_t* kt = sm.k[buf];
-            const uint16_t* vt = sm.v[buf];
-            float16v st[2];
+        const ReadAt<D> kt = at_lane.fresh(lds_address(sm.k[buf]));
+        float16v st[2];
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb) {
+        for (int kb = 0; kb < 2; ++kb) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) st[kb][j] = 0.f;
+            for (int j = 0; j < 16; ++j) st[kb][j] = 0.f;
 #pragma unroll
-                for (int s = 0; s < KS; ++s)
-                    st[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(row_frag<D>(kt, 32 * kb + col, 2 * s + h), qf[s], st[kb], 0, 0, 0);
-            }
-            if (__any(lo > j0 || hi < j0 + kBN)) {
-                const int base = j0 + 4 * h - lo;
-                const unsigned seen = (unsigned)(hi - lo);
-#pragma unroll
-                for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if ((unsigned)(base + 32 * kb + 8 * (i / 4) + i % 4) >= seen) st[kb][i] = -INFINITY;
-            }
-            float top = m;
+            for (int s = 0; s < KS; ++s)
+                st[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kt.row_frag(32 * kb, s), qf[s], st[kb], 0, 0, 0);
+        }
+        sched_reads_ahead<4, 2 * KS, 1>();
+        if (edge) {
+            const int base = j0 + 4 * h - lo;
+            const unsigned seen = (unsigned)(hi - lo);
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) top = fmaxf(top, st[kb][i]);
-            top = max_across32(top);
-            const float shift = top == -INFINITY ? 0.f : top * to2;
-            const float fade = m == top ? 1.f : __builtin_amdgcn_exp2f((m - top) * to2);
-            m = top;
-            float sum = 0.f;
-            bf8v pf[4];
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float x = __builtin_amdgcn_exp2f(st[kb][i] * to2 - shift);
-                    sum += x;
-                    pf[2 * kb + i / 8][i % 8] = (__bf16)x;
-                }
-            l = l * fade + sum;
-            if (__any(fade != 1.f)) {
-#pragma unroll
-                for (int i = 0; i < DB; ++i) o[i] *= fade;
-            }
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-#pragma unroll
-                for (int i = 0; i < DB; ++i)
-                    o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(col_frag<D>(vt, 16 * s, i, lane), pf[s], o[i], 0, 0, 0);
+                for (int i = 0; i < 16; ++i)
+                    if ((unsigned)(base + 32 * kb + 8 * (i / 4) + i % 4) >= seen) st[kb][i] = -INFINITY;
         }
+        float top = m;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, st[kb][i]);
+        top = max_across32(top);
+        const float shift = top == -INFINITY ? 0.f : top * to2;
+        const float fade = m == top ? 1.f : __builtin_amdgcn_exp2f((m - top) * to2);
+        m = top;
+        if (__any(fade != 1.f)) {                     // rare once the maxima have settled
+            asm volatile("");                         // a branch, not 64 products and selects
+#pragma unroll
+            for (int i = 0; i < DB; ++i) o[i] *= fade;
+        }
+        float sum = 0.f;
+        bf8v pf[4];
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float x = __builtin_amdgcn_exp2f(st[kb][i] * to2 - shift);
+                sum += x;
+                pf[2 * kb + i / 8][i % 8] = (__bf16)x;
+            }
+        l = l * fade + sum;
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int i = 0; i < DB; ++i)
+                o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kt.col_frag(16 * s, i, (int)(offsetof(FwdSmem<D>, v) - offsetof(FwdSmem<D>, k))), pf[s], o[i], 0, 0, 0);
+        sched_reads_ahead<4, 4 * DB, 2>();
     }
     if (bad) {
-        __builtin_amdgcn_s_waitcnt(0x0f70);           // no load into LDS outlives the wave
+        wait_loads();                                 // no load into LDS outlives the wave
         rows_one_by_one<D>(p, qp, kp, vp, (uint16_t*)p.o + b * p.sq.b + hq * p.sq.h,
                            p.lse ? p.lse + ((long long)b * p.Hq + hq) * p.Tq : nullptr, r0 + 32 * wave, used, lo, hi, lane);
         return;

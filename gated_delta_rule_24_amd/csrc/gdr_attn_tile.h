@@ -21,54 +21,120 @@ namespace attn {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// 16 (4) bytes a lane from base + off to LDS at `to` + 16 (4) lane; `base` and `to` uniform.
+__device__ __forceinline__ void direct_load16(int off, uint64_t base, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(to) : "memory");
+}
+__device__ __forceinline__ void direct_load4(int off, uint64_t base, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "s"(to) : "memory");
+}
+// every load of this wave has arrived (its own; a barrier makes the others' visible)
+__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0f70); }   // vmcnt(0)
+
 template <int D> __device__ __forceinline__ int swz(int r) {
     if constexpr (D == 128) return ((r & 3) << 2) | ((r >> 2) & 3);
     else return ((r & 2) << 1) | ((r >> 2) & 3);
 }
 
-// ROWS rows starting at row `first` of a tensor with rows `stride` elements
-// apart, into LDS by 16-byte direct loads; row indexes are held inside
-// [0, last].  Issued by WAVES waves; complete after the issuing waves' vmcnt
-// wait and a barrier.
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+
+// ROWS rows of a tensor, its rows `stride` elements apart, into LDS by 16-byte
+// direct loads of WAVES waves: lane offsets fixed, a scalar base that moves.  Rows
+// past `last` are held at it.  The loads are issued in assembly, which the
+// compiler does not count: with the builtin it makes every later LDS read wait for
+// every load in flight (vmcnt(0)), so the next tile's loads could not stay
+// in flight across the work on this one (forward at B=2 H=16 T=8192 d=128 window
+// 2048: 302 us with the builtin).  They have no output registers; wait_loads()
+// and a barrier complete them.
 template <int D, int ROWS, int WAVES>
-__device__ __forceinline__ void stage(const uint16_t* src, long long stride, int first, int last, uint16_t* dst,
-                                      int wave, int lane) {
-    constexpr int CH = D / 8, RPI = 64 / CH;         // rows of one instruction
-    constexpr int N = ROWS / RPI / WAVES;
+struct Stager {
+    static constexpr int CH = D / 8, RPI = 64 / CH;  // chunks of a row, rows of one instruction
+    static constexpr int N = ROWS / RPI / WAVES;
     static_assert(N * RPI * WAVES == ROWS, "rows split over the waves");
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int r0 = (wave * N + i) * RPI, r = r0 + lane / CH, c = (lane % CH) ^ swz<D>(r);
-        int row = first + r;
-        row = row < 0 ? 0 : row > last ? last : row;
-        const uint16_t* g = src + (long long)row * stride + 8 * c;
-        __builtin_amdgcn_global_load_lds(reinterpret_cast<const void __attribute__((address_space(1)))*>(
-                                             reinterpret_cast<uintptr_t>(g)),
-                                         (void __attribute__((address_space(3)))*)(dst + r0 * D), 16, 0, 0);
+    // byte offset of the lane's chunk from the first of an instruction's rows; a row
+    // is at least 2 D bytes from the next, so the swizzle's flips below stay inside it
+    int off;
+    long long stride;
+
+    __device__ __forceinline__ Stager(long long stride_, int lane) : stride(stride_) {
+        const int r = lane / CH;
+        off = (int)(2 * (r * stride + 8 * ((lane % CH) ^ swz<D>(r))));
     }
+    __device__ __forceinline__ void load(const uint16_t* src, int first, int last, uint16_t* dst, int wave, int lane) const {
+        const uint32_t to = lds_address(dst) + wave * N * 1024;
+        const bool inside = first + ROWS - 1 <= last;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int group = wave * N + i;           // swz of the group's rows: swz(lane / CH) ^ swz(group's first)
+            int row = first + group * RPI, at = off ^ (16 * swz<D>(group * RPI));
+            if (!inside) {
+                // the lane offset is unsigned: the base is held inside too
+                const int over = min(row, last) - last + lane / CH;
+                row = min(row, last);
+                at -= over > 0 ? (int)(2 * over * stride) : 0;
+            }
+            const uint64_t base = (uint64_t)(src + row * stride);
+            direct_load16(at, base, to + 1024 * i);
+        }
+    }
+};
+
+// Order of N groups of P products that share R LDS reads: AHEAD groups' reads go
+// first, then products and reads in turn.  Left alone, the compiler reads right
+// before each product and waits for every read.
+template <int AHEAD, int N, int R, int P = 1> __device__ __forceinline__ void sched_reads_ahead() {
+    __builtin_amdgcn_sched_group_barrier(0x100, AHEAD * R, 0);       // LDS reads
+#pragma unroll
+    for (int i = 0; i < N - AHEAD; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, P, 0);           // products
+        __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, AHEAD * P, 0);
 }
 
-// Operand along d: row `r`, channels 8 c .. 8 c + 7.
-template <int D> __device__ __forceinline__ bf8v row_frag(const uint16_t* tile, int r, int c) {
-    return __builtin_bit_cast(bf8v, *reinterpret_cast<const uint4*>(tile + r * D + 8 * (c ^ swz<D>(r))));
-}
+// A lane's two read addresses inside a tile, from which every other one follows by
+// flipping address bits: the swizzle is an exclusive-or of the chunk, and tiles
+// start at multiples of 256 bytes.  fresh() hides them from the compiler once a
+// step; otherwise it keeps all of them in registers across the loop (16 more than
+// the key-side gradient kernel has).
+template <int D> struct ReadAt {
+    uint32_t row, col;
 
-// Operand along the rows: for the lane's channel 32 db + (lane & 31), rows
-// r .. r + 3 and r + 8 .. r + 11 with r = r0 + 4 (lane / 32).
-template <int D> __device__ __forceinline__ bf8v col_frag(const uint16_t* tile, int r0, int db, int lane) {
-    const int j = (lane & 15) >> 2, h = lane >> 5;
-    const int ch = 4 * db + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1), in = 4 * (lane & 1);
-    bf8v f;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int r = r0 + 8 * e + 4 * h + j;
-        const uint16_t* at = tile + r * D + 8 * (ch ^ swz<D>(r)) + in;
-        const short4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) short4v*)at);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f[4 * e + i] = __builtin_bit_cast(__bf16, (short)x[i]);
+    __device__ __forceinline__ explicit ReadAt(int lane) {
+        const int r = lane & 31, h = lane >> 5;
+        row = 2 * (r * D + 8 * (h ^ swz<D>(r)));
+        const int j = 4 * h + ((lane & 15) >> 2), ch = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+        col = 2 * (j * D + 8 * (ch ^ swz<D>(j)) + 4 * (lane & 1));
     }
-    return f;
-}
+    // the same inside the tile at LDS address `tile`
+    __device__ __forceinline__ ReadAt fresh(uint32_t tile) const {
+        ReadAt x = *this;
+        x.row += tile;
+        x.col += tile;
+        asm volatile("" : "+v"(x.row), "+v"(x.col));
+        return x;
+    }
+    // operand along d: row `r0` + (lane & 31), channels 16 s + 8 (lane / 32) .. + 7
+    // (r0 a multiple of 32, `by` bytes further on)
+    __device__ __forceinline__ bf8v row_frag(int r0, int s, int by = 0) const {
+        return __builtin_bit_cast(bf8v, *(const __attribute__((address_space(3))) uint4*)(uintptr_t)((row ^ (s << 5)) + 2 * r0 * D + by));
+    }
+    // operand along the rows: channel 32 db + (lane & 31), rows r .. r + 3 and
+    // r + 8 .. r + 11 with r = r0 + 4 (lane / 32) (r0 a multiple of 16)
+    __device__ __forceinline__ bf8v col_frag(int r0, int db, int by = 0) const {
+        bf8v f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t at = (col ^ (db << 6) ^ (e << 5)) + 2 * (r0 + 8 * e) * D + by;
+            const short4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) short4v*)(uintptr_t)at);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[4 * e + i] = __builtin_bit_cast(__bf16, (short)x[i]);
+        }
+        return f;
+    }
+};
 
 // Whether any of 16 rows of a tile (rows 16 wave ..) holds an infinity or NaN.
 template <int D> __device__ __forceinline__ bool any_not_finite(const uint16_t* rows, int lane) {
@@ -113,18 +179,20 @@ __device__ __forceinline__ void add_rows(float (&acc)[D / 64], float w, const ui
 // Packed sequences: for rows r0 .. r0 + BM - 1 of T, the first row of each one's
 // sequence (`from`) or one past its last (`to`).  Values of cu outside [0, T] are
 // held inside, so that no content of it leads out of the tensors.  `used` is
-// cu[nseq]: rows from there on belong to no sequence.  All threads of the
+// cu[nseq]: rows from there on belong to no sequence; shared[2] tells whether one
+// starts at r0.  All threads of the
 // workgroup call it; ends with a barrier.
 template <int BM, bool TO>
 __device__ __forceinline__ void row_bounds(const int* cu, int nseq, int T, int r0, int* bound, int* shared, int tid,
                                            int nthreads, int& used) {
     for (int i = tid; i < BM; i += nthreads) bound[i] = TO ? T : 0;
-    if (tid == 0) { shared[0] = TO ? T : 0; shared[1] = 0; }
+    if (tid == 0) { shared[0] = TO ? T : 0; shared[1] = 0; shared[2] = 0; }
     __syncthreads();
     int edge = TO ? T : 0;
     for (int s = tid; s <= nseq; s += nthreads) {
         const int raw = cu[s], c = raw < 0 ? 0 : raw > T ? T : raw;
         if (s == nseq) shared[1] = c;
+        if (c == r0) shared[2] = 1;
         if constexpr (TO) {                           // the sequence ends at c: rows below c
             if (c >= r0 + BM) edge = c < edge ? c : edge;
             else if (c > r0) bound[c - 1 - r0] = c;
