@@ -9,6 +9,8 @@
 // scores and dO v once more than a single kernel would: seven products for five.
 #include <limits.h>
 
+#include <type_traits>
+
 #include "gdr_attn_tile.h"
 
 namespace gdr {
@@ -116,13 +118,17 @@ __global__ __launch_bounds__(64 * kQWaves, 2) void attn_dq_kernel(AttnParams p, 
     const long long qrow = b * p.sq.b + hq * p.sq.h + (long long)min(row, p.Tq - 1) * p.sq.t;
     const long long stat = ((long long)b * p.Hq + hq) * p.Tq + min(row, p.Tq - 1);
 
-    const ReadAt<D> at_lane(lane);
-    const Stager<D, kQN, kQWaves> st_kv(p.sk.t, lane);
+    // two tiles a turn, so that every LDS address is a fixed register and a constant
+    const ReadAt<D> kt = ReadAt<D>(lane).in(lds_address(sm.k[0]));
+    const Stager<D, kQN, kQWaves, true> loads(p.sk.t, wave, lane);
     const int j_first = begin / kQN * kQN;
     const int n = end > begin ? (end - j_first + kQN - 1) / kQN : 0;
+    uint64_t k_rows = loads.rows(kp, j_first), v_rows = loads.rows(vp, j_first);
+    const uint64_t tile_bytes = (uint64_t)kQN * 2 * p.sk.t;
+    const uint32_t k_lds = lds_address(sm.k[0]), v_lds = lds_address(sm.v[0]);
     if (n > 0) {
-        st_kv.load(kp, j_first, p.Tk - 1, sm.k[0], wave, lane);
-        st_kv.load(vp, j_first, p.Tk - 1, sm.v[0], wave, lane);
+        loads.load(k_rows, j_first, p.Tk - 1, k_lds, lane);
+        loads.load(v_rows, j_first, p.Tk - 1, v_lds, lane);
     }
     bf8v qf[KS], gf[KS];
     float delta = 0.f;
@@ -149,54 +155,65 @@ __global__ __launch_bounds__(64 * kQWaves, 2) void attn_dq_kernel(AttnParams p, 
     const float to2 = p.scale * kLog2e;
 
     bool bad = false;
-    for (int it = 0; it < n; ++it) {
-        const int j0 = j_first + it * kQN, buf = it & 1;
+    int j0 = j_first;
+    // one tile, in buffer BUF; false ends the walk
+    auto tile_step = [&](auto buffer) {
+        constexpr int BUF = decltype(buffer)::value, kTile = kQN * D * 2;
+        constexpr int kKey = BUF * kTile, kVal = (int)(offsetof(DqSmem<D>, v) - offsetof(DqSmem<D>, k)) + BUF * kTile;
         wait_loads();
         lds_barrier();
-        if (it + 1 < n) {
-            st_kv.load(kp, j0 + kQN, p.Tk - 1, sm.k[buf ^ 1], wave, lane);
-            st_kv.load(vp, j0 + kQN, p.Tk - 1, sm.v[buf ^ 1], wave, lane);
+        if (j0 + kQN < end) {
+            k_rows += tile_bytes;
+            v_rows += tile_bytes;
+            loads.load(k_rows, j0 + kQN, p.Tk - 1, k_lds + (BUF ^ 1) * kTile, lane);
+            loads.load(v_rows, j0 + kQN, p.Tk - 1, v_lds + (BUF ^ 1) * kTile, lane);
         }
-        const bool inner = j0 >= lo_most && j0 + kQN <= hi_least;
-        if (!inner) {
-            const bool mine = any_not_finite<D>(sm.k[buf] + 16 * wave * D, lane);
+        const bool edge = j0 < lo_most || j0 + kQN > hi_least;
+        if (edge) {
+            const bool mine = any_not_finite<D>(sm.k[BUF] + 16 * wave * D, lane);
             if (lane == 0) sm.bad[wave] = mine;
             lds_barrier();
             bad = (sm.bad[0] | sm.bad[1] | sm.bad[2] | sm.bad[3]) != 0;
-            if (bad) break;
+            if (bad) return false;
         }
-        if (!__any(hi > j0 && lo < j0 + kQN)) continue;
-        const bool whole = !__any(lo > j0 || hi < j0 + kQN);
-        const ReadAt<D> kt = at_lane.fresh(lds_address(sm.k[buf]));
-        constexpr int kV = offsetof(DqSmem<D>, v) - offsetof(DqSmem<D>, k);
+        if (!edge || __any(hi > j0 && lo < j0 + kQN)) {
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            float16v st, dp;
-            zero16(st);
-            zero16(dp);
+            for (int kb = 0; kb < 2; ++kb) {
+                float16v st, dp;
+                zero16(st);
+                zero16(dp);
 #pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                st = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kt.row_frag(32 * kb, s), qf[s], st, 0, 0, 0);
-                dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kt.row_frag(32 * kb, s, kV), gf[s], dp, 0, 0, 0);
+                for (int s = 0; s < KS; ++s) {
+                    st = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kt.row_frag(32 * kb, s, kKey), qf[s], st, 0, 0, 0);
+                    dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kt.row_frag(32 * kb, s, kVal), gf[s], dp, 0, 0, 0);
+                }
+                sched_reads_ahead<4, 2 * KS, 1>();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) st[i] = __builtin_amdgcn_exp2f(st[i] * to2 - lse2) * (dp[i] - delta);
+                if (edge) {
+                    const int base = j0 + 32 * kb + 4 * h - lo;
+                    const unsigned seen = (unsigned)(hi - lo);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if ((unsigned)(base + 8 * (i / 4) + i % 4) >= seen) st[i] = 0.f;
+                }
+                bf8v ds[2];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) ds[i / 8][i % 8] = (__bf16)st[i];
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int i = 0; i < DB; ++i)
+                        dq[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kt.col_frag(32 * kb + 16 * s, i, kKey), ds[s], dq[i], 0, 0, 0);
+                sched_reads_ahead<4, 2 * DB, 2>();
             }
-            sched_reads_ahead<4, 2 * KS, 1>();
-            bf8v ds[2];
-            const int base = j0 + 32 * kb + 4 * h - lo;
-            const unsigned seen = (unsigned)(hi - lo);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float x = __builtin_amdgcn_exp2f(st[i] * to2 - lse2) * (dp[i] - delta);
-                if (!whole && (unsigned)(base + 8 * (i / 4) + i % 4) >= seen) x = 0.f;
-                ds[i / 8][i % 8] = (__bf16)x;
-            }
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int i = 0; i < DB; ++i)
-                    dq[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kt.col_frag(32 * kb + 16 * s, i), ds[s], dq[i], 0, 0, 0);
-            sched_reads_ahead<4, 2 * DB, 2>();
         }
-    }
+        j0 += kQN;
+        return j0 < end;
+    };
+    if (n > 0)
+        while (tile_step(std::integral_constant<int, 0>{}) && tile_step(std::integral_constant<int, 1>{})) {
+        }
     if (bad) {
         wait_loads();                                 // no load into LDS outlives the wave
         const long long head = b * p.sq.b + hq * p.sq.h;
@@ -309,6 +326,7 @@ __global__ __launch_bounds__(64 * kKWaves, 2) void attn_dkv_kernel(AttnParams p,
     // the queries that see key j: places j .. j + window - 1, inside its sequence;
     // kept in LDS, for the steps that need them lane by lane
     int see_from = INT_MAX, see_to = 0, all_from = 0, all_to = INT_MAX;   // of the wave's keys: some row / every key
+    int alone_from = INT_MAX, alone_to = -1;
 #pragma unroll
     for (int kb = 0; kb < kKB; ++kb) {
         const int in = 32 * (kKB * wave + kb) + col, j = c0 + in;
@@ -318,7 +336,10 @@ __global__ __launch_bounds__(64 * kKWaves, 2) void attn_dkv_kernel(AttnParams p,
         // a query that sees this key alone, or -1: the window is one key, or the key is
         // its sequence's first
         const bool first = j == 0 || (p.cu_seqlens && (in == 0 ? sm.shared[2] != 0 : sm.bound[in - 1] == j));
-        if (h == 0) sm.range[in] = make_int4(lo, hi, (p.window == 1 || first) ? j - off : -1, 0);
+        const int alone = (p.window == 1 || first) ? j - off : -1;
+        if (h == 0) sm.range[in] = make_int4(lo, hi, alone, 0);
+        if (alone >= 0) alone_from = min(alone_from, alone);
+        alone_to = max(alone_to, alone);
         if (hi > lo) see_from = min(see_from, lo);
         see_to = max(see_to, hi);
         all_from = max(all_from, hi > lo ? lo : INT_MAX);
@@ -329,11 +350,15 @@ __global__ __launch_bounds__(64 * kKWaves, 2) void attn_dkv_kernel(AttnParams p,
         see_to = max(see_to, __shfl_xor(see_to, x, 64));
         all_from = max(all_from, __shfl_xor(all_from, x, 64));
         all_to = min(all_to, __shfl_xor(all_to, x, 64));
+        alone_from = min(alone_from, __shfl_xor(alone_from, x, 64));
+        alone_to = max(alone_to, __shfl_xor(alone_to, x, 64));
     }
     see_from = __builtin_amdgcn_readfirstlane(see_from);
     see_to = __builtin_amdgcn_readfirstlane(see_to);
     all_from = __builtin_amdgcn_readfirstlane(all_from);
     all_to = __builtin_amdgcn_readfirstlane(all_to);
+    alone_from = __builtin_amdgcn_readfirstlane(alone_from);
+    alone_to = __builtin_amdgcn_readfirstlane(alone_to);
     const int last_key = min(c0 + kKN, used) - 1;
     const int begin = max(c0 - off, 0);
     int end = rows, hi_least = rows;
@@ -367,30 +392,41 @@ __global__ __launch_bounds__(64 * kKWaves, 2) void attn_dkv_kernel(AttnParams p,
     const float to2 = p.scale * kLog2e;
 
     const ReadAt<D> at_lane(lane);
-    const Stager<D, kKM, kKWaves> st_q(p.sq.t, lane);
+    const Stager<D, kKM, kKWaves, false> loads(p.sq.t, wave, lane);
     const int i_first = begin / kKM * kKM;
-    const int per = end > begin ? (end - i_first + kKM - 1) / kKM : 0, n = per * heads;
+    const int n = end > begin ? (end - i_first + kKM - 1) / kKM * heads : 0;
     const long long all = (long long)p.B * p.Hq * p.Tq;
+    const uint64_t step_bytes = (uint64_t)kKM * 2 * p.sq.t;
 
-    auto fetch = [&](int it, int buf) {
-        const int hq = h0 + it / per, i0 = i_first + it % per * kKM;
-        const uint16_t* qp = (const uint16_t*)p.q + b * p.sq.b + hq * p.sq.h;
-        const uint16_t* gp = (const uint16_t*)p.dO + b * p.sq.b + hq * p.sq.h;
-        st_q.load(qp, i0, p.Tq - 1, sm.q[buf], wave, lane);
-        st_q.load(gp, i0, p.Tq - 1, sm.g[buf], wave, lane);
-        if (wave < 2) {
-            const float* st = p.delta + (wave ? all : 0) + ((long long)b * p.Hq + hq) * p.Tq + i0;
-            direct_load4(4 * min(lane, p.Tq - 1 - i0), (uint64_t)st,
-                         (uint32_t)(uintptr_t)(__attribute__((address_space(3))) float*)(wave ? sm.lse2[buf] : sm.delta[buf]));
+    // the step whose loads go out next: queries next_i .. of head next_h
+    int next_h = h0, next_i = i_first;
+    uint64_t q_rows = 0, g_rows = 0, stats = 0;
+    auto fetch = [&](int buf) {
+        if (next_i == i_first) {
+            q_rows = loads.rows((const uint16_t*)p.q + b * p.sq.b + next_h * p.sq.h, i_first);
+            g_rows = loads.rows((const uint16_t*)p.dO + b * p.sq.b + next_h * p.sq.h, i_first);
+            stats = (uint64_t)(p.delta + (wave ? all : 0) + ((long long)b * p.Hq + next_h) * p.Tq + i_first);
         }
+        loads.load(q_rows, next_i, p.Tq - 1, lds_address(sm.q[0]) + buf * kKM * D * 2, lane);
+        loads.load(g_rows, next_i, p.Tq - 1, lds_address(sm.g[0]) + buf * kKM * D * 2, lane);
+        if (wave < 2)
+            direct_load4(4 * min(lane, p.Tq - 1 - next_i), stats, lds_address(wave ? sm.lse2[0] : sm.delta[0]) + buf * kKM * 4);
+        q_rows += step_bytes;
+        g_rows += step_bytes;
+        stats += kKM * 4;
+        next_i += kKM;
+        if (next_i >= end) { next_i = i_first; ++next_h; }
     };
-    if (n > 0) fetch(0, 0);
+    if (n > 0) fetch(0);
     bool bad = false;
+    int i0 = i_first - kKM;
     for (int it = 0; it < n; ++it) {
-        const int i0 = i_first + it % per * kKM, buf = it & 1;
+        const int buf = it & 1;
+        i0 += kKM;
+        if (i0 >= end) i0 = i_first;
         wait_loads();
         lds_barrier();
-        if (it + 1 < n) fetch(it + 1, buf ^ 1);
+        if (it + 1 < n) fetch(buf ^ 1);
         const uint16_t* qt = sm.q[buf];
         const uint16_t* gt = sm.g[buf];
         const bool inner = i0 >= lo_most && i0 + kKM <= hi_least;
@@ -401,6 +437,9 @@ __global__ __launch_bounds__(64 * kKWaves, 2) void attn_dkv_kernel(AttnParams p,
                 const int r = (kKM / kKWaves) * wave + 16 * i;
                 mine = mine || any_not_finite<D>(qt + r * D, lane) || any_not_finite<D>(gt + r * D, lane);
             }
+            // a masked pair's weight is 0, and so must be its product with dO v - D
+            const float d = sm.delta[buf][lane], l2 = sm.lse2[buf][lane];
+            mine = mine || __any(!(fabsf(d) < INFINITY) || !(l2 > -INFINITY));
             if (lane == 0) sm.bad[wave] = mine;
             lds_barrier();
             bad = false;
@@ -420,36 +459,47 @@ __global__ __launch_bounds__(64 * kKWaves, 2) void attn_dkv_kernel(AttnParams p,
 #pragma unroll
             for (int kb = 0; kb < kKB; ++kb) zero16(st[kb]);
 #pragma unroll
-            for (int s = 0; s < KS; ++s) {
+            for (int s = 0; s < KR; ++s) {
                 const bf8v a = at.row_frag(32 * ib, s);
 #pragma unroll
-                for (int kb = 0; kb < kKB; ++kb) {
-                    const bf8v k = s < KR ? kf[kb][s < KR ? s : 0]
-                                          : __builtin_bit_cast(bf8v, sm.key[kKB * wave + kb][s < KR ? 0 : s - KR][lane]);
-                    st[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, k, st[kb], 0, 0, 0);
-                }
+                for (int kb = 0; kb < kKB; ++kb) st[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, kf[kb][s], st[kb], 0, 0, 0);
             }
-            sched_reads_ahead<3, KS, 1, kKB>();
+            sched_reads_ahead<2, KR, 1, kKB>();
             __builtin_amdgcn_sched_barrier(0);        // the registers are full: no reads for the next part yet
-            bf8v pf[kKB][2];
+            if constexpr (KR < KS) {
 #pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4) {
-                const float4v l4 = *reinterpret_cast<const float4v*>(&sm.lse2[buf][32 * ib + 8 * q4 + 4 * h]);
+                for (int s = KR; s < KS; ++s) {
+                    const bf8v a = at.row_frag(32 * ib, s);
 #pragma unroll
-                for (int kb = 0; kb < kKB; ++kb)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) st[kb][4 * q4 + i] = __builtin_amdgcn_exp2f(st[kb][4 * q4 + i] * to2 - l4[i]);
+                    for (int kb = 0; kb < kKB; ++kb) {
+                        const bf8v k = __builtin_bit_cast(bf8v, sm.key[kKB * wave + kb][s - KR][lane_now()]);
+                        st[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, k, st[kb], 0, 0, 0);
+                    }
+                }
+                sched_reads_ahead<2, KS - KR, 1 + kKB, kKB>();
+                __builtin_amdgcn_sched_barrier(0);
             }
             if (!whole) {
 #pragma unroll
                 for (int kb = 0; kb < kKB; ++kb) {
-                    const int4 see = sm.range[32 * (kKB * wave + kb) + col];
-                    const int from = ir + 4 * h - see.x;
+                    const int here = lane_now();
+                    const int2 see = *reinterpret_cast<const int2*>(&sm.range[32 * (kKB * wave + kb) + (here & 31)]);
+                    const int from = ir + 4 * (here >> 5) - see.x;
                     const unsigned seen = (unsigned)(see.y - see.x);
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        if ((unsigned)(from + 8 * (i / 4) + i % 4) >= seen) st[kb][i] = 0.f;
+                        if ((unsigned)(from + 8 * (i / 4) + i % 4) >= seen) st[kb][i] = -INFINITY;
                 }
+            }
+            bf8v pf[kKB][2];
+            const float* lse_at = &sm.lse2[buf][32 * ib + 4 * (lane_now() >> 5)];
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4) {
+                const float4v l4 = *reinterpret_cast<const float4v*>(lse_at + 8 * q4);
+#pragma unroll
+                for (int kb = 0; kb < kKB; ++kb)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) st[kb][4 * q4 + i] = __builtin_amdgcn_exp2f(st[kb][4 * q4 + i] * to2 - l4[i]);
             }
 #pragma unroll
             for (int kb = 0; kb < kKB; ++kb)
@@ -463,7 +513,7 @@ __global__ __launch_bounds__(64 * kKWaves, 2) void attn_dkv_kernel(AttnParams p,
 #pragma unroll
                     for (int kb = 0; kb < kKB; ++kb) dv[kb][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(g, pf[kb][s], dv[kb][i], 0, 0, 0);
                 }
-            sched_reads_ahead<3, 2 * DB, 2, kKB>();
+            sched_reads_ahead<2, 2 * DB, 2, kKB>();
             __builtin_amdgcn_sched_barrier(0);
             // their gradients, and dk from them
 #pragma unroll
@@ -474,30 +524,26 @@ __global__ __launch_bounds__(64 * kKWaves, 2) void attn_dkv_kernel(AttnParams p,
 #pragma unroll
                 for (int kb = 0; kb < kKB; ++kb) dp[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(g, vf[kb][s], dp[kb], 0, 0, 0);
             }
-            sched_reads_ahead<3, KS, 1, kKB>();
+            sched_reads_ahead<2, KS, 1, kKB>();
             __builtin_amdgcn_sched_barrier(0);
             bf8v ds[kKB][2];
+            const float* delta_at = &sm.delta[buf][32 * ib + 4 * (lane_now() >> 5)];
 #pragma unroll
             for (int q4 = 0; q4 < 4; ++q4) {
-                const float4v d4 = *reinterpret_cast<const float4v*>(&sm.delta[buf][32 * ib + 8 * q4 + 4 * h]);
+                const float4v d4 = *reinterpret_cast<const float4v*>(delta_at + 8 * q4);
 #pragma unroll
                 for (int kb = 0; kb < kKB; ++kb)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) dp[kb][4 * q4 + i] = st[kb][4 * q4 + i] * (dp[kb][4 * q4 + i] - d4[i]);
             }
-            if (!whole) {
-                // nothing from masked pairs (0 * NaN), nor from a query that sees this key only
+            if (ir <= alone_to && ir + 32 > alone_from) {
+                // nothing from a query that sees this key only
 #pragma unroll
                 for (int kb = 0; kb < kKB; ++kb) {
-                    const int4 see = sm.range[32 * (kKB * wave + kb) + col];
-                    const int from = ir + 4 * h - see.x, alone = see.z - ir - 4 * h;
-                    const unsigned seen = (unsigned)(see.y - see.x);
+                    const int here = lane_now();
+                    const int alone = sm.range[32 * (kKB * wave + kb) + (here & 31)].z - ir - 4 * (here >> 5);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int r = 8 * (i / 4) + i % 4;
-                        dp[kb][i] *= r == alone ? 0.f : 1.f;
-                        if ((unsigned)(from + r) >= seen) dp[kb][i] = 0.f;
-                    }
+                    for (int i = 0; i < 16; ++i) dp[kb][i] *= 8 * (i / 4) + i % 4 == alone ? 0.f : 1.f;
                 }
             }
 #pragma unroll
@@ -512,7 +558,7 @@ __global__ __launch_bounds__(64 * kKWaves, 2) void attn_dkv_kernel(AttnParams p,
 #pragma unroll
                     for (int kb = 0; kb < kKB; ++kb) dk[kb][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, ds[kb][s], dk[kb][i], 0, 0, 0);
                 }
-            sched_reads_ahead<3, 2 * DB, 2, kKB>();
+            sched_reads_ahead<2, 2 * DB, 2, kKB>();
             __builtin_amdgcn_sched_barrier(0);
         }
     }
@@ -529,6 +575,11 @@ __global__ __launch_bounds__(64 * kKWaves, 2) void attn_dkv_kernel(AttnParams p,
     for (int kb = 0; kb < kKB; ++kb) {
         const int key = c0 + 32 * (kKB * wave + kb) + col;
         if (key >= used) continue;
+        const int2 see = *reinterpret_cast<const int2*>(&sm.range[key - c0]);
+        if (see.y <= see.x) {                         // no query sees it: 0, not its 0 * NaN
+#pragma unroll
+            for (int i = 0; i < DB; ++i) { zero16(dk[kb][i]); zero16(dv[kb][i]); }
+        }
         if (p.splits == 1) {
             const long long at = b * p.sk.b + hk * p.sk.h + (long long)key * p.sk.t;
 #pragma unroll

@@ -12,6 +12,8 @@
 // and the rescaling are per lane, and S^T's registers are P^T's operand as they
 // stand: an MFMA contracts over any order of the keys that both operands share,
 // so the value operand is read with the same order (transposing LDS reads).
+#include <type_traits>
+
 #include "gdr_attn_tile.h"
 
 namespace gdr {
@@ -114,86 +116,107 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_kernel(AttnParams p, 
     float m = -INFINITY, l = 0.f;
     const float to2 = p.scale * kLog2e;
 
-    const ReadAt<D> at_lane(lane);
-    const Stager<D, kBN, kWaves> st_kv(p.sk.t, lane);
+    // two tiles a turn, so that every LDS address is a fixed register and a constant
+    const ReadAt<D> kt = ReadAt<D>(lane).in(lds_address(sm.k[0]));
+    const Stager<D, kBN, kWaves, true> loads(p.sk.t, wave, lane);
     const int j_first = begin / kBN * kBN;
     const int n = end > begin ? (end - j_first + kBN - 1) / kBN : 0;
-    if (n > 0) {
-        st_kv.load(kp, j_first, p.Tk - 1, sm.k[0], wave, lane);
-        st_kv.load(vp, j_first, p.Tk - 1, sm.v[0], wave, lane);
-    }
+    uint64_t k_rows = loads.rows(kp, j_first), v_rows = loads.rows(vp, j_first);
+    const uint64_t tile_bytes = (uint64_t)kBN * 2 * p.sk.t;
+    const uint32_t k_lds = lds_address(sm.k[0]), v_lds = lds_address(sm.v[0]);
+    const float ahead = 8.f / to2;
+    float shift = 0.f;
     bool bad = false;
-    for (int it = 0; it < n; ++it) {
-        const int j0 = j_first + it * kBN, buf = it & 1;
+    int j0 = j_first;
+    if (n > 0) {
+        loads.load(k_rows, j0, p.Tk - 1, k_lds, lane);
+        loads.load(v_rows, j0, p.Tk - 1, v_lds, lane);
+    }
+    // one tile, in buffer BUF; false ends the walk
+    auto tile_step = [&](auto buffer) {
+        constexpr int BUF = decltype(buffer)::value, kTile = kBN * D * 2;
+        constexpr int kK = BUF * kTile, kV = (int)(offsetof(FwdSmem<D>, v) - offsetof(FwdSmem<D>, k)) + BUF * kTile;
         wait_loads();
         lds_barrier();
-        if (it + 1 < n) {
-            st_kv.load(kp, j0 + kBN, p.Tk - 1, sm.k[buf ^ 1], wave, lane);
-            st_kv.load(vp, j0 + kBN, p.Tk - 1, sm.v[buf ^ 1], wave, lane);
+        if (j0 + kBN < end) {
+            k_rows += tile_bytes;
+            v_rows += tile_bytes;
+            loads.load(k_rows, j0 + kBN, p.Tk - 1, k_lds + (BUF ^ 1) * kTile, lane);
+            loads.load(v_rows, j0 + kBN, p.Tk - 1, v_lds + (BUF ^ 1) * kTile, lane);
         }
         // tiles that some row of the workgroup sees in part: infinities and NaN among
         // values that are masked for a row must not reach it through 0 * inf
         const bool edge = j0 < lo_most || j0 + kBN > hi_least;
         if (edge) {
-            const bool mine = any_not_finite<D>(sm.v[buf] + 16 * wave * D, lane);
+            const bool mine = any_not_finite<D>(sm.v[BUF] + 16 * wave * D, lane);
             if (lane == 0) sm.bad[wave] = mine;
             lds_barrier();
             bad = (sm.bad[0] | sm.bad[1] | sm.bad[2] | sm.bad[3]) != 0;
-            if (bad) break;
-            if (!__any(hi > j0 && lo < j0 + kBN)) continue;
+            if (bad) return false;
         }
-        const ReadAt<D> kt = at_lane.fresh(lds_address(sm.k[buf]));
-        float16v st[2];
+        if (!edge || __any(hi > j0 && lo < j0 + kBN)) {
+            float16v st[2];
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
+            for (int kb = 0; kb < 2; ++kb) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) st[kb][j] = 0.f;
+                for (int j = 0; j < 16; ++j) st[kb][j] = 0.f;
 #pragma unroll
-            for (int s = 0; s < KS; ++s)
-                st[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kt.row_frag(32 * kb, s), qf[s], st[kb], 0, 0, 0);
-        }
-        sched_reads_ahead<4, 2 * KS, 1>();
-        if (edge) {
-            const int base = j0 + 4 * h - lo;
-            const unsigned seen = (unsigned)(hi - lo);
+                for (int s = 0; s < KS; ++s)
+                    st[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kt.row_frag(32 * kb, s, kK), qf[s], st[kb], 0, 0, 0);
+            }
+            sched_reads_ahead<4, 2 * KS, 1>();
+            if (edge) {
+                const int base = j0 + 4 * h - lo;
+                const unsigned seen = (unsigned)(hi - lo);
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if ((unsigned)(base + 32 * kb + 8 * (i / 4) + i % 4) >= seen) st[kb][i] = -INFINITY;
+            }
+            float top = st[0][0];
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if ((unsigned)(base + 32 * kb + 8 * (i / 4) + i % 4) >= seen) st[kb][i] = -INFINITY;
-        }
-        float top = m;
+                for (int i = 0; i < 16; ++i) top = fmaxf(top, st[kb][i]);
+            top = max_across32(top);
+            // m follows the maximum only when that is more than 2^8 ahead: weights up to
+            // 2^8 keep their relative precision, and the sums their room, while some row
+            // of 32 has a new maximum in most tiles (64 products to rescale o)
+            if (__any(top > m + ahead)) {
+                asm volatile("");                         // a branch, not 64 products and selects
+                top = fmaxf(top, m);
+                const float fade = m == top ? 1.f : __builtin_amdgcn_exp2f((m - top) * to2);
+                m = top;
+                shift = top == -INFINITY ? 0.f : top * to2;
+                l *= fade;
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) top = fmaxf(top, st[kb][i]);
-        top = max_across32(top);
-        const float shift = top == -INFINITY ? 0.f : top * to2;
-        const float fade = m == top ? 1.f : __builtin_amdgcn_exp2f((m - top) * to2);
-        m = top;
-        if (__any(fade != 1.f)) {                     // rare once the maxima have settled
-            asm volatile("");                         // a branch, not 64 products and selects
-#pragma unroll
-            for (int i = 0; i < DB; ++i) o[i] *= fade;
-        }
-        float sum = 0.f;
-        bf8v pf[4];
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float x = __builtin_amdgcn_exp2f(st[kb][i] * to2 - shift);
-                sum += x;
-                pf[2 * kb + i / 8][i % 8] = (__bf16)x;
+                for (int i = 0; i < DB; ++i) o[i] *= fade;
             }
-        l = l * fade + sum;
+            float sum[2] = {0.f, 0.f};
+            bf8v pf[4];
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
+            for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-            for (int i = 0; i < DB; ++i)
-                o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kt.col_frag(16 * s, i, (int)(offsetof(FwdSmem<D>, v) - offsetof(FwdSmem<D>, k))), pf[s], o[i], 0, 0, 0);
-        sched_reads_ahead<4, 4 * DB, 2>();
-    }
+                for (int i = 0; i < 16; ++i) {
+                    const float x = __builtin_amdgcn_exp2f(st[kb][i] * to2 - shift);
+                    sum[kb] += x;
+                    pf[2 * kb + i / 8][i % 8] = (__bf16)x;
+                }
+            l += sum[0] + sum[1];
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int i = 0; i < DB; ++i)
+                    o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kt.col_frag(16 * s, i, kV), pf[s], o[i], 0, 0, 0);
+            sched_reads_ahead<4, 4 * DB, 2>();
+        }
+        j0 += kBN;
+        return j0 < end;
+    };
+    if (n > 0)
+        while (tile_step(std::integral_constant<int, 0>{}) && tile_step(std::integral_constant<int, 1>{})) {
+        }
     if (bad) {
         wait_loads();                                 // no load into LDS outlives the wave
         rows_one_by_one<D>(p, qp, kp, vp, (uint16_t*)p.o + b * p.sq.b + hq * p.sq.h,

@@ -21,9 +21,16 @@ namespace attn {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// 16 (4) bytes a lane from base + off to LDS at `to` + 16 (4) lane; `base` and `to` uniform.
-__device__ __forceinline__ void direct_load16(int off, uint64_t base, uint32_t to) {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(to) : "memory");
+// 16 (4) bytes a lane from base + off (unsigned) to LDS at `to` + `more` + 16 (4)
+// lane; `base` and `to` uniform.
+template <int MORE> __device__ __forceinline__ void direct_load16(int off, uint64_t base, uint32_t to) {
+    asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                 ::"v"(off), "s"(base), "s"(to), "i"(MORE) : "memory", "scc");
+}
+// the same with a 64-bit address per lane
+template <int MORE> __device__ __forceinline__ void direct_load16_far(uint64_t at, uint32_t to) {
+    asm volatile("s_add_u32 m0, %1, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+                 ::"v"(at), "s"(to), "i"(MORE) : "memory", "scc");
 }
 __device__ __forceinline__ void direct_load4(int off, uint64_t base, uint32_t to) {
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "s"(to) : "memory");
@@ -41,45 +48,74 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 }
 
 // ROWS rows of a tensor, its rows `stride` elements apart, into LDS by 16-byte
-// direct loads of WAVES waves: lane offsets fixed, a scalar base that moves.  Rows
-// past `last` are held at it.  The loads are issued in assembly, which the
+// direct loads of WAVES waves: lane offsets fixed, a scalar address that moves.  Rows
+// past the last are held at it.  The loads are issued in assembly, which the
 // compiler does not count: with the builtin it makes every later LDS read wait for
 // every load in flight (vmcnt(0)), so the next tile's loads could not stay
-// in flight across the work on this one (forward at B=2 H=16 T=8192 d=128 window
-// 2048: 302 us with the builtin).  They have no output registers; wait_loads()
-// and a barrier complete them.
-template <int D, int ROWS, int WAVES>
+// in flight across the work on this one.  They have no output registers;
+// wait_loads() and a barrier complete them.  What counts beside the bytes is the
+// instructions: KEEP holds one offset register per load (three instructions each),
+// otherwise one register serves all (six each).
+template <int D, int ROWS, int WAVES, bool KEEP>
 struct Stager {
     static constexpr int CH = D / 8, RPI = 64 / CH;  // chunks of a row, rows of one instruction
     static constexpr int N = ROWS / RPI / WAVES;
     static_assert(N * RPI * WAVES == ROWS, "rows split over the waves");
-    // byte offset of the lane's chunk from the first of an instruction's rows; a row
-    // is at least 2 D bytes from the next, so the swizzle's flips below stay inside it
-    int off;
-    long long stride;
+    // the swizzle of a row is that of lane / CH xor that of the instruction's first
+    // row, and the latter depends on the instruction alone, not on the wave
+    static_assert(N * RPI % 16 == 0, "the swizzle repeats every 16 rows");
+    int off[KEEP ? N : 1];
+    uint32_t group;                                   // bytes between two instructions' first rows
+    int skip;                                         // rows of the waves before this one
 
-    __device__ __forceinline__ Stager(long long stride_, int lane) : stride(stride_) {
+    __device__ __forceinline__ Stager(long long stride, int wave, int lane) {
         const int r = lane / CH;
-        off = (int)(2 * (r * stride + 8 * ((lane % CH) ^ swz<D>(r))));
-    }
-    __device__ __forceinline__ void load(const uint16_t* src, int first, int last, uint16_t* dst, int wave, int lane) const {
-        const uint32_t to = lds_address(dst) + wave * N * 1024;
-        const bool inside = first + ROWS - 1 <= last;
+        group = (uint32_t)(2 * RPI * stride);
+        skip = wave * N * RPI;
+        const int first = (int)(2 * (r * stride + 8 * ((lane % CH) ^ swz<D>(r))));
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int group = wave * N + i;           // swz of the group's rows: swz(lane / CH) ^ swz(group's first)
-            int row = first + group * RPI, at = off ^ (16 * swz<D>(group * RPI));
-            if (!inside) {
-                // the lane offset is unsigned: the base is held inside too
-                const int over = min(row, last) - last + lane / CH;
-                row = min(row, last);
-                at -= over > 0 ? (int)(2 * over * stride) : 0;
-            }
-            const uint64_t base = (uint64_t)(src + row * stride);
-            direct_load16(at, base, to + 1024 * i);
+        for (int i = 0; i < (KEEP ? N : 1); ++i) off[i] = (first ^ (16 * swz<D>(i * RPI))) + (int)(i * group);
+    }
+    // Address of the wave's first row of the tile that starts at row `first`.
+    __device__ __forceinline__ uint64_t rows(const uint16_t* src, int first) const {
+        return (uint64_t)src + (uint64_t)((long long)(first + skip) * (group / RPI));
+    }
+    // the tile that starts at row `first`, its rows() given
+    __device__ __forceinline__ void load(uint64_t rows, int first, int last, uint32_t to, int lane) const {
+        to += 2 * skip * D;
+        if (first + ROWS - 1 <= last) {
+            load_all<0>(rows, to);
+        } else {
+            load_held<0>(rows, first + skip, last, to, lane);
         }
     }
+
+private:
+    template <int I> __device__ __forceinline__ void load_all(uint64_t rows, uint32_t to) const {
+        if constexpr (KEEP) direct_load16<1024 * I>(off[I], rows, to);
+        else direct_load16<1024 * I>(off[0] ^ (16 * swz<D>(I * RPI)), rows + (uint64_t)I * group, to);
+        if constexpr (I + 1 < N) load_all<I + 1>(rows, to);
+    }
+    // the lane offset is unsigned: rows past the last are reached from the last one,
+    // not from a base behind it
+    template <int I> __device__ __forceinline__ void load_held(uint64_t rows, int first, int last, uint32_t to, int lane) const {
+        const int r = lane / CH, row = first + I * RPI + r, held = row < last ? row : last;
+        const long long stride = group / RPI;         // bytes
+        const int c = (lane % CH) ^ swz<D>(I * RPI + r);
+        // this lane's row relative to the tile's: at most ROWS rows before it or behind
+        const uint64_t at = rows + (long long)(held - first) * stride + 16 * c;
+        direct_load16_far<1024 * I>(at, to);
+        if constexpr (I + 1 < N) load_held<I + 1>(rows, first, last, to, lane);
+    }
 };
+
+// The lane's number, made anew where it is used: two instructions instead of a
+// register across the loop.
+__device__ __forceinline__ int lane_now() {
+    int x;
+    asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=&v"(x));
+    return x;
+}
 
 // Order of N groups of P products that share R LDS reads: AHEAD groups' reads go
 // first, then products and reads in turn.  Left alone, the compiler reads right
@@ -108,11 +144,16 @@ template <int D> struct ReadAt {
         const int j = 4 * h + ((lane & 15) >> 2), ch = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
         col = 2 * (j * D + 8 * (ch ^ swz<D>(j)) + 4 * (lane & 1));
     }
-    // the same inside the tile at LDS address `tile`
-    __device__ __forceinline__ ReadAt fresh(uint32_t tile) const {
+    // inside the tile at LDS address `tile`
+    __device__ __forceinline__ ReadAt in(uint32_t tile) const {
         ReadAt x = *this;
         x.row += tile;
         x.col += tile;
+        return x;
+    }
+    // the same, hidden
+    __device__ __forceinline__ ReadAt fresh(uint32_t tile) const {
+        ReadAt x = in(tile);
         asm volatile("" : "+v"(x.row), "+v"(x.col));
         return x;
     }
