@@ -572,14 +572,36 @@ def mixer_epilogue_bwd(o, g, norm_weight, dy, stream=None):
 # ---------------------------------------------------------------------------
 
 
-def _expect(name, t, shape, dtype, device):
-    """The tensor a call takes: its shape, type and device."""
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+def _expect(name, t, shape, dtype, gpu):
+    """The tensor a call takes: its shape, type, GPU and contiguity."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != gpu or not t.is_contiguous():
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if t.dtype is not dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.get_device() != gpu:
+            raise ValueError(f"{name} must be on GPU {gpu}, got {t.device}")
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _gpu_of(name, t):
+    """The index of the GPU that a call's first tensor is on."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU")
+    return t.get_device()
+
+
+def _launch(fn, gpu, stream, *args):
+    """The library call `fn` with the given GPU current, on `stream` or that GPU's
+    current one.  (The wrappers below take pointers and the stream's handle
+    directly: a small call's time is that of the host.)"""
+    if gpu != torch.cuda.current_device():
+        with torch.cuda.device(gpu):
+            return _launch(fn, gpu, stream, *args)
+    st = getattr(_lib or _load(), fn)(*args, torch._C._cuda_getCurrentRawStream(gpu) if stream is None
+                                      else stream.cuda_stream)
+    if st != 0:
+        raise GdrError(fn, st)
 
 
 def _kept_for(stream, *tensors):
@@ -631,54 +653,55 @@ def rope(q, k, inv_freq, positions=None, position0: int = 0, interleaved: bool =
     inv_freq: fp32 [rot_dim/2]; positions: int32 [B,T] (packed: [T]) or None for
     position0 + t.  inverse turns back: the gradients of q and k from those of the
     results.  Returns (q_out, k_out); they may be given, also as q and k themselves."""
-    packed = q.dim() == 3
-    if q.dim() not in (3, 4) or (k is not None and k.dim() != q.dim()):
+    shape = q.shape
+    n = len(shape)
+    if n not in (3, 4) or (k is not None and k.dim() != n):
         raise ValueError("q and k must both be [B,H,T,d] or both packed [H,T,d]")
-    ht = (1, 0) if token_major else (0, 1)
-    B, d = (1 if packed else q.shape[0]), q.shape[-1]
-    inner = q.shape[-3:-1]
-    Hq, T = inner[ht[0]], inner[ht[1]]
-    flags = _act_flag(q)
-    Hk = 0
-    if k is not None:
-        Hk = k.shape[-3:-1][ht[0]]
-        want = ((T, Hk, d) if token_major else (Hk, T, d))
-        _expect("k", k, want if packed else (B,) + want, q.dtype, q.device)
-    _expect("inv_freq", inv_freq, (inv_freq.numel(),), torch.float32, q.device)
-    if positions is not None:
-        _expect("positions", positions, (T,) if packed else (B, T), torch.int32, q.device)
-    flags |= (GDR_TOKEN_MAJOR if token_major else 0) | (GDR_ROPE_INTERLEAVED if interleaved else 0) \
+    gpu, dtype = _gpu_of("q", q), q.dtype
+    lead, d = shape[:-3], shape[-1]
+    B = lead[0] if n == 4 else 1
+    T, Hq = (shape[-3], shape[-2]) if token_major else (shape[-2], shape[-3])
+    flags = _act_flag(q) | (GDR_TOKEN_MAJOR if token_major else 0) | (GDR_ROPE_INTERLEAVED if interleaved else 0) \
         | (GDR_ROPE_INVERSE if inverse else 0)
-    made_q = made_k = None
+    made_q = made_k = k_ptr = ko_ptr = None
+    Hk = 0
+    _expect("q", q, shape, dtype, gpu)
+    if k is not None:
+        Hk = k.shape[-2 if token_major else -3]
+        _expect("k", k, lead + ((T, Hk, d) if token_major else (Hk, T, d)), dtype, gpu)
+        if k_out is None:
+            k_out = made_k = torch.empty_like(k)
+        else:
+            _expect("k_out", k_out, k.shape, dtype, gpu)
+        k_ptr, ko_ptr = k.data_ptr(), k_out.data_ptr()
     if q_out is None:
         q_out = made_q = torch.empty_like(q)
-    if k is not None and k_out is None:
-        k_out = made_k = torch.empty_like(k)
-    _expect("q_out", q_out, q.shape, q.dtype, q.device)
-    if k is not None:
-        _expect("k_out", k_out, k.shape, k.dtype, k.device)
-    with torch.cuda.device(q.device):
-        gdr_rope(q, k, q_out, k_out if k is not None else None, inv_freq, positions, position0, B, Hq, Hk, T, d,
-                 2 * inv_freq.numel(), scale, flags, stream)
+    else:
+        _expect("q_out", q_out, shape, dtype, gpu)
+    half = inv_freq.numel()
+    _expect("inv_freq", inv_freq, (half,), torch.float32, gpu)
+    if positions is not None:
+        _expect("positions", positions, lead + (T,), torch.int32, gpu)
+        positions = positions.data_ptr()
+    _launch("gdr_rope", gpu, stream, q.data_ptr(), k_ptr, q_out.data_ptr(), ko_ptr, inv_freq.data_ptr(), positions,
+            position0, B, Hq, Hk, T, d, 2 * half, scale, flags)
     _kept_for(stream, made_q, made_k)
     return q_out, k_out if k is not None else None
 
 
 def _attn_shapes(q, k, v, packed, token_major):
-    """(B, Hq, Hkv, Tq, Tk, d) of attention's inputs, checked."""
-    n = 3 if packed else 4
-    if q.dim() != n or k.dim() != n:
+    """(B, Hq, Hkv, Tq, Tk, d, GPU) of attention's inputs, checked."""
+    qs, ks = q.shape, k.shape
+    if len(qs) != (3 if packed else 4) or len(ks) != len(qs):
         raise ValueError("q, k and v must be " + ("[H,T,d]" if packed else "[B,H,T,d]"))
-    ht = (1, 0) if token_major else (0, 1)
-    (Hq, Tq), (Hkv, Tk) = ([x.shape[-3:-1][i] for i in ht] for x in (q, k))
-    B, d = (1 if packed else q.shape[0]), q.shape[-1]
-    if q.dtype != torch.bfloat16:
-        raise ValueError(f"q must be torch.bfloat16, got {q.dtype}")
-    want = (Tk, Hkv, d) if token_major else (Hkv, Tk, d)
-    want = want if packed else (B,) + want
-    _expect("k", k, want, torch.bfloat16, q.device)
-    _expect("v", v, want, torch.bfloat16, q.device)
-    return B, Hq, Hkv, Tq, Tk, d
+    gpu = _gpu_of("q", q)
+    h, t = (-2, -3) if token_major else (-3, -2)
+    B, Hq, Hkv, Tq, Tk, d = (1 if packed else qs[0]), qs[h], ks[h], qs[t], ks[t], qs[-1]
+    _expect("q", q, qs, torch.bfloat16, gpu)
+    want = qs[:-3] + ((Tk, Hkv, d) if token_major else (Hkv, Tk, d))
+    _expect("k", k, want, torch.bfloat16, gpu)
+    _expect("v", v, want, torch.bfloat16, gpu)
+    return B, Hq, Hkv, Tq, Tk, d, gpu
 
 
 def attn_fwd(q, k, v, window: int = 0, scale: Optional[float] = None, token_major: bool = False,
@@ -686,12 +709,12 @@ def attn_fwd(q, k, v, window: int = 0, scale: Optional[float] = None, token_majo
     """Causal attention.  q: [B,Hq,Tq,d], k, v: [B,Hkv,Tk,d] bf16 (token_major:
     [B,T,H,d]); query i sees the keys up to i + Tk - Tq, the last `window` of them
     (0: all); scale: 1/sqrt(d) if None.  Returns (o as q, lse fp32 [B,Hq,Tq] or None)."""
-    B, Hq, Hkv, Tq, Tk, d = _attn_shapes(q, k, v, False, token_major)
+    B, Hq, Hkv, Tq, Tk, d, gpu = _attn_shapes(q, k, v, False, token_major)
     o = torch.empty_like(q)
     lse = torch.empty((B, Hq, Tq), dtype=torch.float32, device=q.device) if return_lse else None
-    with torch.cuda.device(q.device):
-        gdr_attn_fwd(q, k, v, o, lse, B, Hq, Hkv, Tq, Tk, d, window, d ** -0.5 if scale is None else scale,
-                     GDR_TOKEN_MAJOR if token_major else 0, stream)
+    _launch("gdr_attn_fwd", gpu, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+            lse.data_ptr() if return_lse else None, B, Hq, Hkv, Tq, Tk, d, window,
+            d ** -0.5 if scale is None else scale, GDR_TOKEN_MAJOR if token_major else 0)
     _kept_for(stream, o, lse)
     return o, lse
 
@@ -701,40 +724,41 @@ def attn_fwd_varlen(q, k, v, cu_seqlens, window: int = 0, scale: Optional[float]
     """Packed sequences: q: [Hq,T,d], k, v: [Hkv,T,d] bf16 (token_major: [T,H,d]);
     cu_seqlens: int32 [nseq+1] on the GPU.  Returns (o as q, lse fp32 [Hq,T] or None);
     rows from cu_seqlens[nseq] on are not written."""
-    B, Hq, Hkv, T, Tk, d = _attn_shapes(q, k, v, True, token_major)
+    B, Hq, Hkv, T, Tk, d, gpu = _attn_shapes(q, k, v, True, token_major)
     if T != Tk:
         raise ValueError("packed q, k and v must have the same tokens")
-    _expect("cu_seqlens", cu_seqlens, (cu_seqlens.numel(),), torch.int32, q.device)
+    nseq = cu_seqlens.numel() - 1
+    _expect("cu_seqlens", cu_seqlens, (nseq + 1,), torch.int32, gpu)
     o = torch.empty_like(q)
     lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device) if return_lse else None
-    with torch.cuda.device(q.device):
-        gdr_attn_fwd_varlen(q, k, v, o, lse, cu_seqlens, cu_seqlens.numel() - 1, Hq, Hkv, T, d, window,
-                            d ** -0.5 if scale is None else scale, GDR_TOKEN_MAJOR if token_major else 0, stream)
+    _launch("gdr_attn_fwd_varlen", gpu, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+            lse.data_ptr() if return_lse else None, cu_seqlens.data_ptr(), nseq, Hq, Hkv, T, d, window,
+            d ** -0.5 if scale is None else scale, GDR_TOKEN_MAJOR if token_major else 0)
     _kept_for(stream, o, lse)
     return o, lse
 
 
 def _attn_bwd(q, k, v, o, lse, dO, cu_seqlens, window, scale, token_major, stream):
     packed = cu_seqlens is not None
-    B, Hq, Hkv, Tq, Tk, d = _attn_shapes(q, k, v, packed, token_major)
+    B, Hq, Hkv, Tq, Tk, d, gpu = _attn_shapes(q, k, v, packed, token_major)
     if packed and Tq != Tk:
         raise ValueError("packed q, k and v must have the same tokens")
-    _expect("o", o, q.shape, torch.bfloat16, q.device)
-    _expect("dO", dO, q.shape, torch.bfloat16, q.device)
-    _expect("lse", lse, (Hq, Tq) if packed else (B, Hq, Tq), torch.float32, q.device)
+    _expect("o", o, q.shape, torch.bfloat16, gpu)
+    _expect("dO", dO, q.shape, torch.bfloat16, gpu)
+    _expect("lse", lse, (Hq, Tq) if packed else (B, Hq, Tq), torch.float32, gpu)
     scale = d ** -0.5 if scale is None else scale
     flags = GDR_TOKEN_MAJOR if token_major else 0
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     nbytes = gdr_attn_bwd_workspace_bytes(B, Hq, Hkv, Tq, Tk, d)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes > 0 else None
-    with torch.cuda.device(q.device):
-        if packed:
-            _expect("cu_seqlens", cu_seqlens, (cu_seqlens.numel(),), torch.int32, q.device)
-            gdr_attn_bwd_varlen(q, k, v, o, lse, dO, dq, dk, dv, cu_seqlens, cu_seqlens.numel() - 1, Hq, Hkv, Tq, d,
-                                window, scale, flags, ws, nbytes, stream)
-        else:
-            gdr_attn_bwd(q, k, v, o, lse, dO, dq, dk, dv, B, Hq, Hkv, Tq, Tk, d, window, scale, flags, ws, nbytes,
-                         stream)
+    ptrs = [t.data_ptr() for t in (q, k, v, o, lse, dO, dq, dk, dv)]
+    tail = (d, window, scale, flags, ws.data_ptr() if nbytes > 0 else None, nbytes)
+    if packed:
+        nseq = cu_seqlens.numel() - 1
+        _expect("cu_seqlens", cu_seqlens, (nseq + 1,), torch.int32, gpu)
+        _launch("gdr_attn_bwd_varlen", gpu, stream, *ptrs, cu_seqlens.data_ptr(), nseq, Hq, Hkv, Tq, *tail)
+    else:
+        _launch("gdr_attn_bwd", gpu, stream, *ptrs, B, Hq, Hkv, Tq, Tk, *tail)
     _kept_for(stream, dq, dk, dv, ws)
     return dict(dq=dq, dk=dk, dv=dv)
 
@@ -771,19 +795,22 @@ def kv_cache(n_pages, Hkv, d, device="cuda") -> KVCache:
                    torch.empty((n_pages, Hkv), dtype=torch.float32, device=device))
 
 
-def _cache_shapes(cache, block_table, cache_len, device):
-    n_pages, Hkv, P, d = cache.k.shape
+def _cache_shapes(cache, block_table, cache_len, gpu):
+    """(n_pages, Hkv, d, nseq, max_pages) of a cache and its tables, checked."""
+    ck, cv, ks, vs = cache
+    n_pages, Hkv, P, d = ck.shape
     if P != GDR_KV_PAGE:
         raise ValueError(f"a page holds {GDR_KV_PAGE} tokens, got {P}")
     if block_table.dim() != 2:
         raise ValueError("block_table must be [nseq, max_pages]")
-    _expect("cache.k", cache.k, (n_pages, Hkv, P, d), torch.uint8, device)
-    _expect("cache.v", cache.v, (n_pages, Hkv, P // 16, d, 16), torch.uint8, device)
-    _expect("cache.k_scale", cache.k_scale, (n_pages, Hkv), torch.float32, device)
-    _expect("cache.v_scale", cache.v_scale, (n_pages, Hkv), torch.float32, device)
-    _expect("block_table", block_table, block_table.shape, torch.int32, device)
-    _expect("cache_len", cache_len, (block_table.shape[0],), torch.int32, device)
-    return n_pages, Hkv, d
+    nseq, max_pages = block_table.shape
+    _expect("cache.k", ck, ck.shape, torch.uint8, gpu)
+    _expect("cache.v", cv, (n_pages, Hkv, P // 16, d, 16), torch.uint8, gpu)
+    _expect("cache.k_scale", ks, (n_pages, Hkv), torch.float32, gpu)
+    _expect("cache.v_scale", vs, (n_pages, Hkv), torch.float32, gpu)
+    _expect("block_table", block_table, block_table.shape, torch.int32, gpu)
+    _expect("cache_len", cache_len, (nseq,), torch.int32, gpu)
+    return n_pages, Hkv, d, nseq, max_pages
 
 
 def kv_append(k, v, cache: KVCache, block_table, cache_len, cu_seqlens=None, token_major: bool = False, stream=None):
@@ -791,8 +818,9 @@ def kv_append(k, v, cache: KVCache, block_table, cache_len, cu_seqlens=None, tok
     k, v: bf16 [nseq,Hkv,d], one token each; or with cu_seqlens int32 [nseq+1]
     packed [Hkv,T,d] (token_major: [T,Hkv,d]).  block_table: int32 [nseq,max_pages].
     cache_len stays as it is: raise it by the new lengths afterwards."""
-    n_pages, Hkv, d = _cache_shapes(cache, block_table, cache_len, k.device)
-    nseq = block_table.shape[0]
+    gpu = _gpu_of("k", k)
+    n_pages, Hkv, d, nseq, max_pages = _cache_shapes(cache, block_table, cache_len, gpu)
+    cu = None
     if cu_seqlens is None:
         T, want = nseq, (nseq, Hkv, d)
     else:
@@ -800,12 +828,13 @@ def kv_append(k, v, cache: KVCache, block_table, cache_len, cu_seqlens=None, tok
             raise ValueError("packed k and v must be [Hkv,T,d] or token-major [T,Hkv,d]")
         T = k.shape[0 if token_major else 1]
         want = (T, Hkv, d) if token_major else (Hkv, T, d)
-        _expect("cu_seqlens", cu_seqlens, (nseq + 1,), torch.int32, k.device)
-    _expect("k", k, want, torch.bfloat16, k.device)
-    _expect("v", v, want, torch.bfloat16, k.device)
-    with torch.cuda.device(k.device):
-        gdr_kv_append(k, v, cache.k, cache.v, cache.k_scale, cache.v_scale, block_table, cache_len, cu_seqlens, nseq,
-                      Hkv, T, d, n_pages, block_table.shape[1], GDR_TOKEN_MAJOR if token_major else 0, stream)
+        _expect("cu_seqlens", cu_seqlens, (nseq + 1,), torch.int32, gpu)
+        cu = cu_seqlens.data_ptr()
+    _expect("k", k, want, torch.bfloat16, gpu)
+    _expect("v", v, want, torch.bfloat16, gpu)
+    _launch("gdr_kv_append", gpu, stream, k.data_ptr(), v.data_ptr(), *[t.data_ptr() for t in cache],
+            block_table.data_ptr(), cache_len.data_ptr(), cu, nseq, Hkv, T, d, n_pages, max_pages,
+            GDR_TOKEN_MAJOR if token_major else 0)
 
 
 def attn_decode(q, cache: KVCache, block_table, cache_len, window: int = 0, scale: Optional[float] = None,
@@ -813,23 +842,26 @@ def attn_decode(q, cache: KVCache, block_table, cache_len, window: int = 0, scal
     """Attention of one token per sequence over the cache: q bf16 [N,Hq,d], the
     last of each sequence's cache_len tokens; sees all of them or the last
     `window`.  Returns o [N,Hq,d] of out_dtype (fp32 or bf16)."""
-    n_pages, Hkv, d = _cache_shapes(cache, block_table, cache_len, q.device)
-    N, max_pages = block_table.shape
+    gpu = _gpu_of("q", q)
+    n_pages, Hkv, d, N, max_pages = _cache_shapes(cache, block_table, cache_len, gpu)
     if q.dim() != 3:
         raise ValueError("q must be [N,Hq,d]")
-    Hq = q.shape[1]
-    _expect("q", q, (N, Hq, d), torch.bfloat16, q.device)
+    shape = (N, q.shape[1], d)
+    Hq = shape[1]
+    _expect("q", q, shape, torch.bfloat16, gpu)
     if out_dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"out_dtype must be float32 or bfloat16, got {out_dtype}")
-    made = None
+    made = ws = None
     if o is None:
-        o = made = torch.empty((N, Hq, d), dtype=out_dtype, device=q.device)
-    _expect("o", o, (N, Hq, d), out_dtype, q.device)
+        o = made = torch.empty(shape, dtype=out_dtype, device=q.device)
+    else:
+        _expect("o", o, shape, out_dtype, gpu)
     nbytes = gdr_attn_decode_workspace_bytes(N, Hq, Hkv, d, max_pages, window)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes > 0 else None
-    with torch.cuda.device(q.device):
-        gdr_attn_decode(q, cache.k, cache.v, cache.k_scale, cache.v_scale, block_table, cache_len, o, N, Hq, Hkv, d,
-                        n_pages, max_pages, window, d ** -0.5 if scale is None else scale,
-                        GDR_OUT_BF16 if out_dtype == torch.bfloat16 else 0, ws, nbytes, stream)
+    if nbytes > 0:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    _launch("gdr_attn_decode", gpu, stream, q.data_ptr(), *[t.data_ptr() for t in cache], block_table.data_ptr(),
+            cache_len.data_ptr(), o.data_ptr(), N, Hq, Hkv, d, n_pages, max_pages, window,
+            d ** -0.5 if scale is None else scale, GDR_OUT_BF16 if out_dtype is torch.bfloat16 else 0,
+            None if ws is None else ws.data_ptr(), nbytes)
     _kept_for(stream, made, ws)
     return o

@@ -82,7 +82,7 @@ struct AttnDecodeParams {
     const int* cache_len;
     void* o;
     float* part_o;              // [splits, N, Hq, d] unnormalised, or null when splits == 1
-    float* part_ml;             // [splits, N, Hq, 2]: running maximum (base 2) and sum
+    float* part_ml;             // [splits, N, Hq, 2]: running maximum (base 2) and sum (2^15 times)
     int N, Hq, Hkv, d, n_pages, max_pages, window;
     int splits, split_pages;    // pages of a split: split s of a sequence is its s-th run of them
     float scale;

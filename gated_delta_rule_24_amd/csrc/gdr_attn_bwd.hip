@@ -250,7 +250,7 @@ struct __attribute__((aligned(256))) DkvSmem {
     // key operands that do not fit the 256 registers beside the sums (d = 128): the
     // last kKeyLds of a key's D / 16
     uint4 key[kKWaves * kKB][kKeyLds<D> > 0 ? kKeyLds<D> : 1][64];
-    int4 range[kKN];            // of each key: first query, one past the last, one that sees only it
+    int4 range[kKN];            // of each key: first query, one past the last, whether alone
     int bound[kKN];
     int shared[3];
     int bad[kKWaves];
@@ -263,12 +263,12 @@ static_assert(sizeof(DkvSmem<128>) <= 80 * 1024 && sizeof(DkvSmem<64>) <= 80 * 1
 template <int D>
 __device__ __forceinline__ void keys_one_by_one(const AttnParams& p, const uint16_t* k, const uint16_t* v, int b, int bh, int hk,
                                                 int h0, int heads, int split, int first, int used, int lo32, int hi32,
-                                                int only32, int lane) {
+                                                int alone32, int lane) {
     const float to2 = p.scale * kLog2e;
     const long long all = (long long)p.B * p.Hq * p.Tq, one = (long long)p.B * p.Hkv * p.Tk * D;
     for (int r = 0; r < 32 && first + r < used; ++r) {
         const int lo = __builtin_amdgcn_readlane(lo32, r), hi = __builtin_amdgcn_readlane(hi32, r);
-        const int only = __builtin_amdgcn_readlane(only32, r);
+        const float by = __builtin_amdgcn_readlane(alone32, r) ? 0.f : p.scale;
         const long long j = (long long)(first + r) * p.sk.t;
         float dk[D / 64] = {}, dv[D / 64] = {};
         for (int hq = h0; hq < h0 + heads; ++hq) {
@@ -280,7 +280,7 @@ __device__ __forceinline__ void keys_one_by_one(const AttnParams& p, const uint1
                 if (i0 + lane < hi) {
                     const long long i = (long long)(i0 + lane) * p.sq.t;
                     x = __builtin_amdgcn_exp2f(dot_row<D>(q + i, k + j) * to2 - p.delta[all + stat + i0 + lane]);
-                    y = x * (dot_row<D>(g + i, v + j) - p.delta[stat + i0 + lane]) * (i0 + lane == only ? 0.f : 1.f);
+                    y = x * (dot_row<D>(g + i, v + j) - p.delta[stat + i0 + lane]);
                 }
                 add_rows<D>(dv, x, g + (long long)i0 * p.sq.t, p.sq.t, min(64, hi - i0), lane);
                 add_rows<D>(dk, y, q + (long long)i0 * p.sq.t, p.sq.t, min(64, hi - i0), lane);
@@ -290,11 +290,11 @@ __device__ __forceinline__ void keys_one_by_one(const AttnParams& p, const uint1
         for (int c = 0; c < D / 64; ++c) {
             if (p.splits == 1) {
                 const long long at = b * p.sk.b + hk * p.sk.h + j + lane + 64 * c;
-                ((uint16_t*)p.dk)[at] = f32_to_bf16(dk[c] * p.scale);
+                ((uint16_t*)p.dk)[at] = f32_to_bf16(dk[c] * by);
                 ((uint16_t*)p.dv)[at] = f32_to_bf16(dv[c]);
             } else {
                 float* at = p.part + split * one + ((long long)bh * p.Tk + first + r) * D + lane + 64 * c;
-                at[0] = dk[c] * p.scale;
+                at[0] = dk[c] * by;
                 at[p.splits * one] = dv[c];
             }
         }
@@ -326,20 +326,17 @@ __global__ __launch_bounds__(64 * kKWaves, 2) void attn_dkv_kernel(AttnParams p,
     // the queries that see key j: places j .. j + window - 1, inside its sequence;
     // kept in LDS, for the steps that need them lane by lane
     int see_from = INT_MAX, see_to = 0, all_from = 0, all_to = INT_MAX;   // of the wave's keys: some row / every key
-    int alone_from = INT_MAX, alone_to = -1;
 #pragma unroll
     for (int kb = 0; kb < kKB; ++kb) {
         const int in = 32 * (kKB * wave + kb) + col, j = c0 + in;
         int lo = max(j - off, 0), hi = p.cu_seqlens ? min(sm.bound[in], rows) : rows;
         if (p.window > 0) hi = min(hi, j - off + p.window);
         if (j >= used || hi <= lo) { lo = 0; hi = 0; }
-        // a query that sees this key alone, or -1: the window is one key, or the key is
-        // its sequence's first
+        // seen by one query that sees no other key: the window is one key, or the key is
+        // all its sequence has.  The softmax over one key is constant, its gradient 0
         const bool first = j == 0 || (p.cu_seqlens && (in == 0 ? sm.shared[2] != 0 : sm.bound[in - 1] == j));
-        const int alone = (p.window == 1 || first) ? j - off : -1;
+        const bool alone = p.window == 1 || (first && j >= off && hi - lo == 1);
         if (h == 0) sm.range[in] = make_int4(lo, hi, alone, 0);
-        if (alone >= 0) alone_from = min(alone_from, alone);
-        alone_to = max(alone_to, alone);
         if (hi > lo) see_from = min(see_from, lo);
         see_to = max(see_to, hi);
         all_from = max(all_from, hi > lo ? lo : INT_MAX);
@@ -350,15 +347,11 @@ __global__ __launch_bounds__(64 * kKWaves, 2) void attn_dkv_kernel(AttnParams p,
         see_to = max(see_to, __shfl_xor(see_to, x, 64));
         all_from = max(all_from, __shfl_xor(all_from, x, 64));
         all_to = min(all_to, __shfl_xor(all_to, x, 64));
-        alone_from = min(alone_from, __shfl_xor(alone_from, x, 64));
-        alone_to = max(alone_to, __shfl_xor(alone_to, x, 64));
     }
     see_from = __builtin_amdgcn_readfirstlane(see_from);
     see_to = __builtin_amdgcn_readfirstlane(see_to);
     all_from = __builtin_amdgcn_readfirstlane(all_from);
     all_to = __builtin_amdgcn_readfirstlane(all_to);
-    alone_from = __builtin_amdgcn_readfirstlane(alone_from);
-    alone_to = __builtin_amdgcn_readfirstlane(alone_to);
     const int last_key = min(c0 + kKN, used) - 1;
     const int begin = max(c0 - off, 0);
     int end = rows, hi_least = rows;
@@ -536,16 +529,6 @@ __global__ __launch_bounds__(64 * kKWaves, 2) void attn_dkv_kernel(AttnParams p,
 #pragma unroll
                     for (int i = 0; i < 4; ++i) dp[kb][4 * q4 + i] = st[kb][4 * q4 + i] * (dp[kb][4 * q4 + i] - d4[i]);
             }
-            if (ir <= alone_to && ir + 32 > alone_from) {
-                // nothing from a query that sees this key only
-#pragma unroll
-                for (int kb = 0; kb < kKB; ++kb) {
-                    const int here = lane_now();
-                    const int alone = sm.range[32 * (kKB * wave + kb) + (here & 31)].z - ir - 4 * (here >> 5);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) dp[kb][i] *= 8 * (i / 4) + i % 4 == alone ? 0.f : 1.f;
-                }
-            }
 #pragma unroll
             for (int kb = 0; kb < kKB; ++kb)
 #pragma unroll
@@ -575,7 +558,8 @@ __global__ __launch_bounds__(64 * kKWaves, 2) void attn_dkv_kernel(AttnParams p,
     for (int kb = 0; kb < kKB; ++kb) {
         const int key = c0 + 32 * (kKB * wave + kb) + col;
         if (key >= used) continue;
-        const int2 see = *reinterpret_cast<const int2*>(&sm.range[key - c0]);
+        const int4 see = sm.range[key - c0];
+        const float by = see.z ? 0.f : p.scale;
         if (see.y <= see.x) {                         // no query sees it: 0, not its 0 * NaN
 #pragma unroll
             for (int i = 0; i < DB; ++i) { zero16(dk[kb][i]); zero16(dv[kb][i]); }
@@ -586,7 +570,7 @@ __global__ __launch_bounds__(64 * kKWaves, 2) void attn_dkv_kernel(AttnParams p,
             for (int i = 0; i < DB; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    store4((uint16_t*)p.dk + at + 32 * i + 8 * j + 4 * h, dk[kb][i], j, p.scale);
+                    store4((uint16_t*)p.dk + at + 32 * i + 8 * j + 4 * h, dk[kb][i], j, by);
                     store4((uint16_t*)p.dv + at + 32 * i + 8 * j + 4 * h, dv[kb][i], j, 1.f);
                 }
         } else {
@@ -598,7 +582,7 @@ __global__ __launch_bounds__(64 * kKWaves, 2) void attn_dkv_kernel(AttnParams p,
                 for (int j = 0; j < 4; ++j) {
                     const float4v x = {dk[kb][i][4 * j], dk[kb][i][4 * j + 1], dk[kb][i][4 * j + 2], dk[kb][i][4 * j + 3]};
                     const float4v y = {dv[kb][i][4 * j], dv[kb][i][4 * j + 1], dv[kb][i][4 * j + 2], dv[kb][i][4 * j + 3]};
-                    *reinterpret_cast<float4v*>(at + 32 * i + 8 * j + 4 * h) = x * p.scale;
+                    *reinterpret_cast<float4v*>(at + 32 * i + 8 * j + 4 * h) = x * by;
                     *reinterpret_cast<float4v*>(at + p.splits * one + 32 * i + 8 * j + 4 * h) = y;
                 }
         }

@@ -240,10 +240,13 @@ hipError_t launch_kv_append(const KvAppendParams& p, hipStream_t st) {
 //           instructions' worth); the key a tile's row m stands for is
 //           16 (m / 4) + 4 tile + m % 4, which leaves lane group g with the
 //           scores of keys 16 g .. 16 g + 15: the keys of its value loads.
-//   output  O^T[channel][query] += V^T P^T with P as the sum of two bf16 values:
-//           16 bits of it count, and an fp32 result keeps them (one bf16 leaves
-//           2^-9 per weight).
-// e4m3 is exact in bf16; the scales multiply the scores and the weights in fp32.
+//   output  O^T[channel][query] += V^T P^T with P as the sum of two f16 values, the
+//           weights 2^15 times theirs: 22 bits of a weight count, down to 2^-39 of the
+//           largest, so that an fp32 result is one (with bf16, 8 bits each, the
+//           results were 1.3e-6 off).  A wave's values stand in units of the largest
+//           scale it has met.
+// e4m3 is exact in bf16 and f16; the scales multiply the scores and the weights in
+// fp32.
 namespace {
 
 constexpr int kDecWaves = 4;
@@ -263,6 +266,15 @@ __device__ __forceinline__ bf8v e4m3x8_to_bf16(uint32_t a, uint32_t b) {
     r[0] = x0[0]; r[1] = x0[1]; r[2] = x1[0]; r[3] = x1[1];
     r[4] = x2[0]; r[5] = x2[1]; r[6] = x3[0]; r[7] = x3[1];
     return r;
+}
+
+__device__ __forceinline__ half8 e4m3x8_to_f16(uint32_t a, uint32_t b) {
+    typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+    const half2v x0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, false);
+    const half2v x1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, true);
+    const half2v x2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, false);
+    const half2v x3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, true);
+    return half8{x0[0], x0[1], x1[0], x1[1], x2[0], x2[1], x3[0], x3[1]};
 }
 
 __device__ __forceinline__ void store_out(const AttnDecodeParams& p, size_t idx, float x) {
@@ -316,7 +328,7 @@ __global__ __launch_bounds__(64 * kDecWaves) void attn_decode_kernel(AttnDecodeP
     float4v o[VT];
 #pragma unroll
     for (int i = 0; i < VT; ++i) o[i] = float4v{0.f, 0.f, 0.f, 0.f};
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, l = 0.f, unit = 0.f;         // unit: the largest value scale so far
     const float to2 = p.scale * 1.4426950408889634f;
     const int krow = 16 * (col >> 2) + (col & 3);     // key of tile 0's row `col`
 
@@ -337,7 +349,7 @@ __global__ __launch_bounds__(64 * kDecWaves) void attn_decode_kernel(AttnDecodeP
 #pragma unroll
         for (int i = 0; i < VT; ++i)
             vv[i] = *reinterpret_cast<const uint4*>(vp + (size_t)(g * D + 16 * i + col) * 16);
-        const float ks = p.k_scale[ph] * to2, vs = p.v_scale[ph];
+        const float ks = p.k_scale[ph] * to2, vs = absent ? 0.f : p.v_scale[ph];
 
         float4v sc[4];
 #pragma unroll
@@ -378,30 +390,32 @@ __global__ __launch_bounds__(64 * kDecWaves) void attn_decode_kernel(AttnDecodeP
         top = fmaxf(top, __shfl_xor(top, 16, 64));
         top = max_across32(top);
         const float at = top == -INFINITY ? 0.f : top;
-        const float fade = __builtin_amdgcn_exp2f(m - at);           // 0 from -inf
+        float fade = __builtin_amdgcn_exp2f(m - at);  // 0 from -inf
         m = top;
         l *= fade;
+        if (vs > unit) { fade *= unit / vs; unit = vs; }
+        const float vr = unit > 0.f ? vs / unit : 0.f;
 #pragma unroll
         for (int i = 0; i < VT; ++i) o[i] *= fade;
-        bf8v hi8[2], lo8[2];
+        half8 hi8[2], lo8[2];
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                float x = __builtin_amdgcn_exp2f(sc[t][i] - at);
+                float x = __builtin_amdgcn_exp2f(sc[t][i] - at + 15.f);
                 l += x;
-                x *= vs;
-                const __bf16 a = (__bf16)x;
+                x *= vr;
+                const _Float16 a = (_Float16)x;
                 hi8[t >> 1][(t & 1) * 4 + i] = a;
-                lo8[t >> 1][(t & 1) * 4 + i] = (__bf16)(x - (float)a);
+                lo8[t >> 1][(t & 1) * 4 + i] = (_Float16)(x - (float)a);
             }
 #pragma unroll
         for (int i = 0; i < VT; ++i) {
-            const bf8v v0 = e4m3x8_to_bf16(vv[i].x, vv[i].y), v1 = e4m3x8_to_bf16(vv[i].z, vv[i].w);
-            o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, hi8[0], o[i], 0, 0, 0);
-            o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, hi8[1], o[i], 0, 0, 0);
-            o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, lo8[0], o[i], 0, 0, 0);
-            o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, lo8[1], o[i], 0, 0, 0);
+            const half8 v0 = e4m3x8_to_f16(vv[i].x, vv[i].y), v1 = e4m3x8_to_f16(vv[i].z, vv[i].w);
+            o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, hi8[0], o[i], 0, 0, 0);
+            o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, hi8[1], o[i], 0, 0, 0);
+            o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, lo8[0], o[i], 0, 0, 0);
+            o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, lo8[1], o[i], 0, 0, 0);
         }
     }
 
@@ -411,7 +425,7 @@ __global__ __launch_bounds__(64 * kDecWaves) void attn_decode_kernel(AttnDecodeP
     if (g == 0) { sm.ml[wave][col][0] = m; sm.ml[wave][col][1] = l; }
 #pragma unroll
     for (int i = 0; i < VT; ++i)
-        *reinterpret_cast<float4v*>(&sm.o[wave][col][16 * i + 4 * g]) = o[i];
+        *reinterpret_cast<float4v*>(&sm.o[wave][col][16 * i + 4 * g]) = o[i] * unit;
     __syncthreads();
     for (int idx = threadIdx.x; idx < nq * D; idx += 64 * kDecWaves) {
         const int c = idx / D, ch = idx % D;
@@ -437,28 +451,56 @@ __global__ __launch_bounds__(64 * kDecWaves) void attn_decode_kernel(AttnDecodeP
     }
 }
 
-// Joins the splits that have pages: one thread per channel, one workgroup of
-// 256 threads per 256 / D heads.
+// Joins the splits that have pages: one workgroup per head; its lanes read the
+// splits' maxima and sums side by side, then 1024 / D groups of them the outputs.
 template <int D>
 __global__ __launch_bounds__(256) void attn_decode_join(AttnDecodeParams p) {
-    const size_t head = (size_t)blockIdx.x * (256 / D) + threadIdx.x / D;
-    const int ch = threadIdx.x % D;
-    const size_t rows = (size_t)p.N * p.Hq;
-    if (head >= rows) return;
+    constexpr int GROUPS = 1024 / D;                  // D / 4 lanes each, four channels a lane
+    __shared__ float s_x[GROUPS][D], s_ml[8], s_sum;
+    const size_t head = blockIdx.x, rows = (size_t)p.N * p.Hq;
+    const int tid = threadIdx.x, gi = tid / (D / 4), ch = 4 * (tid % (D / 4));
     int lo, hi;
     decode_range(p, (int)(head / p.Hq), lo, hi);
     const int pages = (hi + kPage - 1) / kPage - lo / kPage;
     const int splits = max(1, (pages + p.split_pages - 1) / p.split_pages);
-    float top = -INFINITY;
-    for (int s = 0; s < splits; ++s) top = fmaxf(top, p.part_ml[(s * rows + head) * 2]);
-    const float at = top == -INFINITY ? 0.f : top;
-    float sum = 0.f, x = 0.f;
-    for (int s = 0; s < splits; ++s) {
-        const float f = __builtin_amdgcn_exp2f(p.part_ml[(s * rows + head) * 2] - at);
-        sum += p.part_ml[(s * rows + head) * 2 + 1] * f;
-        x += p.part_o[(s * rows + head) * D + ch] * f;
+    float top = -INFINITY, sum = 0.f;
+    for (int s = tid; s < splits; s += 256) {
+        const float2 ml = *reinterpret_cast<const float2*>(&p.part_ml[(s * rows + head) * 2]);
+        const float both = fmaxf(top, ml.x);
+        if (both != -INFINITY) sum = sum * __builtin_amdgcn_exp2f(top - both) + ml.y * __builtin_amdgcn_exp2f(ml.x - both);
+        else sum += ml.y;                             // 0, or NaN where every score is
+        top = both;
     }
-    store_out(p, head * D + ch, top == -INFINITY && !(x != x) ? 0.f : x / sum);
+    for (int o = 32; o > 0; o >>= 1) {
+        const float t2 = __shfl_xor(top, o, 64), s2 = __shfl_xor(sum, o, 64), both = fmaxf(top, t2);
+        sum = both == -INFINITY ? sum + s2
+                                : sum * __builtin_amdgcn_exp2f(top - both) + s2 * __builtin_amdgcn_exp2f(t2 - both);
+        top = both;
+    }
+    if ((tid & 63) == 0) { s_ml[2 * (tid >> 6)] = top; s_ml[2 * (tid >> 6) + 1] = sum; }
+    __syncthreads();
+    top = fmaxf(fmaxf(s_ml[0], s_ml[2]), fmaxf(s_ml[4], s_ml[6]));
+    const float at = top == -INFINITY ? 0.f : top;
+    if (tid == 0) {
+        float all = 0.f;
+        for (int w = 0; w < 4; ++w)
+            all += top == -INFINITY ? s_ml[2 * w + 1] : s_ml[2 * w + 1] * __builtin_amdgcn_exp2f(s_ml[2 * w] - at);
+        s_sum = all;
+    }
+    float4v x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int s = gi; s < splits; s += GROUPS) {
+        const float f = __builtin_amdgcn_exp2f(p.part_ml[(s * rows + head) * 2] - at);
+        x += *reinterpret_cast<const float4v*>(&p.part_o[(s * rows + head) * D + ch]) * f;
+    }
+    *reinterpret_cast<float4v*>(&s_x[gi][ch]) = x;
+    __syncthreads();
+    if (tid < D) {
+        float y = 0.f;
+#pragma unroll
+        for (int i = 0; i < GROUPS; ++i) y += s_x[i][tid];
+        store_out(p, head * D + tid, top == -INFINITY && !(y != y) ? 0.f : y / s_sum);
+    }
 }
 
 int attn_decode_splits(int N, int Hq, int Hkv, int max_pages, int window, int* split_pages) {
@@ -483,8 +525,7 @@ hipError_t launch_attn_decode(const AttnDecodeParams& p, hipStream_t st) {
     else hipLaunchKernelGGL((attn_decode_kernel<128>), grid, block, 0, st, p, groups);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
-    const int per = 256 / p.d;
-    dim3 jgrid((unsigned)(((long long)p.N * p.Hq + per - 1) / per));
+    dim3 jgrid((unsigned)((long long)p.N * p.Hq));
     if (p.d == 64) hipLaunchKernelGGL((attn_decode_join<64>), jgrid, block, 0, st, p);
     else hipLaunchKernelGGL((attn_decode_join<128>), jgrid, block, 0, st, p);
     return hipGetLastError();

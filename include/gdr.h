@@ -543,7 +543,7 @@ gdr_status gdr_kv_append(const void* k, const void* v, void* k_cache, void* v_ca
  *   workspace : device scratch of gdr_attn_decode_workspace_bytes() bytes (0:
  *        none needed, may be NULL), contents on entry ignored; calls that may
  *        overlap need one each
- * Scores, weights and sums are fp32 (the weights enter the product as two bf16
+ * Scores, weights and sums are fp32 (the weights enter the product as two f16
  * parts).  Flags: GDR_OUT_BF16.  Supported: d in {64, 128}.
  */
 size_t gdr_attn_decode_workspace_bytes(int N, int Hq, int Hkv, int d, int max_pages, int window);
