@@ -123,12 +123,13 @@ __global__ __launch_bounds__(64 * kQWaves, 2) void attn_dq_kernel(AttnParams p, 
     const Stager<D, kQN, kQWaves, true> loads(p.sk.t, wave, lane);
     const int j_first = begin / kQN * kQN;
     const int n = end > begin ? (end - j_first + kQN - 1) / kQN : 0;
+    const int last = p.cu_seqlens ? used - 1 : p.Tk - 1;   // of the keys that count
     uint64_t k_rows = loads.rows(kp, j_first), v_rows = loads.rows(vp, j_first);
     const uint64_t tile_bytes = (uint64_t)kQN * 2 * p.sk.t;
     const uint32_t k_lds = lds_address(sm.k[0]), v_lds = lds_address(sm.v[0]);
     if (n > 0) {
-        loads.load(k_rows, j_first, p.Tk - 1, k_lds, lane);
-        loads.load(v_rows, j_first, p.Tk - 1, v_lds, lane);
+        loads.load(k_rows, j_first, last, k_lds, lane);
+        loads.load(v_rows, j_first, last, v_lds, lane);
     }
     bf8v qf[KS], gf[KS];
     float delta = 0.f;
@@ -165,8 +166,8 @@ __global__ __launch_bounds__(64 * kQWaves, 2) void attn_dq_kernel(AttnParams p, 
         if (j0 + kQN < end) {
             k_rows += tile_bytes;
             v_rows += tile_bytes;
-            loads.load(k_rows, j0 + kQN, p.Tk - 1, k_lds + (BUF ^ 1) * kTile, lane);
-            loads.load(v_rows, j0 + kQN, p.Tk - 1, v_lds + (BUF ^ 1) * kTile, lane);
+            loads.load(k_rows, j0 + kQN, last, k_lds + (BUF ^ 1) * kTile, lane);
+            loads.load(v_rows, j0 + kQN, last, v_lds + (BUF ^ 1) * kTile, lane);
         }
         const bool edge = j0 < lo_most || j0 + kQN > hi_least;
         if (edge) {
@@ -237,19 +238,22 @@ __global__ __launch_bounds__(64 * kQWaves, 2) void attn_dq_kernel(AttnParams p, 
 
 namespace {
 
-constexpr int kKN = 128, kKM = 64, kKWaves = 4, kKB = 1;   // keys, queries a step, waves, 32-key blocks of a wave
+constexpr int kKN = 128, kKWaves = 4;                // keys of a workgroup, 32 a wave
 
-template <int D> constexpr int kKeyLds = D == 128 && kKB == 1 ? 3 : 0;
+// Queries a step.  At d = 128 the sums dk, dv (128 registers) and the keys' operands
+// (28 of 32) leave no room for the values' beside the work: those and the last of
+// the keys' stay in LDS, and the steps are half as long so that two workgroups
+// still fit a compute unit.
+template <int D> constexpr int kKM = D == 128 ? 32 : 64;
 
 template <int D>
 struct __attribute__((aligned(256))) DkvSmem {
-    uint16_t q[2][kKM * D];
-    uint16_t g[2][kKM * D];
-    float delta[2][kKM];
-    float lse2[2][kKM];
-    // key operands that do not fit the 256 registers beside the sums (d = 128): the
-    // last kKeyLds of a key's D / 16
-    uint4 key[kKWaves * kKB][kKeyLds<D> > 0 ? kKeyLds<D> : 1][64];
+    uint16_t q[2][kKM<D> * D];
+    uint16_t g[2][kKM<D> * D];
+    uint16_t v[kKN * D];
+    uint4 key[kKWaves][64];     // the last operand of each wave's keys
+    float delta[2][64];
+    float lse2[2][64];
     int4 range[kKN];            // of each key: first query, one past the last, whether alone
     int bound[kKN];
     int shared[3];
@@ -323,12 +327,24 @@ __global__ __launch_bounds__(64 * kKWaves, 2) void attn_dkv_kernel(AttnParams p,
         if (c0 >= used) return;
         rows = used;
     }
+    const uint16_t* kp = (const uint16_t*)p.k + b * p.sk.b + hk * p.sk.h;
+    const uint16_t* vp = (const uint16_t*)p.v + b * p.sk.b + hk * p.sk.h;
+    {
+        const Stager<D, kKN, kKWaves, false> loads(p.sk.t, wave, lane);
+        loads.load(loads.rows(vp, c0), c0, used - 1, lds_address(sm.v), lane);
+    }
+    bf8v kf[KS - 1];
+    {
+        const long long kr = (long long)min(c0 + 32 * wave + col, used - 1) * p.sk.t + 8 * h;
+#pragma unroll
+        for (int s = 0; s < KS - 1; ++s) kf[s] = __builtin_bit_cast(bf8v, *reinterpret_cast<const uint4*>(kp + kr + 16 * s));
+        sm.key[wave][lane] = *reinterpret_cast<const uint4*>(kp + kr + 16 * (KS - 1));
+    }
     // the queries that see key j: places j .. j + window - 1, inside its sequence;
     // kept in LDS, for the steps that need them lane by lane
-    int see_from = INT_MAX, see_to = 0, all_from = 0, all_to = INT_MAX;   // of the wave's keys: some row / every key
-#pragma unroll
-    for (int kb = 0; kb < kKB; ++kb) {
-        const int in = 32 * (kKB * wave + kb) + col, j = c0 + in;
+    int see_from, see_to, all_from, all_to;           // queries that see some key of the wave's / every one
+    {
+        const int in = 32 * wave + col, j = c0 + in;
         int lo = max(j - off, 0), hi = p.cu_seqlens ? min(sm.bound[in], rows) : rows;
         if (p.window > 0) hi = min(hi, j - off + p.window);
         if (j >= used || hi <= lo) { lo = 0; hi = 0; }
@@ -337,12 +353,12 @@ __global__ __launch_bounds__(64 * kKWaves, 2) void attn_dkv_kernel(AttnParams p,
         const bool first = j == 0 || (p.cu_seqlens && (in == 0 ? sm.shared[2] != 0 : sm.bound[in - 1] == j));
         const bool alone = p.window == 1 || (first && j >= off && hi - lo == 1);
         if (h == 0) sm.range[in] = make_int4(lo, hi, alone, 0);
-        if (hi > lo) see_from = min(see_from, lo);
-        see_to = max(see_to, hi);
-        all_from = max(all_from, hi > lo ? lo : INT_MAX);
-        all_to = min(all_to, hi);
+        see_from = hi > lo ? lo : INT_MAX;
+        see_to = hi;
+        all_from = hi > lo ? lo : INT_MAX;
+        all_to = hi;
     }
-    for (int x = 32; x > 0; x >>= 1) {
+    for (int x = 16; x > 0; x >>= 1) {
         see_from = min(see_from, __shfl_xor(see_from, x, 64));
         see_to = max(see_to, __shfl_xor(see_to, x, 64));
         all_from = max(all_from, __shfl_xor(all_from, x, 64));
@@ -362,36 +378,23 @@ __global__ __launch_bounds__(64 * kKWaves, 2) void attn_dkv_kernel(AttnParams p,
     }
     const int lo_most = c0 + kKN <= used ? max(last_key - off, 0) : rows;   // a tile with dead keys is never whole
 
-    const uint16_t* kp = (const uint16_t*)p.k + b * p.sk.b + hk * p.sk.h;
-    const uint16_t* vp = (const uint16_t*)p.v + b * p.sk.b + hk * p.sk.h;
-    constexpr int KR = KS - kKeyLds<D>;
-    bf8v kf[kKB][KR], vf[kKB][KS];
+    float16v dk[DB], dv[DB];
 #pragma unroll
-    for (int kb = 0; kb < kKB; ++kb) {
-        const long long kr = (long long)min(c0 + 32 * (kKB * wave + kb) + col, p.Tk - 1) * p.sk.t + 8 * h;
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            const uint4 u = *reinterpret_cast<const uint4*>(kp + kr + 16 * s);
-            if (s < KR) kf[kb][s < KR ? s : 0] = __builtin_bit_cast(bf8v, u);
-            else sm.key[kKB * wave + kb][s < KR ? 0 : s - KR][lane] = u;
-            vf[kb][s] = __builtin_bit_cast(bf8v, *reinterpret_cast<const uint4*>(vp + kr + 16 * s));
-        }
-    }
-    float16v dk[kKB][DB], dv[kKB][DB];
-#pragma unroll
-    for (int kb = 0; kb < kKB; ++kb)
-#pragma unroll
-        for (int i = 0; i < DB; ++i) { zero16(dk[kb][i]); zero16(dv[kb][i]); }
+    for (int i = 0; i < DB; ++i) { zero16(dk[i]); zero16(dv[i]); }
     const float to2 = p.scale * kLog2e;
 
+    constexpr int KM = kKM<D>, kTile = KM * D * 2;
+    constexpr int kG = offsetof(DkvSmem<D>, g) - offsetof(DkvSmem<D>, q);
     const ReadAt<D> at_lane(lane);
-    const Stager<D, kKM, kKWaves, false> loads(p.sq.t, wave, lane);
-    const int i_first = begin / kKM * kKM;
-    const int n = end > begin ? (end - i_first + kKM - 1) / kKM * heads : 0;
+    const uint32_t v_lds = lds_address(sm.v) + 32 * wave * D * 2;
+    const Stager<D, KM, kKWaves, false> loads(p.sq.t, wave, lane);
+    const int i_first = begin / KM * KM;
+    const int n = end > begin ? (end - i_first + KM - 1) / KM * heads : 0;
     const long long all = (long long)p.B * p.Hq * p.Tq;
-    const uint64_t step_bytes = (uint64_t)kKM * 2 * p.sq.t;
+    const uint64_t step_bytes = (uint64_t)KM * 2 * p.sq.t;
 
-    // the step whose loads go out next: queries next_i .. of head next_h
+    // the step whose loads go out next: queries next_i .. of head next_h; rows behind
+    // the last that counts are held at it, so that no step reads what nothing wrote
     int next_h = h0, next_i = i_first;
     uint64_t q_rows = 0, g_rows = 0, stats = 0;
     auto fetch = [&](int buf) {
@@ -400,192 +403,162 @@ __global__ __launch_bounds__(64 * kKWaves, 2) void attn_dkv_kernel(AttnParams p,
             g_rows = loads.rows((const uint16_t*)p.dO + b * p.sq.b + next_h * p.sq.h, i_first);
             stats = (uint64_t)(p.delta + (wave ? all : 0) + ((long long)b * p.Hq + next_h) * p.Tq + i_first);
         }
-        loads.load(q_rows, next_i, p.Tq - 1, lds_address(sm.q[0]) + buf * kKM * D * 2, lane);
-        loads.load(g_rows, next_i, p.Tq - 1, lds_address(sm.g[0]) + buf * kKM * D * 2, lane);
+        loads.load(q_rows, next_i, rows - 1, lds_address(sm.q[0]) + buf * kTile, lane);
+        loads.load(g_rows, next_i, rows - 1, lds_address(sm.g[0]) + buf * kTile, lane);
         if (wave < 2)
-            direct_load4(4 * min(lane, p.Tq - 1 - next_i), stats, lds_address(wave ? sm.lse2[0] : sm.delta[0]) + buf * kKM * 4);
+            direct_load4(4 * min(lane, rows - 1 - next_i), stats, lds_address(wave ? sm.lse2[0] : sm.delta[0]) + buf * 256);
         q_rows += step_bytes;
         g_rows += step_bytes;
-        stats += kKM * 4;
-        next_i += kKM;
+        stats += KM * 4;
+        next_i += KM;
         if (next_i >= end) { next_i = i_first; ++next_h; }
     };
     if (n > 0) fetch(0);
     bool bad = false;
-    int i0 = i_first - kKM;
+    int i0 = i_first - KM;
     for (int it = 0; it < n; ++it) {
         const int buf = it & 1;
-        i0 += kKM;
+        i0 += KM;
         if (i0 >= end) i0 = i_first;
         wait_loads();
         lds_barrier();
         if (it + 1 < n) fetch(buf ^ 1);
-        const uint16_t* qt = sm.q[buf];
-        const uint16_t* gt = sm.g[buf];
-        const bool inner = i0 >= lo_most && i0 + kKM <= hi_least;
-        if (!inner) {
-            bool mine = false;
-#pragma unroll
-            for (int i = 0; i < kKM / 16 / kKWaves; ++i) {
-                const int r = (kKM / kKWaves) * wave + 16 * i;
-                mine = mine || any_not_finite<D>(qt + r * D, lane) || any_not_finite<D>(gt + r * D, lane);
-            }
+        if (i0 < lo_most || i0 + KM > hi_least) {
+            constexpr int kMine = KM / kKWaves;
+            bool mine = any_not_finite<D, kMine>(sm.q[buf] + kMine * wave * D, lane) ||
+                        any_not_finite<D, kMine>(sm.g[buf] + kMine * wave * D, lane);
             // a masked pair's weight is 0, and so must be its product with dO v - D
             const float d = sm.delta[buf][lane], l2 = sm.lse2[buf][lane];
             mine = mine || __any(!(fabsf(d) < INFINITY) || !(l2 > -INFINITY));
             if (lane == 0) sm.bad[wave] = mine;
             lds_barrier();
-            bad = false;
-#pragma unroll
-            for (int w = 0; w < kKWaves; ++w) bad = bad || sm.bad[w] != 0;
+            bad = (sm.bad[0] | sm.bad[1] | sm.bad[2] | sm.bad[3]) != 0;
             if (bad) break;
         }
-        const ReadAt<D> at = at_lane.fresh(lds_address(qt));
-        constexpr int kG = offsetof(DkvSmem<D>, g) - offsetof(DkvSmem<D>, q);
+        const ReadAt<D> at = at_lane.fresh(lds_address(sm.q[0]) + buf * kTile);
+        uint32_t v_at = at_lane.row + v_lds;
+        asm volatile("" : "+v"(v_at));
 #pragma unroll
-        for (int ib = 0; ib < kKM / 32; ++ib) {
+        for (int ib = 0; ib < KM / 32; ++ib) {
             const int ir = i0 + 32 * ib;
             if (ir >= see_to || ir + 32 <= see_from) continue;
-            const bool whole = ir >= all_from && ir + 32 <= all_to;
-            // the weights, and dv from them
-            float16v st[kKB], dp[kKB];
-#pragma unroll
-            for (int kb = 0; kb < kKB; ++kb) zero16(st[kb]);
-#pragma unroll
-            for (int s = 0; s < KR; ++s) {
-                const bf8v a = at.row_frag(32 * ib, s);
-#pragma unroll
-                for (int kb = 0; kb < kKB; ++kb) st[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, kf[kb][s], st[kb], 0, 0, 0);
-            }
-            sched_reads_ahead<2, KR, 1, kKB>();
-            __builtin_amdgcn_sched_barrier(0);        // the registers are full: no reads for the next part yet
-            if constexpr (KR < KS) {
-#pragma unroll
-                for (int s = KR; s < KS; ++s) {
-                    const bf8v a = at.row_frag(32 * ib, s);
-#pragma unroll
-                    for (int kb = 0; kb < kKB; ++kb) {
-                        const bf8v k = __builtin_bit_cast(bf8v, sm.key[kKB * wave + kb][s - KR][lane_now()]);
-                        st[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, k, st[kb], 0, 0, 0);
-                    }
-                }
-                sched_reads_ahead<2, KS - KR, 1 + kKB, kKB>();
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            if (!whole) {
-#pragma unroll
-                for (int kb = 0; kb < kKB; ++kb) {
-                    const int here = lane_now();
-                    const int2 see = *reinterpret_cast<const int2*>(&sm.range[32 * (kKB * wave + kb) + (here & 31)]);
-                    const int from = ir + 4 * (here >> 5) - see.x;
-                    const unsigned seen = (unsigned)(see.y - see.x);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if ((unsigned)(from + 8 * (i / 4) + i % 4) >= seen) st[kb][i] = -INFINITY;
-                }
-            }
-            bf8v pf[kKB][2];
-            const float* lse_at = &sm.lse2[buf][32 * ib + 4 * (lane_now() >> 5)];
-#pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4) {
-                const float4v l4 = *reinterpret_cast<const float4v*>(lse_at + 8 * q4);
-#pragma unroll
-                for (int kb = 0; kb < kKB; ++kb)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) st[kb][4 * q4 + i] = __builtin_amdgcn_exp2f(st[kb][4 * q4 + i] * to2 - l4[i]);
-            }
-#pragma unroll
-            for (int kb = 0; kb < kKB; ++kb)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) pf[kb][i / 8][i % 8] = (__bf16)st[kb][i];
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int i = 0; i < DB; ++i) {
-                    const bf8v g = at.col_frag(32 * ib + 16 * s, i, kG);
-#pragma unroll
-                    for (int kb = 0; kb < kKB; ++kb) dv[kb][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(g, pf[kb][s], dv[kb][i], 0, 0, 0);
-                }
-            sched_reads_ahead<2, 2 * DB, 2, kKB>();
-            __builtin_amdgcn_sched_barrier(0);
-            // their gradients, and dk from them
-#pragma unroll
-            for (int kb = 0; kb < kKB; ++kb) zero16(dp[kb]);
+            // Four runs of products, the reads of each issued two products ahead (those of
+            // the next run's start as well), the vector work of one run between the
+            // products of the next.  The order is fixed step by step: left alone, the
+            // compiler reads right before each product and puts the vector work in one
+            // piece, and a wave's 32 products took 4,000 cycles instead of 1,024.
+            auto fixed = [] { __builtin_amdgcn_sched_barrier(0); };
+            auto v_frag = [&](int s) {
+                return __builtin_bit_cast(bf8v, *(const __attribute__((address_space(3))) uint4*)(uintptr_t)(v_at ^ (s << 5)));
+            };
+            auto g_col = [&](int t) { return at.col_frag(32 * ib + 16 * (t / DB), t % DB, kG); };
+            auto q_col = [&](int t) { return at.col_frag(32 * ib + 16 * (t / DB), t % DB); };
+            const int half = lane_now() >> 5;
+            const float* lse_at = &sm.lse2[buf][32 * ib + 4 * half];
+            const float* delta_at = &sm.delta[buf][32 * ib + 4 * half];
+
+            // scores
+            float16v st, dp;
+            zero16(st);
+            bf8v a[KS], g[KS], v[KS], c[2 * DB], e[2 * DB], k_last;
+            float4v l4[4], d4[4];
+            a[0] = at.row_frag(32 * ib, 0);
+            a[1] = at.row_frag(32 * ib, 1);
+            fixed();
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                const bf8v g = at.row_frag(32 * ib, s, kG);
-#pragma unroll
-                for (int kb = 0; kb < kKB; ++kb) dp[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(g, vf[kb][s], dp[kb], 0, 0, 0);
+                if (s + 2 < KS) a[s + 2] = at.row_frag(32 * ib, s + 2);
+                else { g[s + 2 - KS] = at.row_frag(32 * ib, s + 2 - KS, kG); v[s + 2 - KS] = v_frag(s + 2 - KS); }
+                if (s == KS - 3) k_last = __builtin_bit_cast(bf8v, sm.key[wave][lane_now()]);
+                if (s == KS - 1) l4[0] = *reinterpret_cast<const float4v*>(lse_at);
+                st = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[s], s < KS - 1 ? kf[s < KS - 1 ? s : 0] : k_last, st, 0, 0, 0);
+                fixed();
             }
-            sched_reads_ahead<2, KS, 1, kKB>();
-            __builtin_amdgcn_sched_barrier(0);
-            bf8v ds[kKB][2];
-            const float* delta_at = &sm.delta[buf][32 * ib + 4 * (lane_now() >> 5)];
+            if (ir < all_from || ir + 32 > all_to) {
+                const int here = lane_now();
+                const int2 see = *reinterpret_cast<const int2*>(&sm.range[32 * wave + (here & 31)]);
+                const int from = ir + 4 * (here >> 5) - see.x;
+                const unsigned seen = (unsigned)(see.y - see.x);
 #pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4) {
-                const float4v d4 = *reinterpret_cast<const float4v*>(delta_at + 8 * q4);
-#pragma unroll
-                for (int kb = 0; kb < kKB; ++kb)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) dp[kb][4 * q4 + i] = st[kb][4 * q4 + i] * (dp[kb][4 * q4 + i] - d4[i]);
+                for (int i = 0; i < 16; ++i)
+                    if ((unsigned)(from + 8 * (i / 4) + i % 4) >= seen) st[i] = -INFINITY;
             }
+            // dO v; beside it the weights
+            bf8v pf[2], ds[2];
+            zero16(dp);
+            fixed();
 #pragma unroll
-            for (int kb = 0; kb < kKB; ++kb)
+            for (int s = 0; s < KS; ++s) {
+                constexpr int PER = 16 / KS;          // weights a product
+                if (s + 2 < KS) { g[s + 2] = at.row_frag(32 * ib, s + 2, kG); v[s + 2] = v_frag(s + 2); }
+                else c[s + 2 - KS] = g_col(s + 2 - KS);
+                if ((s + 1) * PER % 4 == 0 && (s + 1) * PER < 16) l4[(s + 1) * PER / 4] = *reinterpret_cast<const float4v*>(lse_at + 2 * (s + 1) * PER);
+                if (s == KS - 1) d4[0] = *reinterpret_cast<const float4v*>(delta_at);
+                dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(g[s], v[s], dp, 0, 0, 0);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) ds[kb][i / 8][i % 8] = (__bf16)dp[kb][i];
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int i = 0; i < DB; ++i) {
-                    const bf8v a = at.col_frag(32 * ib + 16 * s, i);
-#pragma unroll
-                    for (int kb = 0; kb < kKB; ++kb) dk[kb][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, ds[kb][s], dk[kb][i], 0, 0, 0);
+                for (int i = s * PER; i < (s + 1) * PER; ++i) {
+                    st[i] = __builtin_amdgcn_exp2f(st[i] * to2 - l4[i / 4][i % 4]);
+                    pf[i / 8][i % 8] = (__bf16)st[i];
                 }
-            sched_reads_ahead<2, 2 * DB, 2, kKB>();
-            __builtin_amdgcn_sched_barrier(0);
+                fixed();
+            }
+            // dv; beside it the scores' gradients
+#pragma unroll
+            for (int t = 0; t < 2 * DB; ++t) {
+                constexpr int PER = 16 / (2 * DB);
+                if (t + 2 < 2 * DB) c[t + 2] = g_col(t + 2);
+                else e[t + 2 - 2 * DB] = q_col(t + 2 - 2 * DB);
+                if ((t + 1) * PER % 4 == 0 && (t + 1) * PER < 16) d4[(t + 1) * PER / 4] = *reinterpret_cast<const float4v*>(delta_at + 2 * (t + 1) * PER);
+                dv[t % DB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(c[t], pf[t / DB], dv[t % DB], 0, 0, 0);
+#pragma unroll
+                for (int i = t * PER; i < (t + 1) * PER; ++i) ds[i / 8][i % 8] = (__bf16)(st[i] * (dp[i] - d4[i / 4][i % 4]));
+                fixed();
+            }
+            // dk
+#pragma unroll
+            for (int t = 0; t < 2 * DB; ++t) {
+                if (t + 2 < 2 * DB) e[t + 2] = q_col(t + 2);
+                dk[t % DB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e[t], ds[t / DB], dk[t % DB], 0, 0, 0);
+                fixed();
+            }
         }
     }
     if (bad) {
         wait_loads();                                 // no load into LDS outlives the wave
-#pragma unroll
-        for (int kb = 0; kb < kKB; ++kb) {
-            const int4 see = sm.range[32 * (kKB * wave + kb) + col];
-            keys_one_by_one<D>(p, kp, vp, b, bh, hk, h0, heads, split, c0 + 32 * (kKB * wave + kb), used, see.x, see.y, see.z, lane);
-        }
+        const int4 see = sm.range[32 * wave + col];
+        keys_one_by_one<D>(p, kp, vp, b, bh, hk, h0, heads, split, c0 + 32 * wave, used, see.x, see.y, see.z, lane);
         return;
     }
+    wait_loads();
+    const int key = c0 + 32 * wave + col;
+    if (key >= used) return;
+    const int4 see = sm.range[32 * wave + col];
+    const float by = see.z ? 0.f : p.scale;
+    if (see.y <= see.x) {                             // no query sees it: 0, not its 0 * NaN
 #pragma unroll
-    for (int kb = 0; kb < kKB; ++kb) {
-        const int key = c0 + 32 * (kKB * wave + kb) + col;
-        if (key >= used) continue;
-        const int4 see = sm.range[key - c0];
-        const float by = see.z ? 0.f : p.scale;
-        if (see.y <= see.x) {                         // no query sees it: 0, not its 0 * NaN
+        for (int i = 0; i < DB; ++i) { zero16(dk[i]); zero16(dv[i]); }
+    }
+    if (p.splits == 1) {
+        const long long at = b * p.sk.b + hk * p.sk.h + (long long)key * p.sk.t;
 #pragma unroll
-            for (int i = 0; i < DB; ++i) { zero16(dk[kb][i]); zero16(dv[kb][i]); }
-        }
-        if (p.splits == 1) {
-            const long long at = b * p.sk.b + hk * p.sk.h + (long long)key * p.sk.t;
+        for (int i = 0; i < DB; ++i)
 #pragma unroll
-            for (int i = 0; i < DB; ++i)
+            for (int j = 0; j < 4; ++j) {
+                store4((uint16_t*)p.dk + at + 32 * i + 8 * j + 4 * h, dk[i], j, by);
+                store4((uint16_t*)p.dv + at + 32 * i + 8 * j + 4 * h, dv[i], j, 1.f);
+            }
+    } else {
+        const long long one = (long long)p.B * p.Hkv * p.Tk * D;
+        float* at = p.part + split * one + ((long long)bh * p.Tk + key) * D;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    store4((uint16_t*)p.dk + at + 32 * i + 8 * j + 4 * h, dk[kb][i], j, by);
-                    store4((uint16_t*)p.dv + at + 32 * i + 8 * j + 4 * h, dv[kb][i], j, 1.f);
-                }
-        } else {
-            const long long one = (long long)p.B * p.Hkv * p.Tk * D;
-            float* at = p.part + split * one + ((long long)bh * p.Tk + key) * D;
+        for (int i = 0; i < DB; ++i)
 #pragma unroll
-            for (int i = 0; i < DB; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float4v x = {dk[kb][i][4 * j], dk[kb][i][4 * j + 1], dk[kb][i][4 * j + 2], dk[kb][i][4 * j + 3]};
-                    const float4v y = {dv[kb][i][4 * j], dv[kb][i][4 * j + 1], dv[kb][i][4 * j + 2], dv[kb][i][4 * j + 3]};
-                    *reinterpret_cast<float4v*>(at + 32 * i + 8 * j + 4 * h) = x * by;
-                    *reinterpret_cast<float4v*>(at + p.splits * one + 32 * i + 8 * j + 4 * h) = y;
-                }
-        }
+            for (int j = 0; j < 4; ++j) {
+                const float4v x = {dk[i][4 * j], dk[i][4 * j + 1], dk[i][4 * j + 2], dk[i][4 * j + 3]};
+                const float4v y = {dv[i][4 * j], dv[i][4 * j + 1], dv[i][4 * j + 2], dv[i][4 * j + 3]};
+                *reinterpret_cast<float4v*>(at + 32 * i + 8 * j + 4 * h) = x * by;
+                *reinterpret_cast<float4v*>(at + p.splits * one + 32 * i + 8 * j + 4 * h) = y;
+            }
     }
 }
 

@@ -121,6 +121,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_kernel(AttnParams p, 
     const Stager<D, kBN, kWaves, true> loads(p.sk.t, wave, lane);
     const int j_first = begin / kBN * kBN;
     const int n = end > begin ? (end - j_first + kBN - 1) / kBN : 0;
+    const int last = p.cu_seqlens ? used - 1 : p.Tk - 1;   // of the keys that count
     uint64_t k_rows = loads.rows(kp, j_first), v_rows = loads.rows(vp, j_first);
     const uint64_t tile_bytes = (uint64_t)kBN * 2 * p.sk.t;
     const uint32_t k_lds = lds_address(sm.k[0]), v_lds = lds_address(sm.v[0]);
@@ -129,8 +130,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_kernel(AttnParams p, 
     bool bad = false;
     int j0 = j_first;
     if (n > 0) {
-        loads.load(k_rows, j0, p.Tk - 1, k_lds, lane);
-        loads.load(v_rows, j0, p.Tk - 1, v_lds, lane);
+        loads.load(k_rows, j0, last, k_lds, lane);
+        loads.load(v_rows, j0, last, v_lds, lane);
     }
     // one tile, in buffer BUF; false ends the walk
     auto tile_step = [&](auto buffer) {
@@ -141,8 +142,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_kernel(AttnParams p, 
         if (j0 + kBN < end) {
             k_rows += tile_bytes;
             v_rows += tile_bytes;
-            loads.load(k_rows, j0 + kBN, p.Tk - 1, k_lds + (BUF ^ 1) * kTile, lane);
-            loads.load(v_rows, j0 + kBN, p.Tk - 1, v_lds + (BUF ^ 1) * kTile, lane);
+            loads.load(k_rows, j0 + kBN, last, k_lds + (BUF ^ 1) * kTile, lane);
+            loads.load(v_rows, j0 + kBN, last, v_lds + (BUF ^ 1) * kTile, lane);
         }
         // tiles that some row of the workgroup sees in part: infinities and NaN among
         // values that are masked for a row must not reach it through 0 * inf

@@ -61,9 +61,6 @@ struct Stager {
     static constexpr int CH = D / 8, RPI = 64 / CH;  // chunks of a row, rows of one instruction
     static constexpr int N = ROWS / RPI / WAVES;
     static_assert(N * RPI * WAVES == ROWS, "rows split over the waves");
-    // the swizzle of a row is that of lane / CH xor that of the instruction's first
-    // row, and the latter depends on the instruction alone, not on the wave
-    static_assert(N * RPI % 16 == 0, "the swizzle repeats every 16 rows");
     int off[KEEP ? N : 1];
     uint32_t group;                                   // bytes between two instructions' first rows
     int skip;                                         // rows of the waves before this one
@@ -74,7 +71,8 @@ struct Stager {
         skip = wave * N * RPI;
         const int first = (int)(2 * (r * stride + 8 * ((lane % CH) ^ swz<D>(r))));
 #pragma unroll
-        for (int i = 0; i < (KEEP ? N : 1); ++i) off[i] = (first ^ (16 * swz<D>(i * RPI))) + (int)(i * group);
+        for (int i = 0; i < (KEEP ? N : 1); ++i)
+            off[i] = KEEP ? (first ^ flip(i)) + (int)(i * group) : first;
     }
     // Address of the wave's first row of the tile that starts at row `first`.
     __device__ __forceinline__ uint64_t rows(const uint16_t* src, int first) const {
@@ -91,9 +89,11 @@ struct Stager {
     }
 
 private:
+    // the swizzle of a row is that of lane / CH xor that of the instruction's first row
+    __device__ __forceinline__ int flip(int i) const { return 16 * swz<D>(skip + i * RPI); }
     template <int I> __device__ __forceinline__ void load_all(uint64_t rows, uint32_t to) const {
         if constexpr (KEEP) direct_load16<1024 * I>(off[I], rows, to);
-        else direct_load16<1024 * I>(off[0] ^ (16 * swz<D>(I * RPI)), rows + (uint64_t)I * group, to);
+        else direct_load16<1024 * I>(off[0] ^ flip(I), rows + (uint64_t)I * group, to);
         if constexpr (I + 1 < N) load_all<I + 1>(rows, to);
     }
     // the lane offset is unsigned: rows past the last are reached from the last one,
@@ -101,7 +101,7 @@ private:
     template <int I> __device__ __forceinline__ void load_held(uint64_t rows, int first, int last, uint32_t to, int lane) const {
         const int r = lane / CH, row = first + I * RPI + r, held = row < last ? row : last;
         const long long stride = group / RPI;         // bytes
-        const int c = (lane % CH) ^ swz<D>(I * RPI + r);
+        const int c = (lane % CH) ^ swz<D>(skip + I * RPI + r);
         // this lane's row relative to the tile's: at most ROWS rows before it or behind
         const uint64_t at = rows + (long long)(held - first) * stride + 16 * c;
         direct_load16_far<1024 * I>(at, to);
@@ -177,12 +177,12 @@ template <int D> struct ReadAt {
     }
 };
 
-// Whether any of 16 rows of a tile (rows 16 wave ..) holds an infinity or NaN.
-template <int D> __device__ __forceinline__ bool any_not_finite(const uint16_t* rows, int lane) {
+// Whether any of ROWS rows of a tile holds an infinity or NaN.
+template <int D, int ROWS = 16> __device__ __forceinline__ bool any_not_finite(const uint16_t* rows, int lane) {
     typedef unsigned short ushort2v __attribute__((ext_vector_type(2)));
     ushort2v top = {0, 0};
 #pragma unroll
-    for (int i = 0; i < 16 * D / 512; ++i) {
+    for (int i = 0; i < ROWS * D / 512; ++i) {
         const uint4 u = *reinterpret_cast<const uint4*>(rows + 512 * i + 8 * lane);
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
