@@ -64,7 +64,7 @@ bool attn_sizes_ok(int B, long long H, int T) {
 gdr_status attn_args(int B, int Hq, int Hkv, int Tq, int Tk, int d, int window, float scale, uint32_t flags) {
     if (flags & ~(GDR_ACT_F32 | GDR_TOKEN_MAJOR)) return GDR_ERR_INVALID_ARG;
     if (B < 1 || Hq < 1 || Hkv < 1 || Tq < 0 || Tk < 0 || window < 0) return GDR_ERR_INVALID_ARG;
-    if (Hq % Hkv != 0 || !(scale > 0.f) || !(scale - scale == 0.f)) return GDR_ERR_INVALID_ARG;
+    if (Hq % Hkv != 0 || !(scale >= 1e-30f) || !(scale - scale == 0.f)) return GDR_ERR_INVALID_ARG;
     // byte offsets inside a tile of 64 rows are signed 32-bit
     if (Hq > (1 << 16)) return GDR_ERR_INVALID_ARG;
     // places of queries and keys are signed 32-bit, with room for a tile behind the last
@@ -122,7 +122,7 @@ gdr_status decode_args(int N, int Hq, int Hkv, int d, int n_pages, int max_pages
                        uint32_t flags) {
     if (flags & ~GDR_OUT_BF16) return GDR_ERR_INVALID_ARG;
     if (N < 1 || Hq < 1 || Hkv < 1 || n_pages < 1 || max_pages < 1 || window < 0) return GDR_ERR_INVALID_ARG;
-    if (Hq % Hkv != 0 || !(scale > 0.f) || !(scale - scale == 0.f)) return GDR_ERR_INVALID_ARG;
+    if (Hq % Hkv != 0 || !(scale >= 1e-30f) || !(scale - scale == 0.f)) return GDR_ERR_INVALID_ARG;
     // (sequence, head) pairs and a sequence's tokens are numbered in 32 bits
     if ((long long)N * Hq > (1LL << 28) || max_pages > (1 << 24)) return GDR_ERR_INVALID_ARG;
     if (d != 64 && d != 128) return GDR_ERR_UNSUPPORTED;

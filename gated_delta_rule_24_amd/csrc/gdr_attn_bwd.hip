@@ -171,42 +171,94 @@ __global__ __launch_bounds__(64 * kQWaves, 2) void attn_dq_kernel(AttnParams p, 
         }
         const bool edge = j0 < lo_most || j0 + kQN > hi_least;
         if (edge) {
-            const bool mine = any_not_finite<D>(sm.k[BUF] + 16 * wave * D, lane);
+            // (a masked pair's weight is 0, and so must be its product with dO v - D)
+            const bool mine = any_not_finite<D>(sm.k[BUF] + 16 * wave * D, lane) || any_not_finite<D>(sm.v[BUF] + 16 * wave * D, lane);
             if (lane == 0) sm.bad[wave] = mine;
             lds_barrier();
             bad = (sm.bad[0] | sm.bad[1] | sm.bad[2] | sm.bad[3]) != 0;
             if (bad) return false;
         }
         if (!edge || __any(hi > j0 && lo < j0 + kQN)) {
+            // Six runs of eight products (d = 128) for the tile's two halves of 32 keys:
+            // scores, dO v, scores, dO v, and dq from both; the operands read kAhead
+            // products ahead (four 32-cycle products cover a read), the vector work of one
+            // run between the products of a later one (see the key-side kernel)
+            constexpr int kAhead = 4, kAll = 4 * KS + 4 * DB, PER = 16 / KS;
+            auto fixed = [] { __builtin_amdgcn_sched_barrier(0); };
+            bf8v f[kAll], ds[4];
+            auto read = [&](int u) {
+                const int run = u / KS, s = u % KS, t = u - 4 * KS;
+                if (run < 4) f[u] = kt.row_frag(32 * (run / 2), s, run % 2 ? kVal : kKey);
+                else f[u] = kt.col_frag(16 * (t / DB), t % DB, kKey);
+            };
+            float16v st[2], dp[2];
+            auto weights = [&](int half, int i) { st[half][i] = here(__builtin_amdgcn_exp2f(st[half][i] * to2 - lse2)); };
+            auto gradient = [&](int half, int i) {    // a pair at a time, packed
+                if (i % 2 == 0) return;
+                const float x = st[half][i - 1] * (dp[half][i - 1] - delta), y = st[half][i] * (dp[half][i] - delta);
+                const uint32_t u = here(pack_bf16(x, y));
+                const bf2v pair = __builtin_bit_cast(bf2v, u);
+                ds[2 * half + i / 8][i % 8 - 1] = pair[0];
+                ds[2 * half + i / 8][i % 8] = pair[1];
+            };
+            auto hide = [&](int half) {
+                const int base = j0 + 32 * half + 4 * h - lo;
+                const unsigned seen = (unsigned)(hi - lo);
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb) {
-                float16v st, dp;
-                zero16(st);
-                zero16(dp);
+                for (int i = 0; i < 16; ++i)
+                    if ((unsigned)(base + 8 * (i / 4) + i % 4) >= seen) st[half][i] = -INFINITY;
+            };
 #pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    st = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kt.row_frag(32 * kb, s, kKey), qf[s], st, 0, 0, 0);
-                    dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kt.row_frag(32 * kb, s, kVal), gf[s], dp, 0, 0, 0);
+            for (int u = 0; u < kAhead; ++u) read(u);
+            zero16(st[0]);
+            fixed();
+#pragma unroll
+            for (int u = 0; u < KS; ++u) {
+                read(u + kAhead);
+                st[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[u], qf[u], st[0], 0, 0, 0);
+                fixed();
+            }
+            if (edge) hide(0);
+            zero16(dp[0]);
+            fixed();
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {            // beside dO v, the weights
+                read(KS + s + kAhead);
+                dp[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[KS + s], gf[s], dp[0], 0, 0, 0);
+#pragma unroll
+                for (int i = s * PER; i < (s + 1) * PER; ++i) weights(0, i);
+                fixed();
+            }
+            zero16(st[1]);
+            fixed();
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {            // beside the second half's scores, the first's gradients
+                read(2 * KS + s + kAhead);
+                st[1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[2 * KS + s], qf[s], st[1], 0, 0, 0);
+#pragma unroll
+                for (int i = s * PER; i < (s + 1) * PER; ++i) gradient(0, i);
+                fixed();
+            }
+            if (edge) hide(1);
+            zero16(dp[1]);
+            fixed();
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                read(3 * KS + s + kAhead);
+                dp[1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[3 * KS + s], gf[s], dp[1], 0, 0, 0);
+#pragma unroll
+                for (int i = s * PER; i < (s + 1) * PER; ++i) weights(1, i);
+                fixed();
+            }
+#pragma unroll
+            for (int t = 0; t < 4 * DB; ++t) {        // beside dq, the second half's gradients
+                if (4 * KS + t + kAhead < kAll) read(4 * KS + t + kAhead);
+                dq[t % DB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[4 * KS + t], ds[t / DB], dq[t % DB], 0, 0, 0);
+                if (t < 2 * DB) {
+#pragma unroll
+                    for (int i = t * PER; i < (t + 1) * PER; ++i) gradient(1, i);
                 }
-                sched_reads_ahead<4, 2 * KS, 1>();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) st[i] = __builtin_amdgcn_exp2f(st[i] * to2 - lse2) * (dp[i] - delta);
-                if (edge) {
-                    const int base = j0 + 32 * kb + 4 * h - lo;
-                    const unsigned seen = (unsigned)(hi - lo);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if ((unsigned)(base + 8 * (i / 4) + i % 4) >= seen) st[i] = 0.f;
-                }
-                bf8v ds[2];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) ds[i / 8][i % 8] = (__bf16)st[i];
-#pragma unroll
-                for (int s = 0; s < 2; ++s)
-#pragma unroll
-                    for (int i = 0; i < DB; ++i)
-                        dq[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kt.col_frag(32 * kb + 16 * s, i, kKey), ds[s], dq[i], 0, 0, 0);
-                sched_reads_ahead<4, 2 * DB, 2>();
+                fixed();
             }
         }
         j0 += kQN;
@@ -442,11 +494,11 @@ __global__ __launch_bounds__(64 * kKWaves, 2) void attn_dkv_kernel(AttnParams p,
         for (int ib = 0; ib < KM / 32; ++ib) {
             const int ir = i0 + 32 * ib;
             if (ir >= see_to || ir + 32 <= see_from) continue;
-            // Four runs of products, the reads of each issued two products ahead (those of
-            // the next run's start as well), the vector work of one run between the
-            // products of the next.  The order is fixed step by step: left alone, the
+            // Four runs of products, the reads of each issued four products ahead (two in
+            // the second, where the registers end), the vector work of one run between
+            // the products of the next.  The order is fixed step by step: left alone, the
             // compiler reads right before each product and puts the vector work in one
-            // piece, and a wave's 32 products took 4,000 cycles instead of 1,024.
+            // piece, and a wave's 32 products of 32 cycles took about 4,000.
             auto fixed = [] { __builtin_amdgcn_sched_barrier(0); };
             auto v_frag = [&](int s) {
                 return __builtin_bit_cast(bf8v, *(const __attribute__((address_space(3))) uint4*)(uintptr_t)(v_at ^ (s << 5)));
@@ -462,14 +514,14 @@ __global__ __launch_bounds__(64 * kKWaves, 2) void attn_dkv_kernel(AttnParams p,
             zero16(st);
             bf8v a[KS], g[KS], v[KS], c[2 * DB], e[2 * DB], k_last;
             float4v l4[4], d4[4];
-            a[0] = at.row_frag(32 * ib, 0);
-            a[1] = at.row_frag(32 * ib, 1);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) a[s] = at.row_frag(32 * ib, s);
             fixed();
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                if (s + 2 < KS) a[s + 2] = at.row_frag(32 * ib, s + 2);
-                else { g[s + 2 - KS] = at.row_frag(32 * ib, s + 2 - KS, kG); v[s + 2 - KS] = v_frag(s + 2 - KS); }
-                if (s == KS - 3) k_last = __builtin_bit_cast(bf8v, sm.key[wave][lane_now()]);
+                if (s + 4 < KS) a[s + 4] = at.row_frag(32 * ib, s + 4);
+                if (s + 2 >= KS) { g[s + 2 - KS] = at.row_frag(32 * ib, s + 2 - KS, kG); v[s + 2 - KS] = v_frag(s + 2 - KS); }
+                if (s == (KS > 4 ? KS - 5 : 0)) k_last = __builtin_bit_cast(bf8v, sm.key[wave][lane_now()]);
                 if (s == KS - 1) l4[0] = *reinterpret_cast<const float4v*>(lse_at);
                 st = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[s], s < KS - 1 ? kf[s < KS - 1 ? s : 0] : k_last, st, 0, 0, 0);
                 fixed();
@@ -506,8 +558,12 @@ __global__ __launch_bounds__(64 * kKWaves, 2) void attn_dkv_kernel(AttnParams p,
 #pragma unroll
             for (int t = 0; t < 2 * DB; ++t) {
                 constexpr int PER = 16 / (2 * DB);
-                if (t + 2 < 2 * DB) c[t + 2] = g_col(t + 2);
-                else e[t + 2 - 2 * DB] = q_col(t + 2 - 2 * DB);
+                if (t == 0) {
+#pragma unroll
+                    for (int x = 2; x < 4 && x < 2 * DB; ++x) c[x] = g_col(x);
+                }
+                if (t + 4 < 2 * DB) c[t + 4] = g_col(t + 4);
+                else e[t + 4 - 2 * DB] = q_col(t + 4 - 2 * DB);
                 if ((t + 1) * PER % 4 == 0 && (t + 1) * PER < 16) d4[(t + 1) * PER / 4] = *reinterpret_cast<const float4v*>(delta_at + 2 * (t + 1) * PER);
                 dv[t % DB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(c[t], pf[t / DB], dv[t % DB], 0, 0, 0);
 #pragma unroll
@@ -517,7 +573,7 @@ __global__ __launch_bounds__(64 * kKWaves, 2) void attn_dkv_kernel(AttnParams p,
             // dk
 #pragma unroll
             for (int t = 0; t < 2 * DB; ++t) {
-                if (t + 2 < 2 * DB) e[t + 2] = q_col(t + 2);
+                if (t + 4 < 2 * DB) e[t + 4] = q_col(t + 4);
                 dk[t % DB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e[t], ds[t / DB], dk[t % DB], 0, 0, 0);
                 fixed();
             }

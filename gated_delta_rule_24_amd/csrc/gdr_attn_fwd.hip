@@ -76,6 +76,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_kernel(AttnParams p, 
     const int b = unit / p.Hq, hq = unit % p.Hq, hk = hq / (p.Hq / p.Hkv);
     const int r0 = tile * kBM;
 
+    const uint16_t* qp = (const uint16_t*)p.q + b * p.sq.b + hq * p.sq.h;
+    bf8v qf[KS];
+    {
+        const uint16_t* qr = qp + (long long)min(r0 + 32 * wave + col, p.Tq - 1) * p.sq.t + 8 * h;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) qf[s] = __builtin_bit_cast(bf8v, *reinterpret_cast<const uint4*>(qr + 16 * s));
+    }
     int used = p.Tq;
     if (p.cu_seqlens) {
         row_bounds<kBM, false>(p.cu_seqlens, p.nseq, p.Tq, r0, sm.bound, sm.shared, tid, 64 * kWaves, used);
@@ -98,16 +105,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_kernel(AttnParams p, 
     if (p.window > 0) lo_most = max(lo_most, last_row + p.Tk - p.Tq - p.window + 1);
     const int hi_least = r0 + p.Tk - p.Tq + 1;
 
-    const uint16_t* qp = (const uint16_t*)p.q + b * p.sq.b + hq * p.sq.h;
     const uint16_t* kp = (const uint16_t*)p.k + b * p.sk.b + hk * p.sk.h;
     const uint16_t* vp = (const uint16_t*)p.v + b * p.sk.b + hk * p.sk.h;
 
-    bf8v qf[KS];
-    {
-        const uint16_t* qr = qp + (long long)min(row, p.Tq - 1) * p.sq.t + 8 * h;
-#pragma unroll
-        for (int s = 0; s < KS; ++s) qf[s] = __builtin_bit_cast(bf8v, *reinterpret_cast<const uint4*>(qr + 16 * s));
-    }
     float16v o[DB];
 #pragma unroll
     for (int i = 0; i < DB; ++i)
@@ -125,7 +125,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_kernel(AttnParams p, 
     uint64_t k_rows = loads.rows(kp, j_first), v_rows = loads.rows(vp, j_first);
     const uint64_t tile_bytes = (uint64_t)kBN * 2 * p.sk.t;
     const uint32_t k_lds = lds_address(sm.k[0]), v_lds = lds_address(sm.v[0]);
-    const float ahead = 8.f / to2;
     float shift = 0.f;
     bool bad = false;
     int j0 = j_first;
@@ -184,7 +183,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_kernel(AttnParams p, 
             // m follows the maximum only when that is more than 2^8 ahead: weights up to
             // 2^8 keep their relative precision, and the sums their room, while some row
             // of 32 has a new maximum in most tiles (64 products to rescale o)
-            if (__any(top > m + ahead)) {
+            if (__any((top - m) * to2 > 8.f)) {
                 asm volatile("");                         // a branch, not 64 products and selects
                 top = fmaxf(top, m);
                 const float fade = m == top ? 1.f : __builtin_amdgcn_exp2f((m - top) * to2);

@@ -109,6 +109,13 @@ private:
     }
 };
 
+// Keeps the computation of x where it stands (the compiler would sink it past the
+// next branch, out from between the products).
+template <typename T> __device__ __forceinline__ T here(T x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
 // The lane's number, made anew where it is used: two instructions instead of a
 // register across the loop.
 __device__ __forceinline__ int lane_now() {
@@ -132,12 +139,14 @@ template <int AHEAD, int N, int R, int P = 1> __device__ __forceinline__ void sc
 
 // A lane's two read addresses inside a tile, from which every other one follows by
 // flipping address bits: the swizzle is an exclusive-or of the chunk, and tiles
-// start at multiples of 256 bytes.  fresh() hides them from the compiler once a
+// start at multiples of 256 bytes.  hidden() hides them from the compiler once a
 // step; otherwise it keeps all of them in registers across the loop (16 more than
 // the key-side gradient kernel has).
 template <int D> struct ReadAt {
     uint32_t row, col;
 
+    __device__ __forceinline__ ReadAt() {}
+    __device__ __forceinline__ void hidden() { asm volatile("" : "+v"(row), "+v"(col)); }
     __device__ __forceinline__ explicit ReadAt(int lane) {
         const int r = lane & 31, h = lane >> 5;
         row = 2 * (r * D + 8 * (h ^ swz<D>(r)));
@@ -154,7 +163,7 @@ template <int D> struct ReadAt {
     // the same, hidden
     __device__ __forceinline__ ReadAt fresh(uint32_t tile) const {
         ReadAt x = in(tile);
-        asm volatile("" : "+v"(x.row), "+v"(x.col));
+        x.hidden();
         return x;
     }
     // operand along d: row `r0` + (lane & 31), channels 16 s + 8 (lane / 32) .. + 7

@@ -453,7 +453,7 @@ gdr_status gdr_rope(const void* q, const void* k, void* q_out, void* k_out,
  *
  *   q, o : bf16 [B, Hq, Tq, d]      k, v : bf16 [B, Hkv, Tk, d]
  *   lse  : fp32 [B, Hq, Tq] in both layouts, written; NULL means not written
- *   window : 0 (none) or the number of keys; scale > 0, finite
+ *   window : 0 (none) or the number of keys; scale >= 1e-30, finite
  * Products run on bf16 MFMA with fp32 accumulation; the weights exp(s - m) are
  * rounded to bf16 for the product with v (m the running maximum), their sum is
  * kept in fp32.  Flags: GDR_TOKEN_MAJOR.  Supported: d in {64, 128};
