@@ -47,11 +47,11 @@ __device__ __forceinline__ int clampi(int x, int lo, int hi) { return x < lo ? l
 // append
 // ---------------------------------------------------------------------------
 //
-// One workgroup owns one (touched page, head): it reads the new tokens that fall
-// into the page (1 to 64), takes their largest magnitude, raises the scale if
+// Prompts: one workgroup owns one (touched page, head): it reads the new tokens that
+// fall into the page (1 to 64), takes their largest magnitude, raises the scale if
 // need be (then it re-rounds the page's older tokens), and writes the new ones.
-// Bound by HBM for prompts (2 bytes read, 1 written per value) and by latency
-// for one token.  The page's other slots are left as they were.
+// Bound by HBM: 2 bytes read, 1 written per value.  The page's other slots are left
+// as they were.
 template <int D>
 __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendParams p) {
     constexpr int VPT = D / 8;                        // 16-byte vectors of a token
@@ -62,14 +62,8 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendParams p) {
     const int tid = threadIdx.x, h = blockIdx.y;
 
     // which page: sequence, page of it, first new slot, new tokens, their first row
-    int seq = blockIdx.x, page_i, off, n, row;
-    if (p.cu_seqlens == nullptr) {
-        const int len = max(p.cache_len[seq], 0);
-        page_i = len / kPage;
-        off = len % kPage;
-        n = 1;
-        row = seq;
-    } else {
+    int seq, page_i, off, n, row;
+    {
         // item blockIdx.x of the sequences' touched pages in order: a running
         // sum over 256 sequences at a time
         if (tid == 0) s_work[0] = -1;
@@ -216,9 +210,92 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendParams p) {
     }
 }
 
+// One token of each sequence: 2 L lanes (L = D / 8) own one (sequence, head), L for
+// its keys and L for its values, 8 channels a lane, so that the call is one short
+// chain of reads (length, page, scale) beside the tokens' own: bound by latency.
+template <int D>
+__global__ __launch_bounds__(256) void kv_append_one_kernel(KvAppendParams p) {
+    constexpr int L = D / 8;
+    const long long item = (long long)blockIdx.x * (128 / L) + threadIdx.x / (2 * L);
+    const int c = threadIdx.x % L;
+    const bool value = (threadIdx.x / L) % 2 != 0;
+    if (item >= (long long)p.nseq * p.Hkv) return;
+    const int seq = (int)(item / p.Hkv), h = (int)(item % p.Hkv);
+    const uint4 x = *reinterpret_cast<const uint4*>((const uint16_t*)(value ? p.v : p.k) + (long long)seq * p.st +
+                                                    (long long)h * p.sh + 8 * c);
+    const int len = max(p.cache_len[seq], 0), page_i = len / kPage, off = len % kPage;
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    float top = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float a = fabsf(__uint_as_float(w[j] << 16)), b = fabsf(__uint_as_float(w[j] & 0xffff0000u));
+        if (a < INFINITY) top = fmaxf(top, a);
+        if (b < INFINITY) top = fmaxf(top, b);
+    }
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, L));
+    if (page_i >= p.max_pages) return;                // past the table: dropped
+    const int page = p.block_table[(size_t)seq * p.max_pages + page_i];
+    if ((unsigned)page >= (unsigned)p.n_pages) return;
+    const size_t ph = (size_t)page * p.Hkv + h;
+    uint8_t* dst = (value ? p.v_cache : p.k_cache) + ph * (kPage * D);
+    float* scale_at = (value ? p.v_scale : p.k_scale) + ph;
+    const float old = off > 0 ? *scale_at : 0.f;
+    const float s = fmaxf(old, exp2_int(scale_exponent(top))), inv = 1.f / s;
+    if (off > 0 && s != old) {
+        // the scale grew: the older tokens again, by this lane group alone, before the
+        // new one is written into the same 16 bytes
+        const float r = old * inv;
+        const int vecs = value ? 4 * D : off * (D / 16);
+        for (int vec = c; vec < vecs; vec += L) {
+            const int first = 16 * (vec / D);
+            if (value && first >= off) break;         // later groups of 16 tokens hold none
+            uint4* at = reinterpret_cast<uint4*>(dst + (size_t)vec * 16);
+            const uint4 y = *at;
+            uint32_t u[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t again = rescale_e4m3x4(u[j], r);
+                uint32_t m = 0xffffffffu;
+                if (value) {                          // slots from `off` on stay
+                    m = 0;
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+                        if (first + 4 * j + b < off) m |= 0xffu << (8 * b);
+                }
+                u[j] = (u[j] & ~m) | (again & m);
+            }
+            *at = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+        __threadfence();
+    }
+    if (c == 0) *scale_at = s;
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        f[2 * j] = __uint_as_float(w[j] << 16) * inv;
+        f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u) * inv;
+    }
+    const uint2 y = make_uint2(to_e4m3x4(f[0], f[1], f[2], f[3]), to_e4m3x4(f[4], f[5], f[6], f[7]));
+    if (!value) {
+        *reinterpret_cast<uint2*>(dst + off * D + 8 * c) = y;
+    } else {
+        uint8_t* at = dst + ((off / 16) * D + 8 * c) * 16 + off % 16;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) at[16 * j] = (uint8_t)((j < 4 ? y.x : y.y) >> (8 * (j % 4)));
+    }
+}
+
 hipError_t launch_kv_append(const KvAppendParams& p, hipStream_t st) {
+    if (!p.cu_seqlens) {
+        const long long pairs = (long long)p.nseq * p.Hkv, per = 1024 / p.d;
+        dim3 grid((unsigned)((pairs + per - 1) / per)), block(256);
+        if (p.d == 64) hipLaunchKernelGGL((kv_append_one_kernel<64>), grid, block, 0, st, p);
+        else hipLaunchKernelGGL((kv_append_one_kernel<128>), grid, block, 0, st, p);
+        return hipGetLastError();
+    }
     // a sequence's m new tokens touch at most m / 64 + 2 pages
-    const long long items = p.cu_seqlens ? (long long)p.T / kPage + 2LL * p.nseq : p.nseq;
+    const long long items = (long long)p.T / kPage + 2LL * p.nseq;
     dim3 grid((unsigned)items, (unsigned)p.Hkv), block(256);
     if (p.d == 64) hipLaunchKernelGGL((kv_append_kernel<64>), grid, block, 0, st, p);
     else hipLaunchKernelGGL((kv_append_kernel<128>), grid, block, 0, st, p);
