@@ -2,11 +2,13 @@
 // from the forward's log-sum-exps:
 //   P_ij = exp(scale q_i.k_j - lse_i),  D_i = dO_i.o_i,  dS_ij = P_ij (dO_i.v_j - D_i)
 //   dq_i = scale sum_j dS_ij k_j;  dk_j = scale sum_i dS_ij q_i;  dv_j = sum_i P_ij dO_i
-// Two kernels, each the owner of what it sums, so that no atomics are needed and
-// the result does not depend on the order of workgroups: the query-side one walks
-// the keys of its queries (three products), the key-side one the queries of its
-// keys and of every head that shares them (four products).  That recomputes the
-// scores and dO v once more than a single kernel would: seven products for five.
+// Two kinds of workgroups, each the owner of what it sums, so that no atomics are
+// needed and the result does not depend on their order: the query side walks the
+// keys of its queries (three products), the key side the queries of its keys and of
+// every head that shares them (four products).  That recomputes the scores and dO v
+// once more than a single walk would: seven products for five.  Both kinds run in
+// one kernel, the key side's first, after a small one that forms D: one tail
+// instead of two, and short calls fill the chip with both.
 #include <limits.h>
 
 #include <type_traits>
@@ -32,8 +34,33 @@ __device__ __forceinline__ void store4(uint16_t* at, const float16v& x, int j, f
 
 }  // namespace
 
+// D and the base-2 log-sum-exps of every query row: D / 8 lanes a row.  A row that
+// saw nothing has lse -inf: +inf makes its weights exp2(-inf) = 0.
+template <int D>
+__global__ __launch_bounds__(256) void attn_delta_kernel(AttnParams p) {
+    constexpr int L = D / 8;
+    const long long row = (long long)blockIdx.x * (256 / L) + threadIdx.x / L, all = (long long)p.B * p.Hq * p.Tq;
+    if (row >= all) return;
+    const int c = threadIdx.x % L;
+    const long long bh = row / p.Tq;
+    const int t = (int)(row % p.Tq), b = (int)(bh / p.Hq), hq = (int)(bh % p.Hq);
+    const long long at = b * p.sq.b + hq * p.sq.h + t * p.sq.t + 8 * c;
+    const bf8v x = __builtin_bit_cast(bf8v, *reinterpret_cast<const uint4*>((const uint16_t*)p.o + at));
+    const bf8v y = __builtin_bit_cast(bf8v, *reinterpret_cast<const uint4*>((const uint16_t*)p.dO + at));
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += (float)x[j] * (float)y[j];
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) sum += __shfl_xor(sum, o, L);
+    if (c == 0) {
+        const float lse = p.lse[row];
+        p.delta[row] = lse == -INFINITY ? 0.f : sum;
+        p.delta[all + row] = lse == -INFINITY ? INFINITY : lse * kLog2e;
+    }
+}
+
 // ---------------------------------------------------------------------------
-// query side: dq, and D and the base-2 log-sum-exps for the key side
+// query side: dq
 // ---------------------------------------------------------------------------
 
 namespace {
@@ -80,15 +107,14 @@ __device__ __forceinline__ void queries_one_by_one(const AttnParams& p, long lon
 }  // namespace
 
 template <int D>
-__global__ __launch_bounds__(64 * kQWaves, 2) void attn_dq_kernel(AttnParams p, int tiles) {
+__device__ __forceinline__ void query_side(const AttnParams& p, int item, int tiles, char* smem) {
     constexpr int KS = D / 16, DB = D / 32;
-    extern __shared__ __attribute__((aligned(256))) char smem[];
     DqSmem<D>& sm = *reinterpret_cast<DqSmem<D>*>(smem);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 31, h = lane >> 5;
 
     int unit, tile;
-    work_item(blockIdx.x, p.B * p.Hq, tiles, unit, tile);
+    work_item(item, p.B * p.Hq, tiles, unit, tile);
     tile = tiles - 1 - tile;
     const int b = unit / p.Hq, hq = unit % p.Hq, hk = hq / (p.Hq / p.Hkv);
     const int r0 = tile * kQM, off = p.Tk - p.Tq;
@@ -132,23 +158,12 @@ __global__ __launch_bounds__(64 * kQWaves, 2) void attn_dq_kernel(AttnParams p, 
         loads.load(v_rows, j_first, last, v_lds, lane);
     }
     bf8v qf[KS], gf[KS];
-    float delta = 0.f;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
         qf[s] = __builtin_bit_cast(bf8v, *reinterpret_cast<const uint4*>((const uint16_t*)p.q + qrow + 16 * s + 8 * h));
         gf[s] = __builtin_bit_cast(bf8v, *reinterpret_cast<const uint4*>((const uint16_t*)p.dO + qrow + 16 * s + 8 * h));
-        const bf8v of = __builtin_bit_cast(bf8v, *reinterpret_cast<const uint4*>((const uint16_t*)p.o + qrow + 16 * s + 8 * h));
-#pragma unroll
-        for (int j = 0; j < 8; ++j) delta += (float)gf[s][j] * (float)of[j];
     }
-    delta = sum_across32(delta);
-    // a row that saw nothing has lse -inf: +inf makes its weights exp2(-inf) = 0
-    const bool sees_any = hi > lo;
-    const float lse2 = sees_any ? p.lse[stat] * kLog2e : INFINITY;
-    if (live && h == 0) {
-        p.delta[stat] = sees_any ? delta : 0.f;
-        p.delta[(long long)p.B * p.Hq * p.Tq + stat] = lse2;
-    }
+    const float delta = p.delta[stat], lse2 = p.delta[(long long)p.B * p.Hq * p.Tq + stat];
 
     float16v dq[DB];
 #pragma unroll
@@ -360,15 +375,14 @@ __device__ __forceinline__ void keys_one_by_one(const AttnParams& p, const uint1
 }  // namespace
 
 template <int D>
-__global__ __launch_bounds__(64 * kKWaves, 2) void attn_dkv_kernel(AttnParams p, int tiles) {
+__device__ __forceinline__ void key_side(const AttnParams& p, int item, int tiles, char* smem) {
     constexpr int KS = D / 16, DB = D / 32;
-    extern __shared__ __attribute__((aligned(256))) char smem[];
     DkvSmem<D>& sm = *reinterpret_cast<DkvSmem<D>*>(smem);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 31, h = lane >> 5;
 
     int unit, tile;
-    work_item(blockIdx.x, p.B * p.Hkv * p.splits, tiles, unit, tile);
+    work_item(item, p.B * p.Hkv * p.splits, tiles, unit, tile);
     const int split = unit % p.splits, bh = unit / p.splits, b = bh / p.Hkv, hk = bh % p.Hkv;
     const int heads = p.Hq / p.Hkv / p.splits, h0 = hk * (p.Hq / p.Hkv) + split * heads;
     const int c0 = tile * kKN, off = p.Tk - p.Tq;
@@ -618,6 +632,16 @@ __global__ __launch_bounds__(64 * kKWaves, 2) void attn_dkv_kernel(AttnParams p,
     }
 }
 
+static_assert(kQWaves == kKWaves, "one kernel");
+
+template <int D>
+__global__ __launch_bounds__(64 * kQWaves, 2) void attn_bwd_kernel(AttnParams p, int key_items, int key_tiles, int query_tiles) {
+    extern __shared__ __attribute__((aligned(256))) char smem[];
+    const int item = blockIdx.x;
+    if (item < key_items) key_side<D>(p, item, key_tiles, smem);
+    else query_side<D>(p, item - key_items, query_tiles, smem);
+}
+
 // Sums the splits' partial dk and dv in their order; 8 channels a thread.
 template <int D>
 __global__ __launch_bounds__(256) void attn_dkv_sum(AttnParams p) {
@@ -655,25 +679,25 @@ int attn_bwd_splits(int B, int Hq, int Hkv, int Tk) {
 
 template <int D>
 static hipError_t launch_bwd_d(const AttnParams& p, hipStream_t st) {
-    static std::atomic<unsigned long long> done_q{0}, done_k{0};
-    hipError_t e = ensure_dyn_lds(reinterpret_cast<const void*>(&attn_dq_kernel<D>), (int)sizeof(DqSmem<D>), done_q);
+    static std::atomic<unsigned long long> done{0};
+    constexpr size_t kLds = sizeof(DqSmem<D>) > sizeof(DkvSmem<D>) ? sizeof(DqSmem<D>) : sizeof(DkvSmem<D>);
+    hipError_t e = ensure_dyn_lds(reinterpret_cast<const void*>(&attn_bwd_kernel<D>), (int)kLds, done);
     if (e != hipSuccess) return e;
-    e = ensure_dyn_lds(reinterpret_cast<const void*>(&attn_dkv_kernel<D>), (int)sizeof(DkvSmem<D>), done_k);
-    if (e != hipSuccess) return e;
-    const int qt = (p.Tq + kQM - 1) / kQM, kt = (p.Tk + kKN - 1) / kKN;
-    if (qt > 0) {
-        hipLaunchKernelGGL((attn_dq_kernel<D>), dim3((unsigned)((long long)p.B * p.Hq * qt)), dim3(64 * kQWaves),
-                           sizeof(DqSmem<D>), st, p, qt);
+    const long long rows = (long long)p.B * p.Hq * p.Tq, per = 2048 / D;
+    if (rows > 0) {
+        hipLaunchKernelGGL((attn_delta_kernel<D>), dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, st, p);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    if (kt == 0) return hipSuccess;
-    hipLaunchKernelGGL((attn_dkv_kernel<D>), dim3((unsigned)((long long)p.B * p.Hkv * p.splits * kt)), dim3(64 * kKWaves),
-                       sizeof(DkvSmem<D>), st, p, kt);
+    const int query_tiles = (p.Tq + kQM - 1) / kQM, key_tiles = (p.Tk + kKN - 1) / kKN;
+    const long long key_items = (long long)p.B * p.Hkv * p.splits * key_tiles, items = key_items + (long long)p.B * p.Hq * query_tiles;
+    if (items == 0) return hipSuccess;
+    hipLaunchKernelGGL((attn_bwd_kernel<D>), dim3((unsigned)items), dim3(64 * kQWaves), kLds, st, p, (int)key_items, key_tiles,
+                       query_tiles);
     e = hipGetLastError();
-    if (e != hipSuccess || p.splits == 1) return e;
-    const long long items = (long long)p.B * p.Hkv * p.Tk * D / 8;
-    hipLaunchKernelGGL((attn_dkv_sum<D>), dim3((unsigned)((items + 255) / 256)), dim3(256), 0, st, p);
+    if (e != hipSuccess || p.splits == 1 || key_tiles == 0) return e;
+    const long long sums = (long long)p.B * p.Hkv * p.Tk * D / 8;
+    hipLaunchKernelGGL((attn_dkv_sum<D>), dim3((unsigned)((sums + 255) / 256)), dim3(256), 0, st, p);
     return hipGetLastError();
 }
 
