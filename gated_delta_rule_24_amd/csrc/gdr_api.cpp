@@ -112,7 +112,7 @@ gdr_status attn_bwd_run(const void* q, const void* k, const void* v, const void*
     p.dO = dO; p.dq = dq; p.dk = dk; p.dv = dv;
     p.cu_seqlens = cu_seqlens; p.nseq = nseq;
     p.delta = static_cast<float*>(workspace);
-    p.splits = gdr::attn_bwd_splits(B, Hq, Hkv, Tk);
+    p.splits = gdr::attn_bwd_splits(B, Hq, Hkv, Tq, Tk);
     if (p.splits > 1)
         p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + attn_delta_bytes(B, Hq, Tq));
     return from_hip(gdr::launch_attn_bwd(p, (hipStream_t)stream));
@@ -525,7 +525,7 @@ gdr_status gdr_attn_fwd_varlen(const void* q, const void* k, const void* v, void
 
 size_t gdr_attn_bwd_workspace_bytes(int B, int Hq, int Hkv, int Tq, int Tk, int d) {
     if (attn_args(B, Hq, Hkv, Tq, Tk, d, 0, 1.f, 0) != GDR_OK) return 0;
-    const int splits = gdr::attn_bwd_splits(B, Hq, Hkv, Tk);
+    const int splits = gdr::attn_bwd_splits(B, Hq, Hkv, Tq, Tk);
     const size_t part = splits > 1 ? 2 * (size_t)splits * B * Hkv * Tk * d * sizeof(float) : 0;
     return attn_delta_bytes(B, Hq, Tq) + part;
 }
@@ -560,8 +560,9 @@ gdr_status gdr_kv_append(const void* k, const void* v, void* k_cache, void* v_ca
     if (nseq < 1 || Hkv < 1 || T < 0 || n_pages < 1 || max_pages < 1) return GDR_ERR_INVALID_ARG;
     if (!cu_seqlens && T != nseq) return GDR_ERR_INVALID_ARG;
     if (d != 64 && d != 128) return GDR_ERR_UNSUPPORTED;
-    // pages of one call are numbered in 32 bits, heads on the grid's second axis
-    if (Hkv > 65535 || (long long)nseq * ((long long)T / 64 + 2) > (1LL << 31) - 1) return GDR_ERR_INVALID_ARG;
+    // pages and (sequence, head) pairs of one call are numbered in 32 bits, heads on the
+    // grid's second axis
+    if (Hkv > 65535 || T > (1 << 30) || (long long)nseq * Hkv > (1LL << 31) - 1 || (long long)nseq * ((long long)T / 64 + 2) > (1LL << 31) - 1) return GDR_ERR_INVALID_ARG;
     if ((long long)nseq * max_pages > (1LL << 40)) return GDR_ERR_INVALID_ARG;
     if (T > 0 && (!k || !v)) return GDR_ERR_INVALID_ARG;
     if (!k_cache || !v_cache || !k_scale || !v_scale || !block_table || !cache_len) return GDR_ERR_INVALID_ARG;

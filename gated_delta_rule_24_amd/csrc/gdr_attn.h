@@ -43,19 +43,19 @@ struct AttnParams {
     void* dk;
     void* dv;
     float* delta;               // [B, Hq, Tq]: rowsum(dO o)
-    float* part;                // backward: fp32 partial dk, dv of the head splits, or null
+    float* part;                // backward: fp32 partial dk, dv of the splits, or null
     const int* cu_seqlens;      // packed sequences, or null
     int nseq;
     int B, Hq, Hkv, Tq, Tk, d;
     int window;                 // 0: none
-    int splits;                 // backward: workgroups a shared head's query heads are dealt to
+    int splits;                 // backward: workgroups a key tile's queries (of every head that shares it) are dealt to
     float scale;
     AttnStrides sq, sk;         // queries' tensors (q, o, dO, dq); keys' tensors (k, v, dk, dv)
 };
 hipError_t launch_attn_fwd(const AttnParams& p, hipStream_t st);
 hipError_t launch_attn_bwd(const AttnParams& p, hipStream_t st);
-// Query-head splits of the key-side gradient kernel (1: no partials).
-int attn_bwd_splits(int B, int Hq, int Hkv, int Tk);
+// Splits of the key side's queries (1: no partials).
+int attn_bwd_splits(int B, int Hq, int Hkv, int Tq, int Tk);
 
 struct KvAppendParams {
     const void* k;
@@ -82,7 +82,7 @@ struct AttnDecodeParams {
     const int* cache_len;
     void* o;
     float* part_o;              // [splits, N, Hq, d] unnormalised, or null when splits == 1
-    float* part_ml;             // [splits, N, Hq, 2]: running maximum (base 2) and sum (2^15 times)
+    float* part_ml;             // [splits, N, Hq, 2]: running maximum (base 2) and sum
     int N, Hq, Hkv, d, n_pages, max_pages, window;
     int splits, split_pages;    // pages of a split: split s of a sequence is its s-th run of them
     float scale;

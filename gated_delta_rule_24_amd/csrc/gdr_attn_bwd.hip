@@ -333,8 +333,8 @@ static_assert(sizeof(DkvSmem<128>) <= 80 * 1024 && sizeof(DkvSmem<64>) <= 80 * 1
 // queries.
 template <int D>
 __device__ __forceinline__ void keys_one_by_one(const AttnParams& p, const uint16_t* k, const uint16_t* v, int b, int bh, int hk,
-                                                int h0, int heads, int split, int first, int used, int lo32, int hi32,
-                                                int alone32, int lane) {
+                                                int h0, int split, int first, int used, int i_first, int step, int per, int from,
+                                                int to, int lo32, int hi32, int alone32, int lane) {
     const float to2 = p.scale * kLog2e;
     const long long all = (long long)p.B * p.Hq * p.Tq, one = (long long)p.B * p.Hkv * p.Tk * D;
     for (int r = 0; r < 32 && first + r < used; ++r) {
@@ -342,19 +342,21 @@ __device__ __forceinline__ void keys_one_by_one(const AttnParams& p, const uint1
         const float by = __builtin_amdgcn_readlane(alone32, r) ? 0.f : p.scale;
         const long long j = (long long)(first + r) * p.sk.t;
         float dk[D / 64] = {}, dv[D / 64] = {};
-        for (int hq = h0; hq < h0 + heads; ++hq) {
+        for (int s = from; s < to; s += per - s % per) {          // the split's steps of one head
+            const int hq = h0 + s / per, begin = i_first + s % per * step;
+            const int i_lo = max(lo, begin), i_hi = min(hi, begin + min(to - s, per - s % per) * step);
             const long long head = b * p.sq.b + hq * p.sq.h, stat = ((long long)b * p.Hq + hq) * p.Tq;
             const uint16_t* q = (const uint16_t*)p.q + head;
             const uint16_t* g = (const uint16_t*)p.dO + head;
-            for (int i0 = lo; i0 < hi; i0 += 64) {
+            for (int i0 = i_lo; i0 < i_hi; i0 += 64) {
                 float x = 0.f, y = 0.f;
-                if (i0 + lane < hi) {
+                if (i0 + lane < i_hi) {
                     const long long i = (long long)(i0 + lane) * p.sq.t;
                     x = __builtin_amdgcn_exp2f(dot_row<D>(q + i, k + j) * to2 - p.delta[all + stat + i0 + lane]);
                     y = x * (dot_row<D>(g + i, v + j) - p.delta[stat + i0 + lane]);
                 }
-                add_rows<D>(dv, x, g + (long long)i0 * p.sq.t, p.sq.t, min(64, hi - i0), lane);
-                add_rows<D>(dk, y, q + (long long)i0 * p.sq.t, p.sq.t, min(64, hi - i0), lane);
+                add_rows<D>(dv, x, g + (long long)i0 * p.sq.t, p.sq.t, min(64, i_hi - i0), lane);
+                add_rows<D>(dk, y, q + (long long)i0 * p.sq.t, p.sq.t, min(64, i_hi - i0), lane);
             }
         }
 #pragma unroll
@@ -384,7 +386,7 @@ __device__ __forceinline__ void key_side(const AttnParams& p, int item, int tile
     int unit, tile;
     work_item(item, p.B * p.Hkv * p.splits, tiles, unit, tile);
     const int split = unit % p.splits, bh = unit / p.splits, b = bh / p.Hkv, hk = bh % p.Hkv;
-    const int heads = p.Hq / p.Hkv / p.splits, h0 = hk * (p.Hq / p.Hkv) + split * heads;
+    const int heads = p.Hq / p.Hkv, h0 = hk * heads;
     const int c0 = tile * kKN, off = p.Tk - p.Tq;
 
     int used = p.Tk, rows = p.Tq;
@@ -455,19 +457,23 @@ __device__ __forceinline__ void key_side(const AttnParams& p, int item, int tile
     const uint32_t v_lds = lds_address(sm.v) + 32 * wave * D * 2;
     const Stager<D, KM, kKWaves, false> loads(p.sq.t, wave, lane);
     const int i_first = begin / KM * KM;
-    const int n = end > begin ? (end - i_first + KM - 1) / KM * heads : 0;
+    // steps of the heads that share the keys, one head after the other; this split's
+    const int per = end > begin ? (end - i_first + KM - 1) / KM : 0;
+    const int from = (int)((long long)per * heads * split / p.splits), to = (int)((long long)per * heads * (split + 1) / p.splits);
+    const int n = to - from;
     const long long all = (long long)p.B * p.Hq * p.Tq;
     const uint64_t step_bytes = (uint64_t)KM * 2 * p.sq.t;
 
     // the step whose loads go out next: queries next_i .. of head next_h; rows behind
     // the last that counts are held at it, so that no step reads what nothing wrote
-    int next_h = h0, next_i = i_first;
+    const int i_start = n > 0 ? i_first + from % per * KM : 0;
+    int next_h = n > 0 ? h0 + from / per : h0, next_i = i_start;
     uint64_t q_rows = 0, g_rows = 0, stats = 0;
-    auto fetch = [&](int buf) {
-        if (next_i == i_first) {
-            q_rows = loads.rows((const uint16_t*)p.q + b * p.sq.b + next_h * p.sq.h, i_first);
-            g_rows = loads.rows((const uint16_t*)p.dO + b * p.sq.b + next_h * p.sq.h, i_first);
-            stats = (uint64_t)(p.delta + (wave ? all : 0) + ((long long)b * p.Hq + next_h) * p.Tq + i_first);
+    auto fetch = [&](int buf, bool head) {
+        if (head || next_i == i_first) {
+            q_rows = loads.rows((const uint16_t*)p.q + b * p.sq.b + next_h * p.sq.h, next_i);
+            g_rows = loads.rows((const uint16_t*)p.dO + b * p.sq.b + next_h * p.sq.h, next_i);
+            stats = (uint64_t)(p.delta + (wave ? all : 0) + ((long long)b * p.Hq + next_h) * p.Tq + next_i);
         }
         loads.load(q_rows, next_i, rows - 1, lds_address(sm.q[0]) + buf * kTile, lane);
         loads.load(g_rows, next_i, rows - 1, lds_address(sm.g[0]) + buf * kTile, lane);
@@ -479,16 +485,16 @@ __device__ __forceinline__ void key_side(const AttnParams& p, int item, int tile
         next_i += KM;
         if (next_i >= end) { next_i = i_first; ++next_h; }
     };
-    if (n > 0) fetch(0);
+    if (n > 0) fetch(0, true);
     bool bad = false;
-    int i0 = i_first - KM;
+    int i0 = i_start - KM;
     for (int it = 0; it < n; ++it) {
         const int buf = it & 1;
         i0 += KM;
         if (i0 >= end) i0 = i_first;
         wait_loads();
         lds_barrier();
-        if (it + 1 < n) fetch(buf ^ 1);
+        if (it + 1 < n) fetch(buf ^ 1, false);
         if (i0 < lo_most || i0 + KM > hi_least) {
             constexpr int kMine = KM / kKWaves;
             bool mine = any_not_finite<D, kMine>(sm.q[buf] + kMine * wave * D, lane) ||
@@ -596,7 +602,7 @@ __device__ __forceinline__ void key_side(const AttnParams& p, int item, int tile
     if (bad) {
         wait_loads();                                 // no load into LDS outlives the wave
         const int4 see = sm.range[32 * wave + col];
-        keys_one_by_one<D>(p, kp, vp, b, bh, hk, h0, heads, split, c0 + 32 * wave, used, see.x, see.y, see.z, lane);
+        keys_one_by_one<D>(p, kp, vp, b, bh, hk, h0, split, c0 + 32 * wave, used, i_first, KM, per, from, to, see.x, see.y, see.z, lane);
         return;
     }
     wait_loads();
@@ -666,15 +672,13 @@ __global__ __launch_bounds__(256) void attn_dkv_sum(AttnParams p) {
     }
 }
 
-int attn_bwd_splits(int B, int Hq, int Hkv, int Tk) {
-    const int G = Hq / Hkv;
-    const long long base = (long long)B * Hkv * ((Tk + kKN - 1) / kKN);
-    // the smallest divisor of the shared heads that gives every compute unit's two
-    // workgroups something to do
-    int s = 1;
-    while (s < G && (base * s < 512 || G % s != 0)) ++s;
-    while (G % s != 0) ++s;
-    return s;
+int attn_bwd_splits(int B, int Hq, int Hkv, int Tq, int Tk) {
+    const long long base = (long long)B * Hkv * ((Tk + kKN - 1) / kKN), most = (long long)(Hq / Hkv) * (Tq < 512 ? 1 : Tq / 512);
+    // enough workgroups for one on every compute unit beside the query side's, as far as
+    // a split has a head (twice as many: T=2047, 16/4 heads, no faster)
+    // or 512 queries of one to walk: each writes its partial sums in fp32
+    const long long want = base > 0 ? (256 + base - 1) / base : 1;
+    return (int)(want < most ? want : most);
 }
 
 template <int D>

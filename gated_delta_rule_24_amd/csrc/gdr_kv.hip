@@ -317,13 +317,12 @@ hipError_t launch_kv_append(const KvAppendParams& p, hipStream_t st) {
 //           instructions' worth); the key a tile's row m stands for is
 //           16 (m / 4) + 4 tile + m % 4, which leaves lane group g with the
 //           scores of keys 16 g .. 16 g + 15: the keys of its value loads.
-//   output  O^T[channel][query] += V^T P^T with P as the sum of two f16 values, the
-//           weights 2^15 times theirs: 22 bits of a weight count, down to 2^-39 of the
-//           largest, so that an fp32 result is one (with bf16, 8 bits each, the
-//           results were 1.3e-6 off).  A wave's values stand in units of the largest
-//           scale it has met.
-// e4m3 is exact in bf16 and f16; the scales multiply the scores and the weights in
-// fp32.
+//   output  O^T[channel][query] += V^T W^T with the weights W = exp2(s + log2 v_scale),
+//           relative to their own running maximum and 2^15 times that, as the sum of
+//           two f16 values: 22 bits of a weight count, down to 2^-39 of the largest,
+//           whatever the pages' scales, so that an fp32 result is one (with two bf16
+//           values, 8 bits each, results were 1.3e-6 off).
+// e4m3 is exact in bf16 and f16.
 namespace {
 
 constexpr int kDecWaves = 4;
@@ -405,7 +404,7 @@ __global__ __launch_bounds__(64 * kDecWaves) void attn_decode_kernel(AttnDecodeP
     float4v o[VT];
 #pragma unroll
     for (int i = 0; i < VT; ++i) o[i] = float4v{0.f, 0.f, 0.f, 0.f};
-    float m = -INFINITY, l = 0.f, unit = 0.f;         // unit: the largest value scale so far
+    float m = -INFINITY, l = 0.f, wm = -INFINITY;     // maximum and sum of the scores; maximum of the weights
     const float to2 = p.scale * 1.4426950408889634f;
     const int krow = 16 * (col >> 2) + (col & 3);     // key of tile 0's row `col`
 
@@ -426,7 +425,7 @@ __global__ __launch_bounds__(64 * kDecWaves) void attn_decode_kernel(AttnDecodeP
 #pragma unroll
         for (int i = 0; i < VT; ++i)
             vv[i] = *reinterpret_cast<const uint4*>(vp + (size_t)(g * D + 16 * i + col) * 16);
-        const float ks = p.k_scale[ph] * to2, vs = absent ? 0.f : p.v_scale[ph];
+        const float ks = p.k_scale[ph] * to2, vs = absent ? -INFINITY : __builtin_amdgcn_logf(p.v_scale[ph]);   // base 2
 
         float4v sc[4];
 #pragma unroll
@@ -459,19 +458,20 @@ __global__ __launch_bounds__(64 * kDecWaves) void attn_decode_kernel(AttnDecodeP
                 vv[i].x &= keep[0]; vv[i].y &= keep[1]; vv[i].z &= keep[2]; vv[i].w &= keep[3];
             }
         }
-        float top = m;
+        float top = -INFINITY;
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[t][i]);
         top = fmaxf(top, __shfl_xor(top, 16, 64));
         top = max_across32(top);
-        const float at = top == -INFINITY ? 0.f : top;
-        float fade = __builtin_amdgcn_exp2f(m - at);  // 0 from -inf
+        const float wt = fmaxf(wm, top + vs);
+        top = fmaxf(top, m);
+        const float at = top == -INFINITY ? 0.f : top, wat = wt == -INFINITY ? 0.f : wt;
+        l *= __builtin_amdgcn_exp2f(m - at);          // 0 from -inf
+        const float fade = __builtin_amdgcn_exp2f(wm - wat), up = vs - wat + 15.f;
         m = top;
-        l *= fade;
-        if (vs > unit) { fade *= unit / vs; unit = vs; }
-        const float vr = unit > 0.f ? vs / unit : 0.f;
+        wm = wt;
 #pragma unroll
         for (int i = 0; i < VT; ++i) o[i] *= fade;
         half8 hi8[2], lo8[2];
@@ -479,9 +479,8 @@ __global__ __launch_bounds__(64 * kDecWaves) void attn_decode_kernel(AttnDecodeP
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                float x = __builtin_amdgcn_exp2f(sc[t][i] - at + 15.f);
-                l += x;
-                x *= vr;
+                l += __builtin_amdgcn_exp2f(sc[t][i] - at);
+                const float x = __builtin_amdgcn_exp2f(sc[t][i] + up);
                 const _Float16 a = (_Float16)x;
                 hi8[t >> 1][(t & 1) * 4 + i] = a;
                 lo8[t >> 1][(t & 1) * 4 + i] = (_Float16)(x - (float)a);
@@ -500,9 +499,10 @@ __global__ __launch_bounds__(64 * kDecWaves) void attn_decode_kernel(AttnDecodeP
     l += __shfl_xor(l, 16, 64);
     l = sum_across32(l);
     if (g == 0) { sm.ml[wave][col][0] = m; sm.ml[wave][col][1] = l; }
+    const float down = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(wm - m - 15.f);   // to the scores' maximum
 #pragma unroll
     for (int i = 0; i < VT; ++i)
-        *reinterpret_cast<float4v*>(&sm.o[wave][col][16 * i + 4 * g]) = o[i] * unit;
+        *reinterpret_cast<float4v*>(&sm.o[wave][col][16 * i + 4 * g]) = o[i] * down;
     __syncthreads();
     for (int idx = threadIdx.x; idx < nq * D; idx += 64 * kDecWaves) {
         const int c = idx / D, ch = idx % D;

@@ -136,6 +136,7 @@ hipError_t launch_rope(RopeParams p, hipStream_t st) {
     // enough workgroups to fill the chip, then as many heads per angle as that leaves
     long long heads = all * tiles / 2048;
     heads = heads < 1 ? 1 : heads > all ? all : heads;
+    if (heads < (all + 65534LL) / 65535) heads = (all + 65534LL) / 65535;   // the grid's second axis
     p.heads = (int)heads;
     dim3 grid((unsigned)tiles, (unsigned)((all + heads - 1) / heads)), block(256);
     if (p.flags & GDR_ROPE_INTERLEAVED) {

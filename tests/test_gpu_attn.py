@@ -276,6 +276,27 @@ def test_both_layouts_give_the_same_bits():
     assert all(torch.equal(gt[n].transpose(1, 2), g[n]) for n in g)
 
 
+@pytest.mark.parametrize("d,cu", [(64, None), (128, None), (64, [0, 90, 700, 1100])])
+def test_queries_dealt_to_several_workgroups(d, cu):
+    """Few key tiles and many queries: a tile's queries, of both heads, are split; also
+    where a NaN makes the workgroups that meet it sum row by row."""
+    x = _inputs(1, 2, 1, 1100, 1100, d, 17)
+    assert gdr.gdr_attn_bwd_workspace_bytes(1, 2, 1, 1100, 1100, d) > 4 * 2 * 1100 * d * 4
+    o, lse = _check(x, 0, cu)
+    clean = _backward(x, o, lse, 0, cu)
+    x["dO"][0, 1, 700, 3] = math.nan
+    got = _backward(x, o, lse, 0, cu)
+    y = {n: t.to(F64) for n, t in _inputs(1, 2, 1, 1100, 1100, d, 17).items()}
+    r = ref.attention_bwd(y["q"], y["k"], y["v"], y["dO"], 0, None, cu)
+    begin = 700 if cu else 0
+    for n in ("dk", "dv"):
+        g = _back(got[n], cu is not None, False)
+        keep = [j for j in range(1100) if j > 700 or j < begin]
+        _within(n, g[:, :, keep], r[n][:, :, keep], r[n + "_tol"][:, :, keep])
+    assert bool(torch.isnan(_back(got["dk"], cu is not None, False)[:, :, begin:701]).all())
+    assert torch.equal(_back(got["dq"], cu is not None, False)[:, 0], _back(clean["dq"], cu is not None, False)[:, 0])
+
+
 def test_empty_calls():
     e = lambda T: torch.zeros((2, 2, T, 64), dtype=torch.bfloat16, device="cuda")  # noqa: E731
     o, lse = gdr.attn_fwd(e(0), e(5), e(5))

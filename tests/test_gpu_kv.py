@@ -162,6 +162,20 @@ def test_decode_scales(scale):
     _decode_check(c, _rand((2, 4, 128), 19), table, [130, 256], 0, scale)
 
 
+def test_decode_page_scales_far_apart():
+    """One page's values 2^40 times another's, and the other way round for the keys'
+    weights: every page counts to fp32."""
+    c, table = _cache(8, 1, 64, seed=40), _table(2, 4, 8, 41)
+    c.v_scale[table[0, 0]], c.v_scale[table[0, 1]] = 2.0 ** 20, 2.0 ** -20
+    c.v_scale[table[1, 2]], c.k_scale[table[1, 2]] = 2.0 ** 30, 2.0 ** -20
+    c.k_scale[table[0, 0]] = 2.0 ** -3
+    q = _rand((2, 4, 64), 42)
+    _decode_check(c, q, table, [200, 256])
+    c.v_scale[table[0, 1]] = 2.0 ** -96
+    c.v_scale[table[1, 0]] = 2.0 ** 110
+    _decode_check(c, q, table, [200, 256])
+
+
 def test_decode_ignores_what_is_masked():
     """Bytes behind the last token or before the window, pages that are not there:
     NaN everywhere in them changes nothing."""
