@@ -124,29 +124,25 @@ __device__ __forceinline__ int lane_now() {
     return x;
 }
 
-// Order of N groups of P products that share R LDS reads: AHEAD groups' reads go
-// first, then products and reads in turn.  Left alone, the compiler reads right
-// before each product and waits for every read.
-template <int AHEAD, int N, int R, int P = 1> __device__ __forceinline__ void sched_reads_ahead() {
+// Order of N products of R LDS reads each: the reads of AHEAD products go first,
+// then products and reads in turn.  Left alone, the compiler reads right before
+// each product and waits for every read.
+template <int AHEAD, int N, int R> __device__ __forceinline__ void sched_reads_ahead() {
     __builtin_amdgcn_sched_group_barrier(0x100, AHEAD * R, 0);       // LDS reads
 #pragma unroll
     for (int i = 0; i < N - AHEAD; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x008, P, 0);           // products
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);           // a product
         __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
     }
-    __builtin_amdgcn_sched_group_barrier(0x008, AHEAD * P, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, AHEAD, 0);
 }
 
 // A lane's two read addresses inside a tile, from which every other one follows by
 // flipping address bits: the swizzle is an exclusive-or of the chunk, and tiles
-// start at multiples of 256 bytes.  hidden() hides them from the compiler once a
-// step; otherwise it keeps all of them in registers across the loop (16 more than
-// the key-side gradient kernel has).
+// start at multiples of 256 bytes.
 template <int D> struct ReadAt {
     uint32_t row, col;
 
-    __device__ __forceinline__ ReadAt() {}
-    __device__ __forceinline__ void hidden() { asm volatile("" : "+v"(row), "+v"(col)); }
     __device__ __forceinline__ explicit ReadAt(int lane) {
         const int r = lane & 31, h = lane >> 5;
         row = 2 * (r * D + 8 * (h ^ swz<D>(r)));
@@ -160,10 +156,11 @@ template <int D> struct ReadAt {
         x.col += tile;
         return x;
     }
-    // the same, hidden
+    // the same, hidden from the compiler, which would keep every address in a register
+    // across the loop (16 more than the key-side gradients have)
     __device__ __forceinline__ ReadAt fresh(uint32_t tile) const {
         ReadAt x = in(tile);
-        x.hidden();
+        asm volatile("" : "+v"(x.row), "+v"(x.col));
         return x;
     }
     // operand along d: row `r0` + (lane & 31), channels 16 s + 8 (lane / 32) .. + 7
