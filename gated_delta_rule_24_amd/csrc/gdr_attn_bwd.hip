@@ -79,8 +79,6 @@ template <int D>
 struct __attribute__((aligned(256))) DqSmem {
     uint16_t k[2][kQN * D];
     uint16_t v[2][kQN * D];
-    int bound[kQM];
-    int shared[3];
     int bad[kQWaves];
 };
 
@@ -127,19 +125,17 @@ __device__ __forceinline__ void query_side(const AttnParams& p, int item, int ti
     const int b = unit / p.Hq, hq = unit % p.Hq, hk = hq / (p.Hq / p.Hkv);
     const int r0 = tile * kQM, off = p.Tk - p.Tq;
 
-    int used = p.Tq;
-    if (p.cu_seqlens) {
-        row_bounds<kQM, false>(p.cu_seqlens, p.nseq, p.Tq, r0, sm.bound, sm.shared, tid, 64 * kQWaves, used);
-        if (r0 >= used) return;
-    }
+    SeqRows seq = {p.Tq, 0, 0, 0, false};
+    if (p.cu_seqlens) seq = seq_rows<kQM, false>(p.cu_seqlens, p.nseq, p.Tq, r0, r0 + 32 * wave, lane);
+    const int used = seq.used;
+    if (r0 >= used) return;
     const int row = r0 + 32 * wave + col, at = row + off;
     const bool live = row < used;
-    int lo = p.cu_seqlens ? sm.bound[32 * wave + col] : 0, hi = live ? at + 1 : 0;
+    int lo = seq.mine, hi = live ? at + 1 : 0;
     if (p.window > 0 && at - p.window + 1 > lo) lo = at - p.window + 1;
     if (hi <= lo) { lo = 0; hi = 0; }
     const int last_row = min(r0 + kQM, used) - 1, end = last_row + off + 1;
-    int begin = p.cu_seqlens ? sm.bound[0] : 0;
-    int lo_most = p.cu_seqlens ? sm.bound[last_row - r0] : 0;
+    int begin = seq.first, lo_most = seq.last;
     if (p.window > 0) {
         begin = max(begin, r0 + off - p.window + 1);
         lo_most = max(lo_most, last_row + off - p.window + 1);
@@ -330,8 +326,6 @@ struct __attribute__((aligned(256))) DkvSmem {
     float delta[2][64];
     float lse2[2][64];
     int4 range[kKN];            // of each key: first query, one past the last, whether alone
-    int bound[kKN];
-    int shared[3];
     int bad[kKWaves];
 };
 
@@ -397,12 +391,10 @@ __device__ __forceinline__ void key_side(const AttnParams& p, int item, int tile
     const int heads = p.Hq / p.Hkv, h0 = hk * heads;
     const int c0 = tile * kKN, off = p.Tk - p.Tq;
 
-    int used = p.Tk, rows = p.Tq;
-    if (p.cu_seqlens) {
-        row_bounds<kKN, true>(p.cu_seqlens, p.nseq, p.Tk, c0, sm.bound, sm.shared, tid, 64 * kKWaves, used);
-        if (c0 >= used) return;
-        rows = used;
-    }
+    SeqRows seq = {p.Tk, p.Tq, p.Tq, p.Tq, false};
+    if (p.cu_seqlens) seq = seq_rows<kKN, true>(p.cu_seqlens, p.nseq, p.Tk, c0, c0 + 32 * wave, lane);
+    const int used = seq.used, rows = p.cu_seqlens ? used : p.Tq;
+    if (c0 >= used) return;
     const uint16_t* kp = (const uint16_t*)p.k + b * p.sk.b + hk * p.sk.h;
     const uint16_t* vp = (const uint16_t*)p.v + b * p.sk.b + hk * p.sk.h;
     {
@@ -421,12 +413,12 @@ __device__ __forceinline__ void key_side(const AttnParams& p, int item, int tile
     int see_from, see_to, all_from, all_to;           // queries that see some key of the wave's / every one
     {
         const int in = 32 * wave + col, j = c0 + in;
-        int lo = max(j - off, 0), hi = p.cu_seqlens ? min(sm.bound[in], rows) : rows;
+        int lo = max(j - off, 0), hi = min(seq.mine, rows);
         if (p.window > 0) hi = min(hi, j - off + p.window);
         if (j >= used || hi <= lo) { lo = 0; hi = 0; }
         // seen by one query that sees no other key: the window is one key, or the key is
         // all its sequence has.  The softmax over one key is constant, its gradient 0
-        const bool first = j == 0 || (p.cu_seqlens && (in == 0 ? sm.shared[2] != 0 : sm.bound[in - 1] == j));
+        const bool first = j == 0 || seq.starts;
         const bool alone = p.window == 1 || (first && j >= off && hi - lo == 1);
         if (h == 0) sm.range[in] = make_int4(lo, hi, alone, 0);
         see_from = hi > lo ? lo : INT_MAX;
@@ -446,8 +438,7 @@ __device__ __forceinline__ void key_side(const AttnParams& p, int item, int tile
     all_to = __builtin_amdgcn_readfirstlane(all_to);
     const int last_key = min(c0 + kKN, used) - 1;
     const int begin = max(c0 - off, 0);
-    int end = rows, hi_least = rows;
-    if (p.cu_seqlens) { end = min(end, sm.bound[last_key - c0]); hi_least = min(hi_least, sm.bound[0]); }
+    int end = min(rows, seq.last), hi_least = min(rows, seq.first);
     if (p.window > 0) {
         end = min(end, last_key - off + p.window);
         hi_least = min(hi_least, c0 - off + p.window);

@@ -40,8 +40,6 @@ template <int D>
 struct __attribute__((aligned(256))) FwdSmem {
     uint16_t k[2][kBN * D];
     uint16_t v[2][kBN * D];
-    int bound[kBM];
-    int shared[3];
     int bad[kWaves];
 };
 
@@ -95,25 +93,24 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_kernel(AttnParams p, 
 #pragma unroll
         for (int s = 0; s < KS; ++s) qf[s] = __builtin_bit_cast(bf8v, *reinterpret_cast<const uint4*>(qr + 16 * s));
     }
-    int used = p.Tq;
-    if (p.cu_seqlens) {
-        row_bounds<kBM, false>(p.cu_seqlens, p.nseq, p.Tq, r0, sm.bound, sm.shared, tid, 64 * kWaves, used);
-        if (r0 >= used) return;
-    }
+    SeqRows seq = {p.Tq, 0, 0, 0, false};
+    if (p.cu_seqlens) seq = seq_rows<kBM, false>(p.cu_seqlens, p.nseq, p.Tq, r0, r0 + 32 * wave, lane);
+    const int used = seq.used;
+    if (r0 >= used) return;
     const int row = r0 + 32 * wave + col;
     const int at = row + p.Tk - p.Tq;                 // the query's place among the keys
     const bool live = row < used;
-    int lo = p.cu_seqlens ? sm.bound[32 * wave + col] : 0, hi = live ? at + 1 : 0;
+    int lo = seq.mine, hi = live ? at + 1 : 0;
     if (p.window > 0 && at - p.window + 1 > lo) lo = at - p.window + 1;
     if (hi <= lo) { lo = 0; hi = 0; }                 // sees nothing
     // the workgroup's keys: rows are in order, so their first and last rows bound them
     const int last_row = min(r0 + kBM, used) - 1;
     const int end = last_row + p.Tk - p.Tq + 1;
-    int begin = p.cu_seqlens ? sm.bound[0] : 0;
+    int begin = seq.first;
     if (p.window > 0) begin = max(begin, r0 + p.Tk - p.Tq - p.window + 1);
     begin = max(begin, 0);
     // keys from lo_most on and below hi_least are seen by every row
-    int lo_most = p.cu_seqlens ? sm.bound[max(last_row - r0, 0)] : 0;
+    int lo_most = seq.last;
     if (p.window > 0) lo_most = max(lo_most, last_row + p.Tk - p.Tq - p.window + 1);
     const int hi_least = r0 + p.Tk - p.Tq + 1;
 

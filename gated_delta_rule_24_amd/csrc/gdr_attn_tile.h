@@ -12,6 +12,8 @@
 //            bytes, so 32 lanes cover one bank line exactly.
 #pragma once
 
+#include <limits.h>
+
 #include "gdr_attn.h"
 #include "gdr_device.h"
 #include "gdr_launch.h"
@@ -223,69 +225,71 @@ __device__ __forceinline__ void add_rows(float (&acc)[D / 64], float w, const ui
     }
 }
 
-// Packed sequences: for rows r0 .. r0 + BM - 1 of T, the first row of each one's
-// sequence (`from`) or one past its last (`to`).  Values of cu outside [0, T] are
-// held inside, so that no content of it leads out of the tensors.  `used` is
-// cu[nseq]: rows from there on belong to no sequence; shared[2] tells whether one
-// starts at r0.  All threads of the
-// workgroup call it; ends with a barrier.
+// Packed sequences.  For the wave's rows w0 .. w0 + 31 (row w0 + lane % 32) of a
+// workgroup's r0 .. r0 + BM - 1: where the row's sequence starts (TO: one past its
+// end), the same of the workgroup's first and last row, and whether a sequence starts
+// at the row.  `used` is cu[nseq]: rows from there on belong to no sequence.  Values of
+// cu outside [0, T] are held inside, so that no content of it leads out of the tensors.
+//
+// Every wave finds them for itself, in registers: 64 entries of cu are one load, what
+// lies at or below a row among them one ballot, and more than 64 are first narrowed to
+// the 64th part that holds r0.  That is one trip to memory before the first tile
+// where passing the bounds through LDS took 5 us of a workgroup's 31.
+struct SeqRows {
+    int used, mine, first, last;
+    bool starts;
+};
+
 template <int BM, bool TO>
-__device__ __forceinline__ void row_bounds(const int* cu, int nseq, int T, int r0, int* bound, int* shared, int tid,
-                                           int nthreads, int& used) {
-    for (int i = tid; i < BM; i += nthreads) bound[i] = TO ? T : 0;
-    if (tid == 0) { shared[0] = TO ? T : 0; shared[1] = 0; shared[2] = 0; }
-    __syncthreads();
-    int edge = TO ? T : 0;
-    for (int s = tid; s <= nseq; s += nthreads) {
-        const int raw = cu[s], c = raw < 0 ? 0 : raw > T ? T : raw;
-        if (s == nseq) shared[1] = c;
-        if (c == r0) shared[2] = 1;
-        if constexpr (TO) {                           // the sequence ends at c: rows below c
-            if (c >= r0 + BM) edge = c < edge ? c : edge;
-            else if (c > r0) bound[c - 1 - r0] = c;
-        } else {                                      // a sequence starts at c: rows from c
-            if (c <= r0) edge = c > edge ? c : edge;
-            else if (c < r0 + BM) bound[c - r0] = c;
-        }
+__device__ __forceinline__ SeqRows seq_rows(const int* cu, int nseq, int T, int r0, int w0, int lane) {
+    auto entry = [&](int i, int end) {
+        int c = INT_MAX;
+        if (i < end) { c = cu[i]; c = c < 0 ? 0 : c > T ? T : c; }
+        return c;
+    };
+    auto last_upto = [&](int c, int x) {              // the last entry <= x, or 0
+        const uint64_t m = __ballot(c <= x);
+        return m ? __builtin_amdgcn_readlane(c, 63 - __builtin_clzll(m)) : 0;
+    };
+    auto first_above = [&](int c, int x) {            // the first entry > x, or T
+        const uint64_t m = __ballot(c > x);
+        return m ? min(__builtin_amdgcn_readlane(c, __builtin_ctzll(m)), T) : T;
+    };
+    SeqRows z;
+    z.used = __builtin_amdgcn_readfirstlane(entry(nseq, nseq + 1));
+    int s = 0, n = nseq + 1;                          // the last entry <= r0 is among s .. s + n - 1
+    while (n > 64) {
+        const int step = (n + 63) / 64;
+        const uint64_t m = __ballot(entry(s + lane * step, s + n) <= r0);
+        const int k = m ? 63 - __builtin_clzll(m) : 0;
+        s += k * step;
+        n = min(step, n - k * step);
     }
-    if constexpr (TO) atomicMin(&shared[0], edge);
-    else atomicMax(&shared[0], edge);
-    __syncthreads();
-    // running maximum from the front / minimum from the back, by one wave
-    if (tid < 64) {
-        constexpr int PER = BM / 64;
-        int x[PER];
-        int run = shared[0];
+    const int row = w0 + (lane & 31), last_row = min(r0 + BM, z.used) - 1;
+    z.mine = z.first = z.last = TO ? T : 0;
+    z.starts = false;
+    for (;; s += 64) {
+        const int c = entry(s + lane, nseq + 1);
         if constexpr (TO) {
-            int low = T;
-#pragma unroll
-            for (int i = PER - 1; i >= 0; --i) { const int b = bound[tid * PER + i]; low = b < low ? b : low; x[i] = low; }
-            for (int o = 1; o < 64; o <<= 1) {
-                const int y = __shfl_down(low, o, 64);
-                if (tid + o < 64) low = y < low ? y : low;
-            }
-            int after = __shfl_down(low, 1, 64);
-            if (tid == 63) after = T;
-            run = after < run ? after : run;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) bound[tid * PER + i] = x[i] < run ? x[i] : run;
+            z.first = min(z.first, first_above(c, r0));
+            z.last = min(z.last, first_above(c, last_row));
+            z.mine = min(z.mine, first_above(c, w0 + 31));
         } else {
-            int high = 0;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) { const int b = bound[tid * PER + i]; high = b > high ? b : high; x[i] = high; }
-            for (int o = 1; o < 64; o <<= 1) {
-                const int y = __shfl_up(high, o, 64);
-                if (tid >= o) high = y > high ? y : high;
-            }
-            int before = __shfl_up(high, 1, 64);
-            if (tid == 0) before = 0;
-            run = before > run ? before : run;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) bound[tid * PER + i] = x[i] > run ? x[i] : run;
+            z.first = max(z.first, last_upto(c, r0));
+            z.last = max(z.last, last_upto(c, last_row));
+            z.mine = max(z.mine, last_upto(c, w0));
         }
+        for (uint64_t m = __ballot(c >= w0 && c <= w0 + 31); m; m &= m - 1) {
+            const int v = __builtin_amdgcn_readlane(c, __builtin_ctzll(m));
+            if constexpr (TO) {
+                if (row < v) z.mine = min(z.mine, v);
+                z.starts = z.starts || row == v;
+            } else {
+                if (row >= v) z.mine = max(z.mine, v);
+            }
+        }
+        if (s + 64 > nseq || __builtin_amdgcn_readlane(c, 63) > r0 + BM) return z;
     }
-    __syncthreads();
-    used = shared[1];
 }
 
 // Work items: unit u of `units` (batch and head), tile t of `tiles`; consecutive
