@@ -86,7 +86,7 @@ gdr::AttnParams attn_params(const void* q, const void* k, const void* v, int B, 
     p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.Tq = Tq; p.Tk = Tk; p.d = d;
     // a window that reaches behind the first key is none
     p.window = window < Tk ? window : 0;
-    p.scale = scale; p.splits = 1;
+    p.scale = scale; p.splits = 1; p.split_steps = 0;
     p.sq = attn_strides(Hq, Tq, d, (flags & GDR_TOKEN_MAJOR) != 0);
     p.sk = attn_strides(Hkv, Tk, d, (flags & GDR_TOKEN_MAJOR) != 0);
     return p;
@@ -526,7 +526,7 @@ gdr_status gdr_attn_fwd_varlen(const void* q, const void* k, const void* v, void
 size_t gdr_attn_bwd_workspace_bytes(int B, int Hq, int Hkv, int Tq, int Tk, int d) {
     if (attn_args(B, Hq, Hkv, Tq, Tk, d, 0, 1.f, 0) != GDR_OK) return 0;
     const int splits = gdr::attn_bwd_splits(B, Hq, Hkv, Tq, Tk);
-    const size_t part = splits > 1 ? 2 * (size_t)splits * B * Hkv * Tk * d * sizeof(float) : 0;
+    const size_t part = splits > 1 ? 2 * (size_t)gdr::attn_bwd_splits_most(splits, Tk) * B * Hkv * Tk * d * sizeof(float) : 0;
     return attn_delta_bytes(B, Hq, Tq) + part;
 }
 

@@ -48,14 +48,18 @@ struct AttnParams {
     int nseq;
     int B, Hq, Hkv, Tq, Tk, d;
     int window;                 // 0: none
-    int splits;                 // backward: workgroups a key tile's queries (of every head that shares it) are dealt to
+    int splits;                 // backward: workgroups a key tile's queries (of every head that shares it) are dealt to,
+                                // at most
+    int split_steps;            // backward: steps of one of them; 0: every tile has `splits`
     float scale;
     AttnStrides sq, sk;         // queries' tensors (q, o, dO, dq); keys' tensors (k, v, dk, dv)
 };
 hipError_t launch_attn_fwd(const AttnParams& p, hipStream_t st);
 hipError_t launch_attn_bwd(const AttnParams& p, hipStream_t st);
-// Splits of the key side's queries (1: no partials).
+// Splits of the key side's queries, of a tile on average (1: no partials), and the most
+// that a tile is given then.
 int attn_bwd_splits(int B, int Hq, int Hkv, int Tq, int Tk);
+int attn_bwd_splits_most(int splits, int Tk);
 
 struct KvAppendParams {
     const void* k;

@@ -14,9 +14,11 @@
 // 49%) and by power: on random data the clock falls from 2.4 to about 1.9 GHz (all
 // inputs zero: 634 us for 819).  Measured, d = 128: 2 x 8,192 tokens, 16 heads, window
 // 2,048 820 us, 734 TFLOP/s for the five products of a single walk and 1,030 for the
-// seven; 2,047 tokens, 16 heads on 4, 100 us, 430 and 600, of which 6 form D and 7 sum
-// the splits.  A single walk would add dq into memory from every key tile: with atomics,
-// whose order would change results, or with a partial dq for each of them.
+// seven; 2,047 tokens, 16 heads on 4, 86 us, 497 and 696, of which 6 form D and 7 sum
+// the splits (bound by the steps that one workgroup takes after the other: 40 of 1.8 us
+// on the key side, up to 32 of 1.9 on the query side).  A single walk would add dq into
+// memory from every key tile: with atomics, whose order would change results, or with
+// a partial dq for each of them.
 #include <limits.h>
 
 #include <type_traits>
@@ -378,6 +380,42 @@ __device__ __forceinline__ void keys_one_by_one(const AttnParams& p, const uint1
 
 }  // namespace
 
+// Steps of one head's queries that see some key of tile `tile`, without a window.
+template <int D> __host__ __device__ inline int key_steps(const AttnParams& p, int tile) {
+    const int c0 = tile * kKN, off = p.Tk - p.Tq, begin = c0 > off ? c0 - off : 0;
+    return p.Tq > begin ? (p.Tq + kKM<D> - 1) / kKM<D> - begin / kKM<D> : 0;
+}
+// Workgroups that key tile's queries are dealt to.
+template <int D> __host__ __device__ inline int key_splits(const AttnParams& p, int tile) {
+    if (p.split_steps == 0) return p.splits;
+    const int n = (p.Hq / p.Hkv * key_steps<D>(p, tile) + p.split_steps - 1) / p.split_steps;
+    return n < 1 ? 1 : n > p.splits ? p.splits : n;
+}
+
+// The key tile of item `split` of all tiles' splits in order; leaves the split's number
+// among the tile's and how many it has.  Up to 256 tiles: four a lane and a running sum.
+template <int D> __device__ __forceinline__ int tile_of_split(const AttnParams& p, int tiles, int lane, int& split, int& splits) {
+    int n[4], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum += n[i] = 4 * lane + i < tiles ? key_splits<D>(p, 4 * lane + i) : 0;
+    int end = sum;
+    for (int o = 1; o < 64; o <<= 1) {
+        const int y = __shfl_up(end, o, 64);
+        if (lane >= o) end += y;
+    }
+    const int owner = __builtin_ctzll(__ballot(end > split));
+    split -= __builtin_amdgcn_readlane(end - sum, owner);
+    int tile = 4 * owner;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        splits = __builtin_amdgcn_readlane(n[i], owner);
+        if (split < splits) break;
+        split -= splits;
+        ++tile;
+    }
+    return tile;
+}
+
 template <int D>
 __device__ __forceinline__ void key_side(const AttnParams& p, int item, int tiles, char* smem) {
     constexpr int KS = D / 16, DB = D / 32;
@@ -385,9 +423,17 @@ __device__ __forceinline__ void key_side(const AttnParams& p, int item, int tile
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 31, h = lane >> 5;
 
-    int unit, tile;
-    work_item(item, p.B * p.Hkv * p.splits, tiles, unit, tile);
-    const int split = unit % p.splits, bh = unit / p.splits, b = bh / p.Hkv, hk = bh % p.Hkv;
+    int bh, tile, split, splits = p.splits;
+    if (p.split_steps == 0) {
+        work_item(item, p.B * p.Hkv * splits, tiles, bh, tile);
+        split = bh % splits;
+        bh /= splits;
+    } else {
+        bh = item % (p.B * p.Hkv);
+        split = item / (p.B * p.Hkv);
+        tile = tile_of_split<D>(p, tiles, lane, split, splits);
+    }
+    const int b = bh / p.Hkv, hk = bh % p.Hkv;
     const int heads = p.Hq / p.Hkv, h0 = hk * heads;
     const int c0 = tile * kKN, off = p.Tk - p.Tq;
 
@@ -458,7 +504,7 @@ __device__ __forceinline__ void key_side(const AttnParams& p, int item, int tile
     const int i_first = begin / KM * KM;
     // steps of the heads that share the keys, one head after the other; this split's
     const int per = end > begin ? (end - i_first + KM - 1) / KM : 0;
-    const int from = (int)((long long)per * heads * split / p.splits), to = (int)((long long)per * heads * (split + 1) / p.splits);
+    const int from = (int)((long long)per * heads * split / splits), to = (int)((long long)per * heads * (split + 1) / splits);
     const int n = to - from;
     const long long all = (long long)p.B * p.Hq * p.Tq;
     const uint64_t step_bytes = (uint64_t)KM * 2 * p.sq.t;
@@ -642,9 +688,11 @@ static_assert(kQWaves == kKWaves, "one kernel");
 template <int D>
 __global__ __launch_bounds__(64 * kQWaves, 2) void attn_bwd_kernel(AttnParams p, int key_items, int key_tiles, int query_tiles) {
     extern __shared__ __attribute__((aligned(256))) char smem[];
-    const int item = blockIdx.x;
-    if (item < key_items) key_side<D>(p, item, key_tiles, smem);
-    else query_side<D>(p, item - key_items, query_tiles, smem);
+    // the longest first: on the key side without splits of equal length, else, where every
+    // workgroup runs at once, the query side's
+    const int item = blockIdx.x, first = p.split_steps > 0 && gridDim.x <= 512 ? gridDim.x - key_items : 0;
+    if (item >= first && item - first < key_items) key_side<D>(p, item - first, key_tiles, smem);
+    else query_side<D>(p, first ? item : item - key_items, query_tiles, smem);
 }
 
 // Sums the splits' partial dk and dv in their order; 8 channels a thread.
@@ -658,11 +706,12 @@ __global__ __launch_bounds__(256) void attn_dkv_sum(AttnParams p) {
     const int t = (int)(row % p.Tk), b = (int)(bh / p.Hkv), hk = (int)(bh % p.Hkv);
     if (p.cu_seqlens && t >= p.cu_seqlens[p.nseq]) return;
     const long long to = b * p.sk.b + hk * p.sk.h + t * p.sk.t + c;
+    const int splits = key_splits<D>(p, t / kKN);
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
         const float* src = p.part + side * p.splits * one + at;
         float4v x = {0.f, 0.f, 0.f, 0.f}, y = {0.f, 0.f, 0.f, 0.f};
-        for (int s = 0; s < p.splits; ++s) {
+        for (int s = 0; s < splits; ++s) {
             x += *reinterpret_cast<const float4v*>(src + s * one);
             y += *reinterpret_cast<const float4v*>(src + s * one + 4);
         }
@@ -671,17 +720,27 @@ __global__ __launch_bounds__(256) void attn_dkv_sum(AttnParams p) {
     }
 }
 
+constexpr int kSplitQueries = 512;                   // of one head, the least for a split
+
 int attn_bwd_splits(int B, int Hq, int Hkv, int Tq, int Tk) {
-    const long long base = (long long)B * Hkv * ((Tk + kKN - 1) / kKN), most = (long long)(Hq / Hkv) * (Tq < 512 ? 1 : Tq / 512);
+    const long long base = (long long)B * Hkv * ((Tk + kKN - 1) / kKN);
+    const long long most = (long long)(Hq / Hkv) * (Tq < kSplitQueries ? 1 : Tq / kSplitQueries);
     // one key-side workgroup for every compute unit, beside the query side's, as far as a
     // split has a head or 512 queries of one to walk: each writes its partial sums in fp32
-    // (16 heads on 4, T = 2047: 127 us without splits, 100 with 256 workgroups, 101 with 512)
+    // (16 heads on 4, T = 2047, as many splits for every tile: 127 us with one, 100 with
+    // 256 workgroups, 101 with 512)
     const long long want = base > 0 ? (256 + base - 1) / base : 1;
     return (int)(want < most ? want : most);
 }
 
+// the first of K tiles is seen by 2 K / (K + 1) times as many queries as the mean
+int attn_bwd_splits_most(int splits, int Tk) {
+    const int tiles = (Tk + kKN - 1) / kKN;
+    return (int)((2LL * splits * tiles + tiles) / (tiles + 1));
+}
+
 template <int D>
-static hipError_t launch_bwd_d(const AttnParams& p, hipStream_t st) {
+static hipError_t launch_bwd_d(AttnParams p, hipStream_t st) {
     static std::atomic<unsigned long long> done{0};
     constexpr size_t kLds = sizeof(DqSmem<D>) > sizeof(DkvSmem<D>) ? sizeof(DqSmem<D>) : sizeof(DkvSmem<D>);
     hipError_t e = ensure_dyn_lds(reinterpret_cast<const void*>(&attn_bwd_kernel<D>), (int)kLds, done);
@@ -693,7 +752,25 @@ static hipError_t launch_bwd_d(const AttnParams& p, hipStream_t st) {
         if (e != hipSuccess) return e;
     }
     const int query_tiles = (p.Tq + kQM - 1) / kQM, key_tiles = (p.Tk + kKN - 1) / kKN;
-    const long long key_items = (long long)p.B * p.Hkv * p.splits * key_tiles, items = key_items + (long long)p.B * p.Hq * query_tiles;
+    if (p.splits > 1 && !p.cu_seqlens && p.window == 0) {
+        // The first keys are seen by most queries: splits of as many steps everywhere
+        // (16 heads on 4, T = 2047: 86 us, with as many splits for every tile 100; 16 on 2,
+        // T = 4096: 249, 328).  With a window the tiles have about as many as each other
+        // (4,096 tokens, window 512: 98, 91), and of packed sequences the host knows none.
+        long long steps = 0;
+        for (int t = 0; t < key_tiles; ++t) steps += key_steps<D>(p, t);
+        const long long all = (long long)key_tiles * p.splits - key_tiles / 2;   // half a split of a tile is lost in rounding
+        const long long each = ((long long)(p.Hq / p.Hkv) * steps + all - 1) / all, least = kSplitQueries / kKM<D>;
+        p.split_steps = (int)(each > least ? each : least);
+        p.splits = attn_bwd_splits_most(p.splits, p.Tk);
+    }
+    long long key_items = (long long)key_tiles * p.splits;
+    if (p.split_steps > 0) {
+        key_items = 0;
+        for (int t = 0; t < key_tiles; ++t) key_items += key_splits<D>(p, t);
+    }
+    key_items *= (long long)p.B * p.Hkv;
+    const long long items = key_items + (long long)p.B * p.Hq * query_tiles;
     if (items == 0) return hipSuccess;
     hipLaunchKernelGGL((attn_bwd_kernel<D>), dim3((unsigned)items), dim3(64 * kQWaves), kLds, st, p, (int)key_items, key_tiles,
                        query_tiles);

@@ -19,7 +19,7 @@
 // clock from 2.4 to about 1.9 GHz (all inputs zero: 203 us for 257, a library's
 // product of two 8192 x 8192 matrices 612 for 790).  Measured, d = 128: 2 x 8,192
 // tokens, 16 heads, window 2,048 260 us, 927 TFLOP/s; 16,384 packed tokens as 19
-// sequences, 16 heads on 4, 143 us, 590 TFLOP/s (two fifths of the tiles are seen in
+// sequences, 16 heads on 4, 135 us, 628 TFLOP/s (two fifths of the tiles are seen in
 // part, and the workgroups' lengths differ); 257 tokens 7.5 us on the GPU, 10 a call.
 // Measured and not taken (first case, 254 to 262 beside them): 64 queries a wave and
 // one wave a SIMD 296; tiles of 32 keys and three waves a SIMD 273; the scores of a

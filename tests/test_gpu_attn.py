@@ -276,6 +276,14 @@ def test_both_layouts_give_the_same_bits():
     assert all(torch.equal(gt[n].transpose(1, 2), g[n]) for n in g)
 
 
+@pytest.mark.parametrize("Tq,Tk,Hq,Hkv,d,window", [(2047, 2047, 4, 1, 128, 0), (2500, 2500, 2, 2, 64, 0), (700, 2300, 4, 2, 64, 0),
+                                                   (2300, 700, 4, 2, 64, 0), (1500, 1500, 8, 1, 128, 300)])
+def test_splits_over_many_key_tiles(Tq, Tk, Hq, Hkv, d, window):
+    """Splits of equal length (more of them for the first keys), with a window as many
+    for every tile; also with more keys than queries and fewer."""
+    _check(_inputs(1, Hq, Hkv, Tq, Tk, d, Tq), window)
+
+
 @pytest.mark.parametrize("d,cu", [(64, None), (128, None), (64, [0, 90, 700, 1100])])
 def test_queries_dealt_to_several_workgroups(d, cu):
     """Few key tiles and many queries: a tile's queries, of both heads, are split; also
