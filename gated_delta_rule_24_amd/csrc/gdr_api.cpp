@@ -61,6 +61,8 @@ bool attn_sizes_ok(int B, long long H, int T) {
     return H <= (1LL << 28) && (long long)B * H <= (1LL << 28) && (long long)B * H * (((long long)T + 15) / 16) <= (1LL << 31) - 1;
 }
 
+constexpr int kMostSequences = 1 << 30;               // attention: the kernels number them in 32 bits
+
 gdr_status attn_args(int B, int Hq, int Hkv, int Tq, int Tk, int d, int window, float scale, uint32_t flags) {
     if (flags & ~(GDR_ACT_F32 | GDR_TOKEN_MAJOR)) return GDR_ERR_INVALID_ARG;
     if (B < 1 || Hq < 1 || Hkv < 1 || Tq < 0 || Tk < 0 || window < 0) return GDR_ERR_INVALID_ARG;
@@ -511,7 +513,7 @@ gdr_status gdr_attn_fwd_varlen(const void* q, const void* k, const void* v, void
                                float scale, uint32_t flags, void* stream) {
     const gdr_status st = attn_args(1, Hq, Hkv, T, T, d, window, scale, flags);
     if (st != GDR_OK) return st;
-    if (nseq < 1 || !cu_seqlens) return GDR_ERR_INVALID_ARG;
+    if (nseq < 1 || nseq > kMostSequences || !cu_seqlens) return GDR_ERR_INVALID_ARG;
     if (T > 0 && (!q || !o || !k || !v)) return GDR_ERR_INVALID_ARG;
     const void* ptrs[] = {q, k, v, o, lse, cu_seqlens};
     for (const void* ptr : ptrs)
@@ -547,7 +549,7 @@ gdr_status gdr_attn_bwd_varlen(const void* q, const void* k, const void* v, cons
                                size_t workspace_bytes, void* stream) {
     const gdr_status st = attn_args(1, Hq, Hkv, T, T, d, window, scale, flags);
     if (st != GDR_OK) return st;
-    if (nseq < 1 || !cu_seqlens || !aligned16(cu_seqlens)) return GDR_ERR_INVALID_ARG;
+    if (nseq < 1 || nseq > kMostSequences || !cu_seqlens || !aligned16(cu_seqlens)) return GDR_ERR_INVALID_ARG;
     if (T > 0 && (!q || !k || !v || !o || !lse || !dO || !dq || !dk || !dv)) return GDR_ERR_INVALID_ARG;
     return attn_bwd_run(q, k, v, o, lse, dO, dq, dk, dv, cu_seqlens, nseq, 1, Hq, Hkv, T, T, d, window, scale, flags,
                         workspace, workspace_bytes, stream);

@@ -467,7 +467,7 @@ gdr_status gdr_attn_fwd(const void* q, const void* k, const void* v, void* o, fl
  * The same over packed sequences, as gdr_chunk_fwd_varlen packs them: q, o
  * [Hq, T, d], k, v [Hkv, T, d], lse [Hq, T]; a query sees keys of its own
  * sequence only.  cu_seqlens: int32 [nseq + 1] in device memory, non-decreasing
- * from 0; rows from cu_seqlens[nseq] on (if it is below T) are not written.
+ * from 0 (nseq at most 2^30); rows from cu_seqlens[nseq] on (if it is below T) are not written.
  */
 gdr_status gdr_attn_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* lse,
                                const int* cu_seqlens, int nseq, int Hq, int Hkv, int T, int d,

@@ -64,7 +64,7 @@ FWDV_OK = dict(q=A, k=A, v=A, o=A, lse=A, cu=A, nseq=2, Hq=4, Hkv=2, T=8, d=64, 
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(cu=None), INVALID), (dict(cu=MIS), INVALID), (dict(nseq=0), INVALID), (dict(q=None), INVALID),
+    (dict(cu=None), INVALID), (dict(cu=MIS), INVALID), (dict(nseq=0), INVALID), (dict(nseq=(1 << 30) + 1), INVALID), (dict(q=None), INVALID),
     (dict(T=-1), INVALID), (dict(d=16), UNSUPPORTED), (dict(flags=0x1), UNSUPPORTED), (dict(Hq=5), INVALID),
 ])
 def test_attn_fwd_varlen_refusals(kw, status):
@@ -88,7 +88,7 @@ BWDV = "q k v o lse dO dq dk dv cu nseq Hq Hkv T d window scale flags ws nbytes"
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(cu=None), INVALID), (dict(cu=MIS), INVALID), (dict(nseq=0), INVALID), (dict(dk=None), INVALID),
+    (dict(cu=None), INVALID), (dict(cu=MIS), INVALID), (dict(nseq=0), INVALID), (dict(nseq=(1 << 30) + 1), INVALID), (dict(dk=None), INVALID),
     (dict(nbytes=0), WORKSPACE), (dict(d=48), UNSUPPORTED),
 ])
 def test_attn_bwd_varlen_refusals(kw, status):
