@@ -88,7 +88,7 @@ gdr::AttnParams attn_params(const void* q, const void* k, const void* v, int B, 
     p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.Tq = Tq; p.Tk = Tk; p.d = d;
     // a window that reaches behind the first key is none
     p.window = window < Tk ? window : 0;
-    p.scale = scale; p.splits = 1; p.split_steps = 0;
+    p.scale = scale; p.splits = 1; p.few = false; p.split_steps = 0;
     p.sq = attn_strides(Hq, Tq, d, (flags & GDR_TOKEN_MAJOR) != 0);
     p.sk = attn_strides(Hkv, Tk, d, (flags & GDR_TOKEN_MAJOR) != 0);
     return p;

@@ -276,6 +276,32 @@ def test_both_layouts_give_the_same_bits():
     assert all(torch.equal(gt[n].transpose(1, 2), g[n]) for n in g)
 
 
+@pytest.mark.parametrize("window,cu,d", [(2, None, 128), (3, None, 64), (32, None, 128), (0, list(range(0, 301, 3)), 128)])
+def test_gradients_of_rows_with_few_keys(window, cu, d):
+    """dO v - D is a small difference where few keys share the weight: dq and dk are no
+    further off than the roundings of dS and of the result leave them: each at most
+    2^-8 of a value, as if uniform below that, and the two independent."""
+    x = _inputs(1, 4, 2, 300, 300, d, window + 7)
+    o, lse = _check(x, window, cu)
+    got = _backward(x, o, lse, window, cu)
+    y = {n: t.to(F64) for n, t in x.items()}
+    heads = lambda t: t.repeat_interleave(2, 1)  # noqa: E731
+    q, k, v = (y[n].requires_grad_() for n in ("q", "k", "v"))
+    s = torch.matmul(q, heads(k).transpose(-1, -2)) * d ** -0.5
+    i, j = torch.arange(300, device=s.device)[:, None], torch.arange(300, device=s.device)[None]
+    seen = j <= i
+    if window:
+        seen = seen & (j > i - window)
+    if cu:
+        seen = seen & (i // 3 == j // 3)
+    p = torch.softmax(s.masked_fill(~seen, -math.inf), -1)
+    (torch.matmul(p, heads(v)) * y["dO"]).sum().backward()
+    for n, t in (("dq", q), ("dk", k)):
+        g = _back(got[n], cu is not None, False).to(t.grad.device)
+        off = float((g.to(F64) - t.grad).norm() / t.grad.norm())
+        assert off <= 2 ** -8 / math.sqrt(3) * math.sqrt(2), (n, off)
+
+
 @pytest.mark.parametrize("Tq,Tk,Hq,Hkv,d,window", [(2047, 2047, 4, 1, 128, 0), (2500, 2500, 2, 2, 64, 0), (700, 2300, 4, 2, 64, 0),
                                                    (2300, 700, 4, 2, 64, 0), (1500, 1500, 8, 1, 128, 300)])
 def test_splits_over_many_key_tiles(Tq, Tk, Hq, Hkv, d, window):
