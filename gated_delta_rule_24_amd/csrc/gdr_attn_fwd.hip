@@ -191,10 +191,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_kernel(AttnParams p, 
             top = max_across32(top);
             // m follows the maximum only when that is more than 2^8 ahead: weights up to
             // 2^8 keep their relative precision, and the sums their room, while some row
-            // of 32 has a new maximum in most tiles (64 products to rescale o)
-            if (__any((top - m) * to2 > 8.f)) {
+            // of 32 has a new maximum in most tiles (64 products to rescale o).  Each row
+            // goes by its own maximum, the others' factor is 1: the roundings of a row
+            // do not depend on keys that only its neighbours see
+            const bool ahead = (top - m) * to2 > 8.f;
+            if (__any(ahead)) {
                 asm volatile("");                         // a branch, not 64 products and selects
-                top = fmaxf(top, m);
+                top = ahead ? top : m;
                 const float fade = m == top ? 1.f : __builtin_amdgcn_exp2f((m - top) * to2);
                 m = top;
                 shift = top == -INFINITY ? 0.f : top * to2;

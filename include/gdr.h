@@ -449,7 +449,11 @@ gdr_status gdr_rope(const void* q, const void* k, void* q_out, void* k_out,
  * Tk keys and sees the keys up to it, the last `window` of them when window > 0:
  *   s_ij = scale q_i . k_j,  lse_i = log sum_j exp(s_ij),  o_i = sum_j exp(s_ij - lse_i) v_j.
  * A query that sees no key (Tk < Tq) gets o = 0 and lse = -inf.  A key or value
- * that a query does not see has no effect on it, NaN and infinities included.
+ * that a query does not see has no effect on it, not on one bit when it is finite.
+ * NaN and infinities reach only the queries that see them as well: where a tile of 64
+ * keys that some query sees in part holds one among its values, the tile's 128 queries
+ * are computed one by one, which is many times slower and rounds otherwise (the
+ * weights stay fp32).
  *
  *   q, o : bf16 [B, Hq, Tq, d]      k, v : bf16 [B, Hkv, Tk, d]
  *   lse  : fp32 [B, Hq, Tq] in both layouts, written; NULL means not written
