@@ -36,6 +36,14 @@ __device__ __forceinline__ void zero16(float16v& x) {
     for (int j = 0; j < 16; ++j) x[j] = 0.f;
 }
 
+// A weight times dO v - D, 0 where the weight is 0, as that of every masked pair is.
+// dO v may have overflowed there (values near the type's largest are finite
+// themselves), and 0 times infinity would reach the gradients of rows that do not see
+// each other.  One instruction, as the plain product: the one for which 0 times
+// anything is 0 (the intrinsic by its name, as there is no builtin for it).
+__device__ float multiply_zero_wins(float, float) __asm("llvm.amdgcn.fmul.legacy");
+__device__ __forceinline__ float weighted(float weight, float x) { return multiply_zero_wins(weight, x); }
+
 // four consecutive channels of a gradient row
 __device__ __forceinline__ void store4(uint16_t* at, const float16v& x, int j, float by) {
     *reinterpret_cast<uint2*>(at) = make_uint2(pack_bf16(x[4 * j] * by, x[4 * j + 1] * by),
@@ -270,7 +278,7 @@ __device__ __forceinline__ void query_side(const AttnParams& p, int item, int ti
             auto weights = [&](int half, int i) { st[half][i] = here(__builtin_amdgcn_exp2f(st[half][i] * to2 - lse2)); };
             auto gradient = [&](int half, int i) {    // a pair at a time, packed
                 if (i % 2 == 0) return;
-                const float x = st[half][i - 1] * (dp[half][i - 1] - delta), y = st[half][i] * (dp[half][i] - delta);
+                const float x = weighted(st[half][i - 1], dp[half][i - 1] - delta), y = weighted(st[half][i], dp[half][i] - delta);
                 const uint32_t u = here(pack_bf16(x, y));
                 const bf2v pair = __builtin_bit_cast(bf2v, u);
                 ds[2 * half + i / 8][i % 8 - 1] = pair[0];
@@ -686,7 +694,7 @@ __device__ __forceinline__ void key_side(const AttnParams& p, int item, int tile
                 if ((t + 1) * PER % 4 == 0 && (t + 1) * PER < 16) d4[(t + 1) * PER / 4] = *reinterpret_cast<const float4v*>(delta_at + 2 * (t + 1) * PER);
                 dv[t % DB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(c[t], pf[t / DB], dv[t % DB], 0, 0, 0);
 #pragma unroll
-                for (int i = t * PER; i < (t + 1) * PER; ++i) ds[i / 8][i % 8] = (__bf16)(st[i] * (dp[i] - d4[i / 4][i % 4]));
+                for (int i = t * PER; i < (t + 1) * PER; ++i) ds[i / 8][i % 8] = (__bf16)weighted(st[i], dp[i] - d4[i / 4][i % 4]);
                 fixed();
             }
             // dk

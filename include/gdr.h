@@ -489,7 +489,9 @@ gdr_status gdr_attn_fwd_varlen(const void* q, const void* k, const void* v, void
  *        keys that no query sees get 0)
  *   workspace : device scratch of at least gdr_attn_bwd_workspace_bytes() bytes,
  *        contents on entry ignored; calls that may overlap need one each
- * Sums are fp32; P and dS are rounded to bf16 as operands.  Supported as
+ * Sums are fp32; P and dS are rounded to bf16 as operands.  A pair that is not
+ * seen has no effect on a gradient, as in the forward (finite values near the
+ * type's largest, whose products overflow, included).  Supported as
  * gdr_attn_fwd.  The varlen call leaves rows from cu_seqlens[nseq] on unwritten.
  */
 size_t gdr_attn_bwd_workspace_bytes(int B, int Hq, int Hkv, int Tq, int Tk, int d);
