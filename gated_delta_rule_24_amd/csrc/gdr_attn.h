@@ -50,7 +50,7 @@ struct AttnParams {
     int window;                 // 0: none
     int splits;                 // backward: workgroups a key tile's queries (of every head that shares it) are dealt to,
                                 // at most
-    bool few;                   // backward: rows of few keys may be many (see attn_delta_kernel)
+    bool few;                   // backward: any row may be one of few keys (see attn_delta_kernel)
     int split_steps;            // backward: steps of one of them; 0: every tile has `splits`
     float scale;
     AttnStrides sq, sk;         // queries' tensors (q, o, dO, dq); keys' tensors (k, v, dk, dv)

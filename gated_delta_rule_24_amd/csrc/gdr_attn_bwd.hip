@@ -56,25 +56,97 @@ __device__ __forceinline__ void store4(uint16_t* at, const float16v& x, int j, f
 // saw nothing has lse -inf: +inf makes its weights exp2(-inf) = 0.
 //
 // dO.o carries o's rounding to bf16, up to 2^-8 of it.  Where few keys share the weight, dO v - D
-// is a small difference of such numbers, and dq and dk come out up to 3 times as far off
-// as their own roundings leave them.  So a row of at most kFew keys takes D = sum_j P_ij dO.v_j
-// from the keys themselves, in fp32; with more keys o is the smaller the more they are.
-// Its reads one after the other cost 11 us (2,047 tokens: 92 -> 103 us a call), so it is
-// done where such rows may be a good part: a window of at most kFew, at most 256 keys, or
-// packed sequences.  dq and dk of 300 tokens are 0.24% off with a window
-// of 2 and with none, which the roundings of dS and of the result account for.
+// is a small difference of such numbers, and dq and dk come out many times as far off as
+// their own roundings leave them.  So a row of at most kFew keys takes D = sum_j P_ij dO.v_j
+// from the keys themselves, in fp32, in calls of every size; with more keys o is the
+// smaller the more they are.  The rows behind a call's start that are such rows are one
+// tile of 32 queries and 32 keys of each head, which the grid's first blocks take, a block
+// a head (16 heads x 257 tokens 32.4 -> 34.1 us a call, 2,047 tokens 92.6 -> 92.9).  Where any
+// row may be one (a window of at most kFew, packed sequences: p.few), the row's own lanes
+// go over its keys, 8 at a time.
 // (Where its weights do not sum to 1, o and lse are not what the forward made of these
 // keys, infinities among them say; then o counts.)
 constexpr int kFew = 32;
 
+__device__ __forceinline__ float few_or_all(float direct, float whole, float all) {
+    return fabsf(whole - 1.f) < 1e-4f && fabsf(direct) < INFINITY ? direct : all;
+}
+
+__device__ __forceinline__ void put_delta(const AttnParams& p, long long row, float delta, float lse) {
+    p.delta[row] = lse == -INFINITY ? 0.f : delta;
+    p.delta[(long long)p.B * p.Hq * p.Tq + row] = lse == -INFINITY ? INFINITY : lse * kLog2e;
+}
+
+// Queries first .. first + count - 1 of one head, which see keys 0 .. 31 or fewer: scores
+// and dO v as one 32 x 32 product each (S^T[key][query], as the query side's), rows and keys
+// past the last held at it.  The block's four waves take a quarter of the channels each, so
+// that all of it is one trip to memory, and the first sums them.
+struct __attribute__((aligned(16))) FirstRows {
+    float4v st[3][4][64], dp[3][4][64];
+    float all[3][64];
+};
+
 template <int D>
-__global__ __launch_bounds__(256) void attn_delta_kernel(AttnParams p) {
+__device__ __forceinline__ void first_rows_delta(const AttnParams& p, FirstRows& sm, int b, int hq, int first, int count) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int col = lane & 31, h = lane >> 5, t = first + min(col, count - 1);
+    const long long at = b * p.sq.b + hq * p.sq.h + t * p.sq.t + D / 4 * wave + 8 * h;
+    const long long to = b * p.sk.b + hq / (p.Hq / p.Hkv) * p.sk.h + (long long)min(col, p.Tk - 1) * p.sk.t + D / 4 * wave + 8 * h;
+    const long long row = ((long long)b * p.Hq + hq) * p.Tq + t;
+    const float lse = p.lse[row];
+    auto load = [](const void* x, long long i) { return __builtin_bit_cast(bf8v, *reinterpret_cast<const uint4*>((const uint16_t*)x + i)); };
+    float16v st, dp;
+    zero16(st);
+    zero16(dp);
+    float all = 0.f;
+#pragma unroll
+    for (int s = 0; s < D / 64; ++s) {
+        const bf8v g = load(p.dO, at + 16 * s), x = load(p.o, at + 16 * s);
+        st = __builtin_amdgcn_mfma_f32_32x32x16_bf16(load(p.k, to + 16 * s), load(p.q, at + 16 * s), st, 0, 0, 0);
+        dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(load(p.v, to + 16 * s), g, dp, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) all += (float)x[j] * (float)g[j];
+    }
+    if (wave) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            sm.st[wave - 1][i][lane] = float4v{st[4 * i], st[4 * i + 1], st[4 * i + 2], st[4 * i + 3]};
+            sm.dp[wave - 1][i][lane] = float4v{dp[4 * i], dp[4 * i + 1], dp[4 * i + 2], dp[4 * i + 3]};
+        }
+        sm.all[wave - 1][lane] = all;
+    }
+    __syncthreads();
+    if (wave) return;
+    float direct = 0.f, whole = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        float x = st[i], y = dp[i];
+#pragma unroll
+        for (int w = 0; w < 3; ++w) { x += sm.st[w][i / 4][lane][i % 4]; y += sm.dp[w][i / 4][lane][i % 4]; }
+        if (8 * (i / 4) + 4 * h + i % 4 <= t + p.Tk - p.Tq) {
+            const float w = __builtin_amdgcn_exp2f((x * p.scale - lse) * kLog2e);
+            direct += w * y;
+            whole += w;
+        }
+    }
+#pragma unroll
+    for (int w = 0; w < 3; ++w) all += sm.all[w][lane];
+    const float sum = few_or_all(sum_across32(direct), sum_across32(whole), sum_across32(all));
+    if (h == 0 && col < count) put_delta(p, row, sum, lse);
+}
+
+// `first`, `count`: the queries that the grid's first `heads` blocks take, a block a head.
+template <int D>
+__global__ __launch_bounds__(256, 4) void attn_delta_kernel(AttnParams p, int first, int count, int heads) {
     constexpr int L = D / 8;
-    const long long row = (long long)blockIdx.x * (256 / L) + threadIdx.x / L, all = (long long)p.B * p.Hq * p.Tq;
+    __shared__ FirstRows sm;
+    if (blockIdx.x < (unsigned)heads) return first_rows_delta<D>(p, sm, blockIdx.x / p.Hq, blockIdx.x % p.Hq, first, count);
+    const long long row = (long long)(blockIdx.x - heads) * (256 / L) + threadIdx.x / L, all = (long long)p.B * p.Hq * p.Tq;
     if (row >= all) return;
     const int c = threadIdx.x % L;
     const long long bh = row / p.Tq;
     const int t = (int)(row % p.Tq), b = (int)(bh / p.Hq), hq = (int)(bh % p.Hq);
+    if ((unsigned)(t - first) < (unsigned)count) return;
     const long long at = b * p.sq.b + hq * p.sq.h + t * p.sq.t + 8 * c;
     const bf8v x = __builtin_bit_cast(bf8v, *reinterpret_cast<const uint4*>((const uint16_t*)p.o + at));
     const bf8v y = __builtin_bit_cast(bf8v, *reinterpret_cast<const uint4*>((const uint16_t*)p.dO + at));
@@ -123,12 +195,9 @@ __global__ __launch_bounds__(256) void attn_delta_kernel(AttnParams p) {
                 }
             }
         }
-        if (fabsf(whole - 1.f) < 1e-4f && fabsf(direct) < INFINITY) sum = direct;
+        sum = few_or_all(direct, whole, sum);
     }
-    if (c == 0) {
-        p.delta[row] = lse == -INFINITY ? 0.f : sum;
-        p.delta[all + row] = lse == -INFINITY ? INFINITY : lse * kLog2e;
-    }
+    if (c == 0) put_delta(p, row, sum, lse);
 }
 
 // ---------------------------------------------------------------------------
@@ -803,14 +872,18 @@ int attn_bwd_splits_most(int splits, int Tk) {
 
 template <int D>
 static hipError_t launch_bwd_d(AttnParams p, hipStream_t st) {
-    p.few = p.cu_seqlens || (p.window > 0 && p.window <= kFew) || p.Tk <= 256;
     static std::atomic<unsigned long long> done{0};
     constexpr size_t kLds = sizeof(DqSmem<D>) > sizeof(DkvSmem<D>) ? sizeof(DqSmem<D>) : sizeof(DkvSmem<D>);
     hipError_t e = ensure_dyn_lds(reinterpret_cast<const void*>(&attn_bwd_kernel<D>), (int)kLds, done);
     if (e != hipSuccess) return e;
     const long long rows = (long long)p.B * p.Hq * p.Tq, per = 2048 / D;
     if (rows > 0) {
-        hipLaunchKernelGGL((attn_delta_kernel<D>), dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, st, p);
+        // the queries of each head that see 1 to kFew keys, all of them from the first
+        p.few = p.cu_seqlens || (p.window > 0 && p.window <= kFew);
+        const int off = p.Tk - p.Tq, first = off < 0 ? -off : 0, behind = p.Tq < kFew - off ? p.Tq : kFew - off;
+        const int count = p.few || behind <= first ? 0 : behind - first, heads = count > 0 ? p.B * p.Hq : 0;
+        hipLaunchKernelGGL((attn_delta_kernel<D>), dim3((unsigned)(heads + (rows + per - 1) / per)), dim3(256), 0, st, p,
+                           first, count, heads);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }

@@ -480,7 +480,7 @@ gdr_status gdr_attn_fwd_varlen(const void* q, const void* k, const void* v, void
 /*
  * Gradients of gdr_attn_fwd for the loss <dO, o>: the probabilities are
  * recomputed from lse, P = exp(s - lse), and
- *   D_i = dO_i . o_i,  dS_ij = P_ij (dO_i . v_j - D_i),
+ *   D_i = sum_j P_ij dO_i . v_j = dO_i . o_i,  dS_ij = P_ij (dO_i . v_j - D_i),
  *   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i P_ij dO_i,
  * dk and dv summed over the query heads that share the key head, in a fixed order.
  *
@@ -489,7 +489,9 @@ gdr_status gdr_attn_fwd_varlen(const void* q, const void* k, const void* v, void
  *        keys that no query sees get 0)
  *   workspace : device scratch of at least gdr_attn_bwd_workspace_bytes() bytes,
  *        contents on entry ignored; calls that may overlap need one each
- * Sums are fp32; P and dS are rounded to bf16 as operands.  A pair that is not
+ * Sums are fp32; P and dS are rounded to bf16 as operands.  D is formed from the
+ * keys for queries that see at most 32 of them (there o's rounding would show in dq
+ * and dk), from o for the others.  A pair that is not
  * seen has no effect on a gradient, as in the forward (finite values near the
  * type's largest, whose products overflow, included).  Supported as
  * gdr_attn_fwd.  The varlen call leaves rows from cu_seqlens[nseq] on unwritten.
