@@ -187,6 +187,18 @@ def _check(fn, st):
         raise GdrError(fn, st)
 
 
+def _window(window):
+    """A window as the library counts it, in 32 bits (ctypes would keep the low ones without
+    a word): one past every length is none, one below 0 stays invalid."""
+    return window if -1 < window < 1 << 31 else 0 if window > 0 else -1
+
+
+def _position(position0):
+    if not -(1 << 31) <= position0 < 1 << 31:
+        raise ValueError(f"position0 must fit 32 bits, got {position0}")
+    return position0
+
+
 # ---------------------------------------------------------------------------
 # C-named entry points (outputs provided by the caller)
 # ---------------------------------------------------------------------------
@@ -305,20 +317,20 @@ def gdr_mixer_epilogue_bwd(o, g, norm_weight, dy, d_o, dg, dnorm_weight, B, H, T
 
 def gdr_rope(q, k, q_out, k_out, inv_freq, positions, position0, B, Hq, Hk, T, d, rot_dim, scale, flags,
              stream=None):
-    st = _load().gdr_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(inv_freq), _ptr(positions), position0,
-                          B, Hq, Hk, T, d, rot_dim, scale, flags, _stream(stream))
+    st = _load().gdr_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(inv_freq), _ptr(positions),
+                          _position(position0), B, Hq, Hk, T, d, rot_dim, scale, flags, _stream(stream))
     _check("gdr_rope", st)
 
 
 def gdr_attn_fwd(q, k, v, o, lse, B, Hq, Hkv, Tq, Tk, d, window, scale, flags, stream=None):
-    st = _load().gdr_attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, Hq, Hkv, Tq, Tk, d, window, scale,
-                              flags, _stream(stream))
+    st = _load().gdr_attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, Hq, Hkv, Tq, Tk, d,
+                              _window(window), scale, flags, _stream(stream))
     _check("gdr_attn_fwd", st)
 
 
 def gdr_attn_fwd_varlen(q, k, v, o, lse, cu_seqlens, nseq, Hq, Hkv, T, d, window, scale, flags, stream=None):
     st = _load().gdr_attn_fwd_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(cu_seqlens), nseq, Hq,
-                                     Hkv, T, d, window, scale, flags, _stream(stream))
+                                     Hkv, T, d, _window(window), scale, flags, _stream(stream))
     _check("gdr_attn_fwd_varlen", st)
 
 
@@ -328,15 +340,15 @@ def gdr_attn_bwd_workspace_bytes(B, Hq, Hkv, Tq, Tk, d) -> int:
 
 def gdr_attn_bwd(q, k, v, o, lse, dO, dq, dk, dv, B, Hq, Hkv, Tq, Tk, d, window, scale, flags, workspace,
                  workspace_bytes, stream=None):
-    st = _load().gdr_attn_bwd(*[_ptr(x) for x in (q, k, v, o, lse, dO, dq, dk, dv)], B, Hq, Hkv, Tq, Tk, d, window,
-                              scale, flags, _ptr(workspace), workspace_bytes, _stream(stream))
+    st = _load().gdr_attn_bwd(*[_ptr(x) for x in (q, k, v, o, lse, dO, dq, dk, dv)], B, Hq, Hkv, Tq, Tk, d,
+                              _window(window), scale, flags, _ptr(workspace), workspace_bytes, _stream(stream))
     _check("gdr_attn_bwd", st)
 
 
 def gdr_attn_bwd_varlen(q, k, v, o, lse, dO, dq, dk, dv, cu_seqlens, nseq, Hq, Hkv, T, d, window, scale, flags,
                         workspace, workspace_bytes, stream=None):
     st = _load().gdr_attn_bwd_varlen(*[_ptr(x) for x in (q, k, v, o, lse, dO, dq, dk, dv, cu_seqlens)], nseq, Hq,
-                                     Hkv, T, d, window, scale, flags, _ptr(workspace), workspace_bytes,
+                                     Hkv, T, d, _window(window), scale, flags, _ptr(workspace), workspace_bytes,
                                      _stream(stream))
     _check("gdr_attn_bwd_varlen", st)
 
@@ -350,13 +362,13 @@ def gdr_kv_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cache_l
 
 
 def gdr_attn_decode_workspace_bytes(N, Hq, Hkv, d, max_pages, window) -> int:
-    return int(_load().gdr_attn_decode_workspace_bytes(N, Hq, Hkv, d, max_pages, window))
+    return int(_load().gdr_attn_decode_workspace_bytes(N, Hq, Hkv, d, max_pages, _window(window)))
 
 
 def gdr_attn_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_len, o, N, Hq, Hkv, d, n_pages,
                     max_pages, window, scale, flags, workspace=None, workspace_bytes=0, stream=None):
     st = _load().gdr_attn_decode(*[_ptr(x) for x in (q, k_cache, v_cache, k_scale, v_scale, block_table, cache_len,
-                                                     o)], N, Hq, Hkv, d, n_pages, max_pages, window, scale, flags,
+                                                     o)], N, Hq, Hkv, d, n_pages, max_pages, _window(window), scale, flags,
                                  _ptr(workspace), workspace_bytes, _stream(stream))
     _check("gdr_attn_decode", st)
 
@@ -684,7 +696,7 @@ def rope(q, k, inv_freq, positions=None, position0: int = 0, interleaved: bool =
         _expect("positions", positions, lead + (T,), torch.int32, gpu)
         positions = positions.data_ptr()
     _launch("gdr_rope", gpu, stream, q.data_ptr(), k_ptr, q_out.data_ptr(), ko_ptr, inv_freq.data_ptr(), positions,
-            position0, B, Hq, Hk, T, d, 2 * half, scale, flags)
+            _position(position0), B, Hq, Hk, T, d, 2 * half, scale, flags)
     _kept_for(stream, made_q, made_k)
     return q_out, k_out if k is not None else None
 
@@ -713,7 +725,7 @@ def attn_fwd(q, k, v, window: int = 0, scale: Optional[float] = None, token_majo
     o = torch.empty_like(q)
     lse = torch.empty((B, Hq, Tq), dtype=torch.float32, device=q.device) if return_lse else None
     _launch("gdr_attn_fwd", gpu, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-            lse.data_ptr() if return_lse else None, B, Hq, Hkv, Tq, Tk, d, window,
+            lse.data_ptr() if return_lse else None, B, Hq, Hkv, Tq, Tk, d, _window(window),
             d ** -0.5 if scale is None else scale, GDR_TOKEN_MAJOR if token_major else 0)
     _kept_for(stream, o, lse)
     return o, lse
@@ -732,7 +744,7 @@ def attn_fwd_varlen(q, k, v, cu_seqlens, window: int = 0, scale: Optional[float]
     o = torch.empty_like(q)
     lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device) if return_lse else None
     _launch("gdr_attn_fwd_varlen", gpu, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-            lse.data_ptr() if return_lse else None, cu_seqlens.data_ptr(), nseq, Hq, Hkv, T, d, window,
+            lse.data_ptr() if return_lse else None, cu_seqlens.data_ptr(), nseq, Hq, Hkv, T, d, _window(window),
             d ** -0.5 if scale is None else scale, GDR_TOKEN_MAJOR if token_major else 0)
     _kept_for(stream, o, lse)
     return o, lse
@@ -752,7 +764,7 @@ def _attn_bwd(q, k, v, o, lse, dO, cu_seqlens, window, scale, token_major, strea
     nbytes = gdr_attn_bwd_workspace_bytes(B, Hq, Hkv, Tq, Tk, d)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes > 0 else None
     ptrs = [t.data_ptr() for t in (q, k, v, o, lse, dO, dq, dk, dv)]
-    tail = (d, window, scale, flags, ws.data_ptr() if nbytes > 0 else None, nbytes)
+    tail = (d, _window(window), scale, flags, ws.data_ptr() if nbytes > 0 else None, nbytes)
     if packed:
         nseq = cu_seqlens.numel() - 1
         _expect("cu_seqlens", cu_seqlens, (nseq + 1,), torch.int32, gpu)
@@ -860,7 +872,7 @@ def attn_decode(q, cache: KVCache, block_table, cache_len, window: int = 0, scal
     if nbytes > 0:
         ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
     _launch("gdr_attn_decode", gpu, stream, q.data_ptr(), *[t.data_ptr() for t in cache], block_table.data_ptr(),
-            cache_len.data_ptr(), o.data_ptr(), N, Hq, Hkv, d, n_pages, max_pages, window,
+            cache_len.data_ptr(), o.data_ptr(), N, Hq, Hkv, d, n_pages, max_pages, _window(window),
             d ** -0.5 if scale is None else scale, GDR_OUT_BF16 if out_dtype is torch.bfloat16 else 0,
             None if ws is None else ws.data_ptr(), nbytes)
     _kept_for(stream, made, ws)
