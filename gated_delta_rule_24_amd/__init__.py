@@ -29,6 +29,8 @@ calls with outputs allocated for the caller.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import math
 import os
 from typing import NamedTuple, Optional
@@ -378,6 +380,33 @@ def gdr_attn_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_le
 # ---------------------------------------------------------------------------
 
 
+def _on_its_stream(fn):
+    """A call given a `stream` that is not the current one runs with it current, so that
+    its outputs and workspaces are allocated there: the allocator hands memory out in
+    the order of the stream it is asked on, and another one may still be writing it.
+    What is returned is kept for the caller's stream as well, which goes on with it.  That
+    the inputs are ready on `stream`, and the results before they are used elsewhere, is
+    the caller's to see to."""
+    at = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        stream = kw.get("stream") if len(args) <= at else args[at]
+        if stream is None:
+            return fn(*args, **kw)
+        caller = torch.cuda.current_stream(stream.device)
+        if stream == caller:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            out = fn(*args, **kw)
+        for t in (out,) if isinstance(out, torch.Tensor) else out.values() if isinstance(out, dict) else out:
+            if t is not None:
+                t.record_stream(caller)
+        return out
+    return call
+
+
+@_on_its_stream
 def chunk_fwd(q, k, v, log_alpha, b, w, S0=None, chunk: int = 64,
               out_dtype=torch.float32, return_state: bool = True, stream=None,
               generic: bool = False, path: str = "auto", gate_logits: bool = False):
@@ -411,6 +440,7 @@ def chunk_fwd(q, k, v, log_alpha, b, w, S0=None, chunk: int = 64,
     return o, Sf
 
 
+@_on_its_stream
 def chunk_fwd_varlen(q, k, v, log_alpha, b, w, cu_seqlens, S0=None, out_dtype=torch.float32,
                      return_state: bool = True, stream=None, gate_logits: bool = False):
     """Packed sequences: q, k: [H,T,dk]; v: [H,T,dv]; log_alpha, b: [H,T,dk] or
@@ -435,6 +465,7 @@ def chunk_fwd_varlen(q, k, v, log_alpha, b, w, cu_seqlens, S0=None, out_dtype=to
     return o, Sf
 
 
+@_on_its_stream
 def decode_step(q, k, v, log_alpha, b, w, S, out_dtype=torch.float32, o=None, stream=None,
                 gate_logits: bool = False):
     """One token per (n, h): q, k: [N,H,dk]; v: [N,H,dv]; gates channel or
@@ -450,6 +481,7 @@ def decode_step(q, k, v, log_alpha, b, w, S, out_dtype=torch.float32, o=None, st
     return o
 
 
+@_on_its_stream
 def chunk_bwd(q, k, v, log_alpha, b, w, S0, dO, dS_final=None, chunk: int = 64, stream=None,
               gate_logits: bool = False):
     """Gradients of L = <dO, o> + <dS_final, S_final>.  Returns a dict of fp32
@@ -475,6 +507,7 @@ def chunk_bwd(q, k, v, log_alpha, b, w, S0, dO, dS_final=None, chunk: int = 64, 
     return out
 
 
+@_on_its_stream
 def chunk_bwd_varlen(q, k, v, log_alpha, b, w, cu_seqlens, S0, dO, dS_final=None, stream=None,
                      gate_logits: bool = False):
     """Packed sequences ([H,T,...] streams, cu_seqlens int32 on the GPU): the
@@ -505,6 +538,7 @@ def chunk_bwd_varlen(q, k, v, log_alpha, b, w, cu_seqlens, S0, dO, dS_final=None
     return out
 
 
+@_on_its_stream
 def mixer_prologue(q_pre, k_pre, v_pre, conv_q, conv_k, conv_v, a_pre, b_pre, w_pre, stream=None,
                    gate_logits: bool = False):
     """[B,H,T,d] bf16 projection outputs (a_pre fp32; gate logits [B,H,T,d]
@@ -534,6 +568,7 @@ def mixer_prologue(q_pre, k_pre, v_pre, conv_q, conv_k, conv_v, a_pre, b_pre, w_
     return out
 
 
+@_on_its_stream
 def mixer_epilogue(o, g, norm_weight, stream=None):
     """o fp32 [B,H,T,dv], g bf16 [B,H,T,dv], norm_weight fp32 [dv] -> y bf16."""
     B, H, T, dv = o.shape
@@ -542,6 +577,7 @@ def mixer_epilogue(o, g, norm_weight, stream=None):
     return y
 
 
+@_on_its_stream
 def mixer_prologue_bwd(q_pre, k_pre, v_pre, conv_q, conv_k, conv_v, dq, dk, dv, stream=None):
     """Gradients of the prologue's q, k, v paths: dict dq_pre, dk_pre, dv_pre
     (fp32 [B,H,T,d]) and dconv_q, dconv_k, dconv_v (fp32 [H,d,4])."""
@@ -563,6 +599,7 @@ def mixer_prologue_bwd(q_pre, k_pre, v_pre, conv_q, conv_k, conv_v, dq, dk, dv, 
     return out
 
 
+@_on_its_stream
 def mixer_epilogue_bwd(o, g, norm_weight, dy, stream=None):
     """Gradients of the epilogue: dict d_o, dg (fp32 [B,H,T,dv]), dnorm_weight (fp32 [dv])."""
     B, H, T, dv_ = o.shape
@@ -616,15 +653,6 @@ def _launch(fn, gpu, stream, *args):
         raise GdrError(fn, st)
 
 
-def _kept_for(stream, *tensors):
-    """Tensors allocated here and used on another stream: the allocator must not
-    give their memory away before that stream is done with it."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
-
-
 def rope_frequencies(rot_dim, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
                      trained: int = 0, low: float = 1.0, high: float = 32.0, device="cuda"):
     """(inv_freq fp32 [rot_dim / 2], scale) for :func:`rope`: base^(-2i / rot_dim),
@@ -658,6 +686,7 @@ def rope_frequencies(rot_dim, base: float = 10000.0, scaling: Optional[str] = No
     return f.float().to(device), scale
 
 
+@_on_its_stream
 def rope(q, k, inv_freq, positions=None, position0: int = 0, interleaved: bool = False, inverse: bool = False,
          scale: float = 1.0, token_major: bool = False, q_out=None, k_out=None, stream=None):
     """Rotary positions.  q: [B,Hq,T,d], k: [B,Hk,T,d] or None, bf16 or fp32
@@ -675,19 +704,19 @@ def rope(q, k, inv_freq, positions=None, position0: int = 0, interleaved: bool =
     T, Hq = (shape[-3], shape[-2]) if token_major else (shape[-2], shape[-3])
     flags = _act_flag(q) | (GDR_TOKEN_MAJOR if token_major else 0) | (GDR_ROPE_INTERLEAVED if interleaved else 0) \
         | (GDR_ROPE_INVERSE if inverse else 0)
-    made_q = made_k = k_ptr = ko_ptr = None
+    k_ptr = ko_ptr = None
     Hk = 0
     _expect("q", q, shape, dtype, gpu)
     if k is not None:
         Hk = k.shape[-2 if token_major else -3]
         _expect("k", k, lead + ((T, Hk, d) if token_major else (Hk, T, d)), dtype, gpu)
         if k_out is None:
-            k_out = made_k = torch.empty_like(k)
+            k_out = torch.empty_like(k)
         else:
             _expect("k_out", k_out, k.shape, dtype, gpu)
         k_ptr, ko_ptr = k.data_ptr(), k_out.data_ptr()
     if q_out is None:
-        q_out = made_q = torch.empty_like(q)
+        q_out = torch.empty_like(q)
     else:
         _expect("q_out", q_out, shape, dtype, gpu)
     half = inv_freq.numel()
@@ -697,7 +726,6 @@ def rope(q, k, inv_freq, positions=None, position0: int = 0, interleaved: bool =
         positions = positions.data_ptr()
     _launch("gdr_rope", gpu, stream, q.data_ptr(), k_ptr, q_out.data_ptr(), ko_ptr, inv_freq.data_ptr(), positions,
             _position(position0), B, Hq, Hk, T, d, 2 * half, scale, flags)
-    _kept_for(stream, made_q, made_k)
     return q_out, k_out if k is not None else None
 
 
@@ -716,6 +744,7 @@ def _attn_shapes(q, k, v, packed, token_major):
     return B, Hq, Hkv, Tq, Tk, d, gpu
 
 
+@_on_its_stream
 def attn_fwd(q, k, v, window: int = 0, scale: Optional[float] = None, token_major: bool = False,
              return_lse: bool = True, stream=None):
     """Causal attention.  q: [B,Hq,Tq,d], k, v: [B,Hkv,Tk,d] bf16 (token_major:
@@ -727,10 +756,10 @@ def attn_fwd(q, k, v, window: int = 0, scale: Optional[float] = None, token_majo
     _launch("gdr_attn_fwd", gpu, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
             lse.data_ptr() if return_lse else None, B, Hq, Hkv, Tq, Tk, d, _window(window),
             d ** -0.5 if scale is None else scale, GDR_TOKEN_MAJOR if token_major else 0)
-    _kept_for(stream, o, lse)
     return o, lse
 
 
+@_on_its_stream
 def attn_fwd_varlen(q, k, v, cu_seqlens, window: int = 0, scale: Optional[float] = None,
                     token_major: bool = False, return_lse: bool = True, stream=None):
     """Packed sequences: q: [Hq,T,d], k, v: [Hkv,T,d] bf16 (token_major: [T,H,d]);
@@ -746,7 +775,6 @@ def attn_fwd_varlen(q, k, v, cu_seqlens, window: int = 0, scale: Optional[float]
     _launch("gdr_attn_fwd_varlen", gpu, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
             lse.data_ptr() if return_lse else None, cu_seqlens.data_ptr(), nseq, Hq, Hkv, T, d, _window(window),
             d ** -0.5 if scale is None else scale, GDR_TOKEN_MAJOR if token_major else 0)
-    _kept_for(stream, o, lse)
     return o, lse
 
 
@@ -771,10 +799,10 @@ def _attn_bwd(q, k, v, o, lse, dO, cu_seqlens, window, scale, token_major, strea
         _launch("gdr_attn_bwd_varlen", gpu, stream, *ptrs, cu_seqlens.data_ptr(), nseq, Hq, Hkv, Tq, *tail)
     else:
         _launch("gdr_attn_bwd", gpu, stream, *ptrs, B, Hq, Hkv, Tq, Tk, *tail)
-    _kept_for(stream, dq, dk, dv, ws)
     return dict(dq=dq, dk=dk, dv=dv)
 
 
+@_on_its_stream
 def attn_bwd(q, k, v, o, lse, dO, window: int = 0, scale: Optional[float] = None, token_major: bool = False,
              stream=None):
     """Gradients of <dO, o>: dict dq, dk, dv (bf16, as q, k, v), from what
@@ -782,6 +810,7 @@ def attn_bwd(q, k, v, o, lse, dO, window: int = 0, scale: Optional[float] = None
     return _attn_bwd(q, k, v, o, lse, dO, None, window, scale, token_major, stream)
 
 
+@_on_its_stream
 def attn_bwd_varlen(q, k, v, o, lse, dO, cu_seqlens, window: int = 0, scale: Optional[float] = None,
                     token_major: bool = False, stream=None):
     """The same for :func:`attn_fwd_varlen`."""
@@ -849,6 +878,7 @@ def kv_append(k, v, cache: KVCache, block_table, cache_len, cu_seqlens=None, tok
             GDR_TOKEN_MAJOR if token_major else 0)
 
 
+@_on_its_stream
 def attn_decode(q, cache: KVCache, block_table, cache_len, window: int = 0, scale: Optional[float] = None,
                 out_dtype=torch.float32, o=None, stream=None):
     """Attention of one token per sequence over the cache: q bf16 [N,Hq,d], the
@@ -863,9 +893,9 @@ def attn_decode(q, cache: KVCache, block_table, cache_len, window: int = 0, scal
     _expect("q", q, shape, torch.bfloat16, gpu)
     if out_dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"out_dtype must be float32 or bfloat16, got {out_dtype}")
-    made = ws = None
+    ws = None
     if o is None:
-        o = made = torch.empty(shape, dtype=out_dtype, device=q.device)
+        o = torch.empty(shape, dtype=out_dtype, device=q.device)
     else:
         _expect("o", o, shape, out_dtype, gpu)
     nbytes = gdr_attn_decode_workspace_bytes(N, Hq, Hkv, d, max_pages, window)
@@ -875,5 +905,4 @@ def attn_decode(q, cache: KVCache, block_table, cache_len, window: int = 0, scal
             cache_len.data_ptr(), o.data_ptr(), N, Hq, Hkv, d, n_pages, max_pages, _window(window),
             d ** -0.5 if scale is None else scale, GDR_OUT_BF16 if out_dtype is torch.bfloat16 else 0,
             None if ws is None else ws.data_ptr(), nbytes)
-    _kept_for(stream, made, ws)
     return o
