@@ -97,6 +97,17 @@ struct AttnDecodeParams {
 int attn_decode_splits(int N, int Hq, int Hkv, int max_pages, int window, int* split_pages);
 hipError_t launch_attn_decode(const AttnDecodeParams& p, hipStream_t st);
 
+// Index of the last of cu[0] .. cu[nseq] that is at most t, or 0.
+__host__ __device__ inline int last_at_most(const int* cu, int nseq, int t) {
+    int s = 0, z = nseq;
+    while (s < z) {
+        const int mid = s + (z - s + 1) / 2;       // (s + z may pass 32 bits)
+        if (cu[mid] <= t) s = mid;
+        else z = mid - 1;
+    }
+    return s;
+}
+
 // ---------------------------------------------------------------------------
 // device helpers
 // ---------------------------------------------------------------------------

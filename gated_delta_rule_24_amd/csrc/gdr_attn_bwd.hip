@@ -152,15 +152,8 @@ __global__ __launch_bounds__(256, 4) void attn_delta_kernel(AttnParams p, int fi
     const bf8v y = __builtin_bit_cast(bf8v, *reinterpret_cast<const uint4*>((const uint16_t*)p.dO + at));
     const float lse = p.lse[row];
     int lo = 0;
-    if (p.cu_seqlens) {                               // where the row's sequence starts
-        int s = 0, z = p.nseq;
-        while (s < z) {
-            const int mid = (s + z + 1) / 2;
-            if (p.cu_seqlens[mid] <= t) s = mid;
-            else z = mid - 1;
-        }
-        lo = max(min(p.cu_seqlens[s], t), 0);
-    }
+    // where the row's sequence starts
+    if (p.cu_seqlens) lo = max(min(p.cu_seqlens[last_at_most(p.cu_seqlens, p.nseq, t)], t), 0);
     const int end = t + p.Tk - p.Tq + 1;
     if (p.window > 0) lo = max(lo, end - p.window);
     float sum = 0.f;
