@@ -29,13 +29,6 @@ namespace gdr {
 
 using namespace attn;
 
-namespace {
-
-__device__ __forceinline__ void zero16(float16v& x) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) x[j] = 0.f;
-}
-
 // A weight times dO v - D, 0 where the weight is 0, as that of every masked pair is.
 // dO v may have overflowed there (values near the type's largest are finite
 // themselves), and 0 times infinity would reach the gradients of rows that do not see
@@ -43,6 +36,13 @@ __device__ __forceinline__ void zero16(float16v& x) {
 // anything is 0 (the intrinsic by its name, as there is no builtin for it).
 __device__ float multiply_zero_wins(float, float) __asm("llvm.amdgcn.fmul.legacy");
 __device__ __forceinline__ float weighted(float weight, float x) { return multiply_zero_wins(weight, x); }
+
+namespace {
+
+__device__ __forceinline__ void zero16(float16v& x) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) x[j] = 0.f;
+}
 
 // four consecutive channels of a gradient row
 __device__ __forceinline__ void store4(uint16_t* at, const float16v& x, int j, float by) {
