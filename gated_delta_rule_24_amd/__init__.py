@@ -25,6 +25,9 @@ and :func:`chunk_fwd`, :func:`decode_step`, :func:`chunk_bwd`,
 :func:`attn_fwd`, :func:`attn_bwd`, :func:`attn_fwd_varlen`,
 :func:`attn_bwd_varlen`, :func:`kv_append`, :func:`attn_decode` are the same
 calls with outputs allocated for the caller.
+
+Tensors are contiguous and start at a multiple of 16 bytes, int32 ones as well
+(a slice of a longer tensor may not).
 """
 from __future__ import annotations
 
@@ -62,10 +65,10 @@ _lib = None
 
 
 class GdrError(RuntimeError):
-    def __init__(self, fn: str, status: int):
+    def __init__(self, fn: str, status: int, why: str = ""):
         self.status = status
         msg = _load().gdr_status_string(status).decode() if _lib is not None else _STATUS.get(status)
-        super().__init__(f"{fn} failed with status {status} ({msg})")
+        super().__init__(f"{fn} failed with status {status} ({msg}{why and ': ' + why})")
 
 
 def _load():
@@ -647,10 +650,12 @@ def _launch(fn, gpu, stream, *args):
     if gpu != torch.cuda.current_device():
         with torch.cuda.device(gpu):
             return _launch(fn, gpu, stream, *args)
-    st = getattr(_lib or _load(), fn)(*args, torch._C._cuda_getCurrentRawStream(gpu) if stream is None
-                                      else stream.cuda_stream)
+    call = getattr(_lib or _load(), fn)
+    st = call(*args, torch._C._cuda_getCurrentRawStream(gpu) if stream is None else stream.cuda_stream)
     if st != 0:
-        raise GdrError(fn, st)
+        names = inspect.signature(globals()[fn]).parameters
+        off = [n for n, a, t in zip(names, args, call.argtypes) if t is ctypes.c_void_p and a and a % 16]
+        raise GdrError(fn, st, f"{', '.join(off)} must start at a multiple of 16 bytes (a slice may not)" if off else "")
 
 
 def rope_frequencies(rot_dim, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
