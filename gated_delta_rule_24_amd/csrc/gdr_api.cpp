@@ -61,6 +61,10 @@ bool attn_sizes_ok(int B, long long H, int T) {
     return H <= (1LL << 28) && (long long)B * H <= (1LL << 28) && (long long)B * H * (((long long)T + 15) / 16) <= (1LL << 31) - 1;
 }
 
+// A launch takes 2^32 - 1 threads along its first axis: so many workgroups of 256.
+constexpr long long kMostWorkgroups = (1LL << 24) - 1;
+bool grid_ok(long long workgroups) { return workgroups <= kMostWorkgroups; }
+
 constexpr int kMostSequences = 1 << 30;               // attention: the kernels number them in 32 bits
 
 gdr_status attn_args(int B, int Hq, int Hkv, int Tq, int Tk, int d, int window, float scale, uint32_t flags) {
@@ -73,7 +77,15 @@ gdr_status attn_args(int B, int Hq, int Hkv, int Tq, int Tk, int d, int window, 
     if (Tq > (1 << 30) || Tk > (1 << 30)) return GDR_ERR_INVALID_ARG;
     if (!attn_sizes_ok(B, Hq, Tq) || !attn_sizes_ok(B, Hq, Tk)) return GDR_ERR_INVALID_ARG;
     if ((d != 64 && d != 128) || (flags & GDR_ACT_F32)) return GDR_ERR_UNSUPPORTED;
+    if (!grid_ok(gdr::attn_fwd_workgroups(B, Hq, Tq))) return GDR_ERR_INVALID_ARG;
     return GDR_OK;
+}
+
+// of the backward as well
+gdr_status attn_bwd_args(int B, int Hq, int Hkv, int Tq, int Tk, int d, int window, float scale, uint32_t flags) {
+    const gdr_status st = attn_args(B, Hq, Hkv, Tq, Tk, d, window, scale, flags);
+    if (st == GDR_OK && !grid_ok(gdr::attn_bwd_workgroups(B, Hq, Hkv, Tq, Tk, d))) return GDR_ERR_INVALID_ARG;
+    return st;
 }
 
 gdr::AttnStrides attn_strides(int H, int T, int d, bool token_major) {
@@ -128,6 +140,7 @@ gdr_status decode_args(int N, int Hq, int Hkv, int d, int n_pages, int max_pages
     // (sequence, head) pairs and a sequence's tokens are numbered in 32 bits
     if ((long long)N * Hq > (1LL << 28) || max_pages > (1 << 24)) return GDR_ERR_INVALID_ARG;
     if (d != 64 && d != 128) return GDR_ERR_UNSUPPORTED;
+    if (!grid_ok(gdr::attn_decode_workgroups(N, Hq, Hkv))) return GDR_ERR_INVALID_ARG;
     return GDR_OK;
 }
 
@@ -479,6 +492,7 @@ gdr_status gdr_rope(const void* q, const void* k, void* q_out, void* k_out, cons
     if (rot_dim % 16 != 0) return GDR_ERR_UNSUPPORTED;
     if (!(scale - scale == 0.f)) return GDR_ERR_INVALID_ARG;   // infinite or NaN
     if (!attn_sizes_ok(B, (long long)Hq + Hk, T) || (long long)B * T > (1LL << 31) - 1) return GDR_ERR_INVALID_ARG;
+    if (!grid_ok(gdr::rope_workgroups((long long)B * T, d, flags))) return GDR_ERR_INVALID_ARG;
     if (T > 0 && (!inv_freq || (Hq > 0 && (!q || !q_out)) || (Hk > 0 && (!k || !k_out)))) return GDR_ERR_INVALID_ARG;
     const void* ptrs[] = {q, k, q_out, k_out, inv_freq, positions};
     for (const void* ptr : ptrs)
@@ -526,7 +540,7 @@ gdr_status gdr_attn_fwd_varlen(const void* q, const void* k, const void* v, void
 }
 
 size_t gdr_attn_bwd_workspace_bytes(int B, int Hq, int Hkv, int Tq, int Tk, int d) {
-    if (attn_args(B, Hq, Hkv, Tq, Tk, d, 0, 1.f, 0) != GDR_OK) return 0;
+    if (attn_bwd_args(B, Hq, Hkv, Tq, Tk, d, 0, 1.f, 0) != GDR_OK) return 0;
     const int splits = gdr::attn_bwd_splits(B, Hq, Hkv, Tq, Tk);
     const size_t part = splits > 1 ? 2 * (size_t)gdr::attn_bwd_splits_most(splits, Tk) * B * Hkv * Tk * d * sizeof(float) : 0;
     return attn_delta_bytes(B, Hq, Tq) + part;
@@ -535,7 +549,7 @@ size_t gdr_attn_bwd_workspace_bytes(int B, int Hq, int Hkv, int Tq, int Tk, int 
 gdr_status gdr_attn_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
                         void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int Tq, int Tk, int d, int window,
                         float scale, uint32_t flags, void* workspace, size_t workspace_bytes, void* stream) {
-    const gdr_status st = attn_args(B, Hq, Hkv, Tq, Tk, d, window, scale, flags);
+    const gdr_status st = attn_bwd_args(B, Hq, Hkv, Tq, Tk, d, window, scale, flags);
     if (st != GDR_OK) return st;
     if (Tq > 0 && (!q || !o || !lse || !dO || !dq)) return GDR_ERR_INVALID_ARG;
     if (Tk > 0 && (!k || !v || !dk || !dv)) return GDR_ERR_INVALID_ARG;
@@ -547,7 +561,7 @@ gdr_status gdr_attn_bwd_varlen(const void* q, const void* k, const void* v, cons
                                const void* dO, void* dq, void* dk, void* dv, const int* cu_seqlens, int nseq, int Hq,
                                int Hkv, int T, int d, int window, float scale, uint32_t flags, void* workspace,
                                size_t workspace_bytes, void* stream) {
-    const gdr_status st = attn_args(1, Hq, Hkv, T, T, d, window, scale, flags);
+    const gdr_status st = attn_bwd_args(1, Hq, Hkv, T, T, d, window, scale, flags);
     if (st != GDR_OK) return st;
     if (nseq < 1 || nseq > kMostSequences || !cu_seqlens || !aligned16(cu_seqlens)) return GDR_ERR_INVALID_ARG;
     if (T > 0 && (!q || !k || !v || !o || !lse || !dO || !dq || !dk || !dv)) return GDR_ERR_INVALID_ARG;
@@ -562,9 +576,9 @@ gdr_status gdr_kv_append(const void* k, const void* v, void* k_cache, void* v_ca
     if (nseq < 1 || Hkv < 1 || T < 0 || n_pages < 1 || max_pages < 1) return GDR_ERR_INVALID_ARG;
     if (!cu_seqlens && T != nseq) return GDR_ERR_INVALID_ARG;
     if (d != 64 && d != 128) return GDR_ERR_UNSUPPORTED;
-    // pages and (sequence, head) pairs of one call are numbered in 32 bits, heads on the
-    // grid's second axis
-    if (Hkv > 65535 || T > (1 << 30) || (long long)nseq * Hkv > (1LL << 31) - 1 || (long long)nseq * ((long long)T / 64 + 2) > (1LL << 31) - 1) return GDR_ERR_INVALID_ARG;
+    // (sequence, head) pairs of one call are numbered in 32 bits, heads on the grid's second axis
+    if (Hkv > 65535 || T > (1 << 30) || (long long)nseq * Hkv > (1LL << 31) - 1) return GDR_ERR_INVALID_ARG;
+    if (!grid_ok(gdr::kv_append_workgroups(nseq, Hkv, T, d, cu_seqlens != nullptr))) return GDR_ERR_INVALID_ARG;
     if ((long long)nseq * max_pages > (1LL << 40)) return GDR_ERR_INVALID_ARG;
     if (T > 0 && (!k || !v)) return GDR_ERR_INVALID_ARG;
     if (!k_cache || !v_cache || !k_scale || !v_scale || !block_table || !cache_len) return GDR_ERR_INVALID_ARG;

@@ -25,6 +25,8 @@ struct RopeParams {
     uint32_t flags;
 };
 hipError_t launch_rope(RopeParams p, hipStream_t st);
+// Workgroups of a call's largest launch, along the grid's first axis (the others' below).
+long long rope_workgroups(long long rows, int d, uint32_t flags);
 
 // Element strides of one [.., heads, tokens, d] tensor whose rows of d are
 // contiguous; the same for both layouts.
@@ -57,6 +59,8 @@ struct AttnParams {
 };
 hipError_t launch_attn_fwd(const AttnParams& p, hipStream_t st);
 hipError_t launch_attn_bwd(const AttnParams& p, hipStream_t st);
+long long attn_fwd_workgroups(int B, int Hq, int Tq);
+long long attn_bwd_workgroups(int B, int Hq, int Hkv, int Tq, int Tk, int d);
 // Splits of the key side's queries, of a tile on average (1: no partials), and the most
 // that a tile is given then.
 int attn_bwd_splits(int B, int Hq, int Hkv, int Tq, int Tk);
@@ -76,6 +80,7 @@ struct KvAppendParams {
     long long st, sh;           // element strides of a token and a head of k and v
 };
 hipError_t launch_kv_append(const KvAppendParams& p, hipStream_t st);
+long long kv_append_workgroups(int nseq, int Hkv, int T, int d, bool packed);
 
 struct AttnDecodeParams {
     const void* q;
@@ -96,6 +101,7 @@ struct AttnDecodeParams {
 // Splits of the pages a call may have to read, and the pages of one split.
 int attn_decode_splits(int N, int Hq, int Hkv, int max_pages, int window, int* split_pages);
 hipError_t launch_attn_decode(const AttnDecodeParams& p, hipStream_t st);
+long long attn_decode_workgroups(int N, int Hq, int Hkv);
 
 // Index of the last of cu[0] .. cu[nseq] that is at most t, or 0.
 __host__ __device__ inline int last_at_most(const int* cu, int nseq, int t) {

@@ -863,6 +863,14 @@ int attn_bwd_splits_most(int splits, int Tk) {
     return (int)((2LL * splits * tiles + tiles) / (tiles + 1));
 }
 
+long long attn_bwd_workgroups(int B, int Hq, int Hkv, int Tq, int Tk, int d) {
+    const long long per = 2048 / d, delta = (long long)B * Hq + ((long long)B * Hq * Tq + per - 1) / per;
+    const int splits = attn_bwd_splits(B, Hq, Hkv, Tq, Tk);
+    const long long key_items = (long long)B * Hkv * (((long long)Tk + kKN - 1) / kKN) * (splits > 1 ? attn_bwd_splits_most(splits, Tk) : 1);
+    const long long items = key_items + (long long)B * Hq * (((long long)Tq + kQM - 1) / kQM);
+    return delta > items ? delta : items;
+}
+
 template <int D>
 static hipError_t launch_bwd_d(AttnParams p, hipStream_t st) {
     static std::atomic<unsigned long long> done{0};

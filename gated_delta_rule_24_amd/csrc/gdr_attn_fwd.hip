@@ -254,6 +254,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_kernel(AttnParams p, 
     }
 }
 
+long long attn_fwd_workgroups(int B, int Hq, int Tq) { return (long long)B * Hq * (((long long)Tq + kBM - 1) / kBM); }
+
 template <int D>
 static hipError_t launch_fwd_d(const AttnParams& p, hipStream_t st) {
     static std::atomic<unsigned long long> done{0};
@@ -262,7 +264,7 @@ static hipError_t launch_fwd_d(const AttnParams& p, hipStream_t st) {
     if (e != hipSuccess) return e;
     const int tiles = (p.Tq + kBM - 1) / kBM;
     if (tiles == 0) return hipSuccess;
-    hipLaunchKernelGGL((attn_fwd_kernel<D>), dim3((unsigned)((long long)p.B * p.Hq * tiles)), dim3(64 * kWaves),
+    hipLaunchKernelGGL((attn_fwd_kernel<D>), dim3((unsigned)attn_fwd_workgroups(p.B, p.Hq, p.Tq)), dim3(64 * kWaves),
                        sizeof(FwdSmem<D>), st, p, tiles);
     return hipGetLastError();
 }

@@ -290,17 +290,22 @@ __global__ __launch_bounds__(256) void kv_append_one_kernel(KvAppendParams p) {
     }
 }
 
+long long kv_append_workgroups(int nseq, int Hkv, int T, int d, bool packed) {
+    // a sequence's m new tokens touch at most m / 64 + 2 pages
+    if (packed) return (long long)T / kPage + 2LL * nseq;
+    const long long pairs = (long long)nseq * Hkv, per = 1024 / d;
+    return (pairs + per - 1) / per;
+}
+
 hipError_t launch_kv_append(const KvAppendParams& p, hipStream_t st) {
+    const unsigned items = (unsigned)kv_append_workgroups(p.nseq, p.Hkv, p.T, p.d, p.cu_seqlens != nullptr);
     if (!p.cu_seqlens) {
-        const long long pairs = (long long)p.nseq * p.Hkv, per = 1024 / p.d;
-        dim3 grid((unsigned)((pairs + per - 1) / per)), block(256);
+        dim3 grid(items), block(256);
         if (p.d == 64) hipLaunchKernelGGL((kv_append_one_kernel<64>), grid, block, 0, st, p);
         else hipLaunchKernelGGL((kv_append_one_kernel<128>), grid, block, 0, st, p);
         return hipGetLastError();
     }
-    // a sequence's m new tokens touch at most m / 64 + 2 pages
-    const long long items = (long long)p.T / kPage + 2LL * p.nseq;
-    dim3 grid((unsigned)items, (unsigned)p.Hkv), block(256);
+    dim3 grid(items, (unsigned)p.Hkv), block(256);
     if (p.d == 64) hipLaunchKernelGGL((kv_append_kernel<64>), grid, block, 0, st, p);
     else hipLaunchKernelGGL((kv_append_kernel<128>), grid, block, 0, st, p);
     return hipGetLastError();
@@ -607,9 +612,12 @@ int attn_decode_splits(int N, int Hq, int Hkv, int max_pages, int window, int* s
     return s < 1 ? 1 : (int)s;
 }
 
+// (the join, a workgroup a head, runs only where these are few: see attn_decode_splits)
+long long attn_decode_workgroups(int N, int Hq, int Hkv) { return (long long)N * Hkv * ((Hq / Hkv + 15) / 16); }
+
 hipError_t launch_attn_decode(const AttnDecodeParams& p, hipStream_t st) {
     const int groups = (p.Hq / p.Hkv + 15) / 16;
-    dim3 grid((unsigned)((long long)p.N * p.Hkv * groups), (unsigned)p.splits), block(64 * kDecWaves);
+    dim3 grid((unsigned)attn_decode_workgroups(p.N, p.Hq, p.Hkv), (unsigned)p.splits), block(64 * kDecWaves);
     if (p.d == 64) hipLaunchKernelGGL((attn_decode_kernel<64>), grid, block, 0, st, p, groups);
     else hipLaunchKernelGGL((attn_decode_kernel<128>), grid, block, 0, st, p, groups);
     hipError_t e = hipGetLastError();

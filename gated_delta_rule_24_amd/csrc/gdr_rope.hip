@@ -130,10 +130,14 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeParams p) {
     }
 }
 
+long long rope_workgroups(long long rows, int d, uint32_t flags) {
+    const int units = d / ((flags & GDR_ACT_F32) ? 8 : 16), per = 256 / units;
+    return (rows + per - 1) / per;
+}
+
 hipError_t launch_rope(RopeParams p, hipStream_t st) {
     const bool f32 = (p.flags & GDR_ACT_F32) != 0;
-    const int units = p.d / (f32 ? 8 : 16), per = 256 / units;
-    const long long tiles = (p.rows + per - 1) / per;
+    const long long tiles = rope_workgroups(p.rows, p.d, p.flags);
     if (tiles == 0) return hipSuccess;
     const int all = p.Hq + p.Hk;
     // enough workgroups to fill the chip, then as many heads per angle as that leaves

@@ -416,7 +416,9 @@ gdr_status gdr_mixer_epilogue_bwd(const float* o, const void* g, const float* no
  * of Hkv; query head h reads key head h / (Hq / Hkv).  Indexes and lengths in
  * device memory (positions, cu_seqlens, block_table, cache_len) are not checked
  * on the host; no content of them makes a kernel read or write outside the
- * tensors.  Results do not depend on the order in which workgroups run.
+ * tensors.  Results do not depend on the order in which workgroups run.  A call
+ * whose largest launch would pass 2^24 - 1 workgroups (one for 128 queries of a
+ * head, say) is refused with GDR_ERR_INVALID_ARG.
  */
 
 /*
