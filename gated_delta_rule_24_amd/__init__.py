@@ -888,7 +888,8 @@ def attn_decode(q, cache: KVCache, block_table, cache_len, window: int = 0, scal
                 out_dtype=torch.float32, o=None, stream=None):
     """Attention of one token per sequence over the cache: q bf16 [N,Hq,d], the
     last of each sequence's cache_len tokens; sees all of them or the last
-    `window`.  Returns o [N,Hq,d] of out_dtype (fp32 or bf16)."""
+    `window`.  Calls of few sequences are slow behind a block_table much wider than
+    they need.  Returns o [N,Hq,d] of out_dtype (fp32 or bf16)."""
     gpu = _gpu_of("q", q)
     n_pages, Hkv, d, N, max_pages = _cache_shapes(cache, block_table, cache_len, gpu)
     if q.dim() != 3:

@@ -10,11 +10,16 @@
 // one kernel, the key side's first, after a small one that forms D: one tail
 // instead of two, and short calls fill the chip with both.
 //
+// P and dS are rounded to bf16 for their products, as the forward's weights are and for
+// the same reason.  dS's rounding is as large as that of the results: dq and dk are
+// sqrt(2) times as far off as that alone (0.24% for 0.17%); its remainder as a second
+// operand would be two products more.
+//
 // Bound by the matrix cores' share of the time (query side 55% of the cycles, key side
 // 49%) and by power: on random data the clock falls from 2.4 to about 1.9 GHz (all
 // inputs zero: 634 us for 819).  Measured, d = 128: 2 x 8,192 tokens, 16 heads, window
 // 2,048 820 us, 734 TFLOP/s for the five products of a single walk and 1,030 for the
-// seven; 2,047 tokens, 16 heads on 4, 86 us, 497 and 696, of which 6 form D and 7 sum
+// seven; 2,047 tokens, 16 heads on 4, 88 us, 488 and 683, of which 6 form D and 7 sum
 // the splits (bound by the steps that one workgroup takes after the other: 40 of 1.8 us
 // on the key side, up to 32 of 1.9 on the query side).  A single walk would add dq into
 // memory from every key tile: with atomics, whose order would change results, or with

@@ -13,11 +13,14 @@
 // stand: an MFMA contracts over any order of the keys that both operands share,
 // so the value operand is read with the same order (transposing LDS reads).
 //
-// Bound by the matrix cores' share of the time and by power: two workgroups on a
-// compute unit, so that one's softmax runs beside the other's products, keep the
-// matrix cores at work in 46% of the cycles, and on random data the card lowers its
-// clock from 2.4 to about 1.9 GHz (all inputs zero: 203 us for 257, a library's
-// product of two 8192 x 8192 matrices 612 for 790).  Measured, d = 128: 2 x 8,192
+// The weights are rounded to bf16 for the product with v: the matrix instruction takes
+// both operands in one type, and v is bf16 (their sum l is of the fp32 weights).
+//
+// Bound by matrix cores and vector work taking turns (46% and 44% of the cycles): two workgroups on a
+// compute unit, so that one's softmax runs beside the other's products, overlap
+// no more of them than that.  On random data the card lowers its clock from 2.4 to about
+// 1.9 GHz (all inputs zero: 203 us for 257; a library's product of two 8192 x 8192
+// matrices, which has the same clock, 612 for 790: 1,390 TFLOP/s).  Measured, d = 128: 2 x 8,192
 // tokens, 16 heads, window 2,048 260 us, 927 TFLOP/s; 16,384 packed tokens as 19
 // sequences, 16 heads on 4, 135 us, 628 TFLOP/s (two fifths of the tiles are seen in
 // part, and the workgroups' lengths differ); 257 tokens 7.5 us on the GPU, 10 a call.

@@ -215,8 +215,9 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendParams p) {
 // One token of each sequence: 2 L lanes (L = D / 8) own one (sequence, head), L for
 // its keys and L for its values, 8 channels a lane, so that the call is one short
 // chain of reads (length, page, scale) beside the tokens' own: bound by latency (256
-// sequences x 8 heads: 5 us on the GPU and 9.9 a call from Python, which the host bounds;
-// with the prompts' kernel the GPU bounded it, at 10.9).
+// sequences x 8 heads: 5 us on the GPU at its shortest, 9 in the mean of single calls, and
+// 9.9 a call from Python, which the host bounds; with the prompts' kernel the GPU bounded
+// it, at 10.9).
 template <int D>
 __global__ __launch_bounds__(256) void kv_append_one_kernel(KvAppendParams p) {
     constexpr int L = D / 8;
@@ -334,7 +335,13 @@ hipError_t launch_kv_append(const KvAppendParams& p, hipStream_t st) {
 // e4m3 is exact in bf16 and f16.
 // Measured, 32 query heads on 8, d = 128: 256 sequences of up to 8,192 tokens 474 us,
 // 5.55 TB/s (a plain sum of as many bytes reads 6.15); one of 50,000 26.8 us: 20 for
-// the pages, 4 for the join of the splits, the rest between the two launches.
+// the pages, 4 for the join of the splits, the rest between the two launches (24.1 to 24.6
+// where call after call reads the same pages, out of the last cache).
+// Two limits.  The splits follow the block table's width, as the host does not know the
+// lengths: the sequence of 50,000 tokens takes 28 us behind a table of 782 pages, 35
+// behind 2,048 and 190 behind 16,384.  And the cache is read once for each 16 query heads
+// of a key head: 32 sequences of up to 8,192 tokens with 16, 32, 64 and 128 heads on one
+// take 18, 24, 38 and 65 us.
 namespace {
 
 constexpr int kDecWaves = 4;
@@ -599,7 +606,8 @@ int attn_decode_splits(int N, int Hq, int Hkv, int max_pages, int window, int* s
     if (window > 0 && window / kPage + 2 < pages) pages = window / kPage + 2;
     // Few (sequence, head) pairs: at most two workgroups on a compute unit, every
     // one at work at once (one sequence of 50,000 tokens x 8 heads: 24.6 us with 392
-    // workgroups, 27.3 with 784, 31.4 with 200; 100,000: 38.5 with 392, 41.8 with 784).
+    // workgroups, 27.3 with 784, 31.4 with 200; 100,000: 38.5 with 392, 41.8 with 784; on
+    // the same pages call after call).
     // Many: splits for balance among ragged lengths, up to about 3,000 workgroups (256
     // sequences of up to 8,192 tokens x 8 heads: 474 us, with up to 2,560 492, 4,096 483;
     // 100 of up to 4,000: 113, 113, 112).  The same pages for each wave, two at least.

@@ -495,7 +495,8 @@ gdr_status gdr_attn_fwd_varlen(const void* q, const void* k, const void* v, void
  * keys for queries that see at most 32 of them (there o's rounding would show in dq
  * and dk), from o for the others.  A pair that is not
  * seen has no effect on a gradient, as in the forward (finite values near the
- * type's largest, whose products overflow, included).  Supported as
+ * type's largest, whose products overflow, included; NaN and infinities in partly
+ * seen tiles make the tile's keys or queries slow as there).  Supported as
  * gdr_attn_fwd.  The varlen call leaves rows from cu_seqlens[nseq] on unwritten.
  */
 size_t gdr_attn_bwd_workspace_bytes(int B, int Hq, int Hkv, int Tq, int Tk, int d);
@@ -554,7 +555,11 @@ gdr_status gdr_kv_append(const void* k, const void* v, void* k_cache, void* v_ca
  *        none needed, may be NULL), contents on entry ignored; calls that may
  *        overlap need one each
  * Scores, weights and sums are fp32 (the weights enter the product as two f16
- * parts).  Flags: GDR_OUT_BF16.  Supported: d in {64, 128}.
+ * parts).  The work is dealt out by the table's width (or the window): a table much
+ * wider than its sequences makes calls of few sequences slow (one of 8,192 tokens
+ * behind 128 pages 16 us, behind 16,384 86), so pass its first columns as a table of
+ * their own.  The cache is read once for each 16 query heads of a key head.
+ * Flags: GDR_OUT_BF16.  Supported: d in {64, 128}.
  */
 size_t gdr_attn_decode_workspace_bytes(int N, int Hq, int Hkv, int d, int max_pages, int window);
 
