@@ -321,8 +321,8 @@ __device__ __forceinline__ void query_side(const AttnParams& p, int item, int ti
         }
         const bool edge = j0 < lo_most || j0 + kQN > hi_least;
         if (edge) {
-            // (a masked pair's weight is 0, and so must be its product with dO v - D)
-            const bool mine = any_not_finite<D>(sm.k[BUF] + 16 * wave * D, lane) || any_not_finite<D>(sm.v[BUF] + 16 * wave * D, lane);
+            // (a masked pair's weight is 0, and its product with dO v - D is, whatever v)
+            const bool mine = any_not_finite<D>(sm.k[BUF] + 16 * wave * D, lane);
             if (lane == 0) sm.bad[wave] = mine;
             lds_barrier();
             bad = (sm.bad[0] | sm.bad[1] | sm.bad[2] | sm.bad[3]) != 0;
@@ -673,9 +673,8 @@ __device__ __forceinline__ void key_side(const AttnParams& p, int item, int tile
             constexpr int kMine = KM / kKWaves;
             bool mine = any_not_finite<D, kMine>(sm.q[buf] + kMine * wave * D, lane) ||
                         any_not_finite<D, kMine>(sm.g[buf] + kMine * wave * D, lane);
-            // a masked pair's weight is 0, and so must be its product with dO v - D
-            const float d = sm.delta[buf][lane], l2 = sm.lse2[buf][lane];
-            mine = mine || __any(!(fabsf(d) < INFINITY) || !(l2 > -INFINITY));
+            // (a masked pair's weight must come out 0; its product with dO v - D then does)
+            mine = mine || __any(!(sm.lse2[buf][lane] > -INFINITY));
             if (lane == 0) sm.bad[wave] = mine;
             lds_barrier();
             bad = (sm.bad[0] | sm.bad[1] | sm.bad[2] | sm.bad[3]) != 0;

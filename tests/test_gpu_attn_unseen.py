@@ -78,3 +78,23 @@ def test_gradients_of_keys_do_not_depend_on_queries_that_do_not_see_them(window,
     others = torch.arange(T) != row
     assert torch.equal(_rows(got["dq"], packed, others), _rows(want["dq"], packed, others))
     assert bool(torch.isfinite(got["dq"]).all()) and bool(torch.isfinite(got["dk"]).all())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("window,cu,T,row", [(0, None, 128, 0), (0, None, 300, 0), (20, None, 300, 140),
+                                             (0, [0, 100, 128], 128, 99), (0, [0, 90, 128], 128, 0)])
+def test_a_query_whose_own_sum_overflows_reaches_only_the_keys_that_it_sees(window, cu, T, row, d):
+    """dO near the type's largest in every channel of one query: its D overflows."""
+    x = _inputs(1, 2, 1, T, T, d, 33)
+    packed = cu is not None
+    start = [e for e in cu if e <= row][-1] if cu else 0
+    seen = torch.zeros(T, dtype=torch.bool)
+    seen[max(start, row - window + 1 if window else 0):row + 1] = True
+    o, lse = _forward(x, window, cu)
+    want = _backward(x, o, lse, window, cu)
+    x["dO"][0, :, row] = 3e38
+    got = _backward(x, o, lse, window, cu)
+    for m in ("dk", "dv"):
+        assert torch.equal(_rows(got[m], packed, ~seen), _rows(want[m], packed, ~seen)), m
+    others = torch.arange(T) != row
+    assert torch.equal(_rows(got["dq"], packed, others), _rows(want["dq"], packed, others))
