@@ -58,6 +58,28 @@ def test_memory_that_the_current_stream_still_writes():
         assert all(torch.equal(a, b) for a, b in zip(got, w)), i
 
 
+def test_captured_on_a_stream_beside_the_capturing_one():
+    x = {n: t.cuda() for n, t in _inputs(1, 4, 2, 300, 300, 64, 1).items()}
+    q, k, v, dO = (x[n] for n in ("q", "k", "v", "dO"))
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    gdr.attn_bwd(q, k, v, *gdr.attn_fwd(q, k, v), dO)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        o, lse = gdr.attn_fwd(q, k, v, stream=side)
+        g = gdr.attn_bwd(q, k, v, o, lse, dO, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    for seed in (2, 3, 2):
+        y = {n: t.cuda() for n, t in _inputs(1, 4, 2, 300, 300, 64, seed).items()}
+        for n in x:
+            x[n].copy_(y[n])
+        graph.replay()
+        torch.cuda.synchronize()
+        o2, lse2 = gdr.attn_fwd(*(y[n] for n in "qkv"))
+        g2 = gdr.attn_bwd(y["q"], y["k"], y["v"], o2, lse2, y["dO"])
+        assert torch.equal(o, o2) and torch.equal(lse, lse2) and all(torch.equal(g[n], g2[n]) for n in g)
+
+
 def test_results_are_kept_for_the_stream_that_goes_on_with_them():
     """Used on the current stream behind long work and dropped: a second call on the other
     stream does not get their memory before that."""
