@@ -19,12 +19,16 @@ The entry points keep the C names:
   ones: rotary positions, causal attention over a window or the whole past
 * :func:`gdr_kv_append`, :func:`gdr_attn_decode` — that layer's 8-bit paged
   cache and its attention for one token
+* :func:`gdr_attn_decode_shared`, :func:`gdr_kv_fork`, :func:`gdr_kv_compact`,
+  :func:`gdr_beam_select`, :func:`gdr_state_reorder` — several continuations of one
+  prompt: attention over pages that sequences share, those pages' tables, beam search
 
 and :func:`chunk_fwd`, :func:`decode_step`, :func:`chunk_bwd`,
 :func:`chunk_fwd_varlen`, :func:`chunk_bwd_varlen`, :func:`rope`,
 :func:`attn_fwd`, :func:`attn_bwd`, :func:`attn_fwd_varlen`,
 :func:`attn_bwd_varlen`, :func:`kv_append`, :func:`attn_decode` are the same
-calls with outputs allocated for the caller.
+calls with outputs allocated for the caller; those for several continuations are in
+:mod:`gated_delta_rule_24_amd.generation`.
 
 Tensors are contiguous and start at a multiple of 16 bytes, int32 ones as well
 (a slice of a longer tensor may not).
@@ -55,6 +59,7 @@ GDR_FWD_SPLIT = 0x80
 GDR_TOKEN_MAJOR = 0x1000
 GDR_ROPE_INTERLEAVED = 0x2000
 GDR_ROPE_INVERSE = 0x4000
+GDR_KEEP_SLOTS = 0x8000
 
 # tokens of a cache page
 GDR_KV_PAGE = 64
@@ -132,6 +137,24 @@ def _load():
         lib.gdr_attn_decode_workspace_bytes.restype = S
         lib.gdr_attn_decode.argtypes = [P] * 8 + [I] * 7 + [F, U, P, S, P]
         lib.gdr_attn_decode.restype = I
+        lib.gdr_attn_decode_shared_workspace_bytes.argtypes = [I] * 7
+        lib.gdr_attn_decode_shared_workspace_bytes.restype = S
+        lib.gdr_attn_decode_shared.argtypes = [P] * 10 + [I] * 8 + [F, U, P, S, P]
+        lib.gdr_attn_decode_shared.restype = I
+        lib.gdr_kv_fork_workspace_bytes.argtypes = [I] * 2
+        lib.gdr_kv_fork_workspace_bytes.restype = S
+        lib.gdr_kv_fork.argtypes = [P] * 12 + [I] * 7 + [U, P, S, P]
+        lib.gdr_kv_fork.restype = I
+        lib.gdr_kv_compact_workspace_bytes.argtypes = [I]
+        lib.gdr_kv_compact_workspace_bytes.restype = S
+        lib.gdr_kv_compact.argtypes = [P] * 9 + [I] * 5 + [U, P, S, P]
+        lib.gdr_kv_compact.restype = I
+        lib.gdr_beam_select_workspace_bytes.argtypes = [I] * 4
+        lib.gdr_beam_select_workspace_bytes.restype = S
+        lib.gdr_beam_select.argtypes = [P] * 7 + [I] * 4 + [ctypes.c_longlong, I, U, P, S, P]
+        lib.gdr_beam_select.restype = I
+        lib.gdr_state_reorder.argtypes = [P] * 2 + [I] * 3 + [S, U, P]
+        lib.gdr_state_reorder.restype = I
         _lib = lib
     return _lib
 
@@ -148,7 +171,10 @@ EXPORTED_SYMBOLS = ("gdr_abi_version", "gdr_status_string", "gdr_chunk_fwd_works
                     "gdr_mixer_prologue", "gdr_mixer_epilogue", "gdr_mixer_bwd_workspace_bytes",
                     "gdr_mixer_prologue_bwd", "gdr_mixer_epilogue_bwd", "gdr_rope", "gdr_attn_fwd",
                     "gdr_attn_fwd_varlen", "gdr_attn_bwd_workspace_bytes", "gdr_attn_bwd", "gdr_attn_bwd_varlen",
-                    "gdr_kv_append", "gdr_attn_decode_workspace_bytes", "gdr_attn_decode")
+                    "gdr_kv_append", "gdr_attn_decode_workspace_bytes", "gdr_attn_decode",
+                    "gdr_attn_decode_shared_workspace_bytes", "gdr_attn_decode_shared", "gdr_kv_fork_workspace_bytes",
+                    "gdr_kv_fork", "gdr_kv_compact_workspace_bytes", "gdr_kv_compact", "gdr_beam_select_workspace_bytes",
+                    "gdr_beam_select", "gdr_state_reorder")
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -376,6 +402,62 @@ def gdr_attn_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_le
                                                      o)], N, Hq, Hkv, d, n_pages, max_pages, _window(window), scale, flags,
                                  _ptr(workspace), workspace_bytes, _stream(stream))
     _check("gdr_attn_decode", st)
+
+
+def gdr_attn_decode_shared_workspace_bytes(N, groups, Hq, Hkv, d, max_pages, window) -> int:
+    return int(_load().gdr_attn_decode_shared_workspace_bytes(N, groups, Hq, Hkv, d, max_pages, _window(window)))
+
+
+def gdr_attn_decode_shared(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_len, group_start, shared_pages, o, N,
+                           groups, Hq, Hkv, d, n_pages, max_pages, window, scale, flags, workspace, workspace_bytes,
+                           stream=None):
+    st = _load().gdr_attn_decode_shared(*[_ptr(x) for x in (q, k_cache, v_cache, k_scale, v_scale, block_table, cache_len,
+                                                            group_start, shared_pages, o)], N, groups, Hq, Hkv, d, n_pages,
+                                        max_pages, _window(window), scale, flags, _ptr(workspace), workspace_bytes,
+                                        _stream(stream))
+    _check("gdr_attn_decode_shared", st)
+
+
+def gdr_kv_fork_workspace_bytes(N, n_pages) -> int:
+    return int(_load().gdr_kv_fork_workspace_bytes(N, n_pages))
+
+
+def gdr_kv_fork(k_cache, v_cache, k_scale, v_scale, block_table, cache_len, parent, room, held, table_out, len_out, missing,
+                N_in, N, room_all, Hkv, d, n_pages, max_pages, flags, workspace, workspace_bytes, stream=None):
+    st = _load().gdr_kv_fork(*[_ptr(x) for x in (k_cache, v_cache, k_scale, v_scale, block_table, cache_len, parent, room,
+                                                 held, table_out, len_out, missing)], N_in, N, room_all, Hkv, d, n_pages,
+                             max_pages, flags, _ptr(workspace), workspace_bytes, _stream(stream))
+    _check("gdr_kv_fork", st)
+
+
+def gdr_kv_compact_workspace_bytes(n_pages) -> int:
+    return int(_load().gdr_kv_compact_workspace_bytes(n_pages))
+
+
+def gdr_kv_compact(k_cache, v_cache, k_scale, v_scale, block_table, cache_len, held, table_out, used, N, Hkv, d, n_pages,
+                   max_pages, flags, workspace, workspace_bytes, stream=None):
+    st = _load().gdr_kv_compact(*[_ptr(x) for x in (k_cache, v_cache, k_scale, v_scale, block_table, cache_len, held,
+                                                    table_out, used)], N, Hkv, d, n_pages, max_pages, flags,
+                                _ptr(workspace), workspace_bytes, _stream(stream))
+    _check("gdr_kv_compact", st)
+
+
+def gdr_beam_select_workspace_bytes(G, K, M, V) -> int:
+    return int(_load().gdr_beam_select_workspace_bytes(G, K, M, V))
+
+
+def gdr_beam_select(logits, scores, ended, tokens, rows, scores_out, ended_out, G, K, M, V, stride, end_token, flags,
+                    workspace, workspace_bytes, stream=None):
+    if not logits.is_cuda or logits.stride(-1) != 1:      # (its rows may be those of a wider tensor)
+        raise ValueError("logits must be on the GPU, each row contiguous")
+    st = _load().gdr_beam_select(logits.data_ptr(), *[_ptr(x) for x in (scores, ended, tokens, rows, scores_out, ended_out)],
+                                 G, K, M, V, stride, end_token, flags, _ptr(workspace), workspace_bytes, _stream(stream))
+    _check("gdr_beam_select", st)
+
+
+def gdr_state_reorder(state, parent, layers, N, K, row_bytes, flags=0, stream=None):
+    st = _load().gdr_state_reorder(_ptr(state), _ptr(parent), layers, N, K, row_bytes, flags, _stream(stream))
+    _check("gdr_state_reorder", st)
 
 
 # ---------------------------------------------------------------------------
@@ -912,3 +994,6 @@ def attn_decode(q, cache: KVCache, block_table, cache_len, window: int = 0, scal
             d ** -0.5 if scale is None else scale, GDR_OUT_BF16 if out_dtype is torch.bfloat16 else 0,
             None if ws is None else ws.data_ptr(), nbytes)
     return o
+
+
+from . import generation  # noqa: E402  (it uses the names above)

@@ -7,6 +7,7 @@
 
 #include "gdr_launch.h"
 #include "gdr_attn.h"
+#include "gdr_generation.h"
 
 namespace {
 
@@ -141,6 +142,27 @@ gdr_status decode_args(int N, int Hq, int Hkv, int d, int n_pages, int max_pages
     if ((long long)N * Hq > (1LL << 28) || max_pages > (1 << 24)) return GDR_ERR_INVALID_ARG;
     if (d != 64 && d != 128) return GDR_ERR_UNSUPPORTED;
     if (!grid_ok(gdr::attn_decode_workgroups(N, Hq, Hkv))) return GDR_ERR_INVALID_ARG;
+    return GDR_OK;
+}
+
+// Rows of a block table, and pages, are numbered in 32 bits, as are all rows' pages together.
+gdr_status pages_args(int N, int Hkv, int d, int n_pages, int max_pages, uint32_t flags) {
+    if (flags != 0) return GDR_ERR_INVALID_ARG;
+    if (N < 1 || Hkv < 1 || n_pages < 1 || max_pages < 1) return GDR_ERR_INVALID_ARG;
+    if (N > (1 << 20) || Hkv > 65535 || n_pages > (1 << 30) || max_pages > (1 << 24)) return GDR_ERR_INVALID_ARG;
+    if ((long long)N * max_pages > (1LL << 31) - 1) return GDR_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return GDR_ERR_UNSUPPORTED;
+    return GDR_OK;
+}
+
+gdr_status beam_args(int G, int K, int M, int V, long long stride, int end_token, uint32_t flags) {
+    if (flags & ~(GDR_ACT_F32 | GDR_KEEP_SLOTS)) return GDR_ERR_INVALID_ARG;
+    if (G < 1 || K < 1 || M < 1 || V < 1 || V > (1 << 30) || stride < V || end_token < -1 || end_token >= V)
+        return GDR_ERR_INVALID_ARG;
+    if ((long long)K * V < M || ((flags & GDR_KEEP_SLOTS) && M != K)) return GDR_ERR_INVALID_ARG;
+    if (K > gdr::kMostBeams || M > gdr::kMostSelected) return GDR_ERR_UNSUPPORTED;
+    // rows are on the grid's second axis; element offsets in 64 bits
+    if ((long long)G * K > 65535 || stride > (1LL << 40)) return GDR_ERR_INVALID_ARG;
     return GDR_OK;
 }
 
@@ -631,6 +653,150 @@ gdr_status gdr_attn_decode(const void* q, const void* k_cache, const void* v_cac
     p.part_ml = need > 0 ? p.part_o + (size_t)p.splits * N * Hq * d : nullptr;
     p.scale = scale; p.flags = flags;
     return from_hip(gdr::launch_attn_decode(p, (hipStream_t)stream));
+}
+
+size_t gdr_attn_decode_shared_workspace_bytes(int N, int groups, int Hq, int Hkv, int d, int max_pages, int window) {
+    if (decode_args(N, Hq, Hkv, d, 1, max_pages, window, 1.f, 0) != GDR_OK || groups < 1 || groups > (1 << 28)) return 0;
+    const gdr::SharedPlan x = gdr::attn_shared_plan(N, groups, Hq, Hkv, max_pages, window);
+    return (size_t)(x.shared_splits + x.own_splits) * N * Hq * (d + 2) * sizeof(float);
+}
+
+gdr_status gdr_attn_decode_shared(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                                  const float* v_scale, const int* block_table, const int* cache_len,
+                                  const int* group_start, const int* shared_pages, void* o, int N, int groups, int Hq,
+                                  int Hkv, int d, int n_pages, int max_pages, int window, float scale, uint32_t flags,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+    const gdr_status st = decode_args(N, Hq, Hkv, d, n_pages, max_pages, window, scale, flags);
+    if (st != GDR_OK) return st;
+    if (groups < 1 || groups > (1 << 28)) return GDR_ERR_INVALID_ARG;
+    const gdr::SharedPlan x = gdr::attn_shared_plan(N, groups, Hq, Hkv, max_pages, window);
+    if (!grid_ok(gdr::attn_shared_workgroups(x, Hkv, (long long)N * Hq))) return GDR_ERR_INVALID_ARG;
+    const void* ptrs[] = {q, k_cache, v_cache, k_scale, v_scale, block_table, cache_len, group_start, shared_pages, o};
+    for (const void* ptr : ptrs)
+        if (!ptr || !aligned16(ptr)) return GDR_ERR_INVALID_ARG;
+    if (workspace && !aligned16(workspace)) return GDR_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < gdr_attn_decode_shared_workspace_bytes(N, groups, Hq, Hkv, d, max_pages, window))
+        return GDR_ERR_WORKSPACE;
+    gdr_status ds = check_device();
+    if (ds != GDR_OK) return ds;
+    gdr::SharedParams p;
+    p.q = q;
+    p.k_cache = static_cast<const uint8_t*>(k_cache); p.v_cache = static_cast<const uint8_t*>(v_cache);
+    p.k_scale = k_scale; p.v_scale = v_scale; p.block_table = block_table; p.cache_len = cache_len;
+    p.group_start = group_start; p.shared_pages = shared_pages; p.o = o;
+    p.N = N; p.groups = groups; p.Hq = Hq; p.Hkv = Hkv; p.d = d; p.n_pages = n_pages; p.max_pages = max_pages;
+    p.window = window; p.tiles = x.tiles; p.shared_splits = x.shared_splits; p.own_splits = x.own_splits;
+    p.part_o = static_cast<float*>(workspace);
+    p.part_ml = p.part_o + (size_t)(x.shared_splits + x.own_splits) * N * Hq * d;
+    p.scale = scale; p.flags = flags;
+    return from_hip(gdr::launch_attn_shared(p, x, (hipStream_t)stream));
+}
+
+size_t gdr_kv_fork_workspace_bytes(int N, int n_pages) {
+    if (pages_args(N, 1, 64, n_pages, 1, 0) != GDR_OK) return 0;
+    return gdr::kv_fork_workspace(N, n_pages);
+}
+
+gdr_status gdr_kv_fork(void* k_cache, void* v_cache, float* k_scale, float* v_scale, const int* block_table,
+                       const int* cache_len, const int* parent, const int* room, const uint8_t* held, int* table_out,
+                       int* len_out, int* missing, int N_in, int N, int room_all, int Hkv, int d, int n_pages,
+                       int max_pages, uint32_t flags, void* workspace, size_t workspace_bytes, void* stream) {
+    gdr_status st = pages_args(N, Hkv, d, n_pages, max_pages, flags);
+    if (st == GDR_OK) st = pages_args(N_in, Hkv, d, n_pages, max_pages, flags);
+    if (st != GDR_OK) return st;
+    if (room_all < 0 || (!parent && N_in != N)) return GDR_ERR_INVALID_ARG;
+    if (!grid_ok(gdr::kv_fork_workgroups(N, Hkv, d, n_pages, max_pages))) return GDR_ERR_INVALID_ARG;
+    const void* ptrs[] = {k_cache, v_cache, k_scale, v_scale, block_table, cache_len, table_out, len_out, missing};
+    for (const void* ptr : ptrs)
+        if (!ptr || !aligned16(ptr)) return GDR_ERR_INVALID_ARG;
+    const void* maybe[] = {parent, room, held, workspace};
+    for (const void* ptr : maybe)
+        if (ptr && !aligned16(ptr)) return GDR_ERR_INVALID_ARG;
+    // rows are read by others' workgroups while they are written
+    if (parent && (table_out == block_table || len_out == cache_len)) return GDR_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < gdr_kv_fork_workspace_bytes(N, n_pages)) return GDR_ERR_WORKSPACE;
+    gdr_status ds = check_device();
+    if (ds != GDR_OK) return ds;
+    gdr::PagesParams p = {};
+    p.k_cache = static_cast<uint8_t*>(k_cache); p.v_cache = static_cast<uint8_t*>(v_cache);
+    p.k_scale = k_scale; p.v_scale = v_scale;
+    p.block_table = block_table; p.cache_len = cache_len; p.parent = parent; p.room = room; p.held = held;
+    p.table_out = table_out; p.len_out = len_out; p.missing = missing;
+    p.N_in = N_in; p.N = N; p.room_all = room_all; p.Hkv = Hkv; p.d = d; p.n_pages = n_pages; p.max_pages = max_pages;
+    p.workspace = workspace;
+    return from_hip(gdr::launch_kv_fork(p, (hipStream_t)stream));
+}
+
+size_t gdr_kv_compact_workspace_bytes(int n_pages) {
+    if (pages_args(1, 1, 64, n_pages, 1, 0) != GDR_OK) return 0;
+    return gdr::kv_compact_workspace(n_pages);
+}
+
+gdr_status gdr_kv_compact(void* k_cache, void* v_cache, float* k_scale, float* v_scale, const int* block_table,
+                          const int* cache_len, const uint8_t* held, int* table_out, int* used, int N, int Hkv, int d,
+                          int n_pages, int max_pages, uint32_t flags, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+    const gdr_status st = pages_args(N, Hkv, d, n_pages, max_pages, flags);
+    if (st != GDR_OK) return st;
+    if (!grid_ok(gdr::kv_compact_workgroups(N, n_pages, max_pages))) return GDR_ERR_INVALID_ARG;
+    const void* ptrs[] = {k_cache, v_cache, k_scale, v_scale, block_table, cache_len, table_out, used};
+    for (const void* ptr : ptrs)
+        if (!ptr || !aligned16(ptr)) return GDR_ERR_INVALID_ARG;
+    if ((held && !aligned16(held)) || (workspace && !aligned16(workspace))) return GDR_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < gdr_kv_compact_workspace_bytes(n_pages)) return GDR_ERR_WORKSPACE;
+    gdr_status ds = check_device();
+    if (ds != GDR_OK) return ds;
+    gdr::PagesParams p = {};
+    p.k_cache = static_cast<uint8_t*>(k_cache); p.v_cache = static_cast<uint8_t*>(v_cache);
+    p.k_scale = k_scale; p.v_scale = v_scale;
+    p.block_table = block_table; p.cache_len = cache_len; p.held = held; p.table_out = table_out; p.used = used;
+    p.N_in = N; p.N = N; p.Hkv = Hkv; p.d = d; p.n_pages = n_pages; p.max_pages = max_pages;
+    p.workspace = workspace;
+    return from_hip(gdr::launch_kv_compact(p, (hipStream_t)stream));
+}
+
+size_t gdr_beam_select_workspace_bytes(int G, int K, int M, int V) {
+    if (beam_args(G, K, M, V, V, -1, 0) != GDR_OK) return 0;
+    return (size_t)G * K * gdr::beam_segments(G, K, V) * (8 * (size_t)M + 8);
+}
+
+gdr_status gdr_beam_select(const void* logits, const float* scores, const uint8_t* ended, int* tokens, int* rows,
+                           float* scores_out, uint8_t* ended_out, int G, int K, int M, int V, long long stride,
+                           int end_token, uint32_t flags, void* workspace, size_t workspace_bytes, void* stream) {
+    const gdr_status st = beam_args(G, K, M, V, stride, end_token, flags);
+    if (st != GDR_OK) return st;
+    if (ended && end_token < 0) return GDR_ERR_INVALID_ARG;
+    const void* ptrs[] = {logits, scores, tokens, rows, scores_out, ended_out};
+    for (const void* ptr : ptrs)
+        if (!ptr || !aligned16(ptr)) return GDR_ERR_INVALID_ARG;
+    if ((ended && !aligned16(ended)) || (workspace && !aligned16(workspace))) return GDR_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < gdr_beam_select_workspace_bytes(G, K, M, V)) return GDR_ERR_WORKSPACE;
+    gdr_status ds = check_device();
+    if (ds != GDR_OK) return ds;
+    gdr::BeamParams p;
+    p.logits = logits; p.scores = scores; p.ended = ended;
+    p.tokens = tokens; p.rows = rows; p.scores_out = scores_out; p.ended_out = ended_out;
+    p.G = G; p.K = K; p.M = M; p.V = V; p.end_token = end_token; p.stride = stride; p.flags = flags;
+    p.segs = gdr::beam_segments(G, K, V);
+    p.best = static_cast<uint64_t*>(workspace);
+    p.part = reinterpret_cast<float*>(p.best + (size_t)G * K * p.segs * M);
+    return from_hip(gdr::launch_beam_select(p, (hipStream_t)stream));
+}
+
+gdr_status gdr_state_reorder(void* state, const int* parent, int layers, int N, int K, size_t row_bytes,
+                             uint32_t flags, void* stream) {
+    if (flags != 0 || layers < 1 || N < 1 || K < 1 || N % K != 0) return GDR_ERR_INVALID_ARG;
+    if (row_bytes < 1 || row_bytes % 16 != 0 || row_bytes > ((size_t)1 << 40)) return GDR_ERR_INVALID_ARG;
+    if ((long long)layers * N > (1LL << 28)) return GDR_ERR_INVALID_ARG;
+    if (K > gdr::kMostBeams) return GDR_ERR_UNSUPPORTED;
+    if (!grid_ok(gdr::state_reorder_workgroups(layers, N, K, (long long)row_bytes))) return GDR_ERR_INVALID_ARG;
+    if (!state || !parent || !aligned16(state) || !aligned16(parent)) return GDR_ERR_INVALID_ARG;
+    gdr_status ds = check_device();
+    if (ds != GDR_OK) return ds;
+    gdr::ReorderParams p;
+    p.state = static_cast<uint8_t*>(state); p.parent = parent;
+    p.layers = layers; p.N = N; p.K = K; p.row_bytes = (long long)row_bytes;
+    return from_hip(gdr::launch_state_reorder(p, (hipStream_t)stream));
 }
 
 }  // extern "C"

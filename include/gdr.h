@@ -110,6 +110,9 @@ typedef enum gdr_status {
                                         (i, i + rot_dim / 2)                         */
 #define GDR_ROPE_INVERSE     0x4000u /* turn back: the transpose, which is the gradient  */
 
+/* flag of gdr_beam_select */
+#define GDR_KEEP_SLOTS       0x8000u /* a beam's first continuation stays in the beam's row */
+
 #define GDR_ABI_VERSION 2
 
 int gdr_abi_version(void);
@@ -568,6 +571,146 @@ gdr_status gdr_attn_decode(const void* q, const void* k_cache, const void* v_cac
                            const int* cache_len, void* o, int N, int Hq, int Hkv, int d,
                            int n_pages, int max_pages, int window, float scale, uint32_t flags,
                            void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Several continuations of one prompt: samples, beams, or a batch behind a common
+ * system prompt.  Their sequences share the prompt's pages of the cache, whose tokens
+ * are then read once a group; their block tables are forked, and their recurrent
+ * states moved, as beams go on or end.
+ *
+ * Indexes and lengths in device memory (group_start, shared_pages, block_table,
+ * cache_len, parent, room) are not checked on the host; no content of them makes a
+ * kernel read or write outside the tensors.  Results do not depend on the order in which
+ * workgroups run.  A call whose largest launch would pass 2^24 - 1 workgroups is
+ * refused with GDR_ERR_INVALID_ARG.
+ */
+
+/*
+ * gdr_attn_decode for groups of sequences that share their first pages: group g is the
+ * sequences group_start[g] .. group_start[g + 1] - 1, and their first
+ * shared_pages[g] pages are those in the table's row of the group's first sequence
+ * (the other rows' entries for them are not read).  Their tokens are read once for every
+ * 16 or 32 of the group's (sequence, query head) pairs on a key head, not once for
+ * each sequence.  Lengths and windows are each sequence's own; a sequence may end inside
+ * the shared pages.  Sequences in no group share nothing.
+ *   group_start  : int32 [groups + 1] in device memory, non-decreasing, within 0 .. N
+ *   shared_pages : int32 [groups] in device memory
+ *   the rest as gdr_attn_decode
+ *   workspace    : gdr_attn_decode_shared_workspace_bytes() bytes of device scratch,
+ *        contents on entry ignored; calls that may overlap need one each
+ * A token that a sequence does not see has no effect on it, NaN included.  Scores, softmax
+ * statistics and sums are fp32.  The weights enter the product with v as two f16 parts
+ * (22 bits) where the result is fp32, as one (11 bits) where it is bf16.
+ * Flags: GDR_OUT_BF16.  Supported: d in {64, 128}.
+ */
+size_t gdr_attn_decode_shared_workspace_bytes(int N, int groups, int Hq, int Hkv, int d, int max_pages,
+                                              int window);
+
+gdr_status gdr_attn_decode_shared(const void* q, const void* k_cache, const void* v_cache,
+                                  const float* k_scale, const float* v_scale, const int* block_table,
+                                  const int* cache_len, const int* group_start, const int* shared_pages,
+                                  void* o, int N, int groups, int Hq, int Hkv, int d, int n_pages,
+                                  int max_pages, int window, float scale, uint32_t flags,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Rows of the block table continued, forked, grown and dropped, in one call between two
+ * tokens: row n of the new table continues row parent[n] of the old one, for the
+ * room[n] tokens that it is about to append.  A row holds the pages of its cache_len
+ * tokens, and a page that no row holds (and `held` does not mark) is free.
+ *   - Pages that hold whole pages of tokens are shared by the rows that continue a row.
+ *   - The page that row n is about to write on (cache_len % 64 tokens are in it) is copied
+ *     for it, unless no other row holds that page, or all rows that do are about to write
+ *     on it and n is the lowest of them.  It is copied too where `held` marks it.
+ *   - Fresh pages follow for the tokens that do not fit, as far as max_pages.
+ * The j-th page wanted (row by row, a row's copy first) is the j-th lowest free one.
+ * Nothing is kept between calls, so that a call made again gives the same again; pages
+ * that a row was given for tokens that were never appended are free at the next call.
+ *   block_table : int32 [N_in, max_pages]   cache_len : int32 [N_in]
+ *   parent      : int32 [N], or NULL: row n (N_in = N); outside [0, N_in): row n becomes
+ *                 empty, is given no page, and has length 0
+ *   room        : int32 [N], or NULL: room_all for every row
+ *   held        : uint8 [n_pages], or NULL: pages that others hold (other tables)
+ *   table_out   : int32 [N, max_pages], written; -1 behind a row's pages
+ *   len_out     : int32 [N], written: the tokens that row n has
+ *   missing     : int32 [N], written: pages that were wanted and not free.  A row that
+ *                 misses any must not be appended to (its page may still be shared).
+ *   k_cache, v_cache, k_scale, v_scale : as gdr_kv_append; copied pages are written
+ *   workspace   : gdr_kv_fork_workspace_bytes() bytes of device scratch, contents on
+ *                 entry ignored; calls that may overlap need one each
+ * table_out and len_out may be block_table and cache_len where parent is NULL; no other
+ * aliasing.  Every table that holds pages of this cache is either in the call or in `held`.
+ * flags must be 0.  Supported: d in {64, 128}, N_in, N <= 2^20.
+ */
+size_t gdr_kv_fork_workspace_bytes(int N, int n_pages);
+
+gdr_status gdr_kv_fork(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                       const int* block_table, const int* cache_len, const int* parent,
+                       const int* room, const uint8_t* held, int* table_out, int* len_out,
+                       int* missing, int N_in, int N, int room_all, int Hkv, int d, int n_pages,
+                       int max_pages, uint32_t flags, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/*
+ * Pages in use moved to the lowest places, so that the cache's tail is free: the j-th lowest
+ * free page takes the j-th highest page that rows hold, while that is the higher of the
+ * two.  Pages that `held` marks stay.  (Pages, rows and free ones as in gdr_kv_fork: call it
+ * where cache_len is up to date.)
+ *   table_out : int32 [N, max_pages], written; -1 behind a row's pages; may be block_table
+ *   used      : int32 [1], written: one past the last page in use afterwards
+ *   workspace : gdr_kv_compact_workspace_bytes() bytes of device scratch, contents on
+ *               entry ignored; calls that may overlap need one each
+ * flags must be 0.  Supported: d in {64, 128}, N <= 2^20.
+ */
+size_t gdr_kv_compact_workspace_bytes(int n_pages);
+
+gdr_status gdr_kv_compact(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                          const int* block_table, const int* cache_len, const uint8_t* held,
+                          int* table_out, int* used, int N, int Hkv, int d, int n_pages,
+                          int max_pages, uint32_t flags, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/*
+ * Beam search: the best M continuations of each of G groups of K beams over a vocabulary
+ * of V tokens.  Row r = g K + k of the logits is beam k of group g, and
+ *   score(k, t) = scores[r] + x_rt - log sum_u exp x_ru.
+ * A beam that has ended offers one candidate, end_token at its own score, and its logits
+ * are not read; its other candidates have the score -inf.  So have those of a row without
+ * a finite log-sum (every logit -inf, or one of them NaN or +inf) and of a beam whose
+ * score is not finite.  Candidates are taken in the order: score from the highest; lower
+ * beam; higher logit; lower token.  Equal ones thus go to the lowest (beam, token).
+ *   logits : bf16, or fp32 with GDR_ACT_F32: [G K] rows of V, `stride` elements apart
+ *   scores : fp32 [G, K]     ended : uint8 [G, K] (0 or 1), or NULL: none
+ *   tokens, rows : int32 [G, M], written: the token, and the row g K + k it continues
+ *   scores_out   : fp32 [G, M], written
+ *   ended_out    : uint8 [G, M], written: 1 where the beam had ended or the token ends it
+ *   end_token    : the token that ends a beam; -1: none does (ended is NULL then)
+ *   workspace    : gdr_beam_select_workspace_bytes() bytes of device scratch, contents on
+ *                  entry ignored; calls that may overlap need one each
+ * Results stand in the order taken, or with GDR_KEEP_SLOTS (M = K): the first taken
+ * continuation of a beam in the beam's own place, the others, in order, in the places
+ * left: then what a beam has (its state, its table's row) moves only where it has to.
+ * Log-sums are formed in fp32 from each row's maximum and joined in 64 bits; scores are
+ * compared in 64 bits and rounded once.  Supported: K, M <= 64, M <= K V.
+ */
+size_t gdr_beam_select_workspace_bytes(int G, int K, int M, int V);
+
+gdr_status gdr_beam_select(const void* logits, const float* scores, const uint8_t* ended,
+                           int* tokens, int* rows, float* scores_out, uint8_t* ended_out, int G,
+                           int K, int M, int V, long long stride, int end_token, uint32_t flags,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * States moved to the rows that continue them, in place: state[l][n] becomes what
+ * state[l][parent[n]] was, for rows of any type.  Rows n = g K .. g K + K - 1 are a group,
+ * and parent[n] is in n's group; a row whose parent is not, or is itself, stays as it is
+ * and costs nothing.
+ *   state  : [layers, N, row_bytes], row_bytes a multiple of 16
+ *   parent : int32 [N] in device memory (gdr_beam_select's rows, M = K)
+ * flags must be 0.  Supported: K <= 64, N a multiple of K.
+ */
+gdr_status gdr_state_reorder(void* state, const int* parent, int layers, int N, int K,
+                             size_t row_bytes, uint32_t flags, void* stream);
 
 #ifdef __cplusplus
 }
