@@ -657,8 +657,7 @@ gdr_status gdr_attn_decode(const void* q, const void* k_cache, const void* v_cac
 
 size_t gdr_attn_decode_shared_workspace_bytes(int N, int groups, int Hq, int Hkv, int d, int max_pages, int window) {
     if (decode_args(N, Hq, Hkv, d, 1, max_pages, window, 1.f, 0) != GDR_OK || groups < 1 || groups > (1 << 28)) return 0;
-    const gdr::SharedPlan x = gdr::attn_shared_plan(N, groups, Hq, Hkv, max_pages, window);
-    return (size_t)(x.shared_splits + x.own_splits) * N * Hq * (d + 2) * sizeof(float);
+    return gdr::attn_shared_plan(N, groups, Hq, Hkv, d, max_pages, window).bytes;
 }
 
 gdr_status gdr_attn_decode_shared(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
@@ -669,14 +668,13 @@ gdr_status gdr_attn_decode_shared(const void* q, const void* k_cache, const void
     const gdr_status st = decode_args(N, Hq, Hkv, d, n_pages, max_pages, window, scale, flags);
     if (st != GDR_OK) return st;
     if (groups < 1 || groups > (1 << 28)) return GDR_ERR_INVALID_ARG;
-    const gdr::SharedPlan x = gdr::attn_shared_plan(N, groups, Hq, Hkv, max_pages, window);
-    if (!grid_ok(gdr::attn_shared_workgroups(x, Hkv, (long long)N * Hq))) return GDR_ERR_INVALID_ARG;
+    const gdr::SharedPlan x = gdr::attn_shared_plan(N, groups, Hq, Hkv, d, max_pages, window);
+    if (!grid_ok(gdr::attn_shared_workgroups(x, (long long)N * Hq))) return GDR_ERR_INVALID_ARG;
     const void* ptrs[] = {q, k_cache, v_cache, k_scale, v_scale, block_table, cache_len, group_start, shared_pages, o};
     for (const void* ptr : ptrs)
         if (!ptr || !aligned16(ptr)) return GDR_ERR_INVALID_ARG;
     if (workspace && !aligned16(workspace)) return GDR_ERR_INVALID_ARG;
-    if (!workspace || workspace_bytes < gdr_attn_decode_shared_workspace_bytes(N, groups, Hq, Hkv, d, max_pages, window))
-        return GDR_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < x.bytes) return GDR_ERR_WORKSPACE;
     gdr_status ds = check_device();
     if (ds != GDR_OK) return ds;
     gdr::SharedParams p;
@@ -685,9 +683,16 @@ gdr_status gdr_attn_decode_shared(const void* q, const void* k_cache, const void
     p.k_scale = k_scale; p.v_scale = v_scale; p.block_table = block_table; p.cache_len = cache_len;
     p.group_start = group_start; p.shared_pages = shared_pages; p.o = o;
     p.N = N; p.groups = groups; p.Hq = Hq; p.Hkv = Hkv; p.d = d; p.n_pages = n_pages; p.max_pages = max_pages;
-    p.window = window; p.tiles = x.tiles; p.shared_splits = x.shared_splits; p.own_splits = x.own_splits;
-    p.part_o = static_cast<float*>(workspace);
-    p.part_ml = p.part_o + (size_t)(x.shared_splits + x.own_splits) * N * Hq * d;
+    p.window = window; p.across = x.across; p.items = (int)x.items; p.own_splits = x.own_splits;
+    char* ws = static_cast<char*>(workspace);
+    p.plan_head = reinterpret_cast<int*>(ws + x.at_head);
+    p.plan_groups = ws + x.at_groups;
+    p.plan_group_of = reinterpret_cast<int*>(ws + x.at_group_of);
+    p.plan_items = reinterpret_cast<int*>(ws + x.at_items);
+    p.part_o = reinterpret_cast<float*>(ws + x.at_part_o);
+    p.part_ml = reinterpret_cast<float*>(ws + x.at_part_ml);
+    p.own_o = reinterpret_cast<float*>(ws + x.at_own_o);
+    p.own_ml = reinterpret_cast<float*>(ws + x.at_own_ml);
     p.scale = scale; p.flags = flags;
     return from_hip(gdr::launch_attn_shared(p, x, (hipStream_t)stream));
 }

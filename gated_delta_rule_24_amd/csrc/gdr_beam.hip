@@ -401,6 +401,8 @@ hipError_t launch_beam_select(const BeamParams& p, hipStream_t st) {
 // another's source and itself be replaced.  Rows that keep their own state cost nothing,
 // which is most of them where the beams that live on stay in their rows.
 namespace {
+typedef uint32_t uint2v __attribute__((ext_vector_type(2)));
+typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
 template <int KT, typename V>
 __global__ __launch_bounds__(kThreads) void reorder_kernel(ReorderParams p, int blocks, int groups) {
     long long b = blockIdx.x;
@@ -410,11 +412,20 @@ __global__ __launch_bounds__(kThreads) void reorder_kernel(ReorderParams p, int 
     if (column * (long long)sizeof(V) >= p.row_bytes) return;
     uint8_t* at = p.state + ((long long)layer * p.N + (long long)g * p.K) * p.row_bytes + column * sizeof(V);
     const int* parent = p.parent + (long long)g * p.K;
+    // a row that stays is read as one that moves, whose bytes are at hand: loads without
+    // a branch, all in flight together
+    int moved = -1;
+#pragma unroll
+    for (int k = 0; k < KT; ++k) {
+        const int from = k < p.K ? parent[k] - g * p.K : k;
+        if (from != k && (unsigned)from < (unsigned)p.K) moved = from;
+    }
+    if (moved < 0) return;
     V x[KT];
 #pragma unroll
     for (int k = 0; k < KT; ++k) {
         const int from = k < p.K ? parent[k] - g * p.K : k;
-        if (from != k && (unsigned)from < (unsigned)p.K) x[k] = *reinterpret_cast<const V*>(at + from * p.row_bytes);
+        x[k] = *reinterpret_cast<const V*>(at + (from != k && (unsigned)from < (unsigned)p.K ? from : moved) * p.row_bytes);
     }
 #pragma unroll
     for (int k = 0; k < KT; ++k) {
@@ -436,11 +447,11 @@ long long state_reorder_workgroups(int layers, int N, int K, long long row_bytes
 hipError_t launch_state_reorder(const ReorderParams& p, hipStream_t st) {
     const int blocks = reorder_blocks(p.K, p.row_bytes), groups = p.N / p.K;
     const dim3 grid((unsigned)state_reorder_workgroups(p.layers, p.N, p.K, p.row_bytes)), block(kThreads);
-    if (p.K <= 4) hipLaunchKernelGGL((reorder_kernel<4, uint4>), grid, block, 0, st, p, blocks, groups);
-    else if (p.K <= 8) hipLaunchKernelGGL((reorder_kernel<8, uint4>), grid, block, 0, st, p, blocks, groups);
-    else if (p.K <= 16) hipLaunchKernelGGL((reorder_kernel<16, uint4>), grid, block, 0, st, p, blocks, groups);
-    else if (p.K <= 32) hipLaunchKernelGGL((reorder_kernel<32, uint4>), grid, block, 0, st, p, blocks, groups);
-    else hipLaunchKernelGGL((reorder_kernel<64, uint2>), grid, block, 0, st, p, blocks, groups);
+    if (p.K <= 4) hipLaunchKernelGGL((reorder_kernel<4, uint4v>), grid, block, 0, st, p, blocks, groups);
+    else if (p.K <= 8) hipLaunchKernelGGL((reorder_kernel<8, uint4v>), grid, block, 0, st, p, blocks, groups);
+    else if (p.K <= 16) hipLaunchKernelGGL((reorder_kernel<16, uint4v>), grid, block, 0, st, p, blocks, groups);
+    else if (p.K <= 32) hipLaunchKernelGGL((reorder_kernel<32, uint4v>), grid, block, 0, st, p, blocks, groups);
+    else hipLaunchKernelGGL((reorder_kernel<64, uint2v>), grid, block, 0, st, p, blocks, groups);
     return hipGetLastError();
 }
 

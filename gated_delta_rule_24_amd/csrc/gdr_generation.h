@@ -36,13 +36,14 @@ long long kv_compact_workgroups(int N, int n_pages, int max_pages);
 hipError_t launch_kv_fork(const PagesParams& p, hipStream_t st);
 hipError_t launch_kv_compact(const PagesParams& p, hipStream_t st);
 
-// How a call of attention over shared pages is dealt out; from host values only.
+// How a call of attention over shared pages is dealt out, from what the host knows, and
+// where the parts of its workspace start.
 struct SharedPlan {
-    int columns;                // rows of a workgroup
-    int tiles;                  // workgroups a key head's rows of all groups take, at most
-    int shared_splits;          // runs that a group's shared pages are dealt into
-    int own_splits;             // runs of a sequence's own pages
-    long long own_items;        // (sequence, key head, set of query heads)
+    int across;                 // waves of a workgroup with different rows (32 each) on the same pages
+    long long items;            // workgroups for the shared pages, at most
+    long long own_items;        // (sequence, key head, set of 16 query heads)
+    int own_splits;             // runs that a sequence's own pages are dealt into
+    size_t at_head, at_groups, at_group_of, at_items, at_part_o, at_part_ml, at_own_o, at_own_ml, bytes;
 };
 struct SharedParams {
     const void* q;
@@ -55,15 +56,21 @@ struct SharedParams {
     const int* group_start;     // [groups + 1]
     const int* shared_pages;    // [groups]
     void* o;
-    float* part_o;              // [shared_splits + own_splits, N, Hq, d] unnormalised
-    float* part_ml;             // the same without d, 2: maximum (base 2) and sum
+    int* plan_head;             // [2] items, pages of a run
+    void* plan_groups;          // [groups]
+    int* plan_group_of;         // [N] a sequence's group, or -1
+    int* plan_items;            // [items] an item's group
+    float* part_o;              // [items, 32 across, d] unnormalised
+    float* part_ml;             // [items, 32 across, 2] maximum (base 2) and sum
+    float* own_o;               // [own_splits, N, Hq, d] and its maxima and sums, where own_splits > 1
+    float* own_ml;
     int N, groups, Hq, Hkv, d, n_pages, max_pages, window;
-    int tiles, shared_splits, own_splits;
+    int across, items, own_splits;
     float scale;
     uint32_t flags;
 };
-SharedPlan attn_shared_plan(int N, int groups, int Hq, int Hkv, int max_pages, int window);
-long long attn_shared_workgroups(const SharedPlan& x, int Hkv, long long heads);
+SharedPlan attn_shared_plan(int N, int groups, int Hq, int Hkv, int d, int max_pages, int window);
+long long attn_shared_workgroups(const SharedPlan& x, long long heads);
 hipError_t launch_attn_shared(const SharedParams& p, const SharedPlan& x, hipStream_t st);
 
 constexpr int kMostBeams = 64, kMostSelected = 64;

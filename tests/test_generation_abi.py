@@ -33,8 +33,10 @@ def test_attn_decode_shared_refusals(kw, status):
 def test_attn_decode_shared_workspace_query():
     f = _lib().gdr_attn_decode_shared_workspace_bytes
     one = f(8, 1, 32, 8, 128, 800, 0)
-    assert one > 0 and one % ((128 + 2) * 8 * 32 * 4) == 0   # per partial result: an output row, its maximum and sum
-    assert f(8, 1, 32, 8, 128, 800, 64) < one                # a window bounds the pages read
+    # a partial result of 32 rows, their maxima and sums, for each of 256 workgroups, and more
+    assert one > 256 * 32 * (128 + 2) * 4
+    assert f(8, 1, 32, 8, 128, 800, 64) < one                # a window bounds a sequence's own pages
+    assert f(256, 1, 32, 8, 128, 800, 0) > 512 * 128 * (128 + 2) * 4
     for bad in ((0, 1, 32, 8, 128, 8, 0), (8, 0, 32, 8, 128, 8, 0), (8, 1, 31, 8, 128, 8, 0), (8, 1, 32, 8, 96, 8, 0),
                 (8, 1, 32, 8, 128, 8, -1)):
         assert f(*bad) == 0
