@@ -39,7 +39,7 @@ hipError_t launch_kv_compact(const PagesParams& p, hipStream_t st);
 // How a call of attention over shared pages is dealt out, from what the host knows, and
 // where the parts of its workspace start.
 struct SharedPlan {
-    int across;                 // waves of a workgroup with different rows (32 each) on the same pages
+    int width;                  // rows of a workgroup for shared pages: 32 or 64
     long long items;            // workgroups for the shared pages, at most
     long long own_items;        // (sequence, key head, set of 16 query heads)
     int own_splits;             // runs that a sequence's own pages are dealt into
@@ -60,12 +60,12 @@ struct SharedParams {
     void* plan_groups;          // [groups]
     int* plan_group_of;         // [N] a sequence's group, or -1
     int* plan_items;            // [items] an item's group
-    float* part_o;              // [items, 32 across, d] unnormalised
-    float* part_ml;             // [items, 32 across, 2] maximum (base 2) and sum
+    float* part_o;              // [items, width, d] unnormalised
+    float* part_ml;             // [items, width, 2] maximum (base 2) and sum
     float* own_o;               // [own_splits, N, Hq, d] and its maxima and sums, where own_splits > 1
     float* own_ml;
     int N, groups, Hq, Hkv, d, n_pages, max_pages, window;
-    int across, items, own_splits;
+    int width, items, own_splits;
     float scale;
     uint32_t flags;
 };

@@ -25,6 +25,8 @@ namespace {
 
 constexpr int kPage = 64;
 constexpr int kWaves = 4;
+// Weights reach 2^(kTop + kLag) = 2^15 at most: f16 has room for that.
+constexpr float kLag = 3.f, kTop = 12.f;
 
 __device__ __forceinline__ int clampi(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
 
@@ -58,6 +60,19 @@ __device__ __forceinline__ void store_out(const SharedParams& p, size_t idx, flo
     if (p.flags & GDR_OUT_BF16) reinterpret_cast<uint16_t*>(p.o)[idx] = f32_to_bf16(x);
     else reinterpret_cast<float*>(p.o)[idx] = x;
 }
+
+// bits i of 0 .. 31: key `base` + 32 (i / 16) + i % 16 is one of lo .. hi - 1
+__device__ __forceinline__ uint32_t seen_bits(int base, int lo, int hi) {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        const int from = clampi(lo - base - 32 * b, 0, 16), to = clampi(hi - base - 32 * b, 0, 16);
+        bits |= (((1u << to) - 1) & ~((1u << from) - 1)) << (16 * b);
+    }
+    return bits;
+}
+// bytes 0xff where the four bits from i on are set
+__device__ __forceinline__ uint32_t bytes_of(uint32_t bits, int i) { return (((bits >> i) & 15u) * 0x00204081u & 0x01010101u) * 0xffu; }
 
 // e4m3 bytes that are NaN (0x7f, 0xff), as 0x80 in their places
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
@@ -121,7 +136,7 @@ __device__ __forceinline__ long long plan_sum(long long x, long long* s) {
 __global__ __launch_bounds__(kPlanThreads) void attn_shared_plan_kernel(SharedParams p) {
     __shared__ long long s_sum[kPlanThreads / 64];
     __shared__ int s_most, s_end;                     // pages of the longest prefix; items that have a group
-    const int tid = threadIdx.x, lane = tid & 63, rep = p.Hq / p.Hkv, width = 32 * p.across;
+    const int tid = threadIdx.x, lane = tid & 63, rep = p.Hq / p.Hkv, width = p.width;
     Group* groups = reinterpret_cast<Group*>(p.plan_groups);
     for (int n = tid; n < p.N; n += kPlanThreads) p.plan_group_of[n] = -1;
     if (tid == 0) { s_most = 0; s_end = INT_MAX; }
@@ -158,7 +173,7 @@ __global__ __launch_bounds__(kPlanThreads) void attn_shared_plan_kernel(SharedPa
     long long all = 0;
     for (int g = tid; g < p.groups; g += kPlanThreads) all += (long long)groups[g].tiles * (groups[g].pg1 - groups[g].pg0);
     all = plan_sum(all, s_sum) * p.Hkv;
-    const int most = s_most, least = 2 * kWaves / p.across;
+    const int most = s_most, least = 2 * kWaves;   // two pages a wave
     int per = (int)min((all + p.items - 1) / p.items, (long long)INT_MAX);
     per = max(per, least);
     while (per < most) {
@@ -215,31 +230,31 @@ __global__ __launch_bounds__(kPlanThreads) void attn_shared_plan_kernel(SharedPa
 // the shared pages
 // ---------------------------------------------------------------------------
 //
-// A wave has 32 rows of a group on a key head (row r being query head r % rep of sequence
+// Rows of a group on a key head (row r being query head r % rep of sequence
 // first + r / rep), as the columns of 32 x 32 products:
 //   S^T[key][row] = K Q^T, O^T[channel][row] += V^T W^T.
 // Row m of S^T stands for key 16 (m / 4 % 2) + 4 (m / 8) + m % 4 of 32, which leaves lane half
 // h with the keys 16 h .. 16 h + 15: those of its 16-byte reads of values, a channel each.
 //
-// ACROSS waves of a workgroup have different rows and share their pages, the teams of
-// them take pages in turn.  Pages come through a ring in LDS of R pages a team, as they
-// lie in memory, by direct loads R - 1 pages ahead (no registers, 1 KiB an instruction;
-// read straight to registers in the operands' order, 16 bytes a lane from 32 rows, the same
-// walk took 3 times as long).  A key's row keeps its 16-byte units u at u ^ f(row), so that
-// the 16 rows of a read phase land on 16 different places of the banks' 256 bytes.
+// A wave has 64 rows (32 where groups are smaller): what a page costs beside its products,
+// its bytes' conversion above all, is then shared by as many.  The waves of a workgroup
+// have the same rows and take pages in turn, each for itself: with waves that shared
+// a page and waited for each other at every one, 1,024 rows on 512 pages took 215 us for
+// 181.  Pages come through two places in LDS a wave, as they lie in memory, by direct loads a
+// page ahead (no registers, 1 KiB an instruction): read straight to registers in the
+// operands' order, 16 bytes a lane from 32 rows, the same walk took 265.  A key's row keeps its 16-byte units u at u ^ f(row), so that the 16 rows of a
+// read phase land on 16 different places of the banks' 256 bytes.
 //
-// A weight is exp2(s - m).  For the product with v it is taken times 2^b, b = 15 +
+// A weight is exp2(s - m).  For the product with v it is taken times 2^b, b = 12 +
 // log2 v_scale + m - wm, wm the running maximum of s + log2 v_scale, so that it has
 // its f16 bits whatever the pages' scales: as the sum of two f16 values (22 bits) for
 // fp32 results, as one (11 bits) for bf16 ones, whose own rounding is 8 times that.  The
 // sum takes the same exponentials, times 2^-b once a page; where |b| is large (a page of
 // zeros has a scale of 2^-96) it has its own.
-template <int D, int ACROSS>
+template <int D>
 struct __attribute__((aligned(256))) SharedSmem {
-    static constexpr int TEAMS = kWaves / ACROSS;
-    static constexpr int R = ACROSS == 4 ? 4 : 2;
     union {
-        uint8_t ring[TEAMS][R][2 * kPage * D];        // keys [64][D], then values [4][D][16]
+        uint8_t ring[kWaves][2][2 * kPage * D];       // keys [64][D], then values [4][D][16]
         struct {
             float o[kWaves][32][D + 4];
             float ml[kWaves][32][2];
@@ -247,12 +262,11 @@ struct __attribute__((aligned(256))) SharedSmem {
     };
 };
 
-// A page's loads by one wave of the team that shares it: 16-byte direct loads, a KiB of
-// keys or values each.
-template <int D, int ACROSS>
+// One side of a page into LDS by a wave: 16-byte direct loads, a KiB each.
+template <int D>
 struct PageLoader {
-    static constexpr int KI = kPage * D / 1024, N = 2 * KI / ACROSS;      // loads of a side; of a wave
-    int off;                                          // lane's source inside a KiB of keys, before the instruction's flip
+    static constexpr int N = kPage * D / 1024;        // loads of a side
+    int off;                                          // a lane's place in a KiB of keys, before the instruction's flip
     int lane16;
 
     __device__ __forceinline__ explicit PageLoader(int lane) {
@@ -261,30 +275,24 @@ struct PageLoader {
         off = (lane / CH) * D + 16 * ((lane % CH) ^ f);
         lane16 = 16 * lane;
     }
-    template <int I> __device__ __forceinline__ void issue(uint64_t k, uint64_t v, uint32_t to, int first) const {
-        if constexpr (I < N) {
-            // (a wave's loads are all of one side where two or four waves share a page)
-            const int i = first + I;
-            const bool keys = ACROSS == 1 ? I < KI : first < KI;
-            const int flip = D == 128 ? ((i >> 1) & 1) << 6 : (i & 1) << 5;
-            attn::direct_load16<0>((keys ? off ^ flip : lane16) + 1024 * (keys ? i : i - KI), keys ? k : v, to + 1024 * i);
-            issue<I + 1>(k, v, to, first);
-        }
+    template <int I = 0> __device__ __forceinline__ void keys(uint64_t from, uint32_t to) const {
+        constexpr int flip = D == 128 ? ((I >> 1) & 1) << 6 : (I & 1) << 5;
+        attn::direct_load16<1024 * I>((off ^ flip) + 1024 * I, from, to);
+        if constexpr (I + 1 < N) keys<I + 1>(from, to);
+    }
+    template <int I = 0> __device__ __forceinline__ void values(uint64_t from, uint32_t to) const {
+        attn::direct_load16<1024 * I>(lane16 + 1024 * I, from, to);
+        if constexpr (I + 1 < N) values<I + 1>(from, to);
     }
 };
 
-template <int N> __device__ __forceinline__ void wait_loads_but() {
-    __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | ((N >> 4) << 14));     // vmcnt(N)
-}
-
-template <int D, int PARTS, int ACROSS>
-__global__ __launch_bounds__(64 * kWaves, ACROSS == 1 ? 1 : 2) void attn_shared_kernel(SharedParams p) {
+template <int D, int PARTS, int NB>
+__global__ __launch_bounds__(64 * kWaves, 1) void attn_shared_kernel(SharedParams p) {
     constexpr int KL = D / 32;                        // 16-byte reads of a key's row by a lane
     constexpr int DB = D / 32;                        // 32-channel tiles of the output
-    typedef SharedSmem<D, ACROSS> Smem;
-    constexpr int R = Smem::R, TEAMS = Smem::TEAMS;
+    constexpr int kRows = 32 * NB;                    // of the workgroup: its waves have the same ones
     extern __shared__ __attribute__((aligned(256))) char smem[];
-    Smem& sm = *reinterpret_cast<Smem*>(smem);
+    SharedSmem<D>& sm = *reinterpret_cast<SharedSmem<D>*>(smem);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 31, h = lane >> 5, rep = p.Hq / p.Hkv;
 
@@ -295,33 +303,64 @@ __global__ __launch_bounds__(64 * kWaves, ACROSS == 1 ? 1 : 2) void attn_shared_
     if ((int)(blockIdx.x / 8) >= each || item >= items) return;
     const Group x = group_of(p, p.plan_items[item]);
     const int per = p.plan_head[1];
-    int w = item - x.base;
-    const int tile = w % x.tiles; w /= x.tiles;
-    const int kh = w % p.Hkv, slot = w / p.Hkv;
-    const int row0 = 32 * ACROSS * tile, rows = min(32 * ACROSS, x.rows - row0);
-    const int wr = wave % ACROSS, team = wave / ACROSS;
+    int rest = item - x.base;
+    const int tile = rest % x.tiles; rest /= x.tiles;
+    const int kh = rest % p.Hkv, slot = rest / p.Hkv;
+    const int row0 = kRows * tile, rows = min(kRows, x.rows - row0);
     const int pg0 = x.pg0 + slot * per, pg1 = min(pg0 + per, x.pg1);
-    const int turns = (pg1 - pg0 + TEAMS - 1) / TEAMS;                    // of every team
-    const int n = max(0, (pg1 - pg0 - team + TEAMS - 1) / TEAMS);         // pages of this one
+    const int n = max(0, (pg1 - pg0 - wave + kWaves - 1) / kWaves);      // pages of this wave
 
-    // this lane's row: its query (channels 32 s + 16 h .. + 15) and the keys it sees
-    const int mine = 32 * wr + col;
-    const bool live = mine < rows;
-    const int seq = x.first + (row0 + mine) / rep, head = kh * rep + (row0 + mine) % rep;
-    bf8v qf[KL][2];
+    // this wave's pages k0 .. k0 + 63, one a lane: place (-1: absent) and scales
+    const int* entries = p.block_table + (size_t)x.first * p.max_pages + pg0 + wave;
+    int e_page;
+    float e_ks, e_vs;
+    auto look_up = [&](int k0) {
+        const int k = k0 + lane;
+        const int e = k < n ? entries[k * kWaves] : -1;
+        e_page = (unsigned)e < (unsigned)p.n_pages ? e : -1;
+        const size_t ph = (size_t)max(e_page, 0) * p.Hkv + kh;
+        e_ks = p.k_scale[ph];
+        e_vs = p.v_scale[ph];
+    };
+    const PageLoader<D> loader(lane);
+    const uint32_t ring = attn::lds_address(sm.ring[wave][0]);
+    constexpr uint32_t kSide = kPage * D;
+    // (an absent page is read as the first one: its bytes are masked)
+    auto load = [&](int k) {
+        const int pg = __builtin_amdgcn_readlane(e_page, k & 63);
+        const size_t at = ((size_t)max(pg, 0) * p.Hkv + kh) * kSide;
+        const uint32_t to = ring + (k & 1) * (2 * kSide);
+        loader.keys((uint64_t)p.k_cache + at, to);
+        loader.values((uint64_t)p.v_cache + at, to + kSide);
+    };
+    look_up(0);
+    if (n > 0) load(0);
+
+    // this lane's rows: their queries (channels 32 s + 16 h .. + 15) and the keys they see
+    bf8v qf[NB][KL][2];
+    int lo[NB], hi[NB], lo_most = 0, hi_least = INT_MAX, lo_least = INT_MAX, hi_most = 0;
 #pragma unroll
-    for (int s = 0; s < KL; ++s)
+    for (int c = 0; c < NB; ++c) {
+        const int mine = 32 * c + col;
+        const bool live = mine < rows;
+        const int seq = x.first + (row0 + mine) / rep, head = kh * rep + (row0 + mine) % rep;
 #pragma unroll
-        for (int f = 0; f < 2; ++f) {
-            uint4 u = make_uint4(0, 0, 0, 0);
-            if (live) u = *reinterpret_cast<const uint4*>((const uint16_t*)p.q + ((size_t)seq * p.Hq + head) * D + 32 * s + 16 * h + 8 * f);
-            qf[s][f] = __builtin_bit_cast(bf8v, u);
+        for (int s = 0; s < KL; ++s)
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                uint4 u = make_uint4(0, 0, 0, 0);
+                if (live)
+                    u = *reinterpret_cast<const uint4*>((const uint16_t*)p.q + ((size_t)seq * p.Hq + head) * D + 32 * s + 16 * h + 8 * f);
+                qf[c][s][f] = __builtin_bit_cast(bf8v, u);
+            }
+        lo[c] = hi[c] = 0;
+        if (live) {
+            seen_range(p, seq, lo[c], hi[c]);
+            lo_most = max(lo_most, lo[c]);
+            lo_least = min(lo_least, lo[c]);
+            hi_least = min(hi_least, hi[c]);
+            hi_most = max(hi_most, hi[c]);
         }
-    int lo = 0, hi = 0, lo_most = 0, hi_least = INT_MAX, lo_least = INT_MAX, hi_most = 0;
-    if (live) {
-        seen_range(p, seq, lo, hi);
-        lo_most = lo_least = lo;
-        hi_least = hi_most = hi;
     }
     for (int o = 16; o > 0; o >>= 1) {
         lo_most = max(lo_most, __shfl_xor(lo_most, o, 64));
@@ -332,34 +371,16 @@ __global__ __launch_bounds__(64 * kWaves, ACROSS == 1 ? 1 : 2) void attn_shared_
     lo_most = __builtin_amdgcn_readfirstlane(lo_most);
     hi_least = __builtin_amdgcn_readfirstlane(hi_least);
 
-    // the team's pages k0 .. k0 + 63, one a lane: place (-1: absent) and scales
-    const int* entries = p.block_table + (size_t)x.first * p.max_pages + pg0 + team;
-    int e_page;
-    float e_ks, e_vs;
-    auto look_up = [&](int k0) {
-        const int k = k0 + lane;
-        const int e = k < n ? entries[k * TEAMS] : -1;
-        e_page = (unsigned)e < (unsigned)p.n_pages ? e : -1;
-        const size_t ph = (size_t)max(e_page, 0) * p.Hkv + kh;
-        e_ks = p.k_scale[ph];
-        e_vs = p.v_scale[ph];
-    };
-    const PageLoader<D, ACROSS> loader(lane);
-    const uint32_t ring = attn::lds_address(sm.ring[team][0]);
-    constexpr uint32_t kBytes = 2 * kPage * D;
-    // (an absent page is read as the first one: its bytes are masked)
-    auto load_page = [&](int k) {
-        const int pg = __builtin_amdgcn_readlane(e_page, k & 63);
-        const size_t at = ((size_t)max(pg, 0) * p.Hkv + kh) * (kPage * D);
-        loader.template issue<0>((uint64_t)p.k_cache + at, (uint64_t)p.v_cache + at, ring + (k % R) * kBytes, wr * loader.N);
-    };
-
-    float16v o[DB];
+    float16v o[NB][DB];
+    float m[NB], l[NB], wm[NB];                       // maximum and sum of the scores; maximum of the weights
 #pragma unroll
-    for (int i = 0; i < DB; ++i)
+    for (int c = 0; c < NB; ++c) {
+        m[c] = -INFINITY; l[c] = 0.f; wm[c] = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) o[i][j] = 0.f;
-    float m = -INFINITY, l = 0.f, wm = -INFINITY;     // maximum and sum of the scores; maximum of the weights
+        for (int i = 0; i < DB; ++i)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[c][i][j] = 0.f;
+    }
     const float to2 = p.scale * 1.4426950408889634f;
     uint32_t k_at, v_at;                              // this lane's reads: of keys, to flip by 32 s; of values
     {
@@ -371,196 +392,222 @@ __global__ __launch_bounds__(64 * kWaves, ACROSS == 1 ? 1 : 2) void attn_shared_
     typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
     auto read16 = [](uint32_t at) { return *(const __attribute__((address_space(3))) uint4v*)(uintptr_t)at; };
 
-    look_up(0);
-    int old_page = 0;                                 // of the 64 pages before, while some of them are still to come
-    float old_ks = 0.f, old_vs = 0.f;
-    for (int k = 0; k < R - 1; ++k)
-        if (k < n) load_page(k);
-    for (int k = 0; k < turns; ++k) {
-        const int ahead = k + R - 1;
-        if (ahead < n) wait_loads_but<(R - 2) * PageLoader<D, ACROSS>::N>();
-        else attn::wait_loads();
-        if (ACROSS > 1) lds_barrier();
-        // the ring's place of page k - 1 is free: its reads are done
-        if (ahead < n) {
-            if ((ahead & 63) == 0) {
-                old_page = e_page;
-                old_ks = e_ks;
-                old_vs = e_vs;
-                look_up(ahead);
-            }
-            if (ACROSS == 1) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            load_page(ahead);
-        }
-        if (k >= n || 32 * wr >= rows) continue;      // no page, or no rows
-        const bool before = (min(ahead, n - 1) >> 6) != (k >> 6);
-        const int page = __builtin_amdgcn_readlane(before ? old_page : e_page, k & 63);
-        const float ks = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(before ? old_ks : e_ks), k & 63));
-        const float vs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(before ? old_vs : e_vs), k & 63));
-        const int at0 = (pg0 + team + k * TEAMS) * kPage;
+    uint32_t nans = 0;                                // some value that not every row sees is NaN
+    for (int k = 0; k < n; ++k) {
+        const int page = __builtin_amdgcn_readlane(e_page, k & 63);
+        const float ks = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(e_ks), k & 63));
+        const float vs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(e_vs), k & 63));
+        const int at0 = (pg0 + wave + k * kWaves) * kPage;
         const bool absent = page < 0;
-        const uint32_t ring_k = ring + (k % R) * kBytes + k_at, ring_v = ring + (k % R) * kBytes + v_at;
+        const uint32_t ring_k = ring + (k & 1) * (2 * kSide) + k_at, ring_v = ring + (k & 1) * (2 * kSide) + v_at;
+        // this page is there, and the place of the one before it is free: its reads are done
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        if (k + 1 < n) {
+            if (((k + 1) & 63) == 0) look_up(k + 1);
+            load(k + 1);
+        }
+
+        uint4v kr[2][KL];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int s = 0; s < KL; ++s) kr[b][s] = read16((ring_k ^ (32 * s)) + 32 * b * D);
+        float16v st[NB][2];
+#pragma unroll
+        for (int c = 0; c < NB; ++c)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) st[c][b][j] = 0.f;
+#pragma unroll
+        for (int s = 0; s < KL; ++s)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const bf8v k0 = e4m3x8_to_bf16(kr[b][s].x, kr[b][s].y), k1 = e4m3x8_to_bf16(kr[b][s].z, kr[b][s].w);
+#pragma unroll
+                for (int c = 0; c < NB; ++c) st[c][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k0, qf[c][s][0], st[c][b], 0, 0, 0);
+#pragma unroll
+                for (int c = 0; c < NB; ++c) st[c][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k1, qf[c][s][1], st[c][b], 0, 0, 0);
+            }
+        uint4v vr[2][DB];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int i = 0; i < DB; ++i) vr[b][i] = read16(ring_v + (2 * b * D + 32 * i) * 16);
 
         float by = ks * to2;                          // a score is st times this
-        float16v st[2];
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) st[b][j] = 0.f;
-#pragma unroll
-            for (int s = 0; s < KL; ++s) {
-                const uint4v u = read16((ring_k ^ (32 * s)) + 32 * b * D);
-                st[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3x8_to_bf16(u.x, u.y), qf[s][0], st[b], 0, 0, 0);
-                st[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3x8_to_bf16(u.z, u.w), qf[s][1], st[b], 0, 0, 0);
-            }
-        }
         const bool edge = absent || at0 < lo_most || at0 + kPage > hi_least;
         if (edge || !(by >= 0.f)) {
             // (negative scales turn the order of the scores; masked ones stay -inf whatever the scale)
             asm volatile("");
 #pragma unroll
-            for (int b = 0; b < 2; ++b) st[b] *= by;
+            for (int c = 0; c < NB; ++c)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    st[c][b] *= by;
+                    if (edge) {
+                        const uint32_t sees = absent ? 0 : seen_bits(at0 + 16 * h, lo[c], hi[c]);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) st[c][b][i] = sees >> (16 * b + i) & 1 ? st[c][b][i] : -INFINITY;
+                    }
+                }
             by = 1.f;
-        }
-        if (edge) {
+            if (edge) {
+                // some row sees the page in part: values of keys that no row sees count as 0,
+                // and so do NaNs, which the 0 of a row that does not see them would carry
+                // over: the rows that see them get them at the end
+                const uint32_t some = absent ? 0 : seen_bits(at0 + 16 * h, lo_least, hi_most);
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+                for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int j = at0 + 32 * b + 16 * h + i;
-                    if (absent || j < lo || j >= hi) st[b][i] = -INFINITY;
-                }
-        }
-
-        float top = st[0][0];
+                    for (int t = 0; t < 4; ++t) {
+                        const uint32_t keep = bytes_of(some, 16 * b + 4 * t);
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) top = fmaxf(top, st[b][i]);
-        top = max_across32(top);
-        const bool none = !(top > -INFINITY);         // (the scale of a page that a row does not see does not reach it)
-        top = none ? -INFINITY : top * by;
-        const float log_vs = __builtin_amdgcn_logf(vs);   // base 2
-        const float wt = none ? wm : fmaxf(wm, top + log_vs);
-        top = fmaxf(top, m);
-        if (__any(top > m || wt > wm)) {
-            asm volatile("");
-            l *= top > m ? __builtin_amdgcn_exp2f(m - top) : 1.f;      // 0 from -inf
-            const float fade = wt > wm ? __builtin_amdgcn_exp2f(wm - wt) : 1.f;
-            m = top;
-            wm = wt;
-#pragma unroll
-            for (int i = 0; i < DB; ++i) o[i] *= fade;
-        }
-        const float at = m == -INFINITY ? 0.f : m, wat = wm == -INFINITY ? 0.f : wm;
-        const float up = none ? 0.f : log_vs - wat + 15.f;      // a weight's exponent over its score's
-        const float b2 = up + at;
-        half8 w_hi[2][2], w_lo[2][2];
-        float sum[2] = {0.f, 0.f};
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(st[b][i], by, up));
-                sum[b] += w;
-                const _Float16 a = (_Float16)w;
-                w_hi[b][i / 8][i % 8] = a;
-                if (PARTS == 2) w_lo[b][i / 8][i % 8] = (_Float16)(w - (float)a);
+                        for (int i = 0; i < DB; ++i) {
+                            uint32_t y = vr[b][i][t] & keep;
+                            const uint32_t whole = (nan_bytes(y) >> 7) * 0xffu;
+                            nans |= whole;
+                            vr[b][i][t] = y & ~whole;
+                        }
+                    }
             }
-        if (!__any(!none && !(fabsf(b2) <= 60.f))) {
-            l += (sum[0] + sum[1]) * (none ? 0.f : __builtin_amdgcn_exp2f(-b2));
-        } else {
-            float y = 0.f;
+        }
+
+        // The maxima are followed when they are more than 2^kLag ahead, each row's by itself
+        // (the roundings of a row do not depend on keys that only its neighbours see): in
+        // most pages some row of 32 has a new one, and o would be scaled anew.
+        const float log_vs = __builtin_amdgcn_logf(vs);   // base 2
+        float top[NB];
+        bool none[NB], ahead_m[NB], ahead_w[NB], any = false;
+#pragma unroll
+        for (int c = 0; c < NB; ++c) {
+            top[c] = st[c][0][0];
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    y += __builtin_amdgcn_exp2f(__builtin_fmaf(st[b][i], by, -at));
-                    asm volatile("" : "+v"(y));       // (one after the other: no registers for it)
-                }
-            l += y;
+                for (int i = 0; i < 16; ++i) top[c] = fmaxf(top[c], st[c][b][i]);
+            top[c] = max_across32(top[c]);
+            none[c] = !(top[c] > -INFINITY);          // (the scale of a page that a row does not see does not reach it)
+            top[c] = none[c] ? -INFINITY : top[c] * by;
+            ahead_m[c] = top[c] > m[c] + kLag;
+            ahead_w[c] = !none[c] && top[c] + log_vs > wm[c] + kLag;
+            any = any || ahead_m[c] || ahead_w[c];
         }
-
-        // values, and what remains of them in a page that some row sees in part: masked keys
-        // count nothing, whatever their bytes.  Those of keys that no row sees become 0; a
-        // NaN among those that some row does not see (its 0 would carry it over) becomes 0
-        // as well, and is put into the rows that see it by the product of its place with
-        // what they see.
-        auto products = [&](auto in_part) {
-            constexpr bool EDGE = decltype(in_part)::value;
+        if (__any(any)) {
+            asm volatile("");
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                uint32_t keep[4];
-                half8 sees[2];
-                if constexpr (EDGE) {
+            for (int c = 0; c < NB; ++c) {
+                const float fade = ahead_w[c] ? __builtin_amdgcn_exp2f(wm[c] - (top[c] + log_vs)) : 1.f;
+                l[c] *= ahead_m[c] ? __builtin_amdgcn_exp2f(m[c] - top[c]) : 1.f;      // 0 from -inf
+                m[c] = ahead_m[c] ? top[c] : m[c];
+                wm[c] = ahead_w[c] ? top[c] + log_vs : wm[c];
+#pragma unroll
+                for (int i = 0; i < DB; ++i) o[c][i] *= fade;
+            }
+        }
+        float up[NB], share[NB];                      // a weight's exponent over its score's; its part in the sum
+        bool far = false;
+#pragma unroll
+        for (int c = 0; c < NB; ++c) {
+            const float at = m[c] == -INFINITY ? 0.f : m[c], wat = wm[c] == -INFINITY ? 0.f : wm[c];
+            up[c] = none[c] ? 0.f : log_vs - wat + kTop;
+            share[c] = none[c] ? 0.f : __builtin_amdgcn_exp2f(-(up[c] + at));
+            far = far || (!none[c] && !(fabsf(up[c] + at) <= 60.f));
+        }
+        if (__any(far)) {
+            // the sum's own exponentials
+#pragma unroll
+            for (int c = 0; c < NB; ++c) {
+                const float at = m[c] == -INFINITY ? 0.f : m[c];
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const int j = at0 + 32 * b + 16 * h + i;
-                        if (i % 4 == 0) keep[i / 4] = 0;
-                        if (!absent && j >= lo_least && j < hi_most) keep[i / 4] |= 0xffu << (8 * (i % 4));
-                        sees[i / 8][i % 8] = (_Float16)(!absent && j >= lo && j < hi ? 1.f : 0.f);
+                        l[c] += __builtin_amdgcn_exp2f(__builtin_fmaf(st[c][b][i], by, -at));
+                        asm volatile("" : "+v"(l[c]));    // (one after the other: no registers for it)
                     }
-                }
+                share[c] = 0.f;
+            }
+        }
+
+        half8 w_hi[NB][2], w_lo[NB][2];
+        auto weights = [&](int c, int b) {
+            float sum[2] = {0.f, 0.f};
 #pragma unroll
-                for (int i = 0; i < DB; ++i) {
-                    uint4v u = read16(ring_v + (2 * b * D + 32 * i) * 16);
-                    if constexpr (EDGE) {
-                        uint32_t x[4] = {u.x & keep[0], u.y & keep[1], u.z & keep[2], u.w & keep[3]}, one[4], nan = 0;
+            for (int i = 0; i < 16; ++i) {
+                const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(st[c][b][i], by, up[c]));
+                sum[i & 1] += w;
+                const _Float16 a = (_Float16)w;
+                w_hi[c][i / 8][i % 8] = a;
+                if (PARTS == 2) w_lo[c][i / 8][i % 8] = (_Float16)(w - (float)a);
+            }
+            l[c] += (sum[0] + sum[1]) * share[c];
+        };
+        auto product = [&](int i, half8 v0, half8 v1) {
 #pragma unroll
-                        for (int t = 0; t < 4; ++t) {
-                            const uint32_t whole = (nan_bytes(x[t]) >> 7) * 0xffu;
-                            nan |= whole;
-                            x[t] &= ~whole;
-                            one[t] = whole & 0x38383838u;
-                        }
-                        u = uint4v{x[0], x[1], x[2], x[3]};
-                        if (__any(nan != 0)) {
-                            float16v hit;
+            for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v0, w_hi[c][0], o[c][i], 0, 0, 0);
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) hit[j] = 0.f;
-                            hit = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_f16(one[0], one[1]), sees[0], hit, 0, 0, 0);
-                            hit = __builtin_amdgcn_mfma_f32_32x32x16_f16(e4m3x8_to_f16(one[2], one[3]), sees[1], hit, 0, 0, 0);
+            for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v1, w_hi[c][1], o[c][i], 0, 0, 0);
+            if (PARTS == 2) {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                if (hit[j] > 0.f) o[i][j] = NAN;
-                        }
-                    }
-                    const half8 v0 = e4m3x8_to_f16(u.x, u.y), v1 = e4m3x8_to_f16(u.z, u.w);
-                    o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v0, w_hi[b][0], o[i], 0, 0, 0);
-                    o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v1, w_hi[b][1], o[i], 0, 0, 0);
-                    if (PARTS == 2) {
-                        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v0, w_lo[b][0], o[i], 0, 0, 0);
-                        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v1, w_lo[b][1], o[i], 0, 0, 0);
-                    }
-                }
+                for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v0, w_lo[c][0], o[c][i], 0, 0, 0);
+#pragma unroll
+                for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v1, w_lo[c][1], o[c][i], 0, 0, 0);
             }
         };
-        if (edge) products(std::true_type{});
-        else products(std::false_type{});
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+#pragma unroll
+            for (int c = 0; c < NB; ++c) weights(c, b);
+#pragma unroll
+            for (int i = 0; i < DB; ++i)
+                product(i, e4m3x8_to_f16(vr[b][i].x, vr[b][i].y), e4m3x8_to_f16(vr[b][i].z, vr[b][i].w));
+        }
     }
 
-    // the waves that had the same rows join, in LDS: no load into it is left, and no read of the ring
+    // the waves that had the same rows join, in LDS, 32 rows at a time: no load into it is
+    // left, and no read of the ring
     attn::wait_loads();
-    lds_barrier();
-    l = sum_across32(l);
-    if (h == 0) { sm.ml[wave][col][0] = m; sm.ml[wave][col][1] = l; }
-    const float down = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(wm - m - 15.f);   // to the scores' maximum
 #pragma unroll
-    for (int i = 0; i < DB; ++i)
+    for (int c = 0; c < NB; ++c) {
+        lds_barrier();
+        l[c] = sum_across32(l[c]);
+        if (h == 0) { sm.ml[wave][col][0] = m[c]; sm.ml[wave][col][1] = l[c]; }
+        const float down = m[c] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(wm[c] - m[c] - kTop);   // to the scores' maximum
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float4v y;
+        for (int i = 0; i < DB; ++i)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) y[k] = o[i][4 * j + k] * down;
-            *reinterpret_cast<float4v*>(&sm.o[wave][col][32 * i + 8 * j + 4 * h]) = y;
+            for (int j = 0; j < 4; ++j) {
+                float4v y;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[k] = o[c][i][4 * j + k] * down;
+                *reinterpret_cast<float4v*>(&sm.o[wave][col][32 * i + 8 * j + 4 * h]) = y;
+            }
+        lds_barrier();
+        // all their lanes together
+        const size_t part = (size_t)item * kRows + 32 * c;
+        join_waves<D>(sm.o, sm.ml, 0, 1, kWaves, min(32, rows - 32 * c), wave * 64 + lane, kWaves * 64, [&](int r, int ch, float4v y, float2 ml) {
+            *reinterpret_cast<float4v*>(&p.part_o[(part + r) * D + ch]) = y;
+            if (ch == 0) *reinterpret_cast<float2*>(&p.part_ml[(part + r) * 2]) = ml;
+        });
+    }
+    if (!__syncthreads_or(nans != 0)) return;
+    // NaNs among values that not every row sees: into the rows that see them, one by one
+    __threadfence_block();
+    for (int pg = pg0; pg < pg1; ++pg) {
+        const int page = p.block_table[(size_t)x.first * p.max_pages + pg];
+        if ((unsigned)page >= (unsigned)p.n_pages) continue;
+        const uint8_t* values = p.v_cache + ((size_t)page * p.Hkv + kh) * (kPage * D);
+        for (int i = threadIdx.x; i < kPage * D; i += 64 * kWaves) {
+            if ((values[i] & 0x7f) != 0x7f) continue;
+            const int j = pg * kPage + 16 * (i / (16 * D)) + i % 16, ch = i / 16 % D;
+            for (int r = 0; r < rows; ++r) {
+                int a, b;
+                seen_range(p, x.first + (row0 + r) / rep, a, b);
+                if (j >= a && j < b) p.part_o[((size_t)item * kRows + r) * D + ch] = NAN;
+            }
         }
-    lds_barrier();
-    // all their lanes together; item's row 32 wr + c
-    const size_t part = (size_t)item * (32 * ACROSS) + 32 * wr;
-    join_waves<D>(sm.o, sm.ml, wr, ACROSS, TEAMS, min(32, rows - 32 * wr), team * 64 + lane, TEAMS * 64, [&](int c, int ch, float4v y, float2 ml) {
-        *reinterpret_cast<float4v*>(&p.part_o[(part + c) * D + ch]) = y;
-        if (ch == 0) *reinterpret_cast<float2*>(&p.part_ml[(part + c) * 2]) = ml;
-    });
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -579,7 +626,7 @@ template <int D> struct __attribute__((aligned(16))) OwnSmem {
 
 // where the partial result of run `slot` of group x's pages is for a sequence's query head
 __device__ __forceinline__ size_t part_of(const SharedParams& p, const Group& x, int slot, int kh, int row) {
-    const int width = 32 * p.across;
+    const int width = p.width;
     return (size_t)(x.base + (slot * p.Hkv + kh) * x.tiles + row / width) * width + row % width;
 }
 
@@ -814,13 +861,13 @@ SharedPlan attn_shared_plan(int N, int groups, int Hq, int Hkv, int d, int max_p
     const int rep = Hq / Hkv;
     const long long rows = (long long)N * rep;        // of a key head
     const long long each = (rows + groups - 1) / groups;
-    x.across = each > 64 ? 4 : each > 32 ? 2 : 1;
-    const int width = 32 * x.across;
+    x.width = each > 32 ? 64 : 32;
     // at most: every group's last tile has one row
     const long long some = groups < N ? groups : N;
-    const long long tiles = (rows + some * (width - 1)) / width;
-    // items that are at work at once; more only where there are more tiles than that
-    const long long fill = x.across == 1 ? 256 : 512;
+    const long long tiles = (rows + some * (x.width - 1)) / x.width;
+    // items: as many workgroups as the compute units' LDS holds; more only where there are
+    // more tiles than that
+    const long long fill = d == 64 ? 512 : 256;
     x.items = tiles * Hkv > fill ? tiles * Hkv : fill;
     x.own_items = (long long)N * Hkv * ((rep + 15) / 16);
     int pages = max_pages;
@@ -837,8 +884,8 @@ SharedPlan attn_shared_plan(int N, int groups, int Hq, int Hkv, int d, int max_p
     x.at_groups = take(sizeof(Group) * (size_t)groups);
     x.at_group_of = take(4 * (size_t)N);
     x.at_items = take(4 * (size_t)x.items);
-    x.at_part_o = take(4 * (size_t)x.items * width * d);
-    x.at_part_ml = take(8 * (size_t)x.items * width);
+    x.at_part_o = take(4 * (size_t)x.items * x.width * d);
+    x.at_part_ml = take(8 * (size_t)x.items * x.width);
     const size_t own = x.own_splits > 1 ? (size_t)x.own_splits * N * Hq : 0;
     x.at_own_o = take(4 * own * d);
     x.at_own_ml = take(8 * own);
@@ -851,19 +898,18 @@ long long attn_shared_workgroups(const SharedPlan& x, long long heads) {
     return x.own_splits > 1 && heads > most ? heads : most;
 }
 
-template <int D, int PARTS, int ACROSS> static hipError_t launch_shared(const SharedParams& p, hipStream_t st) {
+template <int D, int PARTS, int NB> static hipError_t launch_shared(const SharedParams& p, hipStream_t st) {
     static std::atomic<unsigned long long> done{0};
-    const int lds = (int)sizeof(SharedSmem<D, ACROSS>);
-    const hipError_t e = ensure_dyn_lds(reinterpret_cast<const void*>(&attn_shared_kernel<D, PARTS, ACROSS>), lds, done);
+    const int lds = (int)sizeof(SharedSmem<D>);
+    const hipError_t e = ensure_dyn_lds(reinterpret_cast<const void*>(&attn_shared_kernel<D, PARTS, NB>), lds, done);
     if (e != hipSuccess) return e;
     // (the items of the 8 XCDs' runs: up to 7 more numbers than items)
-    hipLaunchKernelGGL((attn_shared_kernel<D, PARTS, ACROSS>), dim3((unsigned)((p.items + 7) / 8 * 8)), dim3(64 * kWaves), lds, st, p);
+    hipLaunchKernelGGL((attn_shared_kernel<D, PARTS, NB>), dim3((unsigned)((p.items + 7) / 8 * 8)), dim3(64 * kWaves), lds, st, p);
     return hipGetLastError();
 }
 
 template <int D, int PARTS> static hipError_t launch_d(const SharedParams& p, const SharedPlan& x, hipStream_t st) {
-    hipError_t e = p.across == 4 ? launch_shared<D, PARTS, 4>(p, st)
-                 : p.across == 2 ? launch_shared<D, PARTS, 2>(p, st) : launch_shared<D, PARTS, 1>(p, st);
+    hipError_t e = p.width == 64 ? launch_shared<D, PARTS, 2>(p, st) : launch_shared<D, PARTS, 1>(p, st);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((attn_own_kernel<D, PARTS>), dim3((unsigned)x.own_items, (unsigned)p.own_splits), dim3(64 * kWaves), 0, st, p);
     e = hipGetLastError();

@@ -30,7 +30,8 @@ def shared_decode(q, cache, table, lens, group_start, shared, window=0, scale=No
     of the maxima and the scale's logarithm, four roundings of values up to those; it, the
     weight and the joins of waves and of partial results are exponentials of 2^-22 each
     (six at most).  A weight as two f16 values keeps 22 bits, as one 11, relative to the
-    largest down to 2^-29; below, half a step is 2^-40 of it."""
+    largest down to 2^-26; below, half a step of 2^-24 is 2^-37 of it (it stands at 2^12 or
+    above)."""
     N, Hq, d = q.shape
     H = cache.k.shape[1]
     scale = d ** -0.5 if scale is None else scale
@@ -56,7 +57,7 @@ def shared_decode(q, cache, table, lens, group_start, shared, window=0, scale=No
         A = (p[..., None] * v.abs()).sum(1)
         top = (p[..., None] * cache.vs.amax() * 448).amax(1)
         tol[i] = (2.0 ** -11 if bf16 else 2.0 ** -22) * A + (2.1 * rel[:, None] + (len(at) + 16) * FP32) * A \
-            + len(at) * 2.0 ** -40 * top + (2.0 ** -8 if bf16 else 4 * FP32) * o[i].abs() * 1.01
+            + len(at) * 2.0 ** -37 * top + (2.0 ** -8 if bf16 else 4 * FP32) * o[i].abs() * 1.01
     return o, tol
 
 
