@@ -656,7 +656,7 @@ gdr_status gdr_attn_decode(const void* q, const void* k_cache, const void* v_cac
 }
 
 size_t gdr_attn_decode_shared_workspace_bytes(int N, int groups, int Hq, int Hkv, int d, int max_pages, int window) {
-    if (decode_args(N, Hq, Hkv, d, 1, max_pages, window, 1.f, 0) != GDR_OK || groups < 1 || groups > (1 << 28)) return 0;
+    if (decode_args(N, Hq, Hkv, d, 1, max_pages, window, 1.f, 0) != GDR_OK || groups < 1 || groups > gdr::kMostGroups) return 0;
     return gdr::attn_shared_plan(N, groups, Hq, Hkv, d, max_pages, window).bytes;
 }
 
@@ -667,7 +667,8 @@ gdr_status gdr_attn_decode_shared(const void* q, const void* k_cache, const void
                                   void* workspace, size_t workspace_bytes, void* stream) {
     const gdr_status st = decode_args(N, Hq, Hkv, d, n_pages, max_pages, window, scale, flags);
     if (st != GDR_OK) return st;
-    if (groups < 1 || groups > (1 << 28)) return GDR_ERR_INVALID_ARG;
+    if (groups < 1) return GDR_ERR_INVALID_ARG;
+    if (groups > gdr::kMostGroups) return GDR_ERR_UNSUPPORTED;
     const gdr::SharedPlan x = gdr::attn_shared_plan(N, groups, Hq, Hkv, d, max_pages, window);
     if (!grid_ok(gdr::attn_shared_workgroups(x, (long long)N * Hq))) return GDR_ERR_INVALID_ARG;
     const void* ptrs[] = {q, k_cache, v_cache, k_scale, v_scale, block_table, cache_len, group_start, shared_pages, o};

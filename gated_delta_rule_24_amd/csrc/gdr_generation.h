@@ -45,6 +45,7 @@ struct SharedPlan {
     int own_splits;             // runs that a sequence's own pages are dealt into
     size_t at_head, at_groups, at_group_of, at_items, at_part_o, at_part_ml, at_own_o, at_own_ml, bytes;
 };
+constexpr int kMostGroups = 4096;                     // the plan has them in LDS
 struct SharedParams {
     const void* q;
     const uint8_t* k_cache;

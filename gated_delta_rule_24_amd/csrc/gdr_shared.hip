@@ -78,11 +78,11 @@ __device__ __forceinline__ uint32_t bytes_of(uint32_t bits, int i) { return (((b
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
 
-// Which run of the pages pg0 .. pg1 - 1 is number i of `splits`: a page for each of
-// the waves that take them in turn, at least.
+// Which run of the pages pg0 .. pg1 - 1 is number i of `splits`; two pages at least, as the
+// second is loaded beside the first one's work.
 __device__ __forceinline__ void run_of(int& pg0, int& pg1, int i, int splits) {
     if (pg1 <= pg0) { pg1 = pg0; return; }
-    const int per = max((pg1 - pg0 + splits - 1) / splits, kWaves);
+    const int per = max((pg1 - pg0 + splits - 1) / splits, 2);
     const long long begin = pg0 + (long long)i * per;
     pg0 = begin < pg1 ? (int)begin : pg1;
     pg1 = min(pg0 + per, pg1);
@@ -122,106 +122,104 @@ __device__ __forceinline__ void join_waves(const O& o, const ML& ml, int from, i
 // can be at work at once.
 constexpr int kPlanThreads = 1024;
 
-__device__ __forceinline__ long long plan_sum(long long x, long long* s) {
-    for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o, 64);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = x;
-    __syncthreads();
-    long long sum = 0;
-#pragma unroll
-    for (int w = 0; w < kPlanThreads / 64; ++w) sum += s[w];
-    return sum;
-}
+struct PlanGroup {
+    int first, shared, lo, hi;  // first sequence; pages; first and one past the last token that some sequence sees
+    int base;
+};
 
 __global__ __launch_bounds__(kPlanThreads) void attn_shared_plan_kernel(SharedParams p) {
-    __shared__ long long s_sum[kPlanThreads / 64];
-    __shared__ int s_most, s_end;                     // pages of the longest prefix; items that have a group
-    const int tid = threadIdx.x, lane = tid & 63, rep = p.Hq / p.Hkv, width = p.width;
-    Group* groups = reinterpret_cast<Group*>(p.plan_groups);
-    for (int n = tid; n < p.N; n += kPlanThreads) p.plan_group_of[n] = -1;
-    if (tid == 0) { s_most = 0; s_end = INT_MAX; }
+    extern __shared__ __attribute__((aligned(256))) char smem[];
+    PlanGroup* s = reinterpret_cast<PlanGroup*>(smem);       // [groups + 1]
+    __shared__ int s_per, s_items;
+    const int tid = threadIdx.x, lane = tid & 63, rep = p.Hq / p.Hkv, G = p.groups;
+    for (int g = tid; g <= G; g += kPlanThreads)
+        s[g] = PlanGroup{clampi(p.group_start[g], 0, p.N), g < G ? clampi(p.shared_pages[g], 0, p.max_pages) : 0, INT_MAX, 0, 0};
     __syncthreads();
-    // a wave a group
-    for (int g = tid >> 6; g < p.groups; g += kPlanThreads / 64) {
-        const int first = clampi(p.group_start[g], 0, p.N), end = clampi(p.group_start[g + 1], first, p.N);
-        const int shared = clampi(p.shared_pages[g], 0, p.max_pages);
-        int lo = INT_MAX, hi = 0;
-        for (int n = first + lane; n < end; n += 64) {
-            int a, b;
-            seen_range(p, n, a, b);
-            if (a < b) { lo = min(lo, a); hi = max(hi, b); }
-            p.plan_group_of[n] = g;
+    for (int n = tid; n < p.N; n += kPlanThreads) {
+        int a, b;
+        seen_range(p, n, a, b);
+        int g = 0, z = G - 1;                         // the last start at or before n
+        while (g < z) {
+            const int mid = (g + z + 1) / 2;
+            if (s[mid].first <= n) g = mid;
+            else z = mid - 1;
         }
-        for (int o = 32; o > 0; o >>= 1) { lo = min(lo, __shfl_xor(lo, o, 64)); hi = max(hi, __shfl_xor(hi, o, 64)); }
-        Group x;
-        x.first = first;
-        x.rows = (end - first) * rep;
-        x.pg0 = lo / kPage;
-        x.pg1 = min((int)(((long long)hi + kPage - 1) / kPage), shared);
-        if (x.pg0 >= x.pg1) x.pg0 = x.pg1 = 0;
-        x.tiles = (int)(((long long)x.rows + width - 1) / width);
-        x.slots = x.base = 0;
-        x.shared = shared;
-        if (lane == 0) {
-            groups[g] = x;
-            atomicMax(&s_most, x.pg1 - x.pg0);
+        const bool in = n >= s[g].first && n < s[g + 1].first;
+        p.plan_group_of[n] = in ? g : -1;
+        if (in && a < b) {
+            atomicMin(&s[g].lo, a);
+            atomicMax(&s[g].hi, b);
         }
     }
-    __syncthreads();                                  // (one workgroup: what it wrote, it reads)
-    __threadfence_block();
-    // pages of a run
-    long long all = 0;
-    for (int g = tid; g < p.groups; g += kPlanThreads) all += (long long)groups[g].tiles * (groups[g].pg1 - groups[g].pg0);
-    all = plan_sum(all, s_sum) * p.Hkv;
-    const int most = s_most, least = 2 * kWaves;   // two pages a wave
-    int per = (int)min((all + p.items - 1) / p.items, (long long)INT_MAX);
-    per = max(per, least);
-    while (per < most) {
-        long long items = 0;
-        for (int g = tid; g < p.groups; g += kPlanThreads)
-            items += (long long)groups[g].tiles * ((groups[g].pg1 - groups[g].pg0 + per - 1) / per);
-        if (plan_sum(items, s_sum) * p.Hkv <= p.items) break;
-        per += (per + 15) / 16;
-    }
-    // each group's items behind those of the groups before it
-    long long before = 0;
-    for (int g0 = 0; g0 < p.groups; g0 += kPlanThreads) {
-        const int g = g0 + tid;
-        long long mine = 0;
-        int slots = 0;
-        if (g < p.groups) {
-            slots = (groups[g].pg1 - groups[g].pg0 + per - 1) / per;
-            mine = (long long)slots * groups[g].tiles * p.Hkv;
-        }
-        long long run = mine;
-        for (int o = 1; o < 64; o <<= 1) {
-            const long long y = __shfl_up(run, o, 64);
-            if (lane >= o) run += y;
-        }
-        __syncthreads();
-        if (lane == 63) s_sum[tid >> 6] = run;
-        __syncthreads();
-        long long base = before;
-        for (int w = 0; w < kPlanThreads / 64; ++w) {
-            if (w < (tid >> 6)) base += s_sum[w];
-            before += s_sum[w];
-        }
-        base += run - mine;
-        if (g < p.groups) {
+    __syncthreads();
+    // one wave: a run's pages, and where each group's items start
+    auto tiles_of = [&](int g) {
+        const long long rows = (long long)max(s[g + 1].first - s[g].first, 0) * rep;
+        return (int)((rows + p.width - 1) / p.width);
+    };
+    auto first_page = [&](int g) { return s[g].lo / kPage; };
+    auto pages_of = [&](int g) { return max(0, min((int)(((long long)s[g].hi + kPage - 1) / kPage), s[g].shared) - first_page(g)); };
+    if (tid < 64) {
+        auto sum_of = [&](auto f) {
+            long long x = 0;
+            for (int g = lane; g < G; g += 64) x += f(g);
+            for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o, 64);
+            return x;
+        };
+        int most = 0;
+        for (int g = lane; g < G; g += 64) most = max(most, pages_of(g));
+        for (int o = 32; o > 0; o >>= 1) most = max(most, __shfl_xor(most, o, 64));
+        const long long room = p.items / p.Hkv;       // (tile, run) pairs of a key head
+        const long long all = sum_of([&](int g) { return (long long)tiles_of(g) * pages_of(g); });
+        int per = max((int)min((all + room - 1) / max(room, 1LL), (long long)INT_MAX / 2), 2 * kWaves);   // two pages a wave
+        while (per < most && sum_of([&](int g) { return (long long)tiles_of(g) * ((pages_of(g) + per - 1) / per); }) > room)
+            per += (per + 15) / 16;
+        long long before = 0;
+        int end = INT_MAX;
+        for (int g0 = 0; g0 < G; g0 += 64) {
+            const int g = g0 + lane;
+            const long long mine = g < G ? (long long)tiles_of(g) * ((pages_of(g) + per - 1) / per) * p.Hkv : 0;
+            long long run = mine;
+            for (int o = 1; o < 64; o <<= 1) {
+                const long long y = __shfl_up(run, o, 64);
+                if (lane >= o) run += y;
+            }
+            const long long base = before + run - mine;
             // (bounds that overlap may want more than there are: from there on nothing is shared)
             const bool fits = base + mine <= p.items;
-            if (!fits) atomicMin(&s_end, (int)min(base, (long long)p.items));
-            groups[g].slots = fits ? slots : 0;
-            groups[g].base = fits ? (int)base : 0;
+            if (g < G) s[g].base = fits ? (int)base : -1;
+            if (!fits) end = min(end, (int)min(base, (long long)p.items));
+            before += __shfl(run, 63, 64);
         }
+        for (int o = 32; o > 0; o >>= 1) end = min(end, __shfl_xor(end, o, 64));
+        if (lane == 0) { s_per = per; s_items = (int)min(before, (long long)end); }
     }
     __syncthreads();
-    for (int g = tid >> 6; g < p.groups; g += kPlanThreads / 64) {
-        const int base = groups[g].base, items = groups[g].slots * groups[g].tiles * p.Hkv;
-        for (int i = lane; i < items; i += 64) p.plan_items[base + i] = g;
+    const int per = s_per;
+    Group* groups = reinterpret_cast<Group*>(p.plan_groups);
+    for (int g = tid; g < G; g += kPlanThreads) {
+        Group x;
+        x.first = s[g].first;
+        x.rows = max(s[g + 1].first - s[g].first, 0) * rep;
+        x.pg0 = pages_of(g) > 0 ? first_page(g) : 0;
+        x.pg1 = x.pg0 + pages_of(g);
+        x.tiles = tiles_of(g);
+        x.slots = s[g].base < 0 ? 0 : (pages_of(g) + per - 1) / per;
+        x.base = max(s[g].base, 0);
+        x.shared = s[g].shared;
+        groups[g] = x;
+    }
+    for (int i = tid; i < s_items; i += kPlanThreads) {      // the last group that starts at or before item i
+        int g = 0, z = G - 1;
+        while (g < z) {
+            const int mid = (g + z + 1) / 2;
+            if (s[mid].base >= 0 && s[mid].base <= i) g = mid;
+            else z = mid - 1;
+        }
+        p.plan_items[i] = g;
     }
     if (tid == 0) {
-        p.plan_head[0] = (int)min(before, (long long)s_end);
+        p.plan_head[0] = s_items;
         p.plan_head[1] = per;
     }
 }
@@ -242,8 +240,7 @@ __global__ __launch_bounds__(kPlanThreads) void attn_shared_plan_kernel(SharedPa
 // a page and waited for each other at every one, 1,024 rows on 512 pages took 215 us for
 // 181.  Pages come through two places in LDS a wave, as they lie in memory, by direct loads a
 // page ahead (no registers, 1 KiB an instruction): read straight to registers in the
-// operands' order, 16 bytes a lane from 32 rows, the same walk took 265.  A key's row keeps its 16-byte units u at u ^ f(row), so that the 16 rows of a
-// read phase land on 16 different places of the banks' 256 bytes.
+// operands' order, 16 bytes a lane from 32 rows, the same walk took 265.
 //
 // A weight is exp2(s - m).  For the product with v it is taken times 2^b, b = 12 +
 // log2 v_scale + m - wm, wm the running maximum of s + log2 v_scale, so that it has
@@ -262,22 +259,30 @@ struct __attribute__((aligned(256))) SharedSmem {
     };
 };
 
-// One side of a page into LDS by a wave: 16-byte direct loads, a KiB each.
-template <int D>
+// A page into LDS by a wave: 16-byte direct loads, a KiB of keys or values each.  A key's
+// row keeps its 16-byte units u at u ^ f(row), so that the 16 rows that a phase of the
+// operand's reads takes land on 16 different places of the banks' 256 bytes: rows
+// 4 a + b and 16 + 4 a + b of 32 x 32 products (a in two following ones, b < 4), or
+// 16 a + b of 16 x 16 products (OWN; a, b < 4), + 4 t.
+template <int D, bool OWN> __device__ __forceinline__ constexpr int key_flip(int row) {
+    if (OWN) return D == 128 ? ((row >> 1) & 1) | ((row >> 4) & 3) << 1 : (row >> 4) & 3;
+    return D == 128 ? ((row >> 1) & 3) | ((row >> 4) & 1) << 2 : ((row >> 2) & 1) | ((row >> 4) & 1) << 1;
+}
+template <int D, bool OWN>
 struct PageLoader {
     static constexpr int N = kPage * D / 1024;        // loads of a side
+    static constexpr int ROWS = 1024 / D;             // keys of one
     int off;                                          // a lane's place in a KiB of keys, before the instruction's flip
     int lane16;
 
     __device__ __forceinline__ explicit PageLoader(int lane) {
         constexpr int CH = D / 16;
-        const int f = D == 128 ? (lane >> 4) & 3 : (lane >> 4) & 1;
-        off = (lane / CH) * D + 16 * ((lane % CH) ^ f);
+        off = (lane / CH) * D + 16 * ((lane % CH) ^ key_flip<D, OWN>(lane / CH));
         lane16 = 16 * lane;
     }
+    // (the flip of a row is that of its place in the KiB xor that of the KiB's first row)
     template <int I = 0> __device__ __forceinline__ void keys(uint64_t from, uint32_t to) const {
-        constexpr int flip = D == 128 ? ((I >> 1) & 1) << 6 : (I & 1) << 5;
-        attn::direct_load16<1024 * I>((off ^ flip) + 1024 * I, from, to);
+        attn::direct_load16<1024 * I>((off ^ (16 * key_flip<D, OWN>(ROWS * I))) + 1024 * I, from, to);
         if constexpr (I + 1 < N) keys<I + 1>(from, to);
     }
     template <int I = 0> __device__ __forceinline__ void values(uint64_t from, uint32_t to) const {
@@ -285,6 +290,9 @@ struct PageLoader {
         if constexpr (I + 1 < N) values<I + 1>(from, to);
     }
 };
+
+typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ uint4v read16(uint32_t at) { return *(const __attribute__((address_space(3))) uint4v*)(uintptr_t)at; }
 
 template <int D, int PARTS, int NB>
 __global__ __launch_bounds__(64 * kWaves, 1) void attn_shared_kernel(SharedParams p) {
@@ -322,7 +330,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_shared_kernel(SharedParam
         e_ks = p.k_scale[ph];
         e_vs = p.v_scale[ph];
     };
-    const PageLoader<D> loader(lane);
+    const PageLoader<D, false> loader(lane);
     const uint32_t ring = attn::lds_address(sm.ring[wave][0]);
     constexpr uint32_t kSide = kPage * D;
     // (an absent page is read as the first one: its bytes are masked)
@@ -385,12 +393,9 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_shared_kernel(SharedParam
     uint32_t k_at, v_at;                              // this lane's reads: of keys, to flip by 32 s; of values
     {
         const int tok = 16 * ((col >> 2) & 1) + 4 * (col >> 3) + (col & 3);
-        const int f = D == 128 ? ((tok >> 1) & 3) | ((tok >> 4) & 1) << 2 : ((tok >> 2) & 1) | ((tok >> 4) & 1) << 1;
-        k_at = tok * D + 16 * (h ^ f);
+        k_at = tok * D + 16 * (h ^ key_flip<D, false>(tok));
         v_at = kPage * D + (h * D + col) * 16;
     }
-    typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
-    auto read16 = [](uint32_t at) { return *(const __attribute__((address_space(3))) uint4v*)(uintptr_t)at; };
 
     uint32_t nans = 0;                                // some value that not every row sees is NaN
     for (int k = 0; k < n; ++k) {
@@ -615,42 +620,34 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_shared_kernel(SharedParam
 // ---------------------------------------------------------------------------
 //
 // Up to 16 of a sequence's query heads on a key head are the columns of 16 x 16
-// products, the waves take pages in turn (as attn_decode_kernel has them).  Where one
-// workgroup has all of the pages it joins the shared ones' partial results as well and
-// writes the output; where there are few sequences their pages are dealt to several, and
-// a kernel behind this one joins.
-template <int D> struct __attribute__((aligned(16))) OwnSmem {
-    float o[kWaves][16][D + 4];
-    float ml[kWaves][16][2];
-};
+// products (as attn_decode_kernel has them).  A wave has all of the pages of one, or a run of
+// them where there are few sequences, and loads each page while it works on the one before:
+// a few pages a sequence are too few to be dealt to four waves, whose starts and joins
+// took as long as the pages.  Where a wave
+// has all pages it joins the shared ones' partial results as well and writes the output;
+// else a kernel behind this one does.
 
 // where the partial result of run `slot` of group x's pages is for a sequence's query head
 __device__ __forceinline__ size_t part_of(const SharedParams& p, const Group& x, int slot, int kh, int row) {
-    const int width = p.width;
-    return (size_t)(x.base + (slot * p.Hkv + kh) * x.tiles + row / width) * width + row % width;
+    return (size_t)(x.base + (slot * p.Hkv + kh) * x.tiles + row / p.width) * p.width + row % p.width;
 }
 
 template <int D, int PARTS>
-__global__ __launch_bounds__(64 * kWaves) void attn_own_kernel(SharedParams p) {
+__global__ __launch_bounds__(64) void attn_own_kernel(SharedParams p) {
     constexpr int KS = D / 64;                        // 64-channel steps of a key row
     constexpr int VT = D / 16;                        // 16-channel tiles of the output
-    __shared__ OwnSmem<D> sm;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __shared__ __attribute__((aligned(256))) uint8_t s_ring[2][2 * kPage * D];       // keys [64][D], then values [4][D][16]
+    const int lane = threadIdx.x;
     const int col = lane & 15, g = lane >> 4;
     const int rep = p.Hq / p.Hkv, sets = (rep + 15) / 16;
     int w = blockIdx.x;
     const int qg = w % sets; w /= sets;
     const int kh = w % p.Hkv; w /= p.Hkv;
-    const int n = w, i = blockIdx.y;
+    const int n = w % p.N, run = w / p.N;
     const int q0 = kh * rep + 16 * qg, nq = min(16, rep - 16 * qg);
+    const int gi = p.plan_group_of[n];
     int lo, hi;
     seen_range(p, n, lo, hi);
-    const int gi = p.plan_group_of[n];
-    Group x = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (gi >= 0) x = group_of(p, gi);
-    int pg0 = max(lo / kPage, x.shared), pg1 = (int)(((long long)hi + kPage - 1) / kPage);
-    if (p.own_splits > 1) run_of(pg0, pg1, i, p.own_splits);
-
     // queries: column col, channels 64 s + 16 g + 8 half ..
     bf8v qf[KS][2];
 #pragma unroll
@@ -662,43 +659,75 @@ __global__ __launch_bounds__(64 * kWaves) void attn_own_kernel(SharedParams p) {
                 u = *reinterpret_cast<const uint4*>((const uint16_t*)p.q + ((size_t)n * p.Hq + q0 + col) * D + 64 * s + 16 * g + 8 * hf);
             qf[s][hf] = __builtin_bit_cast(bf8v, u);
         }
+    Group x = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (gi >= 0) x = group_of(p, gi);
+    int pg0 = max(lo / kPage, x.shared), pg1 = (int)(((long long)hi + kPage - 1) / kPage);
+    run_of(pg0, pg1, run, p.own_splits);
+    pg0 = __builtin_amdgcn_readfirstlane(pg0);
+    pg1 = __builtin_amdgcn_readfirstlane(pg1);
+    const int count = pg1 - pg0;
+
+    // pages k0 .. k0 + 63 of the run, one a lane: place (-1: absent) and scales
+    const int* entries = p.block_table + (size_t)n * p.max_pages + pg0;
+    int e_page;
+    float e_ks, e_vs;
+    auto look_up = [&](int k0) {
+        const int e = k0 + lane < count ? entries[k0 + lane] : -1;
+        e_page = (unsigned)e < (unsigned)p.n_pages ? e : -1;
+        const size_t ph = (size_t)max(e_page, 0) * p.Hkv + kh;
+        e_ks = p.k_scale[ph];
+        e_vs = p.v_scale[ph];
+    };
+    const PageLoader<D, true> loader(lane);
+    const uint32_t ring = attn::lds_address(s_ring[0]);
+    constexpr uint32_t kSide = kPage * D;
+    auto load = [&](int k) {                          // (an absent page is read as the first one)
+        const size_t at = ((size_t)max(__builtin_amdgcn_readlane(e_page, k & 63), 0) * p.Hkv + kh) * kSide;
+        const uint32_t to = ring + (k & 1) * (2 * kSide);
+        loader.keys((uint64_t)p.k_cache + at, to);
+        loader.values((uint64_t)p.v_cache + at, to + kSide);
+    };
+    if (count > 0) {
+        look_up(0);
+        load(0);
+    }
+    const int krow = 16 * (col >> 2) + (col & 3);     // key of tile 0's row `col`; its flip is that of the others, + 4 t, too
+    const uint32_t k_at = krow * D + 16 * (g ^ key_flip<D, true>(krow)), v_at = kSide + (g * D + col) * 16;
+
     float4v o[VT];
 #pragma unroll
     for (int j = 0; j < VT; ++j) o[j] = float4v{0.f, 0.f, 0.f, 0.f};
     float m = -INFINITY, l = 0.f, wm = -INFINITY;
     const float to2 = p.scale * 1.4426950408889634f;
-    const int krow = 16 * (col >> 2) + (col & 3);     // key of tile 0's row `col`
-
-    for (int pg = pg0 + wave; pg < pg1; pg += kWaves) {
-        int page = p.block_table[(size_t)n * p.max_pages + pg];
-        const int at0 = pg * kPage;
-        const bool absent = (unsigned)page >= (unsigned)p.n_pages;
-        if (absent) page = 0;
-        const size_t ph = (size_t)page * p.Hkv + kh;
-        const uint8_t* kp = p.k_cache + ph * (kPage * D);
-        const uint8_t* vp = p.v_cache + ph * (kPage * D);
-        uint4 kk[4][KS], vv[VT];
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int s = 0; s < KS; ++s)
-                kk[t][s] = *reinterpret_cast<const uint4*>(kp + (krow + 4 * t) * D + 64 * s + 16 * g);
-#pragma unroll
-        for (int j = 0; j < VT; ++j)
-            vv[j] = *reinterpret_cast<const uint4*>(vp + (size_t)(g * D + 16 * j + col) * 16);
-        const float ks = p.k_scale[ph] * to2, vs = absent ? -INFINITY : __builtin_amdgcn_logf(p.v_scale[ph]);   // base 2
-
+    for (int k = 0; k < count; ++k) {
+        const int page = __builtin_amdgcn_readlane(e_page, k & 63);
+        const float k_scale = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(e_ks), k & 63));
+        const float v_scale = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(e_vs), k & 63));
+        // this page is there, and the place of the one before it is free: its reads are done
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        if (k + 1 < count) {
+            if (((k + 1) & 63) == 0) look_up(k + 1);
+            load(k + 1);
+        }
+        const uint32_t at_k = ring + (k & 1) * (2 * kSide) + k_at, at_v = ring + (k & 1) * (2 * kSide) + v_at;
+        const int at0 = (pg0 + k) * kPage;
+        const bool absent = page < 0;
+        const float ks = k_scale * to2, vs = absent ? -INFINITY : __builtin_amdgcn_logf(v_scale);   // base 2
+        uint4v vv[VT];
         float4v sc[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             sc[t] = float4v{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e4m3x8_to_bf16(kk[t][s].x, kk[t][s].y), qf[s][0], sc[t], 0, 0, 0);
-                sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e4m3x8_to_bf16(kk[t][s].z, kk[t][s].w), qf[s][1], sc[t], 0, 0, 0);
+                const uint4v u = read16((at_k ^ (64 * s)) + 4 * t * D);
+                sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e4m3x8_to_bf16(u.x, u.y), qf[s][0], sc[t], 0, 0, 0);
+                sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e4m3x8_to_bf16(u.z, u.w), qf[s][1], sc[t], 0, 0, 0);
             }
             sc[t] *= ks;
         }
+#pragma unroll
+        for (int j = 0; j < VT; ++j) vv[j] = read16(at_v + 256 * j);
         if (absent || at0 < lo || at0 + kPage > hi) {
             // the first and last pages: masked keys count nothing, whatever their bytes
             uint32_t keep[4];
@@ -706,11 +735,11 @@ __global__ __launch_bounds__(64 * kWaves) void attn_own_kernel(SharedParams p) {
             for (int t = 0; t < 4; ++t) {
                 keep[t] = 0;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int j = at0 + 16 * g + 4 * t + k;
+                for (int i = 0; i < 4; ++i) {
+                    const int j = at0 + 16 * g + 4 * t + i;
                     const bool in = !absent && j >= lo && j < hi;
-                    if (!in) sc[t][k] = -INFINITY;
-                    else keep[t] |= 0xffu << (8 * k);
+                    if (!in) sc[t][i] = -INFINITY;
+                    else keep[t] |= 0xffu << (8 * i);
                 }
             }
 #pragma unroll
@@ -722,7 +751,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_own_kernel(SharedParams p) {
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) top = fmaxf(top, sc[t][k]);
+            for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[t][i]);
         top = fmaxf(top, __shfl_xor(top, 16, 64));
         top = max_across32(top);
         const float wt = fmaxf(wm, top + vs);
@@ -738,12 +767,12 @@ __global__ __launch_bounds__(64 * kWaves) void attn_own_kernel(SharedParams p) {
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                l += __builtin_amdgcn_exp2f(sc[t][k] - at);
-                const float x = __builtin_amdgcn_exp2f(sc[t][k] + up);
-                const _Float16 a = (_Float16)x;
-                w_hi[t >> 1][(t & 1) * 4 + k] = a;
-                if (PARTS == 2) w_lo[t >> 1][(t & 1) * 4 + k] = (_Float16)(x - (float)a);
+            for (int i = 0; i < 4; ++i) {
+                l += __builtin_amdgcn_exp2f(sc[t][i] - at);
+                const float z = __builtin_amdgcn_exp2f(sc[t][i] + up);
+                const _Float16 a = (_Float16)z;
+                w_hi[t >> 1][(t & 1) * 4 + i] = a;
+                if (PARTS == 2) w_lo[t >> 1][(t & 1) * 4 + i] = (_Float16)(z - (float)a);
             }
 #pragma unroll
         for (int j = 0; j < VT; ++j) {
@@ -757,42 +786,51 @@ __global__ __launch_bounds__(64 * kWaves) void attn_own_kernel(SharedParams p) {
         }
     }
 
+    // a lane has channels 16 j + 4 g .. + 3 of column col
     l += __shfl_xor(l, 16, 64);
     l = sum_across32(l);
-    if (g == 0) { sm.ml[wave][col][0] = m; sm.ml[wave][col][1] = l; }
     const float down = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(wm - m - 15.f);   // to the scores' maximum
 #pragma unroll
-    for (int j = 0; j < VT; ++j)
-        *reinterpret_cast<float4v*>(&sm.o[wave][col][16 * j + 4 * g]) = o[j] * down;
-    __syncthreads();
-    const size_t heads = (size_t)p.N * p.Hq;
-    join_waves<D>(sm.o, sm.ml, 0, 1, kWaves, nq, wave * 64 + lane, kWaves * 64, [&](int c, int ch, float4v y, float2 ml) {
-        const size_t head = (size_t)n * p.Hq + q0 + c;
-        if (p.own_splits > 1) {
-            *reinterpret_cast<float4v*>(&p.own_o[(i * heads + head) * D + ch]) = y;
-            if (ch == 0) *reinterpret_cast<float2*>(&p.own_ml[(i * heads + head) * 2]) = ml;
-            return;
-        }
-        const int row = (n - x.first) * rep + 16 * qg + c;
-        float top = ml.x;
-        for (int s = 0; s < x.slots; ++s) top = fmaxf(top, p.part_ml[2 * part_of(p, x, s, kh, row)]);
-        const float at = top == -INFINITY ? 0.f : top, f0 = __builtin_amdgcn_exp2f(ml.x - at);
-        float sum = ml.y * f0;
-        y *= f0;
-        for (int s = 0; s < x.slots; ++s) {
-            const size_t from = part_of(p, x, s, kh, row);
-            const float2 other = *reinterpret_cast<const float2*>(&p.part_ml[2 * from]);
-            const float f = __builtin_amdgcn_exp2f(other.x - at);
-            sum += other.y * f;
-            y += *reinterpret_cast<const float4v*>(&p.part_o[from * D + ch]) * f;
-        }
+    for (int j = 0; j < VT; ++j) o[j] *= down;
+    if (col >= nq) return;
+    const size_t head = (size_t)n * p.Hq + q0 + col, heads = (size_t)p.N * p.Hq;
+    if (p.own_splits > 1) {
+        // (nothing in the run: the join does not read the output)
+        if (count > 0)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) y[k] = top == -INFINITY && !(y[k] != y[k]) ? 0.f : y[k] / sum;
+            for (int j = 0; j < VT; ++j) *reinterpret_cast<float4v*>(&p.own_o[(run * heads + head) * D + 16 * j + 4 * g]) = o[j];
+        if (g == 0) *reinterpret_cast<float2*>(&p.own_ml[(run * heads + head) * 2]) = make_float2(m, l);
+        return;
+    }
+    const int row = (n - x.first) * rep + 16 * qg + col;
+    float top = m;
+    for (int s = 0; s < x.slots; ++s) top = fmaxf(top, p.part_ml[2 * part_of(p, x, s, kh, row)]);
+    const float at = top == -INFINITY ? 0.f : top;
+    {
+        const float f = __builtin_amdgcn_exp2f(m - at);
+        l *= f;
+#pragma unroll
+        for (int j = 0; j < VT; ++j) o[j] *= f;
+    }
+    for (int s = 0; s < x.slots; ++s) {
+        const size_t from = part_of(p, x, s, kh, row);
+        const float2 ml = *reinterpret_cast<const float2*>(&p.part_ml[2 * from]);
+        const float f = __builtin_amdgcn_exp2f(ml.x - at);
+        l += ml.y * f;
+#pragma unroll
+        for (int j = 0; j < VT; ++j) o[j] += *reinterpret_cast<const float4v*>(&p.part_o[from * D + 16 * j + 4 * g]) * f;
+    }
+    const float inv = 1.f / l;
+#pragma unroll
+    for (int j = 0; j < VT; ++j) {
+        float4v y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = l == 0.f && !(o[j][i] != o[j][i]) ? 0.f : o[j][i] * inv;   // l = 0: nothing seen
         if (p.flags & GDR_OUT_BF16)
-            *reinterpret_cast<uint2*>((uint16_t*)p.o + head * D + ch) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+            *reinterpret_cast<uint2*>((uint16_t*)p.o + head * D + 16 * j + 4 * g) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
         else
-            *reinterpret_cast<float4v*>((float*)p.o + head * D + ch) = y;
-    });
+            *reinterpret_cast<float4v*>((float*)p.o + head * D + 16 * j + 4 * g) = y;
+    }
 }
 
 // Joins a head's partial results: one workgroup per head; its lanes read the maxima
@@ -840,15 +878,18 @@ __global__ __launch_bounds__(256) void attn_shared_join(SharedParams p) {
     }
     float4v y = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-    for (int s = gi; s < slots; s += GROUPS)
-        y += *reinterpret_cast<const float4v*>(o_at(s) + ch) * __builtin_amdgcn_exp2f(*ml_at(s) - at);
+    for (int s = gi; s < slots; s += GROUPS) {
+        const float2 ml = *reinterpret_cast<const float2*>(ml_at(s));
+        if (s >= x.slots && ml.x == -INFINITY && ml.y == 0.f) continue;      // an empty run: not written
+        y += *reinterpret_cast<const float4v*>(o_at(s) + ch) * __builtin_amdgcn_exp2f(ml.x - at);
+    }
     *reinterpret_cast<float4v*>(&s_x[gi][ch]) = y;
     __syncthreads();
     if (tid < D) {
         float z = 0.f;
 #pragma unroll
         for (int i = 0; i < GROUPS; ++i) z += s_x[i][tid];
-        store_out(p, head * D + tid, top == -INFINITY && !(z != z) ? 0.f : z / s_sum);
+        store_out(p, head * D + tid, s_sum == 0.f && !(z != z) ? 0.f : z / s_sum);      // (0: nothing seen)
     }
 }
 
@@ -872,8 +913,9 @@ SharedPlan attn_shared_plan(int N, int groups, int Hq, int Hkv, int d, int max_p
     x.own_items = (long long)N * Hkv * ((rep + 15) / 16);
     int pages = max_pages;
     if (window > 0 && window / kPage + 2 < pages) pages = window / kPage + 2;
-    long long s = (512 + x.own_items - 1) / x.own_items;
-    const long long most = (pages + kWaves - 1) / kWaves;
+    // about two waves a SIMD
+    long long s = (2048 + x.own_items / 2) / x.own_items;
+    const long long most = (pages + 1) / 2;
     if (s > most) s = most;
     x.own_splits = s < 1 ? 1 : (int)s;
     // the workspace: plan, then partial results
@@ -894,7 +936,7 @@ SharedPlan attn_shared_plan(int N, int groups, int Hq, int Hkv, int d, int max_p
 }
 
 long long attn_shared_workgroups(const SharedPlan& x, long long heads) {
-    const long long most = x.items > x.own_items ? x.items : x.own_items;
+    const long long own = x.own_items * x.own_splits, most = x.items > own ? x.items : own;
     return x.own_splits > 1 && heads > most ? heads : most;
 }
 
@@ -911,7 +953,8 @@ template <int D, int PARTS, int NB> static hipError_t launch_shared(const Shared
 template <int D, int PARTS> static hipError_t launch_d(const SharedParams& p, const SharedPlan& x, hipStream_t st) {
     hipError_t e = p.width == 64 ? launch_shared<D, PARTS, 2>(p, st) : launch_shared<D, PARTS, 1>(p, st);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((attn_own_kernel<D, PARTS>), dim3((unsigned)x.own_items, (unsigned)p.own_splits), dim3(64 * kWaves), 0, st, p);
+    hipLaunchKernelGGL((attn_own_kernel<D, PARTS>), dim3((unsigned)(x.own_items * p.own_splits)), dim3(64), 0,
+                       st, p);
     e = hipGetLastError();
     if (e != hipSuccess || p.own_splits == 1) return e;
     hipLaunchKernelGGL(attn_shared_join<D>, dim3((unsigned)((long long)p.N * p.Hq)), dim3(256), 0, st, p);
@@ -919,8 +962,11 @@ template <int D, int PARTS> static hipError_t launch_d(const SharedParams& p, co
 }
 
 hipError_t launch_attn_shared(const SharedParams& p, const SharedPlan& x, hipStream_t st) {
-    hipLaunchKernelGGL(attn_shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, p);
-    const hipError_t e = hipGetLastError();
+    static std::atomic<unsigned long long> done{0};
+    hipError_t e = ensure_dyn_lds(reinterpret_cast<const void*>(&attn_shared_plan_kernel), (kMostGroups + 1) * (int)sizeof(PlanGroup), done);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(attn_shared_plan_kernel, dim3(1), dim3(kPlanThreads), (unsigned)((p.groups + 1) * sizeof(PlanGroup)), st, p);
+    e = hipGetLastError();
     if (e != hipSuccess) return e;
     const bool one = (p.flags & GDR_OUT_BF16) != 0;
     if (p.d == 64) return one ? launch_d<64, 1>(p, x, st) : launch_d<64, 2>(p, x, st);

@@ -20,10 +20,10 @@ SHARED_OK = dict(q=A, kc=A, vc=A, ks=A, vs=A, table=A, len=A, starts=A, shared=A
 @pytest.mark.parametrize("kw,status", [
     (dict(q=None), INVALID), (dict(starts=None), INVALID), (dict(shared=None), INVALID), (dict(shared=MIS), INVALID),
     (dict(o=MIS), INVALID), (dict(table=None), INVALID), (dict(N=0), INVALID), (dict(groups=0), INVALID),
-    (dict(groups=-1), INVALID), (dict(groups=BIG), INVALID), (dict(Hq=7), INVALID), (dict(pages=0), INVALID),
+    (dict(groups=-1), INVALID), (dict(groups=4097), UNSUPPORTED), (dict(Hq=7), INVALID), (dict(pages=0), INVALID),
     (dict(width=0), INVALID), (dict(width=1 << 25), INVALID), (dict(window=-1), INVALID), (dict(scale=0.0), INVALID),
     (dict(scale=math.nan), INVALID), (dict(flags=0x1), INVALID), (dict(flags=0x8000), INVALID), (dict(d=32), UNSUPPORTED),
-    (dict(N=1 << 20, Hq=1 << 20), INVALID), (dict(N=1 << 22, Hq=8), INVALID),
+    (dict(N=1 << 20, Hq=1 << 20), INVALID), (dict(N=1 << 25, Hq=8), INVALID),
     (dict(ws=None), WORKSPACE), (dict(nbytes=63), WORKSPACE), (dict(ws=MIS), INVALID),
 ])
 def test_attn_decode_shared_refusals(kw, status):
@@ -35,8 +35,9 @@ def test_attn_decode_shared_workspace_query():
     one = f(8, 1, 32, 8, 128, 800, 0)
     # a partial result of 32 rows, their maxima and sums, for each of 256 workgroups, and more
     assert one > 256 * 32 * (128 + 2) * 4
+    assert f(8, 4097, 32, 8, 128, 800, 0) == 0
     assert f(8, 1, 32, 8, 128, 800, 64) < one                # a window bounds a sequence's own pages
-    assert f(256, 1, 32, 8, 128, 800, 0) > 512 * 128 * (128 + 2) * 4
+    assert f(256, 1, 32, 8, 128, 800, 0) > 256 * 64 * (128 + 2) * 4
     for bad in ((0, 1, 32, 8, 128, 8, 0), (8, 0, 32, 8, 128, 8, 0), (8, 1, 31, 8, 128, 8, 0), (8, 1, 32, 8, 96, 8, 0),
                 (8, 1, 32, 8, 128, 8, -1)):
         assert f(*bad) == 0
