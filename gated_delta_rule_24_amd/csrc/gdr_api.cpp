@@ -157,10 +157,10 @@ gdr_status pages_args(int N, int Hkv, int d, int n_pages, int max_pages, uint32_
 
 gdr_status beam_args(int G, int K, int M, int V, long long stride, int end_token, uint32_t flags) {
     if (flags & ~(GDR_ACT_F32 | GDR_KEEP_SLOTS)) return GDR_ERR_INVALID_ARG;
-    if (G < 1 || K < 1 || M < 1 || V < 1 || V > (1 << 30) || stride < V || end_token < -1 || end_token >= V)
+    if (G < 1 || K < 1 || M < 1 || V < 1 || stride < V || end_token < -1 || end_token >= V)
         return GDR_ERR_INVALID_ARG;
     if ((long long)K * V < M || ((flags & GDR_KEEP_SLOTS) && M != K)) return GDR_ERR_INVALID_ARG;
-    if (K > gdr::kMostBeams || M > gdr::kMostSelected) return GDR_ERR_UNSUPPORTED;
+    if (K > gdr::kMostBeams || M > gdr::kMostSelected || V > gdr::kMostTokens) return GDR_ERR_UNSUPPORTED;
     // rows are on the grid's second axis; element offsets in 64 bits
     if ((long long)G * K > 65535 || stride > (1LL << 40)) return GDR_ERR_INVALID_ARG;
     return GDR_OK;

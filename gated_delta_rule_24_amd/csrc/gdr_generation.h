@@ -75,6 +75,7 @@ long long attn_shared_workgroups(const SharedPlan& x, long long heads);
 hipError_t launch_attn_shared(const SharedParams& p, const SharedPlan& x, hipStream_t st);
 
 constexpr int kMostBeams = 64, kMostSelected = 64;
+constexpr int kMostTokens = 1 << 26;                  // of a vocabulary
 struct BeamParams {
     const void* logits;         // [G * K] rows of V, `stride` elements apart
     const float* scores;        // [G * K]

@@ -691,7 +691,7 @@ gdr_status gdr_kv_compact(void* k_cache, void* v_cache, float* k_scale, float* v
  * continuation of a beam in the beam's own place, the others, in order, in the places
  * left: then what a beam has (its state, its table's row) moves only where it has to.
  * Log-sums are formed in fp32 from each row's maximum and joined in 64 bits; scores are
- * compared in 64 bits and rounded once.  Supported: K, M <= 64, M <= K V.
+ * compared in 64 bits and rounded once.  Supported: K, M <= 64, M <= K V, V <= 2^26.
  */
 size_t gdr_beam_select_workspace_bytes(int G, int K, int M, int V);
 

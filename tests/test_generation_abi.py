@@ -95,7 +95,7 @@ SELECT_OK = dict(logits=A, scores=A, ended=A, tokens=A, rows=A, sout=A, eout=A, 
 @pytest.mark.parametrize("kw,status", [
     (dict(logits=None), INVALID), (dict(logits=MIS), INVALID), (dict(scores=None), INVALID), (dict(ended=MIS), INVALID),
     (dict(tokens=None), INVALID), (dict(rows=None), INVALID), (dict(sout=None), INVALID), (dict(eout=None), INVALID),
-    (dict(G=0), INVALID), (dict(K=0), INVALID), (dict(M=0), INVALID), (dict(V=0), INVALID), (dict(V=BIG), INVALID),
+    (dict(G=0), INVALID), (dict(K=0), INVALID), (dict(M=0), INVALID), (dict(V=0), INVALID), (dict(V=BIG), INVALID), (dict(V=(1 << 26) + 1, stride=1 << 27), UNSUPPORTED),
     (dict(stride=99), INVALID), (dict(end=100), INVALID), (dict(end=-2), INVALID), (dict(end=-1), INVALID),
     (dict(flags=0x2), INVALID), (dict(M=4, flags=0x8000), INVALID), (dict(M=301, K=3), UNSUPPORTED),
     (dict(K=1, M=5, V=4, stride=4), INVALID), (dict(K=65, M=1), UNSUPPORTED), (dict(M=65), UNSUPPORTED),
