@@ -10,6 +10,7 @@
 // the j-th lowest free one.
 #include "gdr_device.h"
 #include "gdr_generation.h"
+#include "gdr_launch.h"
 
 namespace gdr {
 
@@ -19,7 +20,7 @@ constexpr int kPage = 64;
 constexpr int kThreads = 256;
 constexpr int kPagesPerBlock = 4096;                  // pages that a workgroup counts
 constexpr int kEntriesPerBlock = 2048;                // entries of one row that a workgroup copies
-constexpr int kCopyBytes = 16384;                     // bytes of a page that a workgroup copies
+constexpr int kCopyBytes = 8192;                      // bytes of a page that a workgroup copies
 constexpr int kCopyWorkgroups = 4096;                 // compact: workgroups that take the moved pages in turn
 
 // A page's counters: entries that name it in the low half, rows that will write
@@ -102,7 +103,7 @@ __device__ __forceinline__ int block_before(int x, int* s, int& all) {
     return base + run - x;
 }
 
-// 16 KiB of a page from one place to another: part `part` of the keys' bytes, then
+// 8 KiB of a page from one place to another: part `part` of the keys' bytes, then
 // the values', then (part 0) the scales.
 __device__ __forceinline__ void copy_part(const PagesParams& p, int from, int to, int part) {
     const size_t side = (size_t)p.Hkv * kPage * p.d, all = 2 * side;
@@ -230,12 +231,12 @@ __global__ __launch_bounds__(kThreads) void fork_assign(PagesParams p, ForkSpace
         }
     }
     // this thread's pages: 16 in a row, so that their ranks follow each other
-    constexpr int kMine = kPagesPerBlock / kThreads;
-    const int first = blockIdx.x * kPagesPerBlock + tid * kMine;
+    constexpr int kRow = kPagesPerBlock / kThreads;
+    const int first = blockIdx.x * kPagesPerBlock + tid * kRow;
     uint32_t mine = 0;
     if (base < total) {
 #pragma unroll
-        for (int i = 0; i < kMine; ++i)
+        for (int i = 0; i < kRow; ++i)
             if (first + i < p.n_pages && s.count[first + i] == 0 && !(p.held && p.held[first + i])) mine |= 1u << i;
     }
     int all;
@@ -267,8 +268,166 @@ __global__ __launch_bounds__(kThreads) void fork_assign(PagesParams p, ForkSpace
 }
 
 __global__ __launch_bounds__(kThreads) void fork_copy(PagesParams p, ForkSpace s, int parts) {
-    const int n = blockIdx.x / parts, to = s.place[n];
-    if (to >= 0) copy_part(p, s.source[n], to, blockIdx.x % parts);
+    const int n = blockIdx.x / parts, to = s.place[n], from = s.source[n];   // (without a place, no page: not read)
+    if (to >= 0) copy_part(p, from, to, blockIdx.x % parts);
+}
+
+// The same for caches and tables that one workgroup has soon read: the counters are in
+// LDS, and a call is this kernel and the copies.  (A cache of 4,600 pages, 256 rows of 40 pages:
+// five launches take 47.5 us a call, two 32; rows of 68 pages, 51 and 36; of 130 pages, 50 and 42.
+// 4 rows of 17 pages: 28 and 20, of which the kernels are 9.)  Compaction of 120 rows of 66
+// pages: 104 and 88; of 250 rows of 80 pages 43 and 41, of 160 pages 41 and 51.
+constexpr int kSmallThreads = 1024;
+constexpr int kMine = 12;                             // pages a thread
+constexpr int kSmallPages = kMine * kSmallThreads, kSmallRows = 2048;   // (LDS: 8 bytes a page, 16 a row)
+constexpr int kForkEntries = 40 * kSmallThreads;      // (counters of 16 bits)
+constexpr int kCompactEntries = 20 * kSmallThreads;
+bool small_tables(int N, int n_pages, int max_pages, int entries) {
+    return n_pages <= kSmallPages && N <= kSmallRows && (long long)N * max_pages <= entries;
+}
+
+// sum over the threads of 1,024 before this one; `all` the workgroup's
+__device__ __forceinline__ int wide_before(int x, int* s, int& all) {
+    int run = x;
+    for (int o = 1; o < 64; o <<= 1) {
+        const int y = __shfl_up(run, o, 64);
+        if ((int)(threadIdx.x & 63) >= o) run += y;
+    }
+    __syncthreads();
+    if ((threadIdx.x & 63) == 63) s[threadIdx.x >> 6] = run;
+    __syncthreads();
+    int base = 0;
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < kSmallThreads / 64; ++w) {
+        if (w < (int)(threadIdx.x >> 6)) base += s[w];
+        all += s[w];
+    }
+    return base + run - x;
+}
+
+// Bit i: page first + i is held.  (All loads at once, before the first wait.)
+__device__ __forceinline__ uint32_t held_bits(const PagesParams& p, int first) {
+    if (!p.held) return 0;
+    uint32_t h[kMine], bits = 0;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) h[i] = p.held[min(first + i, p.n_pages - 1)];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) bits |= h[i] ? 1u << i : 0;
+    return bits;
+}
+
+// Every entry of the rows' tables, eight at a time a thread (their loads do not wait for
+// each other): f(place, row, entry of the row, the page it names or -1).
+template <typename F>
+__device__ __forceinline__ void entries_of(const PagesParams& p, const int* len, const int* from, const F& f) {
+    constexpr int kAtOnce = 8;
+    const int entries = p.N * p.max_pages;
+    for (int at0 = threadIdx.x; at0 < entries; at0 += kAtOnce * kSmallThreads) {
+        int n[kAtOnce], i[kAtOnce], page[kAtOnce];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            const int at = min(at0 + j * kSmallThreads, entries - 1);
+            n[j] = at / p.max_pages;
+            i[j] = at - n[j] * p.max_pages;
+            page[j] = -1;
+            if (i[j] < pages_of(len[n[j]])) page[j] = p.block_table[from ? (size_t)from[n[j]] * p.max_pages + i[j] : (size_t)at];
+        }
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j)
+            if (at0 + j * kSmallThreads < entries)
+                f(at0 + j * kSmallThreads, n[j], i[j], (unsigned)page[j] < (unsigned)p.n_pages ? page[j] : -1);
+    }
+}
+
+size_t fork_small_lds(int N, int n_pages) { return 8 * (size_t)n_pages + 16 * (size_t)N; }
+
+__global__ __launch_bounds__(kSmallThreads) void fork_small(PagesParams p, ForkSpace s) {
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    __shared__ int s_sum[kSmallThreads / 64];
+    uint32_t* count = reinterpret_cast<uint32_t*>(smem);             // [n_pages] entries that name it, and rows that write into it << 16
+    int* lowest = reinterpret_cast<int*>(count + p.n_pages);         // [n_pages]
+    int* from = lowest + p.n_pages;                                  // [N] the row continued; then 1: the first page is a copy
+    int* len = from + p.N;                                           // [N]
+    int* before = len + p.N;                                         // [N] the entry it writes into, or -1; then the pages wanted by the rows before
+    int* into = before + p.N;                                        // [N] the page it writes into, or -1
+    const int tid = threadIdx.x;
+    const int mine = (p.n_pages + kSmallThreads - 1) / kSmallThreads, first = tid * mine;
+    const uint32_t held = held_bits(p, first);
+    for (int n = tid; n < p.N; n += kSmallThreads) {
+        int l;
+        from[n] = row_of(p, n, l);
+        len[n] = l;
+        before[n] = l % kPage != 0 && room_of(p, n) > 0 ? l / kPage : -1;
+        into[n] = -1;
+        p.len_out[n] = l;
+        s.place[n] = -1;
+    }
+    for (int i = tid; i < 2 * p.n_pages; i += kSmallThreads) count[i] = 0;
+    __syncthreads();
+    entries_of(p, len, from, [&](int at, int n, int i, int page) {
+        p.table_out[at] = page;
+        if (page >= 0) {
+            const bool written = i == before[n];
+            atomicAdd(&count[page], written ? 0x10001u : 1u);
+            if (written) {
+                atomicMax(&lowest[page], p.N - n);
+                into[n] = page;
+            }
+        }
+    });
+    __syncthreads();
+    // what each row wants: `per` rows a thread, one after the other
+    const int per = (p.N + kSmallThreads - 1) / kSmallThreads, first_row = min(tid * per, p.N), end_row = min(first_row + per, p.N);
+    int want_all = 0;
+    for (int n = first_row; n < end_row; ++n) {
+        const int l = len[n], room = room_of(p, n), page = into[n];
+        int want = 0;
+        bool copy = false;
+        if (from[n] >= 0 && room > 0) {
+            want = min(pages_of((long long)l + room), p.max_pages) - pages_of(l);
+            if (page >= 0) {
+                // alone, or the lowest of rows that all write: this row keeps it
+                const uint32_t c = count[page];
+                copy = !((c & 0xffff) == c >> 16 && lowest[page] == p.N - n && !(p.held && p.held[page]));
+            }
+        }
+        want += copy;
+        from[n] = copy;
+        before[n] = want;
+        want_all += want;
+    }
+    int total, free_all;
+    int run = wide_before(want_all, s_sum, total);
+    for (int n = first_row; n < end_row; ++n) {
+        const int want = before[n];
+        before[n] = run;
+        run += want;
+    }
+    // the free pages among this thread's and their ranks
+    uint32_t free = 0;
+    for (int i = 0; i < mine; ++i)
+        if (first + i < p.n_pages && count[first + i] == 0 && !(held >> i & 1)) free |= 1u << i;
+    int rank = wide_before(__popc(free), s_sum, free_all);
+    for (int n = first_row; n < end_row; ++n) {
+        const int end = n + 1 < end_row ? before[n + 1] : run;
+        p.missing[n] = max(0, min(end - before[n], end - free_all));
+    }
+    for (; free && rank < total; free &= free - 1, ++rank) {
+        const int page = first + __ffs(free) - 1;
+        int lo = 0, hi = p.N - 1;                     // the last row that starts at or before this rank: it wants some
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (before[mid] <= rank) lo = mid;
+            else hi = mid - 1;
+        }
+        const int n = lo, k = rank - before[n], copy = from[n];
+        if (copy && k == 0) {
+            s.source[n] = into[n];
+            s.place[n] = page;
+        }
+        p.table_out[(size_t)n * p.max_pages + pages_of(len[n]) + k - copy] = page;
+    }
 }
 
 size_t kv_fork_workspace(int N, int n_pages) {
@@ -284,6 +443,15 @@ long long kv_fork_workgroups(int N, int Hkv, int d, int n_pages, int max_pages) 
 
 hipError_t launch_kv_fork(const PagesParams& p, hipStream_t st) {
     const ForkSpace s = fork_space(p.workspace, p.N, p.n_pages);
+    const int parts = copy_parts(p.Hkv, p.d);
+    if (small_tables(p.N, p.n_pages, p.max_pages, kForkEntries)) {
+        static std::atomic<unsigned long long> done{0};
+        const hipError_t e = ensure_dyn_lds(reinterpret_cast<const void*>(&fork_small), (int)fork_small_lds(kSmallRows, kSmallPages), done);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(fork_small, dim3(1), dim3(kSmallThreads), (unsigned)fork_small_lds(p.N, p.n_pages), st, p, s);
+        hipLaunchKernelGGL(fork_copy, dim3((unsigned)(p.N * (long long)parts)), dim3(kThreads), 0, st, p, s, parts);
+        return hipGetLastError();
+    }
     const long long vecs = (long long)(up16(8 * (size_t)p.n_pages) + up16(4 * (size_t)p.n_pages)) / 16;
     const dim3 block(kThreads);
     hipLaunchKernelGGL(pages_clear, dim3((unsigned)(vecs < 1024 * kThreads ? blocks_of(vecs, kThreads) : 1024)), block, 0, st,
@@ -293,7 +461,6 @@ hipError_t launch_kv_fork(const PagesParams& p, hipStream_t st) {
     const int blocks = blocks_of(p.n_pages, kPagesPerBlock), row_blocks = blocks_of(p.N, kThreads);
     hipLaunchKernelGGL(fork_count, dim3((unsigned)(blocks > row_blocks ? blocks : row_blocks)), block, 0, st, p, s);
     hipLaunchKernelGGL(fork_assign, dim3((unsigned)blocks), block, 0, st, p, s, blocks);
-    const int parts = copy_parts(p.Hkv, p.d);
     hipLaunchKernelGGL(fork_copy, dim3((unsigned)(p.N * (long long)parts)), block, 0, st, p, s, parts);
     return hipGetLastError();
 }
@@ -376,11 +543,11 @@ __global__ __launch_bounds__(kThreads) void compact_lists(PagesParams p, Compact
         free_all += block_sum(f, s_sum);
         used_all += block_sum(u, s_sum);
     }
-    constexpr int kMine = kPagesPerBlock / kThreads;
-    const int first = blockIdx.x * kPagesPerBlock + tid * kMine;
+    constexpr int kRow = kPagesPerBlock / kThreads;
+    const int first = blockIdx.x * kPagesPerBlock + tid * kRow;
     uint32_t free = 0, used = 0;
 #pragma unroll
-    for (int i = 0; i < kMine; ++i) {
+    for (int i = 0; i < kRow; ++i) {
         const int page = first + i;
         if (page < p.n_pages) {
             const bool held = p.held && p.held[page];
@@ -402,7 +569,78 @@ __global__ __launch_bounds__(kThreads) void compact_lists(PagesParams p, Compact
     if (blockIdx.x == 0 && tid == 0) { s.counts[0] = free_all; s.counts[1] = used_all; }
 }
 
-// The moves, 16 KiB a workgroup at a time, and the rows that follow them.
+// The same for caches and tables that one workgroup has soon read: which pages are named, the
+// lists and the ranks are in LDS, the rows follow at once, and what is left to another
+// kernel are the moves.
+size_t compact_small_lds(int N, int n_pages) { return 4 * (size_t)((n_pages + 31) / 32) + 4 * (size_t)N + 6 * (size_t)n_pages; }
+
+__global__ __launch_bounds__(kSmallThreads) void compact_small(PagesParams p, CompactSpace s) {
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    __shared__ int s_sum[kSmallThreads / 64];
+    __shared__ int s_top;
+    uint32_t* named = reinterpret_cast<uint32_t*>(smem);             // a bit a page
+    int* len = reinterpret_cast<int*>(named + (p.n_pages + 31) / 32);                   // [N]
+    uint16_t* free_list = reinterpret_cast<uint16_t*>(len + p.N);    // [n_pages] free pages, ascending
+    uint16_t* used_list = free_list + p.n_pages;                     // [n_pages] pages that may move, descending
+    uint16_t* place = used_list + p.n_pages;                         // [n_pages] where a page is afterwards
+    const int tid = threadIdx.x;
+    const int mine = (p.n_pages + kSmallThreads - 1) / kSmallThreads, first = tid * mine;
+    const uint32_t held = held_bits(p, first);
+    for (int i = tid; i < (p.n_pages + 31) / 32; i += kSmallThreads) named[i] = 0;
+    for (int n = tid; n < p.N; n += kSmallThreads) {
+        int l;
+        row_of(p, n, l);
+        len[n] = l;
+    }
+    if (tid == 0) s_top = 0;
+    __syncthreads();
+    entries_of(p, len, nullptr, [&](int, int, int, int page) {
+        // (rows behind one prompt name the same pages: most find the bit there)
+        if (page >= 0 && !(named[page >> 5] >> (page & 31) & 1)) atomicOr(&named[page >> 5], 1u << (page & 31));
+    });
+    __syncthreads();
+    // this thread's pages, in a row
+    uint32_t free = 0, used = 0;
+    int top = 0;
+    for (int i = 0; i < mine; ++i) {
+        const int page = first + i;
+        if (page < p.n_pages) {
+            place[page] = (uint16_t)page;
+            if (held >> i & 1) top = page + 1;
+            else if (named[page >> 5] >> (page & 31) & 1) used |= 1u << i;
+            else free |= 1u << i;
+        }
+    }
+    int free_all, used_all;
+    int f = wide_before(__popc(free), s_sum, free_all), u = wide_before(__popc(used), s_sum, used_all);
+    u = used_all - u - 1;                             // of this thread's lowest page that may move
+    for (; free; free &= free - 1) free_list[f++] = (uint16_t)(first + __ffs(free) - 1);
+    for (; used; used &= used - 1) used_list[u--] = (uint16_t)(first + __ffs(used) - 1);
+    __syncthreads();
+    for (int j = tid; j < used_all; j += kSmallThreads) {
+        int page = used_list[j];
+        if (j < free_all && free_list[j] < page) {
+            s.free_list[j] = free_list[j];
+            s.used_list[j] = page;
+            place[page] = free_list[j];
+            page = free_list[j];
+        } else if (j < free_all) {                    // (the first of these ends the moves)
+            s.free_list[j] = s.used_list[j] = 0;
+        }
+        top = max(top, page + 1);
+    }
+    for (int o = 32; o > 0; o >>= 1) top = max(top, __shfl_xor(top, o, 64));
+    if ((tid & 63) == 0) atomicMax(&s_top, top);
+    __syncthreads();
+    entries_of(p, len, nullptr, [&](int at, int, int, int page) { p.table_out[at] = page >= 0 ? (int)place[page] : -1; });
+    if (tid == 0) {
+        p.used[0] = s_top;
+        s.counts[0] = free_all;
+        s.counts[1] = used_all;
+    }
+}
+
+// The moves, 8 KiB a workgroup at a time, and (rows > 0) the rows that follow them.
 __global__ __launch_bounds__(kThreads) void compact_move(PagesParams p, CompactSpace s, int parts, int chunks, int rows) {
     const int free = s.counts[0], used = s.counts[1], pairs = min(free, used);
     if ((int)blockIdx.x < rows) {
@@ -431,11 +669,11 @@ __global__ __launch_bounds__(kThreads) void compact_move(PagesParams p, CompactS
     for (long long it = (long long)blockIdx.x - rows; it < items; it += step) {
         const int j = (int)(it / parts);
         const int to = s.free_list[j], from = s.used_list[j];
-        if (to > from) break;
+        if (to >= from) break;
         copy_part(p, from, to, (int)(it % parts));
     }
     // pages up to the last in use: the last destination, or the first that stays
-    if ((int)blockIdx.x == rows) {
+    if (rows > 0 && (int)blockIdx.x == rows) {
         for (int j = threadIdx.x; j <= pairs; j += kThreads) {
             const bool moves = j < pairs && s.free_list[j] < s.used_list[j];
             const bool before = j == 0 || s.free_list[j - 1] < s.used_list[j - 1];
@@ -458,17 +696,26 @@ hipError_t launch_kv_compact(const PagesParams& p, hipStream_t st) {
     CompactSpace s;
     compact_take(p.workspace, p.n_pages, &s);
     const dim3 block(kThreads);
+    const int parts = copy_parts(p.Hkv, p.d);
+    // at most half the pages move
+    const long long items = ((long long)p.n_pages / 2) * parts;
+    const int movers = items < 1 ? 1 : items < kCopyWorkgroups ? (int)items : kCopyWorkgroups;
+    if (small_tables(p.N, p.n_pages, p.max_pages, kCompactEntries)) {
+        static std::atomic<unsigned long long> done{0};
+        const hipError_t e = ensure_dyn_lds(reinterpret_cast<const void*>(&compact_small), (int)compact_small_lds(kSmallRows, kSmallPages), done);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(compact_small, dim3(1), dim3(kSmallThreads), (unsigned)compact_small_lds(p.N, p.n_pages), st, p, s);
+        hipLaunchKernelGGL(compact_move, dim3((unsigned)movers), block, 0, st, p, s, parts, 1, 0);
+        return hipGetLastError();
+    }
     const long long vecs = (long long)up16(4 * (size_t)p.n_pages) / 16;
     hipLaunchKernelGGL(pages_clear, dim3((unsigned)(vecs < 1024 * kThreads ? blocks_of(vecs, kThreads) : 1024)), block, 0, st,
                        reinterpret_cast<uint4*>(s.named), vecs);
     const int chunks = blocks_of(p.max_pages, kEntriesPerBlock), blocks = blocks_of(p.n_pages, kPagesPerBlock);
-    const int rows = p.N * chunks, parts = copy_parts(p.Hkv, p.d);
+    const int rows = p.N * chunks;
     hipLaunchKernelGGL(compact_rows, dim3((unsigned)rows), block, 0, st, p, s, chunks);
     hipLaunchKernelGGL(compact_count, dim3((unsigned)blocks), block, 0, st, p, s);
     hipLaunchKernelGGL(compact_lists, dim3((unsigned)blocks), block, 0, st, p, s, blocks);
-    // at most half the pages move
-    const long long items = ((long long)p.n_pages / 2) * parts;
-    const int movers = items < 1 ? 1 : items < kCopyWorkgroups ? (int)items : kCopyWorkgroups;
     hipLaunchKernelGGL(compact_move, dim3((unsigned)(rows + movers)), block, 0, st, p, s, parts, chunks, rows);
     return hipGetLastError();
 }
