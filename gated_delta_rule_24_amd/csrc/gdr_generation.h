@@ -40,7 +40,8 @@ hipError_t launch_kv_compact(const PagesParams& p, hipStream_t st);
 // where the parts of its workspace start.
 struct SharedPlan {
     int width;                  // rows of a workgroup for shared pages: 32 or 64
-    long long items;            // workgroups for the shared pages, at most
+    long long units;            // (group, key head, `width` of its rows) that there can be
+    int workgroups;             // for the shared pages, at most
     long long own_items;        // (sequence, key head, set of 16 query heads)
     int own_splits;             // runs that a sequence's own pages are dealt into
     size_t at_head, at_groups, at_group_of, at_items, at_part_o, at_part_ml, at_own_o, at_own_ml, bytes;
@@ -57,16 +58,16 @@ struct SharedParams {
     const int* group_start;     // [groups + 1]
     const int* shared_pages;    // [groups]
     void* o;
-    int* plan_head;             // [2] items, pages of a run
+    void* plan_head;            // workgroups, pages of each
     void* plan_groups;          // [groups]
     int* plan_group_of;         // [N] a sequence's group, or -1
-    int* plan_items;            // [items] an item's group
-    float* part_o;              // [items, width, d] unnormalised
-    float* part_ml;             // [items, width, 2] maximum (base 2) and sum
+    int* plan_items;            // [workgroups] the group that one starts in
+    float* part_o;              // [units + workgroups, width, d] unnormalised
+    float* part_ml;             // [units + workgroups, width, 2] maximum (base 2) and sum
     float* own_o;               // [own_splits, N, Hq, d] and its maxima and sums, where own_splits > 1
     float* own_ml;
     int N, groups, Hq, Hkv, d, n_pages, max_pages, window;
-    int width, items, own_splits;
+    int width, units, workgroups, own_splits;
     float scale;
     uint32_t flags;
 };

@@ -10,8 +10,6 @@
 // shared pages are read once for the rows (a sequence's query heads on a key head) of
 // the whole group, as further columns of the products that one sequence's heads
 // already share in gdr_attn_decode.
-#include <type_traits>
-
 #include "gdr_device.h"
 #include "gdr_attn.h"
 #include "gdr_attn_tile.h"
@@ -24,7 +22,7 @@ namespace gdr {
 namespace {
 
 constexpr int kPage = 64;
-constexpr int kWaves = 4;
+constexpr int kWaves = 8;
 // Weights reach 2^(kTop + kLag) = 2^15 at most: f16 has room for that.
 constexpr float kLag = 3.f, kTop = 12.f;
 
@@ -38,23 +36,28 @@ __device__ __forceinline__ void seen_range(const SharedParams& p, int n, int& lo
     lo = (p.window > 0 && len > p.window) ? min(len - p.window, hi) : 0;
 }
 
-// What the plan makes of group g (see attn_shared_plan_kernel).
+// What the plan makes of group g (see attn_shared_plan_kernel).  Unit kh * tiles + tile of it
+// is `width` of its rows on a key head, over all its shared pages.
 struct Group {
     int first, rows;            // its first sequence; rows: its (sequence, query head) pairs on a key head
-    int pg0, pg1;               // the shared pages that some row of it sees
-    int tiles;                  // workgroups that its rows take
-    int slots;                  // runs of pages; 0: nothing shared
-    int base;                   // its first item: item base + (slot * Hkv + kh) * tiles + tile
+    int pg0, pages;             // the shared pages that some row of it sees; 0: nothing shared
+    int unit0;                  // its first unit's number
     int shared;                 // pages that it shares, seen or not
+    long long pos0;             // the place of its first unit's pages in the line of all
 };
 static_assert(sizeof(Group) == 32, "read as two 16-byte loads");
 
-// Which group sequence n is in, or -1; and the one that is read as.
-__device__ __forceinline__ Group group_of(const SharedParams& p, int g) {
+__device__ __forceinline__ Group group_at(const SharedParams& p, int g) {
     const int4* at = reinterpret_cast<const int4*>(p.plan_groups) + 2 * (size_t)g;
     const int4 x = at[0], y = at[1];
-    return Group{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    return Group{x.x, x.y, x.z, x.w, y.x, y.y, (long long)((uint64_t)(uint32_t)y.z | (uint64_t)(uint32_t)y.w << 32)};
 }
+struct PlanHead {
+    int workgroups;
+    int whole;                  // units are stretched to whole runs
+    long long per;              // pages of a workgroup
+};
+__device__ __forceinline__ PlanHead plan_head(const SharedParams& p) { return *reinterpret_cast<const PlanHead*>(p.plan_head); }
 
 __device__ __forceinline__ void store_out(const SharedParams& p, size_t idx, float x) {
     if (p.flags & GDR_OUT_BF16) reinterpret_cast<uint16_t*>(p.o)[idx] = f32_to_bf16(x);
@@ -115,25 +118,28 @@ __device__ __forceinline__ void join_waves(const O& o, const ML& ml, int from, i
 // the plan
 // ---------------------------------------------------------------------------
 //
-// One workgroup looks at the groups and deals out their shared pages, as the host does
-// not know them: a run has the same number of pages in every group, so that long
-// prefixes take more workgroups than short ones and all end together; as many
-// pages as keep the items (run, key head, tile of rows) within the workgroups that
-// can be at work at once.
+// One workgroup looks at the groups, as the host does not know them, and lays the pages of all
+// units end to end: each of as many workgroups as can be at work at once takes a run of the same
+// length of that line, over the ends of units, so that all end together.  (With whole runs of each
+// unit's pages, as many as fit, 3 groups of 340 rows on 256 pages kept 144 of 256
+// workgroups: 119 us, _ now.)
 constexpr int kPlanThreads = 1024;
 
 struct PlanGroup {
     int first, shared, lo, hi;  // first sequence; pages; first and one past the last token that some sequence sees
-    int base;
+    int unit0;                  // -1: not shared
+    long long pos0;
 };
 
 __global__ __launch_bounds__(kPlanThreads) void attn_shared_plan_kernel(SharedParams p) {
     extern __shared__ __attribute__((aligned(256))) char smem[];
     PlanGroup* s = reinterpret_cast<PlanGroup*>(smem);       // [groups + 1]
-    __shared__ int s_per, s_items;
+    __shared__ long long s_per;
+    __shared__ int s_workgroups, s_whole, s_fits[kPlanThreads / 64];
+    static_assert(kPlanThreads / 64 > kWaves, "a wave for each length");
     const int tid = threadIdx.x, lane = tid & 63, rep = p.Hq / p.Hkv, G = p.groups;
     for (int g = tid; g <= G; g += kPlanThreads)
-        s[g] = PlanGroup{clampi(p.group_start[g], 0, p.N), g < G ? clampi(p.shared_pages[g], 0, p.max_pages) : 0, INT_MAX, 0, 0};
+        s[g] = PlanGroup{clampi(p.group_start[g], 0, p.N), g < G ? clampi(p.shared_pages[g], 0, p.max_pages) : 0, INT_MAX, 0, 0, 0};
     __syncthreads();
     for (int n = tid; n < p.N; n += kPlanThreads) {
         int a, b;
@@ -152,75 +158,99 @@ __global__ __launch_bounds__(kPlanThreads) void attn_shared_plan_kernel(SharedPa
         }
     }
     __syncthreads();
-    // one wave: a run's pages, and where each group's items start
+    // one wave: where each group's units and pages start
     auto tiles_of = [&](int g) {
         const long long rows = (long long)max(s[g + 1].first - s[g].first, 0) * rep;
         return (int)((rows + p.width - 1) / p.width);
     };
     auto first_page = [&](int g) { return s[g].lo / kPage; };
     auto pages_of = [&](int g) { return max(0, min((int)(((long long)s[g].hi + kPage - 1) / kPage), s[g].shared) - first_page(g)); };
+    auto sum_of = [&](auto f) {
+        long long x = 0;
+        for (int g = lane; g < G; g += 64) x += (long long)tiles_of(g) * p.Hkv * f(pages_of(g));
+        for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o, 64);
+        return x;
+    };
+    // runs of `per` that a unit's pages take
+    auto runs_of = [&](int pages, long long per) {
+        return pages <= per ? 1 : (int)(((uint32_t)pages + (uint32_t)per - 1) / (uint32_t)per);
+    };
+    // two pages a wave, as the second's keys are loaded beside the first one's work
+    const long long all = sum_of([](int pages) { return (long long)pages; });
+    long long per = max((all + p.workgroups - 1) / p.workgroups, 2LL * kWaves);
+    // a unit's start and end are worth some pages: whole runs of a unit where they are little
+    // longer (each wave looks at another length)
+    {
+        const long long longer = per + (tid >> 6);
+        const bool fits = sum_of([&](int pages) { return pages > 0 ? runs_of(pages, longer) : 0; }) <= p.workgroups;
+        if (lane == 0) s_fits[tid >> 6] = fits;
+    }
+    __syncthreads();
     if (tid < 64) {
-        auto sum_of = [&](auto f) {
-            long long x = 0;
-            for (int g = lane; g < G; g += 64) x += f(g);
-            for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o, 64);
-            return x;
-        };
-        int most = 0;
-        for (int g = lane; g < G; g += 64) most = max(most, pages_of(g));
-        for (int o = 32; o > 0; o >>= 1) most = max(most, __shfl_xor(most, o, 64));
-        const long long room = p.items / p.Hkv;       // (tile, run) pairs of a key head
-        const long long all = sum_of([&](int g) { return (long long)tiles_of(g) * pages_of(g); });
-        int per = max((int)min((all + room - 1) / max(room, 1LL), (long long)INT_MAX / 2), 2 * kWaves);   // two pages a wave
-        while (per < most && sum_of([&](int g) { return (long long)tiles_of(g) * ((pages_of(g) + per - 1) / per); }) > room)
-            per += (per + 15) / 16;
-        long long before = 0;
-        int end = INT_MAX;
+        bool whole = false;
+        for (int i = 0; i <= kWaves && !whole; ++i)
+            if (s_fits[i]) {
+                whole = true;
+                per += i;
+            }
+        long long units = 0, pos = 0;                 // of the groups before
         for (int g0 = 0; g0 < G; g0 += 64) {
             const int g = g0 + lane;
-            const long long mine = g < G ? (long long)tiles_of(g) * ((pages_of(g) + per - 1) / per) * p.Hkv : 0;
-            long long run = mine;
+            const int pages = g < G ? pages_of(g) : 0;
+            long long u = pages > 0 ? (long long)tiles_of(g) * p.Hkv : 0;
+            // (bounds that overlap may want more units than there are: such a group shares nothing)
+            long long run = u;
             for (int o = 1; o < 64; o <<= 1) {
                 const long long y = __shfl_up(run, o, 64);
                 if (lane >= o) run += y;
             }
-            const long long base = before + run - mine;
-            // (bounds that overlap may want more than there are: from there on nothing is shared)
-            const bool fits = base + mine <= p.items;
-            if (g < G) s[g].base = fits ? (int)base : -1;
-            if (!fits) end = min(end, (int)min(base, (long long)p.items));
-            before += __shfl(run, 63, 64);
+            const bool fits = u > 0 && units + run <= p.units;
+            const long long mine = !fits ? 0 : whole ? u * (runs_of(pages, per) * per) : u * pages;
+            long long at = mine;
+            for (int o = 1; o < 64; o <<= 1) {
+                const long long y = __shfl_up(at, o, 64);
+                if (lane >= o) at += y;
+            }
+            if (g < G) {
+                s[g].unit0 = fits ? (int)(units + run - u) : -1;
+                s[g].pos0 = pos + at - mine;
+            }
+            units += __shfl(run, 63, 64);
+            pos += __shfl(at, 63, 64);
         }
-        for (int o = 32; o > 0; o >>= 1) end = min(end, __shfl_xor(end, o, 64));
-        if (lane == 0) { s_per = per; s_items = (int)min(before, (long long)end); }
+        if (lane == 0) {
+            s_per = per;
+            s_whole = whole;
+            s_workgroups = (int)((pos + s_per - 1) / s_per);
+        }
     }
     __syncthreads();
-    const int per = s_per;
     Group* groups = reinterpret_cast<Group*>(p.plan_groups);
     for (int g = tid; g < G; g += kPlanThreads) {
         Group x;
         x.first = s[g].first;
         x.rows = max(s[g + 1].first - s[g].first, 0) * rep;
-        x.pg0 = pages_of(g) > 0 ? first_page(g) : 0;
-        x.pg1 = x.pg0 + pages_of(g);
-        x.tiles = tiles_of(g);
-        x.slots = s[g].base < 0 ? 0 : (pages_of(g) + per - 1) / per;
-        x.base = max(s[g].base, 0);
+        x.pages = s[g].unit0 < 0 ? 0 : pages_of(g);
+        x.pg0 = x.pages > 0 ? first_page(g) : 0;
+        x.unit0 = max(s[g].unit0, 0);
         x.shared = s[g].shared;
+        x.pos0 = s[g].pos0;
         groups[g] = x;
     }
-    for (int i = tid; i < s_items; i += kPlanThreads) {      // the last group that starts at or before item i
+    for (int w = tid; w < s_workgroups; w += kPlanThreads) { // the last group that starts at or before this one's run
         int g = 0, z = G - 1;
         while (g < z) {
             const int mid = (g + z + 1) / 2;
-            if (s[mid].base >= 0 && s[mid].base <= i) g = mid;
+            if (s[mid].pos0 <= w * s_per) g = mid;
             else z = mid - 1;
         }
-        p.plan_items[i] = g;
+        p.plan_items[w] = g;
     }
     if (tid == 0) {
-        p.plan_head[0] = s_items;
-        p.plan_head[1] = per;
+        PlanHead* head = reinterpret_cast<PlanHead*>(p.plan_head);
+        head->workgroups = s_workgroups;
+        head->whole = s_whole;
+        head->per = s_per;
     }
 }
 
@@ -248,10 +278,11 @@ __global__ __launch_bounds__(kPlanThreads) void attn_shared_plan_kernel(SharedPa
 // fp32 results, as one (11 bits) for bf16 ones, whose own rounding is 8 times that.  The
 // sum takes the same exponentials, times 2^-b once a page; where |b| is large (a page of
 // zeros has a scale of 2^-96) it has its own.
-template <int D>
+template <int D, int NB>
 struct __attribute__((aligned(256))) SharedSmem {
+    uint4 q[NB * D / 16][64];                         // queries, operand by operand
     union {
-        uint8_t ring[kWaves][2][2 * kPage * D];       // keys [64][D], then values [4][D][16]
+        uint8_t page[kWaves][2 * kPage * D];          // keys [64][D], then values [4][D][16]
         struct {
             float o[kWaves][32][D + 4];
             float ml[kWaves][32][2];
@@ -292,30 +323,51 @@ struct PageLoader {
 };
 
 typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
+typedef uint32_t uint2v __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint2v read8(uint32_t at) { return *(const __attribute__((address_space(3))) uint2v*)(uintptr_t)at; }
 __device__ __forceinline__ uint4v read16(uint32_t at) { return *(const __attribute__((address_space(3))) uint4v*)(uintptr_t)at; }
 
+// pages of the line that one of group x's units takes
+__device__ __forceinline__ long long length_of(const PlanHead& head, const Group& x) {
+    return head.whole ? (x.pages + head.per - 1) / head.per * head.per : x.pages;
+}
+
+// all but the last N of this wave's loads have arrived
+template <int N> __device__ __forceinline__ void wait_but() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
+
 template <int D, int PARTS, int NB>
-__global__ __launch_bounds__(64 * kWaves, 1) void attn_shared_kernel(SharedParams p) {
+__global__ __launch_bounds__(64 * kWaves, 2) void attn_shared_kernel(SharedParams p) {
     constexpr int KL = D / 32;                        // 16-byte reads of a key's row by a lane
     constexpr int DB = D / 32;                        // 32-channel tiles of the output
     constexpr int kRows = 32 * NB;                    // of the workgroup: its waves have the same ones
     extern __shared__ __attribute__((aligned(256))) char smem[];
-    SharedSmem<D>& sm = *reinterpret_cast<SharedSmem<D>*>(smem);
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int col = lane & 31, h = lane >> 5, rep = p.Hq / p.Hkv;
+    SharedSmem<D, NB>& sm = *reinterpret_cast<SharedSmem<D, NB>*>(smem);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), rep = p.Hq / p.Hkv;
 
-    // consecutive workgroups go round the 8 XCDs: each of these takes a run of items, the
+    // consecutive workgroups go round the 8 XCDs: each of these takes a run of them, the
     // tiles that share pages one after the other
-    const int items = p.plan_head[0], each = (items + 7) / 8;
-    const int item = (blockIdx.x % 8) * each + blockIdx.x / 8;
-    if ((int)(blockIdx.x / 8) >= each || item >= items) return;
-    const Group x = group_of(p, p.plan_items[item]);
-    const int per = p.plan_head[1];
-    int rest = item - x.base;
-    const int tile = rest % x.tiles; rest /= x.tiles;
-    const int kh = rest % p.Hkv, slot = rest / p.Hkv;
+    const PlanHead head = plan_head(p);
+    const int each = (head.workgroups + 7) / 8, wg = (blockIdx.x % 8) * each + blockIdx.x / 8;
+    if ((int)(blockIdx.x / 8) >= each || wg >= head.workgroups) return;
+    int group = p.plan_items[wg];
+    Group x = group_at(p, group);
+    // the unit and its page that the run starts with, and the run's length
+    long long left = head.per, length = length_of(head, x);
+    int unit, page0;
+    {
+        const long long rel = wg * head.per - x.pos0;
+        unit = (int)(rel / length);
+        page0 = (int)(rel % length);
+    }
+    for (;;) {
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));                    // (what follows from it is not kept over the units)
+    const int col = lane & 31, h = lane >> 5;
+    const int tiles = (x.rows + kRows - 1) / kRows, tile = unit % tiles, kh = __builtin_amdgcn_readfirstlane(unit / tiles);
     const int row0 = kRows * tile, rows = min(kRows, x.rows - row0);
-    const int pg0 = x.pg0 + slot * per, pg1 = min(pg0 + per, x.pg1);
+    const int pg0 = __builtin_amdgcn_readfirstlane(x.pg0 + page0);
+    const int pg1 = __builtin_amdgcn_readfirstlane((int)min((long long)pg0 + left, (long long)x.pg0 + x.pages));
+    const size_t part0 = (size_t)(x.unit0 + unit + wg) * kRows;
     const int n = max(0, (pg1 - pg0 - wave + kWaves - 1) / kWaves);      // pages of this wave
 
     // this wave's pages k0 .. k0 + 63, one a lane: place (-1: absent) and scales
@@ -331,36 +383,29 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_shared_kernel(SharedParam
         e_vs = p.v_scale[ph];
     };
     const PageLoader<D, false> loader(lane);
-    const uint32_t ring = attn::lds_address(sm.ring[wave][0]);
+    const uint32_t place = attn::lds_address(sm.page[wave]);
     constexpr uint32_t kSide = kPage * D;
     // (an absent page is read as the first one: its bytes are masked)
-    auto load = [&](int k) {
-        const int pg = __builtin_amdgcn_readlane(e_page, k & 63);
-        const size_t at = ((size_t)max(pg, 0) * p.Hkv + kh) * kSide;
-        const uint32_t to = ring + (k & 1) * (2 * kSide);
-        loader.keys((uint64_t)p.k_cache + at, to);
-        loader.values((uint64_t)p.v_cache + at, to + kSide);
-    };
+    auto page_at = [&](int k) { return ((size_t)max(__builtin_amdgcn_readlane(e_page, k & 63), 0) * p.Hkv + kh) * kSide; };
     look_up(0);
-    if (n > 0) load(0);
+    if (n > 0) {
+        loader.keys((uint64_t)p.k_cache + page_at(0), place);
+        loader.values((uint64_t)p.v_cache + page_at(0), place + kSide);
+    }
 
     // this lane's rows: their queries (channels 32 s + 16 h .. + 15) and the keys they see
-    bf8v qf[NB][KL][2];
     int lo[NB], hi[NB], lo_most = 0, hi_least = INT_MAX, lo_least = INT_MAX, hi_most = 0;
 #pragma unroll
     for (int c = 0; c < NB; ++c) {
         const int mine = 32 * c + col;
         const bool live = mine < rows;
         const int seq = x.first + (row0 + mine) / rep, head = kh * rep + (row0 + mine) % rep;
-#pragma unroll
-        for (int s = 0; s < KL; ++s)
-#pragma unroll
-            for (int f = 0; f < 2; ++f) {
-                uint4 u = make_uint4(0, 0, 0, 0);
-                if (live)
-                    u = *reinterpret_cast<const uint4*>((const uint16_t*)p.q + ((size_t)seq * p.Hq + head) * D + 32 * s + 16 * h + 8 * f);
-                qf[c][s][f] = __builtin_bit_cast(bf8v, u);
-            }
+        for (int s = wave; s < 2 * KL; s += kWaves) {
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (live)
+                u = *reinterpret_cast<const uint4*>((const uint16_t*)p.q + ((size_t)seq * p.Hq + head) * D + 32 * (s / 2) + 16 * h + 8 * (s % 2));
+            sm.q[2 * KL * c + s][lane] = u;
+        }
         lo[c] = hi[c] = 0;
         if (live) {
             seen_range(p, seq, lo[c], hi[c]);
@@ -397,6 +442,10 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_shared_kernel(SharedParam
         v_at = kPage * D + (h * D + col) * 16;
     }
 
+    const uint32_t q_at = attn::lds_address(sm.q) + 16 * lane;
+    // (the pages' loads go on)
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+
     uint32_t nans = 0;                                // some value that not every row sees is NaN
     for (int k = 0; k < n; ++k) {
         const int page = __builtin_amdgcn_readlane(e_page, k & 63);
@@ -404,19 +453,8 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_shared_kernel(SharedParam
         const float vs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(e_vs), k & 63));
         const int at0 = (pg0 + wave + k * kWaves) * kPage;
         const bool absent = page < 0;
-        const uint32_t ring_k = ring + (k & 1) * (2 * kSide) + k_at, ring_v = ring + (k & 1) * (2 * kSide) + v_at;
-        // this page is there, and the place of the one before it is free: its reads are done
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-        if (k + 1 < n) {
-            if (((k + 1) & 63) == 0) look_up(k + 1);
-            load(k + 1);
-        }
-
-        uint4v kr[2][KL];
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int s = 0; s < KL; ++s) kr[b][s] = read16((ring_k ^ (32 * s)) + 32 * b * D);
+        // the keys are there: what was asked for behind them are values
+        wait_but<PageLoader<D, false>::N>();
         float16v st[NB][2];
 #pragma unroll
         for (int c = 0; c < NB; ++c)
@@ -425,20 +463,34 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_shared_kernel(SharedParam
 #pragma unroll
                 for (int j = 0; j < 16; ++j) st[c][b][j] = 0.f;
 #pragma unroll
-        for (int s = 0; s < KL; ++s)
+        for (int s = 0; s < KL; ++s) {
+            uint4v kr[2], qr[NB][2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) kr[b] = read16(((place + k_at) ^ (32 * s)) + 32 * b * D);
+#pragma unroll
+            for (int c = 0; c < NB; ++c)
+#pragma unroll
+                for (int f = 0; f < 2; ++f) qr[c][f] = read16(q_at + 1024 * (2 * KL * c + 2 * s + f));
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const bf8v k0 = e4m3x8_to_bf16(kr[b][s].x, kr[b][s].y), k1 = e4m3x8_to_bf16(kr[b][s].z, kr[b][s].w);
+                const bf8v k0 = e4m3x8_to_bf16(kr[b].x, kr[b].y), k1 = e4m3x8_to_bf16(kr[b].z, kr[b].w);
 #pragma unroll
-                for (int c = 0; c < NB; ++c) st[c][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k0, qf[c][s][0], st[c][b], 0, 0, 0);
+                for (int c = 0; c < NB; ++c) st[c][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k0, __builtin_bit_cast(bf8v, qr[c][0]), st[c][b], 0, 0, 0);
 #pragma unroll
-                for (int c = 0; c < NB; ++c) st[c][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k1, qf[c][s][1], st[c][b], 0, 0, 0);
+                for (int c = 0; c < NB; ++c) st[c][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k1, __builtin_bit_cast(bf8v, qr[c][1]), st[c][b], 0, 0, 0);
             }
-        uint4v vr[2][DB];
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int i = 0; i < DB; ++i) vr[b][i] = read16(ring_v + (2 * b * D + 32 * i) * 16);
+        }
+        // the keys are read: the next page's take their place while these values are worked on
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (k + 1 < n) {
+            if (((k + 1) & 63) == 0) look_up(k + 1);
+            loader.keys((uint64_t)p.k_cache + page_at(k + 1), place);
+        }
+        // (the values are older than these, where there are any)
+        auto wait_values = [&] {
+            if (k + 1 < n) wait_but<PageLoader<D, false>::N>();
+            else wait_but<0>();
+        };
 
         float by = ks * to2;                          // a score is st times this
         const bool edge = absent || at0 < lo_most || at0 + kPage > hi_least;
@@ -461,20 +513,23 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_shared_kernel(SharedParam
                 // some row sees the page in part: values of keys that no row sees count as 0,
                 // and so do NaNs, which the 0 of a row that does not see them would carry
                 // over: the rows that see them get them at the end
+                // (in LDS: a lane writes what it will read)
                 const uint32_t some = absent ? 0 : seen_bits(at0 + 16 * h, lo_least, hi_most);
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
+                wait_values();
+                for (int i = 0; i < 2 * DB; ++i) {
+                    const int b = i & 1;
+                    const uint32_t at = place + v_at + (2 * b * D + 16 * (i & ~1)) * 16;
+                    uint4v u = read16(at);
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
-                        const uint32_t keep = bytes_of(some, 16 * b + 4 * t);
-#pragma unroll
-                        for (int i = 0; i < DB; ++i) {
-                            uint32_t y = vr[b][i][t] & keep;
-                            const uint32_t whole = (nan_bytes(y) >> 7) * 0xffu;
-                            nans |= whole;
-                            vr[b][i][t] = y & ~whole;
-                        }
+                        const uint32_t y = u[t] & bytes_of(some, 16 * b + 4 * t);
+                        const uint32_t whole = (nan_bytes(y) >> 7) * 0xffu;
+                        nans |= whole;
+                        u[t] = y & ~whole;
                     }
+                    *(__attribute__((address_space(3))) uint4v*)(uintptr_t)at = u;
+                }
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
             }
         }
 
@@ -535,39 +590,49 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_shared_kernel(SharedParam
             }
         }
 
-        half8 w_hi[NB][2], w_lo[NB][2];
-        auto weights = [&](int c, int b) {
-            float sum[2] = {0.f, 0.f};
+        wait_values();
+        // (with two parts a weight, the weights of 32 keys do not fit into the registers: 16 at a
+        // time then, 233 us for 247 of 256 sequences behind 3 prompts; with one part, 111 for 101)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(st[c][b][i], by, up[c]));
-                sum[i & 1] += w;
-                const _Float16 a = (_Float16)w;
-                w_hi[c][i / 8][i % 8] = a;
-                if (PARTS == 2) w_lo[c][i / 8][i % 8] = (_Float16)(w - (float)a);
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int f0 = 0; f0 < 2; f0 += 3 - PARTS) {
+                half8 w_hi[NB][3 - PARTS], w_lo[NB];
+#pragma unroll
+                for (int c = 0; c < NB; ++c) {
+                    float sum[2] = {0.f, 0.f};
+#pragma unroll
+                    for (int i = 0; i < 8 * (3 - PARTS); ++i) {
+                        const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(st[c][b][8 * f0 + i], by, up[c]));
+                        sum[i & 1] += w;
+                        const _Float16 a = (_Float16)w;
+                        w_hi[c][i / 8][i % 8] = a;
+                        if (PARTS == 2) w_lo[c][i % 8] = (_Float16)(w - (float)a);
+                    }
+                    l[c] += (sum[0] + sum[1]) * share[c];
+                }
+#pragma unroll
+                for (int i = 0; i < DB; ++i) {
+                    const uint32_t at = place + v_at + (2 * b * D + 32 * i) * 16;
+                    if constexpr (PARTS == 2) {
+                        const uint2v u = read8(at + 8 * f0);
+                        const half8 v = e4m3x8_to_f16(u.x, u.y);
+#pragma unroll
+                        for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w_hi[c][0], o[c][i], 0, 0, 0);
+#pragma unroll
+                        for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w_lo[c], o[c][i], 0, 0, 0);
+                    } else {
+                        const uint4v u = read16(at);
+                        const half8 v0 = e4m3x8_to_f16(u.x, u.y), v1 = e4m3x8_to_f16(u.z, u.w);
+#pragma unroll
+                        for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v0, w_hi[c][0], o[c][i], 0, 0, 0);
+#pragma unroll
+                        for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v1, w_hi[c][2 - PARTS], o[c][i], 0, 0, 0);
+                    }
+                }
             }
-            l[c] += (sum[0] + sum[1]) * share[c];
-        };
-        auto product = [&](int i, half8 v0, half8 v1) {
-#pragma unroll
-            for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v0, w_hi[c][0], o[c][i], 0, 0, 0);
-#pragma unroll
-            for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v1, w_hi[c][1], o[c][i], 0, 0, 0);
-            if (PARTS == 2) {
-#pragma unroll
-                for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v0, w_lo[c][0], o[c][i], 0, 0, 0);
-#pragma unroll
-                for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v1, w_lo[c][1], o[c][i], 0, 0, 0);
-            }
-        };
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-#pragma unroll
-            for (int c = 0; c < NB; ++c) weights(c, b);
-#pragma unroll
-            for (int i = 0; i < DB; ++i)
-                product(i, e4m3x8_to_f16(vr[b][i].x, vr[b][i].y), e4m3x8_to_f16(vr[b][i].z, vr[b][i].w));
-        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (k + 1 < n) loader.values((uint64_t)p.v_cache + page_at(k + 1), place + kSide);
     }
 
     // the waves that had the same rows join, in LDS, 32 rows at a time: no load into it is
@@ -590,13 +655,13 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_shared_kernel(SharedParam
             }
         lds_barrier();
         // all their lanes together
-        const size_t part = (size_t)item * kRows + 32 * c;
+        const size_t part = part0 + 32 * c;
         join_waves<D>(sm.o, sm.ml, 0, 1, kWaves, min(32, rows - 32 * c), wave * 64 + lane, kWaves * 64, [&](int r, int ch, float4v y, float2 ml) {
             *reinterpret_cast<float4v*>(&p.part_o[(part + r) * D + ch]) = y;
             if (ch == 0) *reinterpret_cast<float2*>(&p.part_ml[(part + r) * 2]) = ml;
         });
     }
-    if (!__syncthreads_or(nans != 0)) return;
+    if (__syncthreads_or(nans != 0)) {
     // NaNs among values that not every row sees: into the rows that see them, one by one
     __threadfence_block();
     for (int pg = pg0; pg < pg1; ++pg) {
@@ -609,9 +674,23 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_shared_kernel(SharedParam
             for (int r = 0; r < rows; ++r) {
                 int a, b;
                 seen_range(p, x.first + (row0 + r) / rep, a, b);
-                if (j >= a && j < b) p.part_o[((size_t)item * kRows + r) * D + ch] = NAN;
+                if (j >= a && j < b) p.part_o[(part0 + r) * D + ch] = NAN;
             }
         }
+    }
+    }
+    // the next unit
+    left -= length - page0;
+    if (left <= 0) return;
+    page0 = 0;
+    if (++unit == tiles * p.Hkv) {
+        unit = 0;
+        do {
+            if (++group >= p.groups) return;
+            x = group_at(p, group);
+        } while (x.pages == 0);
+        length = length_of(head, x);
+    }
     }
 }
 
@@ -627,16 +706,33 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_shared_kernel(SharedParam
 // has all pages it joins the shared ones' partial results as well and writes the output;
 // else a kernel behind this one does.
 
-// where the partial result of run `slot` of group x's pages is for a sequence's query head
-__device__ __forceinline__ size_t part_of(const SharedParams& p, const Group& x, int slot, int kh, int row) {
-    return (size_t)(x.base + (slot * p.Hkv + kh) * x.tiles + row / p.width) * p.width + row % p.width;
+// where the partial results of a row's shared pages are: those of a unit's pages, cut at the
+// ends of the workgroups' runs, lie one after the other
+struct Parts {
+    size_t first;
+    int n;
+};
+__device__ __forceinline__ Parts parts_of(const SharedParams& p, const Group& x, int kh, int row) {
+    if (x.pages == 0) return {0, 0};
+    const PlanHead head = plan_head(p);
+    const int unit = kh * ((x.rows + p.width - 1) / p.width) + row / p.width;
+    const long long at = x.pos0 + unit * length_of(head, x), end = at + x.pages - 1;
+    long long w0, w1;
+    if ((end | head.per) >> 32 == 0) {                // (64-bit divisions take some hundred instructions)
+        w0 = (uint32_t)at / (uint32_t)head.per;
+        w1 = (uint32_t)end / (uint32_t)head.per;
+    } else {
+        w0 = at / head.per;
+        w1 = end / head.per;
+    }
+    return {(size_t)(x.unit0 + unit + w0) * p.width + row % p.width, (int)(w1 - w0) + 1};
 }
 
 template <int D, int PARTS>
 __global__ __launch_bounds__(64) void attn_own_kernel(SharedParams p) {
     constexpr int KS = D / 64;                        // 64-channel steps of a key row
     constexpr int VT = D / 16;                        // 16-channel tiles of the output
-    __shared__ __attribute__((aligned(256))) uint8_t s_ring[2][2 * kPage * D];       // keys [64][D], then values [4][D][16]
+    __shared__ __attribute__((aligned(256))) uint8_t s_page[2 * kPage * D];          // keys [64][D], then values [4][D][16]
     const int lane = threadIdx.x;
     const int col = lane & 15, g = lane >> 4;
     const int rep = p.Hq / p.Hkv, sets = (rep + 15) / 16;
@@ -659,8 +755,8 @@ __global__ __launch_bounds__(64) void attn_own_kernel(SharedParams p) {
                 u = *reinterpret_cast<const uint4*>((const uint16_t*)p.q + ((size_t)n * p.Hq + q0 + col) * D + 64 * s + 16 * g + 8 * hf);
             qf[s][hf] = __builtin_bit_cast(bf8v, u);
         }
-    Group x = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (gi >= 0) x = group_of(p, gi);
+    Group x = {0, 0, 0, 0, 0, 0, 0};
+    if (gi >= 0) x = group_at(p, gi);
     int pg0 = max(lo / kPage, x.shared), pg1 = (int)(((long long)hi + kPage - 1) / kPage);
     run_of(pg0, pg1, run, p.own_splits);
     pg0 = __builtin_amdgcn_readfirstlane(pg0);
@@ -679,20 +775,17 @@ __global__ __launch_bounds__(64) void attn_own_kernel(SharedParams p) {
         e_vs = p.v_scale[ph];
     };
     const PageLoader<D, true> loader(lane);
-    const uint32_t ring = attn::lds_address(s_ring[0]);
+    const uint32_t place = attn::lds_address(s_page);
     constexpr uint32_t kSide = kPage * D;
-    auto load = [&](int k) {                          // (an absent page is read as the first one)
-        const size_t at = ((size_t)max(__builtin_amdgcn_readlane(e_page, k & 63), 0) * p.Hkv + kh) * kSide;
-        const uint32_t to = ring + (k & 1) * (2 * kSide);
-        loader.keys((uint64_t)p.k_cache + at, to);
-        loader.values((uint64_t)p.v_cache + at, to + kSide);
-    };
+    // (an absent page is read as the first one)
+    auto page_at = [&](int k) { return ((size_t)max(__builtin_amdgcn_readlane(e_page, k & 63), 0) * p.Hkv + kh) * kSide; };
     if (count > 0) {
         look_up(0);
-        load(0);
+        loader.keys((uint64_t)p.k_cache + page_at(0), place);
+        loader.values((uint64_t)p.v_cache + page_at(0), place + kSide);
     }
     const int krow = 16 * (col >> 2) + (col & 3);     // key of tile 0's row `col`; its flip is that of the others, + 4 t, too
-    const uint32_t k_at = krow * D + 16 * (g ^ key_flip<D, true>(krow)), v_at = kSide + (g * D + col) * 16;
+    const uint32_t at_k = place + krow * D + 16 * (g ^ key_flip<D, true>(krow)), at_v = place + kSide + (g * D + col) * 16;
 
     float4v o[VT];
 #pragma unroll
@@ -703,13 +796,8 @@ __global__ __launch_bounds__(64) void attn_own_kernel(SharedParams p) {
         const int page = __builtin_amdgcn_readlane(e_page, k & 63);
         const float k_scale = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(e_ks), k & 63));
         const float v_scale = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(e_vs), k & 63));
-        // this page is there, and the place of the one before it is free: its reads are done
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-        if (k + 1 < count) {
-            if (((k + 1) & 63) == 0) look_up(k + 1);
-            load(k + 1);
-        }
-        const uint32_t at_k = ring + (k & 1) * (2 * kSide) + k_at, at_v = ring + (k & 1) * (2 * kSide) + v_at;
+        // the keys are there: what was asked for behind them are values
+        wait_but<PageLoader<D, true>::N>();
         const int at0 = (pg0 + k) * kPage;
         const bool absent = page < 0;
         const float ks = k_scale * to2, vs = absent ? -INFINITY : __builtin_amdgcn_logf(v_scale);   // base 2
@@ -726,8 +814,20 @@ __global__ __launch_bounds__(64) void attn_own_kernel(SharedParams p) {
             }
             sc[t] *= ks;
         }
+        // the keys are read: the next page's take their place, then the values'
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        const bool more = k + 1 < count;
+        if (more) {
+            if (((k + 1) & 63) == 0) look_up(k + 1);
+            loader.keys((uint64_t)p.k_cache + page_at(k + 1), place);
+            wait_but<PageLoader<D, true>::N>();
+        } else {
+            wait_but<0>();
+        }
 #pragma unroll
         for (int j = 0; j < VT; ++j) vv[j] = read16(at_v + 256 * j);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (more) loader.values((uint64_t)p.v_cache + page_at(k + 1), place + kSide);
         if (absent || at0 < lo || at0 + kPage > hi) {
             // the first and last pages: masked keys count nothing, whatever their bytes
             uint32_t keep[4];
@@ -804,7 +904,8 @@ __global__ __launch_bounds__(64) void attn_own_kernel(SharedParams p) {
     }
     const int row = (n - x.first) * rep + 16 * qg + col;
     float top = m;
-    for (int s = 0; s < x.slots; ++s) top = fmaxf(top, p.part_ml[2 * part_of(p, x, s, kh, row)]);
+    const Parts parts = parts_of(p, x, kh, row);
+    for (int s = 0; s < parts.n; ++s) top = fmaxf(top, p.part_ml[2 * (parts.first + s * (size_t)p.width)]);
     const float at = top == -INFINITY ? 0.f : top;
     {
         const float f = __builtin_amdgcn_exp2f(m - at);
@@ -812,8 +913,8 @@ __global__ __launch_bounds__(64) void attn_own_kernel(SharedParams p) {
 #pragma unroll
         for (int j = 0; j < VT; ++j) o[j] *= f;
     }
-    for (int s = 0; s < x.slots; ++s) {
-        const size_t from = part_of(p, x, s, kh, row);
+    for (int s = 0; s < parts.n; ++s) {
+        const size_t from = parts.first + s * (size_t)p.width;
         const float2 ml = *reinterpret_cast<const float2*>(&p.part_ml[2 * from]);
         const float f = __builtin_amdgcn_exp2f(ml.x - at);
         l += ml.y * f;
@@ -843,14 +944,15 @@ __global__ __launch_bounds__(256) void attn_shared_join(SharedParams p) {
     const int tid = threadIdx.x, gi = tid / (D / 4), ch = 4 * (tid % (D / 4));
     const int n = (int)(head / p.Hq), hq = (int)(head % p.Hq), rep = p.Hq / p.Hkv;
     const int in = p.plan_group_of[n];
-    Group x = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (in >= 0) x = group_of(p, in);
-    const int row = (n - x.first) * rep + hq % rep, slots = x.slots + p.own_splits;
+    Group x = {0, 0, 0, 0, 0, 0, 0};
+    if (in >= 0) x = group_at(p, in);
+    const Parts parts = parts_of(p, x, hq / rep, (n - x.first) * rep + hq % rep);
+    const int slots = parts.n + p.own_splits;
     auto ml_at = [&](int s) {
-        return s < x.slots ? &p.part_ml[2 * part_of(p, x, s, hq / rep, row)] : &p.own_ml[((s - x.slots) * heads + head) * 2];
+        return s < parts.n ? &p.part_ml[2 * (parts.first + s * (size_t)p.width)] : &p.own_ml[((s - parts.n) * heads + head) * 2];
     };
     auto o_at = [&](int s) {
-        return s < x.slots ? &p.part_o[part_of(p, x, s, hq / rep, row) * D] : &p.own_o[((s - x.slots) * heads + head) * D];
+        return s < parts.n ? &p.part_o[(parts.first + s * (size_t)p.width) * D] : &p.own_o[((s - parts.n) * heads + head) * D];
     };
     float top = -INFINITY, sum = 0.f;
     for (int s = tid; s < slots; s += 256) {
@@ -880,7 +982,7 @@ __global__ __launch_bounds__(256) void attn_shared_join(SharedParams p) {
 #pragma unroll 4
     for (int s = gi; s < slots; s += GROUPS) {
         const float2 ml = *reinterpret_cast<const float2*>(ml_at(s));
-        if (s >= x.slots && ml.x == -INFINITY && ml.y == 0.f) continue;      // an empty run: not written
+        if (s >= parts.n && ml.x == -INFINITY && ml.y == 0.f) continue;      // an empty run: not written
         y += *reinterpret_cast<const float4v*>(o_at(s) + ch) * __builtin_amdgcn_exp2f(ml.x - at);
     }
     *reinterpret_cast<float4v*>(&s_x[gi][ch]) = y;
@@ -906,10 +1008,8 @@ SharedPlan attn_shared_plan(int N, int groups, int Hq, int Hkv, int d, int max_p
     // at most: every group's last tile has one row
     const long long some = groups < N ? groups : N;
     const long long tiles = (rows + some * (x.width - 1)) / x.width;
-    // items: as many workgroups as the compute units' LDS holds; more only where there are
-    // more tiles than that
-    const long long fill = d == 64 ? 512 : 256;
-    x.items = tiles * Hkv > fill ? tiles * Hkv : fill;
+    x.units = tiles * Hkv;
+    x.workgroups = d == 64 && x.width == 32 ? 512 : 256;      // as many as LDS and registers hold
     x.own_items = (long long)N * Hkv * ((rep + 15) / 16);
     int pages = max_pages;
     if (window > 0 && window / kPage + 2 < pages) pages = window / kPage + 2;
@@ -925,9 +1025,9 @@ SharedPlan attn_shared_plan(int N, int groups, int Hq, int Hkv, int d, int max_p
     x.at_head = take(16);
     x.at_groups = take(sizeof(Group) * (size_t)groups);
     x.at_group_of = take(4 * (size_t)N);
-    x.at_items = take(4 * (size_t)x.items);
-    x.at_part_o = take(4 * (size_t)x.items * x.width * d);
-    x.at_part_ml = take(8 * (size_t)x.items * x.width);
+    x.at_items = take(4 * (size_t)x.workgroups);
+    x.at_part_o = take(4 * (size_t)(x.units + x.workgroups) * x.width * d);
+    x.at_part_ml = take(8 * (size_t)(x.units + x.workgroups) * x.width);
     const size_t own = x.own_splits > 1 ? (size_t)x.own_splits * N * Hq : 0;
     x.at_own_o = take(4 * own * d);
     x.at_own_ml = take(8 * own);
@@ -936,17 +1036,17 @@ SharedPlan attn_shared_plan(int N, int groups, int Hq, int Hkv, int d, int max_p
 }
 
 long long attn_shared_workgroups(const SharedPlan& x, long long heads) {
-    const long long own = x.own_items * x.own_splits, most = x.items > own ? x.items : own;
+    // (units are numbered in 32 bits as well)
+    const long long own = x.own_items * x.own_splits, units = x.units + x.workgroups, most = units > own ? units : own;
     return x.own_splits > 1 && heads > most ? heads : most;
 }
 
 template <int D, int PARTS, int NB> static hipError_t launch_shared(const SharedParams& p, hipStream_t st) {
     static std::atomic<unsigned long long> done{0};
-    const int lds = (int)sizeof(SharedSmem<D>);
+    const int lds = (int)sizeof(SharedSmem<D, NB>);
     const hipError_t e = ensure_dyn_lds(reinterpret_cast<const void*>(&attn_shared_kernel<D, PARTS, NB>), lds, done);
     if (e != hipSuccess) return e;
-    // (the items of the 8 XCDs' runs: up to 7 more numbers than items)
-    hipLaunchKernelGGL((attn_shared_kernel<D, PARTS, NB>), dim3((unsigned)((p.items + 7) / 8 * 8)), dim3(64 * kWaves), lds, st, p);
+    hipLaunchKernelGGL((attn_shared_kernel<D, PARTS, NB>), dim3((unsigned)p.workgroups), dim3(64 * kWaves), lds, st, p);
     return hipGetLastError();
 }
 
