@@ -685,17 +685,18 @@ gdr_status gdr_attn_decode_shared(const void* q, const void* k_cache, const void
     p.group_start = group_start; p.shared_pages = shared_pages; p.o = o;
     p.N = N; p.groups = groups; p.Hq = Hq; p.Hkv = Hkv; p.d = d; p.n_pages = n_pages; p.max_pages = max_pages;
     p.window = window; p.width = x.width; p.units = (int)x.units; p.workgroups = x.workgroups; p.own_splits = x.own_splits;
+    p.own_runs = x.own_items * x.own_splits;
     char* ws = static_cast<char*>(workspace);
     p.plan_head = ws + x.at_head;
     p.plan_groups = ws + x.at_groups;
-    p.plan_group_of = reinterpret_cast<int*>(ws + x.at_group_of);
+    p.plan_sequences = ws + x.at_sequences;
     p.plan_items = reinterpret_cast<int*>(ws + x.at_items);
     p.part_o = reinterpret_cast<float*>(ws + x.at_part_o);
     p.part_ml = reinterpret_cast<float*>(ws + x.at_part_ml);
     p.own_o = reinterpret_cast<float*>(ws + x.at_own_o);
     p.own_ml = reinterpret_cast<float*>(ws + x.at_own_ml);
     p.scale = scale; p.flags = flags;
-    return from_hip(gdr::launch_attn_shared(p, x, (hipStream_t)stream));
+    return from_hip(gdr::launch_attn_shared(p, (hipStream_t)stream));
 }
 
 size_t gdr_kv_fork_workspace_bytes(int N, int n_pages) {

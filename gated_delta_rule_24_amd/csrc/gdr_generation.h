@@ -44,7 +44,7 @@ struct SharedPlan {
     int workgroups;             // for the shared pages, at most
     long long own_items;        // (sequence, key head, set of 16 query heads)
     int own_splits;             // runs that a sequence's own pages are dealt into
-    size_t at_head, at_groups, at_group_of, at_items, at_part_o, at_part_ml, at_own_o, at_own_ml, bytes;
+    size_t at_head, at_groups, at_sequences, at_items, at_part_o, at_part_ml, at_own_o, at_own_ml, bytes;
 };
 constexpr int kMostGroups = 4096;                     // the plan has them in LDS
 struct SharedParams {
@@ -60,7 +60,7 @@ struct SharedParams {
     void* o;
     void* plan_head;            // workgroups, pages of each
     void* plan_groups;          // [groups]
-    int* plan_group_of;         // [N] a sequence's group, or -1
+    void* plan_sequences;       // [N] each sequence's group, as in plan_groups
     int* plan_items;            // [workgroups] the group that one starts in
     float* part_o;              // [units + workgroups, width, d] unnormalised
     float* part_ml;             // [units + workgroups, width, 2] maximum (base 2) and sum
@@ -68,12 +68,13 @@ struct SharedParams {
     float* own_ml;
     int N, groups, Hq, Hkv, d, n_pages, max_pages, window;
     int width, units, workgroups, own_splits;
+    long long own_runs;         // own_items * own_splits
     float scale;
     uint32_t flags;
 };
 SharedPlan attn_shared_plan(int N, int groups, int Hq, int Hkv, int d, int max_pages, int window);
 long long attn_shared_workgroups(const SharedPlan& x, long long heads);
-hipError_t launch_attn_shared(const SharedParams& p, const SharedPlan& x, hipStream_t st);
+hipError_t launch_attn_shared(const SharedParams& p, hipStream_t st);
 
 constexpr int kMostBeams = 64, kMostSelected = 64;
 constexpr int kMostTokens = 1 << 26;                  // of a vocabulary

@@ -22,7 +22,7 @@ namespace gdr {
 namespace {
 
 constexpr int kPage = 64;
-constexpr int kWaves = 8;
+constexpr int kWaves = 4;
 // Weights reach 2^(kTop + kLag) = 2^15 at most: f16 has room for that.
 constexpr float kLag = 3.f, kTop = 12.f;
 
@@ -47,8 +47,8 @@ struct Group {
 };
 static_assert(sizeof(Group) == 32, "read as two 16-byte loads");
 
-__device__ __forceinline__ Group group_at(const SharedParams& p, int g) {
-    const int4* at = reinterpret_cast<const int4*>(p.plan_groups) + 2 * (size_t)g;
+__device__ __forceinline__ Group group_at(const void* groups, int g) {
+    const int4* at = reinterpret_cast<const int4*>(groups) + 2 * (size_t)g;
     const int4 x = at[0], y = at[1];
     return Group{x.x, x.y, x.z, x.w, y.x, y.y, (long long)((uint64_t)(uint32_t)y.z | (uint64_t)(uint32_t)y.w << 32)};
 }
@@ -124,6 +124,7 @@ __device__ __forceinline__ void join_waves(const O& o, const ML& ml, int from, i
 // unit's pages, as many as fit, 3 groups of 340 rows on 256 pages kept 144 of 256
 // workgroups: 119 us, _ now.)
 constexpr int kPlanThreads = 1024;
+constexpr int kLonger = 8;                            // pages that a unit's start and end are worth
 
 struct PlanGroup {
     int first, shared, lo, hi;  // first sequence; pages; first and one past the last token that some sequence sees
@@ -136,23 +137,27 @@ __global__ __launch_bounds__(kPlanThreads) void attn_shared_plan_kernel(SharedPa
     PlanGroup* s = reinterpret_cast<PlanGroup*>(smem);       // [groups + 1]
     __shared__ long long s_per;
     __shared__ int s_workgroups, s_whole, s_fits[kPlanThreads / 64];
-    static_assert(kPlanThreads / 64 > kWaves, "a wave for each length");
+    static_assert(kPlanThreads / 64 > kLonger, "a wave for each length");
     const int tid = threadIdx.x, lane = tid & 63, rep = p.Hq / p.Hkv, G = p.groups;
-    for (int g = tid; g <= G; g += kPlanThreads)
-        s[g] = PlanGroup{clampi(p.group_start[g], 0, p.N), g < G ? clampi(p.shared_pages[g], 0, p.max_pages) : 0, INT_MAX, 0, 0, 0};
-    __syncthreads();
-    for (int n = tid; n < p.N; n += kPlanThreads) {
-        int a, b;
-        seen_range(p, n, a, b);
+    int a0 = 0, b0 = 0;                               // of the first sequence it looks at: asked for before the groups
+    if (tid < p.N) seen_range(p, tid, a0, b0);
+    auto group_of = [&](int n) {                      // or -1
         int g = 0, z = G - 1;                         // the last start at or before n
         while (g < z) {
             const int mid = (g + z + 1) / 2;
             if (s[mid].first <= n) g = mid;
             else z = mid - 1;
         }
-        const bool in = n >= s[g].first && n < s[g + 1].first;
-        p.plan_group_of[n] = in ? g : -1;
-        if (in && a < b) {
+        return n >= s[g].first && n < s[g + 1].first ? g : -1;
+    };
+    for (int g = tid; g <= G; g += kPlanThreads)
+        s[g] = PlanGroup{clampi(p.group_start[g], 0, p.N), g < G ? clampi(p.shared_pages[g], 0, p.max_pages) : 0, INT_MAX, 0, 0, 0};
+    __syncthreads();
+    for (int n = tid; n < p.N; n += kPlanThreads) {
+        int a = a0, b = b0;
+        if (n != tid) seen_range(p, n, a, b);
+        const int g = group_of(n);
+        if (g >= 0 && a < b) {
             atomicMin(&s[g].lo, a);
             atomicMax(&s[g].hi, b);
         }
@@ -188,7 +193,7 @@ __global__ __launch_bounds__(kPlanThreads) void attn_shared_plan_kernel(SharedPa
     __syncthreads();
     if (tid < 64) {
         bool whole = false;
-        for (int i = 0; i <= kWaves && !whole; ++i)
+        for (int i = 0; i <= kLonger && !whole; ++i)
             if (s_fits[i]) {
                 whole = true;
                 per += i;
@@ -225,8 +230,7 @@ __global__ __launch_bounds__(kPlanThreads) void attn_shared_plan_kernel(SharedPa
         }
     }
     __syncthreads();
-    Group* groups = reinterpret_cast<Group*>(p.plan_groups);
-    for (int g = tid; g < G; g += kPlanThreads) {
+    auto planned = [&](int g) {
         Group x;
         x.first = s[g].first;
         x.rows = max(s[g + 1].first - s[g].first, 0) * rep;
@@ -235,7 +239,13 @@ __global__ __launch_bounds__(kPlanThreads) void attn_shared_plan_kernel(SharedPa
         x.unit0 = max(s[g].unit0, 0);
         x.shared = s[g].shared;
         x.pos0 = s[g].pos0;
-        groups[g] = x;
+        return x;
+    };
+    for (int g = tid; g < G; g += kPlanThreads) reinterpret_cast<Group*>(p.plan_groups)[g] = planned(g);
+    // (each sequence its group's, so that nobody has to look up which one that is)
+    for (int n = tid; n < p.N; n += kPlanThreads) {
+        const int g = group_of(n);
+        reinterpret_cast<Group*>(p.plan_sequences)[n] = g >= 0 ? planned(g) : Group{0, 0, 0, 0, 0, 0, 0};
     }
     for (int w = tid; w < s_workgroups; w += kPlanThreads) { // the last group that starts at or before this one's run
         int g = 0, z = G - 1;
@@ -280,15 +290,19 @@ __global__ __launch_bounds__(kPlanThreads) void attn_shared_plan_kernel(SharedPa
 // zeros has a scale of 2^-96) it has its own.
 template <int D, int NB>
 struct __attribute__((aligned(256))) SharedSmem {
-    uint4 q[NB * D / 16][64];                         // queries, operand by operand
     union {
-        uint8_t page[kWaves][2 * kPage * D];          // keys [64][D], then values [4][D][16]
+        struct {
+            uint8_t page[kWaves][2 * kPage * D];      // keys [64][D], then values [4][D][16]
+            uint4 q[NB * D / 16][64];                 // queries, operand by operand
+        };
         struct {
             float o[kWaves][32][D + 4];
             float ml[kWaves][32][2];
+            int nans[kWaves];
         };
     };
 };
+static_assert(sizeof(SharedSmem<128, 2>) <= 80 * 1024, "two workgroups' (and no LDS beside it)");
 
 // A page into LDS by a wave: 16-byte direct loads, a KiB of keys or values each.  A key's
 // row keeps its 16-byte units u at u ^ f(row), so that the 16 rows that a phase of the
@@ -335,413 +349,21 @@ __device__ __forceinline__ long long length_of(const PlanHead& head, const Group
 // all but the last N of this wave's loads have arrived
 template <int N> __device__ __forceinline__ void wait_but() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
 
-template <int D, int PARTS, int NB>
-__global__ __launch_bounds__(64 * kWaves, 2) void attn_shared_kernel(SharedParams p) {
-    constexpr int KL = D / 32;                        // 16-byte reads of a key's row by a lane
-    constexpr int DB = D / 32;                        // 32-channel tiles of the output
-    constexpr int kRows = 32 * NB;                    // of the workgroup: its waves have the same ones
-    extern __shared__ __attribute__((aligned(256))) char smem[];
-    SharedSmem<D, NB>& sm = *reinterpret_cast<SharedSmem<D, NB>*>(smem);
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), rep = p.Hq / p.Hkv;
-
-    // consecutive workgroups go round the 8 XCDs: each of these takes a run of them, the
-    // tiles that share pages one after the other
-    const PlanHead head = plan_head(p);
-    const int each = (head.workgroups + 7) / 8, wg = (blockIdx.x % 8) * each + blockIdx.x / 8;
-    if ((int)(blockIdx.x / 8) >= each || wg >= head.workgroups) return;
-    int group = p.plan_items[wg];
-    Group x = group_at(p, group);
-    // the unit and its page that the run starts with, and the run's length
-    long long left = head.per, length = length_of(head, x);
-    int unit, page0;
-    {
-        const long long rel = wg * head.per - x.pos0;
-        unit = (int)(rel / length);
-        page0 = (int)(rel % length);
-    }
-    for (;;) {
-    int lane = threadIdx.x & 63;
-    asm volatile("" : "+v"(lane));                    // (what follows from it is not kept over the units)
-    const int col = lane & 31, h = lane >> 5;
-    const int tiles = (x.rows + kRows - 1) / kRows, tile = unit % tiles, kh = __builtin_amdgcn_readfirstlane(unit / tiles);
-    const int row0 = kRows * tile, rows = min(kRows, x.rows - row0);
-    const int pg0 = __builtin_amdgcn_readfirstlane(x.pg0 + page0);
-    const int pg1 = __builtin_amdgcn_readfirstlane((int)min((long long)pg0 + left, (long long)x.pg0 + x.pages));
-    const size_t part0 = (size_t)(x.unit0 + unit + wg) * kRows;
-    const int n = max(0, (pg1 - pg0 - wave + kWaves - 1) / kWaves);      // pages of this wave
-
-    // this wave's pages k0 .. k0 + 63, one a lane: place (-1: absent) and scales
-    const int* entries = p.block_table + (size_t)x.first * p.max_pages + pg0 + wave;
-    int e_page;
-    float e_ks, e_vs;
-    auto look_up = [&](int k0) {
-        const int k = k0 + lane;
-        const int e = k < n ? entries[k * kWaves] : -1;
-        e_page = (unsigned)e < (unsigned)p.n_pages ? e : -1;
-        const size_t ph = (size_t)max(e_page, 0) * p.Hkv + kh;
-        e_ks = p.k_scale[ph];
-        e_vs = p.v_scale[ph];
-    };
-    const PageLoader<D, false> loader(lane);
-    const uint32_t place = attn::lds_address(sm.page[wave]);
-    constexpr uint32_t kSide = kPage * D;
-    // (an absent page is read as the first one: its bytes are masked)
-    auto page_at = [&](int k) { return ((size_t)max(__builtin_amdgcn_readlane(e_page, k & 63), 0) * p.Hkv + kh) * kSide; };
-    look_up(0);
-    if (n > 0) {
-        loader.keys((uint64_t)p.k_cache + page_at(0), place);
-        loader.values((uint64_t)p.v_cache + page_at(0), place + kSide);
-    }
-
-    // this lane's rows: their queries (channels 32 s + 16 h .. + 15) and the keys they see
-    int lo[NB], hi[NB], lo_most = 0, hi_least = INT_MAX, lo_least = INT_MAX, hi_most = 0;
-#pragma unroll
-    for (int c = 0; c < NB; ++c) {
-        const int mine = 32 * c + col;
-        const bool live = mine < rows;
-        const int seq = x.first + (row0 + mine) / rep, head = kh * rep + (row0 + mine) % rep;
-        for (int s = wave; s < 2 * KL; s += kWaves) {
-            uint4 u = make_uint4(0, 0, 0, 0);
-            if (live)
-                u = *reinterpret_cast<const uint4*>((const uint16_t*)p.q + ((size_t)seq * p.Hq + head) * D + 32 * (s / 2) + 16 * h + 8 * (s % 2));
-            sm.q[2 * KL * c + s][lane] = u;
-        }
-        lo[c] = hi[c] = 0;
-        if (live) {
-            seen_range(p, seq, lo[c], hi[c]);
-            lo_most = max(lo_most, lo[c]);
-            lo_least = min(lo_least, lo[c]);
-            hi_least = min(hi_least, hi[c]);
-            hi_most = max(hi_most, hi[c]);
-        }
-    }
-    for (int o = 16; o > 0; o >>= 1) {
-        lo_most = max(lo_most, __shfl_xor(lo_most, o, 64));
-        hi_least = min(hi_least, __shfl_xor(hi_least, o, 64));
-        lo_least = min(lo_least, __shfl_xor(lo_least, o, 64));
-        hi_most = max(hi_most, __shfl_xor(hi_most, o, 64));
-    }
-    lo_most = __builtin_amdgcn_readfirstlane(lo_most);
-    hi_least = __builtin_amdgcn_readfirstlane(hi_least);
-
-    float16v o[NB][DB];
-    float m[NB], l[NB], wm[NB];                       // maximum and sum of the scores; maximum of the weights
-#pragma unroll
-    for (int c = 0; c < NB; ++c) {
-        m[c] = -INFINITY; l[c] = 0.f; wm[c] = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < DB; ++i)
-#pragma unroll
-            for (int j = 0; j < 16; ++j) o[c][i][j] = 0.f;
-    }
-    const float to2 = p.scale * 1.4426950408889634f;
-    uint32_t k_at, v_at;                              // this lane's reads: of keys, to flip by 32 s; of values
-    {
-        const int tok = 16 * ((col >> 2) & 1) + 4 * (col >> 3) + (col & 3);
-        k_at = tok * D + 16 * (h ^ key_flip<D, false>(tok));
-        v_at = kPage * D + (h * D + col) * 16;
-    }
-
-    const uint32_t q_at = attn::lds_address(sm.q) + 16 * lane;
-    // (the pages' loads go on)
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-
-    uint32_t nans = 0;                                // some value that not every row sees is NaN
-    for (int k = 0; k < n; ++k) {
-        const int page = __builtin_amdgcn_readlane(e_page, k & 63);
-        const float ks = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(e_ks), k & 63));
-        const float vs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(e_vs), k & 63));
-        const int at0 = (pg0 + wave + k * kWaves) * kPage;
-        const bool absent = page < 0;
-        // the keys are there: what was asked for behind them are values
-        wait_but<PageLoader<D, false>::N>();
-        float16v st[NB][2];
-#pragma unroll
-        for (int c = 0; c < NB; ++c)
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int j = 0; j < 16; ++j) st[c][b][j] = 0.f;
-#pragma unroll
-        for (int s = 0; s < KL; ++s) {
-            uint4v kr[2], qr[NB][2];
-#pragma unroll
-            for (int b = 0; b < 2; ++b) kr[b] = read16(((place + k_at) ^ (32 * s)) + 32 * b * D);
-#pragma unroll
-            for (int c = 0; c < NB; ++c)
-#pragma unroll
-                for (int f = 0; f < 2; ++f) qr[c][f] = read16(q_at + 1024 * (2 * KL * c + 2 * s + f));
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const bf8v k0 = e4m3x8_to_bf16(kr[b].x, kr[b].y), k1 = e4m3x8_to_bf16(kr[b].z, kr[b].w);
-#pragma unroll
-                for (int c = 0; c < NB; ++c) st[c][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k0, __builtin_bit_cast(bf8v, qr[c][0]), st[c][b], 0, 0, 0);
-#pragma unroll
-                for (int c = 0; c < NB; ++c) st[c][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k1, __builtin_bit_cast(bf8v, qr[c][1]), st[c][b], 0, 0, 0);
-            }
-        }
-        // the keys are read: the next page's take their place while these values are worked on
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        if (k + 1 < n) {
-            if (((k + 1) & 63) == 0) look_up(k + 1);
-            loader.keys((uint64_t)p.k_cache + page_at(k + 1), place);
-        }
-        // (the values are older than these, where there are any)
-        auto wait_values = [&] {
-            if (k + 1 < n) wait_but<PageLoader<D, false>::N>();
-            else wait_but<0>();
-        };
-
-        float by = ks * to2;                          // a score is st times this
-        const bool edge = absent || at0 < lo_most || at0 + kPage > hi_least;
-        if (edge || !(by >= 0.f)) {
-            // (negative scales turn the order of the scores; masked ones stay -inf whatever the scale)
-            asm volatile("");
-#pragma unroll
-            for (int c = 0; c < NB; ++c)
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    st[c][b] *= by;
-                    if (edge) {
-                        const uint32_t sees = absent ? 0 : seen_bits(at0 + 16 * h, lo[c], hi[c]);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) st[c][b][i] = sees >> (16 * b + i) & 1 ? st[c][b][i] : -INFINITY;
-                    }
-                }
-            by = 1.f;
-            if (edge) {
-                // some row sees the page in part: values of keys that no row sees count as 0,
-                // and so do NaNs, which the 0 of a row that does not see them would carry
-                // over: the rows that see them get them at the end
-                // (in LDS: a lane writes what it will read)
-                const uint32_t some = absent ? 0 : seen_bits(at0 + 16 * h, lo_least, hi_most);
-                wait_values();
-                for (int i = 0; i < 2 * DB; ++i) {
-                    const int b = i & 1;
-                    const uint32_t at = place + v_at + (2 * b * D + 16 * (i & ~1)) * 16;
-                    uint4v u = read16(at);
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const uint32_t y = u[t] & bytes_of(some, 16 * b + 4 * t);
-                        const uint32_t whole = (nan_bytes(y) >> 7) * 0xffu;
-                        nans |= whole;
-                        u[t] = y & ~whole;
-                    }
-                    *(__attribute__((address_space(3))) uint4v*)(uintptr_t)at = u;
-                }
-                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            }
-        }
-
-        // The maxima are followed when they are more than 2^kLag ahead, each row's by itself
-        // (the roundings of a row do not depend on keys that only its neighbours see): in
-        // most pages some row of 32 has a new one, and o would be scaled anew.
-        const float log_vs = __builtin_amdgcn_logf(vs);   // base 2
-        float top[NB];
-        bool none[NB], ahead_m[NB], ahead_w[NB], any = false;
-#pragma unroll
-        for (int c = 0; c < NB; ++c) {
-            top[c] = st[c][0][0];
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) top[c] = fmaxf(top[c], st[c][b][i]);
-            top[c] = max_across32(top[c]);
-            none[c] = !(top[c] > -INFINITY);          // (the scale of a page that a row does not see does not reach it)
-            top[c] = none[c] ? -INFINITY : top[c] * by;
-            ahead_m[c] = top[c] > m[c] + kLag;
-            ahead_w[c] = !none[c] && top[c] + log_vs > wm[c] + kLag;
-            any = any || ahead_m[c] || ahead_w[c];
-        }
-        if (__any(any)) {
-            asm volatile("");
-#pragma unroll
-            for (int c = 0; c < NB; ++c) {
-                const float fade = ahead_w[c] ? __builtin_amdgcn_exp2f(wm[c] - (top[c] + log_vs)) : 1.f;
-                l[c] *= ahead_m[c] ? __builtin_amdgcn_exp2f(m[c] - top[c]) : 1.f;      // 0 from -inf
-                m[c] = ahead_m[c] ? top[c] : m[c];
-                wm[c] = ahead_w[c] ? top[c] + log_vs : wm[c];
-#pragma unroll
-                for (int i = 0; i < DB; ++i) o[c][i] *= fade;
-            }
-        }
-        float up[NB], share[NB];                      // a weight's exponent over its score's; its part in the sum
-        bool far = false;
-#pragma unroll
-        for (int c = 0; c < NB; ++c) {
-            const float at = m[c] == -INFINITY ? 0.f : m[c], wat = wm[c] == -INFINITY ? 0.f : wm[c];
-            up[c] = none[c] ? 0.f : log_vs - wat + kTop;
-            share[c] = none[c] ? 0.f : __builtin_amdgcn_exp2f(-(up[c] + at));
-            far = far || (!none[c] && !(fabsf(up[c] + at) <= 60.f));
-        }
-        if (__any(far)) {
-            // the sum's own exponentials
-#pragma unroll
-            for (int c = 0; c < NB; ++c) {
-                const float at = m[c] == -INFINITY ? 0.f : m[c];
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        l[c] += __builtin_amdgcn_exp2f(__builtin_fmaf(st[c][b][i], by, -at));
-                        asm volatile("" : "+v"(l[c]));    // (one after the other: no registers for it)
-                    }
-                share[c] = 0.f;
-            }
-        }
-
-        wait_values();
-        // (with two parts a weight, the weights of 32 keys do not fit into the registers: 16 at a
-        // time then, 233 us for 247 of 256 sequences behind 3 prompts; with one part, 111 for 101)
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int f0 = 0; f0 < 2; f0 += 3 - PARTS) {
-                half8 w_hi[NB][3 - PARTS], w_lo[NB];
-#pragma unroll
-                for (int c = 0; c < NB; ++c) {
-                    float sum[2] = {0.f, 0.f};
-#pragma unroll
-                    for (int i = 0; i < 8 * (3 - PARTS); ++i) {
-                        const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(st[c][b][8 * f0 + i], by, up[c]));
-                        sum[i & 1] += w;
-                        const _Float16 a = (_Float16)w;
-                        w_hi[c][i / 8][i % 8] = a;
-                        if (PARTS == 2) w_lo[c][i % 8] = (_Float16)(w - (float)a);
-                    }
-                    l[c] += (sum[0] + sum[1]) * share[c];
-                }
-#pragma unroll
-                for (int i = 0; i < DB; ++i) {
-                    const uint32_t at = place + v_at + (2 * b * D + 32 * i) * 16;
-                    if constexpr (PARTS == 2) {
-                        const uint2v u = read8(at + 8 * f0);
-                        const half8 v = e4m3x8_to_f16(u.x, u.y);
-#pragma unroll
-                        for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w_hi[c][0], o[c][i], 0, 0, 0);
-#pragma unroll
-                        for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w_lo[c], o[c][i], 0, 0, 0);
-                    } else {
-                        const uint4v u = read16(at);
-                        const half8 v0 = e4m3x8_to_f16(u.x, u.y), v1 = e4m3x8_to_f16(u.z, u.w);
-#pragma unroll
-                        for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v0, w_hi[c][0], o[c][i], 0, 0, 0);
-#pragma unroll
-                        for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v1, w_hi[c][2 - PARTS], o[c][i], 0, 0, 0);
-                    }
-                }
-            }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        if (k + 1 < n) loader.values((uint64_t)p.v_cache + page_at(k + 1), place + kSide);
-    }
-
-    // the waves that had the same rows join, in LDS, 32 rows at a time: no load into it is
-    // left, and no read of the ring
-    attn::wait_loads();
-#pragma unroll
-    for (int c = 0; c < NB; ++c) {
-        lds_barrier();
-        l[c] = sum_across32(l[c]);
-        if (h == 0) { sm.ml[wave][col][0] = m[c]; sm.ml[wave][col][1] = l[c]; }
-        const float down = m[c] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(wm[c] - m[c] - kTop);   // to the scores' maximum
-#pragma unroll
-        for (int i = 0; i < DB; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float4v y;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) y[k] = o[c][i][4 * j + k] * down;
-                *reinterpret_cast<float4v*>(&sm.o[wave][col][32 * i + 8 * j + 4 * h]) = y;
-            }
-        lds_barrier();
-        // all their lanes together
-        const size_t part = part0 + 32 * c;
-        join_waves<D>(sm.o, sm.ml, 0, 1, kWaves, min(32, rows - 32 * c), wave * 64 + lane, kWaves * 64, [&](int r, int ch, float4v y, float2 ml) {
-            *reinterpret_cast<float4v*>(&p.part_o[(part + r) * D + ch]) = y;
-            if (ch == 0) *reinterpret_cast<float2*>(&p.part_ml[(part + r) * 2]) = ml;
-        });
-    }
-    if (__syncthreads_or(nans != 0)) {
-    // NaNs among values that not every row sees: into the rows that see them, one by one
-    __threadfence_block();
-    for (int pg = pg0; pg < pg1; ++pg) {
-        const int page = p.block_table[(size_t)x.first * p.max_pages + pg];
-        if ((unsigned)page >= (unsigned)p.n_pages) continue;
-        const uint8_t* values = p.v_cache + ((size_t)page * p.Hkv + kh) * (kPage * D);
-        for (int i = threadIdx.x; i < kPage * D; i += 64 * kWaves) {
-            if ((values[i] & 0x7f) != 0x7f) continue;
-            const int j = pg * kPage + 16 * (i / (16 * D)) + i % 16, ch = i / 16 % D;
-            for (int r = 0; r < rows; ++r) {
-                int a, b;
-                seen_range(p, x.first + (row0 + r) / rep, a, b);
-                if (j >= a && j < b) p.part_o[(part0 + r) * D + ch] = NAN;
-            }
-        }
-    }
-    }
-    // the next unit
-    left -= length - page0;
-    if (left <= 0) return;
-    page0 = 0;
-    if (++unit == tiles * p.Hkv) {
-        unit = 0;
-        do {
-            if (++group >= p.groups) return;
-            x = group_at(p, group);
-        } while (x.pages == 0);
-        length = length_of(head, x);
-    }
-    }
-}
-
-// ---------------------------------------------------------------------------
-// a sequence's own pages, and the join
-// ---------------------------------------------------------------------------
-//
-// Up to 16 of a sequence's query heads on a key head are the columns of 16 x 16
-// products (as attn_decode_kernel has them).  A wave has all of the pages of one, or a run of
-// them where there are few sequences, and loads each page while it works on the one before:
-// a few pages a sequence are too few to be dealt to four waves, whose starts and joins
-// took as long as the pages.  Where a wave
-// has all pages it joins the shared ones' partial results as well and writes the output;
-// else a kernel behind this one does.
-
-// where the partial results of a row's shared pages are: those of a unit's pages, cut at the
-// ends of the workgroups' runs, lie one after the other
-struct Parts {
-    size_t first;
-    int n;
-};
-__device__ __forceinline__ Parts parts_of(const SharedParams& p, const Group& x, int kh, int row) {
-    if (x.pages == 0) return {0, 0};
-    const PlanHead head = plan_head(p);
-    const int unit = kh * ((x.rows + p.width - 1) / p.width) + row / p.width;
-    const long long at = x.pos0 + unit * length_of(head, x), end = at + x.pages - 1;
-    long long w0, w1;
-    if ((end | head.per) >> 32 == 0) {                // (64-bit divisions take some hundred instructions)
-        w0 = (uint32_t)at / (uint32_t)head.per;
-        w1 = (uint32_t)end / (uint32_t)head.per;
-    } else {
-        w0 = at / head.per;
-        w1 = end / head.per;
-    }
-    return {(size_t)(x.unit0 + unit + w0) * p.width + row % p.width, (int)(w1 - w0) + 1};
-}
-
+// A sequence's own pages: up to 16 of its query heads on a key head are the columns of 16 x 16
+// products (as attn_decode_kernel has them).  A wave has a run of the pages of one, and
+// loads each page while it works on the one before: a few pages a sequence are too few
+// to be dealt to four waves, whose starts and joins took as long as the pages.
 template <int D, int PARTS>
-__global__ __launch_bounds__(64) void attn_own_kernel(SharedParams p) {
+__device__ __forceinline__ void own_pages(const SharedParams& p, int w, uint32_t place, int lane) {
     constexpr int KS = D / 64;                        // 64-channel steps of a key row
     constexpr int VT = D / 16;                        // 16-channel tiles of the output
-    __shared__ __attribute__((aligned(256))) uint8_t s_page[2 * kPage * D];          // keys [64][D], then values [4][D][16]
-    const int lane = threadIdx.x;
     const int col = lane & 15, g = lane >> 4;
     const int rep = p.Hq / p.Hkv, sets = (rep + 15) / 16;
-    int w = blockIdx.x;
     const int qg = w % sets; w /= sets;
     const int kh = w % p.Hkv; w /= p.Hkv;
     const int n = w % p.N, run = w / p.N;
     const int q0 = kh * rep + 16 * qg, nq = min(16, rep - 16 * qg);
-    const int gi = p.plan_group_of[n];
+    const Group x = group_at(p.plan_sequences, n);
     int lo, hi;
     seen_range(p, n, lo, hi);
     // queries: column col, channels 64 s + 16 g + 8 half ..
@@ -755,8 +377,6 @@ __global__ __launch_bounds__(64) void attn_own_kernel(SharedParams p) {
                 u = *reinterpret_cast<const uint4*>((const uint16_t*)p.q + ((size_t)n * p.Hq + q0 + col) * D + 64 * s + 16 * g + 8 * hf);
             qf[s][hf] = __builtin_bit_cast(bf8v, u);
         }
-    Group x = {0, 0, 0, 0, 0, 0, 0};
-    if (gi >= 0) x = group_at(p, gi);
     int pg0 = max(lo / kPage, x.shared), pg1 = (int)(((long long)hi + kPage - 1) / kPage);
     run_of(pg0, pg1, run, p.own_splits);
     pg0 = __builtin_amdgcn_readfirstlane(pg0);
@@ -775,7 +395,6 @@ __global__ __launch_bounds__(64) void attn_own_kernel(SharedParams p) {
         e_vs = p.v_scale[ph];
     };
     const PageLoader<D, true> loader(lane);
-    const uint32_t place = attn::lds_address(s_page);
     constexpr uint32_t kSide = kPage * D;
     // (an absent page is read as the first one)
     auto page_at = [&](int k) { return ((size_t)max(__builtin_amdgcn_readlane(e_page, k & 63), 0) * p.Hkv + kh) * kSide; };
@@ -894,104 +513,493 @@ __global__ __launch_bounds__(64) void attn_own_kernel(SharedParams p) {
     for (int j = 0; j < VT; ++j) o[j] *= down;
     if (col >= nq) return;
     const size_t head = (size_t)n * p.Hq + q0 + col, heads = (size_t)p.N * p.Hq;
-    if (p.own_splits > 1) {
-        // (nothing in the run: the join does not read the output)
-        if (count > 0)
+    // (nothing in the run: the join does not read the output)
+    if (count > 0)
 #pragma unroll
-            for (int j = 0; j < VT; ++j) *reinterpret_cast<float4v*>(&p.own_o[(run * heads + head) * D + 16 * j + 4 * g]) = o[j];
-        if (g == 0) *reinterpret_cast<float2*>(&p.own_ml[(run * heads + head) * 2]) = make_float2(m, l);
+        for (int j = 0; j < VT; ++j) *reinterpret_cast<float4v*>(&p.own_o[(run * heads + head) * D + 16 * j + 4 * g]) = o[j];
+    if (g == 0) *reinterpret_cast<float2*>(&p.own_ml[(run * heads + head) * 2]) = make_float2(m, l);
+}
+
+template <int D, int PARTS, int NB>
+__global__ __launch_bounds__(64 * kWaves, 2) void attn_shared_kernel(SharedParams p) {
+    constexpr int KL = D / 32;                        // 16-byte reads of a key's row by a lane
+    constexpr int DB = D / 32;                        // 32-channel tiles of the output
+    constexpr int kRows = 32 * NB;                    // of the workgroup: its waves have the same ones
+    extern __shared__ __attribute__((aligned(256))) char smem[];
+    SharedSmem<D, NB>& sm = *reinterpret_cast<SharedSmem<D, NB>*>(smem);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), rep = p.Hq / p.Hkv;
+
+    // a workgroup for shared pages for each of 256 compute units and one for own ones by turns,
+    // as long as there are both (by turns of 8, half the shader engines got all of the
+    // first kind: they are taken one after the other)
+    constexpr int kTurn = 256 / 8;
+    int number = blockIdx.x / 8;
+    const int some = p.workgroups / 8, turns = min(some, (int)(gridDim.x / 8) - some) / kTurn;
+    bool own = number / kTurn & 1;
+    if (number < 2 * turns * kTurn) {
+        number = number / (2 * kTurn) * kTurn + number % kTurn;
+    } else {
+        number -= turns * kTurn;
+        own = number >= some;
+        if (own) number -= some - turns * kTurn;
+    }
+    if (own) {
+        const long long w = (long long)(8 * number + blockIdx.x % 8) * kWaves + wave;
+        if (w < p.own_runs) own_pages<D, PARTS>(p, (int)w, attn::lds_address(sm.page[wave]), threadIdx.x & 63);
         return;
     }
-    const int row = (n - x.first) * rep + 16 * qg + col;
-    float top = m;
-    const Parts parts = parts_of(p, x, kh, row);
-    for (int s = 0; s < parts.n; ++s) top = fmaxf(top, p.part_ml[2 * (parts.first + s * (size_t)p.width)]);
-    const float at = top == -INFINITY ? 0.f : top;
+    // consecutive workgroups go round the 8 XCDs: each of these takes a run of them, the
+    // tiles that share pages one after the other
+    const PlanHead head = plan_head(p);
+    const int each = (head.workgroups + 7) / 8, wg = (blockIdx.x % 8) * each + number;
+    if (number >= each || wg >= head.workgroups) return;
+    int group = p.plan_items[wg];
+    Group x = group_at(p.plan_groups, group);
+    // the unit and its page that the run starts with, and the run's length
+    long long left = head.per, length = length_of(head, x);
+    int unit, page0;
     {
-        const float f = __builtin_amdgcn_exp2f(m - at);
-        l *= f;
-#pragma unroll
-        for (int j = 0; j < VT; ++j) o[j] *= f;
+        const long long rel = wg * head.per - x.pos0;
+        unit = (int)(rel / length);
+        page0 = (int)(rel % length);
     }
-    for (int s = 0; s < parts.n; ++s) {
-        const size_t from = parts.first + s * (size_t)p.width;
-        const float2 ml = *reinterpret_cast<const float2*>(&p.part_ml[2 * from]);
-        const float f = __builtin_amdgcn_exp2f(ml.x - at);
-        l += ml.y * f;
-#pragma unroll
-        for (int j = 0; j < VT; ++j) o[j] += *reinterpret_cast<const float4v*>(&p.part_o[from * D + 16 * j + 4 * g]) * f;
+    for (;;) {
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));                    // (what follows from it is not kept over the units)
+    const int col = lane & 31, h = lane >> 5;
+    const int tiles = (x.rows + kRows - 1) / kRows, tile = unit % tiles, kh = __builtin_amdgcn_readfirstlane(unit / tiles);
+    const int row0 = kRows * tile, rows = min(kRows, x.rows - row0);
+    const int pg0 = __builtin_amdgcn_readfirstlane(x.pg0 + page0);
+    const int pg1 = __builtin_amdgcn_readfirstlane((int)min((long long)pg0 + left, (long long)x.pg0 + x.pages));
+    const size_t part0 = (size_t)(x.unit0 + unit + wg) * kRows;
+    const int n = max(0, (pg1 - pg0 - wave + kWaves - 1) / kWaves);      // pages of this wave
+
+    // this wave's pages k0 .. k0 + 63, one a lane: place (-1: absent) and scales
+    const int* entries = p.block_table + (size_t)x.first * p.max_pages + pg0 + wave;
+    int e_page;
+    float e_ks, e_vs;
+    auto look_up = [&](int k0) {
+        const int k = k0 + lane;
+        const int e = k < n ? entries[k * kWaves] : -1;
+        e_page = (unsigned)e < (unsigned)p.n_pages ? e : -1;
+        const size_t ph = (size_t)max(e_page, 0) * p.Hkv + kh;
+        e_ks = p.k_scale[ph];
+        e_vs = p.v_scale[ph];
+    };
+    const uint32_t place = attn::lds_address(sm.page[wave]);
+    constexpr uint32_t kSide = kPage * D;
+    // (an absent page is read as the first one: its bytes are masked)
+    auto page_at = [&](int k) { return ((size_t)max(__builtin_amdgcn_readlane(e_page, k & 63), 0) * p.Hkv + kh) * kSide; };
+    look_up(0);
+    if (n > 0) {
+        const PageLoader<D, false> loader(lane);
+        loader.keys((uint64_t)p.k_cache + page_at(0), place);
+        loader.values((uint64_t)p.v_cache + page_at(0), place + kSide);
     }
-    const float inv = 1.f / l;
+
+    // this lane's rows: their queries (channels 32 s + 16 h .. + 15) and the keys they see
+    int lo_most = 0, hi_least = INT_MAX, lo_least = INT_MAX, hi_most = 0;
 #pragma unroll
-    for (int j = 0; j < VT; ++j) {
-        float4v y;
+    for (int c = 0; c < NB; ++c) {
+        const int mine = 32 * c + col;
+        const bool live = mine < rows;
+        const int seq = x.first + (row0 + mine) / rep, head = kh * rep + (row0 + mine) % rep;
+        for (int s = wave; s < 2 * KL; s += kWaves) {
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (live)
+                u = *reinterpret_cast<const uint4*>((const uint16_t*)p.q + ((size_t)seq * p.Hq + head) * D + 32 * (s / 2) + 16 * h + 8 * (s % 2));
+            sm.q[2 * KL * c + s][lane] = u;
+        }
+        if (live) {
+            int lo, hi;
+            seen_range(p, seq, lo, hi);
+            lo_most = max(lo_most, lo);
+            lo_least = min(lo_least, lo);
+            hi_least = min(hi_least, hi);
+            hi_most = max(hi_most, hi);
+        }
+    }
+    for (int o = 16; o > 0; o >>= 1) {
+        lo_most = max(lo_most, __shfl_xor(lo_most, o, 64));
+        hi_least = min(hi_least, __shfl_xor(hi_least, o, 64));
+        lo_least = min(lo_least, __shfl_xor(lo_least, o, 64));
+        hi_most = max(hi_most, __shfl_xor(hi_most, o, 64));
+    }
+    lo_most = __builtin_amdgcn_readfirstlane(lo_most);
+    hi_least = __builtin_amdgcn_readfirstlane(hi_least);
+    lo_least = __builtin_amdgcn_readfirstlane(lo_least);
+    hi_most = __builtin_amdgcn_readfirstlane(hi_most);
+
+    float16v o[NB][DB];
+    float m[NB], l[NB], wm[NB];                       // maximum and sum of the scores; maximum of the weights
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = l == 0.f && !(o[j][i] != o[j][i]) ? 0.f : o[j][i] * inv;   // l = 0: nothing seen
-        if (p.flags & GDR_OUT_BF16)
-            *reinterpret_cast<uint2*>((uint16_t*)p.o + head * D + 16 * j + 4 * g) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
-        else
-            *reinterpret_cast<float4v*>((float*)p.o + head * D + 16 * j + 4 * g) = y;
+    for (int c = 0; c < NB; ++c) {
+        m[c] = -INFINITY; l[c] = 0.f; wm[c] = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < DB; ++i)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[c][i][j] = 0.f;
+    }
+    const float to2 = p.scale * 1.4426950408889634f;
+    // (the pages' loads go on)
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+
+    uint32_t nans = 0;                                // some value that not every row sees is NaN
+    for (int k = 0; k < n; ++k) {
+        const int page = __builtin_amdgcn_readlane(e_page, k & 63);
+        const float ks = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(e_ks), k & 63));
+        const float vs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(e_vs), k & 63));
+        const int at0 = (pg0 + wave + k * kWaves) * kPage;
+        const bool absent = page < 0;
+        // A lane's places are made anew for each page: kept over the loop some of them would be
+        // in scratch memory, and a wait for what is read from there is one for the page's
+        // loads as well.
+        int mine = lane;
+        asm volatile("" : "+v"(mine));
+        const PageLoader<D, false> loader(mine);
+        const int tok = 16 * ((mine >> 2) & 1) + 4 * ((mine & 31) >> 3) + (mine & 3);
+        const uint32_t k_at = place + tok * D + 16 * ((mine >> 5) ^ key_flip<D, false>(tok));   // its reads of keys, to flip by 32 s
+        const uint32_t v_at = place + kSide + ((mine >> 5) * D + (mine & 31)) * 16, q_at = attn::lds_address(sm.q) + 16 * mine;
+        // the keys are there: what was asked for behind them are values
+        wait_but<PageLoader<D, false>::N>();
+        float16v st[NB][2];
+#pragma unroll
+        for (int c = 0; c < NB; ++c)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) st[c][b][j] = 0.f;
+#pragma unroll
+        for (int s = 0; s < KL; ++s) {
+            uint4v kr[2], qr[NB][2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) kr[b] = read16((k_at ^ (32 * s)) + 32 * b * D);
+#pragma unroll
+            for (int c = 0; c < NB; ++c)
+#pragma unroll
+                for (int f = 0; f < 2; ++f) qr[c][f] = read16(q_at + 1024 * (2 * KL * c + 2 * s + f));
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const bf8v k0 = e4m3x8_to_bf16(kr[b].x, kr[b].y), k1 = e4m3x8_to_bf16(kr[b].z, kr[b].w);
+#pragma unroll
+                for (int c = 0; c < NB; ++c) st[c][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k0, __builtin_bit_cast(bf8v, qr[c][0]), st[c][b], 0, 0, 0);
+#pragma unroll
+                for (int c = 0; c < NB; ++c) st[c][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k1, __builtin_bit_cast(bf8v, qr[c][1]), st[c][b], 0, 0, 0);
+            }
+        }
+        // the keys are read: the next page's take their place while these values are worked on
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (k + 1 < n) {
+            if (((k + 1) & 63) == 0) look_up(k + 1);
+            loader.keys((uint64_t)p.k_cache + page_at(k + 1), place);
+        }
+        // (the values are older than these, where there are any)
+        auto wait_values = [&] {
+            if (k + 1 < n) wait_but<PageLoader<D, false>::N>();
+            else wait_but<0>();
+        };
+
+        float by = ks * to2;                          // a score is st times this
+        const bool edge = absent || at0 < lo_most || at0 + kPage > hi_least;
+        if (edge || !(by >= 0.f)) {
+            // (negative scales turn the order of the scores; masked ones stay -inf whatever the scale)
+            asm volatile("");
+#pragma unroll
+            for (int c = 0; c < NB; ++c) {
+                uint32_t sees = 0;                    // (looked up again: few pages are read in part)
+                if (edge && !absent && 32 * c + col < rows) {
+                    int lo, hi;
+                    seen_range(p, x.first + (row0 + 32 * c + col) / rep, lo, hi);
+                    sees = seen_bits(at0 + 16 * h, lo, hi);
+                }
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    st[c][b] *= by;
+                    if (edge) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) st[c][b][i] = sees >> (16 * b + i) & 1 ? st[c][b][i] : -INFINITY;
+                    }
+                }
+            }
+            by = 1.f;
+            if (edge) {
+                // some row sees the page in part: values of keys that no row sees count as 0,
+                // and so do NaNs, which the 0 of a row that does not see them would carry
+                // over: the rows that see them get them at the end
+                // (in LDS: a lane writes what it will read)
+                const uint32_t some = absent ? 0 : seen_bits(at0 + 16 * h, lo_least, hi_most);
+                wait_values();
+                for (int i = 0; i < 2 * DB; ++i) {
+                    const int b = i & 1;
+                    const uint32_t at = v_at + (2 * b * D + 16 * (i & ~1)) * 16;
+                    uint4v u = read16(at);
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const uint32_t y = u[t] & bytes_of(some, 16 * b + 4 * t);
+                        const uint32_t whole = (nan_bytes(y) >> 7) * 0xffu;
+                        nans |= whole;
+                        u[t] = y & ~whole;
+                    }
+                    *(__attribute__((address_space(3))) uint4v*)(uintptr_t)at = u;
+                }
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            }
+        }
+
+        // The maxima are followed when they are more than 2^kLag ahead, each row's by itself
+        // (the roundings of a row do not depend on keys that only its neighbours see): in
+        // most pages some row of 32 has a new one, and o would be scaled anew.
+        const float log_vs = __builtin_amdgcn_logf(vs);   // base 2
+        float top[NB];
+        bool none[NB], ahead_m[NB], ahead_w[NB], any = false;
+#pragma unroll
+        for (int c = 0; c < NB; ++c) {
+            top[c] = st[c][0][0];
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) top[c] = fmaxf(top[c], st[c][b][i]);
+            top[c] = max_across32(top[c]);
+            none[c] = !(top[c] > -INFINITY);          // (the scale of a page that a row does not see does not reach it)
+            top[c] = none[c] ? -INFINITY : top[c] * by;
+            ahead_m[c] = top[c] > m[c] + kLag;
+            ahead_w[c] = !none[c] && top[c] + log_vs > wm[c] + kLag;
+            any = any || ahead_m[c] || ahead_w[c];
+        }
+        if (__any(any)) {
+            asm volatile("");
+#pragma unroll
+            for (int c = 0; c < NB; ++c) {
+                const float fade = ahead_w[c] ? __builtin_amdgcn_exp2f(wm[c] - (top[c] + log_vs)) : 1.f;
+                l[c] *= ahead_m[c] ? __builtin_amdgcn_exp2f(m[c] - top[c]) : 1.f;      // 0 from -inf
+                m[c] = ahead_m[c] ? top[c] : m[c];
+                wm[c] = ahead_w[c] ? top[c] + log_vs : wm[c];
+#pragma unroll
+                for (int i = 0; i < DB; ++i) o[c][i] *= fade;
+            }
+        }
+        float up[NB], share[NB];                      // a weight's exponent over its score's; its part in the sum
+        bool far = false;
+#pragma unroll
+        for (int c = 0; c < NB; ++c) {
+            const float at = m[c] == -INFINITY ? 0.f : m[c], wat = wm[c] == -INFINITY ? 0.f : wm[c];
+            up[c] = none[c] ? 0.f : log_vs - wat + kTop;
+            share[c] = none[c] ? 0.f : __builtin_amdgcn_exp2f(-(up[c] + at));
+            far = far || (!none[c] && !(fabsf(up[c] + at) <= 60.f));
+        }
+        if (__any(far)) {
+            // the sum's own exponentials
+#pragma unroll
+            for (int c = 0; c < NB; ++c) {
+                const float at = m[c] == -INFINITY ? 0.f : m[c];
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        l[c] += __builtin_amdgcn_exp2f(__builtin_fmaf(st[c][b][i], by, -at));
+                        asm volatile("" : "+v"(l[c]));    // (one after the other: no registers for it)
+                    }
+                share[c] = 0.f;
+            }
+        }
+
+        wait_values();
+        // (with two parts a weight, the weights of 32 keys do not fit into the registers: 16 at a
+        // time then, 233 us for 247 of 256 sequences behind 3 prompts; with one part, 111 for 101)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int f0 = 0; f0 < 2; f0 += 3 - PARTS) {
+                half8 w_hi[NB][3 - PARTS], w_lo[NB];
+#pragma unroll
+                for (int c = 0; c < NB; ++c) {
+                    float sum[2] = {0.f, 0.f};
+#pragma unroll
+                    for (int i = 0; i < 8 * (3 - PARTS); ++i) {
+                        const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(st[c][b][8 * f0 + i], by, up[c]));
+                        sum[i & 1] += w;
+                        const _Float16 a = (_Float16)w;
+                        w_hi[c][i / 8][i % 8] = a;
+                        if (PARTS == 2) w_lo[c][i % 8] = (_Float16)(w - (float)a);
+                    }
+                    l[c] += (sum[0] + sum[1]) * share[c];
+                }
+#pragma unroll
+                for (int i = 0; i < DB; ++i) {
+                    const uint32_t at = v_at + (2 * b * D + 32 * i) * 16;
+                    if constexpr (PARTS == 2) {
+                        const uint2v u = read8(at + 8 * f0);
+                        const half8 v = e4m3x8_to_f16(u.x, u.y);
+#pragma unroll
+                        for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w_hi[c][0], o[c][i], 0, 0, 0);
+#pragma unroll
+                        for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w_lo[c], o[c][i], 0, 0, 0);
+                    } else {
+                        const uint4v u = read16(at);
+                        const half8 v0 = e4m3x8_to_f16(u.x, u.y), v1 = e4m3x8_to_f16(u.z, u.w);
+#pragma unroll
+                        for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v0, w_hi[c][0], o[c][i], 0, 0, 0);
+#pragma unroll
+                        for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v1, w_hi[c][2 - PARTS], o[c][i], 0, 0, 0);
+                    }
+                }
+            }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (k + 1 < n) loader.values((uint64_t)p.v_cache + page_at(k + 1), place + kSide);
+    }
+
+    // the waves that had the same rows join, in LDS, 32 rows at a time: no load into it is
+    // left, and no read of the ring
+    attn::wait_loads();
+#pragma unroll
+    for (int c = 0; c < NB; ++c) {
+        lds_barrier();
+        l[c] = sum_across32(l[c]);
+        if (h == 0) { sm.ml[wave][col][0] = m[c]; sm.ml[wave][col][1] = l[c]; }
+        if (c == 0) sm.nans[wave] = __any(nans != 0);
+        const float down = m[c] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(wm[c] - m[c] - kTop);   // to the scores' maximum
+#pragma unroll
+        for (int i = 0; i < DB; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float4v y;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[k] = o[c][i][4 * j + k] * down;
+                *reinterpret_cast<float4v*>(&sm.o[wave][col][32 * i + 8 * j + 4 * h]) = y;
+            }
+        lds_barrier();
+        // all their lanes together
+        const size_t part = part0 + 32 * c;
+        join_waves<D>(sm.o, sm.ml, 0, 1, kWaves, min(32, rows - 32 * c), wave * 64 + lane, kWaves * 64, [&](int r, int ch, float4v y, float2 ml) {
+            *reinterpret_cast<float4v*>(&p.part_o[(part + r) * D + ch]) = y;
+            if (ch == 0) *reinterpret_cast<float2*>(&p.part_ml[(part + r) * 2]) = ml;
+        });
+    }
+    int any_nans = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) any_nans |= sm.nans[w];
+    __syncthreads();                                  // (LDS is free again, what was joined is written)
+    if (any_nans) {
+    // NaNs among values that not every row sees: into the rows that see them, one by one
+    __threadfence_block();
+    for (int pg = pg0; pg < pg1; ++pg) {
+        const int page = p.block_table[(size_t)x.first * p.max_pages + pg];
+        if ((unsigned)page >= (unsigned)p.n_pages) continue;
+        const uint8_t* values = p.v_cache + ((size_t)page * p.Hkv + kh) * (kPage * D);
+        for (int i = threadIdx.x; i < kPage * D; i += 64 * kWaves) {
+            if ((values[i] & 0x7f) != 0x7f) continue;
+            const int j = pg * kPage + 16 * (i / (16 * D)) + i % 16, ch = i / 16 % D;
+            for (int r = 0; r < rows; ++r) {
+                int a, b;
+                seen_range(p, x.first + (row0 + r) / rep, a, b);
+                if (j >= a && j < b) p.part_o[(part0 + r) * D + ch] = NAN;
+            }
+        }
+    }
+    }
+    // the next unit
+    left -= length - page0;
+    if (left <= 0) return;
+    page0 = 0;
+    if (++unit == tiles * p.Hkv) {
+        unit = 0;
+        do {
+            if (++group >= p.groups) return;
+            x = group_at(p.plan_groups, group);
+        } while (x.pages == 0);
+        length = length_of(head, x);
+    }
     }
 }
 
-// Joins a head's partial results: one workgroup per head; its lanes read the maxima
-// and sums side by side, then 1024 / D groups of them the outputs.
-template <int D>
-__global__ __launch_bounds__(256) void attn_shared_join(SharedParams p) {
-    constexpr int GROUPS = 1024 / D;                  // D / 4 lanes each, four channels a lane
-    __shared__ float s_x[GROUPS][D], s_ml[8], s_sum;
+// ---------------------------------------------------------------------------
+// a sequence's own pages, and the join
+// ---------------------------------------------------------------------------
+//
+// Up to 16 of a sequence's query heads on a key head are the columns of 16 x 16
+// products (as attn_decode_kernel has them).  A wave has all of the pages of one, or a run of
+// them where there are few sequences, and loads each page while it works on the one before:
+// a few pages a sequence are too few to be dealt to four waves, whose starts and joins
+// took as long as the pages.  Where a wave
+// has all pages it joins the shared ones' partial results as well and writes the output;
+// else a kernel behind this one does.
+
+// where the partial results of a row's shared pages are: those of a unit's pages, cut at the
+// ends of the workgroups' runs, lie one after the other
+struct Parts {
+    size_t first;
+    int n;
+};
+__device__ __forceinline__ Parts parts_of(const SharedParams& p, const Group& x, int kh, int row) {
+    if (x.pages == 0) return {0, 0};
+    const PlanHead head = plan_head(p);
+    const int unit = kh * ((x.rows + p.width - 1) / p.width) + row / p.width;
+    const long long at = x.pos0 + unit * length_of(head, x), end = at + x.pages - 1;
+    long long w0, w1;
+    if ((end | head.per) >> 32 == 0) {                // (64-bit divisions take some hundred instructions)
+        w0 = (uint32_t)at / (uint32_t)head.per;
+        w1 = (uint32_t)end / (uint32_t)head.per;
+    } else {
+        w0 = at / head.per;
+        w1 = end / head.per;
+    }
+    return {(size_t)(x.unit0 + unit + w0) * p.width + row % p.width, (int)(w1 - w0) + 1};
+}
+
+// Joins a head's partial results: THREADS for a head, in 4 THREADS / D groups of lanes, four
+// channels a lane; each takes every so many of the results with a running maximum, four at a
+// time, maxima and outputs asked for together.
+template <int D, int THREADS>
+__global__ __launch_bounds__(THREADS) void attn_shared_join(SharedParams p) {
+    constexpr int GROUPS = 4 * THREADS / D, kAtOnce = 4;
+    __shared__ float s_x[GROUPS][D], s_ml[GROUPS][2];
     const size_t head = blockIdx.x, heads = (size_t)p.N * p.Hq;
     const int tid = threadIdx.x, gi = tid / (D / 4), ch = 4 * (tid % (D / 4));
     const int n = (int)(head / p.Hq), hq = (int)(head % p.Hq), rep = p.Hq / p.Hkv;
-    const int in = p.plan_group_of[n];
-    Group x = {0, 0, 0, 0, 0, 0, 0};
-    if (in >= 0) x = group_at(p, in);
+    const Group x = group_at(p.plan_sequences, n);
     const Parts parts = parts_of(p, x, hq / rep, (n - x.first) * rep + hq % rep);
     const int slots = parts.n + p.own_splits;
-    auto ml_at = [&](int s) {
-        return s < parts.n ? &p.part_ml[2 * (parts.first + s * (size_t)p.width)] : &p.own_ml[((s - parts.n) * heads + head) * 2];
-    };
-    auto o_at = [&](int s) {
-        return s < parts.n ? &p.part_o[(parts.first + s * (size_t)p.width) * D] : &p.own_o[((s - parts.n) * heads + head) * D];
-    };
     float top = -INFINITY, sum = 0.f;
-    for (int s = tid; s < slots; s += 256) {
-        const float2 ml = *reinterpret_cast<const float2*>(ml_at(s));
-        const float both = fmaxf(top, ml.x);
-        if (both != -INFINITY) sum = sum * __builtin_amdgcn_exp2f(top - both) + ml.y * __builtin_amdgcn_exp2f(ml.x - both);
-        else sum += ml.y;                             // 0, or NaN where every score is
-        top = both;
-    }
-    for (int o = 32; o > 0; o >>= 1) {
-        const float t2 = __shfl_xor(top, o, 64), s2 = __shfl_xor(sum, o, 64), both = fmaxf(top, t2);
-        sum = both == -INFINITY ? sum + s2
-                                : sum * __builtin_amdgcn_exp2f(top - both) + s2 * __builtin_amdgcn_exp2f(t2 - both);
-        top = both;
-    }
-    if ((tid & 63) == 0) { s_ml[2 * (tid >> 6)] = top; s_ml[2 * (tid >> 6) + 1] = sum; }
-    __syncthreads();
-    top = fmaxf(fmaxf(s_ml[0], s_ml[2]), fmaxf(s_ml[4], s_ml[6]));
-    const float at = top == -INFINITY ? 0.f : top;
-    if (tid == 0) {
-        float all = 0.f;
-        for (int w = 0; w < 4; ++w)
-            all += top == -INFINITY ? s_ml[2 * w + 1] : s_ml[2 * w + 1] * __builtin_amdgcn_exp2f(s_ml[2 * w] - at);
-        s_sum = all;
-    }
     float4v y = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int s = gi; s < slots; s += GROUPS) {
-        const float2 ml = *reinterpret_cast<const float2*>(ml_at(s));
-        if (s >= parts.n && ml.x == -INFINITY && ml.y == 0.f) continue;      // an empty run: not written
-        y += *reinterpret_cast<const float4v*>(o_at(s) + ch) * __builtin_amdgcn_exp2f(ml.x - at);
+    for (int s0 = gi; s0 < slots; s0 += kAtOnce * GROUPS) {
+        float2 ml[kAtOnce];
+        float4v part[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int s = min(s0 + i * GROUPS, slots - 1);
+            const bool shared = s < parts.n;
+            const size_t at = shared ? parts.first + s * (size_t)p.width : (s - parts.n) * heads + head;
+            ml[i] = *reinterpret_cast<const float2*>((shared ? p.part_ml : p.own_ml) + 2 * at);
+            part[i] = *reinterpret_cast<const float4v*>((shared ? p.part_o : p.own_o) + at * D + ch);
+        }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int s = s0 + i * GROUPS;
+            // (nothing seen there: an empty run's output is not written)
+            if (s >= slots || (ml[i].x == -INFINITY && ml[i].y == 0.f && s >= parts.n)) continue;
+            const float both = fmaxf(top, ml[i].x), at = both == -INFINITY ? 0.f : both;
+            const float f = __builtin_amdgcn_exp2f(top - at), g = __builtin_amdgcn_exp2f(ml[i].x - at);
+            sum = sum * f + ml[i].y * g;
+            y = y * f + part[i] * g;
+            top = both;
+        }
     }
     *reinterpret_cast<float4v*>(&s_x[gi][ch]) = y;
+    if (ch == 0) { s_ml[gi][0] = top; s_ml[gi][1] = sum; }
     __syncthreads();
-    if (tid < D) {
-        float z = 0.f;
+    top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < GROUPS; ++i) z += s_x[i][tid];
-        store_out(p, head * D + tid, s_sum == 0.f && !(z != z) ? 0.f : z / s_sum);      // (0: nothing seen)
+    for (int i = 0; i < GROUPS; ++i) top = fmaxf(top, s_ml[i][0]);
+    const float at = top == -INFINITY ? 0.f : top;
+    for (int c = tid; c < D; c += THREADS) {
+        float z = 0.f, all = 0.f;
+#pragma unroll
+        for (int i = 0; i < GROUPS; ++i) {
+            const float f = __builtin_amdgcn_exp2f(s_ml[i][0] - at);
+            z += s_x[i][c] * f;
+            all += s_ml[i][1] * f;
+        }
+        store_out(p, head * D + c, all == 0.f && !(z != z) ? 0.f : z / all);            // (0: nothing seen)
     }
 }
 
@@ -1009,12 +1017,16 @@ SharedPlan attn_shared_plan(int N, int groups, int Hq, int Hkv, int d, int max_p
     const long long some = groups < N ? groups : N;
     const long long tiles = (rows + some * (x.width - 1)) / x.width;
     x.units = tiles * Hkv;
-    x.workgroups = d == 64 && x.width == 32 ? 512 : 256;      // as many as LDS and registers hold
+// Two workgroups a compute unit where 64 rows share a page's bytes and the products count
+    // (1,024 rows on 512 pages: 170 us, with one 187); one where the bytes do and every cut
+    // costs a start and an end (16 groups of 4 on 63 pages 41.6, with two 44.6; 8 on 512
+    // pages 28.2 and 31.3).
+    x.workgroups = x.width == 64 ? 512 : 256;
     x.own_items = (long long)N * Hkv * ((rep + 15) / 16);
     int pages = max_pages;
     if (window > 0 && window / kPage + 2 < pages) pages = window / kPage + 2;
-    // about two waves a SIMD
-    long long s = (2048 + x.own_items / 2) / x.own_items;
+    // about a wave a SIMD (twice and half as many: the same within 3%)
+    long long s = (1024 + x.own_items / 2) / x.own_items;
     const long long most = (pages + 1) / 2;
     if (s > most) s = most;
     x.own_splits = s < 1 ? 1 : (int)s;
@@ -1024,44 +1036,47 @@ SharedPlan attn_shared_plan(int N, int groups, int Hq, int Hkv, int d, int max_p
     auto take = [&](size_t bytes) { const size_t y = at; at += up(bytes); return y; };
     x.at_head = take(16);
     x.at_groups = take(sizeof(Group) * (size_t)groups);
-    x.at_group_of = take(4 * (size_t)N);
+    x.at_sequences = take(sizeof(Group) * (size_t)N);
     x.at_items = take(4 * (size_t)x.workgroups);
     x.at_part_o = take(4 * (size_t)(x.units + x.workgroups) * x.width * d);
     x.at_part_ml = take(8 * (size_t)(x.units + x.workgroups) * x.width);
-    const size_t own = x.own_splits > 1 ? (size_t)x.own_splits * N * Hq : 0;
+    const size_t own = (size_t)x.own_splits * N * Hq;
     x.at_own_o = take(4 * own * d);
     x.at_own_ml = take(8 * own);
     x.bytes = at;
     return x;
 }
 
+// the most that is numbered in 32 bits: waves for own pages, units and their parts, heads
 long long attn_shared_workgroups(const SharedPlan& x, long long heads) {
-    // (units are numbered in 32 bits as well)
-    const long long own = x.own_items * x.own_splits, units = x.units + x.workgroups, most = units > own ? units : own;
-    return x.own_splits > 1 && heads > most ? heads : most;
+    long long most = x.own_items * x.own_splits + 8LL * kWaves * (x.workgroups + 1);
+    if (x.units + x.workgroups > most) most = x.units + x.workgroups;
+    return heads > most ? heads : most;
 }
 
+// One wave a head in the join where there are many, else four: 8,160 heads 9.1 us, with four 19.9;
+// 2,048: 4.6 and 6.2; 1,024 of some 30 parts: 7.6 and 6.4; 256 of some 70: 9.6 and 5.1.
+constexpr long long kHeadsOfWaves = 2048;
 template <int D, int PARTS, int NB> static hipError_t launch_shared(const SharedParams& p, hipStream_t st) {
     static std::atomic<unsigned long long> done{0};
     const int lds = (int)sizeof(SharedSmem<D, NB>);
     const hipError_t e = ensure_dyn_lds(reinterpret_cast<const void*>(&attn_shared_kernel<D, PARTS, NB>), lds, done);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((attn_shared_kernel<D, PARTS, NB>), dim3((unsigned)p.workgroups), dim3(64 * kWaves), lds, st, p);
+    const long long own = (p.own_runs + 8 * kWaves - 1) / (8 * kWaves);
+    hipLaunchKernelGGL((attn_shared_kernel<D, PARTS, NB>), dim3((unsigned)(p.workgroups + 8 * own)), dim3(64 * kWaves), lds, st, p);
     return hipGetLastError();
 }
 
-template <int D, int PARTS> static hipError_t launch_d(const SharedParams& p, const SharedPlan& x, hipStream_t st) {
-    hipError_t e = p.width == 64 ? launch_shared<D, PARTS, 2>(p, st) : launch_shared<D, PARTS, 1>(p, st);
+template <int D, int PARTS> static hipError_t launch_d(const SharedParams& p, hipStream_t st) {
+    const hipError_t e = p.width == 64 ? launch_shared<D, PARTS, 2>(p, st) : launch_shared<D, PARTS, 1>(p, st);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((attn_own_kernel<D, PARTS>), dim3((unsigned)(x.own_items * p.own_splits)), dim3(64), 0,
-                       st, p);
-    e = hipGetLastError();
-    if (e != hipSuccess || p.own_splits == 1) return e;
-    hipLaunchKernelGGL(attn_shared_join<D>, dim3((unsigned)((long long)p.N * p.Hq)), dim3(256), 0, st, p);
+    const long long heads = (long long)p.N * p.Hq;
+    if (heads >= kHeadsOfWaves) hipLaunchKernelGGL((attn_shared_join<D, 64>), dim3((unsigned)heads), dim3(64), 0, st, p);
+    else hipLaunchKernelGGL((attn_shared_join<D, 256>), dim3((unsigned)heads), dim3(256), 0, st, p);
     return hipGetLastError();
 }
 
-hipError_t launch_attn_shared(const SharedParams& p, const SharedPlan& x, hipStream_t st) {
+hipError_t launch_attn_shared(const SharedParams& p, hipStream_t st) {
     static std::atomic<unsigned long long> done{0};
     hipError_t e = ensure_dyn_lds(reinterpret_cast<const void*>(&attn_shared_plan_kernel), (kMostGroups + 1) * (int)sizeof(PlanGroup), done);
     if (e != hipSuccess) return e;
@@ -1069,8 +1084,8 @@ hipError_t launch_attn_shared(const SharedParams& p, const SharedPlan& x, hipStr
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     const bool one = (p.flags & GDR_OUT_BF16) != 0;
-    if (p.d == 64) return one ? launch_d<64, 1>(p, x, st) : launch_d<64, 2>(p, x, st);
-    return one ? launch_d<128, 1>(p, x, st) : launch_d<128, 2>(p, x, st);
+    if (p.d == 64) return one ? launch_d<64, 1>(p, st) : launch_d<64, 2>(p, st);
+    return one ? launch_d<128, 1>(p, st) : launch_d<128, 2>(p, st);
 }
 
 }  // namespace gdr
