@@ -292,7 +292,7 @@ __global__ __launch_bounds__(kThreads, 4) void beam_rows(BeamParams p, int per) 
 // One workgroup of a group: its rows' sums joined in 64 bits, then the best M of the runs'
 // best by score.  As in the rows: the M-th best of the runs' first ones is a bound, which
 // few others reach.  All it reads comes by two loads, one after the other (27 us with the
-// candidates read one by one, for 64 groups of 8 beams; _ now).
+// candidates read one by one, for 64 groups of 8 beams; so 8.9).
 namespace {
 // Candidates in LDS: the score, ordered (0: none), and what decides between equal ones: the
 // lower beam, the higher logit, the lower token, as one number.

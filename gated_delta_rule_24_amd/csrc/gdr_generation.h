@@ -64,7 +64,7 @@ struct SharedParams {
     int* plan_items;            // [workgroups] the group that one starts in
     float* part_o;              // [units + workgroups, width, d] unnormalised
     float* part_ml;             // [units + workgroups, width, 2] maximum (base 2) and sum
-    float* own_o;               // [own_splits, N, Hq, d] and its maxima and sums, where own_splits > 1
+    float* own_o;               // [own_splits, N, Hq, d] and its maxima and sums
     float* own_ml;
     int N, groups, Hq, Hkv, d, n_pages, max_pages, window;
     int width, units, workgroups, own_splits;

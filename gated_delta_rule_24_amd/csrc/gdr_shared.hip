@@ -36,6 +36,17 @@ __device__ __forceinline__ void seen_range(const SharedParams& p, int n, int& lo
     lo = (p.window > 0 && len > p.window) ? min(len - p.window, hi) : 0;
 }
 
+// a / b of numbers from 0 on; 64-bit divisions take some hundred instructions
+__device__ __forceinline__ long long div_of(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+    return a / b;
+}
+// tiles of `width` (32 or 64) that these rows take
+__device__ __forceinline__ int tiles_of_rows(const SharedParams& p, long long rows) {
+    const int shift = p.width == 64 ? 6 : 5;
+    return (int)((rows + (1 << shift) - 1) >> shift);
+}
+
 // What the plan makes of group g (see attn_shared_plan_kernel).  Unit kh * tiles + tile of it
 // is `width` of its rows on a key head, over all its shared pages.
 struct Group {
@@ -91,22 +102,23 @@ __device__ __forceinline__ void run_of(int& pg0, int& pg1, int i, int splits) {
     pg1 = min(pg0 + per, pg1);
 }
 
-// Joins what the waves from, from + step, .. (n of them) hold in LDS for the same `rows`
-// rows, each relative to its own maximum; `put` gets four channels of a row at a time, with
-// the row's maximum and sum.
+// Joins what the workgroup's waves hold in LDS for the same `rows` rows, each relative to
+// its own maximum; `put` gets four channels of a row at a time, with the row's maximum and sum.
 template <int D, typename O, typename ML, typename F>
-__device__ __forceinline__ void join_waves(const O& o, const ML& ml, int from, int step, int n, int rows, int thread, int threads, F put) {
-    for (int idx = thread; idx < rows * (D / 4); idx += threads) {
+__device__ __forceinline__ void join_waves(const O& o, const ML& ml, int rows, F put) {
+    for (int idx = threadIdx.x; idx < rows * (D / 4); idx += 64 * kWaves) {
         const int c = idx / (D / 4), ch = 4 * (idx % (D / 4));
         float top = -INFINITY;
-        for (int y = 0; y < n; ++y) top = fmaxf(top, ml[from + y * step][c][0]);
+#pragma unroll
+        for (int y = 0; y < kWaves; ++y) top = fmaxf(top, ml[y][c][0]);
         const float at = top == -INFINITY ? 0.f : top;
         float sum = 0.f;
         float4v x = {0.f, 0.f, 0.f, 0.f};
-        for (int y = 0; y < n; ++y) {
-            const float f = __builtin_amdgcn_exp2f(ml[from + y * step][c][0] - at);
-            sum += ml[from + y * step][c][1] * f;
-            x += *reinterpret_cast<const float4v*>(&o[from + y * step][c][ch]) * f;
+#pragma unroll
+        for (int y = 0; y < kWaves; ++y) {
+            const float f = __builtin_amdgcn_exp2f(ml[y][c][0] - at);
+            sum += ml[y][c][1] * f;
+            x += *reinterpret_cast<const float4v*>(&o[y][c][ch]) * f;
         }
         put(c, ch, x, make_float2(top, sum));
     }
@@ -122,7 +134,8 @@ __device__ __forceinline__ void join_waves(const O& o, const ML& ml, int from, i
 // units end to end: each of as many workgroups as can be at work at once takes a run of the same
 // length of that line, over the ends of units, so that all end together.  (With whole runs of each
 // unit's pages, as many as fit, 3 groups of 340 rows on 256 pages kept 144 of 256
-// workgroups: 119 us, _ now.)
+// workgroups: 119 us for the shared pages, over the ends 101.)  Where whole runs of units are
+// little longer they are taken: a unit's start and end cost some pages' time.
 constexpr int kPlanThreads = 1024;
 constexpr int kLonger = 8;                            // pages that a unit's start and end are worth
 
@@ -165,8 +178,7 @@ __global__ __launch_bounds__(kPlanThreads) void attn_shared_plan_kernel(SharedPa
     __syncthreads();
     // one wave: where each group's units and pages start
     auto tiles_of = [&](int g) {
-        const long long rows = (long long)max(s[g + 1].first - s[g].first, 0) * rep;
-        return (int)((rows + p.width - 1) / p.width);
+        return tiles_of_rows(p, (long long)max(s[g + 1].first - s[g].first, 0) * rep);
     };
     auto first_page = [&](int g) { return s[g].lo / kPage; };
     auto pages_of = [&](int g) { return max(0, min((int)(((long long)s[g].hi + kPage - 1) / kPage), s[g].shared) - first_page(g)); };
@@ -182,7 +194,7 @@ __global__ __launch_bounds__(kPlanThreads) void attn_shared_plan_kernel(SharedPa
     };
     // two pages a wave, as the second's keys are loaded beside the first one's work
     const long long all = sum_of([](int pages) { return (long long)pages; });
-    long long per = max((all + p.workgroups - 1) / p.workgroups, 2LL * kWaves);
+    long long per = max(div_of(all + p.workgroups - 1, p.workgroups), 2LL * kWaves);
     // a unit's start and end are worth some pages: whole runs of a unit where they are little
     // longer (each wave looks at another length)
     {
@@ -226,7 +238,7 @@ __global__ __launch_bounds__(kPlanThreads) void attn_shared_plan_kernel(SharedPa
         if (lane == 0) {
             s_per = per;
             s_whole = whole;
-            s_workgroups = (int)((pos + s_per - 1) / s_per);
+            s_workgroups = (int)div_of(pos + per - 1, per);
         }
     }
     __syncthreads();
@@ -237,7 +249,8 @@ __global__ __launch_bounds__(kPlanThreads) void attn_shared_plan_kernel(SharedPa
         x.pages = s[g].unit0 < 0 ? 0 : pages_of(g);
         x.pg0 = x.pages > 0 ? first_page(g) : 0;
         x.unit0 = max(s[g].unit0, 0);
-        x.shared = s[g].shared;
+        // (a group that did not fit is read by its sequences)
+        x.shared = s[g].unit0 < 0 && pages_of(g) > 0 ? 0 : s[g].shared;
         x.pos0 = s[g].pos0;
         return x;
     };
@@ -278,9 +291,19 @@ __global__ __launch_bounds__(kPlanThreads) void attn_shared_plan_kernel(SharedPa
 // its bytes' conversion above all, is then shared by as many.  The waves of a workgroup
 // have the same rows and take pages in turn, each for itself: with waves that shared
 // a page and waited for each other at every one, 1,024 rows on 512 pages took 215 us for
-// 181.  Pages come through two places in LDS a wave, as they lie in memory, by direct loads a
-// page ahead (no registers, 1 KiB an instruction): read straight to registers in the
-// operands' order, 16 bytes a lane from 32 rows, the same walk took 265.
+// 181.  Pages come to a wave's place in LDS as they lie in memory, by direct loads (no
+// registers, 1 KiB an instruction; read straight to registers in the operands'
+// order, 16 bytes a lane from 32 rows, the same walk took 265): the next page's keys when
+// this one's are read, its values when these are.  With one place and the queries in LDS,
+// two waves of 256 registers are on a SIMD, and one's products run beside the other's
+// exponentials and conversions: 170 us, of which the products' share at the matrix cores' peak
+// is 55.  What bounds it are the vector instructions: a page takes a wave 64 products of 32
+// cycles, and beside them some 330 instructions, of which 64 exponentials and 160 conversions
+// count double and more.
+//
+// Workgroups for sequences' own pages, which memory bounds, stand on the compute units beside
+// these, two a unit: one kernel after the other took 101 and 75 us for 256 sequences
+// behind 3 prompts, both together 128.
 //
 // A weight is exp2(s - m).  For the product with v it is taken times 2^b, b = 12 +
 // log2 v_scale + m - wm, wm the running maximum of s + log2 v_scale, so that it has
@@ -343,7 +366,7 @@ __device__ __forceinline__ uint4v read16(uint32_t at) { return *(const __attribu
 
 // pages of the line that one of group x's units takes
 __device__ __forceinline__ long long length_of(const PlanHead& head, const Group& x) {
-    return head.whole ? (x.pages + head.per - 1) / head.per * head.per : x.pages;
+    return head.whole ? div_of(x.pages + head.per - 1, head.per) * head.per : x.pages;
 }
 
 // all but the last N of this wave's loads have arrived
@@ -560,8 +583,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_shared_kernel(SharedParam
     int unit, page0;
     {
         const long long rel = wg * head.per - x.pos0;
-        unit = (int)(rel / length);
-        page0 = (int)(rel % length);
+        unit = (int)div_of(rel, length);
+        page0 = (int)(rel - unit * length);
     }
     for (;;) {
     int lane = threadIdx.x & 63;
@@ -870,7 +893,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_shared_kernel(SharedParam
         lds_barrier();
         // all their lanes together
         const size_t part = part0 + 32 * c;
-        join_waves<D>(sm.o, sm.ml, 0, 1, kWaves, min(32, rows - 32 * c), wave * 64 + lane, kWaves * 64, [&](int r, int ch, float4v y, float2 ml) {
+        join_waves<D>(sm.o, sm.ml, min(32, rows - 32 * c), [&](int r, int ch, float4v y, float2 ml) {
             *reinterpret_cast<float4v*>(&p.part_o[(part + r) * D + ch]) = y;
             if (ch == 0) *reinterpret_cast<float2*>(&p.part_ml[(part + r) * 2]) = ml;
         });
@@ -913,16 +936,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_shared_kernel(SharedParam
 }
 
 // ---------------------------------------------------------------------------
-// a sequence's own pages, and the join
+// the join
 // ---------------------------------------------------------------------------
-//
-// Up to 16 of a sequence's query heads on a key head are the columns of 16 x 16
-// products (as attn_decode_kernel has them).  A wave has all of the pages of one, or a run of
-// them where there are few sequences, and loads each page while it works on the one before:
-// a few pages a sequence are too few to be dealt to four waves, whose starts and joins
-// took as long as the pages.  Where a wave
-// has all pages it joins the shared ones' partial results as well and writes the output;
-// else a kernel behind this one does.
 
 // where the partial results of a row's shared pages are: those of a unit's pages, cut at the
 // ends of the workgroups' runs, lie one after the other
@@ -933,17 +948,10 @@ struct Parts {
 __device__ __forceinline__ Parts parts_of(const SharedParams& p, const Group& x, int kh, int row) {
     if (x.pages == 0) return {0, 0};
     const PlanHead head = plan_head(p);
-    const int unit = kh * ((x.rows + p.width - 1) / p.width) + row / p.width;
-    const long long at = x.pos0 + unit * length_of(head, x), end = at + x.pages - 1;
-    long long w0, w1;
-    if ((end | head.per) >> 32 == 0) {                // (64-bit divisions take some hundred instructions)
-        w0 = (uint32_t)at / (uint32_t)head.per;
-        w1 = (uint32_t)end / (uint32_t)head.per;
-    } else {
-        w0 = at / head.per;
-        w1 = end / head.per;
-    }
-    return {(size_t)(x.unit0 + unit + w0) * p.width + row % p.width, (int)(w1 - w0) + 1};
+    const int unit = kh * tiles_of_rows(p, x.rows) + (row >> (p.width == 64 ? 6 : 5));
+    const long long at = x.pos0 + unit * length_of(head, x);
+    const long long w0 = div_of(at, head.per), w1 = div_of(at + x.pages - 1, head.per);
+    return {(size_t)(x.unit0 + unit + w0) * p.width + (row & (p.width - 1)), (int)(w1 - w0) + 1};
 }
 
 // Joins a head's partial results: THREADS for a head, in 4 THREADS / D groups of lanes, four
