@@ -33,6 +33,13 @@ def _workspace(nbytes, device):
     return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
 
 
+def _int32(name, x):
+    # (ctypes would keep the low 32 bits without a word)
+    if not -(1 << 31) <= x < 1 << 31:
+        raise ValueError(f"{name} must fit 32 bits, got {x}")
+    return x
+
+
 def _held(held, n_pages, gpu):
     if held is None:
         return None
@@ -160,7 +167,8 @@ def beam_select(logits, scores, n_select: Optional[int] = None, ended=None, end_
     if V > 1 and logits.stride(1) != 1:
         raise ValueError("logits' rows must be contiguous")
     _expect("scores", scores, (G, K), torch.float32, gpu)
-    M = K if n_select is None else n_select
+    M = K if n_select is None else _int32("n_select", n_select)
+    _int32("end_token", end_token)
     if ended is not None:
         _expect("ended", ended, (G, K), torch.bool, gpu)
         ended = ended.data_ptr()
@@ -185,6 +193,7 @@ def state_reorder(state, rows, beams: int, dim: int = 0, stream=None):
     values (:func:`beam_select`'s).  A row whose value is its own or not of its
     group stays as it is.  Returns state."""
     gpu = _gpu_of("state", state)
+    _int32("beams", beams)
     if dim not in (0, 1) or state.dim() <= dim:
         raise ValueError("state must be [N,...], or with dim=1 [layers,N,...]")
     _expect("state", state, state.shape, state.dtype, gpu)

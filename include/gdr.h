@@ -590,7 +590,7 @@ gdr_status gdr_attn_decode(const void* q, const void* k_cache, const void* v_cac
  * sequences group_start[g] .. group_start[g + 1] - 1, and their first
  * shared_pages[g] pages are those in the table's row of the group's first sequence
  * (the other rows' entries for them are not read).  Their tokens are read once for every
- * 16 or 32 of the group's (sequence, query head) pairs on a key head, not once for
+ * 32 or 64 of the group's (sequence, query head) pairs on a key head, not once for
  * each sequence.  Lengths and windows are each sequence's own; a sequence may end inside
  * the shared pages.  Sequences in no group share nothing.
  *   group_start  : int32 [groups + 1] in device memory, non-decreasing, within 0 .. N
