@@ -217,15 +217,18 @@ __global__ __launch_bounds__(kThreads, 4) void beam_rows(BeamParams p, int per) 
             return (uint64_t)least << 32;
         };
         if (c == v0) bound = of_runs();
-        const uint32_t least = (uint32_t)(bound >> 32);
-        if (order_of(top) >= least) {
+        // (as floats, one comparison a value: few waves have none that passes, and most of their
+        // values do not; keys are made of those that do)
+        const float least = value_of((uint32_t)(bound >> 32));
+        if (!(top < least)) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (order_of(tops[u]) >= least) {
+                if (!(tops[u] < least)) {
                     const int v = c + u * kThreads + tid, t = v < v1 ? v * VE - shift : p.V;
 #pragma unroll
                     for (int j = 0; j < VE; ++j) {
                         float y = value(u * VE + j);
+                        if (y < least) continue;
                         asm volatile("" : "+v"(y));   // (keys made where they are needed, not 32 of them ahead)
                         const uint64_t k = key_of(y, t + j);
                         if (k > bound && (unsigned)(t + j) < (unsigned)p.V) {

@@ -28,9 +28,10 @@ from . import (GDR_ACT_F32, GDR_KEEP_SLOTS, GDR_OUT_BF16, KVCache, _act_flag, _c
                gdr_kv_compact_workspace_bytes, gdr_kv_fork_workspace_bytes)
 
 
-def _workspace(nbytes, device):
-    # (0: sizes that the call itself refuses, with its own error)
-    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+def _workspace(nbytes, like):
+    # (0: sizes that the call itself refuses, with its own error.  new_empty here and below: it
+    # takes half of torch.empty's time with a type and a device, and a small call's time is the host's)
+    return like.new_empty(max(nbytes, 16), dtype=torch.uint8)
 
 
 def _int32(name, x):
@@ -70,11 +71,11 @@ def attn_decode_shared(q, cache: KVCache, block_table, cache_len, group_start, s
     _expect("shared_pages", shared_pages, (groups,), torch.int32, gpu)
     _expect("group_start", group_start, (groups + 1,), torch.int32, gpu)
     if o is None:
-        o = torch.empty(shape, dtype=out_dtype, device=q.device)
+        o = q.new_empty(shape, dtype=out_dtype)
     else:
         _expect("o", o, shape, out_dtype, gpu)
     nbytes = gdr_attn_decode_shared_workspace_bytes(N, groups, Hq, Hkv, d, max_pages, window)
-    ws = _workspace(nbytes, q.device)
+    ws = _workspace(nbytes, q)
     _launch("gdr_attn_decode_shared", gpu, stream, q.data_ptr(), *[t.data_ptr() for t in cache], block_table.data_ptr(),
             cache_len.data_ptr(), group_start.data_ptr(), shared_pages.data_ptr(), o.data_ptr(), N, groups, Hq, Hkv, d,
             n_pages, max_pages, _window(window), d ** -0.5 if scale is None else scale,
@@ -108,18 +109,17 @@ def kv_fork(cache: KVCache, block_table, cache_len, parent=None, room=1, held=No
         room_all = room
         if not 0 <= room < 1 << 31:
             raise ValueError(f"room must be 0 or more and fit 32 bits, got {room}")
-    dev = block_table.device
     if table_out is None:
-        table_out = torch.empty((N, max_pages), dtype=torch.int32, device=dev)
+        table_out = block_table.new_empty((N, max_pages))
     else:
         _expect("table_out", table_out, (N, max_pages), torch.int32, gpu)
     if len_out is None:
-        len_out = torch.empty((N,), dtype=torch.int32, device=dev)
+        len_out = cache_len.new_empty(N)
     else:
         _expect("len_out", len_out, (N,), torch.int32, gpu)
-    missing = torch.empty((N,), dtype=torch.int32, device=dev)
+    missing = cache_len.new_empty(N)
     nbytes = gdr_kv_fork_workspace_bytes(N, n_pages)
-    ws = _workspace(nbytes, dev)
+    ws = _workspace(nbytes, block_table)
     _launch("gdr_kv_fork", gpu, stream, *[t.data_ptr() for t in cache], block_table.data_ptr(), cache_len.data_ptr(), parent,
             room_ptr, _held(held, n_pages, gpu), table_out.data_ptr(), len_out.data_ptr(), missing.data_ptr(), N_in, N,
             room_all, Hkv, d, n_pages, max_pages, 0, ws.data_ptr(), nbytes)
@@ -133,14 +133,13 @@ def kv_compact(cache: KVCache, block_table, cache_len, held=None, table_out=None
     the last page in use afterwards).  table_out may be block_table."""
     gpu = _gpu_of("cache.k", cache.k)
     n_pages, Hkv, d, N, max_pages = _cache_shapes(cache, block_table, cache_len, gpu)
-    dev = block_table.device
     if table_out is None:
-        table_out = torch.empty((N, max_pages), dtype=torch.int32, device=dev)
+        table_out = block_table.new_empty((N, max_pages))
     else:
         _expect("table_out", table_out, (N, max_pages), torch.int32, gpu)
-    used = torch.empty((1,), dtype=torch.int32, device=dev)
+    used = cache_len.new_empty(1)
     nbytes = gdr_kv_compact_workspace_bytes(n_pages)
-    ws = _workspace(nbytes, dev)
+    ws = _workspace(nbytes, block_table)
     _launch("gdr_kv_compact", gpu, stream, *[t.data_ptr() for t in cache], block_table.data_ptr(), cache_len.data_ptr(),
             _held(held, n_pages, gpu), table_out.data_ptr(), used.data_ptr(), N, Hkv, d, n_pages, max_pages, 0,
             ws.data_ptr(), nbytes)
@@ -172,13 +171,12 @@ def beam_select(logits, scores, n_select: Optional[int] = None, ended=None, end_
     if ended is not None:
         _expect("ended", ended, (G, K), torch.bool, gpu)
         ended = ended.data_ptr()
-    dev = logits.device
-    tokens = torch.empty((G, M), dtype=torch.int32, device=dev)
-    rows = torch.empty((G, M), dtype=torch.int32, device=dev)
-    out = torch.empty((G, M), dtype=torch.float32, device=dev)
-    done = torch.empty((G, M), dtype=torch.bool, device=dev)
+    tokens = scores.new_empty((G, M), dtype=torch.int32)
+    rows = scores.new_empty((G, M), dtype=torch.int32)
+    out = scores.new_empty((G, M))
+    done = scores.new_empty((G, M), dtype=torch.bool)
     nbytes = gdr_beam_select_workspace_bytes(G, K, M, V)
-    ws = _workspace(nbytes, dev)
+    ws = _workspace(nbytes, logits)
     _launch("gdr_beam_select", gpu, stream, logits.data_ptr(), scores.data_ptr(), ended, tokens.data_ptr(), rows.data_ptr(),
             out.data_ptr(), done.data_ptr(), G, K, M, V, logits.stride(0) if G * K > 1 else V, end_token,
             (GDR_ACT_F32 if _act_flag(logits) == GDR_ACT_F32 else 0) | (GDR_KEEP_SLOTS if keep_slots else 0),

@@ -43,14 +43,15 @@ def world(monkeypatch):
         yield
         w["now"].pop()
 
-    def empty(*a, _empty=torch.empty, **k):
-        t = _empty(*a, **k)
+    def empty(like, *a, _empty=torch.Tensor.new_empty, **k):
+        t = _empty(like, *a, **k)
         w["allocated"].append((t, w["now"][-1]))
         return t
 
     monkeypatch.setattr(gen, "_launch", lambda fn, gpu, stream, *a: w["launched"].append((fn, stream)))
     monkeypatch.setattr(gen, "_gpu_of", lambda name, t: t.get_device())
-    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(torch.Tensor, "new_empty", empty)
+    monkeypatch.setattr(torch, "empty", None)         # (not used)
     monkeypatch.setattr(torch.cuda, "stream", on)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: w["now"][-1])
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: w["kept"].append((t, s)))
