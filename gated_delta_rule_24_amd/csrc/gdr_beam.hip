@@ -323,7 +323,7 @@ __device__ __forceinline__ int before_in(const Candidates& c, int n, int i) {
     }
     return before;
 }
-constexpr int kMostRuns = 1024 + kMostBeams;          // of a group (beam_segments)
+constexpr int kMostRuns = 128;                        // of a group (beam_segments)
 constexpr int kCandidate = 8 + 8;
 __device__ __forceinline__ Candidates candidates_at(char* at, int n) {
     Candidates c;
@@ -350,25 +350,16 @@ __global__ __launch_bounds__(kThreads) void beam_join(BeamParams p) {
     const double inf = INFINITY;
 
     // the runs' sums and first keys, the beams' scores
-    constexpr int kEach = (kMostRuns + kThreads - 1) / kThreads;
-    uint64_t keys[kEach];
+    static_assert(kMostRuns <= kThreads, "a run a thread");
+    uint64_t first_key = 0;
     {
-        float2 ms[kEach];
         const float base = tid < K ? p.scores[g * K + tid] : 0.f;
         const bool over = tid < K && p.ended && p.ended[g * K + tid];
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            const int run = tid + kThreads * i;
-            keys[i] = 0;
-            ms[i] = make_float2(-INFINITY, 0.f);
-            if (run < runs) {
-                ms[i] = *reinterpret_cast<const float2*>(p.part + 2 * ((long long)g * runs + run));
-                keys[i] = p.best[((long long)g * runs + run) * M];
-            }
+        if (tid < runs) {
+            const float2 ms = *reinterpret_cast<const float2*>(p.part + 2 * ((long long)g * runs + tid));
+            first_key = p.best[((long long)g * runs + tid) * M];
+            sums[tid] = ms;
         }
-#pragma unroll
-        for (int i = 0; i < kEach; ++i)
-            if (tid + kThreads * i < runs) sums[tid + kThreads * i] = ms[i];
         if (tid < K) { s_score[tid] = base; s_ended[tid] = over; }
         if (tid == 0) s_n = 0;
     }
@@ -418,17 +409,12 @@ __global__ __launch_bounds__(kThreads) void beam_join(BeamParams p) {
     // the runs whose first candidate is among the best M of all first ones
     int lists = runs;
     if (runs > M) {
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            const int run = tid + kThreads * i;
-            if (run < runs) {
-                first.score[run] = candidate(run / S, run % S, 0, keys[i]);
-                first.tie[run] = tie_of(run / S, keys[i]);
-            }
+        if (tid < runs) {
+            first.score[tid] = candidate(tid / S, tid % S, 0, first_key);
+            first.tie[tid] = tie_of(tid / S, first_key);
         }
         __syncthreads();
-        for (int run = tid; run < runs; run += kThreads)
-            if (first.score[run] && before_in(first, runs, run) < M) passed[atomicAdd(&s_n, 1)] = run;
+        if (tid < runs && first.score[tid] && before_in(first, runs, tid) < M) passed[atomicAdd(&s_n, 1)] = tid;
         __syncthreads();
         lists = s_n;
     }
@@ -511,12 +497,16 @@ __global__ __launch_bounds__(kThreads) void beam_join(BeamParams p) {
 }
 
 int beam_segments(int G, int K, int V) {
-    // Enough workgroups for every compute unit where there are few rows; a run of 2,048
-    // values at the least.
+    // Enough workgroups for every compute unit where there are few rows (twice as many and half
+    // as many take 64 x 8 beams over 131,072 tokens from 47.6 us to 52 and 68); a run of
+    // 8,192 values at the least, a bf16 chunk (4 beams over 131,072: 19.3 us a call; of 2,048, 28.5);
+    // and no more runs of a group than the join has soon ranked (4 beams over 2,000,000: 37 us;
+    // of up to 256 runs 36 but one row there 29 for 21, of up to 1,000, 222).
     const long long rows = (long long)G * K;
-    long long s = (1024 + rows - 1) / rows;           // (kMostRuns has room for them)
-    const long long most = ((long long)V + 2047) / 2048;
+    long long s = (1024 + rows - 1) / rows;
+    const long long most = ((long long)V + 8191) / 8192;
     if (s > most) s = most;
+    if (s > kMostRuns / K) s = kMostRuns / K;
     return s < 1 ? 1 : (int)s;
 }
 
