@@ -20,7 +20,8 @@ constexpr int kPage = 64;
 constexpr int kThreads = 256;
 constexpr int kPagesPerBlock = 4096;                  // pages that a workgroup counts
 constexpr int kEntriesPerBlock = 2048;                // entries of one row that a workgroup copies
-constexpr int kCopyBytes = 8192;                      // bytes of a page that a workgroup copies
+constexpr int kPiece = 16 * kThreads;                 // bytes that a workgroup copies at once; a side of a page is whole ones
+constexpr int kForkPieces = 1, kMovePieces = 4;       // that it copies together
 constexpr int kCopyWorkgroups = 4096;                 // compact: workgroups that take the moved pages in turn
 
 // A page's counters: entries that name it in the low half, rows that will write
@@ -103,27 +104,25 @@ __device__ __forceinline__ int block_before(int x, int* s, int& all) {
     return base + run - x;
 }
 
-// 8 KiB of a page from one place to another: part `part` of the keys' bytes, then
-// the values', then (part 0) the scales.
+// PIECES pieces of a page from one place to another, part `part` of the keys' bytes, then the
+// values'; and (part 0) the scales.  Loads without a branch: with one, each waited for the last.
+template <int PIECES>
 __device__ __forceinline__ void copy_part(const PagesParams& p, int from, int to, int part) {
-    const size_t side = (size_t)p.Hkv * kPage * p.d, all = 2 * side;
-    const size_t begin = (size_t)part * kCopyBytes;
-    uint4 x[kCopyBytes / 16 / kThreads];
+    const size_t side = (size_t)p.Hkv * kPage * p.d;
+    const int each = (int)(side / kPiece), at = 16 * threadIdx.x;
+    uint4 x[PIECES];
 #pragma unroll
-    for (int i = 0; i < kCopyBytes / 16 / kThreads; ++i) {
-        const size_t at = begin + 16 * (threadIdx.x + (size_t)kThreads * i);
-        if (at < all) {
-            const uint8_t* src = at < side ? p.k_cache + from * side + at : p.v_cache + from * side + (at - side);
-            x[i] = *reinterpret_cast<const uint4*>(src);
-        }
+    for (int i = 0; i < PIECES; ++i) {
+        const int c = min(part * PIECES + i, 2 * each - 1);
+        const uint8_t* src = c < each ? p.k_cache + from * side + (size_t)c * kPiece : p.v_cache + from * side + (size_t)(c - each) * kPiece;
+        x[i] = *reinterpret_cast<const uint4*>(src + at);
     }
 #pragma unroll
-    for (int i = 0; i < kCopyBytes / 16 / kThreads; ++i) {
-        const size_t at = begin + 16 * (threadIdx.x + (size_t)kThreads * i);
-        if (at < all) {
-            uint8_t* dst = at < side ? p.k_cache + to * side + at : p.v_cache + to * side + (at - side);
-            *reinterpret_cast<uint4*>(dst) = x[i];
-        }
+    for (int i = 0; i < PIECES; ++i) {
+        const int c = part * PIECES + i;
+        if (c >= 2 * each) break;
+        uint8_t* dst = c < each ? p.k_cache + to * side + (size_t)c * kPiece : p.v_cache + to * side + (size_t)(c - each) * kPiece;
+        *reinterpret_cast<uint4*>(dst + at) = x[i];
     }
     if (part == 0)
         for (int h = threadIdx.x; h < p.Hkv; h += kThreads) {
@@ -131,7 +130,7 @@ __device__ __forceinline__ void copy_part(const PagesParams& p, int from, int to
             p.v_scale[(size_t)to * p.Hkv + h] = p.v_scale[(size_t)from * p.Hkv + h];
         }
 }
-int copy_parts(int Hkv, int d) { return blocks_of(2LL * Hkv * kPage * d, kCopyBytes); }
+int copy_parts(int Hkv, int d, int pieces) { return blocks_of(2LL * Hkv * kPage * d, (long long)pieces * kPiece); }
 
 }  // namespace
 
@@ -267,9 +266,12 @@ __global__ __launch_bounds__(kThreads) void fork_assign(PagesParams p, ForkSpace
     }
 }
 
+// One piece a workgroup: 110 pages of 128 KiB behind 256 rows take 6.2 us, 4.7 TB/s.  (Consecutive
+// workgroups go to the 8 XCDs and there to the 4 shader engines by turns.  With 16 for a
+// row, not 32, the rows that copy, mostly every other one, fell on half of them: 17.6.)
 __global__ __launch_bounds__(kThreads) void fork_copy(PagesParams p, ForkSpace s, int parts) {
     const int n = blockIdx.x / parts, to = s.place[n], from = s.source[n];   // (without a place, no page: not read)
-    if (to >= 0) copy_part(p, from, to, blockIdx.x % parts);
+    if (to >= 0) copy_part<kForkPieces>(p, from, to, blockIdx.x % parts);
 }
 
 // The same for caches and tables that one workgroup has soon read: the counters are in
@@ -436,14 +438,14 @@ size_t kv_fork_workspace(int N, int n_pages) {
 }
 
 long long kv_fork_workgroups(int N, int Hkv, int d, int n_pages, int max_pages) {
-    const long long rows = (long long)N * blocks_of(max_pages, kEntriesPerBlock), copies = (long long)N * copy_parts(Hkv, d);
+    const long long rows = (long long)N * blocks_of(max_pages, kEntriesPerBlock), copies = (long long)N * copy_parts(Hkv, d, kForkPieces);
     const long long pages = blocks_of(n_pages, kPagesPerBlock);
     return rows > copies ? (rows > pages ? rows : pages) : copies > pages ? copies : pages;
 }
 
 hipError_t launch_kv_fork(const PagesParams& p, hipStream_t st) {
     const ForkSpace s = fork_space(p.workspace, p.N, p.n_pages);
-    const int parts = copy_parts(p.Hkv, p.d);
+    const int parts = copy_parts(p.Hkv, p.d, kForkPieces);
     if (small_tables(p.N, p.n_pages, p.max_pages, kForkEntries)) {
         static std::atomic<unsigned long long> done{0};
         const hipError_t e = ensure_dyn_lds(reinterpret_cast<const void*>(&fork_small), (int)fork_small_lds(kSmallRows, kSmallPages), done);
@@ -640,7 +642,8 @@ __global__ __launch_bounds__(kSmallThreads) void compact_small(PagesParams p, Co
     }
 }
 
-// The moves, 8 KiB a workgroup at a time, and (rows > 0) the rows that follow them.
+// The moves, 16 KiB a workgroup at a time, and (rows > 0) the rows that follow them.  HBM bounds them:
+// 1,240 pages of 128 KiB take 61 to 66 us, 4.9 to 5.3 TB/s (8 KiB 65, 4 KiB 70, 32 KiB 95).
 __global__ __launch_bounds__(kThreads) void compact_move(PagesParams p, CompactSpace s, int parts, int chunks, int rows) {
     const int free = s.counts[0], used = s.counts[1], pairs = min(free, used);
     if ((int)blockIdx.x < rows) {
@@ -670,7 +673,7 @@ __global__ __launch_bounds__(kThreads) void compact_move(PagesParams p, CompactS
         const int j = (int)(it / parts);
         const int to = s.free_list[j], from = s.used_list[j];
         if (to >= from) break;
-        copy_part(p, from, to, (int)(it % parts));
+        copy_part<kMovePieces>(p, from, to, (int)(it % parts));
     }
     // pages up to the last in use: the last destination, or the first that stays
     if (rows > 0 && (int)blockIdx.x == rows) {
@@ -696,7 +699,7 @@ hipError_t launch_kv_compact(const PagesParams& p, hipStream_t st) {
     CompactSpace s;
     compact_take(p.workspace, p.n_pages, &s);
     const dim3 block(kThreads);
-    const int parts = copy_parts(p.Hkv, p.d);
+    const int parts = copy_parts(p.Hkv, p.d, kMovePieces);
     // at most half the pages move
     const long long items = ((long long)p.n_pages / 2) * parts;
     const int movers = items < 1 ? 1 : items < kCopyWorkgroups ? (int)items : kCopyWorkgroups;
