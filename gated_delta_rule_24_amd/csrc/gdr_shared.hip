@@ -92,14 +92,19 @@ __device__ __forceinline__ uint32_t bytes_of(uint32_t bits, int i) { return (((b
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
 
-// Which run of the pages pg0 .. pg1 - 1 is number i of `splits`; two pages at least, as the
-// second is loaded beside the first one's work.
-__device__ __forceinline__ void run_of(int& pg0, int& pg1, int i, int splits) {
-    if (pg1 <= pg0) { pg1 = pg0; return; }
-    const int per = max((pg1 - pg0 + splits - 1) / splits, 2);
-    const long long begin = pg0 + (long long)i * per;
-    pg0 = begin < pg1 ? (int)begin : pg1;
-    pg1 = min(pg0 + per, pg1);
+// A sequence's own pages: begin .. end - 1, in runs of `per` (own_splits at the most; a short
+// sequence has fewer, as a wave's start and end cost some pages' time).
+constexpr int kOwnRun = 4;
+struct OwnPages {
+    int begin, end, per;
+};
+__device__ __forceinline__ OwnPages own_pages_of(const SharedParams& p, int n, int shared, int& lo, int& hi) {
+    seen_range(p, n, lo, hi);
+    OwnPages x;
+    x.begin = max(lo / kPage, shared);
+    x.end = max(x.begin, (int)(((long long)hi + kPage - 1) / kPage));
+    x.per = max((int)(((uint32_t)(x.end - x.begin) + (uint32_t)p.own_splits - 1) / (uint32_t)p.own_splits), kOwnRun);
+    return x;
 }
 
 // Joins what the workgroup's waves hold in LDS for the same `rows` rows, each relative to
@@ -388,7 +393,11 @@ __device__ __forceinline__ void own_pages(const SharedParams& p, int w, uint32_t
     const int q0 = kh * rep + 16 * qg, nq = min(16, rep - 16 * qg);
     const Group x = group_at(p.plan_sequences, n);
     int lo, hi;
-    seen_range(p, n, lo, hi);
+    const OwnPages mine = own_pages_of(p, n, x.shared, lo, hi);
+    const long long begin = mine.begin + (long long)run * mine.per;
+    if (begin >= mine.end) return;                    // (the join does not read it)
+    const int pg0 = __builtin_amdgcn_readfirstlane((int)begin), pg1 = __builtin_amdgcn_readfirstlane(min((int)begin + mine.per, mine.end));
+    const int count = pg1 - pg0;
     // queries: column col, channels 64 s + 16 g + 8 half ..
     bf8v qf[KS][2];
 #pragma unroll
@@ -400,12 +409,6 @@ __device__ __forceinline__ void own_pages(const SharedParams& p, int w, uint32_t
                 u = *reinterpret_cast<const uint4*>((const uint16_t*)p.q + ((size_t)n * p.Hq + q0 + col) * D + 64 * s + 16 * g + 8 * hf);
             qf[s][hf] = __builtin_bit_cast(bf8v, u);
         }
-    int pg0 = max(lo / kPage, x.shared), pg1 = (int)(((long long)hi + kPage - 1) / kPage);
-    run_of(pg0, pg1, run, p.own_splits);
-    pg0 = __builtin_amdgcn_readfirstlane(pg0);
-    pg1 = __builtin_amdgcn_readfirstlane(pg1);
-    const int count = pg1 - pg0;
-
     // pages k0 .. k0 + 63 of the run, one a lane: place (-1: absent) and scales
     const int* entries = p.block_table + (size_t)n * p.max_pages + pg0;
     int e_page;
@@ -421,11 +424,9 @@ __device__ __forceinline__ void own_pages(const SharedParams& p, int w, uint32_t
     constexpr uint32_t kSide = kPage * D;
     // (an absent page is read as the first one)
     auto page_at = [&](int k) { return ((size_t)max(__builtin_amdgcn_readlane(e_page, k & 63), 0) * p.Hkv + kh) * kSide; };
-    if (count > 0) {
-        look_up(0);
-        loader.keys((uint64_t)p.k_cache + page_at(0), place);
-        loader.values((uint64_t)p.v_cache + page_at(0), place + kSide);
-    }
+    look_up(0);
+    loader.keys((uint64_t)p.k_cache + page_at(0), place);
+    loader.values((uint64_t)p.v_cache + page_at(0), place + kSide);
     const int krow = 16 * (col >> 2) + (col & 3);     // key of tile 0's row `col`; its flip is that of the others, + 4 t, too
     const uint32_t at_k = place + krow * D + 16 * (g ^ key_flip<D, true>(krow)), at_v = place + kSide + (g * D + col) * 16;
 
@@ -536,10 +537,8 @@ __device__ __forceinline__ void own_pages(const SharedParams& p, int w, uint32_t
     for (int j = 0; j < VT; ++j) o[j] *= down;
     if (col >= nq) return;
     const size_t head = (size_t)n * p.Hq + q0 + col, heads = (size_t)p.N * p.Hq;
-    // (nothing in the run: the join does not read the output)
-    if (count > 0)
 #pragma unroll
-        for (int j = 0; j < VT; ++j) *reinterpret_cast<float4v*>(&p.own_o[(run * heads + head) * D + 16 * j + 4 * g]) = o[j];
+    for (int j = 0; j < VT; ++j) *reinterpret_cast<float4v*>(&p.own_o[(run * heads + head) * D + 16 * j + 4 * g]) = o[j];
     if (g == 0) *reinterpret_cast<float2*>(&p.own_ml[(run * heads + head) * 2]) = make_float2(m, l);
 }
 
@@ -553,8 +552,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_shared_kernel(SharedParam
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), rep = p.Hq / p.Hkv;
 
     // a workgroup for shared pages for each of 256 compute units and one for own ones by turns,
-    // as long as there are both (by turns of 8, half the shader engines got all of the
-    // first kind: they are taken one after the other)
+    // as long as there are both (256 sequences behind 3 prompts 147 us; all of the first kind
+    // before the others 163; by turns of 8, as shader engines are taken one after the other, half of
+    // them got all of the first kind: 185)
     constexpr int kTurn = 256 / 8;
     int number = blockIdx.x / 8;
     const int some = p.workgroups / 8, turns = min(some, (int)(gridDim.x / 8) - some) / kTurn;
@@ -966,7 +966,9 @@ __global__ __launch_bounds__(THREADS) void attn_shared_join(SharedParams p) {
     const int n = (int)(head / p.Hq), hq = (int)(head % p.Hq), rep = p.Hq / p.Hkv;
     const Group x = group_at(p.plan_sequences, n);
     const Parts parts = parts_of(p, x, hq / rep, (n - x.first) * rep + hq % rep);
-    const int slots = parts.n + p.own_splits;
+    int lo, hi;
+    const OwnPages own = own_pages_of(p, n, x.shared, lo, hi);
+    const int slots = parts.n + (int)((uint32_t)(own.end - own.begin + own.per - 1) / (uint32_t)own.per);
     float top = -INFINITY, sum = 0.f;
     float4v y = {0.f, 0.f, 0.f, 0.f};
     for (int s0 = gi; s0 < slots; s0 += kAtOnce * GROUPS) {
@@ -983,8 +985,7 @@ __global__ __launch_bounds__(THREADS) void attn_shared_join(SharedParams p) {
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
             const int s = s0 + i * GROUPS;
-            // (nothing seen there: an empty run's output is not written)
-            if (s >= slots || (ml[i].x == -INFINITY && ml[i].y == 0.f && s >= parts.n)) continue;
+            if (s >= slots) continue;
             const float both = fmaxf(top, ml[i].x), at = both == -INFINITY ? 0.f : both;
             const float f = __builtin_amdgcn_exp2f(top - at), g = __builtin_amdgcn_exp2f(ml[i].x - at);
             sum = sum * f + ml[i].y * g;
@@ -1033,9 +1034,11 @@ SharedPlan attn_shared_plan(int N, int groups, int Hq, int Hkv, int d, int max_p
     x.own_items = (long long)N * Hkv * ((rep + 15) / 16);
     int pages = max_pages;
     if (window > 0 && window / kPage + 2 < pages) pages = window / kPage + 2;
-    // about a wave a SIMD (twice and half as many: the same within 3%)
-    long long s = (1024 + x.own_items / 2) / x.own_items;
-    const long long most = (pages + 1) / 2;
+    // Four waves a SIMD, and those of short sequences end at once: 60 sequences of up to 4,000 own
+    // tokens 74 us (with one a SIMD 89), 255 of up to 2,000 behind 3 prompts 152 (168), of up
+    // to 1,000 153 (151); 64 of 200 43 (41.6).
+    long long s = (4096 + x.own_items / 2) / x.own_items;
+    const long long most = (pages + kOwnRun - 1) / kOwnRun;
     if (s > most) s = most;
     x.own_splits = s < 1 ? 1 : (int)s;
     // the workspace: plan, then partial results
