@@ -802,27 +802,30 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_shared_kernel(SharedParam
             }
         }
         float up[NB], share[NB];                      // a weight's exponent over its score's; its part in the sum
-        bool far = false;
+        bool far[NB], some_far = false;
 #pragma unroll
         for (int c = 0; c < NB; ++c) {
             const float at = m[c] == -INFINITY ? 0.f : m[c], wat = wm[c] == -INFINITY ? 0.f : wm[c];
             up[c] = none[c] ? 0.f : log_vs - wat + kTop;
             share[c] = none[c] ? 0.f : __builtin_amdgcn_exp2f(-(up[c] + at));
-            far = far || (!none[c] && !(fabsf(up[c] + at) <= 60.f));
+            far[c] = !none[c] && !(fabsf(up[c] + at) <= 60.f);
+            some_far = some_far || far[c];
         }
-        if (__any(far)) {
-            // the sum's own exponentials
+        if (__any(some_far)) {
+            // the sum's own exponentials, for the rows that need them
 #pragma unroll
             for (int c = 0; c < NB; ++c) {
                 const float at = m[c] == -INFINITY ? 0.f : m[c];
+                float sum = 0.f;
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        l[c] += __builtin_amdgcn_exp2f(__builtin_fmaf(st[c][b][i], by, -at));
-                        asm volatile("" : "+v"(l[c]));    // (one after the other: no registers for it)
+                        sum += __builtin_amdgcn_exp2f(__builtin_fmaf(st[c][b][i], by, -at));
+                        asm volatile("" : "+v"(sum));     // (one after the other: no registers for it)
                     }
-                share[c] = 0.f;
+                l[c] += far[c] ? sum : 0.f;
+                share[c] = far[c] ? 0.f : share[c];
             }
         }
 

@@ -379,3 +379,29 @@ def test_pages_past_32_bits():
     got = gen.attn_decode_shared(q[[0, 1, 2, 2]].cuda(), cache, t, n, *[torch.as_tensor(x, dtype=torch.int32).cuda() for x in ([0, 2, 4], [1, 0])])
     four = [0, 1, 2, 2]
     assert bool(((got.cpu().to(F64) - want[four]).abs() <= tol[four]).all())
+
+
+@pytest.mark.parametrize("out", [torch.float32, BF16])
+@pytest.mark.parametrize("Hq,Hkv,d", [(2, 1, 64), (8, 2, 128), (64, 1, 64)])
+def test_a_neighbours_page_changes_no_bit(Hq, Hkv, d, out):
+    """A page that only the group's other sequences see, with a scale far from the rest: theirs
+    take another way through the pages behind it, the first one's results stay bit for bit."""
+    g = torch.Generator().manual_seed(3)
+    cache = gdr.kv_cache(12, Hkv, d, device="cpu")
+    for x in (cache.k, cache.v):
+        x.copy_((torch.randn(x.shape, generator=g) * 60).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8))
+    for x in (cache.k_scale, cache.v_scale):
+        x.fill_(2.0 ** -6)
+    # pages 1 .. 6 and 4 .. 9 of the shared ten: the second has page 1 for itself
+    lens, window = [640, 448, 448], 384
+    table = torch.arange(10, dtype=torch.int32).repeat(3, 1)
+    q = torch.randn((3, Hq, d), generator=g).to(BF16)
+    ints = [torch.as_tensor(x, dtype=torch.int32).cuda() for x in (table, lens, [0, 3], [10])]
+    outs = []
+    for scale in (2.0 ** -6, 2.0 ** 80, 2.0 ** -96, 0.0):
+        c = gdr.KVCache(*[x.cuda() for x in cache])
+        c.v_scale[1] = scale
+        outs.append(gen.attn_decode_shared(q.cuda(), c, *ints, window=window, out_dtype=out))
+    for o in outs[1:]:
+        assert torch.equal(o[0], outs[0][0])
+        assert not torch.equal(o[1], outs[0][1])
