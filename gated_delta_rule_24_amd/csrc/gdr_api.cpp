@@ -684,7 +684,7 @@ gdr_status gdr_attn_decode_shared(const void* q, const void* k_cache, const void
     p.k_scale = k_scale; p.v_scale = v_scale; p.block_table = block_table; p.cache_len = cache_len;
     p.group_start = group_start; p.shared_pages = shared_pages; p.o = o;
     p.N = N; p.groups = groups; p.Hq = Hq; p.Hkv = Hkv; p.d = d; p.n_pages = n_pages; p.max_pages = max_pages;
-    p.window = window; p.width = x.width; p.units = (int)x.units; p.workgroups = x.workgroups; p.own_splits = x.own_splits;
+    p.window = window; p.width = x.width; p.units = (int)x.units; p.workgroups = x.workgroups; p.own_splits = x.own_splits; p.few = x.few;
     p.own_runs = x.own_items * x.own_splits;
     char* ws = static_cast<char*>(workspace);
     p.plan_head = ws + x.at_head;

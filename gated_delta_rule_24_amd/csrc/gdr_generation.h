@@ -42,6 +42,7 @@ struct SharedPlan {
     int width;                  // rows of a workgroup for shared pages: 32 or 64
     long long units;            // (group, key head, `width` of its rows) that there can be
     int workgroups;             // for the shared pages, at most
+    bool few;                   // groups and sequences: no plan kernel
     long long own_items;        // (sequence, key head, set of 16 query heads)
     int own_splits;             // runs that a sequence's own pages are dealt into
     size_t at_head, at_groups, at_sequences, at_items, at_part_o, at_part_ml, at_own_o, at_own_ml, bytes;
@@ -67,7 +68,7 @@ struct SharedParams {
     float* own_o;               // [own_splits, N, Hq, d] and its maxima and sums
     float* own_ml;
     int N, groups, Hq, Hkv, d, n_pages, max_pages, window;
-    int width, units, workgroups, own_splits;
+    int width, units, workgroups, own_splits, few;
     long long own_runs;         // own_items * own_splits
     float scale;
     uint32_t flags;

@@ -146,9 +146,20 @@ constexpr int kLonger = 8;                            // pages that a unit's sta
 
 struct PlanGroup {
     int first, shared, lo, hi;  // first sequence; pages; first and one past the last token that some sequence sees
-    int unit0;                  // -1: not shared
+    int unit0;
     long long pos0;
 };
+// runs of `per` that a unit's pages take
+__device__ __forceinline__ int runs_of(int pages, long long per) {
+    return pages <= per ? 1 : (int)(((uint32_t)pages + (uint32_t)per - 1) / (uint32_t)per);
+}
+// the pages that some sequence sees of a group's shared ones, whose tokens lo .. hi - 1 some see
+__device__ __forceinline__ int pages_seen(int lo, int hi, int shared) {
+    return max(0, min((int)(((long long)hi + kPage - 1) / kPage), shared) - lo / kPage);
+}
+__device__ __forceinline__ Group planned(int first, int rows, int pages, int lo, int shared, int unit0, long long pos0) {
+    return Group{first, rows, pages > 0 ? lo / kPage : 0, pages, unit0, shared, pos0};
+}
 
 __global__ __launch_bounds__(kPlanThreads) void attn_shared_plan_kernel(SharedParams p) {
     extern __shared__ __attribute__((aligned(256))) char smem[];
@@ -171,6 +182,20 @@ __global__ __launch_bounds__(kPlanThreads) void attn_shared_plan_kernel(SharedPa
     for (int g = tid; g <= G; g += kPlanThreads)
         s[g] = PlanGroup{clampi(p.group_start[g], 0, p.N), g < G ? clampi(p.shared_pages[g], 0, p.max_pages) : 0, INT_MAX, 0, 0, 0};
     __syncthreads();
+    // (bounds that fall are held where they were: no sequence is in two groups)
+    if (tid < 64) {
+        int top = 0;
+        for (int g0 = 0; g0 <= G; g0 += 64) {
+            int first = max(top, g0 + lane <= G ? s[g0 + lane].first : 0);
+            for (int o = 1; o < 64; o <<= 1) {
+                const int y = __shfl_up(first, o, 64);
+                if (lane >= o) first = max(first, y);
+            }
+            if (g0 + lane <= G) s[g0 + lane].first = first;
+            top = __shfl(first, 63, 64);
+        }
+    }
+    __syncthreads();
     for (int n = tid; n < p.N; n += kPlanThreads) {
         int a = a0, b = b0;
         if (n != tid) seen_range(p, n, a, b);
@@ -183,19 +208,14 @@ __global__ __launch_bounds__(kPlanThreads) void attn_shared_plan_kernel(SharedPa
     __syncthreads();
     // one wave: where each group's units and pages start
     auto tiles_of = [&](int g) {
-        return tiles_of_rows(p, (long long)max(s[g + 1].first - s[g].first, 0) * rep);
+        return tiles_of_rows(p, (long long)(s[g + 1].first - s[g].first) * rep);
     };
-    auto first_page = [&](int g) { return s[g].lo / kPage; };
-    auto pages_of = [&](int g) { return max(0, min((int)(((long long)s[g].hi + kPage - 1) / kPage), s[g].shared) - first_page(g)); };
+    auto pages_of = [&](int g) { return pages_seen(s[g].lo, s[g].hi, s[g].shared); };
     auto sum_of = [&](auto f) {
         long long x = 0;
         for (int g = lane; g < G; g += 64) x += (long long)tiles_of(g) * p.Hkv * f(pages_of(g));
         for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o, 64);
         return x;
-    };
-    // runs of `per` that a unit's pages take
-    auto runs_of = [&](int pages, long long per) {
-        return pages <= per ? 1 : (int)(((uint32_t)pages + (uint32_t)per - 1) / (uint32_t)per);
     };
     // two pages a wave, as the second's keys are loaded beside the first one's work
     const long long all = sum_of([](int pages) { return (long long)pages; });
@@ -219,22 +239,15 @@ __global__ __launch_bounds__(kPlanThreads) void attn_shared_plan_kernel(SharedPa
         for (int g0 = 0; g0 < G; g0 += 64) {
             const int g = g0 + lane;
             const int pages = g < G ? pages_of(g) : 0;
-            long long u = pages > 0 ? (long long)tiles_of(g) * p.Hkv : 0;
-            // (bounds that overlap may want more units than there are: such a group shares nothing)
-            long long run = u;
+            const long long u = pages > 0 ? (long long)tiles_of(g) * p.Hkv : 0;
+            const long long mine = whole ? u * (runs_of(pages, per) * per) : u * pages;
+            long long run = u, at = mine;
             for (int o = 1; o < 64; o <<= 1) {
-                const long long y = __shfl_up(run, o, 64);
-                if (lane >= o) run += y;
-            }
-            const bool fits = u > 0 && units + run <= p.units;
-            const long long mine = !fits ? 0 : whole ? u * (runs_of(pages, per) * per) : u * pages;
-            long long at = mine;
-            for (int o = 1; o < 64; o <<= 1) {
-                const long long y = __shfl_up(at, o, 64);
-                if (lane >= o) at += y;
+                const long long y = __shfl_up(run, o, 64), z = __shfl_up(at, o, 64);
+                if (lane >= o) { run += y; at += z; }
             }
             if (g < G) {
-                s[g].unit0 = fits ? (int)(units + run - u) : -1;
+                s[g].unit0 = (int)(units + run - u);
                 s[g].pos0 = pos + at - mine;
             }
             units += __shfl(run, 63, 64);
@@ -247,23 +260,14 @@ __global__ __launch_bounds__(kPlanThreads) void attn_shared_plan_kernel(SharedPa
         }
     }
     __syncthreads();
-    auto planned = [&](int g) {
-        Group x;
-        x.first = s[g].first;
-        x.rows = max(s[g + 1].first - s[g].first, 0) * rep;
-        x.pages = s[g].unit0 < 0 ? 0 : pages_of(g);
-        x.pg0 = x.pages > 0 ? first_page(g) : 0;
-        x.unit0 = max(s[g].unit0, 0);
-        // (a group that did not fit is read by its sequences)
-        x.shared = s[g].unit0 < 0 && pages_of(g) > 0 ? 0 : s[g].shared;
-        x.pos0 = s[g].pos0;
-        return x;
+    auto group = [&](int g) {
+        return planned(s[g].first, (s[g + 1].first - s[g].first) * rep, pages_of(g), s[g].lo, s[g].shared, s[g].unit0, s[g].pos0);
     };
-    for (int g = tid; g < G; g += kPlanThreads) reinterpret_cast<Group*>(p.plan_groups)[g] = planned(g);
+    for (int g = tid; g < G; g += kPlanThreads) reinterpret_cast<Group*>(p.plan_groups)[g] = group(g);
     // (each sequence its group's, so that nobody has to look up which one that is)
     for (int n = tid; n < p.N; n += kPlanThreads) {
         const int g = group_of(n);
-        reinterpret_cast<Group*>(p.plan_sequences)[n] = g >= 0 ? planned(g) : Group{0, 0, 0, 0, 0, 0, 0};
+        reinterpret_cast<Group*>(p.plan_sequences)[n] = g >= 0 ? group(g) : Group{0, 0, 0, 0, 0, 0, 0};
     }
     for (int w = tid; w < s_workgroups; w += kPlanThreads) { // the last group that starts at or before this one's run
         int g = 0, z = G - 1;
@@ -280,6 +284,100 @@ __global__ __launch_bounds__(kPlanThreads) void attn_shared_plan_kernel(SharedPa
         head->whole = s_whole;
         head->per = s_per;
     }
+}
+
+// The same in each workgroup for itself, a group a lane, where there are few groups and
+// sequences: a plan kernel takes 5.5 to 9 us before the others start.  (4 sequences behind 300
+// tokens 16.0 us a call, with a plan kernel 20.6; 16 groups of 4 37.8 and 42.6; 64 of 16 51.6 and
+// 55.6.  Not with 64 rows a wave: the registers of the products have no room left, and scratch
+// memory in the pages' loop costs more than the plan.)
+constexpr int kFewGroups = 64, kFewSequences = 1024;
+struct LanePlan {
+    PlanHead head;
+    Group group;                // lane g's: group g
+    int end;                    // one past the last group's last sequence
+};
+struct LaneScratch {
+    int first[kFewGroups], lo[kFewGroups], hi[kFewGroups], fits[16];
+};
+// first sequence of lane g's group, as the plan kernel has it, and its end in `next`
+__device__ __forceinline__ int lane_bounds(const SharedParams& p, int lane, int& next) {
+    const int G = p.groups;
+    int first = lane < G ? clampi(p.group_start[lane], 0, p.N) : 0, end = clampi(p.group_start[G], 0, p.N);
+    for (int o = 1; o < 64; o <<= 1) {
+        const int y = __shfl_up(first, o, 64);
+        if (lane >= o) first = max(first, y);
+    }
+    end = max(end, __shfl(first, 63, 64));
+    next = __shfl_down(first, 1, 64);
+    if (lane >= G - 1) next = end;
+    return first;
+}
+template <int THREADS>
+__device__ __forceinline__ LanePlan lane_plan(const SharedParams& p, char* smem) {
+    LaneScratch& s = *reinterpret_cast<LaneScratch*>(smem);
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));                     // (what follows from it is not kept between two plans)
+    const int lane = tid & 63, rep = p.Hq / p.Hkv, G = p.groups;
+    int next;
+    const int shared = lane < G ? clampi(p.shared_pages[lane], 0, p.max_pages) : 0;
+    const int first = lane_bounds(p, lane, next), end = __shfl(next, 63, 64);
+    if (tid < 64) { s.first[lane] = first; s.lo[lane] = INT_MAX; s.hi[lane] = 0; }
+    __syncthreads();
+    for (int n = tid; n < p.N; n += THREADS) {
+        int a, b;
+        seen_range(p, n, a, b);
+        int g = 0, z = G - 1;                         // the last start at or before n
+        while (g < z) {
+            const int mid = (g + z + 1) / 2;
+            if (s.first[mid] <= n) g = mid;
+            else z = mid - 1;
+        }
+        if (a < b && n >= s.first[g] && n < (g + 1 < G ? s.first[g + 1] : end)) {
+            atomicMin(&s.lo[g], a);
+            atomicMax(&s.hi[g], b);
+        }
+    }
+    __syncthreads();
+    const int lo = s.lo[lane], pages = lane < G ? pages_seen(lo, s.hi[lane], shared) : 0, rows = lane < G ? (next - first) * rep : 0;
+    const int u = pages > 0 ? tiles_of_rows(p, rows) * p.Hkv : 0;
+    long long all = (long long)u * pages;
+    for (int o = 32; o > 0; o >>= 1) all += __shfl_xor(all, o, 64);
+    long long per = max(div_of(all + p.workgroups - 1, p.workgroups), 2LL * kWaves);
+    for (int i = tid >> 6; i <= kLonger; i += THREADS / 64) {
+        int runs = pages > 0 ? (int)min((long long)u * runs_of(pages, per + i), 1LL << 20) : 0;
+        for (int o = 32; o > 0; o >>= 1) runs += __shfl_xor(runs, o, 64);
+        if (lane == 0) s.fits[i] = runs <= p.workgroups;
+    }
+    __syncthreads();
+    bool whole = false;
+    for (int i = 0; i <= kLonger && !whole; ++i)
+        if (s.fits[i]) {
+            whole = true;
+            per += i;
+        }
+    const long long mine = whole ? u * (runs_of(pages, per) * per) : (long long)u * pages;
+    long long at = mine;
+    int run = u;
+    for (int o = 1; o < 64; o <<= 1) {
+        const int y = __shfl_up(run, o, 64);
+        const long long z = __shfl_up(at, o, 64);
+        if (lane >= o) { run += y; at += z; }
+    }
+    LanePlan x;
+    x.head.workgroups = (int)div_of(__shfl(at, 63, 64) + per - 1, per);
+    x.head.whole = whole;
+    x.head.per = per;
+    x.group = planned(first, rows, pages, lo, shared, run - u, at - mine);
+    x.end = end;
+    __syncthreads();                                  // (the scratch is free)
+    return x;
+}
+__device__ __forceinline__ Group group_of_lane(const Group& x, int g) {
+    auto get = [&](int v) { return __builtin_amdgcn_readlane(v, g); };
+    const uint32_t lo = (uint32_t)get((int)(uint32_t)x.pos0), hi = (uint32_t)get((int)(uint32_t)(x.pos0 >> 32));
+    return Group{get(x.first), get(x.rows), get(x.pg0), get(x.pages), get(x.unit0), get(x.shared),
+                 (long long)((uint64_t)lo | (uint64_t)hi << 32)};
 }
 
 // ---------------------------------------------------------------------------
@@ -381,7 +479,7 @@ template <int N> __device__ __forceinline__ void wait_but() { asm volatile("s_wa
 // products (as attn_decode_kernel has them).  A wave has a run of the pages of one, and
 // loads each page while it works on the one before: a few pages a sequence are too few
 // to be dealt to four waves, whose starts and joins took as long as the pages.
-template <int D, int PARTS>
+template <int D, int PARTS, bool FEW>
 __device__ __forceinline__ void own_pages(const SharedParams& p, int w, uint32_t place, int lane) {
     constexpr int KS = D / 64;                        // 64-channel steps of a key row
     constexpr int VT = D / 16;                        // 16-channel tiles of the output
@@ -391,9 +489,18 @@ __device__ __forceinline__ void own_pages(const SharedParams& p, int w, uint32_t
     const int kh = w % p.Hkv; w /= p.Hkv;
     const int n = w % p.N, run = w / p.N;
     const int q0 = kh * rep + 16 * qg, nq = min(16, rep - 16 * qg);
-    const Group x = group_at(p.plan_sequences, n);
+    int shared;
+    if constexpr (FEW) {
+        const int pages = lane < p.groups ? clampi(p.shared_pages[lane], 0, p.max_pages) : 0;
+        int next;
+        const int first = lane_bounds(p, lane, next);
+        const uint64_t in = __ballot(lane < p.groups && first <= n && n < next);
+        shared = in ? __builtin_amdgcn_readlane(pages, __builtin_ctzll(in)) : 0;
+    } else {
+        shared = group_at(p.plan_sequences, n).shared;
+    }
     int lo, hi;
-    const OwnPages mine = own_pages_of(p, n, x.shared, lo, hi);
+    const OwnPages mine = own_pages_of(p, n, shared, lo, hi);
     const long long begin = mine.begin + (long long)run * mine.per;
     if (begin >= mine.end) return;                    // (the join does not read it)
     const int pg0 = __builtin_amdgcn_readfirstlane((int)begin), pg1 = __builtin_amdgcn_readfirstlane(min((int)begin + mine.per, mine.end));
@@ -542,7 +649,7 @@ __device__ __forceinline__ void own_pages(const SharedParams& p, int w, uint32_t
     if (g == 0) *reinterpret_cast<float2*>(&p.own_ml[(run * heads + head) * 2]) = make_float2(m, l);
 }
 
-template <int D, int PARTS, int NB>
+template <int D, int PARTS, int NB, bool FEW>
 __global__ __launch_bounds__(64 * kWaves, 2) void attn_shared_kernel(SharedParams p) {
     constexpr int KL = D / 32;                        // 16-byte reads of a key's row by a lane
     constexpr int DB = D / 32;                        // 32-channel tiles of the output
@@ -568,16 +675,50 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_shared_kernel(SharedParam
     }
     if (own) {
         const long long w = (long long)(8 * number + blockIdx.x % 8) * kWaves + wave;
-        if (w < p.own_runs) own_pages<D, PARTS>(p, (int)w, attn::lds_address(sm.page[wave]), threadIdx.x & 63);
+        if (w < p.own_runs) own_pages<D, PARTS, FEW>(p, (int)w, attn::lds_address(sm.page[wave]), threadIdx.x & 63);
         return;
     }
     // consecutive workgroups go round the 8 XCDs: each of these takes a run of them, the
     // tiles that share pages one after the other
-    const PlanHead head = plan_head(p);
-    const int each = (head.workgroups + 7) / 8, wg = (blockIdx.x % 8) * each + number;
-    if (number >= each || wg >= head.workgroups) return;
-    int group = p.plan_items[wg];
-    Group x = group_at(p.plan_groups, group);
+    PlanHead head;
+    int wg, group;
+    Group x;
+    if constexpr (FEW) {
+        const LanePlan plan = lane_plan<64 * kWaves>(p, smem);
+        head = plan.head;
+        if (blockIdx.x == 0) {
+            // for the join
+            if (threadIdx.x == 0) *reinterpret_cast<PlanHead*>(p.plan_head) = head;
+            for (int n0 = 0; n0 < p.N; n0 += 64 * kWaves) {
+                const int n = n0 + threadIdx.x;
+                int g = -1;
+                for (int i = 0; i < p.groups; ++i) {
+                    const int first = __builtin_amdgcn_readlane(plan.group.first, i);
+                    const int end = i + 1 < p.groups ? __builtin_amdgcn_readlane(plan.group.first, i + 1) : plan.end;
+                    if (n >= first && n < end) g = i;
+                }
+                auto get = [&](int v) { return __shfl(v, max(g, 0), 64); };
+                const int pos_lo = get((int)(uint32_t)plan.group.pos0), pos_hi = get((int)(uint32_t)(plan.group.pos0 >> 32));
+                const Group y = {get(plan.group.first), get(plan.group.rows), get(plan.group.pg0), get(plan.group.pages), get(plan.group.unit0),
+                                 get(plan.group.shared), (long long)((uint64_t)(uint32_t)pos_lo | (uint64_t)(uint32_t)pos_hi << 32)};
+                if (n < p.N) reinterpret_cast<Group*>(p.plan_sequences)[n] = g >= 0 ? y : Group{0, 0, 0, 0, 0, 0, 0};
+            }
+        }
+        const int each = (head.workgroups + 7) / 8;
+        wg = (blockIdx.x % 8) * each + number;
+        if (number >= each || wg >= head.workgroups) return;
+        // the last group that starts at or before this run: it has pages
+        const int lane = threadIdx.x & 63;
+        group = 63 - __builtin_clzll(__ballot(lane < p.groups && plan.group.pos0 <= wg * head.per));
+        x = group_of_lane(plan.group, group);
+    } else {
+        head = plan_head(p);
+        const int each = (head.workgroups + 7) / 8;
+        wg = (blockIdx.x % 8) * each + number;
+        if (number >= each || wg >= head.workgroups) return;
+        group = p.plan_items[wg];
+        x = group_at(p.plan_groups, group);
+    }
     // the unit and its page that the run starts with, and the run's length
     long long left = head.per, length = length_of(head, x);
     int unit, page0;
@@ -929,10 +1070,21 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_shared_kernel(SharedParam
     page0 = 0;
     if (++unit == tiles * p.Hkv) {
         unit = 0;
-        do {
-            if (++group >= p.groups) return;
-            x = group_at(p.plan_groups, group);
-        } while (x.pages == 0);
+        if constexpr (FEW) {
+            // (made again: kept, the groups would take registers that the pages' products need)
+            const LanePlan plan = lane_plan<64 * kWaves>(p, smem);
+            int lane = threadIdx.x & 63;
+            asm volatile("" : "+v"(lane));
+            const uint64_t later = __ballot(lane < p.groups && lane > group && plan.group.pages > 0);
+            if (later == 0) return;
+            group = __builtin_ctzll(later);
+            x = group_of_lane(plan.group, group);
+        } else {
+            do {
+                if (++group >= p.groups) return;
+                x = group_at(p.plan_groups, group);
+            } while (x.pages == 0);
+        }
         length = length_of(head, x);
     }
     }
@@ -1034,6 +1186,7 @@ SharedPlan attn_shared_plan(int N, int groups, int Hq, int Hkv, int d, int max_p
     // costs a start and an end (16 groups of 4 on 63 pages 41.6, with two 44.6; 8 on 512
     // pages 28.2 and 31.3).
     x.workgroups = x.width == 64 ? 512 : 256;
+    x.few = x.width == 32 && groups <= kFewGroups && N <= kFewSequences;
     x.own_items = (long long)N * Hkv * ((rep + 15) / 16);
     int pages = max_pages;
     if (window > 0 && window / kPage + 2 < pages) pages = window / kPage + 2;
@@ -1071,18 +1224,20 @@ long long attn_shared_workgroups(const SharedPlan& x, long long heads) {
 // One wave a head in the join where there are many, else four: 8,160 heads 9.1 us, with four 19.9;
 // 2,048: 4.6 and 6.2; 1,024 of some 30 parts: 7.6 and 6.4; 256 of some 70: 9.6 and 5.1.
 constexpr long long kHeadsOfWaves = 2048;
-template <int D, int PARTS, int NB> static hipError_t launch_shared(const SharedParams& p, hipStream_t st) {
+template <int D, int PARTS, int NB, bool FEW> static hipError_t launch_shared(const SharedParams& p, hipStream_t st) {
     static std::atomic<unsigned long long> done{0};
     const int lds = (int)sizeof(SharedSmem<D, NB>);
-    const hipError_t e = ensure_dyn_lds(reinterpret_cast<const void*>(&attn_shared_kernel<D, PARTS, NB>), lds, done);
+    const hipError_t e = ensure_dyn_lds(reinterpret_cast<const void*>(&attn_shared_kernel<D, PARTS, NB, FEW>), lds, done);
     if (e != hipSuccess) return e;
     const long long own = (p.own_runs + 8 * kWaves - 1) / (8 * kWaves);
-    hipLaunchKernelGGL((attn_shared_kernel<D, PARTS, NB>), dim3((unsigned)(p.workgroups + 8 * own)), dim3(64 * kWaves), lds, st, p);
+    hipLaunchKernelGGL((attn_shared_kernel<D, PARTS, NB, FEW>), dim3((unsigned)(p.workgroups + 8 * own)), dim3(64 * kWaves), lds, st, p);
     return hipGetLastError();
 }
 
 template <int D, int PARTS> static hipError_t launch_d(const SharedParams& p, hipStream_t st) {
-    const hipError_t e = p.width == 64 ? launch_shared<D, PARTS, 2>(p, st) : launch_shared<D, PARTS, 1>(p, st);
+    hipError_t e;
+    if (p.width == 64) e = launch_shared<D, PARTS, 2, false>(p, st);
+    else e = p.few ? launch_shared<D, PARTS, 1, true>(p, st) : launch_shared<D, PARTS, 1, false>(p, st);
     if (e != hipSuccess) return e;
     const long long heads = (long long)p.N * p.Hq;
     if (heads >= kHeadsOfWaves) hipLaunchKernelGGL((attn_shared_join<D, 64>), dim3((unsigned)heads), dim3(64), 0, st, p);
@@ -1091,12 +1246,14 @@ template <int D, int PARTS> static hipError_t launch_d(const SharedParams& p, hi
 }
 
 hipError_t launch_attn_shared(const SharedParams& p, hipStream_t st) {
-    static std::atomic<unsigned long long> done{0};
-    hipError_t e = ensure_dyn_lds(reinterpret_cast<const void*>(&attn_shared_plan_kernel), (kMostGroups + 1) * (int)sizeof(PlanGroup), done);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(attn_shared_plan_kernel, dim3(1), dim3(kPlanThreads), (unsigned)((p.groups + 1) * sizeof(PlanGroup)), st, p);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (!p.few) {
+        static std::atomic<unsigned long long> done{0};
+        hipError_t e = ensure_dyn_lds(reinterpret_cast<const void*>(&attn_shared_plan_kernel), (kMostGroups + 1) * (int)sizeof(PlanGroup), done);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(attn_shared_plan_kernel, dim3(1), dim3(kPlanThreads), (unsigned)((p.groups + 1) * sizeof(PlanGroup)), st, p);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
     const bool one = (p.flags & GDR_OUT_BF16) != 0;
     if (p.d == 64) return one ? launch_d<64, 1>(p, st) : launch_d<64, 2>(p, st);
     return one ? launch_d<128, 1>(p, st) : launch_d<128, 2>(p, st);

@@ -405,3 +405,60 @@ def test_a_neighbours_page_changes_no_bit(Hq, Hkv, d, out):
     for o in outs[1:]:
         assert torch.equal(o[0], outs[0][0])
         assert not torch.equal(o[1], outs[0][1])
+
+
+@pytest.mark.parametrize("groups", [1, 20, 64, 65, 150])
+@pytest.mark.parametrize("window", [0, 3000])
+def test_groups_of_uneven_length(groups, window):
+    """Workgroups' runs that end and start inside units of different groups, some of which share
+    nothing, have no sequence, or see nothing of what they share; as many groups as one wave plans
+    for, and more."""
+    d, n_pages, Hq, Hkv = 64, 9, 8, 4
+    g = torch.Generator().manual_seed(groups)
+    cache = gdr.kv_cache(n_pages, Hkv, d, device="cpu")
+    for x in (cache.k, cache.v):
+        x.copy_((torch.randn(x.shape, generator=g) * 60).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8))
+    for x in (cache.k_scale, cache.v_scale):
+        x.copy_(torch.pow(2.0, torch.randint(-8, -4, x.shape, generator=g).float()))
+    sizes = torch.randint(0, 4, (groups,), generator=g).tolist()
+    sizes[0] = 2
+    shared = [int(torch.randint(0, 250, (1,), generator=g)) * (i % 5 != 3) for i in range(groups)]
+    starts = [1] + (1 + torch.tensor(sizes).cumsum(0)).tolist()                  # the first and the last are in no group
+    N = starts[-1] + 1
+    lens = torch.randint(0, 260 * 64, (N,), generator=g).tolist()
+    table = torch.randint(0, n_pages, (N, 260), generator=g, dtype=torch.int32)
+    q = torch.randn((N, Hq, d), generator=g).to(BF16)
+    ints = [torch.as_tensor(x, dtype=torch.int32).cuda() for x in (table, lens, starts, shared)]
+    got = gen.attn_decode_shared(q.cuda(), gdr.KVCache(*[x.cuda() for x in cache]), *ints, window=window).cpu().to(F64)
+    some = sorted(set(list(range(0, N, max(1, N // 10))) + [N - 1]))
+    read = ref.shared_table(table, starts, shared)
+    want, tol = ref.shared_decode(q[some].to(F64), attn.Cache(*cache), read[some], [lens[n] for n in some], list(range(len(some) + 1)),
+                                  [0] * len(some), window)
+    off = (got[some] - want).abs()
+    assert bool((off <= tol).all()), float((off / tol.clamp_min(1e-300)).max())
+
+
+@pytest.mark.parametrize("groups", [3, 64, 65, 300])
+def test_bounds_in_no_order_stay_inside(groups):
+    """Any numbers as bounds: every sequence has some result of its own rows, nothing else is
+    touched, and a call with bounds in order behind it is right."""
+    d, N = 64, 40
+    g = torch.Generator().manual_seed(groups)
+    cache = gdr.kv_cache(5, 2, d)
+    for x in (cache.k, cache.v):
+        x.copy_(torch.randint(0, 100, x.shape, generator=g).to(torch.uint8))
+    for x in (cache.k_scale, cache.v_scale):
+        x.fill_(0.01)
+    table = torch.randint(0, 5, (N, 6), generator=g, dtype=torch.int32).cuda()
+    lens = torch.randint(0, 6 * 64, (N,), generator=g).int().cuda()
+    q = torch.randn((N, 4, d), generator=g).to(BF16).cuda()
+    for high in (N, 10 ** 9):
+        starts = torch.randint(-high, high, (groups + 1,), generator=g).int().cuda()
+        shared = torch.randint(-3, 9, (groups,), generator=g).int().cuda()
+        room = torch.full((N + 2, 4, d), 7.0, device="cuda")
+        gen.attn_decode_shared(q, cache, table, lens, starts, shared, o=room[1:-1])
+        assert bool((room[0] == 7).all()) and bool((room[-1] == 7).all())
+    starts = torch.zeros(groups + 1, dtype=torch.int32, device="cuda")
+    alone = gen.attn_decode_shared(q, cache, table, lens, starts, shared)
+    want, tol = ref.shared_decode(q.cpu().to(F64), attn.Cache(*cache), table.cpu(), lens.tolist(), list(range(N + 1)), [0] * N)
+    assert bool(((alone.cpu().to(F64) - want).abs() <= tol).all())
