@@ -728,365 +728,365 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_shared_kernel(SharedParam
         page0 = (int)(rel - unit * length);
     }
     for (;;) {
-    int lane = threadIdx.x & 63;
-    asm volatile("" : "+v"(lane));                    // (what follows from it is not kept over the units)
-    const int col = lane & 31, h = lane >> 5;
-    const int tiles = (x.rows + kRows - 1) / kRows, tile = unit % tiles, kh = __builtin_amdgcn_readfirstlane(unit / tiles);
-    const int row0 = kRows * tile, rows = min(kRows, x.rows - row0);
-    const int pg0 = __builtin_amdgcn_readfirstlane(x.pg0 + page0);
-    const int pg1 = __builtin_amdgcn_readfirstlane((int)min((long long)pg0 + left, (long long)x.pg0 + x.pages));
-    const size_t part0 = (size_t)(x.unit0 + unit + wg) * kRows;
-    const int n = max(0, (pg1 - pg0 - wave + kWaves - 1) / kWaves);      // pages of this wave
+        int lane = threadIdx.x & 63;
+        asm volatile("" : "+v"(lane));                    // (what follows from it is not kept over the units)
+        const int col = lane & 31, h = lane >> 5;
+        const int tiles = (x.rows + kRows - 1) / kRows, tile = unit % tiles, kh = __builtin_amdgcn_readfirstlane(unit / tiles);
+        const int row0 = kRows * tile, rows = min(kRows, x.rows - row0);
+        const int pg0 = __builtin_amdgcn_readfirstlane(x.pg0 + page0);
+        const int pg1 = __builtin_amdgcn_readfirstlane((int)min((long long)pg0 + left, (long long)x.pg0 + x.pages));
+        const size_t part0 = (size_t)(x.unit0 + unit + wg) * kRows;
+        const int n = max(0, (pg1 - pg0 - wave + kWaves - 1) / kWaves);      // pages of this wave
 
-    // this wave's pages k0 .. k0 + 63, one a lane: place (-1: absent) and scales
-    const int* entries = p.block_table + (size_t)x.first * p.max_pages + pg0 + wave;
-    int e_page;
-    float e_ks, e_vs;
-    auto look_up = [&](int k0) {
-        const int k = k0 + lane;
-        const int e = k < n ? entries[k * kWaves] : -1;
-        e_page = (unsigned)e < (unsigned)p.n_pages ? e : -1;
-        const size_t ph = (size_t)max(e_page, 0) * p.Hkv + kh;
-        e_ks = p.k_scale[ph];
-        e_vs = p.v_scale[ph];
-    };
-    const uint32_t place = attn::lds_address(sm.page[wave]);
-    constexpr uint32_t kSide = kPage * D;
-    // (an absent page is read as the first one: its bytes are masked)
-    auto page_at = [&](int k) { return ((size_t)max(__builtin_amdgcn_readlane(e_page, k & 63), 0) * p.Hkv + kh) * kSide; };
-    look_up(0);
-    if (n > 0) {
-        const PageLoader<D, false> loader(lane);
-        loader.keys((uint64_t)p.k_cache + page_at(0), place);
-        loader.values((uint64_t)p.v_cache + page_at(0), place + kSide);
-    }
-
-    // this lane's rows: their queries (channels 32 s + 16 h .. + 15) and the keys they see
-    int lo_most = 0, hi_least = INT_MAX, lo_least = INT_MAX, hi_most = 0;
-#pragma unroll
-    for (int c = 0; c < NB; ++c) {
-        const int mine = 32 * c + col;
-        const bool live = mine < rows;
-        const int seq = x.first + (row0 + mine) / rep, head = kh * rep + (row0 + mine) % rep;
-        for (int s = wave; s < 2 * KL; s += kWaves) {
-            uint4 u = make_uint4(0, 0, 0, 0);
-            if (live)
-                u = *reinterpret_cast<const uint4*>((const uint16_t*)p.q + ((size_t)seq * p.Hq + head) * D + 32 * (s / 2) + 16 * h + 8 * (s % 2));
-            sm.q[2 * KL * c + s][lane] = u;
+        // this wave's pages k0 .. k0 + 63, one a lane: place (-1: absent) and scales
+        const int* entries = p.block_table + (size_t)x.first * p.max_pages + pg0 + wave;
+        int e_page;
+        float e_ks, e_vs;
+        auto look_up = [&](int k0) {
+            const int k = k0 + lane;
+            const int e = k < n ? entries[k * kWaves] : -1;
+            e_page = (unsigned)e < (unsigned)p.n_pages ? e : -1;
+            const size_t ph = (size_t)max(e_page, 0) * p.Hkv + kh;
+            e_ks = p.k_scale[ph];
+            e_vs = p.v_scale[ph];
+        };
+        const uint32_t place = attn::lds_address(sm.page[wave]);
+        constexpr uint32_t kSide = kPage * D;
+        // (an absent page is read as the first one: its bytes are masked)
+        auto page_at = [&](int k) { return ((size_t)max(__builtin_amdgcn_readlane(e_page, k & 63), 0) * p.Hkv + kh) * kSide; };
+        look_up(0);
+        if (n > 0) {
+            const PageLoader<D, false> loader(lane);
+            loader.keys((uint64_t)p.k_cache + page_at(0), place);
+            loader.values((uint64_t)p.v_cache + page_at(0), place + kSide);
         }
-        if (live) {
-            int lo, hi;
-            seen_range(p, seq, lo, hi);
-            lo_most = max(lo_most, lo);
-            lo_least = min(lo_least, lo);
-            hi_least = min(hi_least, hi);
-            hi_most = max(hi_most, hi);
+
+        // this lane's rows: their queries (channels 32 s + 16 h .. + 15) and the keys they see
+        int lo_most = 0, hi_least = INT_MAX, lo_least = INT_MAX, hi_most = 0;
+#pragma unroll
+        for (int c = 0; c < NB; ++c) {
+            const int mine = 32 * c + col;
+            const bool live = mine < rows;
+            const int seq = x.first + (row0 + mine) / rep, head = kh * rep + (row0 + mine) % rep;
+            for (int s = wave; s < 2 * KL; s += kWaves) {
+                uint4 u = make_uint4(0, 0, 0, 0);
+                if (live)
+                    u = *reinterpret_cast<const uint4*>((const uint16_t*)p.q + ((size_t)seq * p.Hq + head) * D + 32 * (s / 2) + 16 * h + 8 * (s % 2));
+                sm.q[2 * KL * c + s][lane] = u;
+            }
+            if (live) {
+                int lo, hi;
+                seen_range(p, seq, lo, hi);
+                lo_most = max(lo_most, lo);
+                lo_least = min(lo_least, lo);
+                hi_least = min(hi_least, hi);
+                hi_most = max(hi_most, hi);
+            }
         }
-    }
-    for (int o = 16; o > 0; o >>= 1) {
-        lo_most = max(lo_most, __shfl_xor(lo_most, o, 64));
-        hi_least = min(hi_least, __shfl_xor(hi_least, o, 64));
-        lo_least = min(lo_least, __shfl_xor(lo_least, o, 64));
-        hi_most = max(hi_most, __shfl_xor(hi_most, o, 64));
-    }
-    lo_most = __builtin_amdgcn_readfirstlane(lo_most);
-    hi_least = __builtin_amdgcn_readfirstlane(hi_least);
-    lo_least = __builtin_amdgcn_readfirstlane(lo_least);
-    hi_most = __builtin_amdgcn_readfirstlane(hi_most);
+        for (int o = 16; o > 0; o >>= 1) {
+            lo_most = max(lo_most, __shfl_xor(lo_most, o, 64));
+            hi_least = min(hi_least, __shfl_xor(hi_least, o, 64));
+            lo_least = min(lo_least, __shfl_xor(lo_least, o, 64));
+            hi_most = max(hi_most, __shfl_xor(hi_most, o, 64));
+        }
+        lo_most = __builtin_amdgcn_readfirstlane(lo_most);
+        hi_least = __builtin_amdgcn_readfirstlane(hi_least);
+        lo_least = __builtin_amdgcn_readfirstlane(lo_least);
+        hi_most = __builtin_amdgcn_readfirstlane(hi_most);
 
-    float16v o[NB][DB];
-    float m[NB], l[NB], wm[NB];                       // maximum and sum of the scores; maximum of the weights
+        float16v o[NB][DB];
+        float m[NB], l[NB], wm[NB];                       // maximum and sum of the scores; maximum of the weights
 #pragma unroll
-    for (int c = 0; c < NB; ++c) {
-        m[c] = -INFINITY; l[c] = 0.f; wm[c] = -INFINITY;
+        for (int c = 0; c < NB; ++c) {
+            m[c] = -INFINITY; l[c] = 0.f; wm[c] = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < DB; ++i)
+            for (int i = 0; i < DB; ++i)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) o[c][i][j] = 0.f;
-    }
-    const float to2 = p.scale * 1.4426950408889634f;
-    // (the pages' loads go on)
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                for (int j = 0; j < 16; ++j) o[c][i][j] = 0.f;
+        }
+        const float to2 = p.scale * 1.4426950408889634f;
+        // (the pages' loads go on)
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 
-    uint32_t nans = 0;                                // some value that not every row sees is NaN
-    for (int k = 0; k < n; ++k) {
-        const int page = __builtin_amdgcn_readlane(e_page, k & 63);
-        const float ks = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(e_ks), k & 63));
-        const float vs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(e_vs), k & 63));
-        const int at0 = (pg0 + wave + k * kWaves) * kPage;
-        const bool absent = page < 0;
-        // A lane's places are made anew for each page: kept over the loop some of them would be
-        // in scratch memory, and a wait for what is read from there is one for the page's
-        // loads as well.
-        int mine = lane;
-        asm volatile("" : "+v"(mine));
-        const PageLoader<D, false> loader(mine);
-        const int tok = 16 * ((mine >> 2) & 1) + 4 * ((mine & 31) >> 3) + (mine & 3);
-        const uint32_t k_at = place + tok * D + 16 * ((mine >> 5) ^ key_flip<D, false>(tok));   // its reads of keys, to flip by 32 s
-        const uint32_t v_at = place + kSide + ((mine >> 5) * D + (mine & 31)) * 16, q_at = attn::lds_address(sm.q) + 16 * mine;
-        // the keys are there: what was asked for behind them are values
-        wait_but<PageLoader<D, false>::N>();
-        float16v st[NB][2];
-#pragma unroll
-        for (int c = 0; c < NB; ++c)
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int j = 0; j < 16; ++j) st[c][b][j] = 0.f;
-#pragma unroll
-        for (int s = 0; s < KL; ++s) {
-            uint4v kr[2], qr[NB][2];
-#pragma unroll
-            for (int b = 0; b < 2; ++b) kr[b] = read16((k_at ^ (32 * s)) + 32 * b * D);
+        uint32_t nans = 0;                                // some value that not every row sees is NaN
+        for (int k = 0; k < n; ++k) {
+            const int page = __builtin_amdgcn_readlane(e_page, k & 63);
+            const float ks = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(e_ks), k & 63));
+            const float vs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(e_vs), k & 63));
+            const int at0 = (pg0 + wave + k * kWaves) * kPage;
+            const bool absent = page < 0;
+            // A lane's places are made anew for each page: kept over the loop some of them would be
+            // in scratch memory, and a wait for what is read from there is one for the page's
+            // loads as well.
+            int mine = lane;
+            asm volatile("" : "+v"(mine));
+            const PageLoader<D, false> loader(mine);
+            const int tok = 16 * ((mine >> 2) & 1) + 4 * ((mine & 31) >> 3) + (mine & 3);
+            const uint32_t k_at = place + tok * D + 16 * ((mine >> 5) ^ key_flip<D, false>(tok));   // its reads of keys, to flip by 32 s
+            const uint32_t v_at = place + kSide + ((mine >> 5) * D + (mine & 31)) * 16, q_at = attn::lds_address(sm.q) + 16 * mine;
+            // the keys are there: what was asked for behind them are values
+            wait_but<PageLoader<D, false>::N>();
+            float16v st[NB][2];
 #pragma unroll
             for (int c = 0; c < NB; ++c)
 #pragma unroll
-                for (int f = 0; f < 2; ++f) qr[c][f] = read16(q_at + 1024 * (2 * KL * c + 2 * s + f));
+                for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const bf8v k0 = e4m3x8_to_bf16(kr[b].x, kr[b].y), k1 = e4m3x8_to_bf16(kr[b].z, kr[b].w);
+                    for (int j = 0; j < 16; ++j) st[c][b][j] = 0.f;
 #pragma unroll
-                for (int c = 0; c < NB; ++c) st[c][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k0, __builtin_bit_cast(bf8v, qr[c][0]), st[c][b], 0, 0, 0);
+            for (int s = 0; s < KL; ++s) {
+                uint4v kr[2], qr[NB][2];
 #pragma unroll
-                for (int c = 0; c < NB; ++c) st[c][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k1, __builtin_bit_cast(bf8v, qr[c][1]), st[c][b], 0, 0, 0);
-            }
-        }
-        // the keys are read: the next page's take their place while these values are worked on
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        if (k + 1 < n) {
-            if (((k + 1) & 63) == 0) look_up(k + 1);
-            loader.keys((uint64_t)p.k_cache + page_at(k + 1), place);
-        }
-        // (the values are older than these, where there are any)
-        auto wait_values = [&] {
-            if (k + 1 < n) wait_but<PageLoader<D, false>::N>();
-            else wait_but<0>();
-        };
-
-        float by = ks * to2;                          // a score is st times this
-        const bool edge = absent || at0 < lo_most || at0 + kPage > hi_least;
-        if (edge || !(by >= 0.f)) {
-            // (negative scales turn the order of the scores; masked ones stay -inf whatever the scale)
-            asm volatile("");
+                for (int b = 0; b < 2; ++b) kr[b] = read16((k_at ^ (32 * s)) + 32 * b * D);
 #pragma unroll
-            for (int c = 0; c < NB; ++c) {
-                uint32_t sees = 0;                    // (looked up again: few pages are read in part)
-                if (edge && !absent && 32 * c + col < rows) {
-                    int lo, hi;
-                    seen_range(p, x.first + (row0 + 32 * c + col) / rep, lo, hi);
-                    sees = seen_bits(at0 + 16 * h, lo, hi);
-                }
+                for (int c = 0; c < NB; ++c)
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) qr[c][f] = read16(q_at + 1024 * (2 * KL * c + 2 * s + f));
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    st[c][b] *= by;
-                    if (edge) {
+                    const bf8v k0 = e4m3x8_to_bf16(kr[b].x, kr[b].y), k1 = e4m3x8_to_bf16(kr[b].z, kr[b].w);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) st[c][b][i] = sees >> (16 * b + i) & 1 ? st[c][b][i] : -INFINITY;
-                    }
+                    for (int c = 0; c < NB; ++c) st[c][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k0, __builtin_bit_cast(bf8v, qr[c][0]), st[c][b], 0, 0, 0);
+#pragma unroll
+                    for (int c = 0; c < NB; ++c) st[c][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k1, __builtin_bit_cast(bf8v, qr[c][1]), st[c][b], 0, 0, 0);
                 }
             }
-            by = 1.f;
-            if (edge) {
-                // some row sees the page in part: values of keys that no row sees count as 0,
-                // and so do NaNs, which the 0 of a row that does not see them would carry
-                // over: the rows that see them get them at the end
-                // (in LDS: a lane writes what it will read)
-                const uint32_t some = absent ? 0 : seen_bits(at0 + 16 * h, lo_least, hi_most);
-                wait_values();
-                for (int i = 0; i < 2 * DB; ++i) {
-                    const int b = i & 1;
-                    const uint32_t at = v_at + (2 * b * D + 16 * (i & ~1)) * 16;
-                    uint4v u = read16(at);
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const uint32_t y = u[t] & bytes_of(some, 16 * b + 4 * t);
-                        const uint32_t whole = (nan_bytes(y) >> 7) * 0xffu;
-                        nans |= whole;
-                        u[t] = y & ~whole;
-                    }
-                    *(__attribute__((address_space(3))) uint4v*)(uintptr_t)at = u;
-                }
-                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            // the keys are read: the next page's take their place while these values are worked on
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            if (k + 1 < n) {
+                if (((k + 1) & 63) == 0) look_up(k + 1);
+                loader.keys((uint64_t)p.k_cache + page_at(k + 1), place);
             }
-        }
+            // (the values are older than these, where there are any)
+            auto wait_values = [&] {
+                if (k + 1 < n) wait_but<PageLoader<D, false>::N>();
+                else wait_but<0>();
+            };
 
-        // The maxima are followed when they are more than 2^kLag ahead, each row's by itself
-        // (the roundings of a row do not depend on keys that only its neighbours see): in
-        // most pages some row of 32 has a new one, and o would be scaled anew.
-        const float log_vs = __builtin_amdgcn_logf(vs);   // base 2
-        float top[NB];
-        bool none[NB], ahead_m[NB], ahead_w[NB], any = false;
+            float by = ks * to2;                          // a score is st times this
+            const bool edge = absent || at0 < lo_most || at0 + kPage > hi_least;
+            if (edge || !(by >= 0.f)) {
+                // (negative scales turn the order of the scores; masked ones stay -inf whatever the scale)
+                asm volatile("");
 #pragma unroll
-        for (int c = 0; c < NB; ++c) {
-            top[c] = st[c][0][0];
+                for (int c = 0; c < NB; ++c) {
+                    uint32_t sees = 0;                    // (looked up again: few pages are read in part)
+                    if (edge && !absent && 32 * c + col < rows) {
+                        int lo, hi;
+                        seen_range(p, x.first + (row0 + 32 * c + col) / rep, lo, hi);
+                        sees = seen_bits(at0 + 16 * h, lo, hi);
+                    }
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+                    for (int b = 0; b < 2; ++b) {
+                        st[c][b] *= by;
+                        if (edge) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) top[c] = fmaxf(top[c], st[c][b][i]);
-            top[c] = max_across32(top[c]);
-            none[c] = !(top[c] > -INFINITY);          // (the scale of a page that a row does not see does not reach it)
-            top[c] = none[c] ? -INFINITY : top[c] * by;
-            ahead_m[c] = top[c] > m[c] + kLag;
-            ahead_w[c] = !none[c] && top[c] + log_vs > wm[c] + kLag;
-            any = any || ahead_m[c] || ahead_w[c];
-        }
-        if (__any(any)) {
-            asm volatile("");
+                            for (int i = 0; i < 16; ++i) st[c][b][i] = sees >> (16 * b + i) & 1 ? st[c][b][i] : -INFINITY;
+                        }
+                    }
+                }
+                by = 1.f;
+                if (edge) {
+                    // some row sees the page in part: values of keys that no row sees count as 0,
+                    // and so do NaNs, which the 0 of a row that does not see them would carry
+                    // over: the rows that see them get them at the end
+                    // (in LDS: a lane writes what it will read)
+                    const uint32_t some = absent ? 0 : seen_bits(at0 + 16 * h, lo_least, hi_most);
+                    wait_values();
+                    for (int i = 0; i < 2 * DB; ++i) {
+                        const int b = i & 1;
+                        const uint32_t at = v_at + (2 * b * D + 16 * (i & ~1)) * 16;
+                        uint4v u = read16(at);
 #pragma unroll
-            for (int c = 0; c < NB; ++c) {
-                const float fade = ahead_w[c] ? __builtin_amdgcn_exp2f(wm[c] - (top[c] + log_vs)) : 1.f;
-                l[c] *= ahead_m[c] ? __builtin_amdgcn_exp2f(m[c] - top[c]) : 1.f;      // 0 from -inf
-                m[c] = ahead_m[c] ? top[c] : m[c];
-                wm[c] = ahead_w[c] ? top[c] + log_vs : wm[c];
-#pragma unroll
-                for (int i = 0; i < DB; ++i) o[c][i] *= fade;
+                        for (int t = 0; t < 4; ++t) {
+                            const uint32_t y = u[t] & bytes_of(some, 16 * b + 4 * t);
+                            const uint32_t whole = (nan_bytes(y) >> 7) * 0xffu;
+                            nans |= whole;
+                            u[t] = y & ~whole;
+                        }
+                        *(__attribute__((address_space(3))) uint4v*)(uintptr_t)at = u;
+                    }
+                    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                }
             }
-        }
-        float up[NB], share[NB];                      // a weight's exponent over its score's; its part in the sum
-        bool far[NB], some_far = false;
-#pragma unroll
-        for (int c = 0; c < NB; ++c) {
-            const float at = m[c] == -INFINITY ? 0.f : m[c], wat = wm[c] == -INFINITY ? 0.f : wm[c];
-            up[c] = none[c] ? 0.f : log_vs - wat + kTop;
-            share[c] = none[c] ? 0.f : __builtin_amdgcn_exp2f(-(up[c] + at));
-            far[c] = !none[c] && !(fabsf(up[c] + at) <= 60.f);
-            some_far = some_far || far[c];
-        }
-        if (__any(some_far)) {
-            // the sum's own exponentials, for the rows that need them
+
+            // The maxima are followed when they are more than 2^kLag ahead, each row's by itself
+            // (the roundings of a row do not depend on keys that only its neighbours see): in
+            // most pages some row of 32 has a new one, and o would be scaled anew.
+            const float log_vs = __builtin_amdgcn_logf(vs);   // base 2
+            float top[NB];
+            bool none[NB], ahead_m[NB], ahead_w[NB], any = false;
 #pragma unroll
             for (int c = 0; c < NB; ++c) {
-                const float at = m[c] == -INFINITY ? 0.f : m[c];
-                float sum = 0.f;
+                top[c] = st[c][0][0];
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        sum += __builtin_amdgcn_exp2f(__builtin_fmaf(st[c][b][i], by, -at));
-                        asm volatile("" : "+v"(sum));     // (one after the other: no registers for it)
-                    }
-                l[c] += far[c] ? sum : 0.f;
-                share[c] = far[c] ? 0.f : share[c];
+                    for (int i = 0; i < 16; ++i) top[c] = fmaxf(top[c], st[c][b][i]);
+                top[c] = max_across32(top[c]);
+                none[c] = !(top[c] > -INFINITY);          // (the scale of a page that a row does not see does not reach it)
+                top[c] = none[c] ? -INFINITY : top[c] * by;
+                ahead_m[c] = top[c] > m[c] + kLag;
+                ahead_w[c] = !none[c] && top[c] + log_vs > wm[c] + kLag;
+                any = any || ahead_m[c] || ahead_w[c];
             }
-        }
-
-        wait_values();
-        // (with two parts a weight, the weights of 32 keys do not fit into the registers: 16 at a
-        // time then, 233 us for 247 of 256 sequences behind 3 prompts; with one part, 111 for 101)
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int f0 = 0; f0 < 2; f0 += 3 - PARTS) {
-                half8 w_hi[NB][3 - PARTS], w_lo[NB];
+            if (__any(any)) {
+                asm volatile("");
 #pragma unroll
                 for (int c = 0; c < NB; ++c) {
-                    float sum[2] = {0.f, 0.f};
+                    const float fade = ahead_w[c] ? __builtin_amdgcn_exp2f(wm[c] - (top[c] + log_vs)) : 1.f;
+                    l[c] *= ahead_m[c] ? __builtin_amdgcn_exp2f(m[c] - top[c]) : 1.f;      // 0 from -inf
+                    m[c] = ahead_m[c] ? top[c] : m[c];
+                    wm[c] = ahead_w[c] ? top[c] + log_vs : wm[c];
 #pragma unroll
-                    for (int i = 0; i < 8 * (3 - PARTS); ++i) {
-                        const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(st[c][b][8 * f0 + i], by, up[c]));
-                        sum[i & 1] += w;
-                        const _Float16 a = (_Float16)w;
-                        w_hi[c][i / 8][i % 8] = a;
-                        if (PARTS == 2) w_lo[c][i % 8] = (_Float16)(w - (float)a);
-                    }
-                    l[c] += (sum[0] + sum[1]) * share[c];
-                }
-#pragma unroll
-                for (int i = 0; i < DB; ++i) {
-                    const uint32_t at = v_at + (2 * b * D + 32 * i) * 16;
-                    if constexpr (PARTS == 2) {
-                        const uint2v u = read8(at + 8 * f0);
-                        const half8 v = e4m3x8_to_f16(u.x, u.y);
-#pragma unroll
-                        for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w_hi[c][0], o[c][i], 0, 0, 0);
-#pragma unroll
-                        for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w_lo[c], o[c][i], 0, 0, 0);
-                    } else {
-                        const uint4v u = read16(at);
-                        const half8 v0 = e4m3x8_to_f16(u.x, u.y), v1 = e4m3x8_to_f16(u.z, u.w);
-#pragma unroll
-                        for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v0, w_hi[c][0], o[c][i], 0, 0, 0);
-#pragma unroll
-                        for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v1, w_hi[c][2 - PARTS], o[c][i], 0, 0, 0);
-                    }
+                    for (int i = 0; i < DB; ++i) o[c][i] *= fade;
                 }
             }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        if (k + 1 < n) loader.values((uint64_t)p.v_cache + page_at(k + 1), place + kSide);
-    }
+            float up[NB], share[NB];                      // a weight's exponent over its score's; its part in the sum
+            bool far[NB], some_far = false;
+#pragma unroll
+            for (int c = 0; c < NB; ++c) {
+                const float at = m[c] == -INFINITY ? 0.f : m[c], wat = wm[c] == -INFINITY ? 0.f : wm[c];
+                up[c] = none[c] ? 0.f : log_vs - wat + kTop;
+                share[c] = none[c] ? 0.f : __builtin_amdgcn_exp2f(-(up[c] + at));
+                far[c] = !none[c] && !(fabsf(up[c] + at) <= 60.f);
+                some_far = some_far || far[c];
+            }
+            if (__any(some_far)) {
+                // the sum's own exponentials, for the rows that need them
+#pragma unroll
+                for (int c = 0; c < NB; ++c) {
+                    const float at = m[c] == -INFINITY ? 0.f : m[c];
+                    float sum = 0.f;
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            sum += __builtin_amdgcn_exp2f(__builtin_fmaf(st[c][b][i], by, -at));
+                            asm volatile("" : "+v"(sum));     // (one after the other: no registers for it)
+                        }
+                    l[c] += far[c] ? sum : 0.f;
+                    share[c] = far[c] ? 0.f : share[c];
+                }
+            }
 
-    // the waves that had the same rows join, in LDS, 32 rows at a time: no load into it is
-    // left, and no read of the ring
-    attn::wait_loads();
+            wait_values();
+            // (with two parts a weight, the weights of 32 keys do not fit into the registers: 16 at a
+            // time then, 233 us for 247 of 256 sequences behind 3 prompts; with one part, 111 for 101)
 #pragma unroll
-    for (int c = 0; c < NB; ++c) {
-        lds_barrier();
-        l[c] = sum_across32(l[c]);
-        if (h == 0) { sm.ml[wave][col][0] = m[c]; sm.ml[wave][col][1] = l[c]; }
-        if (c == 0) sm.nans[wave] = __any(nans != 0);
-        const float down = m[c] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(wm[c] - m[c] - kTop);   // to the scores' maximum
+            for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int i = 0; i < DB; ++i)
+                for (int f0 = 0; f0 < 2; f0 += 3 - PARTS) {
+                    half8 w_hi[NB][3 - PARTS], w_lo[NB];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float4v y;
+                    for (int c = 0; c < NB; ++c) {
+                        float sum[2] = {0.f, 0.f};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) y[k] = o[c][i][4 * j + k] * down;
-                *reinterpret_cast<float4v*>(&sm.o[wave][col][32 * i + 8 * j + 4 * h]) = y;
-            }
-        lds_barrier();
-        // all their lanes together
-        const size_t part = part0 + 32 * c;
-        join_waves<D>(sm.o, sm.ml, min(32, rows - 32 * c), [&](int r, int ch, float4v y, float2 ml) {
-            *reinterpret_cast<float4v*>(&p.part_o[(part + r) * D + ch]) = y;
-            if (ch == 0) *reinterpret_cast<float2*>(&p.part_ml[(part + r) * 2]) = ml;
-        });
-    }
-    int any_nans = 0;
+                        for (int i = 0; i < 8 * (3 - PARTS); ++i) {
+                            const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(st[c][b][8 * f0 + i], by, up[c]));
+                            sum[i & 1] += w;
+                            const _Float16 a = (_Float16)w;
+                            w_hi[c][i / 8][i % 8] = a;
+                            if (PARTS == 2) w_lo[c][i % 8] = (_Float16)(w - (float)a);
+                        }
+                        l[c] += (sum[0] + sum[1]) * share[c];
+                    }
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) any_nans |= sm.nans[w];
-    __syncthreads();                                  // (LDS is free again, what was joined is written)
-    if (any_nans) {
-    // NaNs among values that not every row sees: into the rows that see them, one by one
-    __threadfence_block();
-    for (int pg = pg0; pg < pg1; ++pg) {
-        const int page = p.block_table[(size_t)x.first * p.max_pages + pg];
-        if ((unsigned)page >= (unsigned)p.n_pages) continue;
-        const uint8_t* values = p.v_cache + ((size_t)page * p.Hkv + kh) * (kPage * D);
-        for (int i = threadIdx.x; i < kPage * D; i += 64 * kWaves) {
-            if ((values[i] & 0x7f) != 0x7f) continue;
-            const int j = pg * kPage + 16 * (i / (16 * D)) + i % 16, ch = i / 16 % D;
-            for (int r = 0; r < rows; ++r) {
-                int a, b;
-                seen_range(p, x.first + (row0 + r) / rep, a, b);
-                if (j >= a && j < b) p.part_o[(part0 + r) * D + ch] = NAN;
+                    for (int i = 0; i < DB; ++i) {
+                        const uint32_t at = v_at + (2 * b * D + 32 * i) * 16;
+                        if constexpr (PARTS == 2) {
+                            const uint2v u = read8(at + 8 * f0);
+                            const half8 v = e4m3x8_to_f16(u.x, u.y);
+#pragma unroll
+                            for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w_hi[c][0], o[c][i], 0, 0, 0);
+#pragma unroll
+                            for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w_lo[c], o[c][i], 0, 0, 0);
+                        } else {
+                            const uint4v u = read16(at);
+                            const half8 v0 = e4m3x8_to_f16(u.x, u.y), v1 = e4m3x8_to_f16(u.z, u.w);
+#pragma unroll
+                            for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v0, w_hi[c][0], o[c][i], 0, 0, 0);
+#pragma unroll
+                            for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v1, w_hi[c][2 - PARTS], o[c][i], 0, 0, 0);
+                        }
+                    }
+                }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            if (k + 1 < n) loader.values((uint64_t)p.v_cache + page_at(k + 1), place + kSide);
+        }
+
+        // the waves that had the same rows join, in LDS, 32 rows at a time: no load into it is
+        // left, and no read of the ring
+        attn::wait_loads();
+#pragma unroll
+        for (int c = 0; c < NB; ++c) {
+            lds_barrier();
+            l[c] = sum_across32(l[c]);
+            if (h == 0) { sm.ml[wave][col][0] = m[c]; sm.ml[wave][col][1] = l[c]; }
+            if (c == 0) sm.nans[wave] = __any(nans != 0);
+            const float down = m[c] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(wm[c] - m[c] - kTop);   // to the scores' maximum
+#pragma unroll
+            for (int i = 0; i < DB; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float4v y;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) y[k] = o[c][i][4 * j + k] * down;
+                    *reinterpret_cast<float4v*>(&sm.o[wave][col][32 * i + 8 * j + 4 * h]) = y;
+                }
+            lds_barrier();
+            // all their lanes together
+            const size_t part = part0 + 32 * c;
+            join_waves<D>(sm.o, sm.ml, min(32, rows - 32 * c), [&](int r, int ch, float4v y, float2 ml) {
+                *reinterpret_cast<float4v*>(&p.part_o[(part + r) * D + ch]) = y;
+                if (ch == 0) *reinterpret_cast<float2*>(&p.part_ml[(part + r) * 2]) = ml;
+            });
+        }
+        int any_nans = 0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) any_nans |= sm.nans[w];
+        __syncthreads();                                  // (LDS is free again, what was joined is written)
+        if (any_nans) {
+            // NaNs among values that not every row sees: into the rows that see them, one by one
+            __threadfence_block();
+            for (int pg = pg0; pg < pg1; ++pg) {
+                const int page = p.block_table[(size_t)x.first * p.max_pages + pg];
+                if ((unsigned)page >= (unsigned)p.n_pages) continue;
+                const uint8_t* values = p.v_cache + ((size_t)page * p.Hkv + kh) * (kPage * D);
+                for (int i = threadIdx.x; i < kPage * D; i += 64 * kWaves) {
+                    if ((values[i] & 0x7f) != 0x7f) continue;
+                    const int j = pg * kPage + 16 * (i / (16 * D)) + i % 16, ch = i / 16 % D;
+                    for (int r = 0; r < rows; ++r) {
+                        int a, b;
+                        seen_range(p, x.first + (row0 + r) / rep, a, b);
+                        if (j >= a && j < b) p.part_o[(part0 + r) * D + ch] = NAN;
+                    }
+                }
             }
         }
-    }
-    }
-    // the next unit
-    left -= length - page0;
-    if (left <= 0) return;
-    page0 = 0;
-    if (++unit == tiles * p.Hkv) {
-        unit = 0;
-        if constexpr (FEW) {
-            // (made again: kept, the groups would take registers that the pages' products need)
-            const LanePlan plan = lane_plan<64 * kWaves>(p, smem);
-            int lane = threadIdx.x & 63;
-            asm volatile("" : "+v"(lane));
-            const uint64_t later = __ballot(lane < p.groups && lane > group && plan.group.pages > 0);
-            if (later == 0) return;
-            group = __builtin_ctzll(later);
-            x = group_of_lane(plan.group, group);
-        } else {
-            do {
-                if (++group >= p.groups) return;
-                x = group_at(p.plan_groups, group);
-            } while (x.pages == 0);
+        // the next unit
+        left -= length - page0;
+        if (left <= 0) return;
+        page0 = 0;
+        if (++unit == tiles * p.Hkv) {
+            unit = 0;
+            if constexpr (FEW) {
+                // (made again: kept, the groups would take registers that the pages' products need)
+                const LanePlan plan = lane_plan<64 * kWaves>(p, smem);
+                int lane = threadIdx.x & 63;
+                asm volatile("" : "+v"(lane));
+                const uint64_t later = __ballot(lane < p.groups && lane > group && plan.group.pages > 0);
+                if (later == 0) return;
+                group = __builtin_ctzll(later);
+                x = group_of_lane(plan.group, group);
+            } else {
+                do {
+                    if (++group >= p.groups) return;
+                    x = group_at(p.plan_groups, group);
+                } while (x.pages == 0);
+            }
+            length = length_of(head, x);
         }
-        length = length_of(head, x);
-    }
     }
 }
 
