@@ -153,6 +153,12 @@ struct PlanGroup {
 __device__ __forceinline__ int runs_of(int pages, long long per) {
     return pages <= per ? 1 : (int)(((uint32_t)pages + (uint32_t)per - 1) / (uint32_t)per);
 }
+// Workgroups that the pages of all units are dealt to: two a compute unit only where each has many
+// (128 rows on 512 pages 45 us, with two 51; 256 on 125 35.5 and 40.6; 512 on 256 63.6 and 65.8).
+constexpr int kShort = 64;
+__device__ __forceinline__ int workgroups_for(const SharedParams& p, long long all) {
+    return p.workgroups > 256 && all < (long long)p.workgroups * kShort ? 256 : p.workgroups;
+}
 // the pages that some sequence sees of a group's shared ones, whose tokens lo .. hi - 1 some see
 __device__ __forceinline__ int pages_seen(int lo, int hi, int shared) {
     return max(0, min((int)(((long long)hi + kPage - 1) / kPage), shared) - lo / kPage);
@@ -219,12 +225,13 @@ __global__ __launch_bounds__(kPlanThreads) void attn_shared_plan_kernel(SharedPa
     };
     // two pages a wave, as the second's keys are loaded beside the first one's work
     const long long all = sum_of([](int pages) { return (long long)pages; });
-    long long per = max(div_of(all + p.workgroups - 1, p.workgroups), 2LL * kWaves);
+    const int workgroups = workgroups_for(p, all);
+    long long per = max(div_of(all + workgroups - 1, workgroups), 2LL * kWaves);
     // a unit's start and end are worth some pages: whole runs of a unit where they are little
     // longer (each wave looks at another length)
     {
         const long long longer = per + (tid >> 6);
-        const bool fits = sum_of([&](int pages) { return pages > 0 ? runs_of(pages, longer) : 0; }) <= p.workgroups;
+        const bool fits = sum_of([&](int pages) { return pages > 0 ? runs_of(pages, longer) : 0; }) <= workgroups;
         if (lane == 0) s_fits[tid >> 6] = fits;
     }
     __syncthreads();
@@ -343,11 +350,12 @@ __device__ __forceinline__ LanePlan lane_plan(const SharedParams& p, char* smem)
     const int u = pages > 0 ? tiles_of_rows(p, rows) * p.Hkv : 0;
     long long all = (long long)u * pages;
     for (int o = 32; o > 0; o >>= 1) all += __shfl_xor(all, o, 64);
-    long long per = max(div_of(all + p.workgroups - 1, p.workgroups), 2LL * kWaves);
+    const int workgroups = workgroups_for(p, all);
+    long long per = max(div_of(all + workgroups - 1, workgroups), 2LL * kWaves);
     for (int i = tid >> 6; i <= kLonger; i += THREADS / 64) {
         int runs = pages > 0 ? (int)min((long long)u * runs_of(pages, per + i), 1LL << 20) : 0;
         for (int o = 32; o > 0; o >>= 1) runs += __shfl_xor(runs, o, 64);
-        if (lane == 0) s.fits[i] = runs <= p.workgroups;
+        if (lane == 0) s.fits[i] = runs <= workgroups;
     }
     __syncthreads();
     bool whole = false;
@@ -1176,20 +1184,23 @@ SharedPlan attn_shared_plan(int N, int groups, int Hq, int Hkv, int d, int max_p
     const int rep = Hq / Hkv;
     const long long rows = (long long)N * rep;        // of a key head
     const long long each = (rows + groups - 1) / groups;
-    x.width = each > 32 ? 64 : 32;
+    int pages = max_pages;
+    if (window > 0 && window / kPage + 2 < pages) pages = window / kPage + 2;
+    // Rows of a wave: 64 share what a page costs beside its products, 32 start and end sooner and
+    // plan for themselves.  160 rows on 256 pages 34 us, with 64 a wave 41; 256 on 125 29 and 35; on
+    // 256 42 and 45; 340 of each of 3 groups 170 and 150; 128 on 512 44 and 45, on 1,563 110 and 92.
+    x.width = each > 256 || (each > 64 && pages > 1024) ? 64 : 32;
     // at most: every group's last tile has one row
     const long long some = groups < N ? groups : N;
     const long long tiles = (rows + some * (x.width - 1)) / x.width;
     x.units = tiles * Hkv;
-// Two workgroups a compute unit where 64 rows share a page's bytes and the products count
+    // Two workgroups a compute unit where 64 rows share a page's bytes and the products count
     // (1,024 rows on 512 pages: 170 us, with one 187); one where the bytes do and every cut
     // costs a start and an end (16 groups of 4 on 63 pages 41.6, with two 44.6; 8 on 512
     // pages 28.2 and 31.3).
     x.workgroups = x.width == 64 ? 512 : 256;
     x.few = x.width == 32 && groups <= kFewGroups && N <= kFewSequences;
     x.own_items = (long long)N * Hkv * ((rep + 15) / 16);
-    int pages = max_pages;
-    if (window > 0 && window / kPage + 2 < pages) pages = window / kPage + 2;
     // Four waves a SIMD, and those of short sequences end at once: 60 sequences of up to 4,000 own
     // tokens 74 us (with one a SIMD 89), 255 of up to 2,000 behind 3 prompts 152 (168), of up
     // to 1,000 153 (151); 64 of 200 43 (41.6).

@@ -304,7 +304,7 @@ def _repeated(q, host, table, lens, bf16):
 @pytest.mark.parametrize("sizes,shared,own,Hq,Hkv", [
     ([2], [20001], 70, 4, 4),          # a wave has more shared pages than it looks up at once
     ([1, 700, 400], [0, 1, 2], 5000, 1, 1),        # more own ones, of many sequences
-    ([90, 3], [3000, 41], 65, 8, 2),   # 64 rows a wave, runs over the ends of units
+    ([90, 3], [3000, 41], 65, 16, 2),   # 64 rows a wave, runs over the ends of units
     ([3] * 600, [9] * 600, 20, 2, 1)])             # more units than workgroups
 @pytest.mark.parametrize("out", [torch.float32, BF16])
 def test_attention_over_many_pages(sizes, shared, own, Hq, Hkv, out):
@@ -382,7 +382,7 @@ def test_pages_past_32_bits():
 
 
 @pytest.mark.parametrize("out", [torch.float32, BF16])
-@pytest.mark.parametrize("Hq,Hkv,d", [(2, 1, 64), (8, 2, 128), (64, 1, 64)])
+@pytest.mark.parametrize("Hq,Hkv,d", [(2, 1, 64), (8, 2, 128), (64, 1, 64), (130, 1, 64), (200, 2, 128)])
 def test_a_neighbours_page_changes_no_bit(Hq, Hkv, d, out):
     """A page that only the group's other sequences see, with a scale far from the rest: theirs
     take another way through the pages behind it, the first one's results stay bit for bit."""
