@@ -418,8 +418,9 @@ __device__ __forceinline__ Group group_of_lane(const Group& x, int g) {
 //
 // A weight is exp2(s - m).  For the product with v it is taken times 2^b, b = 12 +
 // log2 v_scale + m - wm, wm the running maximum of s + log2 v_scale, so that it has
-// its f16 bits whatever the pages' scales: as the sum of two f16 values (22 bits) for
-// fp32 results, as one (11 bits) for bf16 ones, whose own rounding is 8 times that.  The
+// its f16 bits whatever the pages' scales: as the sum of two f16 values, 22 bits, as
+// gdr_attn_decode has it.  (As one, 11 bits, 255 sequences behind 3 prompts take 149 us for 174,
+// but 9% of bf16 results are then another value than the fp32 ones rounded.)  The
 // sum takes the same exponentials, times 2^-b once a page; where |b| is large (a page of
 // zeros has a scale of 2^-96) it has its own.
 template <int D, int NB>
@@ -487,7 +488,7 @@ template <int N> __device__ __forceinline__ void wait_but() { asm volatile("s_wa
 // products (as attn_decode_kernel has them).  A wave has a run of the pages of one, and
 // loads each page while it works on the one before: a few pages a sequence are too few
 // to be dealt to four waves, whose starts and joins took as long as the pages.
-template <int D, int PARTS, bool FEW>
+template <int D, bool FEW>
 __device__ __forceinline__ void own_pages(const SharedParams& p, int w, uint32_t place, int lane) {
     constexpr int KS = D / 64;                        // 64-channel steps of a key row
     constexpr int VT = D / 16;                        // 16-channel tiles of the output
@@ -630,17 +631,15 @@ __device__ __forceinline__ void own_pages(const SharedParams& p, int w, uint32_t
                 const float z = __builtin_amdgcn_exp2f(sc[t][i] + up);
                 const _Float16 a = (_Float16)z;
                 w_hi[t >> 1][(t & 1) * 4 + i] = a;
-                if (PARTS == 2) w_lo[t >> 1][(t & 1) * 4 + i] = (_Float16)(z - (float)a);
+                w_lo[t >> 1][(t & 1) * 4 + i] = (_Float16)(z - (float)a);
             }
 #pragma unroll
         for (int j = 0; j < VT; ++j) {
             const half8 v0 = e4m3x8_to_f16(vv[j].x, vv[j].y), v1 = e4m3x8_to_f16(vv[j].z, vv[j].w);
             o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, w_hi[0], o[j], 0, 0, 0);
             o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, w_hi[1], o[j], 0, 0, 0);
-            if (PARTS == 2) {
-                o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, w_lo[0], o[j], 0, 0, 0);
-                o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, w_lo[1], o[j], 0, 0, 0);
-            }
+            o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, w_lo[0], o[j], 0, 0, 0);
+            o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, w_lo[1], o[j], 0, 0, 0);
         }
     }
 
@@ -657,7 +656,7 @@ __device__ __forceinline__ void own_pages(const SharedParams& p, int w, uint32_t
     if (g == 0) *reinterpret_cast<float2*>(&p.own_ml[(run * heads + head) * 2]) = make_float2(m, l);
 }
 
-template <int D, int PARTS, int NB, bool FEW>
+template <int D, int NB, bool FEW>
 __global__ __launch_bounds__(64 * kWaves, 2) void attn_shared_kernel(SharedParams p) {
     constexpr int KL = D / 32;                        // 16-byte reads of a key's row by a lane
     constexpr int DB = D / 32;                        // 32-channel tiles of the output
@@ -683,7 +682,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_shared_kernel(SharedParam
     }
     if (own) {
         const long long w = (long long)(8 * number + blockIdx.x % 8) * kWaves + wave;
-        if (w < p.own_runs) own_pages<D, PARTS, FEW>(p, (int)w, attn::lds_address(sm.page[wave]), threadIdx.x & 63);
+        if (w < p.own_runs) own_pages<D, FEW>(p, (int)w, attn::lds_address(sm.page[wave]), threadIdx.x & 63);
         return;
     }
     // consecutive workgroups go round the 8 XCDs: each of these takes a run of them, the
@@ -979,44 +978,33 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_shared_kernel(SharedParam
             }
 
             wait_values();
-            // (with two parts a weight, the weights of 32 keys do not fit into the registers: 16 at a
-            // time then, 233 us for 247 of 256 sequences behind 3 prompts; with one part, 111 for 101)
+            // (16 keys of the page at a time: the two parts of 32 keys' weights do not fit into the registers)
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int f0 = 0; f0 < 2; f0 += 3 - PARTS) {
-                    half8 w_hi[NB][3 - PARTS], w_lo[NB];
+                for (int f = 0; f < 2; ++f) {
+                    half8 w_hi[NB], w_lo[NB];
 #pragma unroll
                     for (int c = 0; c < NB; ++c) {
                         float sum[2] = {0.f, 0.f};
 #pragma unroll
-                        for (int i = 0; i < 8 * (3 - PARTS); ++i) {
-                            const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(st[c][b][8 * f0 + i], by, up[c]));
+                        for (int i = 0; i < 8; ++i) {
+                            const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(st[c][b][8 * f + i], by, up[c]));
                             sum[i & 1] += w;
                             const _Float16 a = (_Float16)w;
-                            w_hi[c][i / 8][i % 8] = a;
-                            if (PARTS == 2) w_lo[c][i % 8] = (_Float16)(w - (float)a);
+                            w_hi[c][i] = a;
+                            w_lo[c][i] = (_Float16)(w - (float)a);
                         }
                         l[c] += (sum[0] + sum[1]) * share[c];
                     }
 #pragma unroll
                     for (int i = 0; i < DB; ++i) {
-                        const uint32_t at = v_at + (2 * b * D + 32 * i) * 16;
-                        if constexpr (PARTS == 2) {
-                            const uint2v u = read8(at + 8 * f0);
-                            const half8 v = e4m3x8_to_f16(u.x, u.y);
+                        const uint2v u = read8(v_at + (2 * b * D + 32 * i) * 16 + 8 * f);
+                        const half8 v = e4m3x8_to_f16(u.x, u.y);
 #pragma unroll
-                            for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w_hi[c][0], o[c][i], 0, 0, 0);
+                        for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w_hi[c], o[c][i], 0, 0, 0);
 #pragma unroll
-                            for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w_lo[c], o[c][i], 0, 0, 0);
-                        } else {
-                            const uint4v u = read16(at);
-                            const half8 v0 = e4m3x8_to_f16(u.x, u.y), v1 = e4m3x8_to_f16(u.z, u.w);
-#pragma unroll
-                            for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v0, w_hi[c][0], o[c][i], 0, 0, 0);
-#pragma unroll
-                            for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v1, w_hi[c][2 - PARTS], o[c][i], 0, 0, 0);
-                        }
+                        for (int c = 0; c < NB; ++c) o[c][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w_lo[c], o[c][i], 0, 0, 0);
                     }
                 }
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -1235,20 +1223,20 @@ long long attn_shared_workgroups(const SharedPlan& x, long long heads) {
 // One wave a head in the join where there are many, else four: 8,160 heads 9.1 us, with four 19.9;
 // 2,048: 4.6 and 6.2; 1,024 of some 30 parts: 7.6 and 6.4; 256 of some 70: 9.6 and 5.1.
 constexpr long long kHeadsOfWaves = 2048;
-template <int D, int PARTS, int NB, bool FEW> static hipError_t launch_shared(const SharedParams& p, hipStream_t st) {
+template <int D, int NB, bool FEW> static hipError_t launch_shared(const SharedParams& p, hipStream_t st) {
     static std::atomic<unsigned long long> done{0};
     const int lds = (int)sizeof(SharedSmem<D, NB>);
-    const hipError_t e = ensure_dyn_lds(reinterpret_cast<const void*>(&attn_shared_kernel<D, PARTS, NB, FEW>), lds, done);
+    const hipError_t e = ensure_dyn_lds(reinterpret_cast<const void*>(&attn_shared_kernel<D, NB, FEW>), lds, done);
     if (e != hipSuccess) return e;
     const long long own = (p.own_runs + 8 * kWaves - 1) / (8 * kWaves);
-    hipLaunchKernelGGL((attn_shared_kernel<D, PARTS, NB, FEW>), dim3((unsigned)(p.workgroups + 8 * own)), dim3(64 * kWaves), lds, st, p);
+    hipLaunchKernelGGL((attn_shared_kernel<D, NB, FEW>), dim3((unsigned)(p.workgroups + 8 * own)), dim3(64 * kWaves), lds, st, p);
     return hipGetLastError();
 }
 
-template <int D, int PARTS> static hipError_t launch_d(const SharedParams& p, hipStream_t st) {
+template <int D> static hipError_t launch_d(const SharedParams& p, hipStream_t st) {
     hipError_t e;
-    if (p.width == 64) e = launch_shared<D, PARTS, 2, false>(p, st);
-    else e = p.few ? launch_shared<D, PARTS, 1, true>(p, st) : launch_shared<D, PARTS, 1, false>(p, st);
+    if (p.width == 64) e = launch_shared<D, 2, false>(p, st);
+    else e = p.few ? launch_shared<D, 1, true>(p, st) : launch_shared<D, 1, false>(p, st);
     if (e != hipSuccess) return e;
     const long long heads = (long long)p.N * p.Hq;
     if (heads >= kHeadsOfWaves) hipLaunchKernelGGL((attn_shared_join<D, 64>), dim3((unsigned)heads), dim3(64), 0, st, p);
@@ -1265,9 +1253,7 @@ hipError_t launch_attn_shared(const SharedParams& p, hipStream_t st) {
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    const bool one = (p.flags & GDR_OUT_BF16) != 0;
-    if (p.d == 64) return one ? launch_d<64, 1>(p, st) : launch_d<64, 2>(p, st);
-    return one ? launch_d<128, 1>(p, st) : launch_d<128, 2>(p, st);
+    return p.d == 64 ? launch_d<64>(p, st) : launch_d<128>(p, st);
 }
 
 }  // namespace gdr

@@ -599,8 +599,8 @@ gdr_status gdr_attn_decode(const void* q, const void* k_cache, const void* v_cac
  *   workspace    : gdr_attn_decode_shared_workspace_bytes() bytes of device scratch,
  *        contents on entry ignored; calls that may overlap need one each
  * A token that a sequence does not see has no effect on it, NaN included.  Scores, softmax
- * statistics and sums are fp32.  The weights enter the product with v as two f16 parts
- * (22 bits) where the result is fp32, as one (11 bits) where it is bf16.
+ * statistics and sums are fp32 (the weights enter the product with v as two f16 parts, 22
+ * bits); a bf16 result is the fp32 one rounded once.
  * Flags: GDR_OUT_BF16.  Supported: d in {64, 128}, groups <= 4096, N Hq < 2^24.
  */
 size_t gdr_attn_decode_shared_workspace_bytes(int N, int groups, int Hq, int Hkv, int d, int max_pages,
