@@ -150,8 +150,8 @@ def kv_compact(cache: KVCache, block_table, cache_len, held=None, table_out=None
 def beam_select(logits, scores, n_select: Optional[int] = None, ended=None, end_token: int = -1, keep_slots: bool = False,
                 stream=None):
     """The best n_select (None: K) continuations of each group of K beams.
-    logits: bf16 or fp32 [G*K,V] (rows may be those of a wider tensor), row g*K+k being
-    beam k of group g; scores: fp32 [G,K], the beams' log probabilities; ended: bool
+    logits: bf16 or fp32 [G*K,V] (rows may be those of a wider tensor; at most 65,535), row g*K+k
+    being beam k of group g; scores: fp32 [G,K], the beams' log probabilities; ended: bool
     [G,K], beams that end_token has ended (they go on as they are).
     Returns (tokens int32, rows int32: the row g*K+k that each continues, scores fp32,
     ended bool), all [G,n_select], from the best; with keep_slots (n_select = K) the first

@@ -601,7 +601,8 @@ gdr_status gdr_attn_decode(const void* q, const void* k_cache, const void* v_cac
  * A token that a sequence does not see has no effect on it, NaN included.  Scores, softmax
  * statistics and sums are fp32 (the weights enter the product with v as two f16 parts, 22
  * bits); a bf16 result is the fp32 one rounded once.
- * Flags: GDR_OUT_BF16.  Supported: d in {64, 128}, groups <= 4096, N Hq < 2^24.
+ * Flags: GDR_OUT_BF16.  Supported: d in {64, 128}, groups <= 4096, N Hq <= 2^24 - 2^15,
+ * max_pages <= 2^24.
  */
 size_t gdr_attn_decode_shared_workspace_bytes(int N, int groups, int Hq, int Hkv, int d, int max_pages,
                                               int window);
@@ -640,7 +641,8 @@ gdr_status gdr_attn_decode_shared(const void* q, const void* k_cache, const void
  *                 entry ignored; calls that may overlap need one each
  * table_out and len_out may be block_table and cache_len where parent is NULL; no other
  * aliasing.  Every table that holds pages of this cache is either in the call or in `held`.
- * flags must be 0.  Supported: d in {64, 128}, N_in, N <= 2^20.
+ * flags must be 0.  Supported: d in {64, 128}, N_in, N <= 2^20, Hkv <= 65535, n_pages <= 2^30,
+ * max_pages <= 2^24, N_in max_pages and N max_pages < 2^31.
  */
 size_t gdr_kv_fork_workspace_bytes(int N, int n_pages);
 
@@ -660,7 +662,7 @@ gdr_status gdr_kv_fork(void* k_cache, void* v_cache, float* k_scale, float* v_sc
  *   used      : int32 [1], written: one past the last page in use afterwards
  *   workspace : gdr_kv_compact_workspace_bytes() bytes of device scratch, contents on
  *               entry ignored; calls that may overlap need one each
- * flags must be 0.  Supported: d in {64, 128}, N <= 2^20.
+ * flags must be 0.  Supported: as gdr_kv_fork.
  */
 size_t gdr_kv_compact_workspace_bytes(int n_pages);
 
@@ -691,7 +693,8 @@ gdr_status gdr_kv_compact(void* k_cache, void* v_cache, float* k_scale, float* v
  * continuation of a beam in the beam's own place, the others, in order, in the places
  * left: then what a beam has (its state, its table's row) moves only where it has to.
  * Log-sums are formed in fp32 from each row's maximum and joined in 64 bits; scores are
- * compared in 64 bits and rounded once.  Supported: K, M <= 64, M <= K V, V <= 2^26.
+ * compared in 64 bits and rounded once.  Supported: K, M <= 64, M <= K V, V <= 2^26, G K <= 65535,
+ * stride <= 2^40.
  */
 size_t gdr_beam_select_workspace_bytes(int G, int K, int M, int V);
 
@@ -707,7 +710,7 @@ gdr_status gdr_beam_select(const void* logits, const float* scores, const uint8_
  * and costs nothing.
  *   state  : [layers, N, row_bytes], row_bytes a multiple of 16
  *   parent : int32 [N] in device memory (gdr_beam_select's rows, M = K)
- * flags must be 0.  Supported: K <= 64, N a multiple of K.
+ * flags must be 0.  Supported: K <= 64, N a multiple of K, layers N <= 2^28, row_bytes <= 2^40.
  */
 gdr_status gdr_state_reorder(void* state, const int* parent, int layers, int N, int K,
                              size_t row_bytes, uint32_t flags, void* stream);
