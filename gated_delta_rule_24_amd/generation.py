@@ -93,7 +93,8 @@ def kv_fork(cache: KVCache, block_table, cache_len, parent=None, room=1, held=No
     pages that other tables hold.  Returns (table_out [N,max_pages], -1 behind a row's pages;
     len_out [N]; missing [N], the pages each row wanted and did not get: it must not be
     appended to then).  table_out and len_out may be given; without parent also as
-    block_table and cache_len themselves."""
+    block_table and cache_len themselves.  The pages are one layer's: layers under one table take
+    a call each, all from the old table (only the last may write over it), and get the same new one."""
     gpu = _gpu_of("cache.k", cache.k)
     n_pages, Hkv, d, N_in, max_pages = _cache_shapes(cache, block_table, cache_len, gpu)
     N = N_in
@@ -130,7 +131,8 @@ def kv_fork(cache: KVCache, block_table, cache_len, parent=None, room=1, held=No
 def kv_compact(cache: KVCache, block_table, cache_len, held=None, table_out=None, stream=None):
     """Pages in use moved to the lowest free places (those that `held` marks stay), and the
     table that names them there.  Returns (table_out [N,max_pages], used int32 [1]: one past
-    the last page in use afterwards).  table_out may be block_table."""
+    the last page in use afterwards).  table_out may be block_table; layers under one table take a
+    call each, all from the old table, as for :func:`kv_fork`."""
     gpu = _gpu_of("cache.k", cache.k)
     n_pages, Hkv, d, N, max_pages = _cache_shapes(cache, block_table, cache_len, gpu)
     if table_out is None:

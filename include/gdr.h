@@ -623,7 +623,8 @@ gdr_status gdr_attn_decode_shared(const void* q, const void* k_cache, const void
  *   - The page that row n is about to write on (cache_len % 64 tokens are in it) is copied
  *     for it, unless no other row holds that page, or all rows that do are about to write
  *     on it and n is the lowest of them.  It is copied too where `held` marks it.
- *   - Fresh pages follow for the tokens that do not fit, as far as max_pages.
+ *   - Fresh pages follow for the tokens that do not fit, as far as max_pages: a row whose table has no
+ *     place left wants none and misses none.
  * The j-th page wanted (row by row, a row's copy first) is the j-th lowest free one.
  * Nothing is kept between calls, so that a call made again gives the same again; pages
  * that a row was given for tokens that were never appended are free at the next call.
@@ -641,6 +642,9 @@ gdr_status gdr_attn_decode_shared(const void* q, const void* k_cache, const void
  *                 entry ignored; calls that may overlap need one each
  * table_out and len_out may be block_table and cache_len where parent is NULL; no other
  * aliasing.  Every table that holds pages of this cache is either in the call or in `held`.
+ * A call copies the pages of one layer's cache.  Layers under one table take a call each, all
+ * with the same old table, lengths, parent, room and held, which give the same new table: only the last of
+ * them may write over the old one.
  * flags must be 0.  Supported: d in {64, 128}, N_in, N <= 2^20, Hkv <= 65535, n_pages <= 2^30,
  * max_pages <= 2^24, N_in max_pages and N max_pages < 2^31.
  */
@@ -659,6 +663,7 @@ gdr_status gdr_kv_fork(void* k_cache, void* v_cache, float* k_scale, float* v_sc
  * two.  Pages that `held` marks stay.  (Pages, rows and free ones as in gdr_kv_fork: call it
  * where cache_len is up to date.)
  *   table_out : int32 [N, max_pages], written; -1 behind a row's pages; may be block_table
+ *               (of layers under one table, which take a call each, in the last one only)
  *   used      : int32 [1], written: one past the last page in use afterwards
  *   workspace : gdr_kv_compact_workspace_bytes() bytes of device scratch, contents on
  *               entry ignored; calls that may overlap need one each
