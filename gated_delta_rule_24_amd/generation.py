@@ -56,7 +56,8 @@ def attn_decode_shared(q, cache: KVCache, block_table, cache_len, group_start, s
     """:func:`attn_decode` for groups of sequences that share their first pages.
     q: bf16 [N,Hq,d]; group_start: int32 [groups+1], group g being sequences
     group_start[g] .. group_start[g+1]-1; shared_pages: int32 [groups], how many of
-    their first pages are those in the row of the group's first sequence.
+    their first pages are those in the row of the group's first sequence (which must hold them: a
+    group whose first row was emptied begins behind it).
     Returns o [N,Hq,d] of out_dtype (fp32 or bf16)."""
     gpu = _gpu_of("q", q)
     n_pages, Hkv, d, N, max_pages = _cache_shapes(cache, block_table, cache_len, gpu)

@@ -589,7 +589,9 @@ gdr_status gdr_attn_decode(const void* q, const void* k_cache, const void* v_cac
  * gdr_attn_decode for groups of sequences that share their first pages: group g is the
  * sequences group_start[g] .. group_start[g + 1] - 1, and their first
  * shared_pages[g] pages are those in the table's row of the group's first sequence
- * (the other rows' entries for them are not read).  Their tokens are read once for every
+ * (the other rows' entries for them are not read, and of that row those entries whatever the
+ * sequence's length: where it was dropped and its row emptied, as gdr_kv_fork does for a parent
+ * outside the table, let the group begin behind it, or its shared tokens count as masked).  Their tokens are read once for every
  * 32 or 64 of the group's (sequence, query head) pairs on a key head, not once for
  * each sequence.  Lengths and windows are each sequence's own; a sequence may end inside
  * the shared pages.  Sequences in no group share nothing.

@@ -71,3 +71,21 @@ def test_bytes_that_one_sequence_sees_and_another_does_not(Hq, Hkv, window, out)
                         assert bool(hit.all()) if side == "k" else bool(hit[:, 5:9].all()) and int(hit.sum()) == 4 * Hq
                     else:
                         assert not bool(got[n].isnan().any())
+
+
+@pytest.mark.parametrize("Hq", [8, 150])
+def test_a_group_whose_first_sequence_was_dropped(Hq):
+    """Its emptied row has no shared pages; the group that begins behind it has them all."""
+    sizes, shared, d = [4], [2], 64
+    total, table = _tables(sizes, [0], [200, 150, 140, 190], 40)
+    table[:, :2] = table[0, :2]
+    c, q = base._cache(total, 1, d, 41), base._rand((4, Hq, d), 42)
+    lens = torch.tensor([200, 150, 140, 190], dtype=torch.int32)
+    parent = torch.tensor([-1, 1, 2, 3], dtype=torch.int32).cuda()
+    dev = gdr.KVCache(*[x.cuda() for x in c])
+    table, lens, missing = gdr.generation.kv_fork(dev, table.cuda(), lens.cuda(), parent, room=0)
+    table, lens = table.cpu(), lens.tolist()
+    assert lens == [0, 150, 140, 190] and bool((table[0] == -1).all()) and not bool(missing.any())
+    whole = base._check(c, q, table, lens, [1, 4], shared)
+    base._check(c, q, table, lens, [0, 4], shared)    # (the shared pages count as masked)
+    assert not bool(whole[0].any())
