@@ -502,10 +502,10 @@ __global__ __launch_bounds__(kThreads) void beam_join(BeamParams p) {
 
 int beam_segments(int G, int K, int V) {
     // Enough workgroups for every compute unit where there are few rows (twice as many and half
-    // as many take 64 x 8 beams over 131,072 tokens from 47.6 us to 52 and 68); a run of
-    // 8,192 values at the least, a bf16 chunk (4 beams over 131,072: 19.3 us a call; of 2,048, 28.5);
-    // and no more runs of a group than the join has soon ranked (4 beams over 2,000,000: 37 us;
-    // of up to 256 runs 36 but one row there 29 for 21, of up to 1,000, 222).
+    // as many take 64 x 8 beams over 131,072 tokens from 53.7 us a call to 58 and 70.5); a run of
+    // 8,192 values at the least, a bf16 chunk (4 beams over 131,072: 19.0; of 2,048, 20.8, and 28 with
+    // up to 256 runs); and no more runs of a group than the join has soon ranked (4 beams over
+    // 2,000,000: 36.2; of up to 256 runs 34.9, but one row there 28.6 for 21.3; of up to 64, 46.8 and 19.8).
     const long long rows = (long long)G * K;
     long long s = (1024 + rows - 1) / rows;
     const long long most = ((long long)V + 8191) / 8192;

@@ -275,10 +275,11 @@ __global__ __launch_bounds__(kThreads) void fork_copy(PagesParams p, ForkSpace s
 }
 
 // The same for caches and tables that one workgroup has soon read: the counters are in
-// LDS, and a call is this kernel and the copies.  (A cache of 4,600 pages, 256 rows of 40 pages:
-// five launches take 47.5 us a call, two 32; rows of 68 pages, 51 and 36; of 130 pages, 50 and 42.
-// 4 rows of 17 pages: 28 and 20, of which the kernels are 9.)  Compaction of 120 rows of 66
-// pages: 104 and 88; of 250 rows of 80 pages 43 and 41, of 160 pages 41 and 51.
+// LDS, and a call is this kernel and the copies.  (256 rows of 40 pages: five launches take 41 us a
+// call, two 20.5; of 130, 44 and 28; of 157, next to the limit, 42 and 30; past it, of 200, 42.5 and
+// 34 and of 272, 44 and 40.6: the limit is not where they cross but keeps clear of the counters' 16
+// bits.  4 rows of 17 pages: 29 and 19.)  Compaction of 120 rows of 66 pages: 101 and 86; of 250 rows of
+// 80 pages 37.9 and 39.6, of 160 pages 39 and 51.
 constexpr int kSmallThreads = 1024;
 constexpr int kMine = 12;                             // pages a thread
 constexpr int kSmallPages = kMine * kSmallThreads, kSmallRows = 2048;   // (LDS: 8 bytes a page, 16 a row)

@@ -138,9 +138,10 @@ __device__ __forceinline__ void join_waves(const O& o, const ML& ml, int rows, F
 // One workgroup looks at the groups, as the host does not know them, and lays the pages of all
 // units end to end: each of as many workgroups as can be at work at once takes a run of the same
 // length of that line, over the ends of units, so that all end together.  (With whole runs of each
-// unit's pages, as many as fit, 3 groups of 340 rows on 256 pages kept 144 of 256
-// workgroups: 119 us for the shared pages, over the ends 101.)  Where whole runs of units are
-// little longer they are taken: a unit's start and end cost some pages' time.
+// unit's pages, as many as fit, 3 groups of 340 rows on 256 pages keep 144 of 256
+// workgroups: 119 us for the shared pages, over the ends 101, when a weight had one f16 part.)  Where
+// whole runs of units are little longer they are taken: a unit's start and end cost some pages' time
+// (16 groups of 4 39.3 us a call, never 40.6; 255 sequences behind 3 prompts 174 either way).
 constexpr int kPlanThreads = 1024;
 constexpr int kLonger = 8;                            // pages that a unit's start and end are worth
 
@@ -154,7 +155,8 @@ __device__ __forceinline__ int runs_of(int pages, long long per) {
     return pages <= per ? 1 : (int)(((uint32_t)pages + (uint32_t)per - 1) / (uint32_t)per);
 }
 // Workgroups that the pages of all units are dealt to: two a compute unit only where each has many
-// (128 rows on 512 pages 45 us, with two 51; 256 on 125 35.5 and 40.6; 512 on 256 63.6 and 65.8).
+// (64 rows a wave: 128 rows on 512 pages 49 us a call, with two 57; 256 on 125 39 and 44; 512 on 256 79
+// and 78; 1,024 on 512 240 and 220).
 constexpr int kShort = 64;
 __device__ __forceinline__ int workgroups_for(const SharedParams& p, long long all) {
     return p.workgroups > 256 && all < (long long)p.workgroups * kShort ? 256 : p.workgroups;
@@ -295,8 +297,8 @@ __global__ __launch_bounds__(kPlanThreads) void attn_shared_plan_kernel(SharedPa
 
 // The same in each workgroup for itself, a group a lane, where there are few groups and
 // sequences: a plan kernel takes 5.5 to 9 us before the others start.  (4 sequences behind 300
-// tokens 16.0 us a call, with a plan kernel 20.6; 16 groups of 4 37.8 and 42.6; 64 of 16 51.6 and
-// 55.6.  Not with 64 rows a wave: the registers of the products have no room left, and scratch
+// tokens 17.5 us a call, with a plan kernel 19.5; 16 groups of 4 39 to 40.5 and 43; 64 of 16 52.5 and
+// 57.  Not with 64 rows a wave: the registers of the products have no room left, and scratch
 // memory in the pages' loop costs more than the plan.)
 constexpr int kFewGroups = 64, kFewSequences = 1024;
 struct LanePlan {
@@ -400,21 +402,23 @@ __device__ __forceinline__ Group group_of_lane(const Group& x, int g) {
 //
 // A wave has 64 rows (32 where groups are smaller): what a page costs beside its products,
 // its bytes' conversion above all, is then shared by as many.  The waves of a workgroup
-// have the same rows and take pages in turn, each for itself: with waves that shared
-// a page and waited for each other at every one, 1,024 rows on 512 pages took 215 us for
-// 181.  Pages come to a wave's place in LDS as they lie in memory, by direct loads (no
+// have the same rows and take pages in turn, each for itself (times here, but for the last, are
+// of weights in one f16 part): with waves that shared a page and waited for each other at every
+// one, 1,024 rows on 512 pages took 215 us for 181.  Pages come to a wave's place in LDS as they lie in memory, by direct loads (no
 // registers, 1 KiB an instruction; read straight to registers in the operands'
 // order, 16 bytes a lane from 32 rows, the same walk took 265): the next page's keys when
 // this one's are read, its values when these are.  With one place and the queries in LDS,
-// two waves of 256 registers are on a SIMD, and one's products run beside the other's
-// exponentials and conversions: 170 us, of which the products' share at the matrix cores' peak
-// is 55.  What bounds it are the vector instructions: a page takes a wave 64 products of 32
-// cycles, and beside them some 330 instructions, of which 64 exponentials and 160 conversions
-// count double and more.
+// two waves of 256 registers are on a SIMD: 170 us, and with weights in two parts 220, of which
+// the products' share at the matrix cores' peak is 82.  A page takes a wave 96 products of 32 cycles,
+// and beside them the conversions of its bytes, 64 exponentials and those weights' conversions to two
+// parts.  For 255 sequences behind 3 prompts a SIMD's vector instructions take 53% of the cycles and
+// its products 36%, 89% together: neither is full, what bounds it is that they hardly overlap.  A
+// page's score products all come first, then the maxima, then exponentials and value products, and
+// two waves in the same phase have nothing for the other unit.
 //
 // Workgroups for sequences' own pages, which memory bounds, stand on the compute units beside
-// these, two a unit: one kernel after the other took 101 and 75 us for 256 sequences
-// behind 3 prompts, both together 128.
+// these, two a unit: one kernel after the other took 101 and 75 us for 255 sequences
+// behind 3 prompts, both together 128 (with one f16 part a weight).
 //
 // A weight is exp2(s - m).  For the product with v it is taken times 2^b, b = 12 +
 // log2 v_scale + m - wm, wm the running maximum of s + log2 v_scale, so that it has
@@ -666,9 +670,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_shared_kernel(SharedParam
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), rep = p.Hq / p.Hkv;
 
     // a workgroup for shared pages for each of 256 compute units and one for own ones by turns,
-    // as long as there are both (256 sequences behind 3 prompts 147 us; all of the first kind
-    // before the others 163; by turns of 8, as shader engines are taken one after the other, half of
-    // them got all of the first kind: 185)
+    // as long as there are both (255 sequences behind 3 prompts 174 us; all of the first kind
+    // before the others 175, and 163 for 147 when a weight had one f16 part; by turns of 8, as shader
+    // engines are taken one after the other, half of them get all of the first kind: 216)
     constexpr int kTurn = 256 / 8;
     int number = blockIdx.x / 8;
     const int some = p.workgroups / 8, turns = min(some, (int)(gridDim.x / 8) - some) / kTurn;
@@ -1175,23 +1179,24 @@ SharedPlan attn_shared_plan(int N, int groups, int Hq, int Hkv, int d, int max_p
     int pages = max_pages;
     if (window > 0 && window / kPage + 2 < pages) pages = window / kPage + 2;
     // Rows of a wave: 64 share what a page costs beside its products, 32 start and end sooner and
-    // plan for themselves.  160 rows on 256 pages 34 us, with 64 a wave 41; 256 on 125 29 and 35; on
-    // 256 42 and 45; 340 of each of 3 groups 170 and 150; 128 on 512 44 and 45, on 1,563 110 and 92.
+    // plan for themselves (not by the lengths, which the host does not know, nor by single groups).  160
+    // rows on 256 pages 40 us a call, with 64 a wave 49; 256 on 125 32 and 39; on 256 47 and 51; 340 of
+    // each of 3 groups 190 and 176; 512 on 256 81 and 79; 128 on 512 48 and 49, on 1,563 129 and 114.
     x.width = each > 256 || (each > 64 && pages > 1024) ? 64 : 32;
     // at most: every group's last tile has one row
     const long long some = groups < N ? groups : N;
     const long long tiles = (rows + some * (x.width - 1)) / x.width;
     x.units = tiles * Hkv;
     // Two workgroups a compute unit where 64 rows share a page's bytes and the products count
-    // (1,024 rows on 512 pages: 170 us, with one 187); one where the bytes do and every cut
-    // costs a start and an end (16 groups of 4 on 63 pages 41.6, with two 44.6; 8 on 512
-    // pages 28.2 and 31.3).
+    // (1,024 rows on 512 pages: 220 us, with one 240); one where the bytes do and every cut
+    // costs a start and an end (16 groups of 4 on 63 pages 39 to 40.5, with two 43.7; 32 rows on 512
+    // pages 26.6 and 30.1).
     x.workgroups = x.width == 64 ? 512 : 256;
     x.few = x.width == 32 && groups <= kFewGroups && N <= kFewSequences;
     x.own_items = (long long)N * Hkv * ((rep + 15) / 16);
-    // Four waves a SIMD, and those of short sequences end at once: 60 sequences of up to 4,000 own
-    // tokens 74 us (with one a SIMD 89), 255 of up to 2,000 behind 3 prompts 152 (168), of up
-    // to 1,000 153 (151); 64 of 200 43 (41.6).
+    // Four waves a SIMD, and those of short sequences end at once: 255 sequences of up to 2,000 own
+    // tokens behind 3 prompts of up to 4,000 154 us a call (with one a SIMD 173), of up to 1,000
+    // behind up to 16,384 174 (178), behind none 86 (88); 60 of up to 4,000 67 (67), 64 of 200 17.4 (17.7).
     long long s = (4096 + x.own_items / 2) / x.own_items;
     const long long most = (pages + kOwnRun - 1) / kOwnRun;
     if (s > most) s = most;
